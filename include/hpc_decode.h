@@ -209,7 +209,8 @@ hpc_status hpc_decode_plan_static_compute(const int32_t* seq_lens, int32_t num_s
 #define HPC_DEVCHK_BAD_BLOCK 2        /* block id outside [0, num_blocks) */
 #define HPC_DEVCHK_TABLE_TOO_SHORT 4  /* a sequence needs more than max_blocks */
 #define HPC_DEVCHK_TIMEOUT 8          /* a bounded wait gave up */
-#define HPC_DEVCHK_CAPACITY 16        /* a step larger than the plan's capacity */
+#define HPC_DEVCHK_CAPACITY 16        /* a step larger than the plan's capacity, or than a buffer */
+#define HPC_DEVCHK_NO_BLOCKS 32       /* too few free blocks for a step's new tokens */
 hpc_status hpc_decode_plan_status(hpc_plan_t plan, int32_t* device_error);
 
 /* hpc_decode_plan_destroy -- free a plan (NULL is a no-op). Synchronises the
@@ -468,6 +469,83 @@ hpc_status hpc_extend_attn_ex(const hpc_tensor* q, const hpc_tensor* k_cache,
                               const hpc_tensor* seq_lens, const hpc_tensor* cu_q_lens,
                               hpc_tensor* out, hpc_tensor* lse, float softmax_scale,
                               int32_t tiles_per_cta, int32_t* device_error, void* stream);
+
+/*
+ * hpc_block_table_append -- block tables, slot maps and positions of a step,
+ * built on the GPU from the sequences' lengths. Sequence b has o_b =
+ * seq_lens[b] tokens in the cache and gets n_b = new_lens[b] new ones; it
+ * needs a_b = ceil((o_b + n_b) / 64) - ceil(o_b / 64) more blocks, taken from
+ * the top of a stack of free block ids (free_blocks[0 .. free_count - 1], the
+ * last one on top). With A and N the exclusive prefix sums of a and n:
+ *   block_table[b][ceil(o_b / 64) + i] = free_blocks[free_count - 1 - (A_b + i)]
+ *   seq_lens_out[b] = o_b + n_b,  cu_q_lens[b] = N_b (cu_q_lens[B] = all new),
+ *   positions[N_b + i] = o_b + i,
+ *   slots[N_b + i] = 64 * block_table[b][(o_b + i) / 64] + (o_b + i) % 64,
+ *   free_count_out = free_count - sum a.
+ * These are the inputs of hpc_rope_kv_write (positions, slots), of
+ * hpc_extend_attn (cu_q_lens, seq_lens) and of the decode calls. The result
+ * depends on the arguments alone (no atomics). Sequences that share a prefix
+ * start from rows that hold the prefix's whole blocks, with seq_lens[b] = 64
+ * times their number; the last, partly filled block is never a shared one.
+ *   seq_lens, new_lens  device int32 [B], each >= 0; B <= 16384 (else
+ *                       HPC_ERR_UNSUPPORTED); B = 0 is allowed
+ *   free_blocks         device int32 [cap] (read)
+ *   free_count          device int32 [1], 0 <= free_count <= cap
+ *   num_blocks          blocks of the cache; ids outside [0, num_blocks) give
+ *                       table entries and slots of -1 and HPC_DEVCHK_BAD_BLOCK
+ *   block_table         device int32 [B][max_blocks], rows contiguous; only
+ *                       the new entries are written
+ *   seq_lens_out        device int32 [B]; may be seq_lens (in place)
+ *   cu_q_lens           device int32 [B + 1] (written)
+ *   positions, slots    device int32 [cap_tokens] (written); entries past the
+ *                       last new token become position 0 and slot -1, so that a
+ *                       captured step of fixed size skips them
+ *   free_count_out      device int32 [1]; may be free_count (in place)
+ *   device_error        optional device int32 receiving HPC_DEVCHK_* bits
+ * A step that cannot be met is refused as a whole: block_table stays as it
+ * was, seq_lens_out and free_count_out repeat their inputs, cu_q_lens is zero,
+ * every slot is -1 and every position 0, and the bits say why: BAD_LENGTH (a
+ * negative length or a sum past int32), TABLE_TOO_SHORT (a sequence needs more
+ * than max_blocks), CAPACITY (more new tokens than cap_tokens, or a count
+ * outside the stack), NO_BLOCKS (more blocks needed than free). Apart from the
+ * two in-place forms no output may overlap an input or another output
+ * (HPC_ERR_INVALID_ARG). One launch; allocates nothing.
+ */
+hpc_status hpc_block_table_append(const hpc_tensor* seq_lens, const hpc_tensor* new_lens,
+                                  const hpc_tensor* free_blocks, const hpc_tensor* free_count,
+                                  int32_t num_blocks, hpc_tensor* block_table,
+                                  hpc_tensor* seq_lens_out, hpc_tensor* cu_q_lens,
+                                  hpc_tensor* positions, hpc_tensor* slots,
+                                  hpc_tensor* free_count_out, int32_t* device_error,
+                                  void* stream);
+
+/*
+ * hpc_block_table_truncate -- the way back: sequence b keeps its first
+ * k_b = min(seq_lens[b], to_lens[b]) tokens (a finished sequence 0, a
+ * speculative one its accepted tokens), and its blocks ceil(k_b / 64) ..
+ * ceil(seq_lens[b] / 64) - 1 go back on the stack, so that block 0 of the
+ * first shortened sequence ends on top: a truncate to the old lengths undoes
+ * an append, stack order included. seq_lens_out[b] = k_b, free_count_out =
+ * free_count + the released blocks. The table is not written: entries past a
+ * sequence's end have no meaning. Blocks that several rows share must not be
+ * released through more than one of them: keep to_lens[b] at or above the
+ * shared prefix.
+ *   seq_lens, to_lens  device int32 [B], each >= 0; B <= 16384
+ *   block_table        device int32 [B][max_blocks], rows contiguous (read)
+ *   num_blocks         blocks of the cache; an entry outside [0, num_blocks)
+ *                      is pushed as -1 and sets HPC_DEVCHK_BAD_BLOCK
+ *   free_blocks        device int32 [cap] (written above free_count only)
+ *   free_count, free_count_out, seq_lens_out, device_error: as for append
+ * Refused as a whole (free_blocks untouched, both outputs repeat their
+ * inputs): BAD_LENGTH (a negative length), TABLE_TOO_SHORT (a released block
+ * past max_blocks), CAPACITY (the stack would pass cap, or a count outside
+ * it). One launch; allocates nothing.
+ */
+hpc_status hpc_block_table_truncate(const hpc_tensor* seq_lens, const hpc_tensor* to_lens,
+                                    const hpc_tensor* block_table, int32_t num_blocks,
+                                    hpc_tensor* free_blocks, const hpc_tensor* free_count,
+                                    hpc_tensor* seq_lens_out, hpc_tensor* free_count_out,
+                                    int32_t* device_error, void* stream);
 
 /* hpc_device_sm_count -- streaming multiprocessors of the current device. */
 hpc_status hpc_device_sm_count(int32_t* num_sms);

@@ -27,6 +27,7 @@ __all__ = [
     "hpc_decode_plan_set_timing_events", "hpc_decode_attn_noalloc", "hpc_decode_step",
     "hpc_decode_step_host",
     "hpc_rope_norm_kv_write", "hpc_extend_attn", "hpc_decode_tc_min_q_len",
+    "hpc_block_table_append", "hpc_block_table_truncate",
     "HPC_OK", "HPC_ERR_INVALID_ARG", "HPC_ERR_UNSUPPORTED", "HPC_ERR_CUDA", "HPC_ERR_OOM",
     "HPC_ERR_DEVICE_CHECK",
 ]
@@ -37,7 +38,7 @@ HPC_BF16, HPC_FP8_E4M3, HPC_F32, HPC_I32 = range(4)
 HPC_PLAN_DYNAMIC, HPC_PLAN_STATIC, HPC_PLAN_STEP = 0, 1, 2
 HPC_SEG_WHOLE = 1
 HPC_DEVCHK_BAD_LENGTH, HPC_DEVCHK_BAD_BLOCK, HPC_DEVCHK_TABLE_TOO_SHORT, \
-    HPC_DEVCHK_TIMEOUT, HPC_DEVCHK_CAPACITY = 1, 2, 4, 8, 16
+    HPC_DEVCHK_TIMEOUT, HPC_DEVCHK_CAPACITY, HPC_DEVCHK_NO_BLOCKS = 1, 2, 4, 8, 16, 32
 
 _STATUS_NAMES = {0: "HPC_OK", 1: "HPC_ERR_INVALID_ARG", 2: "HPC_ERR_UNSUPPORTED",
                  3: "HPC_ERR_CUDA", 4: "HPC_ERR_OOM", 5: "HPC_ERR_DEVICE_CHECK"}
@@ -110,6 +111,8 @@ def load_library():
                                        T, T, T, T, P, P],
             "hpc_extend_attn": [T, T, T, T, T, T, T, T, ctypes.c_float, P, P],
             "hpc_extend_attn_ex": [T, T, T, T, T, T, T, T, ctypes.c_float, i32, P, P],
+            "hpc_block_table_append": [T, T, T, T, i32, T, T, T, T, T, T, P, P],
+            "hpc_block_table_truncate": [T, T, T, i32, T, T, T, T, P, P],
         }
         for name, args in sigs.items():
             fn = getattr(lib, name)
@@ -442,3 +445,40 @@ def hpc_decode_attn_noalloc(q, k_cache, v_cache, block_table, seq_lens, out, lse
     err = ctypes.c_void_p(device_error.data_ptr()) if device_error is not None else None
     _check(lib.hpc_decode_attn_noalloc(ref(tq), ref(tk), ref(tv), ref(tb), ref(ts), int(num_sms),
                                        ref(to), ref(tl), err, _stream_ptr(stream)))
+
+
+def _ref(d):
+    return ctypes.byref(d) if d is not None else None
+
+
+def _err_ptr(device_error):
+    return ctypes.c_void_p(device_error.data_ptr()) if device_error is not None else None
+
+
+def hpc_block_table_append(seq_lens, new_lens, free_blocks, free_count, num_blocks: int,
+                           block_table, seq_lens_out, cu_q_lens, positions, slots,
+                           free_count_out, device_error=None, stream=None):
+    """Block tables, slot maps and positions of a step, on the GPU: sequence b
+    goes from seq_lens[b] to seq_lens[b] + new_lens[b] tokens, new blocks come
+    from the top of the stack free_blocks[:free_count]. All int32 CUDA tensors;
+    seq_lens_out / free_count_out may be seq_lens / free_count (in place).
+    positions and slots are padded with 0 and -1 past the last new token."""
+    _check(load_library().hpc_block_table_append(
+        _ref(make_tensor(seq_lens)), _ref(make_tensor(new_lens)), _ref(make_tensor(free_blocks)),
+        _ref(make_tensor(free_count)), int(num_blocks), _ref(make_tensor(block_table)),
+        _ref(make_tensor(seq_lens_out)), _ref(make_tensor(cu_q_lens)),
+        _ref(make_tensor(positions)), _ref(make_tensor(slots)), _ref(make_tensor(free_count_out)),
+        _err_ptr(device_error), _stream_ptr(stream)))
+
+
+def hpc_block_table_truncate(seq_lens, to_lens, block_table, num_blocks: int, free_blocks,
+                             free_count, seq_lens_out, free_count_out, device_error=None,
+                             stream=None):
+    """Shorten every sequence to min(seq_lens[b], to_lens[b]) tokens and push the
+    blocks behind it on the stack free_blocks[:free_count] (0 releases a
+    finished sequence); undoes hpc_block_table_append exactly."""
+    _check(load_library().hpc_block_table_truncate(
+        _ref(make_tensor(seq_lens)), _ref(make_tensor(to_lens)), _ref(make_tensor(block_table)),
+        int(num_blocks), _ref(make_tensor(free_blocks)), _ref(make_tensor(free_count)),
+        _ref(make_tensor(seq_lens_out)), _ref(make_tensor(free_count_out)),
+        _err_ptr(device_error), _stream_ptr(stream)))

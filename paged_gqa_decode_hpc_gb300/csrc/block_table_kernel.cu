@@ -1,0 +1,305 @@
+// Block tables, slot maps and positions of a step, built on the GPU from the
+// sequences' lengths, and the way back: the blocks behind a shortened
+// sequence returned to the stack of free ones.
+//
+// With o_b tokens in the cache, n_b new ones and 64-token blocks, sequence b
+// takes a_b = ceil((o_b + n_b) / 64) - ceil(o_b / 64) blocks from the top of
+// the stack. With A_b and N_b the exclusive prefix sums of a and n,
+//   table[b][ceil(o_b / 64) + i] = free[count - 1 - (A_b + i)],   i < a_b
+//   token N_b + i of the step: position o_b + i, slot
+//   64 * table[b][position / 64] + position % 64,                 i < n_b.
+// Every place is a closed form of two prefix sums, so the result is the same
+// in every run: no atomic hands out blocks. Truncating pushes the blocks so
+// that the first released block ends on top; a truncate to the old lengths
+// therefore undoes an append exactly, stack order included.
+//
+// What bounds it: latency. A decode step of 256 sequences moves 7 KB, and
+// prefill chunks of half a million tokens 4 MB. So each call is one launch of
+// ONE cluster of 1 or 8 CTAs: every CTA scans all the lengths itself
+// (warp shuffles, no exchange between CTAs) and then takes its share of the
+// tokens and blocks, finding the sequence of each by binary search in shared
+// memory. The lengths and the stack's count may be updated in place: each CTA
+// has read them before the cluster barrier, and the first CTA writes them
+// after it; no counter in global memory, so nothing is left over between
+// calls and captured graphs may run side by side.
+//
+// A call that cannot be met as a whole (too few free blocks, a table or token
+// buffer too small, a bad length) is refused as a whole: every CTA comes to
+// the same verdict from the same sums.
+#include "cache_ops.h"
+#include "hpc_internal.h"
+#include "ptx.cuh"
+
+namespace hpc {
+
+namespace {
+
+constexpr int kThreads = 1024;
+
+__device__ __forceinline__ int ceil_block(int x) {
+  return (int)(((int64_t)x + kBlockTokens - 1) / kBlockTokens);
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Inclusive block scan of a pair of 64-bit sums.
+__device__ __forceinline__ void block_scan2(int64_t& a, int64_t& b, int64_t (*warp_tot)[32],
+                                            int64_t& tot_a, int64_t& tot_b) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
+    if (lane >= o) {
+      a += x;
+      b += y;
+    }
+  }
+  if (lane == 31) {
+    warp_tot[0][warp] = a;
+    warp_tot[1][warp] = b;
+  }
+  __syncthreads();
+  if (warp < 2) {
+    int64_t t = warp_tot[warp][lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, t, o);
+      if (lane >= o) t += x;
+    }
+    warp_tot[warp][lane] = t;
+  }
+  __syncthreads();
+  if (warp > 0) {
+    a += warp_tot[0][warp - 1];
+    b += warp_tot[1][warp - 1];
+  }
+  tot_a = warp_tot[0][31];
+  tot_b = warp_tot[1][31];
+  __syncthreads();  // warp_tot is used again
+}
+
+// Last index i of sum[0 .. n] (non-decreasing, sum[0] = 0) with sum[i] <= x;
+// for x < sum[n] that is the sequence that holds item x.
+__device__ __forceinline__ int find(const int32_t* sum, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (sum[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) {
+  extern __shared__ int32_t sm[];
+  __shared__ int64_t warp_tot[2][32];
+  __shared__ int s_bad;  // HPC_DEVCHK_* bits of every thread
+  const int B = p.num_seqs, tid = threadIdx.x;
+  int32_t* old = sm;            // [B]
+  int32_t* tok = sm + B;        // [B + 1] first token of each sequence
+  int32_t* blk = tok + B + 1;   // [B + 1] first new block of each sequence
+  griddep_wait();
+  griddep_launch_dependents();
+  const int rank = (int)cluster_rank();
+  const int gtid = rank * kThreads + tid, gstep = (int)cluster_size() * kThreads;
+
+  const int32_t count = *p.count;
+  int bad = (count < 0 || count > p.free_cap) ? HPC_DEVCHK_CAPACITY : 0;
+  int64_t tokens = 0, blocks = 0;
+  if (tid == 0) tok[0] = blk[0] = s_bad = 0;
+  __syncthreads();
+  for (int base = 0; base < B; base += kThreads) {
+    const int b = base + tid;
+    int64_t n = 0, a = 0;
+    if (b < B) {
+      const int o = p.lens[b], m = p.new_lens[b];
+      old[b] = o;
+      if (o < 0 || m < 0 || (int64_t)o + m > INT32_MAX) {
+        bad |= HPC_DEVCHK_BAD_LENGTH;
+      } else {
+        const int b1 = ceil_block(o + m);
+        if (b1 > p.max_blocks) bad |= HPC_DEVCHK_TABLE_TOO_SHORT;
+        n = m;
+        a = b1 - ceil_block(o);
+      }
+    }
+    int64_t tn, ta;
+    block_scan2(n, a, warp_tot, tn, ta);
+    if (b < B) {  // sums past int32 belong to a call that is refused below
+      tok[b + 1] = (int32_t)(tokens + n);
+      blk[b + 1] = (int32_t)(blocks + a);
+    }
+    tokens += tn;
+    blocks += ta;
+  }
+  if (tokens > p.cap_tokens) bad |= HPC_DEVCHK_CAPACITY;
+  if (blocks > count) bad |= HPC_DEVCHK_NO_BLOCKS;
+  if (bad) atomicOr(&s_bad, bad);
+  __syncthreads();
+  const int any = s_bad;
+
+  cluster_sync();  // every CTA has read the lengths and the count
+  if (any) {
+    if (rank == 0) {
+      if (tid == 0) {
+        if (p.err) atomicOr(p.err, any);
+        *p.count_out = count;
+      }
+      for (int b = tid; b < B; b += kThreads) p.lens_out[b] = old[b];
+      for (int b = tid; b <= B; b += kThreads) p.cu[b] = 0;
+    }
+    for (int t = gtid; t < p.cap_tokens; t += gstep) {
+      p.slots[t] = -1;
+      p.positions[t] = 0;
+    }
+    return;
+  }
+  if (rank == 0) {
+    if (tid == 0) *p.count_out = (int32_t)(count - blocks);
+    for (int b = tid; b < B; b += kThreads) p.lens_out[b] = old[b] + (tok[b + 1] - tok[b]);
+    for (int b = tid; b <= B; b += kThreads) p.cu[b] = tok[b];
+  }
+  // an id outside [0, num_blocks) would make slots of another cache's memory
+  auto checked = [&](int32_t id) -> int32_t {
+    if ((uint32_t)id < (uint32_t)p.num_blocks) return id;
+    if (p.err) atomicOr(p.err, HPC_DEVCHK_BAD_BLOCK);
+    return -1;
+  };
+  for (int x = gtid; x < (int)blocks; x += gstep) {
+    const int b = find(blk, B, x);
+    p.table[b * p.bt_sb + ceil_block(old[b]) + (x - blk[b])] = checked(p.free_blocks[count - 1 - x]);
+  }
+  for (int t = gtid; t < p.cap_tokens; t += gstep) {
+    int32_t slot = -1, pos = 0;
+    if (t < (int)tokens) {
+      const int b = find(tok, B, t);
+      pos = old[b] + (t - tok[b]);
+      const int j = pos / kBlockTokens, fresh = j - ceil_block(old[b]);
+      const int32_t id = checked(fresh >= 0 ? p.free_blocks[count - 1 - (blk[b] + fresh)]
+                                            : p.table[b * p.bt_sb + j]);
+      if (id >= 0) slot = id * kBlockTokens + pos % kBlockTokens;
+    }
+    p.slots[t] = slot;
+    p.positions[t] = pos;
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) truncate_kernel(const TruncateParams p) {
+  extern __shared__ int32_t sm[];
+  __shared__ int64_t warp_tot[2][32];
+  __shared__ int s_bad;  // HPC_DEVCHK_* bits of every thread
+  const int B = p.num_seqs, tid = threadIdx.x;
+  int32_t* keep = sm;          // [B]
+  int32_t* blk = sm + B;       // [B + 1] first released block of each sequence
+  griddep_wait();
+  griddep_launch_dependents();
+  const int rank = (int)cluster_rank();
+  const int gtid = rank * kThreads + tid, gstep = (int)cluster_size() * kThreads;
+
+  const int32_t count = *p.count;
+  int bad = (count < 0 || count > p.free_cap) ? HPC_DEVCHK_CAPACITY : 0;
+  int64_t blocks = 0;
+  if (tid == 0) blk[0] = s_bad = 0;
+  __syncthreads();
+  for (int base = 0; base < B; base += kThreads) {
+    const int b = base + tid;
+    int64_t a = 0, none = 0;
+    if (b < B) {
+      const int n = p.lens[b], to = p.to_lens[b];
+      const int k = to < n ? to : n;
+      keep[b] = k;
+      if (n < 0 || to < 0) {
+        bad |= HPC_DEVCHK_BAD_LENGTH;
+      } else {
+        a = ceil_block(n) - ceil_block(k);
+        if (a > 0 && ceil_block(n) > p.max_blocks) bad |= HPC_DEVCHK_TABLE_TOO_SHORT;
+      }
+    }
+    int64_t ta, tn;
+    block_scan2(a, none, warp_tot, ta, tn);
+    if (b < B) blk[b + 1] = (int32_t)(blocks + a);
+    blocks += ta;
+  }
+  if (count + blocks > p.free_cap) bad |= HPC_DEVCHK_CAPACITY;
+  if (bad) atomicOr(&s_bad, bad);
+  __syncthreads();
+  const int any = s_bad;
+
+  if (any && rank == 0)  // refused: the lengths as they were, read again before anyone writes
+    for (int b = tid; b < B; b += kThreads) keep[b] = p.lens[b];
+  cluster_sync();  // every CTA has read the lengths and the count
+  if (rank == 0) {
+    if (tid == 0) {
+      if (any && p.err) atomicOr(p.err, any);
+      *p.count_out = any ? count : (int32_t)(count + blocks);
+    }
+    for (int b = tid; b < B; b += kThreads) p.lens_out[b] = keep[b];
+  }
+  if (any) return;
+  for (int x = gtid; x < (int)blocks; x += gstep) {
+    const int b = find(blk, B, x);
+    int32_t id = p.table[b * p.bt_sb + ceil_block(keep[b]) + (x - blk[b])];
+    if ((uint32_t)id >= (uint32_t)p.num_blocks) {
+      if (p.err) atomicOr(p.err, HPC_DEVCHK_BAD_BLOCK);
+      id = -1;
+    }
+    p.free_blocks[count + (int)blocks - 1 - x] = id;
+  }
+}
+
+template <typename P>
+cudaError_t launch_cluster(void (*kernel)(P), const P& p, int ctas, size_t smem,
+                           std::atomic<uint64_t>& configured, cudaStream_t stream) {
+  const cudaError_t e = once_per_device(configured, [&] {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (3 * kBlockTableMaxSeqs + 2) * (int)sizeof(int32_t));
+  });
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)ctas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+// CTAs of the cluster for a call of at most `items` tokens or blocks: one
+// while a thread has at most two items, else 8 (the portable cluster size).
+int cluster_for(int64_t items) { return items <= 2 * kThreads ? 1 : 8; }
+
+}  // namespace
+
+cudaError_t launch_append(const AppendParams& p, cudaStream_t stream) {
+  static std::atomic<uint64_t> configured{0};
+  return launch_cluster(append_kernel, p, cluster_for(p.cap_tokens),
+                        (size_t)(3 * p.num_seqs + 2) * sizeof(int32_t), configured, stream);
+}
+
+cudaError_t launch_truncate(const TruncateParams& p, cudaStream_t stream) {
+  static std::atomic<uint64_t> configured{0};
+  return launch_cluster(truncate_kernel, p,
+                        cluster_for((int64_t)p.num_seqs * p.max_blocks),
+                        (size_t)(2 * p.num_seqs + 1) * sizeof(int32_t), configured, stream);
+}
+
+}  // namespace hpc

@@ -17,11 +17,14 @@ namespace hpc {
 
 namespace {
 thread_local std::string g_last_error;
+}  // namespace
 
 hpc_status fail(hpc_status st, const std::string& msg) {
   g_last_error = msg;
   return st;
 }
+
+namespace {
 
 #define HPC_CUDA_TRY(expr)                                                                  \
   do {                                                                                      \
@@ -31,6 +34,8 @@ hpc_status fail(hpc_status st, const std::string& msg) {
                   std::string(#expr) + ": " + cudaGetErrorString(e__));                     \
     }                                                                                       \
   } while (0)
+
+}  // namespace
 
 unsigned long long wait_limit_ns() {
   static unsigned long long v = [] {
@@ -52,6 +57,7 @@ bool withhold_copies() {
   return s && s[0] == '1';
 }
 
+namespace {
 // Smallest q_len (new tokens per sequence) that hpc_decode_attn* and
 // hpc_decode_step run on the tensor-core decode kernel (decode_tc_kernel.cu)
 // instead of the one-warp-per-token kernel (attn_kernel.cu); values above
@@ -81,6 +87,8 @@ int32_t decode_plan_parts(const hpc_tensor* q, const hpc_tensor* k_cache, int32_
   return (int32_t)std::max<int64_t>(1, num_sms / hkv);
 }
 
+}  // namespace
+
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
     void* ptr = nullptr;
@@ -94,6 +102,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
+namespace {
 void free_plan(hpc_plan_s* pl) {
   if (!pl) return;
   if (pl->d_words) cudaFree(pl->d_words);
@@ -145,9 +154,11 @@ int elt_bytes(int32_t dt) {
   }
 }
 
+}  // namespace
+
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-hpc_status check_tensor(const hpc_tensor* t, const char* name, int ndim, bool nullable = false) {
+hpc_status check_tensor(const hpc_tensor* t, const char* name, int ndim, bool nullable) {
   if (!t || !t->data) {
     if (nullable && (!t || !t->data)) return HPC_OK;
     return fail(HPC_ERR_INVALID_ARG, std::string(name) + " is null");
@@ -195,6 +206,7 @@ hpc_status make_kv_map(const hpc_tensor* t, bool fp8, bool swap, CUtensorMap* ma
   return HPC_OK;
 }
 
+namespace {
 // Copy a capacity-layout word array into the canonical export layout.
 hpc_status write_canonical(const int32_t* w, const PlanLayout& L, int32_t* buf, int64_t cap,
                            int64_t* len) {

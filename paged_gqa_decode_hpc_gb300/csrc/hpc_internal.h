@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -245,6 +246,15 @@ constexpr int32_t kFusedPlanMaxSeqs = 3072;
 cudaError_t launch_merge(const MergeParams& p, int32_t num_kv_heads, cudaStream_t stream);
 
 void set_error(const std::string& msg);
+
+// Shared by the entry-point files (capi.cu, capi_cache.cu).
+hpc_status fail(hpc_status st, const std::string& msg);  // records hpc_last_error's message
+unsigned long long wait_limit_ns();                      // limit of the kernels' waits
+bool withhold_copies();                                  // failure-path test switch
+bool aligned(const void* p, uintptr_t a);
+hpc_status check_tensor(const hpc_tensor* t, const char* name, int ndim, bool nullable = false);
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
+hpc_status make_kv_map(const hpc_tensor* t, bool fp8, bool swap, CUtensorMap* map);
 
 // Every argument check hpc_decode_attn makes, with no launch and no
 // allocation (capi.cu).
