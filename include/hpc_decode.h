@@ -509,7 +509,8 @@ hpc_status hpc_extend_attn_ex(const hpc_tensor* q, const hpc_tensor* k_cache,
  * than max_blocks), CAPACITY (more new tokens than cap_tokens, or a count
  * outside the stack), NO_BLOCKS (more blocks needed than free). Apart from the
  * two in-place forms no output may overlap an input or another output
- * (HPC_ERR_INVALID_ARG). One launch; allocates nothing.
+ * (HPC_ERR_INVALID_ARG). One launch (two for more than 32768 tokens); allocates
+ * nothing.
  */
 hpc_status hpc_block_table_append(const hpc_tensor* seq_lens, const hpc_tensor* new_lens,
                                   const hpc_tensor* free_blocks, const hpc_tensor* free_count,

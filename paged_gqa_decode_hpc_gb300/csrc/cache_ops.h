@@ -14,6 +14,10 @@ namespace hpc {
 // two prefix sums) in one CTA's shared memory.
 constexpr int32_t kBlockTableMaxSeqs = 16384;
 
+// What one launch of the append kernel writes: everything, the tokens and
+// table entries only, or the lengths, their sums and the count only.
+enum AppendParts { kAppendAll = 0, kAppendTokens, kAppendLengths };
+
 struct AppendParams {
   const int32_t* lens;          // [B] tokens in the cache
   const int32_t* new_lens;      // [B] tokens to add
@@ -29,8 +33,10 @@ struct AppendParams {
   int32_t* positions;           // [cap_tokens]
   int32_t* slots;               // [cap_tokens]
   int32_t cap_tokens;
+  int32_t vec4;                 // positions and slots are 16-byte aligned
   int32_t* count_out;           // [1], may alias count
   int32_t* err;                 // may be null
+  int32_t parts;                // AppendParts, set by launch_append
 };
 cudaError_t launch_append(const AppendParams& p, cudaStream_t stream);
 

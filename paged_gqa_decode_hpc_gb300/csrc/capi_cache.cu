@@ -36,7 +36,7 @@ hpc_status check_vec(const hpc_tensor* t, const char* name, int64_t n) {
     return fail(HPC_ERR_INVALID_ARG, std::string(name) + " must be contiguous device int32" +
                                          (n >= 0 ? " [" + std::to_string(n) + "]" : ""));
   if (!aligned(t->data, 4)) return fail(HPC_ERR_INVALID_ARG, std::string(name) + " is misaligned");
-  if (t->shape[0] > INT_MAX) return fail(HPC_ERR_INVALID_ARG, std::string(name) + " is too long");
+  if (t->shape[0] > INT_MAX - 4) return fail(HPC_ERR_INVALID_ARG, std::string(name) + " is too long");
   return HPC_OK;
 }
 
@@ -138,6 +138,7 @@ hpc_status hpc_block_table_append(const hpc_tensor* seq_lens, const hpc_tensor* 
     p.positions = (int32_t*)positions->data;
     p.slots = (int32_t*)slots->data;
     p.cap_tokens = (int32_t)positions->shape[0];
+    p.vec4 = aligned(p.positions, 16) && aligned(p.slots, 16);
     p.count_out = (int32_t*)free_count_out->data;
     p.err = device_error;
     const cudaError_t e = launch_append(p, (cudaStream_t)stream);

@@ -123,6 +123,15 @@ def test_append_refuses_as_a_whole(name, in_place):
     assert bits
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+def test_append_of_many_tokens_refused(in_place):
+    c = _case(random.Random(6), 60, 500, 2000, pad=5)
+    assert c["cap"] > 32768
+    c["count"] -= 4  # one block too few
+    _, bits = _check_append(c, _append(c, in_place))
+    assert bits == R.NO_BLOCKS
+
+
 def test_append_huge_sums_do_not_wrap():
     # 3000 sequences of 2^30 new tokens: the sum passes 2^41
     c = dict(old=[0] * 3000, new=[2**30] * 3000, table=[[-1]] * 3000, free=[0], count=1, blocks=1,
