@@ -548,6 +548,86 @@ hpc_status hpc_block_table_truncate(const hpc_tensor* seq_lens, const hpc_tensor
                                     hpc_tensor* seq_lens_out, hpc_tensor* free_count_out,
                                     int32_t* device_error, void* stream);
 
+/*
+ * hpc_rope -- a table of rotary frequencies, made once by hpc_rope_init and
+ * passed by hpc_rope_kv_write to its kernel (host memory, plain data).
+ */
+typedef struct {
+  int32_t rot_dim;      /* the first rot_dim elements of a head turn */
+  int32_t interleaved;  /* pairs (2i, 2i + 1); else (i, i + rot_dim / 2) */
+  float magnitude;      /* factor on cosine and sine */
+  float freq_hi[64];    /* angle per position of pair i = freq_hi[i] + freq_lo[i] */
+  float freq_lo[64];
+} hpc_rope;
+
+#define HPC_ROPE_NONE 0    /* f_i = base^(-2i / rot_dim) */
+#define HPC_ROPE_LINEAR 1  /* f_i / factor (positions interpolated) */
+#define HPC_ROPE_BASE 2    /* base * factor^(rot_dim / (rot_dim - 2)) in base's place */
+#define HPC_ROPE_BANDED 3  /* by wavelength: see hpc_rope_init */
+#define HPC_ROPE_RAMP 4    /* by pair index, with a magnitude: see hpc_rope_init */
+
+/*
+ * hpc_rope_init -- fill a frequency table (no device is touched). With R =
+ * rot_dim and f_i = base^(-2i / R), i < R / 2:
+ *   HPC_ROPE_BANDED: t_i = original_len f_i / (2 pi), the turns of pair i over
+ *     the original_len positions trained on; w = clamp((t_i - low) / (high -
+ *     low), 0, 1); the frequency becomes w f_i + (1 - w) f_i / factor.
+ *   HPC_ROPE_RAMP: d(t) = R ln(original_len / (2 pi t)) / (2 ln base) is the
+ *     (real) pair index of t turns; with a = max(0, floor d(high)), b =
+ *     min(R - 1, ceil d(low)) and u = clamp((i - a) / max(b - a, 0.001), 0, 1)
+ *     the frequency becomes u f_i / factor + (1 - u) f_i, and the magnitude is
+ *     0.1 ln(factor) + 1.
+ *   rot_dim      even, 2 .. 128 (HPC_ROPE_BASE: above 2)
+ *   base         > 1
+ *   factor       >= 1 (not read for HPC_ROPE_NONE)
+ *   original_len, low, high  for BANDED and RAMP: > 0, low < high (turns)
+ *   magnitude    0: 1, or the ramp's; > 0: this value
+ */
+hpc_status hpc_rope_init(hpc_rope* rope, int32_t rot_dim, int32_t interleaved, double base,
+                         int32_t scaling, double factor, int32_t original_len, double low,
+                         double high, double magnitude);
+
+/*
+ * hpc_rope_kv_write -- rotary positions of a ragged batch of tokens and the
+ * write of their K and V into the cache: hpc_rope_norm_kv_write for any number
+ * of tokens per sequence (prefill chunks, drafts, decode), any part of the
+ * head, both pair layouts and scaled frequencies. Token n sits at position
+ * positions[n] and goes to slot slots[n] % 64 of block slots[n] / 64 (as
+ * hpc_block_table_append gives them):
+ *   q' = turn(norm(q)), k' = turn(norm(k)); norm(x) = x / sqrt(mean(x^2) + eps)
+ *   * weight over head_dim, or x where the weight is NULL; turn rotates pair
+ *   (a, b) to magnitude * (a cos t - b sin t, b cos t + a sin t), t =
+ *   positions[n] * f_i, and passes elements past rot_dim through;
+ *   q' is written to q_out (bf16) and, if given, e4m3(q' / scale) to q_out_fp8;
+ *   k' and v go to the cache (bf16, or e4m3(x / scale) rounded to nearest even,
+ *   saturating at 448).
+ *   q_in [N][H_q][128], k_in / v_in [N][H_kv][128], q_out [N][H_q][128]: device
+ *       bf16, rows contiguous, other strides multiples of 8 elements, bases
+ *       16-byte aligned (slices of one projection's output pass as views);
+ *       q_out may be q_in itself (the same strides), and must not overlap it
+ *       otherwise
+ *   positions, slots  device int32 [N]. slots[n] < 0 marks padding: nothing is
+ *       written for the token. A position outside [0, 2^24) sets
+ *       HPC_DEVCHK_BAD_LENGTH and skips the token; a slot past the cache sets
+ *       HPC_DEVCHK_BAD_BLOCK and skips the cache write. Two tokens of one call
+ *       must not name the same slot.
+ *   rope    from hpc_rope_init
+ *   q_norm_weight, k_norm_weight  device bf16 or f32 [128], 16-byte aligned, or
+ *       NULL (no norm)
+ *   k_cache, v_cache  [num_blocks][H_kv][64][128] bf16 or fp8_e4m3 (both the
+ *       same shape and strides, innermost 1, others multiples of 8 elements),
+ *       written in place
+ *   device_error  optional device int32 receiving HPC_DEVCHK_* bits
+ * H_q a multiple of H_kv; head_dim 128 and 64-token blocks (else
+ * HPC_ERR_UNSUPPORTED). One launch; allocates nothing.
+ */
+hpc_status hpc_rope_kv_write(const hpc_tensor* q_in, const hpc_tensor* k_in, const hpc_tensor* v_in,
+                             const hpc_tensor* positions, const hpc_tensor* slots,
+                             const hpc_rope* rope, const hpc_tensor* q_norm_weight,
+                             const hpc_tensor* k_norm_weight, float eps, hpc_tensor* q_out,
+                             hpc_tensor* q_out_fp8, hpc_tensor* k_cache, hpc_tensor* v_cache,
+                             int32_t* device_error, void* stream);
+
 /* hpc_device_sm_count -- streaming multiprocessors of the current device. */
 hpc_status hpc_device_sm_count(int32_t* num_sms);
 

@@ -28,7 +28,8 @@ __all__ = [
     "hpc_decode_plan_set_timing_events", "hpc_decode_attn_noalloc", "hpc_decode_step",
     "hpc_decode_step_host",
     "hpc_rope_norm_kv_write", "hpc_extend_attn", "hpc_decode_tc_min_q_len",
-    "hpc_block_table_append", "hpc_block_table_truncate",
+    "hpc_block_table_append", "hpc_block_table_truncate", "HpcRope", "hpc_rope_init",
+    "hpc_rope_kv_write",
     "HPC_OK", "HPC_ERR_INVALID_ARG", "HPC_ERR_UNSUPPORTED", "HPC_ERR_CUDA", "HPC_ERR_OOM",
     "HPC_ERR_DEVICE_CHECK",
 ]
@@ -55,6 +56,13 @@ class HpcTensor(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("ndim", ctypes.c_int32),
                 ("shape", ctypes.c_int64 * 4), ("stride", ctypes.c_int64 * 4),
                 ("scale", ctypes.c_float)]
+
+
+class HpcRope(ctypes.Structure):
+    """A table of rotary frequencies (hpc_rope), made by hpc_rope_init."""
+    _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("magnitude", ctypes.c_float), ("freq_hi", ctypes.c_float * 64),
+                ("freq_lo", ctypes.c_float * 64)]
 
 
 _lib = None
@@ -87,7 +95,7 @@ def load_library():
         lib = ctypes.CDLL(path)
         P, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
         pi32, pi64 = ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int64)
-        T, D = ctypes.POINTER(HpcTensor), ctypes.c_char_p
+        T, D, F64 = ctypes.POINTER(HpcTensor), ctypes.c_char_p, ctypes.c_double
         sigs = {
             "hpc_decode_plan": [pi32, i32, i32, ctypes.POINTER(P)],
             "hpc_decode_plan_ex": [pi32, i32, i32, i32, ctypes.POINTER(P)],
@@ -115,6 +123,9 @@ def load_library():
             # descriptors packed by _desc
             "hpc_block_table_append": [D, D, D, D, i32, D, D, D, D, D, D, P, P],
             "hpc_block_table_truncate": [D, D, D, i32, D, D, D, D, P, P],
+            "hpc_rope_init": [ctypes.POINTER(HpcRope), i32, i32, F64, i32, F64, i32, F64, F64, F64],
+            "hpc_rope_kv_write": [D, D, D, D, D, ctypes.POINTER(HpcRope), D, D, ctypes.c_float,
+                                  D, D, D, D, P, P],
         }
         for name, args in sigs.items():
             fn = getattr(lib, name)
@@ -497,4 +508,36 @@ def hpc_block_table_truncate(seq_lens, to_lens, block_table, num_blocks: int, fr
         _desc(seq_lens), _desc(to_lens), _desc(block_table),
         int(num_blocks), _desc(free_blocks), _desc(free_count),
         _desc(seq_lens_out), _desc(free_count_out),
+        _err_ptr(device_error), _stream_ptr(stream)))
+
+
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "banded": 3, "ramp": 4}
+
+
+def hpc_rope_init(rot_dim: int = 128, interleaved: bool = False, base: float = 10000.0,
+                  scaling: str = "none", factor: float = 1.0, original_len: int = 0,
+                  low: float = 0.0, high: float = 0.0, magnitude: float = 0.0) -> HpcRope:
+    """A frequency table for hpc_rope_kv_write: the first rot_dim elements of a
+    head turn, in pairs (i, i + rot_dim / 2) or, interleaved, (2i, 2i + 1);
+    scaling one of ROPE_SCALINGS (formulas in include/hpc_decode.h)."""
+    if scaling not in ROPE_SCALINGS:
+        raise HpcError(HPC_ERR_INVALID_ARG, f"unknown scaling {scaling!r}")
+    r = HpcRope()
+    _check(load_library().hpc_rope_init(ctypes.byref(r), int(rot_dim), int(bool(interleaved)),
+                                        base, ROPE_SCALINGS[scaling], factor, int(original_len),
+                                        low, high, magnitude))
+    return r
+
+
+def hpc_rope_kv_write(q_in, k_in, v_in, positions, slots, rope: HpcRope, q_out, k_cache, v_cache,
+                      q_norm_weight=None, k_norm_weight=None, eps: float = 1e-6, q_out_fp8=None,
+                      q_fp8_scale: float = 1.0, k_scale: float = 1.0, v_scale: float = 1.0,
+                      device_error=None, stream=None):
+    """Rotary positions (and QK-norm where weights are given) of N tokens of any
+    sequences, and the write of their K and V rows into the paged cache at
+    `slots` (int32 [N], < 0: padding, skipped); `rope` from hpc_rope_init."""
+    _check(load_library().hpc_rope_kv_write(
+        _desc(q_in), _desc(k_in), _desc(v_in), _desc(positions), _desc(slots), rope,
+        _desc(q_norm_weight), _desc(k_norm_weight), eps, _desc(q_out),
+        _desc(q_out_fp8, q_fp8_scale), _desc(k_cache, k_scale), _desc(v_cache, v_scale),
         _err_ptr(device_error), _stream_ptr(stream)))

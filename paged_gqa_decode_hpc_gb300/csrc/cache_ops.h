@@ -56,4 +56,40 @@ struct TruncateParams {
 };
 cudaError_t launch_truncate(const TruncateParams& p, cudaStream_t stream);
 
+// Positions of the rotary kernel are exact in fp32.
+constexpr int32_t kRopeMaxPosition = 1 << 24;
+
+struct RopeParams {
+  const __nv_bfloat16* q_in;    // [N][H_q][128]; strides in elements over token, head
+  int64_t qi_sn, qi_sh;
+  const __nv_bfloat16* k_in;
+  int64_t ki_sn, ki_sh;
+  const __nv_bfloat16* v_in;
+  int64_t vi_sn, vi_sh;
+  const int32_t* positions;     // [N]
+  const int32_t* slots;         // [N], < 0: padding
+  int64_t num_tokens;
+  int32_t num_q_heads, num_kv_heads, num_blocks;
+  const void* wq;               // norm weights, null: no norm
+  const void* wk;
+  int32_t wq_dtype, wk_dtype;
+  float eps;
+  int32_t rot_dim, interleaved;
+  float magnitude;
+  float two_pi[3];              // 2 pi as a sum of floats
+  float freq_hi[64], freq_lo[64];
+  __nv_bfloat16* q_out;
+  int64_t qo_sn, qo_sh;
+  uint8_t* q_fp8;               // may be null
+  int64_t qf_sn, qf_sh;
+  float q_fp8_scale;
+  void* k_cache;
+  void* v_cache;
+  int64_t c_sblk, c_shead, c_sslot;
+  int32_t cache_fp8;
+  float k_scale, v_scale;
+  int32_t* err;                 // may be null
+};
+cudaError_t launch_rope(const RopeParams& p, int sm_count, cudaStream_t stream);
+
 }  // namespace hpc

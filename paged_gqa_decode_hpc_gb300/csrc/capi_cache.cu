@@ -1,6 +1,9 @@
 // C ABI of the calls that maintain the paged cache: block tables and slot
-// maps. See include/hpc_decode.h for the contract of every call.
+// maps, rotary positions with the KV write. See include/hpc_decode.h for the contract of every call.
+#include <algorithm>
 #include <climits>
+#include <cmath>
+#include <cstring>
 #include <string>
 
 #include "cache_ops.h"
@@ -188,6 +191,202 @@ hpc_status hpc_block_table_truncate(const hpc_tensor* seq_lens, const hpc_tensor
     const cudaError_t e = launch_truncate(p, (cudaStream_t)stream);
     if (e != cudaSuccess)
       return fail(HPC_ERR_CUDA, std::string("truncate launch: ") + cudaGetErrorString(e));
+    return HPC_OK;
+  });
+}
+
+hpc_status hpc_rope_init(hpc_rope* rope, int32_t rot_dim, int32_t interleaved, double base,
+                         int32_t scaling, double factor, int32_t original_len, double low,
+                         double high, double magnitude) {
+  return guarded([&]() -> hpc_status {
+    if (!rope) return fail(HPC_ERR_INVALID_ARG, "rope is null");
+    if (rot_dim < 2 || rot_dim > kHeadDim || rot_dim % 2)
+      return fail(HPC_ERR_INVALID_ARG, "rot_dim must be even, 2 to 128");
+    if (!(base > 1.0) || !std::isfinite(base))
+      return fail(HPC_ERR_INVALID_ARG, "base must be finite and above 1");
+    if (scaling < HPC_ROPE_NONE || scaling > HPC_ROPE_RAMP)
+      return fail(HPC_ERR_INVALID_ARG, "unknown scaling");
+    if (!(magnitude >= 0.0) || !std::isfinite(magnitude))
+      return fail(HPC_ERR_INVALID_ARG, "magnitude must be finite and >= 0 (0: by the scaling)");
+    if (scaling != HPC_ROPE_NONE && (!(factor >= 1.0) || !std::isfinite(factor)))
+      return fail(HPC_ERR_INVALID_ARG, "factor must be finite and at least 1");
+    if (scaling == HPC_ROPE_BASE && rot_dim == 2)
+      return fail(HPC_ERR_INVALID_ARG, "scaling the base needs rot_dim > 2");
+    const bool bands = scaling == HPC_ROPE_BANDED || scaling == HPC_ROPE_RAMP;
+    if (bands && (original_len <= 0 || !(low > 0.0) || !(high > low) || !std::isfinite(high)))
+      return fail(HPC_ERR_INVALID_ARG, "need original_len > 0 and 0 < low < high");
+    const double two_pi = 2.0 * 3.14159265358979323846;
+    const int R = rot_dim;
+    if (scaling == HPC_ROPE_BASE) base *= std::pow(factor, R / (R - 2.0));
+    // the pair whose wavelength makes `turns` turns over the trained positions
+    auto pair_of = [&](double turns) {
+      return R * std::log(original_len / (turns * two_pi)) / (2.0 * std::log(base));
+    };
+    double ramp_lo = 0.0, ramp_hi = 1.0;
+    if (scaling == HPC_ROPE_RAMP) {
+      ramp_lo = std::max(0.0, std::floor(pair_of(high)));
+      ramp_hi = std::min(R - 1.0, std::ceil(pair_of(low)));
+    }
+    hpc_rope r;
+    std::memset(&r, 0, sizeof r);
+    r.rot_dim = R;
+    r.interleaved = interleaved != 0;
+    double mag = magnitude;
+    if (mag == 0.0) mag = scaling == HPC_ROPE_RAMP ? 0.1 * std::log(factor) + 1.0 : 1.0;
+    r.magnitude = (float)mag;
+    for (int i = 0; i < R / 2; ++i) {
+      double f = std::pow(base, -2.0 * i / R);
+      auto clamp01 = [](double x) { return x < 0.0 ? 0.0 : x > 1.0 ? 1.0 : x; };
+      if (scaling == HPC_ROPE_LINEAR) {
+        f /= factor;
+      } else if (scaling == HPC_ROPE_BANDED) {
+        const double keep = clamp01((original_len * f / two_pi - low) / (high - low));
+        f = f * keep + f / factor * (1.0 - keep);
+      } else if (scaling == HPC_ROPE_RAMP) {
+        const double ramp = clamp01((i - ramp_lo) / std::max(ramp_hi - ramp_lo, 0.001));
+        f = f / factor * ramp + f * (1.0 - ramp);
+      }
+      r.freq_hi[i] = (float)f;
+      r.freq_lo[i] = (float)(f - (double)r.freq_hi[i]);
+    }
+    *rope = r;
+    return HPC_OK;
+  });
+}
+
+hpc_status hpc_rope_kv_write(const hpc_tensor* q_in, const hpc_tensor* k_in, const hpc_tensor* v_in,
+                             const hpc_tensor* positions, const hpc_tensor* slots,
+                             const hpc_rope* rope, const hpc_tensor* q_norm_weight,
+                             const hpc_tensor* k_norm_weight, float eps, hpc_tensor* q_out,
+                             hpc_tensor* q_out_fp8, hpc_tensor* k_cache, hpc_tensor* v_cache,
+                             int32_t* device_error, void* stream) {
+  return guarded([&]() -> hpc_status {
+    hpc_status st;
+    const hpc_tensor* rows[] = {q_in, k_in, v_in, q_out};
+    const char* names[] = {"q_in", "k_in", "v_in", "q_out"};
+    for (int i = 0; i < 4; ++i)
+      if (!empty(rows[i], 3) && (st = check_tensor(rows[i], names[i], 3)) != HPC_OK) return st;
+    const int64_t N = q_in->shape[0], Hq = q_in->shape[1], Hkv = k_in->shape[1];
+    if ((st = check_vec(positions, "positions", N)) != HPC_OK) return st;
+    if ((st = check_vec(slots, "slots", N)) != HPC_OK) return st;
+    if ((st = check_tensor(k_cache, "k_cache", 4)) != HPC_OK) return st;
+    if ((st = check_tensor(v_cache, "v_cache", 4)) != HPC_OK) return st;
+    if ((st = check_tensor(q_norm_weight, "q_norm_weight", 1, true)) != HPC_OK) return st;
+    if ((st = check_tensor(k_norm_weight, "k_norm_weight", 1, true)) != HPC_OK) return st;
+    const bool has_qf = q_out_fp8 && (q_out_fp8->data || empty(q_out_fp8, 3));
+    if (!rope) return fail(HPC_ERR_INVALID_ARG, "rope is null");
+    if (rope->rot_dim < 2 || rope->rot_dim > kHeadDim || rope->rot_dim % 2 ||
+        (rope->interleaved != 0 && rope->interleaved != 1) || !std::isfinite(rope->magnitude))
+      return fail(HPC_ERR_INVALID_ARG, "rope must come from hpc_rope_init");
+    for (int i = 0; i < rope->rot_dim / 2; ++i)
+      if (!(std::fabs(rope->freq_hi[i]) <= 1.f) || !(std::fabs(rope->freq_lo[i]) <= 1.f))
+        return fail(HPC_ERR_INVALID_ARG, "rope must come from hpc_rope_init");
+    for (const hpc_tensor* t : rows) {
+      if (t->dtype != HPC_BF16)
+        return fail(HPC_ERR_INVALID_ARG, "q_in, k_in, v_in and q_out must be bf16");
+      if (t->shape[2] != kHeadDim) return fail(HPC_ERR_UNSUPPORTED, "head_dim must be 128");
+      if (t->shape[0] != N) return fail(HPC_ERR_INVALID_ARG, "q/k/v/out hold different tokens");
+      if (t->stride[2] != 1 || t->stride[0] % 8 || t->stride[1] % 8 || !aligned(t->data, 16))
+        return fail(HPC_ERR_INVALID_ARG,
+                    "q/k/v/out rows must be contiguous and 16-byte aligned");
+    }
+    if (k_cache->shape[3] != kHeadDim) return fail(HPC_ERR_UNSUPPORTED, "head_dim must be 128");
+    if (k_cache->shape[2] != kBlockTokens)
+      return fail(HPC_ERR_UNSUPPORTED, "KV blocks must hold 64 tokens");
+    if (Hkv <= 0 || Hq <= 0 || Hq % Hkv || v_in->shape[1] != Hkv || q_out->shape[1] != Hq ||
+        k_cache->shape[1] != Hkv)
+      return fail(HPC_ERR_INVALID_ARG, "inconsistent heads of q/k/v/out/cache");
+    if (Hq > 65536 || Hkv > 65536) return fail(HPC_ERR_UNSUPPORTED, "at most 65536 heads");
+    // q may be rotated in place, rows on their own rows; anything else would
+    // read what another CTA has written
+    if (N > 0 && q_out->data == q_in->data &&
+        ((N > 1 && q_out->stride[0] != q_in->stride[0]) ||
+         (Hq > 1 && q_out->stride[1] != q_in->stride[1])))
+      return fail(HPC_ERR_INVALID_ARG, "q_out on q_in must have q_in's strides");
+    if (has_qf && (q_out_fp8->dtype != HPC_FP8_E4M3 || q_out_fp8->ndim != 3 ||
+                   q_out_fp8->shape[0] != N || q_out_fp8->shape[1] != Hq ||
+                   q_out_fp8->shape[2] != kHeadDim || q_out_fp8->stride[2] != 1 ||
+                   q_out_fp8->stride[0] % 8 || q_out_fp8->stride[1] % 8 ||
+                   q_out_fp8->stride[0] < 0 || q_out_fp8->stride[1] < 0 ||
+                   !aligned(q_out_fp8->data, 8) || !(q_out_fp8->scale > 0.f) ||
+                   !std::isfinite(q_out_fp8->scale)))
+      return fail(HPC_ERR_INVALID_ARG, "q_out_fp8 must be e4m3 [N][H_q][128] with a positive scale");
+    for (const hpc_tensor* w : {q_norm_weight, k_norm_weight})
+      if (w && w->data && ((w->dtype != HPC_BF16 && w->dtype != HPC_F32) ||
+                           w->shape[0] != kHeadDim || w->stride[0] != 1 || !aligned(w->data, 16)))
+        return fail(HPC_ERR_INVALID_ARG,
+                    "norm weights must be contiguous bf16/f32 [128], 16-B aligned");
+    if (!(eps >= 0.f) || !std::isfinite(eps))
+      return fail(HPC_ERR_INVALID_ARG, "eps must be finite and >= 0");
+    if (k_cache->dtype != v_cache->dtype ||
+        (k_cache->dtype != HPC_BF16 && k_cache->dtype != HPC_FP8_E4M3))
+      return fail(HPC_ERR_INVALID_ARG, "k_cache/v_cache must both be bf16 or both fp8_e4m3");
+    const bool fp8 = k_cache->dtype == HPC_FP8_E4M3;
+    for (int i = 0; i < 4; ++i)
+      if (k_cache->shape[i] != v_cache->shape[i] || k_cache->stride[i] != v_cache->stride[i])
+        return fail(HPC_ERR_INVALID_ARG, "k_cache and v_cache must have the same shape and strides");
+    const uintptr_t unit = fp8 ? 8 : 16;  // bytes of one store
+    if (k_cache->stride[3] != 1 || k_cache->stride[0] % 8 || k_cache->stride[1] % 8 ||
+        k_cache->stride[2] % 8 || !aligned(k_cache->data, unit) || !aligned(v_cache->data, unit))
+      return fail(HPC_ERR_INVALID_ARG, "cache rows must be contiguous and aligned to 8 elements");
+    if (fp8 && (!(k_cache->scale > 0.f) || !(v_cache->scale > 0.f) ||
+                !std::isfinite(k_cache->scale) || !std::isfinite(v_cache->scale)))
+      return fail(HPC_ERR_INVALID_ARG, "FP8 caches need positive finite scales");
+    if (N == 0) return HPC_OK;
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess)
+      return fail(HPC_ERR_CUDA, std::string("device query: ") + cudaGetErrorString(e));
+    RopeParams p;
+    std::memset(&p, 0, sizeof p);
+    p.q_in = (const __nv_bfloat16*)q_in->data; p.qi_sn = q_in->stride[0]; p.qi_sh = q_in->stride[1];
+    p.k_in = (const __nv_bfloat16*)k_in->data; p.ki_sn = k_in->stride[0]; p.ki_sh = k_in->stride[1];
+    p.v_in = (const __nv_bfloat16*)v_in->data; p.vi_sn = v_in->stride[0]; p.vi_sh = v_in->stride[1];
+    p.positions = (const int32_t*)positions->data;
+    p.slots = (const int32_t*)slots->data;
+    p.num_tokens = N;
+    p.num_q_heads = (int32_t)Hq;
+    p.num_kv_heads = (int32_t)Hkv;
+    p.num_blocks = (int32_t)(k_cache->shape[0] < INT_MAX ? k_cache->shape[0] : INT_MAX);
+    if (q_norm_weight && q_norm_weight->data) {
+      p.wq = q_norm_weight->data;
+      p.wq_dtype = q_norm_weight->dtype;
+    }
+    if (k_norm_weight && k_norm_weight->data) {
+      p.wk = k_norm_weight->data;
+      p.wk_dtype = k_norm_weight->dtype;
+    }
+    p.eps = eps;
+    p.rot_dim = rope->rot_dim;
+    p.interleaved = rope->interleaved;
+    p.magnitude = rope->magnitude;
+    std::memcpy(p.freq_hi, rope->freq_hi, sizeof p.freq_hi);
+    std::memcpy(p.freq_lo, rope->freq_lo, sizeof p.freq_lo);
+    // 2 pi = 6.28318530717958647692528676655900577; the double holds 53 bits,
+    // the third float takes what it leaves out as well
+    const double two_pi = 6.283185307179586;         // nearest double
+    const double rest = 2.4492935982947064e-16;      // 2 pi minus it
+    p.two_pi[0] = (float)two_pi;
+    p.two_pi[1] = (float)(two_pi - (double)p.two_pi[0]);
+    p.two_pi[2] = (float)(two_pi - (double)p.two_pi[0] - (double)p.two_pi[1] + rest);
+    p.q_out = (__nv_bfloat16*)q_out->data; p.qo_sn = q_out->stride[0]; p.qo_sh = q_out->stride[1];
+    if (has_qf) {
+      p.q_fp8 = (uint8_t*)q_out_fp8->data;
+      p.qf_sn = q_out_fp8->stride[0];
+      p.qf_sh = q_out_fp8->stride[1];
+      p.q_fp8_scale = q_out_fp8->scale;
+    }
+    p.k_cache = k_cache->data;
+    p.v_cache = v_cache->data;
+    p.c_sblk = k_cache->stride[0]; p.c_shead = k_cache->stride[1]; p.c_sslot = k_cache->stride[2];
+    p.cache_fp8 = fp8;
+    p.k_scale = fp8 ? k_cache->scale : 1.f;
+    p.v_scale = fp8 ? v_cache->scale : 1.f;
+    p.err = device_error;
+    e = launch_rope(p, sms, (cudaStream_t)stream);
+    if (e != cudaSuccess)
+      return fail(HPC_ERR_CUDA, std::string("rope launch: ") + cudaGetErrorString(e));
     return HPC_OK;
   });
 }
