@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "convert.cuh"
 #include "hpc_decode.h"
 
 namespace hpc {
@@ -82,12 +83,12 @@ struct RopeParams {
   int64_t qo_sn, qo_sh;
   uint8_t* q_fp8;               // may be null
   int64_t qf_sn, qf_sh;
-  float q_fp8_scale;
+  E4m3Scale q_fp8_scale;
   void* k_cache;
   void* v_cache;
   int64_t c_sblk, c_shead, c_sslot;
   int32_t cache_fp8;
-  float k_scale, v_scale;
+  E4m3Scale k_scale, v_scale;
   int32_t* err;                 // may be null
 };
 cudaError_t launch_rope(const RopeParams& p, int sm_count, cudaStream_t stream);

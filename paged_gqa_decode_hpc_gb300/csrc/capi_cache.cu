@@ -375,14 +375,14 @@ hpc_status hpc_rope_kv_write(const hpc_tensor* q_in, const hpc_tensor* k_in, con
       p.q_fp8 = (uint8_t*)q_out_fp8->data;
       p.qf_sn = q_out_fp8->stride[0];
       p.qf_sh = q_out_fp8->stride[1];
-      p.q_fp8_scale = q_out_fp8->scale;
+      p.q_fp8_scale = e4m3_scale(q_out_fp8->scale);
     }
     p.k_cache = k_cache->data;
     p.v_cache = v_cache->data;
     p.c_sblk = k_cache->stride[0]; p.c_shead = k_cache->stride[1]; p.c_sslot = k_cache->stride[2];
     p.cache_fp8 = fp8;
-    p.k_scale = fp8 ? k_cache->scale : 1.f;
-    p.v_scale = fp8 ? v_cache->scale : 1.f;
+    p.k_scale = e4m3_scale(fp8 ? k_cache->scale : 1.f);
+    p.v_scale = e4m3_scale(fp8 ? v_cache->scale : 1.f);
     p.err = device_error;
     e = launch_rope(p, sms, (cudaStream_t)stream);
     if (e != cudaSuccess)

@@ -15,15 +15,18 @@
 // right to about an ulp for every position below 2^24 (GB300's fp64 rate is
 // no way to get there).
 //
-// What bounds it: HBM. Each element is read and written once, and a token's
-// 64 (cos, sin) pairs are formed once per CTA for all its heads: a CTA is one
-// token, 16 half-warps take a row each (8 elements, 16 bytes, per lane), so a
-// lane keeps its pairs' cos and sin in registers for all rows. All rows' loads
-// (5 per half-warp for 64 + 16 heads) are in flight before the angles are
-// formed. With few tokens the rows of a token are spread over several CTAs.
-// A row's partner elements sit in another lane (half layout, R / 2 a multiple
-// of 8: shuffles), in the same lane (interleaved), or anywhere (half layout,
-// other R: through shared memory).
+// What bounds it: HBM, and next to it the instructions that a row costs. Each
+// element is read and written once, and a token's 64 (cos, sin) pairs are
+// formed once per CTA for all its heads. A CTA is one token; 8 lanes take a
+// row, 16 elements each as two 16-byte chunks chosen so that (half layout, R a
+// multiple of 16) an element and its partner lie in the same lane: chunk t and
+// chunk t + R / 16. Then a pair of pairs turns in four paired-fp32
+// instructions, no value moves between lanes, and a lane keeps its cos and sin
+// in registers for all rows. (16 lanes a row with the partner fetched by
+// shuffles took 83 us for 8192 tokens of 64 + 16 heads.) The rows' loads are in
+// flight before the angles are formed. With few tokens the rows of a token are
+// spread over several CTAs. Interleaved pairs lie in one lane anyway; the half
+// layout at other R goes through shared memory.
 #include <cuda_bf16.h>
 
 #include "cache_ops.h"
@@ -35,9 +38,10 @@ namespace hpc {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kRowsAtOnce = kThreads / 16;  // one row per half-warp
-constexpr int kUnroll = 5;                  // rows of a half-warp loaded together
+constexpr int kThreads = 128;
+constexpr int kLanes = 8;                        // lanes of a row
+constexpr int kRowsAtOnce = kThreads / kLanes;
+constexpr int kUnroll = 2;                       // rows of a lane loaded together
 
 enum Layout { kInterleaved = 0, kHalfLanes, kHalfAny };
 
@@ -62,160 +66,243 @@ __device__ __forceinline__ TurnPair turn(float fpos, float f_hi, float f_lo, con
   return {(c - s * r_lo) * p.magnitude, (s + c * r_lo) * p.magnitude};
 }
 
-__device__ __forceinline__ void unpack(uint4 u, float (&x)[8]) {
+// Paired fp32: two lanes' worth of FMA in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mov.b64 z, {%6, %7};\n\tfma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
+// 8 bf16 <-> 4 pairs of floats.
+__device__ __forceinline__ void unpack(uint4 u, float2* x) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
+  for (int i = 0; i < 4; ++i)
+    x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
 }
-__device__ __forceinline__ uint4 pack(const float (&x)[8]) {
+__device__ __forceinline__ uint4 pack(const float2* x) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    const __nv_bfloat162 v = __floats2bfloat162_rn(x[i].x, x[i].y);
     w[i] = *reinterpret_cast<const uint32_t*>(&v);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ uint2 quantise(const float (&x)[8], float scale) {
-  return make_uint2(quantise_e4m3x4(make_float4(x[0], x[1], x[2], x[3]), scale),
-                    quantise_e4m3x4(make_float4(x[4], x[5], x[6], x[7]), scale));
+__device__ __forceinline__ uint2 quantise(const float2* x, const E4m3Scale& scale) {
+  const float v[8] = {x[0].x, x[0].y, x[1].x, x[1].y, x[2].x, x[2].y, x[3].x, x[3].y};
+  return quantise_e4m3x8(v, scale);
 }
-// Eight norm weights from element e0 on.
-__device__ __forceinline__ void load_weights(const void* w, int32_t dtype, int e0, float (&x)[8]) {
-  if (dtype == HPC_F32) {
-    const float4 a = *reinterpret_cast<const float4*>((const float*)w + e0);
-    const float4 b = *reinterpret_cast<const float4*>((const float*)w + e0 + 4);
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-  } else {
-    unpack(*reinterpret_cast<const uint4*>((const __nv_bfloat16*)w + e0), x);
-  }
+__device__ __forceinline__ float load_weight(const void* w, int32_t dtype, int i) {
+  return dtype == HPC_F32 ? ((const float*)w)[i] : __bfloat162float(((const __nv_bfloat16*)w)[i]);
 }
 
-template <int LAYOUT>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
-  __shared__ TurnPair s_turn[kHeadDim / 2];
+// CTAs per SM, which bounds the registers: 8 where nothing spills that counts
+// (8192 tokens: 52.7 us against 55.6 with 6), 6 with a norm (64 tokens: 3.36
+// against 3.52 us with 8), 5 where every element's partner comes from shared
+// memory.
+constexpr int min_ctas(int layout, bool norm) { return layout == 2 ? 5 : norm ? 6 : 8; }
+
+template <int LAYOUT, bool NORM>
+__global__ void __launch_bounds__(kThreads, min_ctas(LAYOUT, NORM))
+    rope_kernel(const __grid_constant__ RopeParams p) {
+  __shared__ float s_cos[kHeadDim / 2], s_sin[kHeadDim / 2];
+  __shared__ float s_w[NORM ? 2 : 1][kHeadDim];  // norm weights of q and k
   __shared__ float s_row[LAYOUT == kHalfAny ? kRowsAtOnce : 1][kHeadDim];
   griddep_wait();
   griddep_launch_dependents();
   const int64_t n = blockIdx.x;
-  const int half_warp = threadIdx.x >> 4, chunk = threadIdx.x & 15, e0 = 8 * chunk;
+  const int tid = threadIdx.x, row_of = tid / kLanes, lane = tid % kLanes;
   const int num_rows = p.num_q_heads + 2 * p.num_kv_heads;
-  const int pos = p.positions[n], slot = p.slots[n];
-  if (slot < 0) return;  // padding: nothing is written for it
-  if (pos < 0 || pos >= kRopeMaxPosition) {
-    if (threadIdx.x == 0 && blockIdx.y == 0 && p.err) atomicOr(p.err, HPC_DEVCHK_BAD_LENGTH);
-    return;
-  }
-  const int blk = slot / kBlockTokens;
-  const bool store_kv = blk < p.num_blocks;
-  if (!store_kv && threadIdx.x == 0 && blockIdx.y == 0 && p.err)
-    atomicOr(p.err, HPC_DEVCHK_BAD_BLOCK);
-  const int64_t cache_row = blk * p.c_sblk + (slot % kBlockTokens) * p.c_sslot + e0;
-
   const int R = p.rot_dim;
-  float c[8], s[8];  // of this lane's elements (interleaved: of its four pairs)
+  // this lane's two chunks of 8 elements
+  int ca = lane, cb = lane + kLanes;
+  if (LAYOUT == kHalfLanes) {
+    const int hop = R / 16;  // chunks between the halves; chunks past 2 hop pass through
+    ca = lane < hop ? lane : 2 * lane;
+    cb = lane < hop ? lane + hop : 2 * lane + 1;
+  }
+  const int ea = 8 * ca, eb = 8 * cb;
+  const int pos = p.positions[n], slot = p.slots[n];
+
   const int step = kRowsAtOnce * gridDim.y;  // rows the token's CTAs take together
-  // base: the CTA's first row of a batch of kUnroll rows per half-warp; all
-  // the loop's conditions are the CTA's, so its warps stay whole
+  float2 c[8], s[8];  // cos and signed sin of the lane's elements (see below)
+  int64_t cache_row = 0;
+  bool store_kv = false;
+  // base: the CTA's first row of a batch of kUnroll rows per lane; all the
+  // loop's conditions are the CTA's, so its warps stay whole
   for (int base = kRowsAtOnce * blockIdx.y; base < num_rows; base += step * kUnroll) {
-    const int row0 = base + half_warp;
-    uint4 raw[kUnroll];
+    uint4 raw[kUnroll][2];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int r = row0 + u * step;
-      raw[u] = make_uint4(0u, 0u, 0u, 0u);
+      const int r = base + row_of + u * step;
+      const __nv_bfloat16* src = nullptr;
       if (r < p.num_q_heads)
-        raw[u] = *reinterpret_cast<const uint4*>(p.q_in + n * p.qi_sn + r * p.qi_sh + e0);
+        src = p.q_in + n * p.qi_sn + r * p.qi_sh;
       else if (r < p.num_q_heads + p.num_kv_heads)
-        raw[u] = *reinterpret_cast<const uint4*>(p.k_in + n * p.ki_sn +
-                                                 (r - p.num_q_heads) * p.ki_sh + e0);
+        src = p.k_in + n * p.ki_sn + (r - p.num_q_heads) * p.ki_sh;
       else if (r < num_rows)
-        raw[u] = *reinterpret_cast<const uint4*>(
-            p.v_in + n * p.vi_sn + (r - p.num_q_heads - p.num_kv_heads) * p.vi_sh + e0);
+        src = p.v_in + n * p.vi_sn + (r - p.num_q_heads - p.num_kv_heads) * p.vi_sh;
+      raw[u][0] = src ? *reinterpret_cast<const uint4*>(src + ea) : make_uint4(0u, 0u, 0u, 0u);
+      raw[u][1] = src ? *reinterpret_cast<const uint4*>(src + eb) : make_uint4(0u, 0u, 0u, 0u);
     }
-    if (base < step) {  // once: this token's angles
-      if (threadIdx.x < R / 2)
-        s_turn[threadIdx.x] = turn((float)pos, p.freq_hi[threadIdx.x], p.freq_lo[threadIdx.x], p);
+    if (base < step) {  // once: this token's angles and place
+      if (slot < 0) return;  // padding: nothing is written for it
+      if (pos < 0 || pos >= kRopeMaxPosition) {
+        if (tid == 0 && blockIdx.y == 0 && p.err) atomicOr(p.err, HPC_DEVCHK_BAD_LENGTH);
+        return;
+      }
+      const int blk = slot / kBlockTokens;
+      store_kv = blk < p.num_blocks;
+      if (!store_kv && tid == 0 && blockIdx.y == 0 && p.err) atomicOr(p.err, HPC_DEVCHK_BAD_BLOCK);
+      cache_row = blk * p.c_sblk + (slot % kBlockTokens) * p.c_sslot;
+      if (tid < R / 2) {
+        const TurnPair t = turn((float)pos, p.freq_hi[tid], p.freq_lo[tid], p);
+        s_cos[tid] = t.c;
+        s_sin[tid] = t.s;
+      }
+      if constexpr (NORM) {
+        for (int i = tid; i < 2 * kHeadDim; i += kThreads) {
+          const void* w = i < kHeadDim ? p.wq : p.wk;
+          s_w[i / kHeadDim][i % kHeadDim] =
+              w ? load_weight(w, i < kHeadDim ? p.wq_dtype : p.wk_dtype, i % kHeadDim) : 0.f;
+        }
+      }
       __syncthreads();
+      if constexpr (LAYOUT == kHalfLanes) {
+        // c, s [0..3]: of the pairs (ea + j, eb + j), j < 8
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        // element e0 + j belongs to pair i; past R none is used
-        const int e = e0 + j;
-        const int i = LAYOUT == kInterleaved ? e / 2 : (e < R / 2 ? e : e - R / 2);
-        const TurnPair t = e < R ? s_turn[i] : TurnPair{1.f, 0.f};
-        c[j] = t.c;
-        // new a = a cos - b sin, new b = b cos + a sin: the sign goes with the element
-        const bool lower = LAYOUT == kInterleaved ? (j & 1) == 0 : e < R / 2;
-        s[j] = lower ? -t.s : t.s;
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int r = row0 + u * step;
-      if (base + u * step >= num_rows) break;
-      const bool is_q = r < p.num_q_heads, is_k = !is_q && r < p.num_q_heads + p.num_kv_heads;
-      float x[8];
-      unpack(raw[u], x);
-      const void* w = is_q ? p.wq : p.wk;
-      float ss = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) ss += x[j] * x[j];
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if ((is_q || is_k) && w) {
-        float g[8];
-        load_weights(w, is_q ? p.wq_dtype : p.wk_dtype, e0, g);
-        const float inv = __frcp_rn(__fsqrt_rn(ss * (1.0f / kHeadDim) + p.eps));
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = x[j] * inv * g[j];
-      }
-      // the partner of each element
-      float y[8];
-      if constexpr (LAYOUT == kInterleaved) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = x[j ^ 1];
-      } else if constexpr (LAYOUT == kHalfLanes) {
-        const int hop = R / 16;  // lanes between the halves
-        const int from = chunk < hop ? chunk + hop : (chunk < 2 * hop ? chunk - hop : chunk);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = __shfl_sync(0xffffffffu, x[j], from, 16);
+        for (int j = 0; j < 4; ++j) {
+          const int i = ea + 2 * j < R / 2 ? ea + 2 * j : 0;
+          c[j] = make_float2(s_cos[i], s_cos[i + 1]);
+          s[j] = make_float2(s_sin[i], s_sin[i + 1]);
+        }
       } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s_row[half_warp][e0 + j] = x[j];
-        __syncwarp();
+        // c, s [j]: of the two elements of pair j of the lane's 16; the sine
+        // with its sign (new a = a cos - b sin, new b = b cos + a sin)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const int e = e0 + j;
-          y[j] = s_row[half_warp][e < R / 2 ? e + R / 2 : (e < R ? e - R / 2 : e)];
-        }
-        __syncwarp();
-      }
-      if (is_q || is_k) {
+          const int e = (j < 4 ? ea : eb) + 2 * (j & 3);
+          if constexpr (LAYOUT == kInterleaved) {
+            const int i = e < R ? e / 2 : 0;
+            c[j] = make_float2(s_cos[i], s_cos[i]);
+            s[j] = make_float2(-s_sin[i], s_sin[i]);
+          } else {
+            float cc[2], ss[2];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (e0 + j < R) x[j] = fmaf(x[j], c[j], y[j] * s[j]);
+            for (int k = 0; k < 2; ++k) {
+              const int x = e + k, i = x < R / 2 ? x : (x < R ? x - R / 2 : 0);
+              cc[k] = s_cos[i];
+              ss[k] = x < R / 2 ? -s_sin[i] : s_sin[i];
+            }
+            c[j] = make_float2(cc[0], cc[1]);
+            s[j] = make_float2(ss[0], ss[1]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      if (base + u * step >= num_rows) break;
+      const int r = base + row_of + u * step;
+      const bool is_q = r < p.num_q_heads, is_k = !is_q && r < p.num_q_heads + p.num_kv_heads;
+      float2 x[8];
+      unpack(raw[u][0], x);
+      unpack(raw[u][1], x + 4);
+      if constexpr (NORM) {
+        float2 q = mul2(x[0], x[0]);
+#pragma unroll
+        for (int j = 1; j < 8; ++j) q = fma2(x[j], x[j], q);
+        float ss = q.x + q.y;
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (is_q ? p.wq != nullptr : (is_k && p.wk != nullptr)) {
+          const float inv = __frcp_rn(__fsqrt_rn(ss * (1.0f / kHeadDim) + p.eps));
+          const float* w = s_w[is_q ? 0 : 1];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float2 g = *reinterpret_cast<const float2*>(w + (j < 4 ? ea : eb) + 2 * (j & 3));
+            x[j] = mul2(mul2(x[j], make_float2(inv, inv)), g);
+          }
+        }
+      }
+      if constexpr (LAYOUT == kHalfLanes) {
+        if ((is_q || is_k) && ea < R / 2) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 a = x[j], b = x[j + 4], m = mul2(b, s[j]);
+            x[j] = fma2(a, c[j], make_float2(-m.x, -m.y));
+            x[j + 4] = fma2(b, c[j], mul2(a, s[j]));
+          }
+        }
+      } else {
+        float2 y[8];  // the partner of each element
+        if constexpr (LAYOUT == kInterleaved) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) y[j] = make_float2(x[j].y, x[j].x);
+        } else {
+          float* row = s_row[row_of];
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<float2*>(row + (j < 4 ? ea : eb) + 2 * (j & 3)) = x[j];
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int e = (j < 4 ? ea : eb) + 2 * (j & 3), f = e + 1;
+            y[j] = make_float2(row[e < R / 2 ? e + R / 2 : (e < R ? e - R / 2 : e)],
+                               row[f < R / 2 ? f + R / 2 : (f < R ? f - R / 2 : f)]);
+          }
+          __syncwarp();
+        }
+        if (is_q || is_k) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)  // R is even: two neighbours turn or stay together
+            if ((j < 4 ? ea : eb) + 2 * (j & 3) < R) x[j] = fma2(x[j], c[j], mul2(y[j], s[j]));
+        }
       }
       if (is_q) {
-        *reinterpret_cast<uint4*>(p.q_out + n * p.qo_sn + r * p.qo_sh + e0) = pack(x);
-        if (p.q_fp8)
-          *reinterpret_cast<uint2*>(p.q_fp8 + n * p.qf_sn + r * p.qf_sh + e0) =
-              quantise(x, p.q_fp8_scale);
+        __nv_bfloat16* dst = p.q_out + n * p.qo_sn + r * p.qo_sh;
+        *reinterpret_cast<uint4*>(dst + ea) = pack(x);
+        *reinterpret_cast<uint4*>(dst + eb) = pack(x + 4);
+        if (p.q_fp8) {
+          uint8_t* d8 = p.q_fp8 + n * p.qf_sn + r * p.qf_sh;
+          *reinterpret_cast<uint2*>(d8 + ea) = quantise(x, p.q_fp8_scale);
+          *reinterpret_cast<uint2*>(d8 + eb) = quantise(x + 4, p.q_fp8_scale);
+        }
       } else if (r < num_rows && store_kv) {
         const int h = r - p.num_q_heads - (is_k ? 0 : p.num_kv_heads);
-        void* cache = is_k ? p.k_cache : p.v_cache;
         const int64_t off = cache_row + h * p.c_shead;
-        if (p.cache_fp8)
-          *reinterpret_cast<uint2*>((uint8_t*)cache + off) =
-              quantise(x, is_k ? p.k_scale : p.v_scale);
-        else
-          *reinterpret_cast<uint4*>((__nv_bfloat16*)cache + off) = is_k ? pack(x) : raw[u];
+        if (p.cache_fp8) {
+          uint8_t* dst = (uint8_t*)(is_k ? p.k_cache : p.v_cache) + off;
+          const E4m3Scale sc = is_k ? p.k_scale : p.v_scale;
+          *reinterpret_cast<uint2*>(dst + ea) = quantise(x, sc);
+          *reinterpret_cast<uint2*>(dst + eb) = quantise(x + 4, sc);
+        } else {
+          __nv_bfloat16* dst = (__nv_bfloat16*)(is_k ? p.k_cache : p.v_cache) + off;
+          *reinterpret_cast<uint4*>(dst + ea) = is_k ? pack(x) : raw[u][0];
+          *reinterpret_cast<uint4*>(dst + eb) = is_k ? pack(x + 4) : raw[u][1];
+        }
       }
     }
   }
+}
+
+template <bool NORM>
+cudaError_t launch_layout(const cudaLaunchConfig_t& cfg, const RopeParams& p) {
+  if (p.interleaved) return cudaLaunchKernelEx(&cfg, rope_kernel<kInterleaved, NORM>, p);
+  if (p.rot_dim % 16 == 0) return cudaLaunchKernelEx(&cfg, rope_kernel<kHalfLanes, NORM>, p);
+  return cudaLaunchKernelEx(&cfg, rope_kernel<kHalfAny, NORM>, p);
 }
 
 }  // namespace
@@ -223,8 +310,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
 cudaError_t launch_rope(const RopeParams& p, int sm_count, cudaStream_t stream) {
   if (p.num_tokens == 0) return cudaSuccess;
   const int rows = p.num_q_heads + 2 * p.num_kv_heads;
-  // one CTA per token from two CTAs per SM on; fewer tokens spread their rows
-  const int64_t want = (2LL * sm_count + p.num_tokens - 1) / p.num_tokens;
+  // one CTA per token from four CTAs per SM on; fewer tokens spread their rows
+  const int64_t want = (4LL * sm_count + p.num_tokens - 1) / p.num_tokens;
   const int most = (rows + kRowsAtOnce - 1) / kRowsAtOnce;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.num_tokens, (unsigned)(want < most ? want : most));
@@ -235,9 +322,7 @@ cudaError_t launch_rope(const RopeParams& p, int sm_count, cudaStream_t stream) 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (p.interleaved) return cudaLaunchKernelEx(&cfg, rope_kernel<kInterleaved>, p);
-  if (p.rot_dim % 16 == 0) return cudaLaunchKernelEx(&cfg, rope_kernel<kHalfLanes>, p);
-  return cudaLaunchKernelEx(&cfg, rope_kernel<kHalfAny>, p);
+  return p.wq || p.wk ? launch_layout<true>(cfg, p) : launch_layout<false>(cfg, p);
 }
 
 }  // namespace hpc

@@ -157,6 +157,32 @@ def test_fp8(interleaved, rot_dim, normed):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("scale", [4.0 / 448, 1.0 / 112, 0.01, 1.0, 0.25, 3.0, 1.0 / 3, 0.0117, 700.0, 2.0 ** -40])
+def test_e4m3_rounds_the_exact_quotient(scale):
+    """Every finite bf16 magnitude around the e4m3 range, ties included: each byte is the nearest one."""
+    codes = torch.arange(0, 0x7F80).to(torch.int16).view(torch.bfloat16)
+    s = np.float64(np.float32(scale))
+    keep = (codes.double() / s > 2.0 ** -11) & (codes.double() / s < 1000)
+    v = torch.cat([codes[keep], -codes[keep], torch.tensor([0.0, -0.0, float("inf"), float("-inf")], dtype=torch.bfloat16)])
+    n = -(-v.numel() // 128)
+    rows = torch.zeros(n * 128, dtype=torch.bfloat16)
+    rows[:v.numel()] = v[torch.randperm(v.numel(), generator=torch.Generator().manual_seed(1))]
+    rows = rows.view(n, 1, 128).cuda()
+    cache = torch.zeros((2, n // 64 + 1, 1, 64, 128), dtype=torch.uint8, device="cuda")
+    q8 = torch.zeros(rows.shape, dtype=torch.uint8, device="cuda")
+    hpc.hpc_rope_kv_write(rows, rows.clone(), rows.clone(), torch.zeros(n, dtype=torch.int32, device="cuda"),
+                          torch.arange(n, dtype=torch.int32, device="cuda"), hpc.hpc_rope_init(rot_dim=2), rows.clone(),
+                          cache[0], cache[1], q_out_fp8=q8, q_fp8_scale=scale, k_scale=scale, v_scale=scale)
+    ref = [PR.e4m3_encode(x / s) for x in rows.double().cpu().numpy().ravel()]
+    assert cache[1].flatten()[:n * 128].tolist() == ref  # v
+    # position 0 turns nothing: q and k are the same rows (0 * inf spoils a pair that holds one)
+    fine = torch.isfinite(rows).view(-1, 2).all(1).repeat_interleave(2).cpu()
+    for got in (cache[0].flatten()[:n * 128], q8.flatten()):
+        same = got.cpu() == torch.tensor(ref, dtype=torch.uint8)
+        same |= (rows.cpu().flatten() == 0)  # the sign of a zero
+        assert same[fine].all()
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_token_major_cache(fp8):
     c = Case(90, 16, 4, fp8=fp8, token_major=True, seed=6)
