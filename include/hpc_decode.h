@@ -81,6 +81,8 @@ typedef struct hpc_plan_s* hpc_plan_t;
 #define HPC_PLAN_STATIC 1
 /* The work list a one-token hpc_decode_step ran (see hpc_decode_step). */
 #define HPC_PLAN_STEP 2
+/* A plan from hpc_decode_prefix_plan_create (not exported). */
+#define HPC_PLAN_PREFIX 3
 
 /* Segment flag: the segment covers every tile of its sequence. */
 #define HPC_SEG_WHOLE 1
@@ -627,6 +629,53 @@ hpc_status hpc_rope_kv_write(const hpc_tensor* q_in, const hpc_tensor* k_in, con
                              const hpc_tensor* k_norm_weight, float eps, hpc_tensor* q_out,
                              hpc_tensor* q_out_fp8, hpc_tensor* k_cache, hpc_tensor* v_cache,
                              int32_t* device_error, void* stream);
+
+/*
+ * hpc_decode_prefix_plan_create -- a plan for hpc_decode_prefix_attn: the
+ * device work list, partial states and error word of steps of at most max_seqs
+ * (<= 4096) sequences with max_q_len (1 .. 8) new tokens each and num_q_heads
+ * query heads, on num_sms CTAs (normally the SM count). All device memory is
+ * allocated here: 4.2 KB per (new token, KV head) twice, and 131 KB per CTA.
+ * hpc_decode_plan_status and hpc_decode_plan_destroy take it; the other calls
+ * refuse it. Calls on one plan must not overlap on the GPU.
+ */
+hpc_status hpc_decode_prefix_plan_create(int32_t max_seqs, int32_t max_q_len, int32_t num_sms,
+                                         int32_t num_q_heads, hpc_plan_t* plan_out);
+
+/*
+ * hpc_decode_prefix_attn -- hpc_decode_step for a batch whose sequences share
+ * prefixes: the same outputs, with the shared blocks of a group read once for
+ * all its sequences instead of once for each. The batch is cut into groups of
+ * neighbouring sequences; the first prefix_lens[g] positions of group g's
+ * sequences hold the same keys and values. The whole 64-token blocks among them
+ * that every new token of each non-empty sequence sees (all of prefix_lens[g] /
+ * 64 where the sequences are longer than the prefix) are read through the block
+ * table row of the group's first non-empty sequence; all else through each
+ * sequence's own row. A group with fewer than two non-empty sequences shares
+ * nothing. Runs on the tcgen05 tensor cores in three launches (plan, attention,
+ * merge), planned from the device lengths.
+ *   q, k_cache, v_cache, block_table, seq_lens, out, lse: as hpc_decode_step
+ *       (q_len 1 .. 8), with q's tokens evenly spaced (stride 0 = q_len *
+ *       stride 1)
+ *   cu_groups    device int32 [G + 1], 0 = cu_groups[0] <= ... <= cu_groups[G]
+ *                = B (else HPC_DEVCHK_BAD_LENGTH and nothing is shared), or NULL:
+ *                one group
+ *   prefix_lens  device int32 [G], 1 <= G <= 4096; a negative length sets
+ *                HPC_DEVCHK_BAD_LENGTH and counts as 0
+ *   plan         from hpc_decode_prefix_plan_create, for at least this step's
+ *                sequences, new tokens and heads
+ *   softmax_scale  > 0, or <= 0 for 1/sqrt(128)
+ * Cache slots past a sequence's end may hold anything, NaN included. A new
+ * token that sees no position, and every token of an empty sequence, gets out =
+ * 0, lse = -inf; a negative length counts as 0 and sets HPC_DEVCHK_BAD_LENGTH.
+ * Bad block ids read zeros and set HPC_DEVCHK_BAD_BLOCK. Allocates nothing; may
+ * be captured in a CUDA graph after a first call outside the capture.
+ */
+hpc_status hpc_decode_prefix_attn(const hpc_tensor* q, const hpc_tensor* k_cache,
+                                  const hpc_tensor* v_cache, const hpc_tensor* block_table,
+                                  const hpc_tensor* seq_lens, const hpc_tensor* cu_groups,
+                                  const hpc_tensor* prefix_lens, hpc_plan_t plan, hpc_tensor* out,
+                                  hpc_tensor* lse, float softmax_scale, void* stream);
 
 /* hpc_device_sm_count -- streaming multiprocessors of the current device. */
 hpc_status hpc_device_sm_count(int32_t* num_sms);

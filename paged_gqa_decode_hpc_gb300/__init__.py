@@ -29,7 +29,7 @@ __all__ = [
     "hpc_decode_step_host",
     "hpc_rope_norm_kv_write", "hpc_extend_attn", "hpc_decode_tc_min_q_len",
     "hpc_block_table_append", "hpc_block_table_truncate", "HpcRope", "hpc_rope_init",
-    "hpc_rope_kv_write",
+    "hpc_rope_kv_write", "hpc_decode_prefix_plan_create", "hpc_decode_prefix_attn",
     "HPC_OK", "HPC_ERR_INVALID_ARG", "HPC_ERR_UNSUPPORTED", "HPC_ERR_CUDA", "HPC_ERR_OOM",
     "HPC_ERR_DEVICE_CHECK",
 ]
@@ -37,7 +37,7 @@ __all__ = [
 HPC_OK, HPC_ERR_INVALID_ARG, HPC_ERR_UNSUPPORTED, HPC_ERR_CUDA, HPC_ERR_OOM, \
     HPC_ERR_DEVICE_CHECK = range(6)
 HPC_BF16, HPC_FP8_E4M3, HPC_F32, HPC_I32 = range(4)
-HPC_PLAN_DYNAMIC, HPC_PLAN_STATIC, HPC_PLAN_STEP = 0, 1, 2
+HPC_PLAN_DYNAMIC, HPC_PLAN_STATIC, HPC_PLAN_STEP, HPC_PLAN_PREFIX = 0, 1, 2, 3
 HPC_SEG_WHOLE = 1
 HPC_DEVCHK_BAD_LENGTH, HPC_DEVCHK_BAD_BLOCK, HPC_DEVCHK_TABLE_TOO_SHORT, \
     HPC_DEVCHK_TIMEOUT, HPC_DEVCHK_CAPACITY, HPC_DEVCHK_NO_BLOCKS = 1, 2, 4, 8, 16, 32
@@ -123,6 +123,8 @@ def load_library():
             # descriptors packed by _desc
             "hpc_block_table_append": [D, D, D, D, i32, D, D, D, D, D, D, P, P],
             "hpc_block_table_truncate": [D, D, D, i32, D, D, D, D, P, P],
+            "hpc_decode_prefix_plan_create": [i32, i32, i32, i32, ctypes.POINTER(P)],
+            "hpc_decode_prefix_attn": [D, D, D, D, D, D, D, P, D, D, ctypes.c_float, P],
             "hpc_rope_init": [ctypes.POINTER(HpcRope), i32, i32, F64, i32, F64, i32, F64, F64, F64],
             "hpc_rope_kv_write": [D, D, D, D, D, ctypes.POINTER(HpcRope), D, D, ctypes.c_float,
                                   D, D, D, D, P, P],
@@ -541,3 +543,25 @@ def hpc_rope_kv_write(q_in, k_in, v_in, positions, slots, rope: HpcRope, q_out, 
         _desc(q_norm_weight), _desc(k_norm_weight), eps, _desc(q_out),
         _desc(q_out_fp8, q_fp8_scale), _desc(k_cache, k_scale), _desc(v_cache, v_scale),
         _err_ptr(device_error), _stream_ptr(stream)))
+
+
+def hpc_decode_prefix_plan_create(max_seqs: int, max_q_len: int, num_sms: int,
+                                  num_q_heads: int) -> Plan:
+    """A plan (work list, partial states, error word) for hpc_decode_prefix_attn."""
+    h = ctypes.c_void_p()
+    _check(load_library().hpc_decode_prefix_plan_create(int(max_seqs), int(max_q_len), int(num_sms),
+                                                        int(num_q_heads), ctypes.byref(h)))
+    return Plan(h, HPC_PLAN_PREFIX)
+
+
+def hpc_decode_prefix_attn(q, k_cache, v_cache, block_table, seq_lens, prefix_lens, plan: Plan,
+                           out, lse=None, cu_groups=None, softmax_scale: Optional[float] = None,
+                           stream=None, k_scale: float = 1.0, v_scale: float = 1.0):
+    """Decode attention of a batch whose sequences share prefixes: group g is the
+    sequences cu_groups[g] .. cu_groups[g + 1] - 1 (None: one group), which hold
+    the same first prefix_lens[g] positions; their shared blocks are read once.
+    q, out, lse and the caches as for hpc_decode_step (q_len 1 to 8)."""
+    _check(load_library().hpc_decode_prefix_attn(
+        _desc(q), _desc(k_cache, k_scale), _desc(v_cache, v_scale), _desc(block_table),
+        _desc(seq_lens), _desc(cu_groups), _desc(prefix_lens), plan.handle, _desc(out), _desc(lse),
+        -1.0 if softmax_scale is None else softmax_scale, _stream_ptr(stream)))

@@ -421,6 +421,8 @@ hpc_status hpc_decode_plan_update(const int32_t* seq_lens, int32_t num_seqs, int
 
 hpc_status hpc_decode_plan_export(hpc_plan_t plan, int32_t* buf, int64_t cap, int64_t* len) {
   if (!plan || !len) return fail(HPC_ERR_INVALID_ARG, "plan or len is null");
+  if (plan->kind == HPC_PLAN_PREFIX)
+    return fail(HPC_ERR_UNSUPPORTED, "a prefix plan has no export");
   const PlanLayout& L = plan->layout;
   std::vector<int32_t> w((size_t)L.words());
   HPC_CUDA_TRY(cudaDeviceSynchronize());
@@ -544,6 +546,8 @@ hpc_status attn_impl(const hpc_tensor* q, const hpc_tensor* k_cache, const hpc_t
   if ((st = check_tensor(out, "out", qnd)) != HPC_OK) return st;
   if ((st = check_tensor(lse, "lse", qnd - 1, true)) != HPC_OK) return st;
   if (!plan) return fail(HPC_ERR_INVALID_ARG, "plan is null");
+  if (plan->kind == HPC_PLAN_PREFIX)
+    return fail(HPC_ERR_INVALID_ARG, "a prefix plan serves hpc_decode_prefix_attn only");
   const bool has_lse = lse && lse->data;
   const bool multi = qnd == 4;
   const int64_t B = q->shape[0], T = multi ? q->shape[1] : 1;

@@ -71,6 +71,7 @@ struct hpc_plan_s {
   void* d_stage = nullptr;
   size_t stage_bytes = 0;
   int64_t ws_floats = 0;         // floats allocated at d_ws
+  int32_t prefix_q_len = 0;      // HPC_PLAN_PREFIX: new tokens per sequence it was sized for
 };
 
 namespace hpc {

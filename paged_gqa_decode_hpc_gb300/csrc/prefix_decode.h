@@ -1,0 +1,102 @@
+// Internal declarations of shared-prefix decode attention (prefix_plan_kernel.cu,
+// prefix_decode_kernel.cu, prefix_merge_kernel.cu); not part of the public ABI.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace hpc {
+
+// A query "pair" is one new token of one sequence, i = b * q_len + t: the 8
+// query heads of a KV head make it 8 rows of the 128-row MMA tile, 16 pairs a
+// tile. A "work row" v is a set of pairs that read the same K / V tiles: up to
+// 32 pairs of a group on the group's shared tiles, or the q_len pairs of one
+// sequence on its own tiles behind them. Its work units are (KV head, tile),
+// head-major; units of all work rows in order, weighted, are cut into parts of
+// equal cost, one part per CTA.
+constexpr int kPrefixRowPairs = 32;     // pairs of a shared work row (two MMA tiles)
+constexpr int kPrefixTilePairs = 16;    // pairs of one MMA tile
+constexpr int32_t kPrefixMaxSeqs = 4096;
+
+// Plan words (device int32).
+enum PrefixHeader { kPxRows = 0, kPxShared, kPxParts, kPxPad, kPrefixHeader };
+struct PrefixRec {  // one work row, 8 words
+  int32_t pair0, pairs;   // its pairs
+  int32_t table;          // block table row
+  int32_t tile0, tiles;   // its tiles in that row
+  int32_t own;            // 1: a sequence's own tiles (masked at its end)
+  int32_t len;            // own: positions of the sequence
+  int32_t pad;
+};
+struct PrefixLayout {
+  int32_t cap_seqs = 0, cap_q_len = 0, cap_parts = 0;
+  // work rows: shared ones (every group's last may be partly filled), then own ones
+  int64_t cap_rows() const {
+    return 2LL * cap_seqs + (int64_t)cap_seqs * cap_q_len / kPrefixRowPairs + 1;
+  }
+  int64_t bound_off() const { return kPrefixHeader; }                       // [parts + 1][2]
+  int64_t seq_off() const { return bound_off() + 2LL * (cap_parts + 1); }   // [seqs][2]
+  int64_t rec_off() const { return (seq_off() + 2LL * cap_seqs + 7) & ~7LL; }
+  int64_t words() const { return rec_off() + 8 * cap_rows(); }
+};
+
+// Partial softmax states, in blocks of the 8 rows of a (pair, KV head):
+// o [32 column groups][8 heads] float4 (unnormalised), m and l [8]. A piece
+// that starts a (work row, KV head) goes to the block of its pair, shared or
+// own; a piece that continues one to its part's blocks.
+struct PrefixWorkspace {
+  float4* o;
+  float* m;      // log2 units
+  float* l;
+  int64_t own0;  // first block of the own pieces (shared ones start at 0)
+  int64_t cont0; // first block of the parts' continuing pieces, 32 per part
+};
+
+struct PrefixPlanParams {
+  const int32_t* seq_lens;
+  const int32_t* cu_groups;     // [G + 1] or null: one group
+  const int32_t* prefix_lens;   // [G]
+  int32_t num_seqs, num_groups, q_len, num_kv_heads, max_blocks, num_parts;
+  int32_t* words;
+  int32_t bound_off, seq_off, rec_off;
+  int32_t* err;
+};
+cudaError_t launch_prefix_plan(const PrefixPlanParams& p, cudaStream_t stream);
+
+struct PrefixParams {
+  const int32_t* words;         // plan
+  int32_t bound_off, rec_off;
+  const int32_t* block_table;
+  int64_t bt_sb;
+  int32_t max_blocks;
+  int32_t num_kv_heads, num_blocks, q_len;
+  int32_t kv_swap;              // KV tensor map dims are (d, head, slot, block)
+  PrefixWorkspace ws;
+  float score_scale_log2;       // softmax_scale * log2(e) (* k_scale for e4m3)
+  int32_t* err;
+  unsigned long long timeout_ns;
+  int32_t withhold_copies;
+};
+// tq16 / tqt: maps over q as [pairs][H_q][128], boxes of 64 columns x 8 heads x
+// 16 pairs / q_len pairs, 128-byte swizzle.
+cudaError_t launch_prefix_decode(const PrefixParams& p, const CUtensorMap& tq16,
+                                 const CUtensorMap& tqt, const CUtensorMap& tk,
+                                 const CUtensorMap& tv, bool fp8, int num_parts,
+                                 cudaStream_t stream);
+
+struct PrefixMergeParams {
+  const int32_t* words;
+  int32_t bound_off, seq_off, rec_off;
+  int32_t num_seqs, num_kv_heads, q_len;
+  PrefixWorkspace ws;
+  float v_scale;
+  __nv_bfloat16* out;           // element strides over sequence, token, head
+  int64_t o_sb, o_st, o_sh;
+  float* lse;                   // may be null
+  int64_t l_sb, l_st, l_sh;
+};
+cudaError_t launch_prefix_merge(const PrefixMergeParams& p, cudaStream_t stream);
+
+}  // namespace hpc
