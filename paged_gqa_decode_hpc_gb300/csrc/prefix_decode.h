@@ -54,7 +54,16 @@ struct PrefixWorkspace {
   int64_t cont0; // first block of the parts' continuing pieces, 32 per part
 };
 
+// What a KV head of a work row costs its CTA, in units of 10 ns: a fixed part
+// (Q and the first tile's way through the pipeline, the epilogue) and each tile.
+struct PrefixCosts {
+  int32_t shared_fixed, two_tile, one_tile, own_fixed, own_tile;
+};
+constexpr PrefixCosts kPrefixCostsBf16 = {200, 88, 50, 100, 62};
+constexpr PrefixCosts kPrefixCostsFp8 = {300, 105, 80, 250, 80};
+
 struct PrefixPlanParams {
+  PrefixCosts costs;
   const int32_t* seq_lens;
   const int32_t* cu_groups;     // [G + 1] or null: one group
   const int32_t* prefix_lens;   // [G]

@@ -8,11 +8,11 @@
 // So no shared tile needs a mask, and what lies behind is the sequences' own:
 // sequence b has ceil(L_b / 64) - s_g tiles of its own.
 // Work rows: for every group with s_g > 0, its pairs in sets of 32; then one
-// row per sequence. A unit is a (KV head, tile) of a work row; part p of P
-// covers the cost interval [p C / P, (p + 1) C / P) of all units in order, a
-// boundary inside a unit belonging to the part before it. Costs: a tile of a
-// shared row of more than 16 pairs costs kCostTwo (both MMA tiles of the CTA work on it),
-// any other kCostOne.
+// row per sequence. A unit is a (KV head, tile) of a work row. A KV head of a
+// row of n tiles costs f + w n, f and w by the row's kind (measured times, see
+// PrefixCosts), and part p of P covers the cost interval [p C / P, (p + 1) C / P)
+// of all heads of all rows in order; a boundary inside a unit leaves it to the
+// part before, one inside f falls before the head's first unit.
 //
 // One CTA of 1024 threads; what bounds it is latency (a few block-wide scans).
 #include "hpc_internal.h"
@@ -24,7 +24,6 @@ namespace hpc {
 namespace {
 
 constexpr int kThreads = 1024;
-constexpr int kCostOne = 1, kCostTwo = 2;
 
 __device__ __forceinline__ int64_t block_scan(int64_t a, int64_t* warp_tot, int64_t* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -61,6 +60,12 @@ __device__ __forceinline__ int find(const T* a, int n, T x) {
     else hi = mid;
   }
   return lo;
+}
+
+// Costs of a KV head of a work row: fixed, and per tile.
+__device__ __forceinline__ int2 costs(const PrefixCosts& c, bool own, int pairs) {
+  if (own) return make_int2(c.own_fixed, c.own_tile);
+  return make_int2(c.shared_fixed, pairs > kPrefixTilePairs ? c.two_tile : c.one_tile);
 }
 
 __global__ void __launch_bounds__(kThreads) prefix_plan_kernel(const PrefixPlanParams p) {
@@ -135,6 +140,7 @@ __global__ void __launch_bounds__(kThreads) prefix_plan_kernel(const PrefixPlanP
   const int V = shared + B;
   if (tid == 0) grow[G] = shared;
   __syncthreads();
+  int64_t units = 0;  // of this thread's rows
   PrefixRec* recs = reinterpret_cast<PrefixRec*>(p.words + p.rec_off);
   carry = 0;
   for (int base = 0; base < V; base += kThreads) {
@@ -155,7 +161,6 @@ __global__ void __launch_bounds__(kThreads) prefix_plan_kernel(const PrefixPlanP
         r.tiles = gtiles[g];
         r.own = 0;
         r.len = INT32_MAX;
-        cost = r.pairs > kPrefixTilePairs ? kCostTwo : kCostOne;
       } else {
         const int b = v - shared, L = max(p.seq_lens[b], 0), g = find(cu, G, b);
         const int t0 = L > 0 ? gtiles[g] : 0;
@@ -166,14 +171,15 @@ __global__ void __launch_bounds__(kThreads) prefix_plan_kernel(const PrefixPlanP
         r.tiles = (int)(((int64_t)L + kBlockTokens - 1) / kBlockTokens) - t0;
         r.own = 1;
         r.len = L;
-        cost = kCostOne;
         int32_t* sr = p.words + p.seq_off + 2 * b;
         // the sequence's first shared work row and pair, or -1
         const bool has = t0 > 0;
         sr[0] = has ? grow[g] : -1;
         sr[1] = cu[g] * T;
       }
-      cost *= (int64_t)H * r.tiles;
+      const int2 fw = costs(p.costs, r.own != 0, r.pairs);
+      if (r.tiles > 0) cost = H * (fw.x + (int64_t)fw.y * r.tiles);
+      units += (int64_t)H * r.tiles;
       int4* dst = reinterpret_cast<int4*>(recs + v);
       const int4* src = reinterpret_cast<const int4*>(&r);
       dst[0] = src[0];
@@ -185,19 +191,24 @@ __global__ void __launch_bounds__(kThreads) prefix_plan_kernel(const PrefixPlanP
     carry += total;
   }
   const int64_t C = carry;
+  int64_t all_units;
+  block_scan(units, warp_tot, &all_units);
   if (tid == 0) cum[V] = C;
   __syncthreads();
   // units of a work row are counted in 32 bits by its readers
-  const bool huge = C > INT32_MAX;
-  const int P = huge ? 0 : (int)min((int64_t)p.num_parts, C);
+  const bool huge = all_units > INT32_MAX;
+  const int P = huge ? 0 : (int)min((int64_t)p.num_parts, all_units);
   for (int q = tid; q <= P; q += kThreads) {
     int v = V, u = 0;
     if (q < P) {
-      const int64_t c = C * q / P;
+      const int64_t c = C / P * q + C % P * q / P;
       v = find(cum, V, c);
-      const int w = (v < shared && min(kPrefixRowPairs, recs[v].pairs) > kPrefixTilePairs)
-                        ? kCostTwo : kCostOne;
-      u = (int)((c - cum[v] + w - 1) / w);  // a boundary inside a unit: the part before has it
+      const PrefixRec r = recs[v];  // written by this CTA before the barrier
+      const int2 fw = costs(p.costs, v >= shared, r.pairs);
+      const int64_t head = fw.x + (int64_t)fw.y * r.tiles, in = c - cum[v];
+      const int h = (int)(in / head);
+      const int64_t rest = in - h * head - fw.x;
+      u = h * r.tiles + (rest > 0 ? (int)((rest + fw.y - 1) / fw.y) : 0);
     }
     p.words[p.bound_off + 2 * q] = v;
     p.words[p.bound_off + 2 * q + 1] = u;
