@@ -11,8 +11,12 @@
 //
 // One CTA of 256 threads per (pair, KV head): thread = (column group of 4, row),
 // the 8 rows of a column group adjacent, as the states are stored. What bounds
-// it: latency for few pairs, HBM (or L2, where the states just written still
-// are) for many: 4 KB a state.
+// it: latency for few pairs, L2 (where the states just written still are) for
+// many: 4 KB a state. So which states there are is worked out before the wait
+// for the attention kernel (the plan is complete by then: the attention kernel
+// lets this one start only after its own wait for it), and the states are
+// loaded kBatch at a time, none waiting for another (one after the other took
+// 7 us for the 8 states of a row at 512 shared tiles).
 #include <cuda_bf16.h>
 
 #include "hpc_internal.h"
@@ -24,63 +28,100 @@ namespace hpc {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kBatch = 4;  // states in flight
 constexpr float kLn2 = 0.6931471805599453f;
 
 __global__ void __launch_bounds__(kThreads) prefix_merge_kernel(const PrefixMergeParams p) {
-  griddep_wait();
-  griddep_launch_dependents();
   const int H = p.num_kv_heads, T = p.q_len;
   const int64_t item = blockIdx.x;
   const int pair = (int)(item / H), h = (int)(item % H), b = pair / T, t = pair % T;
   const int row = threadIdx.x & 7, col = threadIdx.x >> 3;
   const int rows_all = p.words[kPxRows], parts = p.words[kPxParts];
   const int2* bounds = reinterpret_cast<const int2*>(p.words + p.bound_off);
-  const int2* seqs = reinterpret_cast<const int2*>(p.words + p.seq_off);
   const int4* recs = reinterpret_cast<const int4*>(p.words + p.rec_off);
 
-  float M = -INFINITY, L = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto add = [&](int64_t blk) {
-    const float m = p.ws.m[blk * 8 + row], l = p.ws.l[blk * 8 + row];
-    const float4 o = p.ws.o[blk * 256 + col * 8 + row];
-    if (m == -INFINITY) return;  // the piece held no visible key for this row
-    const float Mn = fmaxf(M, m);
-    const float a = ptx_ex2(M - Mn), w = ptx_ex2(m - Mn);
-    L = L * a + l * w;
-    acc.x = acc.x * a + o.x * w;
-    acc.y = acc.y * a + o.y * w;
-    acc.z = acc.z * a + o.z * w;
-    acc.w = acc.w * a + o.w * w;
-    M = Mn;
-  };
-  // the states of work row v for head h; `local`: the pair's number within it
-  auto join = [&](int v, int64_t home, int local) {
-    const int n = recs[2 * v + 1].x;
-    if (n == 0) return;
-    const int first = h * n;
-    add(home);
-    // parts whose boundary lies inside (first, first + n) of row v
-    int lo = 0, hi = 0;
+  // the two work rows: block of the first piece's state, parts [lo, hi) that
+  // may hold more, the pair's number in a part's blocks
+  int64_t home[2] = {-1, -1};
+  int lo[2] = {0, 0}, hi[2] = {0, 0}, local[2] = {0, t};
+  if (rows_all > 0) {
+    const int2 s = reinterpret_cast<const int2*>(p.words + p.seq_off)[b];
+    const int k = s.x >= 0 ? pair - s.y : 0;
+    const int v[2] = {s.x >= 0 ? s.x + k / kPrefixRowPairs : -1, rows_all - p.num_seqs + b};
+    int n[2];
+    n[0] = s.x >= 0 ? recs[2 * v[0] + 1].x : 0;
+    n[1] = recs[2 * v[1] + 1].x;
+    local[0] = k % kPrefixRowPairs;
+    if (n[0] > 0) home[0] = (int64_t)pair * H + h;
+    if (n[1] > 0) home[1] = p.ws.own0 + (int64_t)pair * H + h;
+    // parts whose boundary lies inside a row's units (h n, h n + n)
     for (int q0 = 0; q0 < parts; q0 += kThreads) {
       const int q = q0 + threadIdx.x;
       int2 bd = make_int2(INT32_MAX, 0);
       if (q < parts) bd = bounds[q];
-      lo += __syncthreads_count(bd.x < v || (bd.x == v && bd.y <= first));
-      hi += __syncthreads_count(bd.x < v || (bd.x == v && bd.y < first + n));
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        if (n[w] == 0) continue;  // the whole CTA has the same
+        const int first = h * n[w];
+        lo[w] += __syncthreads_count(bd.x < v[w] || (bd.x == v[w] && bd.y <= first));
+        hi[w] += __syncthreads_count(bd.x < v[w] || (bd.x == v[w] && bd.y < first + n[w]));
+      }
     }
-    for (int q = lo; q < hi; ++q) {
-      const int2 b0 = bounds[q], b1 = bounds[q + 1];
-      if (b0.x == b1.x && b0.y == b1.y) continue;  // a part without units
-      add(p.ws.cont0 + (int64_t)q * kPrefixRowPairs + local);
+  }
+  griddep_wait();  // the states
+  griddep_launch_dependents();
+
+  float M = -INFINITY, L = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    if (home[w] < 0) continue;
+    // state 0 is home's, state 1 + i part lo + i's
+    const int count = 1 + hi[w] - lo[w];
+    for (int s0 = 0; s0 < count; s0 += kBatch) {
+      float m[kBatch], l[kBatch];
+      float4 o[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int s = s0 + i;
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+        o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        int64_t blk = -1;
+        if (s == 0) {
+          blk = home[w];
+        } else if (s < count) {
+          const int q = lo[w] + s - 1;
+          const int2 b0 = bounds[q], b1 = bounds[q + 1];
+          if (b0.x != b1.x || b0.y != b1.y)  // a part without units leaves none
+            blk = p.ws.cont0 + (int64_t)q * kPrefixRowPairs + local[w];
+        }
+        if (blk >= 0) {
+          m[i] = p.ws.m[blk * 8 + row];
+          l[i] = p.ws.l[blk * 8 + row];
+          o[i] = p.ws.o[blk * 256 + col * 8 + row];
+        }
+      }
+      float Mn = M;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) Mn = fmaxf(Mn, m[i]);
+      if (Mn == -INFINITY) continue;  // no visible key for this row so far
+      const float a = ptx_ex2(M - Mn);
+      L *= a;
+      acc.x *= a; acc.y *= a; acc.z *= a; acc.w *= a;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        // a state without a visible key (m = -inf) may hold anything in o
+        const float f = ptx_ex2(m[i] - Mn);
+        if (m[i] == -INFINITY) continue;
+        L += l[i] * f;
+        acc.x += o[i].x * f;
+        acc.y += o[i].y * f;
+        acc.z += o[i].z * f;
+        acc.w += o[i].w * f;
+      }
+      M = Mn;
     }
-  };
-  if (rows_all > 0) {
-    const int2 s = seqs[b];
-    if (s.x >= 0) {
-      const int k = pair - s.y;
-      join(s.x + k / kPrefixRowPairs, (int64_t)pair * H + h, k % kPrefixRowPairs);
-    }
-    join(rows_all - p.num_seqs + b, p.ws.own0 + (int64_t)pair * H + h, t);
   }
   const float inv = L == 0.f ? 0.f : p.v_scale / L;
   __nv_bfloat16* o = p.out + (int64_t)b * p.o_sb + (int64_t)t * p.o_st +
