@@ -176,6 +176,7 @@ hpc_status hpc_decode_prefix_attn(const hpc_tensor* q, const hpc_tensor* k_cache
     pp.words = plan->d_words;
     pp.bound_off = (int32_t)L.bound_off();
     pp.seq_off = (int32_t)L.seq_off();
+    pp.first_off = (int32_t)L.first_off();
     pp.rec_off = (int32_t)L.rec_off();
     pp.err = plan->d_err;
     cudaError_t e = launch_prefix_plan(pp, s);
@@ -186,6 +187,7 @@ hpc_status hpc_decode_prefix_attn(const hpc_tensor* q, const hpc_tensor* k_cache
     std::memset(&p, 0, sizeof p);
     p.words = plan->d_words;
     p.bound_off = pp.bound_off;
+    p.first_off = pp.first_off;
     p.rec_off = pp.rec_off;
     p.block_table = (const int32_t*)block_table->data;
     p.bt_sb = block_table->stride[0];

@@ -21,15 +21,10 @@ constexpr int kPrefixTilePairs = 16;    // pairs of one MMA tile
 constexpr int32_t kPrefixMaxSeqs = 4096;
 
 // Plan words (device int32).
-enum PrefixHeader { kPxRows = 0, kPxShared, kPxParts, kPxPad, kPrefixHeader };
-struct PrefixRec {  // one work row, 8 words
-  int32_t pair0, pairs;   // its pairs
-  int32_t table;          // block table row
-  int32_t tile0, tiles;   // its tiles in that row
-  int32_t own;            // 1: a sequence's own tiles (masked at its end)
-  int32_t len;            // own: positions of the sequence
-  int32_t pad;
-};
+enum PrefixHeader { kPxRows = 0, kPxParts, kPxPad0, kPxPad1, kPrefixHeader };
+// A work row's record, 8 words: {first pair, pairs, block table row, first tile},
+// {tiles, 1 for a sequence's own tiles (masked at its end), its length, -}. A
+// part's first record is kept beside its boundary, one load away.
 struct PrefixLayout {
   int32_t cap_seqs = 0, cap_q_len = 0, cap_parts = 0;
   // work rows: shared ones (every group's last may be partly filled), then own ones
@@ -38,7 +33,8 @@ struct PrefixLayout {
   }
   int64_t bound_off() const { return kPrefixHeader; }                       // [parts + 1][2]
   int64_t seq_off() const { return bound_off() + 2LL * (cap_parts + 1); }   // [seqs][2]
-  int64_t rec_off() const { return (seq_off() + 2LL * cap_seqs + 7) & ~7LL; }
+  int64_t first_off() const { return (seq_off() + 2LL * cap_seqs + 7) & ~7LL; }  // [parts][8]
+  int64_t rec_off() const { return first_off() + 8LL * cap_parts; }              // [rows][8]
   int64_t words() const { return rec_off() + 8 * cap_rows(); }
 };
 
@@ -69,14 +65,14 @@ struct PrefixPlanParams {
   const int32_t* prefix_lens;   // [G]
   int32_t num_seqs, num_groups, q_len, num_kv_heads, max_blocks, num_parts;
   int32_t* words;
-  int32_t bound_off, seq_off, rec_off;
+  int32_t bound_off, seq_off, first_off, rec_off;
   int32_t* err;
 };
 cudaError_t launch_prefix_plan(const PrefixPlanParams& p, cudaStream_t stream);
 
 struct PrefixParams {
   const int32_t* words;         // plan
-  int32_t bound_off, rec_off;
+  int32_t bound_off, first_off, rec_off;
   const int32_t* block_table;
   int64_t bt_sb;
   int32_t max_blocks;

@@ -177,17 +177,18 @@ struct Walk {
     const int2* bounds = reinterpret_cast<const int2*>(p.words + p.bound_off);
     recs = reinterpret_cast<const int4*>(p.words + p.rec_off);
     H = p.num_kv_heads;
-    v = u = v1 = u1 = 0;
-    ra = rb = na = nb = make_int4(0, 0, 0, 0);
-    if (part < p.words[kPxParts]) {
-      const int2 b0 = bounds[part], b1 = bounds[part + 1];
-      v = b0.x;
-      u = b0.y;
-      v1 = b1.x;
-      u1 = b1.y;
-      if (has(v)) load(v, ra, rb);
-      if (has(v + 1)) load(v + 1, na, nb);
-    }
+    // the part's boundaries and its first record in one trip (a plan without
+    // units has all boundaries behind the last row)
+    const int2 b0 = bounds[part], b1 = bounds[part + 1];
+    const int4* first = reinterpret_cast<const int4*>(p.words + p.first_off) + 2 * part;
+    ra = first[0];
+    rb = first[1];
+    na = nb = make_int4(0, 0, 0, 0);
+    v = b0.x;
+    u = b0.y;
+    v1 = b1.x;
+    u1 = b1.y;
+    if (has(v + 1)) load(v + 1, na, nb);
   }
   __device__ __forceinline__ bool next(Piece& s) {
     while (v < v1 || (v == v1 && u < u1)) {

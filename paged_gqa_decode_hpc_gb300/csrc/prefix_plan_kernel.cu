@@ -14,7 +14,10 @@
 // of all heads of all rows in order; a boundary inside a unit leaves it to the
 // part before, one inside f falls before the head's first unit.
 //
-// One CTA of 1024 threads; what bounds it is latency (a few block-wide scans).
+// One CTA; what bounds it is latency: one trip to memory for all the inputs
+// (loaded before anything else), two block-wide scans, binary searches in
+// shared memory, 32-bit divisions where the numbers allow. 256 threads for
+// small batches (barriers and scans of 8 warps), else 1024.
 #include "hpc_internal.h"
 #include "prefix_decode.h"
 #include "ptx.cuh"
@@ -23,7 +26,7 @@ namespace hpc {
 
 namespace {
 
-constexpr int kThreads = 1024;
+constexpr int kMaxThreads = 1024;
 
 __device__ __forceinline__ int64_t block_scan(int64_t a, int64_t* warp_tot, int64_t* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -35,7 +38,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t a, int64_t* warp_tot, int6
   if (lane == 31) warp_tot[warp] = a;
   __syncthreads();
   if (warp == 0) {
-    int64_t t = warp_tot[lane];
+    int64_t t = lane < (int)(blockDim.x >> 5) ? warp_tot[lane] : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t x = __shfl_up_sync(0xffffffffu, t, o);
@@ -68,11 +71,18 @@ __device__ __forceinline__ int2 costs(const PrefixCosts& c, bool own, int pairs)
   return make_int2(c.shared_fixed, pairs > kPrefixTilePairs ? c.two_tile : c.one_tile);
 }
 
-__global__ void __launch_bounds__(kThreads) prefix_plan_kernel(const PrefixPlanParams p) {
+// a * b / c of non-negative numbers whose result fits 32 bits, c > 0.
+__device__ __forceinline__ int64_t muldiv(int64_t a, int b, int c) {
+  const int64_t ab = a * b;
+  return ab <= UINT32_MAX ? (int64_t)((uint32_t)ab / (uint32_t)c) : a / c * b + a % c * b / c;
+}
+
+__global__ void __launch_bounds__(kMaxThreads) prefix_plan_kernel(const PrefixPlanParams p) {
   extern __shared__ int64_t dyn[];
   __shared__ int64_t warp_tot[32];
   __shared__ int s_bad, s_err;
-  const int tid = threadIdx.x, B = p.num_seqs, G = p.num_groups, T = p.q_len, H = p.num_kv_heads;
+  const int tid = threadIdx.x, nt = blockDim.x;
+  const int B = p.num_seqs, G = p.num_groups, T = p.q_len, H = p.num_kv_heads, P = p.num_parts;
   // [G + 1] each: group starts, least visible length, non-empty sequences, first of them,
   // shared tiles, first work row
   int32_t* cu = reinterpret_cast<int32_t*>(dyn);
@@ -84,28 +94,32 @@ __global__ void __launch_bounds__(kThreads) prefix_plan_kernel(const PrefixPlanP
   int64_t* cum = dyn + (6LL * (G + 1) + 1) / 2;  // [rows + 1] cost before each work row
   griddep_wait();
   griddep_launch_dependents();
+  // this thread's first inputs, all on their way at once
+  const int cu0 = p.cu_groups && tid <= G ? p.cu_groups[tid] : (tid == 0 ? 0 : B);
+  const int want0 = tid < G ? p.prefix_lens[tid] : 0;
+  const int len0 = tid < B ? p.seq_lens[tid] : 0;
   if (tid == 0) s_bad = s_err = 0;
-  __syncthreads();
-  for (int g = tid; g <= G; g += kThreads) {
-    cu[g] = p.cu_groups ? p.cu_groups[g] : (g == 0 ? 0 : B);
+  for (int g = tid; g <= G; g += nt) {
+    cu[g] = g == tid ? cu0 : (p.cu_groups ? p.cu_groups[g] : B);
     gmin[g] = INT32_MAX;
     gcnt[g] = 0;
     gfirst[g] = INT32_MAX;
   }
   __syncthreads();
-  for (int g = tid; g <= G; g += kThreads)
+  for (int g = tid; g <= G; g += nt)
     if (cu[g] < 0 || cu[g] > B || (g == 0 && cu[g] != 0) || (g == G && cu[g] != B) ||
         (g > 0 && cu[g] < cu[g - 1]))
       s_bad = 1;  // every writer stores 1
   __syncthreads();
   if (s_bad) {  // not a partition of the batch: one group without a prefix
     __syncthreads();
-    for (int g = tid; g <= G; g += kThreads) cu[g] = g == 0 ? 0 : B;
+    for (int g = tid; g <= G; g += nt) cu[g] = g == 0 ? 0 : B;
     if (tid == 0) s_err = HPC_DEVCHK_BAD_LENGTH;
     __syncthreads();
   }
-  for (int b = tid; b < B; b += kThreads) {
-    const int L = p.seq_lens[b];
+  auto length = [&](int b) { return b == tid ? len0 : p.seq_lens[b]; };
+  for (int b = tid; b < B; b += nt) {
+    const int L = length(b);
     if (L < 0) s_err = HPC_DEVCHK_BAD_LENGTH;
     if (L > 0) {
       const int g = find(cu, G, b);
@@ -116,11 +130,11 @@ __global__ void __launch_bounds__(kThreads) prefix_plan_kernel(const PrefixPlanP
   }
   __syncthreads();
   int64_t carry = 0;
-  for (int base = 0; base < G; base += kThreads) {
+  for (int base = 0; base < G; base += nt) {
     const int g = base + tid;
     int64_t rows = 0;
     if (g < G) {
-      const int want = p.prefix_lens[g];
+      const int want = g == tid ? want0 : p.prefix_lens[g];
       if (want < 0) s_err = HPC_DEVCHK_BAD_LENGTH;
       int s = 0;
       if (!s_bad && gcnt[g] >= 2) {
@@ -128,8 +142,7 @@ __global__ void __launch_bounds__(kThreads) prefix_plan_kernel(const PrefixPlanP
         s = min(s > 0 ? s / kBlockTokens : 0, p.max_blocks);
       }
       gtiles[g] = s;
-      if (s > 0)
-        rows = ((int64_t)(cu[g + 1] - cu[g]) * T + kPrefixRowPairs - 1) / kPrefixRowPairs;
+      if (s > 0) rows = ((cu[g + 1] - cu[g]) * T + kPrefixRowPairs - 1) / kPrefixRowPairs;
     }
     int64_t total;
     const int64_t incl = block_scan(rows, warp_tot, &total);
@@ -140,50 +153,45 @@ __global__ void __launch_bounds__(kThreads) prefix_plan_kernel(const PrefixPlanP
   const int V = shared + B;
   if (tid == 0) grow[G] = shared;
   __syncthreads();
-  int64_t units = 0;  // of this thread's rows
-  PrefixRec* recs = reinterpret_cast<PrefixRec*>(p.words + p.rec_off);
+  // a shared row's group: groups without rows repeat their neighbour's start,
+  // the last one with grow <= v has rows
+  auto shared_pairs = [&](int v, int g) {
+    return min(kPrefixRowPairs, (cu[g + 1] - cu[g]) * T - kPrefixRowPairs * (v - grow[g]));
+  };
+  auto record = [&](int v, int4& a, int4& b) {
+    if (v < shared) {
+      const int g = find(grow, G, v);
+      a = make_int4(cu[g] * T + kPrefixRowPairs * (v - grow[g]), shared_pairs(v, g), gfirst[g], 0);
+      b = make_int4(gtiles[g], 0, INT32_MAX, 0);
+    } else {
+      const int s = v - shared, L = max(length(s), 0);
+      const int t0 = L > 0 ? gtiles[find(cu, G, s)] : 0;
+      a = make_int4(s * T, T, s, t0);
+      b = make_int4((int)(((int64_t)L + kBlockTokens - 1) / kBlockTokens) - t0, 1, L, 0);
+    }
+  };
+  int4* recs = reinterpret_cast<int4*>(p.words + p.rec_off);
   carry = 0;
-  for (int base = 0; base < V; base += kThreads) {
+  for (int base = 0; base < V; base += nt) {
     const int v = base + tid;
     int64_t cost = 0;
     if (v < V) {
-      PrefixRec r;
-      r.pad = 0;
-      if (v < shared) {
-        // groups without rows repeat their neighbour's start: the last one with
-        // grow <= v has rows
-        const int g = find(grow, G, v);
-        const int k = v - grow[g], all = (cu[g + 1] - cu[g]) * T;
-        r.pair0 = cu[g] * T + kPrefixRowPairs * k;
-        r.pairs = min(kPrefixRowPairs, all - kPrefixRowPairs * k);
-        r.table = gfirst[g];
-        r.tile0 = 0;
-        r.tiles = gtiles[g];
-        r.own = 0;
-        r.len = INT32_MAX;
-      } else {
-        const int b = v - shared, L = max(p.seq_lens[b], 0), g = find(cu, G, b);
-        const int t0 = L > 0 ? gtiles[g] : 0;
-        r.pair0 = b * T;
-        r.pairs = T;
-        r.table = b;
-        r.tile0 = t0;
-        r.tiles = (int)(((int64_t)L + kBlockTokens - 1) / kBlockTokens) - t0;
-        r.own = 1;
-        r.len = L;
-        int32_t* sr = p.words + p.seq_off + 2 * b;
-        // the sequence's first shared work row and pair, or -1
-        const bool has = t0 > 0;
-        sr[0] = has ? grow[g] : -1;
-        sr[1] = cu[g] * T;
+      int4 a, b;
+      record(v, a, b);
+      recs[2 * v] = a;
+      recs[2 * v + 1] = b;
+      if (v >= shared) {  // the sequence's first shared work row, or -1, and its first pair
+        const int g = find(cu, G, a.z);
+        reinterpret_cast<int2*>(p.words + p.seq_off)[a.z] =
+            make_int2(a.w > 0 ? grow[g] : -1, cu[g] * T);
       }
-      const int2 fw = costs(p.costs, r.own != 0, r.pairs);
-      if (r.tiles > 0) cost = H * (fw.x + (int64_t)fw.y * r.tiles);
-      units += (int64_t)H * r.tiles;
-      int4* dst = reinterpret_cast<int4*>(recs + v);
-      const int4* src = reinterpret_cast<const int4*>(&r);
-      dst[0] = src[0];
-      dst[1] = src[1];
+      const int2 fw = costs(p.costs, b.y != 0, a.y);
+      if (b.x > 0) cost = H * (fw.x + (int64_t)fw.y * b.x);
+      // the units of a row are counted in 32 bits
+      if ((int64_t)H * b.x > INT32_MAX) {
+        s_err = HPC_DEVCHK_BAD_LENGTH;
+        s_bad = 2;
+      }
     }
     int64_t total;
     const int64_t incl = block_scan(cost, warp_tot, &total);
@@ -191,34 +199,35 @@ __global__ void __launch_bounds__(kThreads) prefix_plan_kernel(const PrefixPlanP
     carry += total;
   }
   const int64_t C = carry;
-  int64_t all_units;
-  block_scan(units, warp_tot, &all_units);
   if (tid == 0) cum[V] = C;
   __syncthreads();
-  // units of a work row are counted in 32 bits by its readers
-  const bool huge = all_units > INT32_MAX;
-  const int P = huge ? 0 : (int)min((int64_t)p.num_parts, all_units);
-  for (int q = tid; q <= P; q += kThreads) {
+  const bool none = C == 0 || s_bad == 2;
+  // boundary q: row v, unit u, and the record of row v for the part behind it
+  for (int q = tid; q <= P; q += nt) {
     int v = V, u = 0;
-    if (q < P) {
-      const int64_t c = C / P * q + C % P * q / P;
+    int4 a = make_int4(0, 0, 0, 0), b = a;
+    if (q < P && !none) {
+      const int64_t c = muldiv(C, q, P);
       v = find(cum, V, c);
-      const PrefixRec r = recs[v];  // written by this CTA before the barrier
-      const int2 fw = costs(p.costs, v >= shared, r.pairs);
-      const int64_t head = fw.x + (int64_t)fw.y * r.tiles, in = c - cum[v];
-      const int h = (int)(in / head);
+      record(v, a, b);
+      const int2 fw = costs(p.costs, b.y != 0, a.y);
+      const int64_t head = fw.x + (int64_t)fw.y * b.x, in = c - cum[v];
+      const int h = in <= UINT32_MAX && head <= UINT32_MAX ? (int)((uint32_t)in / (uint32_t)head)
+                                                           : (int)(in / head);
       const int64_t rest = in - h * head - fw.x;
-      u = h * r.tiles + (rest > 0 ? (int)((rest + fw.y - 1) / fw.y) : 0);
+      u = h * b.x + (rest > 0 ? (int)((uint32_t)(rest + fw.y - 1) / (uint32_t)fw.y) : 0);
     }
-    p.words[p.bound_off + 2 * q] = v;
-    p.words[p.bound_off + 2 * q + 1] = u;
+    reinterpret_cast<int2*>(p.words + p.bound_off)[q] = make_int2(v, u);
+    if (q < P) {
+      int4* first = reinterpret_cast<int4*>(p.words + p.first_off) + 2 * q;
+      first[0] = a;
+      first[1] = b;
+    }
   }
   if (tid == 0) {
-    if (huge) s_err = HPC_DEVCHK_BAD_LENGTH;
     if (s_err) atomicOr(p.err, s_err);
-    p.words[kPxRows] = huge ? 0 : V;
-    p.words[kPxShared] = shared;
-    p.words[kPxParts] = P;
+    p.words[kPxRows] = none ? 0 : V;
+    p.words[kPxParts] = none ? 0 : P;
   }
 }
 
@@ -234,7 +243,7 @@ cudaError_t launch_prefix_plan(const PrefixPlanParams& p, cudaStream_t stream) {
   const int64_t rows = 2LL * p.num_seqs + (int64_t)p.num_seqs * p.q_len / kPrefixRowPairs + 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(1);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(p.num_seqs <= 256 && p.num_groups < 256 ? 256 : kMaxThreads);
   cfg.dynamicSmemBytes =
       (size_t)(((6LL * (p.num_groups + 1) + 1) / 2 + rows + 1) * sizeof(int64_t));
   cfg.stream = stream;
