@@ -186,6 +186,9 @@ hpc_status hpc_decode_prefix_attn(const hpc_tensor* q, const hpc_tensor* k_cache
     PrefixParams p;
     std::memset(&p, 0, sizeof p);
     p.words = plan->d_words;
+    p.q = (const __nv_bfloat16*)q->data;
+    p.q_sp = pair_stride;
+    p.q_sh = hs;
     p.bound_off = pp.bound_off;
     p.first_off = pp.first_off;
     p.rec_off = pp.rec_off;

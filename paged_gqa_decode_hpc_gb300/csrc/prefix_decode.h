@@ -73,6 +73,8 @@ cudaError_t launch_prefix_plan(const PrefixPlanParams& p, cudaStream_t stream);
 struct PrefixParams {
   const int32_t* words;         // plan
   int32_t bound_off, first_off, rec_off;
+  const __nv_bfloat16* q;       // [pairs][H_q][128]
+  int64_t q_sp, q_sh;           // element strides over pair, head
   const int32_t* block_table;
   int64_t bt_sb;
   int32_t max_blocks;

@@ -23,6 +23,14 @@
 //    A lone chain S -> softmax -> P V leaves the tensor cores and the ring
 //    idle between its steps; two chains on alternate tiles fill in for each
 //    other.
+// Own pieces of a single new token have 8 rows only, and a chain through tensor
+// memory costs each tile its full latency (0.65 us a tile and 2.2 us a piece;
+// 64 x 1000 own positions: 52 us). They run as warp pieces: the 8 softmax warps take tiles in
+// turn, each alone from the ring with mma.sync (8 heads = the N of one
+// instruction; decode_unit.cuh) and fp32 state in registers; e4m3 tiles are read
+// as they are. At the end each warp leaves its state in shared memory (the Q
+// slots, which own pieces do not need and which follow all shared ones) and goes
+// on; the MMA warps join the 8 states of alternate pieces and write them out.
 // Q sits in two slots of 128 rows: one per row tile, or, with one row tile,
 // used in turn, so that the next piece's Q loads early.
 //
@@ -43,6 +51,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "decode_unit.cuh"
 #include "hpc_decode.h"
 #include "hpc_internal.h"
 #include "prefix_decode.h"
@@ -71,36 +80,40 @@ struct Lay {
   static constexpr int kConvWarps = FP8 ? 4 : 0;
   static constexpr int kConvWarp0 = 8;
   static constexpr int kProducerWarp = 8 + kConvWarps, kMmaWarp0 = kProducerWarp + 1;
-  static constexpr int kThreads = 32 * (kMmaWarp0 + 2);
-  static constexpr int kStages = FP8 ? 4 : 5;   // 16-bit K + V ring
-  static constexpr int kStages8 = FP8 ? 2 : 0;  // e4m3 K + V ring
+  // FP8: whole warpgroups (one warp idle), so that registers can move to the softmax ones
+  static constexpr int kThreads = FP8 ? 512 : 32 * (kMmaWarp0 + 2);
+  static constexpr int kStages = FP8 ? 3 : 5;   // 16-bit K + V ring
+  static constexpr int kStages8 = FP8 ? 4 : 0;  // e4m3 K + V ring
+  static constexpr int kTmaStages = FP8 ? kStages8 : kStages;  // the ring that TMA fills
+  static constexpr uint32_t kTmaStageBytes = FP8 ? kStageBytes8 : kStageBytes;
   static constexpr uint32_t kOffQ = 0;
   static constexpr uint32_t kOffKV = 2 * kQSlotBytes;
   static constexpr uint32_t kOffKV8 = kOffKV + kStages * kStageBytes;
+  static constexpr uint32_t kOffTma = FP8 ? kOffKV8 : kOffKV;
   static constexpr uint32_t kOffBar = kOffKV8 + kStages8 * kStageBytes8;
   // q_full[2], q_empty[2], q_ready[2], kv_full[S], kv_empty[S], kv8_full[S8],
-  // kv8_empty[S8], x_full, x_free, per pipeline: s_full, s_free, p_full[2],
-  // pv_done[2], drain
-  static constexpr int kNumBars = 6 + 2 * kStages + 2 * kStages8 + 2 + 14;
+  // kv8_empty[S8], x_full, x_free, dep_full[2], dep_free[2], q_done, per pipeline:
+  // s_full, s_free, p_full[2], pv_done[2], drain
+  static constexpr int kNumBars = 6 + 2 * kStages + 2 * kStages8 + 7 + 14;
   // int8 [2 slots][2 fills][128]: a warpgroup that lags may still read the scales
   // of a slot's fill while the next one is converted, never the one after that
   static constexpr uint32_t kOffScale = kOffBar + 8 * kNumBars;
   static constexpr uint32_t kOffX = kOffScale + (FP8 ? 4 * kRows : 0);  // float [2][128]
-  static constexpr uint32_t kOffMisc = kOffX + 2 * kRows * 4;
+  static constexpr uint32_t kOffWord = kOffX + 2 * kRows * 4;           // tile in each TMA slot
+  static constexpr uint32_t kOffMisc = kOffWord + 4 * kTmaStages;
   static constexpr uint32_t kSmemBytes = kOffMisc + 16 + 1024;  // + slack to align to 1024
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
+// FP8: of the launch's 512 x 128 registers, the two softmax warpgroups take 176
+// a thread and the two others keep 80: 256 * 176 + 256 * 80 = 65536.
+constexpr int kRegsSoftmax = 176, kRegsOther = 80;
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax) : "memory");
+}
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther) : "memory");
+}
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
   uint64_t r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
@@ -124,11 +137,6 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t x) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(x));
-  return h;
-}
 __device__ __forceinline__ void named_bar_sync(int id, int nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
@@ -147,6 +155,39 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
     if (mbar_try_wait(bar, parity)) return true;
     if ((it & 63u) == 0) {
       if (honour_abort && *abort_flag) return false;
+      if (globaltimer() - t0 > limit_ns) {
+        atomicOr(err, HPC_DEVCHK_TIMEOUT);
+        *abort_flag = 1;
+        return false;
+      }
+    }
+  }
+}
+
+// Several arrivals at once.
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+  asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(bar),
+               "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void st_release_word(uint32_t addr, uint32_t v) {
+  asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+// Bounded wait until the producer has issued tile `tile` into its slot. A slot's
+// successive rounds go to different warps, so a warp may ask for round r while
+// the slot's barrier has completed only round r - 2, which the parity cannot
+// tell apart. Once the slot's word equals the tile, rounds < r are complete and
+// round r + 1 cannot start before this warp lets go, so the parity wait that
+// follows is exact.
+__device__ __forceinline__ bool wait_word(uint32_t word, uint32_t tile, volatile int* abort_flag,
+                                          int32_t* err, unsigned long long limit_ns) {
+  const unsigned long long t0 = globaltimer();
+  for (uint32_t it = 1;; ++it) {
+    uint32_t v;
+    asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(v) : "r"(word) : "memory");
+    if (v == tile) return true;
+    if ((it & 63u) == 0) {
+      if (*abort_flag) return false;
       if (globaltimer() - t0 > limit_ns) {
         atomicOr(err, HPC_DEVCHK_TIMEOUT);
         *abort_flag = 1;
@@ -236,7 +277,10 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
   auto kv8_full = [&](int s) { return bars + 8u * (6 + 2 * S + s); };
   auto kv8_empty = [&](int s) { return bars + 8u * (6 + 2 * S + S8 + s); };
   const uint32_t x_full = bars + 8u * (6 + 2 * S + 2 * S8), x_free = x_full + 8u;
-  auto gbar = [&](int g, int k) { return x_full + 16u + 8u * (7 * g + k); };
+  auto dep_full = [&](int i) { return x_full + 16u + 8u * i; };  // warp pieces' states
+  auto dep_free = [&](int i) { return x_full + 32u + 8u * i; };
+  const uint32_t q_done = x_full + 48u;  // the last MMA on a Q slot is done
+  auto gbar = [&](int g, int k) { return x_full + 56u + 8u * (7 * g + k); };
   auto s_full = [&](int g) { return gbar(g, 0); };
   auto s_free = [&](int g) { return gbar(g, 1); };
   auto p_full = [&](int g, int i) { return gbar(g, 2 + i); };
@@ -275,6 +319,13 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
       }
       mbar_init(x_full, kRows);
       mbar_init(x_free, kRows);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(dep_full(i), 8);  // one arrival per softmax warp
+        mbar_init(dep_free(i), 1);
+      }
+      mbar_init(q_done, 2);  // one commit per MMA warp
+      for (int s = 0; s < Lt::kTmaStages; ++s)
+        st_release_word(base + Lt::kOffWord + 4 * s, 0xFFFFFFFFu);
       for (int g = 0; g < 2; ++g) {
         mbar_init(s_full(g), 1);
         mbar_init(s_free(g), kRows);
@@ -301,6 +352,9 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
   griddep_wait();  // the plan (and inputs) of the preceding kernels are visible
   griddep_launch_dependents();
   const uint32_t tmem = *s_tmem;
+  // one new token per sequence: own pieces (they come after all shared ones) are
+  // warp pieces
+  const bool warp_own = p.q_len == 1;
 
   Walk walk;
   walk.begin(p, part);
@@ -311,6 +365,7 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
 
   if (warp == Lt::kProducerWarp) {
     // ------------------------------------------------------------ producer
+    if (FP8) regs_dec();
     int issued = 0;                               // K / V tiles issued, in order
     int q_issued[2] = {0, 0};                     // fills issued per Q slot
     int stop = p.withhold_copies != 0 ? 1 : 0;    // failure-path test: nothing is issued
@@ -320,7 +375,7 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
       const bool own = walk.rb.y != 0;
       const int c1 = p.kv_swap ? pc.h : 0, c2 = p.kv_swap ? 0 : pc.h;
       const int slot0 = pc.two ? 0 : (ones & 1), slot1 = pc.two ? 1 : slot0;
-      for (int sl = slot0; sl <= slot1; ++sl) {
+      for (int sl = slot0; sl <= slot1 && !(own && warp_own); ++sl) {
         if (lane == 0 && !stop) {
           const int fill = uses[sl];
           if (fill == 0 || wait(q_empty(sl), fill - 1)) {
@@ -364,6 +419,7 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
               const int slot = j % S8n, round = j / S8n;
               if (round == 0 || wait(kv8_empty(slot), round - 1)) {
                 const uint32_t fb = kv8_full(slot);
+                st_release_word(base + Lt::kOffWord + 4 * slot, (uint32_t)j);
                 const uint32_t dk = sKV8 + slot * kStageBytes8, dv = dk + kKVTileBytes8;
                 mbar_expect_tx(fb, kStageBytes8);
                 tma_load_4d(dk, &tmk, fb, 0, c1, c2, bk);
@@ -376,6 +432,7 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
               const int slot = j % S, round = j / S;
               if (round == 0 || wait(kv_empty(slot), round - 1)) {
                 const uint32_t fb = kv_full(slot);
+                st_release_word(base + Lt::kOffWord + 4 * slot, (uint32_t)j);
                 const uint32_t dk = sKV + slot * kStageBytes, dv = dk + kKVTileBytes;
                 mbar_expect_tx(fb, kStageBytes);
                 tma_load_4d(dk, &tmk, fb, 0, c1, c2, bk);
@@ -414,11 +471,13 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
     // c' ^ (t % 8)). Each group of 8 threads serving one 16-byte access covers
     // all 8 bank groups on the load and both stores. V rows behind the end of
     // the sequence become zeros.
+    regs_dec();
     constexpr int kNT = 128;
     const int ct = threadIdx.x - 32 * Lt::kConvWarp0;
     const int cq = ct & 15, c = cq & 7, cr = ((cq >> 2) & 1) ^ (cq >> 3);
     bool ok = true;
     while (ok && walk.next(pc)) {
+      if (walk.rb.y && warp_own) break;  // the e4m3 tiles of warp pieces are read as they are
       const int n = pc.te - pc.tb;
       const int len = walk.rb.y ? walk.rb.z : INT32_MAX, tile0 = walk.ra.w + pc.tb;
       for (int j = 0; ok && j < n; ++j) {
@@ -440,8 +499,8 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
           const bool gone = mat == 1 && t >= valid;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            w[2 * q] = gone ? 0u : e4m3x2_to_f16x2((uint16_t)(xs[q] & 0xFFFFu));
-            w[2 * q + 1] = gone ? 0u : e4m3x2_to_f16x2((uint16_t)(xs[q] >> 16));
+            w[2 * q] = gone ? 0u : e4m3x2_to_f16x2(xs[q]);
+            w[2 * q + 1] = gone ? 0u : e4m3x2_to_f16x2(xs[q] >> 16);
           }
           const int cc = (c & 3) * 2;
           const uint32_t row = kb + mat * kKVTileBytes + (c >> 2) * (kKVTileBytes / 2) + t * 128;
@@ -461,10 +520,14 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
       kt += n;
     }
     named_bar_sync(1, Lt::kThreads);
+  } else if (FP8 && warp >= Lt::kMmaWarp0 + 2) {
+    regs_dec();  // the idle warp of the last warpgroup
+    named_bar_sync(1, Lt::kThreads);
   } else if (warp >= Lt::kMmaWarp0) {
     // ------------------------------------------- MMA issue for pipeline g
     // The whole warp runs the schedule so its values stay warp-uniform; one
     // elected lane issues the MMAs and commits.
+    if (FP8) regs_dec();
     const int g = warp - Lt::kMmaWarp0;
     const bool leader = elect_one() != 0;
     bool issued_any = false;
@@ -476,10 +539,75 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
     // V: MN-major; 64-column halves 8 KB apart, 8-token row groups 1 KB apart
     const uint64_t vd0 = smem_desc_sw128(sKV + kKVTileBytes, kKVTileBytes / 2, 1024);
     const uint32_t dS = tmem + kColsPerPipe * g + kColS, od = tmem + kColsPerPipe * g + kColO;
+    // The end of a warp piece (warp pieces of parity g are this warp's): the
+    // states of the 8 softmax warps joined, in warp order, and written out.
+    auto finish_warp_piece = [&](int use) -> bool {
+      if (!wait_all(dep_full(g), use)) return false;
+      const int d8 = lane >> 2, h2 = 2 * (lane & 3);  // accumulator lane: rows d8, heads h2, h2 + 1
+      const volatile float* ml = s_x + g * kRows;     // [8 warps][m of 8 heads, l of 8 heads]
+      float M0 = -INFINITY, M1 = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        M0 = fmaxf(M0, ml[16 * w + h2]);
+        M1 = fmaxf(M1, ml[16 * w + h2 + 1]);
+      }
+      float l0 = 0.f, l1 = 0.f, acc[8][4];
+#pragma unroll
+      for (int dm = 0; dm < 8; ++dm) acc[dm][0] = acc[dm][1] = acc[dm][2] = acc[dm][3] = 0.f;
+#pragma unroll 1
+      for (int w = 0; w < 8; ++w) {
+        const float m0 = ml[16 * w + h2], m1 = ml[16 * w + h2 + 1];
+        if (m0 == -INFINITY && ml[16 * w + 8 + h2] == 0.f) continue;  // no tile in this piece
+        const float f0 = ex2(m0 - M0), f1 = ex2(m1 - M1);
+        l0 += ml[16 * w + 8 + h2] * f0;
+        l1 += ml[16 * w + 9 + h2] * f1;
+        const uint32_t src = sQ + (uint32_t)g * kQSlotBytes + (uint32_t)w * 4096u + 16u * lane;
+#pragma unroll
+        for (int dm = 0; dm < 8; ++dm) {
+          float a, b, c2, d2;
+          asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(a), "=f"(b), "=f"(c2), "=f"(d2)
+                       : "r"(src + 512u * dm));
+          acc[dm][0] += a * f0;
+          acc[dm][1] += b * f1;
+          acc[dm][2] += c2 * f0;
+          acc[dm][3] += d2 * f1;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(dep_free(g));
+      const int64_t blk = pc.tb == 0
+                              ? p.ws.own0 + (int64_t)walk.ra.x * p.num_kv_heads + pc.h
+                              : p.ws.cont0 + (int64_t)part * kPrefixRowPairs;
+      float* dst = reinterpret_cast<float*>(p.ws.o + blk * 256);  // [d / 4][head][d % 4]
+#pragma unroll
+      for (int dm = 0; dm < 8; ++dm)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int d = acc_d<FP8>(dm, r, d8);
+          dst[(d >> 2) * 32 + 4 * h2 + (d & 3)] = acc[dm][2 * r];
+          dst[(d >> 2) * 32 + 4 * h2 + 4 + (d & 3)] = acc[dm][2 * r + 1];
+        }
+      if (lane < 4) {
+        p.ws.m[blk * 8 + h2] = M0;
+        p.ws.m[blk * 8 + h2 + 1] = M1;
+        p.ws.l[blk * 8 + h2] = l0;
+        p.ws.l[blk * 8 + h2 + 1] = l1;
+      }
+      return true;
+    };
     int c = 0;  // tiles of this pipeline before this piece
+    int warp_pieces = 0;
     bool ok = true;
     while (ok && walk.next(pc)) {
       const int n = pc.te - pc.tb;
+      if (walk.rb.y && warp_own) {
+        if (warp_pieces == 0 && leader) mma_commit(q_done);
+        __syncwarp();
+        if ((warp_pieces & 1) == g) ok = finish_warp_piece(warp_pieces >> 1);
+        ++warp_pieces;
+        continue;
+      }
       const int slot0 = pc.two ? 0 : (ones & 1), slot1 = pc.two ? 1 : slot0;
       const int my_slot = pc.two ? g : slot0;
       const int stride = pc.two ? 1 : 2, first = pc.two ? 0 : g;
@@ -572,6 +700,7 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
     if (warp == Lt::kMmaWarp0) tmem_dealloc(tmem, 2 * kColsPerPipe);
   } else {
     // ------------------------------------------- softmax warpgroup of pipeline g
+    if (FP8) regs_inc();
     const int g = warp >> 2;
     const int r = threadIdx.x - kRows * g;  // query row = TMEM lane
     const int wg_warp = warp & 3;
@@ -580,9 +709,88 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
     const int T = p.q_len;
     int cnt_of[2] = {0, 0};  // tiles of each pipeline before this piece
     int joins = 0;           // pieces whose two states were joined, before this one
+    int warp_pieces = 0;
     bool ok = true;
     while (ok && walk.next(pc)) {
       const int n = pc.te - pc.tb;
+      if (walk.rb.y && warp_own) {
+        // ---- warp piece: this warp takes every 8th tile of the ring
+        float acc[8][4];
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+        for (int dm = 0; dm < 8; ++dm) acc[dm][0] = acc[dm][1] = acc[dm][2] = acc[dm][3] = 0.f;
+        const int j0 = (warp - kt) & 7;
+        if (j0 < n) {
+          uint32_t qf[8][2];
+          const float sl2 =
+              p.score_scale_log2 * load_q<FP8>(p.q + (int64_t)walk.ra.x * p.q_sp +
+                                                   (int64_t)(kGroupRows * pc.h) * p.q_sh,
+                                               p.q_sh, lane, qf);
+          for (int j = j0; j < n; j += 8) {
+            const int k = kt + j, slot = k % Lt::kTmaStages;
+            ok = __all_sync(0xffffffffu, wait_word(base + Lt::kOffWord + 4 * slot, (uint32_t)k,
+                                                   s_abort, err, lim_ns));
+            if (ok) ok = wait_all(FP8 ? kv8_full(slot) : kv_full(slot), k / Lt::kTmaStages);
+            if (!ok) break;
+            const uint32_t kb = base + Lt::kOffTma + slot * Lt::kTmaStageBytes;
+            const uint32_t vb = kb + Lt::kTmaStageBytes / 2;
+            const int valid = walk.rb.z - (walk.ra.w + pc.tb + j) * kBlockTokens;
+            if (valid < kBlockTokens) {
+              // V rows behind the sequence's end (both column halves of a 16-bit tile)
+              constexpr int kHalves = FP8 ? 1 : 2;
+              for (int q = lane; q < (kBlockTokens - valid) * 8 * kHalves; q += 32)
+                st_shared_zero16(vb + (q & 8) / 8 * (kHalves - 1) * (kKVTileBytes / 2) +
+                                 (uint32_t)(valid + q / (8 * kHalves)) * 128 +
+                                 (uint32_t)(q & 7) * 16);
+              __syncwarp();
+            }
+            compute_unit<FP8>(kb, vb, qf, valid, sl2, m, l, acc, lane);
+            if (valid < kBlockTokens) fence_async_shared();  // before TMA writes there again
+            __syncwarp();
+            if (lane == 0) {
+              if (FP8) mbar_arrive_n(kv8_empty(slot), 32 * Lt::kConvWarps);
+              else mbar_arrive_n(kv_empty(slot), 2);
+            }
+          }
+          if (!ok) break;
+        }
+        // the state of this warp to the piece's buffer; the warp that joins them
+        // is the MMA warp of the buffer's number
+        const int buf = warp_pieces & 1, use = warp_pieces >> 1;
+        if (use > 0) {
+          ok = wait_all(dep_free(buf), use - 1);
+        } else {
+          // first use: the buffers lie in the Q slots and the join cells
+          ok = wait_all(q_done, 0);
+          if (ok && joins > 0) ok = wait_all(x_free, joins - 1);
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
+          l[1] += __shfl_xor_sync(0xffffffffu, l[1], o);
+        }
+        volatile float* ml = s_x + buf * kRows + 16 * warp;
+        if (lane < 4) {
+          ml[2 * lane] = m[0];
+          ml[2 * lane + 1] = m[1];
+          ml[8 + 2 * lane] = l[0];
+          ml[9 + 2 * lane] = l[1];
+        }
+        if (j0 < n) {
+          const uint32_t dst = sQ + (uint32_t)buf * kQSlotBytes + (uint32_t)warp * 4096u + 16u * lane;
+#pragma unroll
+          for (int dm = 0; dm < 8; ++dm)
+            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 512u * dm),
+                         "f"(acc[dm][0]), "f"(acc[dm][1]), "f"(acc[dm][2]), "f"(acc[dm][3])
+                         : "memory");
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(dep_full(buf));
+        ++warp_pieces;
+        kt += n;
+        continue;
+      }
       const int slot0 = pc.two ? 0 : (ones & 1);
       const int my_slot = pc.two ? g : slot0;
       const int stride = pc.two ? 1 : 2, first = pc.two ? 0 : g;

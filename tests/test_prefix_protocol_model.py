@@ -5,6 +5,11 @@ pipes and the two softmax warpgroups run as step-wise processes over the same
 random pieces; mbarriers have their hardware semantics (phases, arrival counts,
 waits on a phase PARITY only).
 
+With one new token per sequence the pieces of own tiles come last and run
+differently: each softmax warp takes every 8th tile straight from the ring (after
+the slot's issued word, as its phases go to different warps), leaves its state in
+one of two buffers in the Q slots, and MMA warp g joins the pieces of parity g.
+
 Checked: no wait passes on a stale phase, no buffer is overwritten before its
 reader is done (Q slots, ring slots, S, P, O during a rescale and while the two
 states are joined, the exchanged maxima), no MMA reads a Q slot before it is
@@ -36,8 +41,9 @@ class Barrier:
 
 
 class Model:
-    def __init__(self, rng, fp8, pieces, stages, stages8):
+    def __init__(self, rng, fp8, pieces, stages, stages8, warp_pieces=()):
         self.rng, self.fp8, self.pieces, self.S, self.S8 = rng, fp8, pieces, stages, stages8
+        self.warp_pieces = list(warp_pieces)
         B = Barrier
         two = lambda name, n: [B(f"{name}{i}", n) for i in range(2)]
         self.q_full, self.q_empty, self.q_ready = two("q_full", 1), two("q_empty", 2), two("q_ready", 1)
@@ -46,6 +52,11 @@ class Model:
         self.kv8_full = [B(f"kv8_full{s}", 1) for s in range(stages8)]
         self.kv8_empty = [B(f"kv8_empty{s}", 1) for s in range(stages8)]
         self.x_full, self.x_free = B("x_full", 1), B("x_free", 1)
+        self.dep_full, self.dep_free = two("dep_full", 8), two("dep_free", 1)
+        self.q_done = B("q_done", 2)
+        self.word = [None] * (stages8 if fp8 else stages)   # tile issued into a slot
+        self.dep = [{}, {}]              # warp -> (piece, its tiles) in a buffer
+        self.joined = []                 # (piece, tiles) written out
         self.s_full, self.s_free = two("s_full", 1), two("s_free", 1)
         self.p_full = [two(f"p_full{g}.", 1) for g in range(2)]
         self.pv_done = [two(f"pv_done{g}.", 1) for g in range(2)]
@@ -119,6 +130,76 @@ class Model:
                     full[k % S].arrive()
                 self.tma.append((self.tick + self.rng.randint(1, 30), land))
                 yield
+        kt = sum(n for n, _ in self.pieces)
+        full, empty, S, ring = (self.kv8_full, self.kv8_empty, self.S8, self.ring8) if self.fp8 else \
+            (self.kv_full, self.kv_empty, self.S, self.ring)
+        for n in self.warp_pieces:
+            for k in range(kt, kt + n):
+                if k >= S:
+                    yield from self.until(empty[k % S], k // S - 1)
+                old = ring[k % S]  # (an e4m3 tile before the warp pieces: its converter is done)
+                assert (self.fp8 and not isinstance(old, tuple)) or not self.ring_reads.get(old), "ring slot overwritten"
+                ring[k % S], self.word[k % S], self.ring_reads[("w", k)] = None, k, 1
+
+                def land(k=k):
+                    ring[k % S] = ("w", k)
+                    full[k % S].arrive()
+                self.tma.append((self.tick + self.rng.randint(1, 30), land))
+                yield
+            kt += n
+
+    def consumer(self, w):
+        """Softmax warp w in the warp pieces."""
+        joins = sum(1 for n, two in self.pieces if not two and n > 1)
+        full, empty, S, ring = (self.kv8_full, self.kv8_empty, self.S8, self.ring8) if self.fp8 else \
+            (self.kv_full, self.kv_empty, self.S, self.ring)
+        kt = sum(n for n, _ in self.pieces)
+        for i, n in enumerate(self.warp_pieces):
+            got = []
+            for j in range((w - kt) % 8, n, 8):
+                k = kt + j
+                while self.word[k % S] != k:
+                    yield WAIT
+                yield from self.until(full[k % S], k // S)
+                assert ring[k % S] == ("w", k)
+                for _ in range(self.rng.randint(0, 6)):
+                    yield
+                assert ring[k % S] == ("w", k)
+                got.append(j)
+                self.ring_reads[("w", k)] = 0
+                for _ in range(empty[k % S].count):
+                    empty[k % S].arrive()
+            buf, use = i & 1, i >> 1
+            if use:
+                yield from self.until(self.dep_free[buf], use - 1)
+            else:
+                yield from self.until(self.q_done, 0)
+                if joins:
+                    yield from self.until(self.x_free, joins - 1)
+                assert not self.q_readers[buf] and not self.q_left[buf], "state over a Q slot in use"
+                assert not self.o_joining, "state over the join cells in use"
+            assert w not in self.dep[buf], "state overwritten"
+            self.dep[buf][w] = (i, got)
+            yield
+            self.dep_full[buf].arrive()
+            kt += n
+
+    def join_warps(self, g):
+        """MMA warp g behind its last MMA: the pieces of parity g."""
+        if self.warp_pieces:
+            self.commit(g, self.q_done)
+        for i, n in enumerate(self.warp_pieces):
+            if i & 1 == g:
+                yield from self.until(self.dep_full[g], i >> 1)
+                tiles = []
+                for w in range(8):
+                    piece, got = self.dep[g][w]
+                    assert piece == i
+                    tiles += got
+                    yield
+                self.joined.append((i, sorted(tiles)))
+                self.dep[g] = {}
+                self.dep_free[g].arrive()
 
     def fill(self, k, two):
         old = self.ring[k % self.S]
@@ -219,6 +300,7 @@ class Model:
                     yield from issue_s(q + 1)
                 yield from issue_pv(q)
             c += len(mine)
+        yield from self.join_warps(g)
 
     def softmax(self, g):
         count, joins = [0, 0], 0
@@ -277,14 +359,15 @@ class Model:
                 self.x_full.arrive()
             joins += join
             count = [count[0] + len(mines[0]), count[1] + len(mines[1])]
+        self.more += [self.consumer(w) for w in range(4 * g, 4 * g + 4)]
 
     def run(self):
         roles = [self.producer(), self.mma(0), self.mma(1), self.softmax(0), self.softmax(1)]
         if self.fp8:
             roles.append(self.converter())
         weights = [self.rng.choice([1, 1, 3, 10]) for _ in roles]  # some run ahead, some lag
-        idle = 0
-        while roles or self.tma or any(self.pipe):
+        idle, self.more = 0, []
+        while roles or self.more or self.tma or any(self.pipe):
             self.tick += 1
             moved = False
             for t in [t for t in self.tma if t[0] <= self.tick]:
@@ -302,6 +385,8 @@ class Model:
                     if head[0] <= 0:
                         self.pipe[g].pop(0)
                         head[2]()
+            weights += [self.rng.choice([1, 1, 3, 10]) for _ in self.more]
+            roles, self.more = roles + self.more, []
             if roles:
                 r = self.rng.choices(range(len(roles)), weights)[0]
                 try:
@@ -314,6 +399,7 @@ class Model:
             assert idle < 3000, "deadlock"
         assert sorted(self.out) == sorted((i, g) for i, (n, two) in enumerate(self.pieces)
                                           for g in ((0, 1) if two else (0,)))
+        assert sorted(self.joined) == [(i, list(range(n))) for i, n in enumerate(self.warp_pieces)]
 
 
 @pytest.mark.parametrize("fp8", [False, True])
@@ -322,7 +408,8 @@ def test_no_stale_wait_no_overwrite_no_deadlock(fp8, seed):
     rng = random.Random(seed * 2 + fp8)
     for _ in range(25):
         pieces = [(rng.choice([1, 1, 2, 3, 4, 5, 9]), rng.random() < 0.4) for _ in range(rng.randint(1, 8))]
-        Model(rng, fp8, pieces, *((4, 2) if fp8 else (5, 0))).run()
+        last = [rng.choice([1, 2, 5, 8, 9, 20]) for _ in range(rng.choice([0, 0, 1, 3, 7]))]
+        Model(rng, fp8, pieces if rng.random() < 0.9 or not last else [], *((3, 4) if fp8 else (5, 0)), last).run()
 
 
 def test_the_model_sees_a_missing_wait():
@@ -352,13 +439,33 @@ def test_the_model_sees_a_missing_wait():
                         list.__setitem__(self, 0, v)
                 self.scale[s] = Cell([None])
 
-    for broken in (NoJoinWait, OneArrival, OneScale):
+    class NoWord(Model):  # a warp trusts the parity alone
+        def __init__(self, *a):
+            super().__init__(*a)
+
+            class Any(list):
+                def __getitem__(self, i):
+                    return Always()
+
+            class Always:
+                def __ne__(self, other):
+                    return False
+            self.word = Any(self.word)
+
+    class NoSlotWait(Model):  # states go to the Q slots without asking for them
+        def until(self, bar, phase):
+            if bar is self.q_done:
+                return
+            yield from super().until(bar, phase)
+
+    for broken in (NoJoinWait, OneArrival, OneScale, NoWord, NoSlotWait):
         failed = 0
         for seed in range(200):
             rng = random.Random(seed)
             pieces = [(rng.choice([1, 1, 2, 3, 4]), rng.random() < 0.3) for _ in range(12)]
             try:
-                broken(rng, broken is OneScale, pieces, *((4, 2) if broken is OneScale else (5, 0))).run()
+                last = [rng.choice([1, 3, 9]) for _ in range(6)] if broken in (NoWord, NoSlotWait) else []
+                broken(rng, broken is OneScale, pieces, *((3, 4) if broken is OneScale else (5, 0)), last).run()
             except AssertionError:
                 failed += 1
         assert failed, broken.__name__
