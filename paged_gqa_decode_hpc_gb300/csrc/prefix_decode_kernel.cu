@@ -72,7 +72,9 @@ constexpr uint32_t kKVTileBytes = 64 * 128 * 2;     // 16 KB: two 8 KB column ha
 constexpr uint32_t kStageBytes = 2 * kKVTileBytes;  // K + V
 constexpr uint32_t kKVTileBytes8 = 64 * 128;        // 8 KB: one e4m3 K or V tile
 constexpr uint32_t kStageBytes8 = 2 * kKVTileBytes8;
-constexpr uint32_t kColS = 0, kColP = 64, kColO = 128, kColsPerPipe = 256;
+// tensor memory of a pipeline: two S buffers of 64 columns (P of a tile overwrites
+// the first half of its S), O
+constexpr uint32_t kColS = 0, kColO = 128, kColsPerPipe = 256;
 constexpr float kRescaleThreshold = 8.0f;           // log2 units
 
 template <bool FP8>
@@ -93,7 +95,7 @@ struct Lay {
   static constexpr uint32_t kOffBar = kOffKV8 + kStages8 * kStageBytes8;
   // q_full[2], q_empty[2], q_ready[2], kv_full[S], kv_empty[S], kv8_full[S8],
   // kv8_empty[S8], x_full, x_free, dep_full[2], dep_free[2], q_done, per pipeline:
-  // s_full, s_free, p_full[2], pv_done[2], drain
+  // s_full[2], p_full[2], pv_done[2], drain
   static constexpr int kNumBars = 6 + 2 * kStages + 2 * kStages8 + 7 + 14;
   // int8 [2 slots][2 fills][128]: a warpgroup that lags may still read the scales
   // of a slot's fill while the next one is converted, never the one after that
@@ -142,6 +144,18 @@ __device__ __forceinline__ void named_bar_sync(int id, int nthreads) {
 }
 __device__ __forceinline__ void st_shared_zero16(uint32_t a) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0) : "memory");
+}
+
+// One look at an mbarrier phase.
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 // Bounded wait on an mbarrier phase; false when the CTA aborts or the limit
@@ -281,8 +295,7 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
   auto dep_free = [&](int i) { return x_full + 32u + 8u * i; };
   const uint32_t q_done = x_full + 48u;  // the last MMA on a Q slot is done
   auto gbar = [&](int g, int k) { return x_full + 56u + 8u * (7 * g + k); };
-  auto s_full = [&](int g) { return gbar(g, 0); };
-  auto s_free = [&](int g) { return gbar(g, 1); };
+  auto s_full = [&](int g, int i) { return gbar(g, i); };
   auto p_full = [&](int g, int i) { return gbar(g, 2 + i); };
   auto pv_done = [&](int g, int i) { return gbar(g, 4 + i); };
   auto drain = [&](int g) { return gbar(g, 6); };
@@ -327,9 +340,8 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
       for (int s = 0; s < Lt::kTmaStages; ++s)
         st_release_word(base + Lt::kOffWord + 4 * s, 0xFFFFFFFFu);
       for (int g = 0; g < 2; ++g) {
-        mbar_init(s_full(g), 1);
-        mbar_init(s_free(g), kRows);
         for (int i = 0; i < 2; ++i) {
+          mbar_init(s_full(g, i), 1);
           mbar_init(p_full(g, i), kRows);
           mbar_init(pv_done(g, i), 1);
         }
@@ -612,36 +624,34 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
       const int my_slot = pc.two ? g : slot0;
       const int stride = pc.two ? 1 : 2, first = pc.two ? 0 : g;
       const int mine = first < n ? (n - first + stride - 1) / stride : 0;  // tiles of this pipeline
-      // S(i) = Q K^T for the pipeline's i-th tile of the piece into its single
-      // S buffer, once its softmax warps have copied the previous S out
+      // S(i) = Q K^T for the pipeline's i-th tile of the piece, into the S buffer
+      // of its parity. That held P of the tile two before, whose P V this thread
+      // has issued earlier: the tensor pipe runs them in order.
       const uint64_t qd = smem_desc_sw128(sQ + (uint32_t)my_slot * kQSlotBytes, 16, 1024);
-      auto issue_s = [&](int i, bool last) -> bool {
-        const int k = kt + first + i * stride, slot = k % S;
-        if (!wait_all(kv_full(slot), k / S)) return false;
-        if (c + i >= 1 && !wait_all(s_free(g), c + i - 1)) return false;
+      auto issue_s = [&](int i) {
+        const int slot = (kt + first + i * stride) % S;
         tc_fence_after();
         const uint64_t kd = kd0 + (uint64_t)(slot * (kStageBytes >> 4));
+        const uint32_t d = dS + 64u * (uint32_t)((c + i) & 1);
         if (leader) {
           // Q and K: K-major; 64-column halves 16 KB / 8 KB apart, 16 columns = 32 bytes
-          mma_f16_ss(dS, qd, kd, kIdS, 0u);
+          mma_f16_ss(d, qd, kd, kIdS, 0u);
 #pragma unroll
           for (int kk = 1; kk < 8; ++kk)
-            mma_f16_ss(dS, qd + (kk >> 2) * (kQHalfBytes >> 4) + (kk & 3) * 2,
+            mma_f16_ss(d, qd + (kk >> 2) * (kQHalfBytes >> 4) + (kk & 3) * 2,
                        kd + (kk >> 2) * ((kKVTileBytes / 2) >> 4) + (kk & 3) * 2, kIdS, 1u);
-          mma_commit(s_full(g));
-          if (last) mma_commit(q_empty(my_slot));
+          mma_commit(s_full(g, (c + i) & 1));
+          if (i + 1 == mine) mma_commit(q_empty(my_slot));
         }
         __syncwarp();
-        return true;
       };
       // O += P V for the i-th tile, P from tensor memory (16 keys = 8 columns
       // per step); the ring slot is released once the MMAs on it are done
-      auto issue_pv = [&](int i) -> bool {
+      auto issue_pv = [&](int i) {
         const int k = kt + first + i * stride, x = c + i;
-        if (!wait_all(p_full(g, x & 1), x >> 1)) return false;
         tc_fence_after();
         const uint64_t vd = vd0 + (uint64_t)((k % S) * (kStageBytes >> 4));
-        const uint32_t pa = tmem + kColsPerPipe * g + kColP + 32u * (uint32_t)(x & 1);
+        const uint32_t pa = tmem + kColsPerPipe * g + kColS + 64u * (uint32_t)(x & 1);
         if (leader) {
           mma_f16_ts(od, pa, vd, kIdPV, i > 0 ? 1u : 0u);
 #pragma unroll
@@ -650,16 +660,6 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
           mma_commit(kv_empty(k % S));
         }
         __syncwarp();
-        return true;
-      };
-      // a tile of the other pipeline: this warp's arrival, in the right round
-      // (once the tile has landed, the slot's previous round is over)
-      auto skip = [&](int j) -> bool {
-        const int k = kt + j;
-        if (!wait_all(kv_full(k % S), k / S)) return false;
-        if (leader) mbar_arrive(kv_empty(k % S));
-        __syncwarp();
-        return true;
       };
       // Q as landed (BF16) or converted (FP8); a slot that this pipeline does
       // not use gets its arrival once it is filled
@@ -671,20 +671,49 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
         }
         ++uses[sl];
       }
-      if (!pc.two) {
-        ++ones;
-        if (ok && g == 1) ok = skip(0);
-      }
-      // S(i + 1) runs while the softmax warps work on tile i; P V(i) follows
-      // once P(i) is written
-      if (ok && mine > 0) {
-        ok = issue_s(0, mine == 1);
-        issued_any = true;
-      }
-      for (int i = 0; ok && i < mine; ++i) {
-        if (stride == 2 && first + 2 * i + 1 < n) ok = skip(first + 2 * i + 1);
-        if (ok && i + 1 < mine) ok = issue_s(i + 1, i + 2 == mine);
-        if (ok) ok = issue_pv(i);
+      if (!pc.two) ++ones;
+      // Whatever is ready next. The ring's tiles in their order (a look at a later
+      // slot's barrier could see a stale phase): S(s) for this pipeline's, whose
+      // buffer is free once P V(s - 2) is issued; for the other pipeline's, with
+      // one row tile, this warp's arrival once the tile has landed. And P V(v).
+      int s = 0, v = 0, j = 0;  // S and P V issued, tiles of the ring passed
+      unsigned long long idle_since = 0;
+      for (uint32_t it = 1; ok && (v < mine || j < n);) {
+        bool did = false;
+        const bool own_tile = stride == 1 || (j & 1) == g;
+        if (j < n && (!own_tile || s < v + 2)) {
+          const int k = kt + j;
+          if (__all_sync(0xffffffffu, mbar_test_wait(kv_full(k % S), (k / S) & 1))) {
+            if (own_tile) {
+              issue_s(s++);
+              issued_any = true;
+            } else {
+              if (leader) mbar_arrive(kv_empty(k % S));
+              __syncwarp();
+            }
+            ++j;
+            did = true;
+          }
+        }
+        if (v < s && __all_sync(0xffffffffu,
+                                mbar_test_wait(p_full(g, (c + v) & 1), ((c + v) >> 1) & 1))) {
+          issue_pv(v++);
+          did = true;
+        }
+        if (did) {
+          idle_since = 0;
+        } else if ((++it & 63u) == 0) {  // bounded: nothing ready for the limit
+          const unsigned long long now = globaltimer();
+          if (idle_since == 0) idle_since = now;
+          const bool late = now - idle_since > lim_ns;
+          if (__any_sync(0xffffffffu, late || *s_abort)) {
+            if (late && lane == 0) {
+              atomicOr(err, HPC_DEVCHK_TIMEOUT);
+              *s_abort = 1;
+            }
+            ok = false;
+          }
+        }
       }
       c += mine;
       kt += n;
@@ -877,7 +906,7 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
         const int x = c + i;            // tile of this pipeline
         const int j = first + i * stride;  // tile of the piece
         const int kv0 = (tile0 + j) * kBlockTokens;
-        ok = wait_all(s_full(g), x);
+        ok = wait_all(s_full(g, x & 1), x >> 1);
         if (!ok) break;
         tc_fence_after();
         // S is there, so the Q rows were converted: their scale comes back out
@@ -900,16 +929,12 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
                              (uint32_t)(valid + (q >> 4)) * 128 + (uint32_t)(q & 7) * 16);
           fence_async_shared();  // the P V MMA reads V through the async proxy
         }
-        if (!live) {
-          tc_fence_before();
-          mbar_arrive(s_free(g));
-        } else {
+        if (live) {
+          const uint32_t ts = trow + kColS + 64u * (uint32_t)(x & 1);
           float s[64];
-          tmem_ld32(trow + kColS, *reinterpret_cast<float(*)[32]>(&s[0]));
-          tmem_ld32(trow + kColS + 32, *reinterpret_cast<float(*)[32]>(&s[32]));
+          tmem_ld32(ts, *reinterpret_cast<float(*)[32]>(&s[0]));
+          tmem_ld32(ts + 32, *reinterpret_cast<float(*)[32]>(&s[32]));
           tmem_wait_ld();
-          tc_fence_before();
-          mbar_arrive(s_free(g));
           if (kv0 + 64 > lim) {
 #pragma unroll
             for (int q = 0; q < 64; ++q)
@@ -948,9 +973,6 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
           unpack2(fadd2(fadd2(acc2[0], acc2[1]), fadd2(acc2[2], acc2[3])), r0, r1);
           l = l * alpha + (r0 + r1);
           m = m_use;
-          // The P buffer of tile x was last read by the P V of tile x - 2, which
-          // the MMA warp issued before S(x); the commit behind s_full(x) fires
-          // only when every earlier MMA of that thread has completed.
           if (i > 0 && __any_sync(0xffffffffu, need)) {
             // O is stable once the P V of tile x - 1 is done
             ok = wait_all(pv_done(g, (x - 1) & 1), (x - 1) >> 1);
@@ -966,7 +988,7 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
               tmem_st32(trow + kColO + q * 32, o);
             }
           }
-          tmem_st32(trow + kColP + 32u * (uint32_t)(x & 1), pk);
+          tmem_st32(ts, pk);  // over S of this tile, which is in registers
           tmem_wait_st();
         }
         tc_fence_before();

@@ -57,7 +57,7 @@ class Model:
         self.word = [None] * (stages8 if fp8 else stages)   # tile issued into a slot
         self.dep = [{}, {}]              # warp -> (piece, its tiles) in a buffer
         self.joined = []                 # (piece, tiles) written out
-        self.s_full, self.s_free = two("s_full", 1), two("s_free", 1)
+        self.s_full = [two(f"s_full{g}.", 1) for g in range(2)]
         self.p_full = [two(f"p_full{g}.", 1) for g in range(2)]
         self.pv_done = [two(f"pv_done{g}.", 1) for g in range(2)]
         self.tma, self.pipe, self.tick = [], [[], []], 0
@@ -67,7 +67,7 @@ class Model:
         self.q_left = [set(), set()]     # pipelines that have not let go of a slot's fill
         self.ring, self.ring8 = [None] * stages, [None] * stages8
         self.ring_reads = {}             # tile -> readers outstanding
-        self.s_buf, self.s_read = [None, None], [True, True]
+        self.s_buf, self.s_read = [[None, None], [None, None]], [[True, True], [True, True]]
         self.p_buf = [[None, None], [None, None]]
         self.pv_reads = [[None, None], [None, None]]
         self.o = [[], []]                # tiles accumulated in O of a pipeline
@@ -236,21 +236,19 @@ class Model:
 
             def issue_s(q):
                 k = kt + mine[q]
-                yield from self.until(self.kv_full[k % self.S], k // self.S)
-                if c + q >= 1:
-                    yield from self.until(self.s_free[g], c + q - 1)
                 self.q_readers[my].add((g, q))
 
-                def start(k=k, i=i, my=my):
+                def start(k=k, i=i, my=my, b=(c + q) & 1):
                     assert self.q[my] == (i, True), "S on a Q slot that is not ready"
-                    assert self.ring[k % self.S] == k and self.s_read[g]
+                    assert self.ring[k % self.S] == k and self.s_read[g][b]
+                    assert self.pv_reads[g][b] is None, "S over a P in use"
 
-                def end(k=k, q=q, i=i, my=my):
+                def end(k=k, q=q, i=i, my=my, b=(c + q) & 1):
                     self.ring_reads[k] -= 1
                     self.q_readers[my].discard((g, q))
-                    self.s_buf[g], self.s_read[g] = (i, q), False
+                    self.s_buf[g][b], self.s_read[g][b] = (i, q), False
                 self.op(g, start, end)
-                self.commit(g, self.s_full[g])
+                self.commit(g, self.s_full[g][(c + q) & 1])
                 if q + 1 == len(mine):
                     def let_go(my=my):
                         self.q_left[my].discard(g)
@@ -259,7 +257,6 @@ class Model:
 
             def issue_pv(q):
                 k, x = kt + mine[q], c + q
-                yield from self.until(self.p_full[g][x & 1], x >> 1)
                 self.pv_reads[g][x & 1] = x
                 self.pv_open[g] += 1
 
@@ -278,27 +275,30 @@ class Model:
                 self.commit(g, self.pv_done[g][x & 1])
                 self.commit(g, self.kv_empty[k % self.S])
 
-            def skip(j):
-                k = kt + j
-                yield from self.until(self.kv_full[k % self.S], k // self.S)
-                self.kv_empty[k % self.S].arrive()
-
             for s in slots:
                 yield from self.until((self.q_ready if self.fp8 else self.q_full)[s], uses[s])
                 if s != my or not mine:
                     self.q_left[s].discard(g)
                     self.q_empty[s].arrive()
-            if not two and g == 1:
-                yield from skip(0)
-            if mine:
-                yield from issue_s(0)
-            for q in range(len(mine)):
-                yield
-                if not two and mine[q] + 1 < n:
-                    yield from skip(mine[q] + 1)
-                if q + 1 < len(mine):
-                    yield from issue_s(q + 1)
-                yield from issue_pv(q)
+            s = v = j = 0
+            while v < len(mine) or j < n:
+                did, own = False, two or j % 2 == g
+                if j < n and (not own or s < v + 2):
+                    k = kt + j
+                    if self.kv_full[k % self.S].ready(k // self.S):
+                        if own:
+                            issue_s(s)
+                            s += 1
+                        else:
+                            self.kv_empty[k % self.S].arrive()
+                        j, did = j + 1, True
+                        yield
+                if v < s and self.p_full[g][(c + v) & 1].ready((c + v) >> 1):
+                    issue_pv(v)
+                    v, did = v + 1, True
+                    yield
+                if not did:
+                    yield WAIT
             c += len(mine)
         yield from self.join_warps(g)
 
@@ -316,16 +316,15 @@ class Model:
                 self.q_ready[g].arrive()
             for q in range(len(mine)):
                 x = c + q
-                yield from self.until(self.s_full[g], x)
+                yield from self.until(self.s_full[g][x & 1], x >> 1)
                 if self.fp8 and q == 0:
                     assert self.scale[my][uses[my] & 1] == i, "scale of another fill"
                 if g == 1 and q == 0 and joins:
                     yield from self.until(self.x_free, joins - 1)
-                assert self.s_buf[g] == (i, q) and not self.s_read[g]
+                assert self.s_buf[g][x & 1] == (i, q) and not self.s_read[g][x & 1]
                 yield
-                assert self.s_buf[g] == (i, q)
-                self.s_read[g] = True
-                self.s_free[g].arrive()
+                assert self.s_buf[g][x & 1] == (i, q)
+                self.s_read[g][x & 1] = True
                 for _ in range(self.rng.randint(0, 4)):
                     yield
                 if q > 0 and self.rng.random() < 0.4:  # rescale O
