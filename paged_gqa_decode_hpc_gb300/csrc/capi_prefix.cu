@@ -163,7 +163,7 @@ hpc_status hpc_decode_prefix_attn(const hpc_tensor* q, const hpc_tensor* k_cache
 
     PrefixPlanParams pp;
     std::memset(&pp, 0, sizeof pp);
-    pp.costs = fp8 ? kPrefixCostsFp8 : kPrefixCostsBf16;
+    pp.costs = kPrefixCosts[fp8][T > 1];
     pp.seq_lens = (const int32_t*)seq_lens->data;
     pp.cu_groups = cu_groups ? (const int32_t*)cu_groups->data : nullptr;
     pp.prefix_lens = (const int32_t*)prefix_lens->data;

@@ -51,12 +51,16 @@ struct PrefixWorkspace {
 };
 
 // What a KV head of a work row costs its CTA, in units of 10 ns: a fixed part
-// (Q and the first tile's way through the pipeline, the epilogue) and each tile.
+// (Q and the first tile's way through the pipeline, the epilogue) and each tile;
+// measured per piece on 64 x (32768 shared + 128 .. 2048 own), 32 x (4096 + 64 ..
+// 1024) and 16 x 4 new tokens x (8192 + 100 .. 600) positions with 8 KV heads.
+// Own pieces of one new token run as warp pieces and differ from those of several.
 struct PrefixCosts {
   int32_t shared_fixed, two_tile, one_tile, own_fixed, own_tile;
 };
-constexpr PrefixCosts kPrefixCostsBf16 = {200, 88, 50, 100, 62};
-constexpr PrefixCosts kPrefixCostsFp8 = {300, 105, 80, 250, 80};
+constexpr PrefixCosts kPrefixCosts[2][2] = {  // [e4m3][several new tokens]
+    {{600, 84, 70, 10, 56}, {600, 84, 70, 200, 70}},
+    {{500, 90, 70, 20, 48}, {500, 90, 70, 250, 80}}};
 
 struct PrefixPlanParams {
   PrefixCosts costs;

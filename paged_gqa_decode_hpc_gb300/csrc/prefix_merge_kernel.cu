@@ -28,7 +28,8 @@ namespace hpc {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 4;  // states in flight
+constexpr int kBatch = 4;   // states in flight
+constexpr int kListed = 64;  // states listed before the wait
 constexpr float kLn2 = 0.6931471805599453f;
 
 __global__ void __launch_bounds__(kThreads) prefix_merge_kernel(const PrefixMergeParams p) {
@@ -40,10 +41,11 @@ __global__ void __launch_bounds__(kThreads) prefix_merge_kernel(const PrefixMerg
   const int2* bounds = reinterpret_cast<const int2*>(p.words + p.bound_off);
   const int4* recs = reinterpret_cast<const int4*>(p.words + p.rec_off);
 
-  // the two work rows: block of the first piece's state, parts [lo, hi) that
-  // may hold more, the pair's number in a part's blocks
+  // The list of states: for the pair's shared and own work row the first piece's,
+  // then those of the parts that continue it.
+  __shared__ int64_t s_blk[kListed];
   int64_t home[2] = {-1, -1};
-  int lo[2] = {0, 0}, hi[2] = {0, 0}, local[2] = {0, t};
+  int lo[2] = {0, 0}, count[2] = {0, 0}, local[2] = {0, t};
   if (rows_all > 0) {
     const int2 s = reinterpret_cast<const int2*>(p.words + p.seq_off)[b];
     const int k = s.x >= 0 ? pair - s.y : 0;
@@ -55,6 +57,7 @@ __global__ void __launch_bounds__(kThreads) prefix_merge_kernel(const PrefixMerg
     if (n[0] > 0) home[0] = (int64_t)pair * H + h;
     if (n[1] > 0) home[1] = p.ws.own0 + (int64_t)pair * H + h;
     // parts whose boundary lies inside a row's units (h n, h n + n)
+    int hi[2] = {0, 0};
     for (int q0 = 0; q0 < parts; q0 += kThreads) {
       const int q = q0 + threadIdx.x;
       int2 bd = make_int2(INT32_MAX, 0);
@@ -67,61 +70,60 @@ __global__ void __launch_bounds__(kThreads) prefix_merge_kernel(const PrefixMerg
         hi[w] += __syncthreads_count(bd.x < v[w] || (bd.x == v[w] && bd.y < first + n[w]));
       }
     }
+    for (int w = 0; w < 2; ++w) count[w] = n[w] > 0 ? 1 + hi[w] - lo[w] : 0;
   }
+  const int total = count[0] + count[1];
+  // state s's block, or -1 (a part without units leaves none)
+  auto block_of = [&](int s) -> int64_t {
+    const int w = s < count[0] ? 0 : 1, i = w == 0 ? s : s - count[0];
+    if (i == 0) return home[w];
+    const int q = lo[w] + i - 1;
+    const int2 b0 = bounds[q], b1 = bounds[q + 1];
+    if (b0.x == b1.x && b0.y == b1.y) return -1;
+    return p.ws.cont0 + (int64_t)q * kPrefixRowPairs + local[w];
+  };
+  for (int s = threadIdx.x; s < total && s < kListed; s += kThreads) s_blk[s] = block_of(s);
+  __syncthreads();
   griddep_wait();  // the states
   griddep_launch_dependents();
 
   float M = -INFINITY, L = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = 0; s0 < total; s0 += kBatch) {
+    float m[kBatch], l[kBatch];
+    float4 o[kBatch];
 #pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    if (home[w] < 0) continue;
-    // state 0 is home's, state 1 + i part lo + i's
-    const int count = 1 + hi[w] - lo[w];
-    for (int s0 = 0; s0 < count; s0 += kBatch) {
-      float m[kBatch], l[kBatch];
-      float4 o[kBatch];
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int s = s0 + i;
-        m[i] = -INFINITY;
-        l[i] = 0.f;
-        o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        int64_t blk = -1;
-        if (s == 0) {
-          blk = home[w];
-        } else if (s < count) {
-          const int q = lo[w] + s - 1;
-          const int2 b0 = bounds[q], b1 = bounds[q + 1];
-          if (b0.x != b1.x || b0.y != b1.y)  // a part without units leaves none
-            blk = p.ws.cont0 + (int64_t)q * kPrefixRowPairs + local[w];
-        }
-        if (blk >= 0) {
-          m[i] = p.ws.m[blk * 8 + row];
-          l[i] = p.ws.l[blk * 8 + row];
-          o[i] = p.ws.o[blk * 256 + col * 8 + row];
-        }
+    for (int i = 0; i < kBatch; ++i) {
+      const int s = s0 + i;
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+      o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      const int64_t blk = s >= total ? -1 : s < kListed ? s_blk[s] : block_of(s);
+      if (blk >= 0) {
+        m[i] = p.ws.m[blk * 8 + row];
+        l[i] = p.ws.l[blk * 8 + row];
+        o[i] = p.ws.o[blk * 256 + col * 8 + row];
       }
-      float Mn = M;
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) Mn = fmaxf(Mn, m[i]);
-      if (Mn == -INFINITY) continue;  // no visible key for this row so far
-      const float a = ptx_ex2(M - Mn);
-      L *= a;
-      acc.x *= a; acc.y *= a; acc.z *= a; acc.w *= a;
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        // a state without a visible key (m = -inf) may hold anything in o
-        const float f = ptx_ex2(m[i] - Mn);
-        if (m[i] == -INFINITY) continue;
-        L += l[i] * f;
-        acc.x += o[i].x * f;
-        acc.y += o[i].y * f;
-        acc.z += o[i].z * f;
-        acc.w += o[i].w * f;
-      }
-      M = Mn;
     }
+    float Mn = M;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) Mn = fmaxf(Mn, m[i]);
+    if (Mn == -INFINITY) continue;  // no visible key for this row so far
+    const float a = ptx_ex2(M - Mn);
+    L *= a;
+    acc.x *= a; acc.y *= a; acc.z *= a; acc.w *= a;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      // a state without a visible key (m = -inf) may hold anything in o
+      const float f = ptx_ex2(m[i] - Mn);
+      if (m[i] == -INFINITY) continue;
+      L += l[i] * f;
+      acc.x += o[i].x * f;
+      acc.y += o[i].y * f;
+      acc.z += o[i].z * f;
+      acc.w += o[i].w * f;
+    }
+    M = Mn;
   }
   const float inv = L == 0.f ? 0.f : p.v_scale / L;
   __nv_bfloat16* o = p.out + (int64_t)b * p.o_sb + (int64_t)t * p.o_st +

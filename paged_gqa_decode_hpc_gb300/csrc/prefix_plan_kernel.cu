@@ -8,11 +8,15 @@
 // So no shared tile needs a mask, and what lies behind is the sequences' own:
 // sequence b has ceil(L_b / 64) - s_g tiles of its own.
 // Work rows: for every group with s_g > 0, its pairs in sets of 32; then one
-// row per sequence. A unit is a (KV head, tile) of a work row. A KV head of a
-// row of n tiles costs f + w n, f and w by the row's kind (measured times, see
-// PrefixCosts), and part p of P covers the cost interval [p C / P, (p + 1) C / P)
-// of all heads of all rows in order; a boundary inside a unit leaves it to the
-// part before, one inside f falls before the head's first unit.
+// row per sequence. A unit is a (KV head, tile) of a work row. Costs are measured
+// times (PrefixCosts). A KV head of a row of n tiles costs f + w n. Shared heads
+// are long and cut into several pieces, each of which pays the fixed part f (its
+// Q, its epilogue) anew, so a tile there costs w X / (X - f), X being the cost of
+// a part: P X = S X / (X - f) + O, with S the shared tiles' plain cost and O all
+// the rest, is solved by a few steps. Part p of P covers the cost interval
+// [p C / P, (p + 1) C / P) of all heads of all rows in order; a boundary inside a
+// unit leaves it to the part before, one inside f falls before the head's first
+// unit. Parts cost at least kMinPart, or there are fewer of them.
 //
 // One CTA; what bounds it is latency: one trip to memory for all the inputs
 // (loaded before anything else), two block-wide scans, binary searches in
@@ -27,6 +31,7 @@ namespace hpc {
 namespace {
 
 constexpr int kMaxThreads = 1024;
+constexpr int kMinPart = 100;  // 1 us
 
 __device__ __forceinline__ int64_t block_scan(int64_t a, int64_t* warp_tot, int64_t* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -65,10 +70,12 @@ __device__ __forceinline__ int find(const T* a, int n, T x) {
   return lo;
 }
 
-// Costs of a KV head of a work row: fixed, and per tile.
-__device__ __forceinline__ int2 costs(const PrefixCosts& c, bool own, int pairs) {
+// Costs of a KV head of a work row: fixed, and per tile. `stretch`: what a
+// piece's fixed part adds to a shared tile, in 64ths.
+__device__ __forceinline__ int2 costs(const PrefixCosts& c, bool own, int pairs, int stretch) {
   if (own) return make_int2(c.own_fixed, c.own_tile);
-  return make_int2(c.shared_fixed, pairs > kPrefixTilePairs ? c.two_tile : c.one_tile);
+  return make_int2(c.shared_fixed,
+                   (pairs > kPrefixTilePairs ? c.two_tile : c.one_tile) * stretch / 64);
 }
 
 // a * b / c of non-negative numbers whose result fits 32 bits, c > 0.
@@ -80,9 +87,11 @@ __device__ __forceinline__ int64_t muldiv(int64_t a, int b, int c) {
 __global__ void __launch_bounds__(kMaxThreads) prefix_plan_kernel(const PrefixPlanParams p) {
   extern __shared__ int64_t dyn[];
   __shared__ int64_t warp_tot[32];
+  __shared__ float2 s_sum[32];
   __shared__ int s_bad, s_err;
   const int tid = threadIdx.x, nt = blockDim.x;
-  const int B = p.num_seqs, G = p.num_groups, T = p.q_len, H = p.num_kv_heads, P = p.num_parts;
+  const int B = p.num_seqs, G = p.num_groups, T = p.q_len, H = p.num_kv_heads;
+  int P = p.num_parts;
   // [G + 1] each: group starts, least visible length, non-empty sequences, first of them,
   // shared tiles, first work row
   int32_t* cu = reinterpret_cast<int32_t*>(dyn);
@@ -171,13 +180,50 @@ __global__ void __launch_bounds__(kMaxThreads) prefix_plan_kernel(const PrefixPl
     }
   };
   int4* recs = reinterpret_cast<int4*>(p.words + p.rec_off);
+  // this thread's first row, kept
+  int4 mine_a = make_int4(0, 0, 0, 0), mine_b = mine_a;
+  if (tid < V) record(tid, mine_a, mine_b);
+  // the plain costs of the shared tiles and of all else, and the stretch
+  int stretch = 64;
+  if (shared > 0) {
+    float sum_s = 0.f, sum_o = 0.f;  // estimates: fp32 will do
+    for (int v = tid; v < V; v += nt) {
+      int4 a = mine_a, b = mine_b;
+      if (v != tid) record(v, a, b);
+      if (b.x == 0) continue;
+      const int2 fw = costs(p.costs, b.y != 0, a.y, 64);
+      sum_o += (float)H * (float)fw.x;
+      if (b.y) sum_o += (float)H * (float)fw.y * (float)b.x;
+      else sum_s += (float)H * (float)fw.y * (float)b.x;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      sum_s += __shfl_xor_sync(0xffffffffu, sum_s, o);
+      sum_o += __shfl_xor_sync(0xffffffffu, sum_o, o);
+    }
+    if ((tid & 31) == 0) s_sum[tid >> 5] = make_float2(sum_s, sum_o);
+    __syncthreads();
+    sum_s = sum_o = 0.f;
+    for (int w = 0; w < nt / 32; ++w) {  // the same order in every thread
+      sum_s += s_sum[w].x;
+      sum_o += s_sum[w].y;
+    }
+    const float F = (float)p.costs.shared_fixed;
+    float X = (sum_s + sum_o) / (float)P + F, ratio = 1.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      ratio = fminf(X / fmaxf(X - F, 1.f), 4.f);
+      X = (sum_s * ratio + sum_o) / (float)P;
+    }
+    stretch = (int)(64.f * ratio);
+  }
   carry = 0;
   for (int base = 0; base < V; base += nt) {
     const int v = base + tid;
     int64_t cost = 0;
     if (v < V) {
-      int4 a, b;
-      record(v, a, b);
+      int4 a = mine_a, b = mine_b;
+      if (v != tid) record(v, a, b);
       recs[2 * v] = a;
       recs[2 * v + 1] = b;
       if (v >= shared) {  // the sequence's first shared work row, or -1, and its first pair
@@ -185,7 +231,7 @@ __global__ void __launch_bounds__(kMaxThreads) prefix_plan_kernel(const PrefixPl
         reinterpret_cast<int2*>(p.words + p.seq_off)[a.z] =
             make_int2(a.w > 0 ? grow[g] : -1, cu[g] * T);
       }
-      const int2 fw = costs(p.costs, b.y != 0, a.y);
+      const int2 fw = costs(p.costs, b.y != 0, a.y, stretch);
       if (b.x > 0) cost = H * (fw.x + (int64_t)fw.y * b.x);
       // the units of a row are counted in 32 bits
       if ((int64_t)H * b.x > INT32_MAX) {
@@ -202,15 +248,16 @@ __global__ void __launch_bounds__(kMaxThreads) prefix_plan_kernel(const PrefixPl
   if (tid == 0) cum[V] = C;
   __syncthreads();
   const bool none = C == 0 || s_bad == 2;
+  P = (int)min((int64_t)P, C / kMinPart + 1);
   // boundary q: row v, unit u, and the record of row v for the part behind it
-  for (int q = tid; q <= P; q += nt) {
+  for (int q = tid; q <= p.num_parts; q += nt) {
     int v = V, u = 0;
     int4 a = make_int4(0, 0, 0, 0), b = a;
     if (q < P && !none) {
       const int64_t c = muldiv(C, q, P);
       v = find(cum, V, c);
       record(v, a, b);
-      const int2 fw = costs(p.costs, b.y != 0, a.y);
+      const int2 fw = costs(p.costs, b.y != 0, a.y, stretch);
       const int64_t head = fw.x + (int64_t)fw.y * b.x, in = c - cum[v];
       const int h = in <= UINT32_MAX && head <= UINT32_MAX ? (int)((uint32_t)in / (uint32_t)head)
                                                            : (int)(in / head);
@@ -218,7 +265,7 @@ __global__ void __launch_bounds__(kMaxThreads) prefix_plan_kernel(const PrefixPl
       u = h * b.x + (rest > 0 ? (int)((uint32_t)(rest + fw.y - 1) / (uint32_t)fw.y) : 0);
     }
     reinterpret_cast<int2*>(p.words + p.bound_off)[q] = make_int2(v, u);
-    if (q < P) {
+    if (q < p.num_parts) {
       int4* first = reinterpret_cast<int4*>(p.words + p.first_off) + 2 * q;
       first[0] = a;
       first[1] = b;
