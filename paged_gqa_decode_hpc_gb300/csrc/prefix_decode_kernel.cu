@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
       float l0 = 0.f, l1 = 0.f, acc[8][4];
 #pragma unroll
       for (int dm = 0; dm < 8; ++dm) acc[dm][0] = acc[dm][1] = acc[dm][2] = acc[dm][3] = 0.f;
-#pragma unroll 1
+#pragma unroll 2
       for (int w = 0; w < 8; ++w) {
         const float m0 = ml[16 * w + h2], m1 = ml[16 * w + h2 + 1];
         if (m0 == -INFINITY && ml[16 * w + 8 + h2] == 0.f) continue;  // no tile in this piece

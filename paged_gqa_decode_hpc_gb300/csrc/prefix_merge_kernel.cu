@@ -28,11 +28,11 @@ namespace hpc {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 4;   // states in flight
+constexpr int kBatch = 6;   // states in flight
 constexpr int kListed = 64;  // states listed before the wait
 constexpr float kLn2 = 0.6931471805599453f;
 
-__global__ void __launch_bounds__(kThreads) prefix_merge_kernel(const PrefixMergeParams p) {
+__global__ void __launch_bounds__(kThreads, 4) prefix_merge_kernel(const PrefixMergeParams p) {
   const int H = p.num_kv_heads, T = p.q_len;
   const int64_t item = blockIdx.x;
   const int pair = (int)(item / H), h = (int)(item % H), b = pair / T, t = pair % T;

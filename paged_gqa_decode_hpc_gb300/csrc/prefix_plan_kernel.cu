@@ -31,8 +31,11 @@ namespace hpc {
 namespace {
 
 constexpr int kMaxThreads = 1024;
-constexpr int kMinPart = 100;  // 1 us
+constexpr int kMinPart = 100;    // 1 us
+constexpr int kKeptLens = 1024;  // lengths kept in shared memory
 
+// Inclusive block scan; the total too. One barrier, and one more before the
+// totals' cells are used again.
 __device__ __forceinline__ int64_t block_scan(int64_t a, int64_t* warp_tot, int64_t* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -42,20 +45,15 @@ __device__ __forceinline__ int64_t block_scan(int64_t a, int64_t* warp_tot, int6
   }
   if (lane == 31) warp_tot[warp] = a;
   __syncthreads();
-  if (warp == 0) {
-    int64_t t = lane < (int)(blockDim.x >> 5) ? warp_tot[lane] : 0;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t x = __shfl_up_sync(0xffffffffu, t, o);
-      if (lane >= o) t += x;
-    }
-    warp_tot[lane] = t;
+  int64_t before = 0, all = 0;
+  for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
+    const int64_t x = warp_tot[w];
+    if (w < warp) before += x;
+    all += x;
   }
+  *total = all;
   __syncthreads();
-  if (warp > 0) a += warp_tot[warp - 1];
-  *total = warp_tot[31];
-  __syncthreads();
-  return a;
+  return a + before;
 }
 
 // Last i in [0, n) with a[i] <= x (a non-decreasing, a[0] <= x).
@@ -88,6 +86,7 @@ __global__ void __launch_bounds__(kMaxThreads) prefix_plan_kernel(const PrefixPl
   extern __shared__ int64_t dyn[];
   __shared__ int64_t warp_tot[32];
   __shared__ float2 s_sum[32];
+  __shared__ int s_len[kKeptLens];
   __shared__ int s_bad, s_err;
   const int tid = threadIdx.x, nt = blockDim.x;
   const int B = p.num_seqs, G = p.num_groups, T = p.q_len, H = p.num_kv_heads;
@@ -126,9 +125,10 @@ __global__ void __launch_bounds__(kMaxThreads) prefix_plan_kernel(const PrefixPl
     if (tid == 0) s_err = HPC_DEVCHK_BAD_LENGTH;
     __syncthreads();
   }
-  auto length = [&](int b) { return b == tid ? len0 : p.seq_lens[b]; };
+  auto length = [&](int b) { return b < kKeptLens ? s_len[b] : p.seq_lens[b]; };
   for (int b = tid; b < B; b += nt) {
-    const int L = length(b);
+    const int L = b == tid ? len0 : p.seq_lens[b];
+    if (b < kKeptLens) s_len[b] = L;
     if (L < 0) s_err = HPC_DEVCHK_BAD_LENGTH;
     if (L > 0) {
       const int g = find(cu, G, b);
@@ -138,30 +138,35 @@ __global__ void __launch_bounds__(kMaxThreads) prefix_plan_kernel(const PrefixPl
     }
   }
   __syncthreads();
-  int64_t carry = 0;
-  for (int base = 0; base < G; base += nt) {
-    const int g = base + tid;
-    int64_t rows = 0;
-    if (g < G) {
-      const int want = g == tid ? want0 : p.prefix_lens[g];
-      if (want < 0) s_err = HPC_DEVCHK_BAD_LENGTH;
-      int s = 0;
-      if (!s_bad && gcnt[g] >= 2) {
-        s = min(want, gmin[g]);
-        s = min(s > 0 ? s / kBlockTokens : 0, p.max_blocks);
+  if (tid < 32) {  // the groups' shared tiles and first work rows, by one warp
+    int carry = 0;
+    for (int base = 0; base < G; base += 32) {
+      const int g = base + tid;
+      int s = 0, rows = 0;
+      if (g < G) {
+        const int want = g == tid ? want0 : p.prefix_lens[g];
+        if (want < 0) s_err = HPC_DEVCHK_BAD_LENGTH;
+        if (!s_bad && gcnt[g] >= 2) {
+          s = min(want, gmin[g]);
+          s = min(s > 0 ? s / kBlockTokens : 0, p.max_blocks);
+        }
+        gtiles[g] = s;
+        if (s > 0) rows = ((cu[g + 1] - cu[g]) * T + kPrefixRowPairs - 1) / kPrefixRowPairs;
       }
-      gtiles[g] = s;
-      if (s > 0) rows = ((cu[g + 1] - cu[g]) * T + kPrefixRowPairs - 1) / kPrefixRowPairs;
+      int incl = rows;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (tid >= o) incl += x;
+      }
+      if (g < G) grow[g] = carry + incl - rows;
+      carry += __shfl_sync(0xffffffffu, incl, 31);
     }
-    int64_t total;
-    const int64_t incl = block_scan(rows, warp_tot, &total);
-    if (g < G) grow[g] = (int32_t)(carry + incl - rows);
-    carry += total;
+    if (tid == 0) grow[G] = carry;
   }
-  const int shared = (int)carry;
-  const int V = shared + B;
-  if (tid == 0) grow[G] = shared;
   __syncthreads();
+  const int shared = grow[G];
+  const int V = shared + B;
   // a shared row's group: groups without rows repeat their neighbour's start,
   // the last one with grow <= v has rows
   auto shared_pairs = [&](int v, int g) {
@@ -209,15 +214,16 @@ __global__ void __launch_bounds__(kMaxThreads) prefix_plan_kernel(const PrefixPl
       sum_o += s_sum[w].y;
     }
     const float F = (float)p.costs.shared_fixed;
-    float X = (sum_s + sum_o) / (float)P + F, ratio = 1.f;
+    const float per_part = 1.f / (float)P;
+    float X = (sum_s + sum_o) * per_part + F, ratio = 1.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      ratio = fminf(X / fmaxf(X - F, 1.f), 4.f);
-      X = (sum_s * ratio + sum_o) / (float)P;
+    for (int i = 0; i < 3; ++i) {
+      ratio = fminf(__fdividef(X, fmaxf(X - F, 1.f)), 4.f);
+      X = (sum_s * ratio + sum_o) * per_part;
     }
     stretch = (int)(64.f * ratio);
   }
-  carry = 0;
+  int64_t carry = 0;
   for (int base = 0; base < V; base += nt) {
     const int v = base + tid;
     int64_t cost = 0;
