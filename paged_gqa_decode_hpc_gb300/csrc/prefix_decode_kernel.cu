@@ -499,31 +499,49 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
         if (!ok) break;
         const int valid = len - (tile0 + j) * kBlockTokens;  // rows of this tile that exist
         const uint32_t e8 = sKV8 + s8 * kStageBytes8, kb = sKV + sb * kStageBytes;
-#pragma unroll 2
-        for (int it = 0; it < 1024 / kNT; ++it) {
-          const int mat = it >> 2;
-          const int t = (it & 3) * 16 + (ct >> 4) * 2 + cr;
-          uint32_t xs[4];
-          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(xs[0]), "=r"(xs[1]), "=r"(xs[2]), "=r"(xs[3])
-                       : "r"(e8 + mat * kKVTileBytes8 + t * 128 + ((uint32_t)(c ^ (t & 7)) << 4)));
-          uint32_t w[8];
-          const bool gone = mat == 1 && t >= valid;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            w[2 * q] = gone ? 0u : e4m3x2_to_f16x2(xs[q]);
-            w[2 * q + 1] = gone ? 0u : e4m3x2_to_f16x2(xs[q] >> 16);
+        for (int it0 = 0; it0 < 1024 / kNT; it0 += 4) {  // four loads in flight per thread
+          uint32_t xs[4][4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int t = u * 16 + (ct >> 4) * 2 + cr;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(xs[u][0]), "=r"(xs[u][1]), "=r"(xs[u][2]), "=r"(xs[u][3])
+                         : "r"(e8 + (it0 >> 2) * kKVTileBytes8 + t * 128 +
+                               ((uint32_t)(c ^ (t & 7)) << 4)));
           }
-          const int cc = (c & 3) * 2;
-          const uint32_t row = kb + mat * kKVTileBytes + (c >> 2) * (kKVTileBytes / 2) + t * 128;
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                           row + ((uint32_t)(cc ^ (t & 7)) << 4)),
-                       "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                       : "memory");
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                           row + ((uint32_t)((cc + 1) ^ (t & 7)) << 4)),
-                       "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                       : "memory");
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int t = u * 16 + (ct >> 4) * 2 + cr;
+            uint32_t w[8];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              w[2 * q] = e4m3x2_to_f16x2(xs[u][q]);
+              w[2 * q + 1] = e4m3x2_to_f16x2(xs[u][q] >> 16);
+            }
+            const int cc = (c & 3) * 2;
+            const uint32_t row =
+                kb + (it0 >> 2) * kKVTileBytes + (c >> 2) * (kKVTileBytes / 2) + t * 128;
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             row + ((uint32_t)(cc ^ (t & 7)) << 4)),
+                         "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                         : "memory");
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             row + ((uint32_t)((cc + 1) ^ (t & 7)) << 4)),
+                         "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                         : "memory");
+          }
+        }
+        if (valid < kBlockTokens) {  // V rows behind the sequence's end: this thread's chunks
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int t = u * 16 + (ct >> 4) * 2 + cr, cc = (c & 3) * 2;
+            const uint32_t row = kb + kKVTileBytes + (c >> 2) * (kKVTileBytes / 2) + t * 128;
+            if (t >= valid) {
+              st_shared_zero16(row + ((uint32_t)(cc ^ (t & 7)) << 4));
+              st_shared_zero16(row + ((uint32_t)((cc + 1) ^ (t & 7)) << 4));
+            }
+          }
         }
         fence_async_shared();  // the MMAs read the f16 tile through the async proxy
         mbar_arrive(kv8_empty(s8));
