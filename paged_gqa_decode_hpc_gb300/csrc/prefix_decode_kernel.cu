@@ -84,26 +84,28 @@ struct Lay {
   static constexpr int kProducerWarp = 8 + kConvWarps, kMmaWarp0 = kProducerWarp + 1;
   // FP8: whole warpgroups (one warp idle), so that registers can move to the softmax ones
   static constexpr int kThreads = FP8 ? 512 : 32 * (kMmaWarp0 + 2);
-  static constexpr int kStages = FP8 ? 3 : 5;   // 16-bit K + V ring
-  static constexpr int kStages8 = FP8 ? 4 : 0;  // e4m3 K + V ring
-  static constexpr int kTmaStages = FP8 ? kStages8 : kStages;  // the ring that TMA fills
-  static constexpr uint32_t kTmaStageBytes = FP8 ? kStageBytes8 : kStageBytes;
+  static constexpr int kStages = FP8 ? 4 : 5;   // 16-bit K + V ring
+  static constexpr int kStages8 = FP8 ? 2 : 0;  // e4m3 K + V ring
+  // warp pieces: the 16-bit ring, or, all as e4m3 slots, the space of both rings
+  static constexpr int kWStages = FP8 ? 2 * kStages + kStages8 : kStages;
+  static constexpr uint32_t kWStageBytes = FP8 ? kStageBytes8 : kStageBytes;
   static constexpr uint32_t kOffQ = 0;
   static constexpr uint32_t kOffKV = 2 * kQSlotBytes;
   static constexpr uint32_t kOffKV8 = kOffKV + kStages * kStageBytes;
-  static constexpr uint32_t kOffTma = FP8 ? kOffKV8 : kOffKV;
   static constexpr uint32_t kOffBar = kOffKV8 + kStages8 * kStageBytes8;
   // q_full[2], q_empty[2], q_ready[2], kv_full[S], kv_empty[S], kv8_full[S8],
   // kv8_empty[S8], x_full, x_free, dep_full[2], dep_free[2], q_done, per pipeline:
-  // s_full[2], p_full[2], pv_done[2], drain
-  static constexpr int kNumBars = 6 + 2 * kStages + 2 * kStages8 + 7 + 14;
+  // s_full[2], p_full[2], pv_done[2], drain; FP8: w_full[W], w_empty[W]
+  static constexpr int kNumBars =
+      6 + 2 * kStages + 2 * kStages8 + 7 + 14 + (FP8 ? 2 * kWStages : 0);
   // int8 [2 slots][2 fills][128]: a warpgroup that lags may still read the scales
   // of a slot's fill while the next one is converted, never the one after that
   static constexpr uint32_t kOffScale = kOffBar + 8 * kNumBars;
   static constexpr uint32_t kOffX = kOffScale + (FP8 ? 4 * kRows : 0);  // float [2][128]
-  static constexpr uint32_t kOffWord = kOffX + 2 * kRows * 4;           // tile in each TMA slot
-  static constexpr uint32_t kOffMisc = kOffWord + 4 * kTmaStages;
-  static constexpr uint32_t kSmemBytes = kOffMisc + 16 + 1024;  // + slack to align to 1024
+  static constexpr uint32_t kOffWord = kOffX + 2 * kRows * 4;  // warp pieces: tile in each slot
+  static constexpr uint32_t kOffMisc = (kOffWord + 4 * kWStages + 15) / 16 * 16;
+  // + slack to align to 1024 from the 16 that dynamic shared memory has
+  static constexpr uint32_t kSmemBytes = kOffMisc + 16 + 1008;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
 // FP8: of the launch's 512 x 128 registers, the two softmax warpgroups take 176
@@ -299,6 +301,8 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
   auto p_full = [&](int g, int i) { return gbar(g, 2 + i); };
   auto pv_done = [&](int g, int i) { return gbar(g, 4 + i); };
   auto drain = [&](int g) { return gbar(g, 6); };
+  auto w_full = [&](int s) { return FP8 ? gbar(2, s) : kv_full(s); };  // warp pieces
+  auto w_empty = [&](int s) { return FP8 ? gbar(2, Lt::kWStages + s) : kv_empty(s); };
   volatile int8_t* s_exp = reinterpret_cast<volatile int8_t*>(smem + Lt::kOffScale);  // Q scales
   volatile float* s_x = reinterpret_cast<volatile float*>(smem + Lt::kOffX);  // m, l of pipeline 1
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + Lt::kOffMisc);
@@ -337,8 +341,13 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
         mbar_init(dep_free(i), 1);
       }
       mbar_init(q_done, 2);  // one commit per MMA warp
-      for (int s = 0; s < Lt::kTmaStages; ++s)
+      for (int s = 0; s < Lt::kWStages; ++s) {
         st_release_word(base + Lt::kOffWord + 4 * s, 0xFFFFFFFFu);
+        if (FP8) {
+          mbar_init(w_full(s), 1);
+          mbar_init(w_empty(s), 1);
+        }
+      }
       for (int g = 0; g < 2; ++g) {
         for (int i = 0; i < 2; ++i) {
           mbar_init(s_full(g, i), 1);
@@ -374,11 +383,12 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
   int uses[2] = {0, 0};  // fills of each Q slot before this piece
   int ones = 0;          // one-row-tile pieces before this one (their Q slots alternate)
   int kt = 0;            // K / V tiles of the ring before this piece
+  int kw = 0;            // FP8: the same, of the warp pieces' ring
 
   if (warp == Lt::kProducerWarp) {
     // ------------------------------------------------------------ producer
     if (FP8) regs_dec();
-    int issued = 0;                               // K / V tiles issued, in order
+    int issued = 0, issued_w = 0;                 // K / V tiles issued, in order
     int q_issued[2] = {0, 0};                     // fills issued per Q slot
     int stop = p.withhold_copies != 0 ? 1 : 0;    // failure-path test: nothing is issued
     while (!stop && walk.next(pc)) {
@@ -409,6 +419,12 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
       }
       if (!pc.two) ++ones;
       stop = __shfl_sync(0xffffffffu, stop, 0);
+      const bool to_warps = FP8 && own && warp_own;
+      if (to_warps && kw == 0) {
+        // the warp pieces' ring lies over the two others: every MMA on them is done
+        if (lane == 0 && !wait(q_done, 0)) stop = 1;
+        stop = __shfl_sync(0xffffffffu, stop, 0);
+      }
       const int32_t* btrow = p.block_table + (int64_t)table * p.bt_sb;
       for (int j0 = 0; j0 < n && !stop; j0 += 32) {
         int blk = -1;  // out of range: TMA fills zeros
@@ -426,12 +442,23 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
         for (int q = 0; q < cnt; ++q) {
           const int bk = __shfl_sync(0xffffffffu, blk, q);
           if (lane == 0) {
-            const int j = kt + j0 + q;
-            if (FP8) {
+            const int j = (to_warps ? kw : kt) + j0 + q;
+            if (to_warps) {
+              const int slot = j % Lt::kWStages, round = j / Lt::kWStages;
+              if (round == 0 || wait(w_empty(slot), round - 1)) {
+                st_release_word(base + Lt::kOffWord + 4 * slot, (uint32_t)j);
+                const uint32_t dk = sKV + slot * kStageBytes8;
+                mbar_expect_tx(w_full(slot), kStageBytes8);
+                tma_load_4d(dk, &tmk, w_full(slot), 0, c1, c2, bk);
+                tma_load_4d(dk + kKVTileBytes8, &tmv, w_full(slot), 0, c1, c2, bk);
+                issued_w = j + 1;
+              } else {
+                stop = 1;
+              }
+            } else if (FP8) {
               const int slot = j % S8n, round = j / S8n;
               if (round == 0 || wait(kv8_empty(slot), round - 1)) {
                 const uint32_t fb = kv8_full(slot);
-                st_release_word(base + Lt::kOffWord + 4 * slot, (uint32_t)j);
                 const uint32_t dk = sKV8 + slot * kStageBytes8, dv = dk + kKVTileBytes8;
                 mbar_expect_tx(fb, kStageBytes8);
                 tma_load_4d(dk, &tmk, fb, 0, c1, c2, bk);
@@ -461,7 +488,8 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
           if (stop) break;
         }
       }
-      kt += n;
+      if (to_warps) kw += n;
+      else kt += n;
     }
     named_bar_sync(1, Lt::kThreads);
     // drain: the last copy issued into each ring slot and each Q slot has landed
@@ -470,6 +498,10 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
       for (int s = 0; s < SR && s < issued; ++s) {
         const int rounds = (issued - s + SR - 1) / SR;
         wait_bar(FP8 ? kv8_full(s) : kv_full(s), (rounds - 1) & 1, s_abort, err, lim_ns, false);
+      }
+      for (int s = 0; s < Lt::kWStages && s < issued_w; ++s) {
+        const int rounds = (issued_w - s + Lt::kWStages - 1) / Lt::kWStages;
+        wait_bar(w_full(s), (rounds - 1) & 1, s_abort, err, lim_ns, false);
       }
       for (int i = 0; i < 2; ++i)
         if (q_issued[i] > 0)
@@ -766,7 +798,8 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
         for (int dm = 0; dm < 8; ++dm) acc[dm][0] = acc[dm][1] = acc[dm][2] = acc[dm][3] = 0.f;
-        const int j0 = (warp - kt) & 7;
+        const int k0 = FP8 ? kw : kt;  // the piece's first tile in its ring
+        const int j0 = (warp - k0) & 7;
         if (j0 < n) {
           uint32_t qf[8][2];
           const float sl2 =
@@ -774,13 +807,13 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
                                                    (int64_t)(kGroupRows * pc.h) * p.q_sh,
                                                p.q_sh, lane, qf);
           for (int j = j0; j < n; j += 8) {
-            const int k = kt + j, slot = k % Lt::kTmaStages;
+            const int k = k0 + j, slot = k % Lt::kWStages;
             ok = __all_sync(0xffffffffu, wait_word(base + Lt::kOffWord + 4 * slot, (uint32_t)k,
                                                    s_abort, err, lim_ns));
-            if (ok) ok = wait_all(FP8 ? kv8_full(slot) : kv_full(slot), k / Lt::kTmaStages);
+            if (ok) ok = wait_all(w_full(slot), k / Lt::kWStages);
             if (!ok) break;
-            const uint32_t kb = base + Lt::kOffTma + slot * Lt::kTmaStageBytes;
-            const uint32_t vb = kb + Lt::kTmaStageBytes / 2;
+            const uint32_t kb = sKV + slot * Lt::kWStageBytes;
+            const uint32_t vb = kb + Lt::kWStageBytes / 2;
             const int valid = walk.rb.z - (walk.ra.w + pc.tb + j) * kBlockTokens;
             if (valid < kBlockTokens) {
               // V rows behind the sequence's end (both column halves of a 16-bit tile)
@@ -794,10 +827,7 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
             compute_unit<FP8>(kb, vb, qf, valid, sl2, m, l, acc, lane);
             if (valid < kBlockTokens) fence_async_shared();  // before TMA writes there again
             __syncwarp();
-            if (lane == 0) {
-              if (FP8) mbar_arrive_n(kv8_empty(slot), 32 * Lt::kConvWarps);
-              else mbar_arrive_n(kv_empty(slot), 2);
-            }
+            if (lane == 0) mbar_arrive_n(w_empty(slot), FP8 ? 1 : 2);  // (both MMA warps' arrivals)
           }
           if (!ok) break;
         }
@@ -835,7 +865,8 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(dep_full(buf));
         ++warp_pieces;
-        kt += n;
+        if (FP8) kw += n;
+        else kt += n;
         continue;
       }
       const int slot0 = pc.two ? 0 : (ones & 1);

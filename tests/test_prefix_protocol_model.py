@@ -54,7 +54,12 @@ class Model:
         self.x_full, self.x_free = B("x_full", 1), B("x_free", 1)
         self.dep_full, self.dep_free = two("dep_full", 8), two("dep_free", 1)
         self.q_done = B("q_done", 2)
-        self.word = [None] * (stages8 if fp8 else stages)   # tile issued into a slot
+        # warp pieces: the ring of BF16, or e4m3 slots over the space of both rings
+        self.W = 2 * stages + stages8 if fp8 else stages
+        self.w_full = [B(f"w_full{s}", 1) for s in range(self.W)] if fp8 else self.kv_full
+        self.w_empty = [B(f"w_empty{s}", 1) for s in range(self.W)] if fp8 else self.kv_empty
+        self.w_ring = [None] * self.W
+        self.word = [None] * self.W      # tile issued into a slot
         self.dep = [{}, {}]              # warp -> (piece, its tiles) in a buffer
         self.joined = []                 # (piece, tiles) written out
         self.s_full = [two(f"s_full{g}.", 1) for g in range(2)]
@@ -130,15 +135,18 @@ class Model:
                     full[k % S].arrive()
                 self.tma.append((self.tick + self.rng.randint(1, 30), land))
                 yield
-        kt = sum(n for n, _ in self.pieces)
-        full, empty, S, ring = (self.kv8_full, self.kv8_empty, self.S8, self.ring8) if self.fp8 else \
-            (self.kv_full, self.kv_empty, self.S, self.ring)
+        kt = 0 if self.fp8 else sum(n for n, _ in self.pieces)
+        full, empty, S = self.w_full, self.w_empty, self.W
+        if self.fp8 and self.warp_pieces:
+            yield from self.until(self.q_done, 0)
+            assert not any(self.ring_reads.values()) and not any(self.pv_open), "rings in use"
+            assert all(b.pending == b.count for b in self.kv8_empty), "a converter reads its ring"
+        ring = self.w_ring if self.fp8 else self.ring
         for n in self.warp_pieces:
             for k in range(kt, kt + n):
                 if k >= S:
                     yield from self.until(empty[k % S], k // S - 1)
-                old = ring[k % S]  # (an e4m3 tile before the warp pieces: its converter is done)
-                assert (self.fp8 and not isinstance(old, tuple)) or not self.ring_reads.get(old), "ring slot overwritten"
+                assert not self.ring_reads.get(ring[k % S]), "ring slot overwritten"
                 ring[k % S], self.word[k % S], self.ring_reads[("w", k)] = None, k, 1
 
                 def land(k=k):
@@ -151,9 +159,8 @@ class Model:
     def consumer(self, w):
         """Softmax warp w in the warp pieces."""
         joins = sum(1 for n, two in self.pieces if not two and n > 1)
-        full, empty, S, ring = (self.kv8_full, self.kv8_empty, self.S8, self.ring8) if self.fp8 else \
-            (self.kv_full, self.kv_empty, self.S, self.ring)
-        kt = sum(n for n, _ in self.pieces)
+        full, empty, S = self.w_full, self.w_empty, self.W
+        kt = 0 if self.fp8 else sum(n for n, _ in self.pieces)
         for i, n in enumerate(self.warp_pieces):
             got = []
             for j in range((w - kt) % 8, n, 8):
@@ -161,6 +168,7 @@ class Model:
                 while self.word[k % S] != k:
                     yield WAIT
                 yield from self.until(full[k % S], k // S)
+                ring = self.w_ring if self.fp8 else self.ring
                 assert ring[k % S] == ("w", k)
                 for _ in range(self.rng.randint(0, 6)):
                     yield
@@ -408,7 +416,7 @@ def test_no_stale_wait_no_overwrite_no_deadlock(fp8, seed):
     for _ in range(25):
         pieces = [(rng.choice([1, 1, 2, 3, 4, 5, 9]), rng.random() < 0.4) for _ in range(rng.randint(1, 8))]
         last = [rng.choice([1, 2, 5, 8, 9, 20]) for _ in range(rng.choice([0, 0, 1, 3, 7]))]
-        Model(rng, fp8, pieces if rng.random() < 0.9 or not last else [], *((3, 4) if fp8 else (5, 0)), last).run()
+        Model(rng, fp8, pieces if rng.random() < 0.9 or not last else [], *((4, 2) if fp8 else (5, 0)), last).run()
 
 
 def test_the_model_sees_a_missing_wait():
@@ -464,7 +472,7 @@ def test_the_model_sees_a_missing_wait():
             pieces = [(rng.choice([1, 1, 2, 3, 4]), rng.random() < 0.3) for _ in range(12)]
             try:
                 last = [rng.choice([1, 3, 9]) for _ in range(6)] if broken in (NoWord, NoSlotWait) else []
-                broken(rng, broken is OneScale, pieces, *((3, 4) if broken is OneScale else (5, 0)), last).run()
+                broken(rng, broken is OneScale, pieces, *((4, 2) if broken is OneScale else (5, 0)), last).run()
             except AssertionError:
                 failed += 1
         assert failed, broken.__name__
