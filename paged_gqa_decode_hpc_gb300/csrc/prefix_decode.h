@@ -60,7 +60,7 @@ struct PrefixCosts {
 };
 constexpr PrefixCosts kPrefixCosts[2][2] = {  // [e4m3][several new tokens]
     {{600, 84, 70, 10, 56}, {600, 84, 70, 200, 70}},
-    {{500, 90, 70, 20, 48}, {500, 90, 70, 250, 80}}};
+    {{450, 92, 64, 45, 37}, {450, 92, 64, 250, 80}}};
 
 struct PrefixPlanParams {
   PrefixCosts costs;
