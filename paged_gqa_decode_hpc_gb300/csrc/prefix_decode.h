@@ -107,6 +107,8 @@ struct PrefixMergeParams {
   int64_t o_sb, o_st, o_sh;
   float* lse;                   // may be null
   int64_t l_sb, l_st, l_sh;
+  int32_t* err;
+  unsigned long long timeout_ns;
 };
 cudaError_t launch_prefix_merge(const PrefixMergeParams& p, cudaStream_t stream);
 

@@ -31,7 +31,7 @@ namespace hpc {
 namespace {
 
 constexpr int kMaxThreads = 1024;
-constexpr int kMinPart = 100;    // 1 us
+constexpr int kMinPart = 100;    // 1 us (4 us: 4 x (200 + 1 .. 40) positions 15.7 against 13.0 us)
 constexpr int kKeptLens = 1024;  // lengths kept in shared memory
 
 // Inclusive block scan; the total too. One barrier, and one more before the
