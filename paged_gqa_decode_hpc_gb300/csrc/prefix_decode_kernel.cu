@@ -148,6 +148,17 @@ __device__ __forceinline__ void st_shared_zero16(uint32_t a) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0) : "memory");
 }
 
+// A K / V tile with an L2 eviction priority.
+__device__ __forceinline__ void tma_load_tile(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                              int c0, int c1, int c2, int c3, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3),
+      "l"(policy)
+      : "memory");
+}
+
 // One look at an mbarrier phase.
 __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
   uint32_t ok;
@@ -388,6 +399,9 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
   if (warp == Lt::kProducerWarp) {
     // ------------------------------------------------------------ producer
     if (FP8) regs_dec();
+    uint64_t read_once, shared_tiles;  // own tiles leave L2 first: row tiles read shared ones again
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(read_once));
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(shared_tiles));
     int issued = 0, issued_w = 0;                 // K / V tiles issued, in order
     int q_issued[2] = {0, 0};                     // fills issued per Q slot
     int stop = p.withhold_copies != 0 ? 1 : 0;    // failure-path test: nothing is issued
@@ -420,6 +434,7 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
       if (!pc.two) ++ones;
       stop = __shfl_sync(0xffffffffu, stop, 0);
       const bool to_warps = FP8 && own && warp_own;
+      const uint64_t policy = own ? read_once : shared_tiles;
       if (to_warps && kw == 0) {
         // the warp pieces' ring lies over the two others: every MMA on them is done
         if (lane == 0 && !wait(q_done, 0)) stop = 1;
@@ -449,8 +464,8 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
                 st_release_word(base + Lt::kOffWord + 4 * slot, (uint32_t)j);
                 const uint32_t dk = sKV + slot * kStageBytes8;
                 mbar_expect_tx(w_full(slot), kStageBytes8);
-                tma_load_4d(dk, &tmk, w_full(slot), 0, c1, c2, bk);
-                tma_load_4d(dk + kKVTileBytes8, &tmv, w_full(slot), 0, c1, c2, bk);
+                tma_load_tile(dk, &tmk, w_full(slot), 0, c1, c2, bk, policy);
+                tma_load_tile(dk + kKVTileBytes8, &tmv, w_full(slot), 0, c1, c2, bk, policy);
                 issued_w = j + 1;
               } else {
                 stop = 1;
@@ -461,8 +476,8 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
                 const uint32_t fb = kv8_full(slot);
                 const uint32_t dk = sKV8 + slot * kStageBytes8, dv = dk + kKVTileBytes8;
                 mbar_expect_tx(fb, kStageBytes8);
-                tma_load_4d(dk, &tmk, fb, 0, c1, c2, bk);
-                tma_load_4d(dv, &tmv, fb, 0, c1, c2, bk);
+                tma_load_tile(dk, &tmk, fb, 0, c1, c2, bk, policy);
+                tma_load_tile(dv, &tmv, fb, 0, c1, c2, bk, policy);
                 issued = j + 1;
               } else {
                 stop = 1;
@@ -474,10 +489,10 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
                 st_release_word(base + Lt::kOffWord + 4 * slot, (uint32_t)j);
                 const uint32_t dk = sKV + slot * kStageBytes, dv = dk + kKVTileBytes;
                 mbar_expect_tx(fb, kStageBytes);
-                tma_load_4d(dk, &tmk, fb, 0, c1, c2, bk);
-                tma_load_4d(dk + kKVTileBytes / 2, &tmk, fb, 64, c1, c2, bk);
-                tma_load_4d(dv, &tmv, fb, 0, c1, c2, bk);
-                tma_load_4d(dv + kKVTileBytes / 2, &tmv, fb, 64, c1, c2, bk);
+                tma_load_tile(dk, &tmk, fb, 0, c1, c2, bk, policy);
+                tma_load_tile(dk + kKVTileBytes / 2, &tmk, fb, 64, c1, c2, bk, policy);
+                tma_load_tile(dv, &tmv, fb, 0, c1, c2, bk, policy);
+                tma_load_tile(dv + kKVTileBytes / 2, &tmv, fb, 64, c1, c2, bk, policy);
                 issued = j + 1;
               } else {
                 stop = 1;
