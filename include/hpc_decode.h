@@ -509,7 +509,8 @@ hpc_status hpc_extend_attn_ex(const hpc_tensor* q, const hpc_tensor* k_cache,
  * every slot is -1 and every position 0, and the bits say why: BAD_LENGTH (a
  * negative length or a sum past int32), TABLE_TOO_SHORT (a sequence needs more
  * than max_blocks), CAPACITY (more new tokens than cap_tokens, or a count
- * outside the stack), NO_BLOCKS (more blocks needed than free). Apart from the
+ * outside the stack), NO_BLOCKS (more blocks needed than free). Calls that use
+ * one stack must be ordered on the GPU (one stream). Apart from the
  * two in-place forms no output may overlap an input or another output
  * (HPC_ERR_INVALID_ARG). One launch (two for more than 32768 tokens); allocates
  * nothing.

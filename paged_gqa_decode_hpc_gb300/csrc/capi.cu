@@ -994,6 +994,8 @@ hpc_status hpc_decode_tc_min_q_len(int32_t q_len, int32_t* previous) {
 hpc_status hpc_decode_plan_set_timing_events(hpc_plan_t plan, void* ev_start, void* ev_attn_done,
                                              void* ev_end) {
   if (!plan) return fail(HPC_ERR_INVALID_ARG, "plan is null");
+  if (plan->kind == HPC_PLAN_PREFIX)
+    return fail(HPC_ERR_INVALID_ARG, "a prefix plan serves hpc_decode_prefix_attn only");
   plan->ev_start = (cudaEvent_t)ev_start;
   plan->ev_mid = (cudaEvent_t)ev_attn_done;
   plan->ev_end = (cudaEvent_t)ev_end;

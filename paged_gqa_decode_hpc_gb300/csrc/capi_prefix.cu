@@ -88,6 +88,7 @@ hpc_status hpc_decode_prefix_plan_create(int32_t max_seqs, int32_t max_q_len, in
     if (e == cudaSuccess) e = cudaMalloc(&pl->d_ws, (size_t)pl->ws_floats * sizeof(float));
     if (e != cudaSuccess) {
       hpc_decode_plan_destroy(pl);
+      cudaGetLastError();  // a failed allocation must not look like a later launch's error
       return fail(e == cudaErrorMemoryAllocation ? HPC_ERR_OOM : HPC_ERR_CUDA,
                   std::string("prefix plan: ") + cudaGetErrorString(e));
     }
@@ -102,8 +103,6 @@ hpc_status hpc_decode_prefix_attn(const hpc_tensor* q, const hpc_tensor* k_cache
                                   const hpc_tensor* prefix_lens, hpc_plan_t plan, hpc_tensor* out,
                                   hpc_tensor* lse, float softmax_scale, void* stream) {
   return guarded([&]() -> hpc_status {
-    if (!plan || plan->kind != HPC_PLAN_PREFIX)
-      return fail(HPC_ERR_INVALID_ARG, "plan must come from hpc_decode_prefix_plan_create");
     // what every decode call checks of its tensors
     hpc_plan_s any;
     any.num_seqs = q && q->ndim > 0 && q->ndim <= 4 ? (int32_t)q->shape[0] : 0;
@@ -122,14 +121,16 @@ hpc_status hpc_decode_prefix_attn(const hpc_tensor* q, const hpc_tensor* k_cache
     if (cu_groups && (st = check_ints(cu_groups, "cu_groups", G + 1)) != HPC_OK) return st;
     if (!cu_groups && G != 1)
       return fail(HPC_ERR_INVALID_ARG, "without cu_groups prefix_lens holds one length");
-    if (B > plan->max_seqs || T > plan->prefix_q_len || Hq > plan->ws_heads)
-      return fail(HPC_ERR_INVALID_ARG, "the plan was created for fewer sequences, tokens or heads");
     const int64_t pair_stride = multi ? q->stride[1] : q->stride[0];
     if (multi && B > 1 && q->stride[0] != T * q->stride[1])
       return fail(HPC_ERR_INVALID_ARG, "q's tokens must be evenly spaced over the batch "
                                        "(stride 0 = q_len * stride 1)");
     if (!(softmax_scale <= 0.f) && !std::isfinite(softmax_scale))
       return fail(HPC_ERR_INVALID_ARG, "softmax_scale must be finite");
+    if (!plan || plan->kind != HPC_PLAN_PREFIX)
+      return fail(HPC_ERR_INVALID_ARG, "plan must come from hpc_decode_prefix_plan_create");
+    if (B > plan->max_seqs || T > plan->prefix_q_len || Hq > plan->ws_heads)
+      return fail(HPC_ERR_INVALID_ARG, "the plan was created for fewer sequences, tokens or heads");
     if (B == 0) return HPC_OK;
     if (NB == 0) return fail(HPC_ERR_INVALID_ARG, "k_cache has no blocks");
     if (NB > INT_MAX || block_table->shape[1] > INT_MAX)

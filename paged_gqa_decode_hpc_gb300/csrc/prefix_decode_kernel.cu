@@ -224,6 +224,13 @@ __device__ __forceinline__ bool wait_word(uint32_t word, uint32_t tile, volatile
   }
 }
 
+// The maximum that a state leaves with: -inf for a row without a visible key
+// (the merge then skips its o), and a finite one where the scores were NaN only,
+// which the maximum has passed over, so that the NaN in l and o are not skipped.
+__device__ __forceinline__ float state_max(float m, float l) {
+  return l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m);
+}
+
 // One piece: tiles [tb, te) of (work row v, KV head h).
 struct Piece {
   int h, tb, te;
@@ -666,8 +673,8 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
           dst[(d >> 2) * 32 + 4 * h2 + 4 + (d & 3)] = acc[dm][2 * r + 1];
         }
       if (lane < 4) {
-        p.ws.m[blk * 8 + h2] = M0;
-        p.ws.m[blk * 8 + h2 + 1] = M1;
+        p.ws.m[blk * 8 + h2] = state_max(M0, l0);
+        p.ws.m[blk * 8 + h2 + 1] = state_max(M1, l1);
         p.ws.l[blk * 8 + h2] = l0;
         p.ws.l[blk * 8 + h2 + 1] = l1;
       }
@@ -1111,7 +1118,7 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
           }
           if (row_ok) {
             const float lt = join ? l * a0 + l1 * a1 : l;
-            p.ws.m[blk * 8 + (r & 7)] = lt == 0.f ? -INFINITY : M;
+            p.ws.m[blk * 8 + (r & 7)] = state_max(M, lt);
             p.ws.l[blk * 8 + (r & 7)] = lt;
           }
         }

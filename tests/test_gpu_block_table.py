@@ -89,6 +89,18 @@ def test_append_strided_table_keeps_its_gaps():
     assert (wide[:, :2] == 55).all() and (wide[:, 2 + c["width"]:] == 55).all()
 
 
+def test_append_into_unaligned_buffers():
+    c = _case(random.Random(5), 30, 200, 90, pad=3)
+    buf = [_dev([77] * (c["cap"] + 6)) for _ in range(2)]
+    B = 30
+    out = dict(table=_table(c), lens=_dev([0] * B), cu=_dev([0] * (B + 1)), positions=buf[0][1:1 + c["cap"]],
+               slots=buf[1][3:3 + c["cap"]], count=_dev([0]), err=_dev([0]))
+    hpc.hpc_block_table_append(_dev(c["old"]), _dev(c["new"]), _dev(c["free"]), _dev([c["count"]]), c["blocks"], out["table"],
+                               out["lens"], out["cu"], out["positions"], out["slots"], out["count"], device_error=out["err"])
+    _check_append(c, out)
+    assert buf[0][0] == 77 and (buf[0][1 + c["cap"]:] == 77).all() and (buf[1][:3] == 77).all() and (buf[1][3 + c["cap"]:] == 77).all()
+
+
 def _refused(name):
     c = _case(random.Random(9), 12, 200, 100, pad=2)
     if name == "negative length":

@@ -289,6 +289,49 @@ def test_captured_steps_follow_the_device_lengths():
             c.check(got)
 
 
+def test_large_batches():
+    rng = np.random.default_rng(15)
+    # 4096 sequences in 700 groups, some empty, most of one or two blocks; 8 new tokens of 300 sequences
+    cuts = np.sort(rng.choice(np.arange(1, 4096), 699, replace=False)).tolist()
+    groups = [(int(rng.choice([0, 64, 130])), [int(x) for x in rng.integers(0, 200, b - a)])
+              for a, b in zip([0] + cuts, cuts + [4096])]
+    groups = [(p, [n if n == 0 or n >= p else p + n for n in lens]) for p, lens in groups]
+    Case(groups, hkv=1, seed=16).check()
+    Case([(192, [200 + i % 90 for i in range(200)]), (64, [72 + i for i in range(100)])], q_len=8, hkv=1, fp8=True, seed=17).check()
+
+
+def test_queries_that_are_not_finite_spoil_their_rows_only():
+    for fp8 in (False, True):
+        c = Case([(256, [300, 260, 400])], seed=18, fp8=fp8)
+        clean = c.run()[0]
+        c.q[1, 3, 7] = float("nan")
+        out, lse = c.run()
+        bad = torch.zeros(out.shape[:2], dtype=torch.bool)
+        bad[1, 3] = True
+        assert torch.isnan(out[1, 3]).all() and torch.isnan(lse[1, 3])
+        assert torch.equal(out.cpu()[~bad], clean.cpu()[~bad])
+
+
+def test_plans_are_not_mixed():
+    c = Case([(64, [100, 90])], seed=19)
+    d, out = c.device(), torch.zeros(c.q.shape, dtype=torch.bfloat16, device="cuda")
+    prefix = hpc.hpc_decode_prefix_plan_create(2, 1, 152, 16)
+    other = hpc.hpc_decode_plan_create(2, 152, 16)
+    small = [hpc.hpc_decode_prefix_plan_create(1, 1, 152, 16), hpc.hpc_decode_prefix_plan_create(2, 8, 152, 8), other]
+    for plan in small:
+        with pytest.raises(hpc.HpcError) as e:
+            hpc.hpc_decode_prefix_attn(d["q"], d["k"], d["v"], d["bt"], d["sl"], d["pl"], plan, out)
+        assert e.value.status == hpc.HPC_ERR_INVALID_ARG
+    calls = [lambda: hpc.hpc_decode_step(d["q"], d["k"], d["v"], d["bt"], d["sl"], prefix, 152, out),
+             lambda: hpc.hpc_decode_attn(d["q"], d["k"], d["v"], d["bt"], d["sl"], prefix, out),
+             lambda: hpc.hpc_decode_plan_device(d["sl"], 152, prefix), lambda: hpc.hpc_decode_plan_update([1, 2], 152, prefix),
+             lambda: hpc.hpc_decode_plan_export(prefix), lambda: hpc.hpc_decode_plan_set_timing_events(prefix)]
+    for call in calls:
+        with pytest.raises(hpc.HpcError):
+            call()
+    c.check(c.run(d, plan=prefix))
+
+
 def test_agrees_with_the_decode_step():
     c = Case([(1024, [1100 + i for i in range(24)])], hkv=8, seed=13)
     d = c.device()
