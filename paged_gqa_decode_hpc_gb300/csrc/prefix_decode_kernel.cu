@@ -82,10 +82,13 @@ struct Lay {
   static constexpr int kConvWarps = FP8 ? 4 : 0;
   static constexpr int kConvWarp0 = 8;
   static constexpr int kProducerWarp = 8 + kConvWarps, kMmaWarp0 = kProducerWarp + 1;
-  // FP8: whole warpgroups (one warp idle), so that registers can move to the softmax ones
-  static constexpr int kThreads = FP8 ? 512 : 32 * (kMmaWarp0 + 2);
-  static constexpr int kStages = FP8 ? 4 : 5;   // 16-bit K + V ring
-  static constexpr int kStages8 = FP8 ? 2 : 0;  // e4m3 K + V ring
+  // whole warpgroups (one warp idle), so that registers can move to the softmax ones
+  static constexpr int kThreads = FP8 ? 512 : 384;
+  // K + V rings, 16-bit and e4m3. Of the e4m3 cache's 160 KB more slots went to the
+  // ring that copies land in: with 4 + 2, loads beside own pieces that saturate the
+  // memory came late (6 groups of 4 to 20, 1300 .. 14300 shared: 65.1 against 62.3 us).
+  static constexpr int kStages = FP8 ? 3 : 5;
+  static constexpr int kStages8 = FP8 ? 4 : 0;
   // warp pieces: the 16-bit ring, or, all as e4m3 slots, the space of both rings
   static constexpr int kWStages = FP8 ? 2 * kStages + kStages8 : kStages;
   static constexpr uint32_t kWStageBytes = FP8 ? kStageBytes8 : kStageBytes;
@@ -103,13 +106,13 @@ struct Lay {
   static constexpr uint32_t kOffScale = kOffBar + 8 * kNumBars;
   static constexpr uint32_t kOffX = kOffScale + (FP8 ? 4 * kRows : 0);  // float [2][128]
   static constexpr uint32_t kOffWord = kOffX + 2 * kRows * 4;  // warp pieces: tile in each slot
-  static constexpr uint32_t kOffMisc = (kOffWord + 4 * kWStages + 15) / 16 * 16;
-  // + slack to align to 1024 from the 16 that dynamic shared memory has
-  static constexpr uint32_t kSmemBytes = kOffMisc + 16 + 1008;
+  static constexpr uint32_t kOffMisc = kOffWord + 4 * kWStages;
+  // + slack to align to 1024 from the 128 that the declaration gives
+  static constexpr uint32_t kSmemBytes = kOffMisc + 8 + 896;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
-// FP8: of the launch's 512 x 128 registers, the two softmax warpgroups take 176
-// a thread and the two others keep 80: 256 * 176 + 256 * 80 = 65536.
+// Of the launch's 512 x 128 registers (e4m3; bf16 384 x 168) the softmax
+// warpgroups take 176 a thread and the other warps keep 80: 256 * 176 + 256 * 80 = 65536.
 constexpr int kRegsSoftmax = 176, kRegsOther = 80;
 __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax) : "memory");
@@ -241,7 +244,7 @@ struct Piece {
 // work row's record is loaded one row ahead.
 struct Walk {
   const int4* recs;
-  int v, u, v1, u1, H;
+  int v, u, h, v1, u1, H;  // h: the KV head of unit u, kept beside it: no division per piece
   int4 ra, rb, na, nb;  // records of rows v and v + 1: {pair0, pairs, table, tile0}, {tiles, own, len, -}
   __device__ __forceinline__ void load(int row, int4& a, int4& b) const {
     a = recs[2 * row];
@@ -263,22 +266,24 @@ struct Walk {
     u = b0.y;
     v1 = b1.x;
     u1 = b1.y;
+    h = rb.x > 0 ? u / rb.x : 0;
     if (has(v + 1)) load(v + 1, na, nb);
   }
   __device__ __forceinline__ bool next(Piece& s) {
     while (v < v1 || (v == v1 && u < u1)) {
       const int n = rb.x, all = H * n, end = v == v1 ? min(u1, all) : all;
       if (u < end) {
-        s.h = u / n;
-        const int first = s.h * n;
+        const int first = h * n;
+        s.h = h;
         s.tb = u - first;
         s.te = min(first + n, end) - first;
         s.two = ra.y > kPrefixTilePairs;
         u = first + s.te;
+        h += s.te == n;
         return true;
       }
       ++v;
-      u = 0;
+      u = h = 0;
       ra = na;
       rb = nb;
       if (has(v + 1)) load(v + 1, na, nb);
@@ -297,7 +302,7 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
   using Lt = Lay<FP8>;
   constexpr int S = Lt::kStages, S8 = Lt::kStages8;
   constexpr int S8n = S8 > 0 ? S8 : 1;
-  extern __shared__ uint8_t smem_raw[];
+  extern __shared__ __align__(128) uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;  // 128-byte swizzle atoms need 1024-B alignment
   uint8_t* smem = smem_raw + (base - raw);
@@ -395,8 +400,9 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
   // warp pieces
   const bool warp_own = p.q_len == 1;
 
+  // Each role begins its walk behind its register split: one that lives across it
+  // was kept in local memory (e4m3: 71.2 -> 65.1 us).
   Walk walk;
-  walk.begin(p, part);
   Piece pc;
   int uses[2] = {0, 0};  // fills of each Q slot before this piece
   int ones = 0;          // one-row-tile pieces before this one (their Q slots alternate)
@@ -405,7 +411,8 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
 
   if (warp == Lt::kProducerWarp) {
     // ------------------------------------------------------------ producer
-    if (FP8) regs_dec();
+    regs_dec();
+    walk.begin(p, part);
     uint64_t read_once, shared_tiles;  // own tiles leave L2 first: row tiles read shared ones again
     asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(read_once));
     asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(shared_tiles));
@@ -538,6 +545,7 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
     // all 8 bank groups on the load and both stores. V rows behind the end of
     // the sequence become zeros.
     regs_dec();
+    walk.begin(p, part);
     constexpr int kNT = 128;
     const int ct = threadIdx.x - 32 * Lt::kConvWarp0;
     const int cq = ct & 15, c = cq & 7, cr = ((cq >> 2) & 1) ^ (cq >> 3);
@@ -604,14 +612,15 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
       kt += n;
     }
     named_bar_sync(1, Lt::kThreads);
-  } else if (FP8 && warp >= Lt::kMmaWarp0 + 2) {
+  } else if (warp >= Lt::kMmaWarp0 + 2) {
     regs_dec();  // the idle warp of the last warpgroup
     named_bar_sync(1, Lt::kThreads);
   } else if (warp >= Lt::kMmaWarp0) {
     // ------------------------------------------- MMA issue for pipeline g
     // The whole warp runs the schedule so its values stay warp-uniform; one
     // elected lane issues the MMAs and commits.
-    if (FP8) regs_dec();
+    regs_dec();
+    walk.begin(p, part);
     const int g = warp - Lt::kMmaWarp0;
     const bool leader = elect_one() != 0;
     bool issued_any = false;
@@ -801,7 +810,8 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
     if (warp == Lt::kMmaWarp0) tmem_dealloc(tmem, 2 * kColsPerPipe);
   } else {
     // ------------------------------------------- softmax warpgroup of pipeline g
-    if (FP8) regs_inc();
+    regs_inc();
+    walk.begin(p, part);
     const int g = warp >> 2;
     const int r = threadIdx.x - kRows * g;  // query row = TMEM lane
     const int wg_warp = warp & 3;

@@ -416,7 +416,7 @@ def test_no_stale_wait_no_overwrite_no_deadlock(fp8, seed):
     for _ in range(25):
         pieces = [(rng.choice([1, 1, 2, 3, 4, 5, 9]), rng.random() < 0.4) for _ in range(rng.randint(1, 8))]
         last = [rng.choice([1, 2, 5, 8, 9, 20]) for _ in range(rng.choice([0, 0, 1, 3, 7]))]
-        Model(rng, fp8, pieces if rng.random() < 0.9 or not last else [], *((4, 2) if fp8 else (5, 0)), last).run()
+        Model(rng, fp8, pieces if rng.random() < 0.9 or not last else [], *((3, 4) if fp8 else (5, 0)), last).run()
 
 
 def test_the_model_sees_a_missing_wait():
@@ -472,7 +472,7 @@ def test_the_model_sees_a_missing_wait():
             pieces = [(rng.choice([1, 1, 2, 3, 4]), rng.random() < 0.3) for _ in range(12)]
             try:
                 last = [rng.choice([1, 3, 9]) for _ in range(6)] if broken in (NoWord, NoSlotWait) else []
-                broken(rng, broken is OneScale, pieces, *((4, 2) if broken is OneScale else (5, 0)), last).run()
+                broken(rng, broken is OneScale, pieces, *((3, 4) if broken is OneScale else (5, 0)), last).run()
             except AssertionError:
                 failed += 1
         assert failed, broken.__name__
