@@ -50,17 +50,20 @@ struct PrefixWorkspace {
   int64_t cont0; // first block of the parts' continuing pieces, 32 per part
 };
 
-// What a KV head of a work row costs its CTA, in units of 10 ns: a fixed part
-// (Q and the first tile's way through the pipeline, the epilogue) and each tile;
-// measured per piece on 64 x (32768 shared + 128 .. 2048 own), 32 x (4096 + 64 ..
-// 1024) and 16 x 4 new tokens x (8192 + 100 .. 600) positions with 8 KV heads.
-// Own pieces of one new token run as warp pieces and differ from those of several.
+// What a KV head of a work row costs its CTA, in units of about 10 ns: a fixed part
+// (a shared piece's Q and epilogue; its start counts for every part and cancels)
+// and each tile. Found by a random search on the geometric mean of 4 to 8 mixed
+// batches of each kind (8 to 60 sequences, 512 .. 32768 shared and 1 .. 2048 own
+// positions, 1 to 5 groups); before, with a shared piece priced by its latency
+// alone (600), mid-sized batches took up to a fifth more (16 x (2048 + 16 .. 256):
+// 26.7 against 21.7 us). Own pieces of one new token run as warp pieces and differ
+// from those of several.
 struct PrefixCosts {
   int32_t shared_fixed, two_tile, one_tile, own_fixed, own_tile;
 };
 constexpr PrefixCosts kPrefixCosts[2][2] = {  // [e4m3][several new tokens]
-    {{600, 84, 70, 10, 56}, {600, 84, 70, 200, 70}},
-    {{450, 92, 64, 45, 37}, {450, 92, 64, 250, 80}}};
+    {{330, 100, 71, 18, 68}, {400, 84, 70, 200, 70}},
+    {{300, 90, 63, 58, 35}, {600, 83, 56, 390, 80}}};
 
 struct PrefixPlanParams {
   PrefixCosts costs;
