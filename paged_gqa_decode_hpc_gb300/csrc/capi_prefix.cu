@@ -231,7 +231,7 @@ hpc_status hpc_decode_prefix_attn(const hpc_tensor* q, const hpc_tensor* k_cache
     mp.l_sh = has_lse ? lse->stride[lse->ndim - 1] : 0;
     mp.err = plan->d_err;
     mp.timeout_ns = wait_limit_ns();
-    e = launch_prefix_merge(mp, s);
+    e = launch_prefix_merge(mp, plan->num_sms, s);
     if (e != cudaSuccess)
       return fail(HPC_ERR_CUDA, std::string("prefix merge launch: ") + cudaGetErrorString(e));
     return HPC_OK;

@@ -113,6 +113,6 @@ struct PrefixMergeParams {
   int32_t* err;
   unsigned long long timeout_ns;
 };
-cudaError_t launch_prefix_merge(const PrefixMergeParams& p, cudaStream_t stream);
+cudaError_t launch_prefix_merge(const PrefixMergeParams& p, int num_sms, cudaStream_t stream);
 
 }  // namespace hpc

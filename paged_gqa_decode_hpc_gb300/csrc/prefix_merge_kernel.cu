@@ -9,16 +9,19 @@
 // states are added in that order, so the result does not depend on timing. A
 // row that no piece has seen gets out = 0, lse = -inf.
 //
-// One CTA of 256 threads per (pair, KV head): thread = (column group of 4, row),
-// the 8 rows of a column group adjacent, as the states are stored. What bounds
-// it: latency for few pairs, L2 (where the states just written still are) for
-// many: 4 KB a state. So which states there are is worked out before the wait
-// for the attention kernel (the plan is complete by then: the attention kernel
-// lets this one start only after its own wait for it), and up to kStates states
-// are fetched at once, by bulk copies into shared memory: no state waits for
-// another and none takes registers, so that five CTAs fit on an SM (loads of six
-// states a thread at a time, two rounds for the 7 to 9 states of a row cut over
-// as many CTAs, took 3.4 us where this takes 2.5).
+// A CTA has the columns of a (pair, KV head), or a half or quarter of them: thread =
+// (column group of 4, row), the 8 rows of a column group adjacent, as the states are
+// stored. What bounds it: latency for few pairs, L2 (where the states just written
+// still are) for many: 4 KB a state. So which states there are is worked out before
+// the wait for the attention kernel (the plan is complete by then: the attention
+// kernel lets this one start only after its own wait for it), and 10 states, or 20
+// of halves, 30 of quarters, are fetched at once, by bulk copies into shared memory:
+// no state waits for another and none takes registers. A long prefix of few
+// sequences is cut over many CTAs (8 x 20000 positions: 20 states a pair), which
+// whole columns took in rounds: a step of 39.8 us, 37.4 in halves, 35.8 in quarters.
+// But CTAs that are not resident when the attention kernel ends have all of this
+// ahead of them then (480 pairs and heads, 960 halves: 60.9 -> 63.2 us), so the
+// columns are cut as far as all CTAs fit on the GPU at once.
 #include <cuda_bf16.h>
 
 #include "hpc_internal.h"
@@ -29,11 +32,21 @@
 namespace hpc {
 
 namespace {
-
-constexpr int kThreads = 256;
-constexpr int kStates = 10;  // states in shared memory
 constexpr int kListed = 64;  // states listed before the wait
-constexpr uint32_t kStateBytes = 8 * kHeadDim * 4, kRowBytes = 8 * 4;
+constexpr int kBatch = 10;   // states joined at a time
+constexpr uint32_t kRowBytes = 8 * 4;
+
+// kSplit CTAs share the columns of a (pair, KV head).
+template <int kSplit>
+struct MergeLay {
+  static constexpr int kThreads = 256 / kSplit;
+  static constexpr int kStates = kBatch * (kSplit < 4 ? kSplit : 3);  // in shared memory
+  static_assert(kStates <= 32, "one warp fetches them");
+  static constexpr uint32_t kStateBytes = kThreads * 16;
+  // CTAs that an SM's 228 KB hold: the states, 8 bytes a listed one, the barrier and 1 KB each
+  static constexpr int kResident =
+      228 * 1024 / (kStates * (kStateBytes + 2 * kRowBytes) + 8 * kListed + 8 + 1024);
+};
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
                                           uint32_t bar) {
@@ -45,9 +58,14 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 }
 constexpr float kLn2 = 0.6931471805599453f;
 
-__global__ void __launch_bounds__(kThreads) prefix_merge_kernel(const PrefixMergeParams p) {
+template <int kSplit>
+__global__ void __launch_bounds__(256 / kSplit) prefix_merge_kernel(const PrefixMergeParams p) {
+  using Lt = MergeLay<kSplit>;
+  constexpr int kThreads = Lt::kThreads, kStates = Lt::kStates;
+  constexpr uint32_t kStateBytes = Lt::kStateBytes;
   const int H = p.num_kv_heads, T = p.q_len;
-  const int64_t item = blockIdx.x;
+  const int64_t item = blockIdx.x / kSplit;
+  const int c0 = (int)(blockIdx.x % kSplit) * (32 / kSplit);  // first column group
   const int pair = (int)(item / H), h = (int)(item % H), b = pair / T, t = pair % T;
   const int row = threadIdx.x & 7, col = threadIdx.x >> 3;
   const int rows_all = p.words[kPxRows], parts = p.words[kPxParts];
@@ -124,7 +142,7 @@ __global__ void __launch_bounds__(kThreads) prefix_merge_kernel(const PrefixMerg
       if (blk >= 0) {
         bulk_load(tc05::smem_u32(s_m[threadIdx.x]), p.ws.m + blk * 8, kRowBytes, bar);
         bulk_load(tc05::smem_u32(s_l[threadIdx.x]), p.ws.l + blk * 8, kRowBytes, bar);
-        bulk_load(tc05::smem_u32(s_o[threadIdx.x]), p.ws.o + blk * 256, kStateBytes, bar);
+        bulk_load(tc05::smem_u32(s_o[threadIdx.x]), p.ws.o + blk * 256 + c0 * 8, kStateBytes, bar);
       } else if ((int)threadIdx.x < n) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) s_m[threadIdx.x][i] = -INFINITY;
@@ -138,23 +156,24 @@ __global__ void __launch_bounds__(kThreads) prefix_merge_kernel(const PrefixMerg
         break;
       }
     }
-    // unrolled over all cells: absent states and those without a visible key have
-    // m = -inf, and what stands in their o is not used
-    float m[kStates], Mn = M;
+    // unrolled over the cells of a batch: absent states and those without a visible
+    // key have m = -inf, and what stands in their o is not used
+    for (int i0 = 0; i0 < n; i0 += kBatch) {
+      float m[kBatch], Mn = M;
 #pragma unroll
-    for (int i = 0; i < kStates; ++i) {
-      m[i] = i < n ? s_m[i][row] : -INFINITY;
-      Mn = fmaxf(Mn, m[i]);
-    }
-    if (Mn != -INFINITY) {  // else no visible key for this row so far
+      for (int i = 0; i < kBatch; ++i) {
+        m[i] = i0 + i < n ? s_m[i0 + i][row] : -INFINITY;
+        Mn = fmaxf(Mn, m[i]);
+      }
+      if (Mn == -INFINITY) continue;  // no visible key for this row so far
       const float a = ptx_ex2(M - Mn);
       L *= a;
       acc.x *= a; acc.y *= a; acc.z *= a; acc.w *= a;
 #pragma unroll
-      for (int i = 0; i < kStates; ++i) {
+      for (int i = 0; i < kBatch; ++i) {
         const float f = ptx_ex2(m[i] - Mn);
-        float4 o = s_o[i][col * 8 + row];
-        float l = s_l[i][row];
+        float4 o = s_o[i0 + i][col * 8 + row];
+        float l = s_l[i0 + i][row];
         if (m[i] == -INFINITY) {
           o = make_float4(0.f, 0.f, 0.f, 0.f);
           l = 0.f;
@@ -171,29 +190,37 @@ __global__ void __launch_bounds__(kThreads) prefix_merge_kernel(const PrefixMerg
   }
   const float inv = L == 0.f ? 0.f : p.v_scale / L;
   __nv_bfloat16* o = p.out + (int64_t)b * p.o_sb + (int64_t)t * p.o_st +
-                     (int64_t)(8 * h + row) * p.o_sh + 4 * col;
+                     (int64_t)(8 * h + row) * p.o_sh + 4 * (c0 + col);
   const __nv_bfloat162 x = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
   const __nv_bfloat162 y = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
   *reinterpret_cast<uint2*>(o) = make_uint2(*reinterpret_cast<const uint32_t*>(&x),
                                             *reinterpret_cast<const uint32_t*>(&y));
-  if (p.lse && col == 0)
+  if (p.lse && c0 + col == 0)
     p.lse[(int64_t)b * p.l_sb + (int64_t)t * p.l_st + (int64_t)(8 * h + row) * p.l_sh] =
         L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
-}  // namespace
-
-cudaError_t launch_prefix_merge(const PrefixMergeParams& p, cudaStream_t stream) {
+template <int kSplit>
+cudaError_t launch_split(const PrefixMergeParams& p, int64_t items, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((int64_t)p.num_seqs * p.q_len * p.num_kv_heads));
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3((unsigned)(items * kSplit));
+  cfg.blockDim = dim3(MergeLay<kSplit>::kThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prefix_merge_kernel, p);
+  return cudaLaunchKernelEx(&cfg, prefix_merge_kernel<kSplit>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_prefix_merge(const PrefixMergeParams& p, int num_sms, cudaStream_t stream) {
+  const int64_t items = (int64_t)p.num_seqs * p.q_len * p.num_kv_heads;
+  if (items * 4 <= (int64_t)num_sms * MergeLay<4>::kResident) return launch_split<4>(p, items, stream);
+  if (items * 2 <= (int64_t)num_sms * MergeLay<2>::kResident) return launch_split<2>(p, items, stream);
+  return launch_split<1>(p, items, stream);
 }
 
 }  // namespace hpc
