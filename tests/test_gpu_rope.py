@@ -149,6 +149,26 @@ def test_more_rows_than_a_pass(hq, hkv):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("n", [1250, 2000, 3100])  # CTAs a token: 1 or 2 with the layout's residents
+@pytest.mark.parametrize("interleaved,rot_dim", [(False, 128), (True, 64), (False, 60)])
+def test_a_token_does_not_depend_on_its_batch(n, interleaved, rot_dim):
+    def part(c, a, b):
+        d = Case(1, 44, 4)
+        d.__dict__.update(c.__dict__, n=b - a, qkv=c.qkv[a:b], pos=c.pos[a:b], slots=c.slots[a:b])
+        return d
+    c = Case(n, 44, 4, rot_dim=rot_dim, interleaved=interleaved, fp8=True, q_fp8=True, seed=n)
+    q, q8, caches = c.run()
+    first = part(c, 0, 40)
+    small = first.run()
+    first.check(small)
+    block, off = c.slots // 64, c.slots % 64
+    for a, b in ((0, 40), (40, 47), (n - 300, n)):
+        sq, sq8, sc = part(c, a, b).run()
+        assert torch.equal(sq, q[a:b]) and torch.equal(sq8, q8[a:b])
+        for x, y in zip(sc, caches):
+            assert torch.equal(x[block[a:b], :, off[a:b]], y[block[a:b], :, off[a:b]])
+
+
 @pytest.mark.parametrize("interleaved,rot_dim", [(False, 128), (True, 80), (False, 60)])
 @pytest.mark.parametrize("normed", [False, True])
 def test_fp8(interleaved, rot_dim, normed):
