@@ -25,8 +25,8 @@
 // in registers for all rows. (16 lanes a row with the partner fetched by
 // shuffles took 83 us for 8192 tokens of 64 + 16 heads.) The rows' loads are in
 // flight before the angles are formed. With few tokens the rows of a token are
-// spread over several CTAs. Interleaved pairs lie in one lane anyway; the half
-// layout at other R goes through shared memory.
+// spread over several CTAs. Interleaved pairs lie in one lane anyway; in the half
+// layout at other R the partners come from a copy of the row in shared memory.
 #include <cuda_bf16.h>
 
 #include "cache_ops.h"
@@ -42,6 +42,12 @@ constexpr int kThreads = 128;
 constexpr int kLanes = 8;                        // lanes of a row
 constexpr int kRowsAtOnce = kThreads / kLanes;
 constexpr int kUnroll = 2;                       // rows of a lane loaded together
+
+// kHalfAny: a row's first R elements in shared memory as pairs, its first half once
+// more behind them, so that the partners of eight neighbours, elements e + R / 2
+// modulo R, are neighbours too. At most 96 words; an odd pitch, so that the four rows
+// of a warp lie a bank apart and their lanes' chunks (4 words) in different banks.
+constexpr int kRowPitch = 97;
 
 enum Layout { kInterleaved = 0, kHalfLanes, kHalfAny };
 
@@ -108,18 +114,28 @@ __device__ __forceinline__ float load_weight(const void* w, int32_t dtype, int i
   return dtype == HPC_F32 ? ((const float*)w)[i] : __bfloat162float(((const __nv_bfloat16*)w)[i]);
 }
 
-// CTAs per SM, which bounds the registers: 8 where nothing spills that counts
-// (8192 tokens: 52.7 us against 55.6 with 6), 6 with a norm (64 tokens: 3.36
-// against 3.52 us with 8), 5 where every element's partner comes from shared
-// memory.
-constexpr int min_ctas(int layout, bool norm) { return layout == 2 ? 5 : norm ? 6 : 8; }
+// With a norm, or where partners come through shared memory, an element's two
+// factors, norm weights included, are read from tables in shared memory for every row
+// instead of staying in up to 32 registers, so that 8 CTAs of either fit on an SM
+// (8000 tokens of 80 rows: normed, R = 128, 68.8 -> 58.6 us; R = 90 in halves
+// 125.6 -> 56.5 us, with the partners as below).
+// Element e's place: four neighbours of all chunks, then the other four.
+__device__ __forceinline__ int table_at(int e) { return (e & 4) * 16 + (e >> 3) * 4 + (e & 3); }
+
+// CTAs per SM, which bounds the registers (8192 tokens: 52.7 us against 55.6 with 6).
+constexpr int kCtas = 8;
 
 template <int LAYOUT, bool NORM>
-__global__ void __launch_bounds__(kThreads, min_ctas(LAYOUT, NORM))
+__global__ void __launch_bounds__(kThreads, kCtas)
     rope_kernel(const __grid_constant__ RopeParams p) {
+  constexpr bool kTables = NORM || LAYOUT == kHalfAny;  // see table_at
   __shared__ float s_cos[kHeadDim / 2], s_sin[kHeadDim / 2];
   __shared__ float s_w[NORM ? 2 : 1][kHeadDim];  // norm weights of q and k
-  __shared__ float s_row[LAYOUT == kHalfAny ? kRowsAtOnce : 1][kHeadDim];
+  __shared__ uint32_t s_row[LAYOUT == kHalfAny ? kRowsAtOnce : 1][kRowPitch];
+  // kTables: what multiplies an element and its partner (cos and signed sin, times
+  // the norm weights), of q and of k, by table_at
+  __shared__ __align__(16) float s_own[kTables ? 1 + NORM : 1][kHeadDim];
+  __shared__ __align__(16) float s_other[kTables ? 1 + NORM : 1][kHeadDim];
   griddep_wait();
   griddep_launch_dependents();
   const int64_t n = blockIdx.x;
@@ -137,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, min_ctas(LAYOUT, NORM))
   const int pos = p.positions[n], slot = p.slots[n];
 
   const int step = kRowsAtOnce * gridDim.y;  // rows the token's CTAs take together
-  float2 c[8], s[8];  // cos and signed sin of the lane's elements (see below)
+  float2 c[kTables ? 1 : 8], s[kTables ? 1 : 8];  // cos, sin of the lane's elements
   int64_t cache_row = 0;
   bool store_kv = false;
   // base: the CTA's first row of a batch of kUnroll rows per lane; all the
@@ -180,7 +196,21 @@ __global__ void __launch_bounds__(kThreads, min_ctas(LAYOUT, NORM))
         }
       }
       __syncthreads();
-      if constexpr (LAYOUT == kHalfLanes) {
+      if constexpr (kTables) {
+        static_assert(kThreads == kHeadDim, "an element per thread");
+        constexpr bool kPairs = LAYOUT == kInterleaved;
+        const int e = tid, r2 = R / 2;
+        const int i = e < R ? (kPairs ? e / 2 : (e < r2 ? e : e - r2)) : 0;  // its pair
+        const int other = e < R ? (kPairs ? e ^ 1 : (e < r2 ? e + r2 : e - r2)) : e;
+        const bool first = kPairs ? (e & 1) == 0 : e < r2;
+        for (int kind = 0; kind < 1 + NORM; ++kind) {
+          const bool weighted = NORM && (kind == 0 ? p.wq : p.wk) != nullptr;
+          const float w = weighted ? s_w[kind][e] : 1.f, wo = weighted ? s_w[kind][other] : 1.f;
+          s_own[kind][table_at(e)] = e < R ? s_cos[i] * w : w;
+          s_other[kind][table_at(e)] = (first ? -s_sin[i] : s_sin[i]) * wo;
+        }
+        __syncthreads();
+      } else if constexpr (LAYOUT == kHalfLanes) {
         // c, s [0..3]: of the pairs (ea + j, eb + j), j < 8
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -193,22 +223,9 @@ __global__ void __launch_bounds__(kThreads, min_ctas(LAYOUT, NORM))
         // with its sign (new a = a cos - b sin, new b = b cos + a sin)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const int e = (j < 4 ? ea : eb) + 2 * (j & 3);
-          if constexpr (LAYOUT == kInterleaved) {
-            const int i = e < R ? e / 2 : 0;
-            c[j] = make_float2(s_cos[i], s_cos[i]);
-            s[j] = make_float2(-s_sin[i], s_sin[i]);
-          } else {
-            float cc[2], ss[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int x = e + k, i = x < R / 2 ? x : (x < R ? x - R / 2 : 0);
-              cc[k] = s_cos[i];
-              ss[k] = x < R / 2 ? -s_sin[i] : s_sin[i];
-            }
-            c[j] = make_float2(cc[0], cc[1]);
-            s[j] = make_float2(ss[0], ss[1]);
-          }
+          const int e = (j < 4 ? ea : eb) + 2 * (j & 3), i = e < R ? e / 2 : 0;
+          c[j] = make_float2(s_cos[i], s_cos[i]);
+          s[j] = make_float2(-s_sin[i], s_sin[i]);
         }
       }
     }
@@ -220,6 +237,35 @@ __global__ void __launch_bounds__(kThreads, min_ctas(LAYOUT, NORM))
       float2 x[8];
       unpack(raw[u][0], x);
       unpack(raw[u][1], x + 4);
+      float2 y[kTables ? 8 : 1];  // the partner of each element
+      if constexpr (LAYOUT == kHalfAny) {
+        uint32_t* row = s_row[row_of];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const uint32_t w[4] = {raw[u][q].x, raw[u][q].y, raw[u][q].z, raw[u][q].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int k = (q == 0 ? ea : eb) / 2 + i;
+            if (k < R / 2) row[k] = w[i];
+            if (2 * k < R / 2) row[R / 2 + k] = w[i];
+          }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          // (past the R elements: whatever is there, not used)
+          const int e = (q == 0 ? ea : eb) + R / 2;
+          uint32_t w[5];
+#pragma unroll
+          for (int i = 0; i < 5; ++i) w[i] = row[e / 2 + i];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (e & 1) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+          unpack(make_uint4(w[0], w[1], w[2], w[3]), y + 4 * q);
+        }
+        __syncwarp();
+      }
+      float inv = 1.f;
       if constexpr (NORM) {
         float2 q = mul2(x[0], x[0]);
 #pragma unroll
@@ -228,16 +274,35 @@ __global__ void __launch_bounds__(kThreads, min_ctas(LAYOUT, NORM))
 #pragma unroll
         for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         if (is_q ? p.wq != nullptr : (is_k && p.wk != nullptr)) {
-          const float inv = __frcp_rn(__fsqrt_rn(ss * (1.0f / kHeadDim) + p.eps));
-          const float* w = s_w[is_q ? 0 : 1];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float2 g = *reinterpret_cast<const float2*>(w + (j < 4 ? ea : eb) + 2 * (j & 3));
-            x[j] = mul2(mul2(x[j], make_float2(inv, inv)), g);
-          }
+          // (rsqrtf is within 2 ulp: 2^-22 next to the result's 2^-9)
+          inv = rsqrtf(ss * (1.0f / kHeadDim) + p.eps);
         }
       }
-      if constexpr (LAYOUT == kHalfLanes) {
+      if constexpr (kTables) {
+        if (is_q || is_k) {
+          const int kind = NORM && is_k ? 1 : 0;
+          if constexpr (LAYOUT != kHalfAny) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              y[j] = LAYOUT == kInterleaved ? make_float2(x[j].y, x[j].x) : x[j ^ 4];
+          }
+#pragma unroll
+          for (int j = 0; j < 8; j += 2) {
+            const int e = (j < 4 ? ea : eb) + 2 * (j & 3);
+            const float4 own = *reinterpret_cast<const float4*>(s_own[kind] + table_at(e));
+            const float4 oth = *reinterpret_cast<const float4*>(s_other[kind] + table_at(e));
+            const float2 none = make_float2(-0.f, -0.f);  // (adding it changes nothing)
+            x[j] = fma2(x[j], make_float2(own.x, own.y),
+                        e < R ? mul2(y[j], make_float2(oth.x, oth.y)) : none);
+            x[j + 1] = fma2(x[j + 1], make_float2(own.z, own.w),
+                            e + 2 < R ? mul2(y[j + 1], make_float2(oth.z, oth.w)) : none);
+            if constexpr (NORM) {
+              x[j] = mul2(x[j], make_float2(inv, inv));
+              x[j + 1] = mul2(x[j + 1], make_float2(inv, inv));
+            }
+          }
+        }
+      } else if constexpr (LAYOUT == kHalfLanes) {
         if ((is_q || is_k) && ea < R / 2) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -246,29 +311,12 @@ __global__ void __launch_bounds__(kThreads, min_ctas(LAYOUT, NORM))
             x[j + 4] = fma2(b, c[j], mul2(a, s[j]));
           }
         }
-      } else {
-        float2 y[8];  // the partner of each element
-        if constexpr (LAYOUT == kInterleaved) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) y[j] = make_float2(x[j].y, x[j].x);
-        } else {
-          float* row = s_row[row_of];
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            *reinterpret_cast<float2*>(row + (j < 4 ? ea : eb) + 2 * (j & 3)) = x[j];
-          __syncwarp();
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int e = (j < 4 ? ea : eb) + 2 * (j & 3), f = e + 1;
-            y[j] = make_float2(row[e < R / 2 ? e + R / 2 : (e < R ? e - R / 2 : e)],
-                               row[f < R / 2 ? f + R / 2 : (f < R ? f - R / 2 : f)]);
-          }
-          __syncwarp();
-        }
+      } else if constexpr (LAYOUT == kInterleaved) {
         if (is_q || is_k) {
 #pragma unroll
           for (int j = 0; j < 8; ++j)  // R is even: two neighbours turn or stay together
-            if ((j < 4 ? ea : eb) + 2 * (j & 3) < R) x[j] = fma2(x[j], c[j], mul2(y[j], s[j]));
+            if ((j < 4 ? ea : eb) + 2 * (j & 3) < R)
+              x[j] = fma2(x[j], c[j], mul2(make_float2(x[j].y, x[j].x), s[j]));
         }
       }
       if (is_q) {
@@ -318,7 +366,7 @@ cudaError_t launch_rope(const RopeParams& p, int sm_count, cudaStream_t stream) 
   int64_t want = (4LL * sm_count + p.num_tokens - 1) / p.num_tokens;
   const int most = (rows + kRowsAtOnce - 1) / kRowsAtOnce;
   const int layout = p.interleaved ? kInterleaved : p.rot_dim % 16 == 0 ? kHalfLanes : kHalfAny;
-  const int64_t resident = (int64_t)sm_count * min_ctas(layout, p.wq || p.wk);
+  const int64_t resident = (int64_t)sm_count * kCtas;
   if (p.num_tokens > resident && 2 * p.num_tokens <= 5 * resident && most >= 4) want = 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.num_tokens, (unsigned)(want < most ? want : most));
