@@ -636,7 +636,7 @@ hpc_status hpc_rope_kv_write(const hpc_tensor* q_in, const hpc_tensor* k_in, con
  * device work list, partial states and error word of steps of at most max_seqs
  * (<= 4096) sequences with max_q_len (1 .. 8) new tokens each and num_q_heads
  * query heads, on num_sms CTAs (normally the SM count). All device memory is
- * allocated here: 4.2 KB per (new token, KV head) twice, and 131 KB per CTA.
+ * allocated here: 4.2 KB per (new token, KV head) twice, and 133 KB per CTA.
  * hpc_decode_plan_status and hpc_decode_plan_destroy take it; the other calls
  * refuse it. Calls on one plan must not overlap on the GPU.
  */

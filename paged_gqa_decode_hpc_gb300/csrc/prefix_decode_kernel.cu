@@ -24,8 +24,9 @@
 //    idle between its steps; two chains on alternate tiles fill in for each
 //    other.
 // Own pieces of a single new token have 8 rows only, and a chain through tensor
-// memory costs each tile its full latency (0.65 us a tile and 2.2 us a piece;
-// 64 x 1000 own positions: 52 us). They run as warp pieces: the 8 softmax warps take tiles in
+// memory costs each tile its full latency (as own pieces of several tokens do: about
+// 0.6 us a tile and 3 us a piece). They run as warp pieces, 0.55 us a tile and 0.3 a
+// piece (e4m3 0.32 and 0.7): the 8 softmax warps take tiles in
 // turn, each alone from the ring with mma.sync (8 heads = the N of one
 // instruction; decode_unit.cuh) and fp32 state in registers; e4m3 tiles are read
 // as they are. At the end each warp leaves its state in shared memory (the Q
@@ -48,6 +49,14 @@
 // zeroed in shared memory before the P V product reads them.
 // Every wait is bounded; a timeout sets the error bit, all roles stop issuing,
 // and the CTA drains its copies and MMAs and frees its tensor memory.
+//
+// What bounds it (64 sequences of 32768 shared and 128 .. 2048 own positions, 8 KV
+// heads, bf16: 83 us of a step of 90, 431 MB from memory): a shared tile of two row
+// tiles takes 0.82 us, of which the tensor pipe works 0.7 (S with N = 64 reads Q from
+// shared memory again for every tile: 384 of its cycles where the MMAs need 269) and
+// the softmax 0.6; own tiles take what their loads take, and more loads in flight do
+// not help: five loading threads instead of one (92.8 -> 98.7 us) and tiles asked into
+// L2 ten ahead of the ring (90.4 -> 98.9 us) were both slower.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
