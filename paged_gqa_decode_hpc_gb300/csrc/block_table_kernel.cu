@@ -24,6 +24,8 @@
 // graphs may run side by side. From kAppendSplitTokens tokens on, 8 SMs are
 // too few (index arithmetic: half a million tokens took them 30 us), and the
 // tokens go to CTAs on all SMs, the lengths to a second launch behind them.
+// (256 sequences, one token each: 5.2 us of the GPU's time; 512 sequences and half a
+// million tokens 7.5 us; truncating 1024 sequences 3.6 us.)
 //
 // A call that cannot be met as a whole (too few free blocks, a table or token
 // buffer too small, a bad length) is refused as a whole: every CTA comes to

@@ -15,7 +15,9 @@
 // right to about an ulp for every position below 2^24 (GB300's fp64 rate is
 // no way to get there).
 //
-// What bounds it: HBM, and next to it the instructions that a row costs. Each
+// What bounds it: HBM, and next to it the instructions that a row costs (8192 tokens
+// of 64 + 8 + 8 rows, 336 MB: 52.6 us, 6.38 TB/s; e4m3 cache and queries, half the
+// bytes out, 62: the rounding; 64 tokens 3.3 us: latency). Each
 // element is read and written once, and a token's 64 (cos, sin) pairs are
 // formed once per CTA for all its heads. A CTA is one token; 8 lanes take a
 // row, 16 elements each as two 16-byte chunks chosen so that (half layout, R a
