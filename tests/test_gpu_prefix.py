@@ -289,6 +289,19 @@ def test_captured_steps_follow_the_device_lengths():
             c.check(got)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("prefix,lens,hkv,q_len", [
+    (20000, [20010, 20300], 1, 1),           # a pair's states come from more CTAs than are listed at once
+    (9000, [9003, 9100, 9500], 1, 4),
+    (3000, [3001 + 5 * i for i in range(5)], 4, 1),
+    (700, [701 + i for i in range(29)], 8, 1),  # quarters, halves and whole columns a CTA of the merge
+    (700, [701 + i for i in range(47)], 8, 1),
+    (700, [701 + i for i in range(48)], 8, 1),
+])
+def test_states_of_many_parts(prefix, lens, hkv, q_len, fp8):
+    Case([(prefix, lens)], q_len=q_len, hkv=hkv, fp8=fp8, seed=prefix + len(lens)).check()
+
+
 def test_large_batches():
     rng = np.random.default_rng(15)
     # 4096 sequences in 700 groups, some empty, most of one or two blocks; 8 new tokens of 300 sequences

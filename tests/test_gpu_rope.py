@@ -247,6 +247,31 @@ def test_values_that_are_not_finite_stay_in_their_pair():
     assert q_out[2, 0, 127] == float("-inf")
 
 
+@pytest.mark.parametrize("rot_dim,interleaved", [(44, False), (64, True), (128, False)])
+def test_values_that_are_not_finite_in_every_layout(rot_dim, interleaved):
+    c = Case(3, rot_dim=rot_dim, interleaved=interleaved, seed=12)
+    q, k, v = c.rows(c.qkv)
+    q[1, 2, 6], k[2, 0, 3], v[0, 0, 9] = float("inf"), float("nan"), float("nan")
+    q[0, 4, 127] = float("-inf")
+    q_out, _, caches = c.run()
+    mate = (lambda i: i ^ 1) if interleaved else lambda i: i + rot_dim // 2
+    far = [(0, 4, 127)] + ([(0, 4, 63)] if rot_dim == 128 else [])
+    bad = ~torch.isfinite(q_out)
+    assert sorted(map(tuple, bad.nonzero().tolist())) == sorted([(1, 2, 6), (1, 2, mate(6))] + far)
+    at = [(int(s) // 64, int(s) % 64) for s in c.slots]
+    kept = [[~torch.isfinite(x[b, 0, o]) for b, o in at] for x in caches]
+    assert kept[0][2].nonzero().flatten().tolist() == sorted([3, mate(3)]) and not kept[0][0].any() and not kept[0][1].any()
+    assert kept[1][0].nonzero().flatten().tolist() == [9] and not kept[1][1].any() and not kept[1][2].any()
+
+
+@pytest.mark.parametrize("rot_dim,interleaved", [(96, False), (128, False), (64, True), (90, False), (20, False)])
+@pytest.mark.parametrize("which", [0, 1])
+def test_a_norm_of_q_or_k_only(rot_dim, interleaved, which):
+    c = Case(45, 24, 2, rot_dim=rot_dim, interleaved=interleaved, scaling="ramp", normed=True, seed=rot_dim + which)
+    c.w[which] = None
+    c.check(c.run(in_place=True))
+
+
 def test_agrees_with_the_decode_prologue():
     """One token per sequence, the whole head, no scaling: the fused decode
     prologue computes the same rows (each within its own fp32 error)."""
