@@ -1,6 +1,7 @@
 """Mixed-length paged GQA decode attention for GB300 (sm_103a).
 
-A thin ctypes binding over libhpc_decode.so (see include/hpc_decode.h). Each
+A thin binding over libhpc_decode.so (see include/hpc_decode.h), by ctypes and,
+for the calls of a few microseconds, a small extension module. Each
 function here has the C entry point's name and only marshals arguments:
 torch tensors become `hpc_tensor` descriptors, torch streams become
 cudaStream_t handles. Every step of the computation runs in the library's
@@ -66,6 +67,7 @@ class HpcRope(ctypes.Structure):
 
 
 _lib = None
+_native = None  # the extension module of csrc/binding.cpp, or None
 _lock = threading.Lock()
 
 
@@ -137,8 +139,30 @@ def load_library():
         lib.hpc_decode_plan_destroy.restype = None
         lib.hpc_last_error.argtypes = []
         lib.hpc_last_error.restype = ctypes.c_char_p
+        _load_native(lib)
         _lib = lib
         return lib
+
+
+def _load_native(lib):
+    """The extension module, given the addresses of the entries that it calls."""
+    global _native
+    if not os.path.exists(_build.BINDING_PATH):
+        return
+    try:
+        import torch  # noqa: F401
+    except Exception:  # without torch there are no tensors to pass
+        return
+    import importlib.machinery
+    import importlib.util
+    loader = importlib.machinery.ExtensionFileLoader("hpc_binding", _build.BINDING_PATH)
+    spec = importlib.util.spec_from_file_location("hpc_binding", _build.BINDING_PATH, loader=loader)
+    module = importlib.util.module_from_spec(spec)
+    loader.exec_module(module)
+    module.bind(_dtypes(), *(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        lib.hpc_block_table_append, lib.hpc_block_table_truncate, lib.hpc_rope_kv_write,
+        lib.hpc_decode_prefix_attn)))
+    _native = module
 
 
 def hpc_last_error() -> str:
@@ -179,12 +203,16 @@ def _current_stream() -> int:
     return _raw_stream()
 
 
-def _stream_ptr(stream) -> ctypes.c_void_p:
+def _stream_handle(stream) -> int:
     if stream is None:
-        return ctypes.c_void_p(_current_stream())
+        return _current_stream()
     if hasattr(stream, "cuda_stream"):
         stream = stream.cuda_stream
-    return ctypes.c_void_p(int(stream))
+    return int(stream)
+
+
+def _stream_ptr(stream) -> ctypes.c_void_p:
+    return ctypes.c_void_p(_stream_handle(stream))
 
 
 class Plan:
@@ -336,14 +364,18 @@ def hpc_device_sm_count() -> int:
 _DTYPES = None
 
 
-def _dtype_code(t) -> int:
+def _dtypes() -> dict:
     global _DTYPES
     if _DTYPES is None:
         import torch
         _DTYPES = {torch.bfloat16: HPC_BF16, torch.uint8: HPC_FP8_E4M3,
                    torch.float8_e4m3fn: HPC_FP8_E4M3, torch.float32: HPC_F32,
                    torch.int32: HPC_I32}
-    code = _DTYPES.get(t.dtype)
+    return _DTYPES
+
+
+def _dtype_code(t) -> int:
+    code = (_DTYPES or _dtypes()).get(t.dtype)
     if code is None:
         raise HpcError(HPC_ERR_INVALID_ARG, f"unsupported tensor dtype {t.dtype}")
     return code
@@ -511,7 +543,14 @@ def hpc_block_table_append(seq_lens, new_lens, free_blocks, free_count, num_bloc
     from the top of the stack free_blocks[:free_count]. All int32 CUDA tensors;
     seq_lens_out / free_count_out may be seq_lens / free_count (in place).
     positions and slots are padded with 0 and -1 past the last new token."""
-    _check(load_library().hpc_block_table_append(
+    lib = _lib or load_library()
+    if _native is not None:
+        status = _native.append(seq_lens, new_lens, free_blocks, free_count, num_blocks, block_table,
+                                seq_lens_out, cu_q_lens, positions, slots, free_count_out,
+                                device_error, _stream_handle(stream))
+        if status is not None:
+            return _check(status)
+    _check(lib.hpc_block_table_append(
         _desc(seq_lens), _desc(new_lens), _desc(free_blocks),
         _desc(free_count), int(num_blocks), _desc(block_table),
         _desc(seq_lens_out), _desc(cu_q_lens),
@@ -525,7 +564,13 @@ def hpc_block_table_truncate(seq_lens, to_lens, block_table, num_blocks: int, fr
     """Shorten every sequence to min(seq_lens[b], to_lens[b]) tokens and push the
     blocks behind it on the stack free_blocks[:free_count] (0 releases a
     finished sequence); undoes hpc_block_table_append exactly."""
-    _check(load_library().hpc_block_table_truncate(
+    lib = _lib or load_library()
+    if _native is not None:
+        status = _native.truncate(seq_lens, to_lens, block_table, num_blocks, free_blocks, free_count,
+                                  seq_lens_out, free_count_out, device_error, _stream_handle(stream))
+        if status is not None:
+            return _check(status)
+    _check(lib.hpc_block_table_truncate(
         _desc(seq_lens), _desc(to_lens), _desc(block_table),
         int(num_blocks), _desc(free_blocks), _desc(free_count),
         _desc(seq_lens_out), _desc(free_count_out),
@@ -557,7 +602,15 @@ def hpc_rope_kv_write(q_in, k_in, v_in, positions, slots, rope: HpcRope, q_out, 
     """Rotary positions (and QK-norm where weights are given) of N tokens of any
     sequences, and the write of their K and V rows into the paged cache at
     `slots` (int32 [N], < 0: padding, skipped); `rope` from hpc_rope_init."""
-    _check(load_library().hpc_rope_kv_write(
+    lib = _lib or load_library()
+    if _native is not None and isinstance(rope, HpcRope):
+        status = _native.rope_kv_write(q_in, k_in, v_in, positions, slots, rope, q_norm_weight,
+                                       k_norm_weight, eps, q_out, q_out_fp8, q_fp8_scale, k_cache,
+                                       k_scale, v_cache, v_scale, device_error,
+                                       _stream_handle(stream))
+        if status is not None:
+            return _check(status)
+    _check(lib.hpc_rope_kv_write(
         _desc(q_in), _desc(k_in), _desc(v_in), _desc(positions), _desc(slots), rope,
         _desc(q_norm_weight), _desc(k_norm_weight), eps, _desc(q_out),
         _desc(q_out_fp8, q_fp8_scale), _desc(k_cache, k_scale), _desc(v_cache, v_scale),
@@ -580,7 +633,16 @@ def hpc_decode_prefix_attn(q, k_cache, v_cache, block_table, seq_lens, prefix_le
     sequences cu_groups[g] .. cu_groups[g + 1] - 1 (None: one group), which hold
     the same first prefix_lens[g] positions; their shared blocks are read once.
     q, out, lse and the caches as for hpc_decode_step (q_len 1 to 8)."""
-    _check(load_library().hpc_decode_prefix_attn(
+    lib = _lib or load_library()
+    if _native is not None:
+        handle = plan.handle
+        status = _native.prefix_attn(q, k_cache, k_scale, v_cache, v_scale, block_table, seq_lens,
+                                     cu_groups, prefix_lens, handle.value if handle else None, out, lse,
+                                     -1.0 if softmax_scale is None else softmax_scale,
+                                     _stream_handle(stream))
+        if status is not None:
+            return _check(status)
+    _check(lib.hpc_decode_prefix_attn(
         _desc(q), _desc(k_cache, k_scale), _desc(v_cache, v_scale), _desc(block_table),
         _desc(seq_lens), _desc(cu_groups), _desc(prefix_lens), plan.handle, _desc(out), _desc(lse),
         -1.0 if softmax_scale is None else softmax_scale, _stream_ptr(stream)))

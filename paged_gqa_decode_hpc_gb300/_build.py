@@ -10,6 +10,8 @@ import glob
 import os
 import shutil
 import subprocess
+import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +21,9 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB_NAME = "libhpc_decode.so"
 LIB_PATH = os.path.join(OUT_DIR, LIB_NAME)
+# the Python binding's fast calls; left out where Python's headers are missing
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING_PATH = os.path.join(OUT_DIR, f"hpc_binding.{sys.implementation.cache_tag}.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -33,13 +38,18 @@ def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def _python_include():
+    path = sysconfig.get_path("include")
+    return path if path and os.path.exists(os.path.join(path, "Python.h")) else None
+
+
 def _inputs():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + \
+    return _sources() + [BINDING_SRC] + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + \
         glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
 
 
 def is_stale() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or (_python_include() and not os.path.exists(BINDING_PATH)):
         return True
     t = os.path.getmtime(LIB_PATH)
     return any(os.path.getmtime(f) > t for f in _inputs())
@@ -72,6 +82,14 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
 
     with ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
         objs = list(ex.map(compile_one, srcs))
+    if _python_include():
+        tmp = BINDING_PATH + f".tmp{os.getpid()}"
+        cmd = [cc, "-O2", "-std=c++17", "-shared", "-cudart", "none", "-Xcompiler", "-fPIC",
+               "-I", INCLUDE, "-I", _python_include(), BINDING_SRC, "-o", tmp]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"nvcc failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, BINDING_PATH)
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "shared"]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -145,10 +145,11 @@ hpc_status hpc_decode_prefix_attn(const hpc_tensor* q, const hpc_tensor* k_cache
     CUtensorMap tq16, tqt, tk, tv;
     const int64_t hs = q->stride[q->ndim - 2];
     if ((st = make_pair_map(q, B * T, pair_stride, hs, Hq, kPrefixTilePairs, &tq16)) != HPC_OK ||
-        (st = make_pair_map(q, B * T, pair_stride, hs, Hq, (int)T, &tqt)) != HPC_OK ||
+        (T > 1 && (st = make_pair_map(q, B * T, pair_stride, hs, Hq, (int)T, &tqt)) != HPC_OK) ||
         (st = make_kv_map(k_cache, fp8, swap, &tk)) != HPC_OK ||
         (st = make_kv_map(v_cache, fp8, swap, &tv)) != HPC_OK)
       return st;
+    if (T == 1) tqt = tq16;  // own rows of single tokens are read without a map
     PrefixLayout L;
     L.cap_seqs = plan->max_seqs;
     L.cap_q_len = plan->prefix_q_len;
