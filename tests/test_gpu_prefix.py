@@ -294,12 +294,21 @@ def test_captured_steps_follow_the_device_lengths():
     (20000, [20010, 20300], 1, 1),           # a pair's states come from more CTAs than are listed at once
     (9000, [9003, 9100, 9500], 1, 4),
     (3000, [3001 + 5 * i for i in range(5)], 4, 1),
-    (700, [701 + i for i in range(29)], 8, 1),  # quarters, halves and whole columns a CTA of the merge
+    (700, [701 + i for i in range(9)], 8, 1),   # eighths, quarters, halves and whole columns a CTA of the merge
+    (700, [701 + i for i in range(13)], 8, 1),
+    (700, [701 + i for i in range(18)], 8, 1),
+    (700, [701 + i for i in range(29)], 8, 1),
     (700, [701 + i for i in range(47)], 8, 1),
     (700, [701 + i for i in range(48)], 8, 1),
 ])
 def test_states_of_many_parts(prefix, lens, hkv, q_len, fp8):
     Case([(prefix, lens)], q_len=q_len, hkv=hkv, fp8=fp8, seed=prefix + len(lens)).check()
+
+
+@pytest.mark.parametrize("seqs,hkv", [(2, 1), (100, 2)])
+def test_more_parts_than_the_device_has_sms(seqs, hkv):
+    # states past those that a CTA of the merge lists beforehand (320 for few pairs, 64 for many)
+    Case([(44000, [44001 + 3 * i for i in range(seqs)])], hkv=hkv, seed=44).check(sms=900)
 
 
 def test_large_batches():
