@@ -177,7 +177,7 @@ def test_fp8(interleaved, rot_dim, normed):
     c.check(c.run())
 
 
-@pytest.mark.parametrize("scale", [4.0 / 448, 1.0 / 112, 0.01, 1.0, 0.25, 3.0, 1.0 / 3, 0.0117, 700.0, 2.0 ** -40])
+@pytest.mark.parametrize("scale", [4.0 / 448, 1.0 / 112, 0.01, 1.0, 0.25, 3.0, 1.0 / 3, 0.0117, 700.0, 2.0 ** -40, 3e37, 1e-37])
 def test_e4m3_rounds_the_exact_quotient(scale):
     """Every finite bf16 magnitude around the e4m3 range, ties included: each byte is the nearest one."""
     codes = torch.arange(0, 0x7F80).to(torch.int16).view(torch.bfloat16)
