@@ -43,7 +43,7 @@
 // unrounded probabilities.
 // E4m3 caches run the MMAs in fp16: every e4m3 value is an f16 value, and each
 // query row is converted in place with a power-of-two scale putting its largest
-// |q| in [2^14, 2^15).
+// |q| in [2^14, 2^15), and the sign of the K scale.
 // Slots of a sequence's last block behind its end may hold anything (NaN in V
 // would pass 0 * NaN into O): their scores are masked, and their V rows are
 // zeroed in shared memory before the P V product reads them.
@@ -57,6 +57,8 @@
 // the softmax 0.6; own tiles take what their loads take, and more loads in flight do
 // not help: five loading threads instead of one (92.8 -> 98.7 us) and tiles asked into
 // L2 ten ahead of the ring (90.4 -> 98.9 us) were both slower.
+#include <cfloat>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -965,7 +967,9 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
               e2 = 14 - ((int)((__float_as_uint(mq) >> 23) & 0xFF) - 127);
               e2 = e2 < -100 ? -100 : (e2 > 100 ? 100 : e2);
             }
-            const float qs = __uint_as_float((uint32_t)(127 + e2) << 23);
+            // a negative scale turns Q around, so that the scores' factor is positive
+            const float qs = __uint_as_float(((uint32_t)(127 + e2) << 23) |
+                                             (__float_as_uint(p.score_scale_log2) & 0x80000000u));
             s_exp[(2 * g + ((g == 0 ? uses[0] : uses[1]) & 1)) * kRows + r] = (int8_t)e2;
 #pragma unroll 4
             for (int i = 0; i < 16; ++i) {
@@ -1000,8 +1004,12 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         // S is there, so the Q rows were converted: their scale comes back out
+        // (a factor of 0 would make NaN of masked scores: the least normal number
+        // times any score, below 2^31, is 0 to every exponential)
         if (FP8 && i == 0 && row_ok)
-          sc *= __uint_as_float((uint32_t)(127 - s_exp[(2 * my_slot + (fill & 1)) * kRows + r]) << 23);
+          sc = fmaxf(fabsf(sc) * __uint_as_float(
+                                     (uint32_t)(127 - s_exp[(2 * my_slot + (fill & 1)) * kRows + r]) << 23),
+                     FLT_MIN);
         // the state that this pipeline's first P V of the piece overwrites has
         // been joined into warpgroup 0's
         if (g == 1 && i == 0 && joins > 0) {
