@@ -61,8 +61,9 @@ typedef enum {
 /*
  * Strided tensor descriptor. `shape`/`stride` hold `ndim` entries (outermost
  * first); strides are in elements. `scale` is the per-tensor dequantisation
- * scale of an FP8 K or V cache (value = e4m3(byte) * scale); it is ignored for
- * every other tensor.
+ * scale of an FP8 K or V cache (value = e4m3(byte) * scale): any finite value
+ * where the cache is read, a positive one where it is written. It is ignored
+ * for every other tensor but an e4m3 q_out_fp8.
  */
 typedef struct {
   void* data;

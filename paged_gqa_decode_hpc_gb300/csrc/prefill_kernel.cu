@@ -44,6 +44,8 @@
 //  * Every wait is bounded (globaltimer); a timeout sets the error bit, all
 //    roles stop issuing, and the CTA drains its copies and MMAs and frees its
 //    tensor memory before leaving. No trap, no assert.
+#include <cfloat>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -638,7 +640,9 @@ __global__ void __launch_bounds__(Layout<QT, FP8>::kThreads, 1)
           e2 = 14 - ((int)((__float_as_uint(mx) >> 23) & 0xFF) - 127);
           e2 = e2 < -100 ? -100 : (e2 > 100 ? 100 : e2);
         }
-        const float qs = __uint_as_float((uint32_t)(127 + e2) << 23);
+        // a negative K scale turns Q around, so that the scores' factor is positive
+        const float qs = __uint_as_float(((uint32_t)(127 + e2) << 23) |
+                                         (__float_as_uint(p.score_scale_log2) & 0x80000000u));
         qinv = __uint_as_float((uint32_t)(127 - e2) << 23);
 #pragma unroll 4
         for (int i = 0; i < 16; ++i) {
@@ -658,7 +662,9 @@ __global__ void __launch_bounds__(Layout<QT, FP8>::kThreads, 1)
       }
       mbar_arrive(q_ready(g));
     }
-    const float sc = p.score_scale_log2 * qinv;
+    // (a factor of 0 would make NaN of masked scores: the least normal number times
+    // any score of an e4m3 K, below 2^31, is 0 to every exponential)
+    const float sc = FP8 ? fmaxf(fabsf(p.score_scale_log2) * qinv, FLT_MIN) : p.score_scale_log2;
     float m = -INFINITY, l = 0.f;
     for (int j = 0; ok && j < nk; ++j) {
       ok = __all_sync(0xffffffffu, wait_bar(s_full(g), j & 1, s_abort, err, lim_ns));
