@@ -608,8 +608,10 @@ hpc_status hpc_rope_init(hpc_rope* rope, int32_t rot_dim, int32_t interleaved, d
  *   q_in [N][H_q][128], k_in / v_in [N][H_kv][128], q_out [N][H_q][128]: device
  *       bf16, rows contiguous, other strides multiples of 8 elements, bases
  *       16-byte aligned (slices of one projection's output pass as views);
- *       q_out may be q_in itself (the same strides), and must not overlap it
- *       otherwise
+ *       q_out may be q_in itself (the same strides). Otherwise no row of q_out
+ *       or q_out_fp8 may share bytes with another one, with a row of q_in, k_in
+ *       or v_in, or with each other's; where strides differ, byte ranges
+ *       decide. Nor may their byte ranges meet a cache's (HPC_ERR_INVALID_ARG)
  *   positions, slots  device int32 [N]. slots[n] < 0 marks padding: nothing is
  *       written for the token. A position outside [0, 2^24) sets
  *       HPC_DEVCHK_BAD_LENGTH and skips the token; a slot past the cache sets

@@ -58,6 +58,53 @@ bool overlap(const hpc_tensor* a, const hpc_tensor* b) {
   return x < end(b) && y < end(a);
 }
 
+// Rows [tokens][heads] of a fixed number of bytes, strides in bytes.
+struct Rows {
+  const char* p;
+  int64_t n, h, sn, sh, row;
+  Rows(const hpc_tensor* t, int64_t elt)
+      : p((const char*)t->data), n(t->shape[0]), h(t->shape[1]), sn(t->stride[0] * elt),
+        sh(t->stride[1] * elt), row(kHeadDim * elt) {}
+  const char* end() const { return p + (n - 1) * sn + (h - 1) * sh + row; }
+};
+
+int64_t floor_div(int64_t a, int64_t b) { return a / b - (a % b != 0 && (a < 0) != (b < 0)); }
+
+// Whether a row of `a` shares bytes with one of `b` (itself: with another one of its
+// rows). Exact for equal strides, as views of one buffer have them. With unequal
+// token strides byte ranges that meet count as overlapping, with unequal head
+// strides the ranges of a token's rows.
+bool rows_overlap(Rows a, Rows b, bool itself = false) {
+  if (a.n == 0 || b.n == 0 || a.end() <= b.p || b.end() <= a.p) return false;
+  if (a.n == 1) a.sn = b.sn;  // a stride that no row is reached by
+  if (b.n == 1) b.sn = a.sn;
+  if (a.h == 1) a.sh = b.sh;
+  if (b.h == 1) b.sh = a.sh;
+  if (a.n == 1 && b.n == 1) a.sn = b.sn = 0;
+  if (a.h == 1 && b.h == 1) a.sh = b.sh = 0;
+  if (a.sn != b.sn) return true;
+  const int64_t sn = a.sn, d = b.p - a.p;
+  const int64_t ea = (a.h - 1) * a.sh + a.row, eb = (b.h - 1) * b.sh + b.row;  // a token's extent
+  if (itself) {
+    if ((a.h == 1 || a.sh >= a.row) && (a.n == 1 || sn >= ea)) return false;
+  } else if (sn > 0) {
+    const int64_t at = d - floor_div(d, sn) * sn;  // b's tokens behind a's, modulo the stride
+    if (ea <= at && at + eb <= sn) return false;
+  }
+  if (a.sh != b.sh) return true;
+  const int64_t sh = a.sh;
+  // row (n, h) of a and (n + i, h + j) of b are d + i sn + j sh bytes apart
+  for (int64_t j = -(a.h - 1); j < b.h; ++j) {
+    const int64_t x = d + j * sh;
+    int64_t lo = -(a.n - 1);
+    if (sn > 0) lo = std::max(lo, floor_div(-b.row - x, sn) + 1);  // the first with x + i sn > -b.row
+    if (itself && j == 0 && lo == 0) ++lo;
+    for (int64_t i = lo; i < b.n && x + i * sn < a.row; ++i)
+      if (x + i * sn > -b.row && !(itself && i == 0 && j == 0)) return true;
+  }
+  return false;
+}
+
 // What append and truncate have in common: the lengths, the table and the
 // stack of free blocks.
 hpc_status check_pool(const hpc_tensor* seq_lens, const hpc_tensor* other, const char* other_name,
@@ -299,10 +346,16 @@ hpc_status hpc_rope_kv_write(const hpc_tensor* q_in, const hpc_tensor* k_in, con
     if (Hq > 65536 || Hkv > 65536) return fail(HPC_ERR_UNSUPPORTED, "at most 65536 heads");
     // q may be rotated in place, rows on their own rows; anything else would
     // read what another CTA has written
-    if (N > 0 && q_out->data == q_in->data &&
-        ((N > 1 && q_out->stride[0] != q_in->stride[0]) ||
-         (Hq > 1 && q_out->stride[1] != q_in->stride[1])))
-      return fail(HPC_ERR_INVALID_ARG, "q_out on q_in must have q_in's strides");
+    const bool in_place = q_out->data == q_in->data &&
+                          (N <= 1 || q_out->stride[0] == q_in->stride[0]) &&
+                          (Hq == 1 || q_out->stride[1] == q_in->stride[1]);
+    const Rows out_rows(q_out, 2);
+    if (rows_overlap(out_rows, out_rows, true))
+      return fail(HPC_ERR_INVALID_ARG, "rows of q_out overlap");
+    if (!in_place && rows_overlap(out_rows, Rows(q_in, 2)))
+      return fail(HPC_ERR_INVALID_ARG, "q_out overlaps q_in other than in place (its rows and strides)");
+    if (rows_overlap(out_rows, Rows(k_in, 2)) || rows_overlap(out_rows, Rows(v_in, 2)))
+      return fail(HPC_ERR_INVALID_ARG, "q_out overlaps k_in or v_in");
     if (has_qf && (q_out_fp8->dtype != HPC_FP8_E4M3 || q_out_fp8->ndim != 3 ||
                    q_out_fp8->shape[0] != N || q_out_fp8->shape[1] != Hq ||
                    q_out_fp8->shape[2] != kHeadDim || q_out_fp8->stride[2] != 1 ||
@@ -311,6 +364,14 @@ hpc_status hpc_rope_kv_write(const hpc_tensor* q_in, const hpc_tensor* k_in, con
                    !aligned(q_out_fp8->data, 8) || !(q_out_fp8->scale > 0.f) ||
                    !std::isfinite(q_out_fp8->scale)))
       return fail(HPC_ERR_INVALID_ARG, "q_out_fp8 must be e4m3 [N][H_q][128] with a positive scale");
+    if (has_qf) {
+      const Rows fp8_rows(q_out_fp8, 1);
+      if (rows_overlap(fp8_rows, fp8_rows, true))
+        return fail(HPC_ERR_INVALID_ARG, "rows of q_out_fp8 overlap");
+      for (const hpc_tensor* t : rows)
+        if (rows_overlap(fp8_rows, Rows(t, 2)))
+          return fail(HPC_ERR_INVALID_ARG, "q_out_fp8 overlaps q_in, k_in, v_in or q_out");
+    }
     for (const hpc_tensor* w : {q_norm_weight, k_norm_weight})
       if (w && w->data && ((w->dtype != HPC_BF16 && w->dtype != HPC_F32) ||
                            w->shape[0] != kHeadDim || w->stride[0] != 1 || !aligned(w->data, 16)))
@@ -333,6 +394,15 @@ hpc_status hpc_rope_kv_write(const hpc_tensor* q_in, const hpc_tensor* k_in, con
                 !std::isfinite(k_cache->scale) || !std::isfinite(v_cache->scale)))
       return fail(HPC_ERR_INVALID_ARG, "FP8 caches need positive finite scales");
     if (N == 0) return HPC_OK;
+    for (const hpc_tensor* c : {k_cache, v_cache}) {
+      int64_t last = kHeadDim - 1;
+      for (int i = 0; i < 3; ++i) last += std::max<int64_t>(c->shape[i] - 1, 0) * c->stride[i];
+      const char* begin = (const char*)c->data;
+      const char* end = begin + (last + 1) * (fp8 ? 1 : 2);
+      auto inside = [&](const Rows& r) { return r.p < end && begin < r.end(); };
+      if (inside(out_rows) || (has_qf && inside(Rows(q_out_fp8, 1))))
+        return fail(HPC_ERR_INVALID_ARG, "q_out or q_out_fp8 overlaps a cache");
+    }
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
