@@ -147,7 +147,7 @@ def load_library():
 def _load_native(lib):
     """The extension module, given the addresses of the entries that it calls."""
     global _native
-    if not os.path.exists(_build.BINDING_PATH):
+    if _build.binding_is_stale():  # missing, or of another interface
         return
     try:
         import torch  # noqa: F401

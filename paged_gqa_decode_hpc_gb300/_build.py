@@ -43,16 +43,31 @@ def _python_include():
     return path if path and os.path.exists(os.path.join(path, "Python.h")) else None
 
 
+def _headers():
+    return glob.glob(os.path.join(INCLUDE, "*.h"))
+
+
 def _inputs():
-    return _sources() + [BINDING_SRC] + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + \
-        glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
+    return _sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + \
+        _headers() + [os.path.abspath(__file__)]
+
+
+def _older(path, inputs) -> bool:
+    """Whether the built file is missing or older than something it is made of."""
+    if not os.path.exists(path):
+        return True
+    t = os.path.getmtime(path)
+    return any(os.path.getmtime(f) > t for f in inputs)
+
+
+def binding_is_stale() -> bool:
+    """The extension module calls the library by the descriptors and signatures it was compiled
+    with: one older than them (another interpreter's, which rebuilt the library only) is not used."""
+    return _older(BINDING_PATH, [BINDING_SRC, os.path.abspath(__file__)] + _headers())
 
 
 def is_stale() -> bool:
-    if not os.path.exists(LIB_PATH) or (_python_include() and not os.path.exists(BINDING_PATH)):
-        return True
-    t = os.path.getmtime(LIB_PATH)
-    return any(os.path.getmtime(f) > t for f in _inputs())
+    return _older(LIB_PATH, _inputs()) or (_python_include() is not None and binding_is_stale())
 
 
 def common_flags():
@@ -60,12 +75,30 @@ def common_flags():
                    "-I", INCLUDE, "-I", CSRC]
 
 
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what}:\n{r.stdout}\n{r.stderr}")
+    return r.stdout + r.stderr
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile and link; returns the library path."""
+    """Compile and link what is stale; returns the library path."""
     if not force and not is_stale():
         return LIB_PATH
     os.makedirs(OUT_DIR, exist_ok=True)
     cc = nvcc()
+    if force or _older(LIB_PATH, _inputs()):
+        _build_library(cc, verbose, extra_flags)
+    if _python_include() and (force or binding_is_stale()):
+        tmp = BINDING_PATH + f".tmp{os.getpid()}"
+        _run([cc, "-O2", "-std=c++17", "-shared", "-cudart", "none", "-Xcompiler", "-fPIC",
+              "-I", INCLUDE, "-I", _python_include(), BINDING_SRC, "-o", tmp], f"nvcc failed on {BINDING_SRC}")
+        os.replace(tmp, BINDING_PATH)
+    return LIB_PATH
+
+
+def _build_library(cc: str, verbose: bool, extra_flags):
     srcs = _sources()
 
     def compile_one(src):
@@ -73,30 +106,16 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         cmd = [cc, *common_flags(), *extra_flags, "-c", src, "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
-        if verbose and (r.stdout or r.stderr):
-            print(r.stdout + r.stderr, flush=True)
+        said = _run(cmd, f"nvcc failed on {src}")
+        if verbose and said:
+            print(said, flush=True)
         return obj
 
     with ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
         objs = list(ex.map(compile_one, srcs))
-    if _python_include():
-        tmp = BINDING_PATH + f".tmp{os.getpid()}"
-        cmd = [cc, "-O2", "-std=c++17", "-shared", "-cudart", "none", "-Xcompiler", "-fPIC",
-               "-I", INCLUDE, "-I", _python_include(), BINDING_SRC, "-o", tmp]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
-        os.replace(tmp, BINDING_PATH)
     tmp = LIB_PATH + f".tmp{os.getpid()}"
-    cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "shared"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _run([cc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "shared"], "link failed")
     os.replace(tmp, LIB_PATH)
-    return LIB_PATH
 
 
 if __name__ == "__main__":
