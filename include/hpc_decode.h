@@ -659,8 +659,8 @@ hpc_status hpc_decode_prefix_plan_create(int32_t max_seqs, int32_t max_q_len, in
  * nothing. Runs on the tcgen05 tensor cores in three launches (plan, attention,
  * merge), planned from the device lengths.
  *   q, k_cache, v_cache, block_table, seq_lens, out, lse: as hpc_decode_step
- *       (q_len 1 .. 8), with q's tokens evenly spaced (stride 0 = q_len *
- *       stride 1)
+ *       (q_len 1 .. 8), with q's tokens evenly spaced (for q_len > 1, stride 0
+ *       = q_len * stride 1)
  *   cu_groups    device int32 [G + 1], 0 = cu_groups[0] <= ... <= cu_groups[G]
  *                = B (else HPC_DEVCHK_BAD_LENGTH and nothing is shared), or NULL:
  *                one group

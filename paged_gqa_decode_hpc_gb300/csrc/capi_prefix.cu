@@ -121,8 +121,8 @@ hpc_status hpc_decode_prefix_attn(const hpc_tensor* q, const hpc_tensor* k_cache
     if (cu_groups && (st = check_ints(cu_groups, "cu_groups", G + 1)) != HPC_OK) return st;
     if (!cu_groups && G != 1)
       return fail(HPC_ERR_INVALID_ARG, "without cu_groups prefix_lens holds one length");
-    const int64_t pair_stride = multi ? q->stride[1] : q->stride[0];
-    if (multi && B > 1 && q->stride[0] != T * q->stride[1])
+    const int64_t pair_stride = T > 1 ? q->stride[1] : q->stride[0];  // (token to token)
+    if (T > 1 && B > 1 && q->stride[0] != T * q->stride[1])
       return fail(HPC_ERR_INVALID_ARG, "q's tokens must be evenly spaced over the batch "
                                        "(stride 0 = q_len * stride 1)");
     if (!(softmax_scale <= 0.f) && !std::isfinite(softmax_scale))

@@ -24,3 +24,15 @@ def test_e4m3_scales_that_are_not_positive(k_scale, q_len):
              fp8=True, seed=q_len, q_scale=4.0)
     c.scales = (k_scale, 0.17)
     c.check()
+
+
+def test_one_token_of_a_wider_batch():
+    # q [B][1][H_q][128] whose sequences lie more than a token apart: evenly spaced all the same
+    c = Case([(128, [200, 190, 130]), (0, [70])], seed=4)
+    d, n = c.device(), len(c.lens)
+    wide = torch.full((n, 4, 16, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+    out, lse = (torch.full(s, 5.0, dtype=t, device="cuda") for s, t in (((n, 2, 16, 128), torch.bfloat16), ((n, 3, 16), torch.float32)))
+    d["q"] = wide[:, 2:3].copy_(d["q"][:, None])
+    c.run(d, out=out[:, :1], lse=lse[:, 1:2])
+    c.check((out[:, 0], lse[:, 1]))
+    assert (out[:, 1] == 5).all() and (lse[:, ::2] == 5).all()
