@@ -1033,7 +1033,7 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
           tmem_ld32(ts, *reinterpret_cast<float(*)[32]>(&s[0]));
           tmem_ld32(ts + 32, *reinterpret_cast<float(*)[32]>(&s[32]));
           tmem_wait_ld();
-          if (kv0 + 64 > lim) {
+          if (kv0 > lim - 64) {  // (kv0 + 64 may pass int32)
 #pragma unroll
             for (int q = 0; q < 64; ++q)
               if (kv0 + q >= lim) s[q] = -INFINITY;

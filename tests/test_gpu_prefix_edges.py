@@ -1,5 +1,7 @@
 """hpc_decode_prefix_attn at the ends of what its contract allows, against the fp64 decode oracle; inputs and
 tolerances as in test_gpu_prefix.py, which derives them."""
+import math
+
 import pytest
 import torch
 
@@ -36,3 +38,32 @@ def test_one_token_of_a_wider_batch():
     c.run(d, out=out[:, :1], lse=lse[:, 1:2])
     c.check((out[:, 0], lse[:, 1]))
     assert (out[:, 1] == 5).all() and (lse[:, ::2] == 5).all()
+
+
+@pytest.mark.parametrize("q_len", [1, 2])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_the_longest_sequence(fp8, q_len):
+    """2^31 - 1 positions, all but the last 63 of them in one block: scores 0, V of -1, 0 and 1, so that the sums of a
+    CTA, below 2^24, are exact. Of the last block slot 63 is behind the end (its K is NaN), and slot 62 hidden from the
+    first of two new tokens. The merge rounds 2^31 and its like to 24 bits, a few times."""
+    n, tiles = 2 ** 31 - 1, 2 ** 25
+    g = torch.Generator().manual_seed(1)
+    k, v = torch.zeros(2, 1, 64, 128), torch.zeros(2, 1, 64, 128)
+    v[0] = torch.randint(-1, 2, (1, 64, 128), generator=g)
+    k[1, 0, 63] = v[1, 0, 63] = float("nan")
+    k, v = (x.cuda().to(torch.float8_e4m3fn if fp8 else torch.bfloat16) for x in (k, v))
+    table = torch.zeros(1, tiles, dtype=torch.int32, device="cuda")
+    table[0, -1] = 1
+    shape = (1, 8, 128) if q_len == 1 else (1, q_len, 8, 128)
+    q = torch.zeros(shape, dtype=torch.bfloat16, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty(shape[:-1], device="cuda")
+    i32 = lambda x: torch.tensor([x], dtype=torch.int32, device="cuda")
+    plan = hpc.hpc_decode_prefix_plan_create(1, q_len, hpc.hpc_device_sm_count(), 8)
+    hpc.hpc_decode_prefix_attn(q, k, v, table, i32(n), i32(0), plan, out, lse)
+    assert hpc.hpc_decode_plan_status(plan) == 0
+    total = v[0, 0].double().sum(0) * (tiles - 1)
+    for t in range(q_len):
+        ref = total / (n - (q_len - 1 - t))
+        got = out.view(q_len, 8, 128)[t].double()
+        assert ((got - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -20).all()
+        assert ((lse.view(q_len, 8)[t].double() - math.log(n)).abs() <= 2.0 ** -18).all()
