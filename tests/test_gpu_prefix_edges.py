@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import paged_gqa_decode_hpc_gb300 as hpc
-from tests.test_gpu_prefix import Case
+from tests.test_gpu_prefix import SHAPES, Case
 
 pytestmark = pytest.mark.gpu
 
@@ -67,3 +67,45 @@ def test_the_longest_sequence(fp8, q_len):
         got = out.view(q_len, 8, 128)[t].double()
         assert ((got - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -20).all()
         assert ((lse.view(q_len, 8)[t].double() - math.log(n)).abs() <= 2.0 ** -18).all()
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_different_steps_queued_on_one_plan(captured):
+    """Steps of different sizes, types and prefixes one after the other on one plan, nothing waited for in between (or
+    one graph of them all, replayed): each has the bits that it has alone."""
+    plan = hpc.hpc_decode_prefix_plan_create(80, 4, 152, 64)
+    steps = []
+    for name, hkv, q_len, fp8 in (("three tiles", 8, 1, False), ("two", 1, 4, True), ("groups", 2, 3, False), ("long", 1, 1, False),
+                                  ("one sequence", 8, 1, True), ("short and empty", 4, 2, False), ("33 pairs", 2, 1, True),
+                                  ("no prefix", 1, 1, False), ("long", 8, 2, True), ("17 pairs", 1, 1, False)):
+        groups = [(p, [n + (q_len if n else 0) for n in lens]) for p, lens in SHAPES[name]]
+        c = Case(groups, hkv=hkv, q_len=q_len, fp8=fp8, seed=21)
+        d = c.device()
+        alone = c.run(d, plan=plan)
+        c.check(alone)
+        steps.append((c, d, alone, [torch.empty_like(x) for x in alone]))
+
+    def queue(order):
+        for i in order:
+            c, d, _, (out, lse) = steps[i]
+            hpc.hpc_decode_prefix_attn(d["q"], d["k"], d["v"], d["bt"], d["sl"], d["pl"], plan, out, lse, cu_groups=d["cu"],
+                                       k_scale=c.scales[0], v_scale=c.scales[1])
+    orders = [torch.randperm(len(steps), generator=torch.Generator().manual_seed(i)).tolist() for i in range(30)]
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for order in orders:
+                queue(order)
+    for _ in range(10 if captured else 1):
+        for _, _, _, got in steps:
+            for x in got:
+                x.fill_(float("nan"))
+        torch.cuda.synchronize()
+        if captured:
+            graph.replay()
+        else:
+            for order in orders:
+                queue(order)
+        assert hpc.hpc_decode_plan_status(plan) == 0
+        for _, _, alone, got in steps:
+            assert all(torch.equal(a, b) for a, b in zip(alone, got))
