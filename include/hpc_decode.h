@@ -582,10 +582,10 @@ typedef struct {
  *     the frequency becomes u f_i / factor + (1 - u) f_i, and the magnitude is
  *     0.1 ln(factor) + 1.
  *   rot_dim      even, 2 .. 128 (HPC_ROPE_BASE: above 2)
- *   base         > 1
+ *   base         > 1, finite; HPC_ROPE_BASE: the scaled one too
  *   factor       >= 1 (not read for HPC_ROPE_NONE)
  *   original_len, low, high  for BANDED and RAMP: > 0, low < high (turns)
- *   magnitude    0: 1, or the ramp's; > 0: this value
+ *   magnitude    0: 1, or the ramp's; > 0: this value, which fp32 has to hold
  */
 hpc_status hpc_rope_init(hpc_rope* rope, int32_t rot_dim, int32_t interleaved, double base,
                          int32_t scaling, double factor, int32_t original_len, double low,

@@ -265,6 +265,8 @@ hpc_status hpc_rope_init(hpc_rope* rope, int32_t rot_dim, int32_t interleaved, d
     const double two_pi = 2.0 * 3.14159265358979323846;
     const int R = rot_dim;
     if (scaling == HPC_ROPE_BASE) base *= std::pow(factor, R / (R - 2.0));
+    if (!std::isfinite(base))
+      return fail(HPC_ERR_INVALID_ARG, "the scaled base must be finite");
     // the pair whose wavelength makes `turns` turns over the trained positions
     auto pair_of = [&](double turns) {
       return R * std::log(original_len / (turns * two_pi)) / (2.0 * std::log(base));
@@ -281,6 +283,8 @@ hpc_status hpc_rope_init(hpc_rope* rope, int32_t rot_dim, int32_t interleaved, d
     double mag = magnitude;
     if (mag == 0.0) mag = scaling == HPC_ROPE_RAMP ? 0.1 * std::log(factor) + 1.0 : 1.0;
     r.magnitude = (float)mag;
+    if (!(r.magnitude > 0.f) || !std::isfinite(r.magnitude))
+      return fail(HPC_ERR_INVALID_ARG, "magnitude must be in fp32's range");
     for (int i = 0; i < R / 2; ++i) {
       double f = std::pow(base, -2.0 * i / R);
       auto clamp01 = [](double x) { return x < 0.0 ? 0.0 : x > 1.0 ? 1.0 : x; };
