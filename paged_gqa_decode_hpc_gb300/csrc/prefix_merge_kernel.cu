@@ -12,8 +12,8 @@
 // What bounds it: latency for few pairs, L2 (where the states just written still are)
 // for many: 4 KB a state. So which states there are is worked out before the wait for
 // the attention kernel (the plan is complete by then: the attention kernel lets this
-// one start only after its own wait for it; it is read from L2, so that no line of an
-// earlier step's plan in an SM's L1 can stand for it), and the CTAs are cut as small as they
+// one start only after its own wait for it; its first word is acquired, so that no line
+// of an earlier step's plan in an SM's L1 can stand for it), and the CTAs are cut as small as they
 // still all fit on the GPU while that kernel ends; those that do not have all of this
 // ahead of them (480 pairs and heads: whole 60.9 us a step, halves 63.2, quarters 66).
 // Thread = (column group of 4, row), the 8 rows of a column group adjacent, as the
@@ -49,6 +49,11 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       "l"(src), "r"(bytes), "r"(bar)
       : "memory");
 }
+__device__ __forceinline__ int32_t ld_acquire(const int32_t* p) {
+  int32_t v;
+  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
 constexpr float kLn2 = 0.6931471805599453f;
 
 // The states of pair `pair` (new token t of sequence b) and KV head h: for the pair's
@@ -60,16 +65,16 @@ struct StateList {
   __device__ __forceinline__ StateList(const PrefixMergeParams& params, int pair, int h, int b, int t)
       : p(params), local{0, t} {
     const int H = p.num_kv_heads;
-    const int rows_all = __ldcg(p.words + kPxRows), parts = __ldcg(p.words + kPxParts);
+    const int rows_all = ld_acquire(p.words + kPxRows), parts = p.words[kPxParts];
     if (rows_all == 0) return;
     const int2* bounds = reinterpret_cast<const int2*>(p.words + p.bound_off);
     const int4* recs = reinterpret_cast<const int4*>(p.words + p.rec_off);
-    const int2 s = __ldcg(reinterpret_cast<const int2*>(p.words + p.seq_off) + b);
+    const int2 s = reinterpret_cast<const int2*>(p.words + p.seq_off)[b];
     const int k = s.x >= 0 ? pair - s.y : 0;
     const int v[2] = {s.x >= 0 ? s.x + k / kPrefixRowPairs : -1, rows_all - p.num_seqs + b};
     int n[2];
-    n[0] = s.x >= 0 ? __ldcg(&recs[2 * v[0] + 1].x) : 0;
-    n[1] = __ldcg(&recs[2 * v[1] + 1].x);
+    n[0] = s.x >= 0 ? recs[2 * v[0] + 1].x : 0;
+    n[1] = recs[2 * v[1] + 1].x;
     local[0] = k % kPrefixRowPairs;
     if (n[0] > 0) home[0] = (int64_t)pair * H + h;
     if (n[1] > 0) home[1] = p.ws.own0 + (int64_t)pair * H + h;
@@ -78,7 +83,7 @@ struct StateList {
     for (int q0 = 0; q0 < parts; q0 += (int)blockDim.x) {
       const int q = q0 + (int)threadIdx.x;
       int2 bd = make_int2(INT32_MAX, 0);
-      if (q < parts) bd = __ldcg(bounds + q);
+      if (q < parts) bd = bounds[q];
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
         if (n[w] == 0) continue;  // the whole CTA has the same
@@ -96,7 +101,7 @@ struct StateList {
     if (i == 0) return home[w];
     const int q = lo[w] + i - 1;
     const int2* bounds = reinterpret_cast<const int2*>(p.words + p.bound_off);
-    const int2 b0 = __ldcg(bounds + q), b1 = __ldcg(bounds + q + 1);
+    const int2 b0 = bounds[q], b1 = bounds[q + 1];
     if (b0.x == b1.x && b0.y == b1.y) return -1;
     return p.ws.cont0 + (int64_t)q * kPrefixRowPairs + local[w];
   }
