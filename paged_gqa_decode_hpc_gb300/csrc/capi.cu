@@ -745,7 +745,11 @@ hpc_status attn_impl(const hpc_tensor* q, const hpc_tensor* k_cache, const hpc_t
     // q_len >= the tensor-core threshold with a tile plan: the q_len x 8 query
     // rows of a KV head go through tcgen05 (decode_tc_kernel.cu)
     CUtensorMap tq;
-    const bool tc = multi && T >= tc_min_q_len(fp8) &&
+    // That kernel multiplies masked scores and takes its maximum before the scores' factor:
+    // with e4m3 that has to stay above 0 with the 2^-100 of a query row's scale. A cache of
+    // zeros (scale 0) or a negative scale goes to the other kernel, which masks afterwards.
+    const bool factor_ok = !fp8 || p.score_scale_log2 >= 0x1p-48f;
+    const bool tc = multi && T >= tc_min_q_len(fp8) && factor_ok &&
                     plan->kind == HPC_PLAN_DYNAMIC && plan->units == 1 && fused_num_sms == 0 &&
                     make_decode_q_map(q, &tq);
     if (plan->ev_start) HPC_CUDA_TRY(cudaEventRecord(plan->ev_start, s));

@@ -47,8 +47,6 @@
 //  * Every wait is bounded (globaltimer); a timeout sets the error bit, all
 //    roles stop issuing, and the CTA drains its copies and MMAs and frees its
 //    tensor memory before leaving. No trap, no assert.
-#include <cfloat>
-
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -565,12 +563,8 @@ __global__ void __launch_bounds__(TcLayout<FP8>::kThreads, 1)
             e2 = 14 - ((int)((__float_as_uint(mq) >> 23) & 0xFF) - 127);
             e2 = e2 < -100 ? -100 : (e2 > 100 ? 100 : e2);
           }
-          // a negative K scale turns Q around, so that the scores' factor is positive;
-          // a factor of 0 would make NaN of masked scores (the least normal number
-          // times any score, below 2^31, is 0 to every exponential)
-          const float qs = __uint_as_float(((uint32_t)(127 + e2) << 23) |
-                                           (__float_as_uint(sc0) & 0x80000000u));
-          sc = fmaxf(fabsf(sc0) * __uint_as_float((uint32_t)(127 - e2) << 23), FLT_MIN);
+          const float qs = __uint_as_float((uint32_t)(127 + e2) << 23);
+          sc = sc0 * __uint_as_float((uint32_t)(127 - e2) << 23);
 #pragma unroll 4
           for (int i = 0; i < 16; ++i) {
             uint32_t x[4], y[4];
