@@ -486,7 +486,11 @@ hpc_status hpc_extend_attn_ex(const hpc_tensor* q, const hpc_tensor* k_cache,
  *   slots[N_b + i] = 64 * block_table[b][(o_b + i) / 64] + (o_b + i) % 64,
  *   free_count_out = free_count - sum a.
  * These are the inputs of hpc_rope_kv_write (positions, slots), of
- * hpc_extend_attn (cu_q_lens, seq_lens) and of the decode calls. The result
+ * hpc_extend_attn (cu_q_lens, seq_lens) and of the decode calls. The tokens are
+ * packed. The decode calls take q_len rows of every sequence, which are the
+ * packed ones while every n_b is q_len; else row [b][t] is packed row
+ * cu_q_lens[b + 1] - q_len + t (any row where that is below 0), and what lies
+ * before the sequence's own n_b rows means nothing. The result
  * depends on the arguments alone (no atomics). Sequences that share a prefix
  * start from rows that hold the prefix's whole blocks, with seq_lens[b] = 64
  * times their number; the last, partly filled block is never a shared one.
@@ -534,7 +538,9 @@ hpc_status hpc_block_table_append(const hpc_tensor* seq_lens, const hpc_tensor* 
  * free_count + the released blocks. The table is not written: entries past a
  * sequence's end have no meaning. Blocks that several rows share must not be
  * released through more than one of them: keep to_lens[b] at or above the
- * shared prefix.
+ * shared blocks' 64 k positions. A sequence that is done before the others of
+ * its prefix is truncated to 64 k and its length then set to 0; the last one is
+ * truncated to 0 and returns the shared blocks.
  *   seq_lens, to_lens  device int32 [B], each >= 0; B <= 16384
  *   block_table        device int32 [B][max_blocks], rows contiguous (read)
  *   num_blocks         blocks of the cache; an entry outside [0, num_blocks)
@@ -669,7 +675,12 @@ hpc_status hpc_decode_prefix_plan_create(int32_t max_seqs, int32_t max_q_len, in
  *   plan         from hpc_decode_prefix_plan_create, for at least this step's
  *                sequences, new tokens and heads
  *   softmax_scale  > 0, or <= 0 for 1/sqrt(128)
- * Cache slots past a sequence's end may hold anything, NaN included. A new
+ * Cache slots past a sequence's end may hold anything, NaN included; a V before
+ * it that is not finite spoils every new token of its sequence, and K those that
+ * see it. Sums, maxima and states are fp32. Probabilities are rounded to bf16
+ * (2^-8 of each) for a bf16 cache, to f16 for e4m3: 2^-11 of each, and at least
+ * 2^-25 of the row's largest, so that n keys far below it can cost n 2^-25 max |v|
+ * (2^-8 at 131072 keys, all but one of them 17 nats below that one). A new
  * token that sees no position, and every token of an empty sequence, gets out =
  * 0, lse = -inf; a negative length counts as 0 and sets HPC_DEVCHK_BAD_LENGTH.
  * Bad block ids read zeros and set HPC_DEVCHK_BAD_BLOCK. Allocates nothing; may

@@ -38,8 +38,8 @@
 // The tile loop is the extend kernel's: S_j = Q K_j^T (M 128, N 64, K 128);
 // online softmax in the log2 domain, the running maximum moved only when it
 // grows by more than 8; P as 16-bit pairs back to tensor memory (bf16 for a
-// bf16 cache, whose V has bf16's range: 2^-9 of each probability; f16 for e4m3:
-// 2^-12, see below); O += P V_j (M 128, N 128, K 64). Row sums are fp32 of the
+// bf16 cache, whose V has bf16's range: 2^-8 of each probability; f16 for e4m3:
+// 2^-11, see below, and at least 2^-25 of the row's largest); O += P V_j (M 128, N 128, K 64). Row sums are fp32 of the
 // unrounded probabilities.
 // E4m3 caches run the MMAs in fp16: every e4m3 value is an f16 value, and each
 // query row is converted in place with a power-of-two scale putting its largest

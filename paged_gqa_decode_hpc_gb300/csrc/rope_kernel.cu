@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
 #pragma unroll
         for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         if (is_q ? p.wq != nullptr : (is_k && p.wk != nullptr)) {
-          // (rsqrtf is within 2 ulp: 2^-22 next to the result's 2^-9)
+          // (rsqrtf is within 2 ulp: 2^-22 next to the result's 2^-8)
           inv = rsqrtf(ss * (1.0f / kHeadDim) + p.eps);
         }
       }
