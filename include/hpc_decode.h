@@ -55,7 +55,8 @@ typedef enum {
   HPC_BF16 = 0,
   HPC_FP8_E4M3 = 1,
   HPC_F32 = 2,
-  HPC_I32 = 3
+  HPC_I32 = 3,
+  HPC_KV4 = 4 /* bytes of 4-bit cache rows, see hpc_rope_kv4_write */
 } hpc_dtype;
 
 /*
@@ -84,6 +85,8 @@ typedef struct hpc_plan_s* hpc_plan_t;
 #define HPC_PLAN_STEP 2
 /* A plan from hpc_decode_prefix_plan_create (not exported). */
 #define HPC_PLAN_PREFIX 3
+/* A plan from hpc_decode_kv4_plan_create (not exported). */
+#define HPC_PLAN_KV4 4
 
 /* Segment flag: the segment covers every tile of its sequence. */
 #define HPC_SEG_WHOLE 1
@@ -691,6 +694,119 @@ hpc_status hpc_decode_prefix_attn(const hpc_tensor* q, const hpc_tensor* k_cache
                                   const hpc_tensor* seq_lens, const hpc_tensor* cu_groups,
                                   const hpc_tensor* prefix_lens, hpc_plan_t plan, hpc_tensor* out,
                                   hpc_tensor* lse, float softmax_scale, void* stream);
+
+/*
+ * A cache held in 4 bits (hpc_rope_kv4_write, hpc_decode_kv4_attn,
+ * hpc_extend_kv4_attn): K and V are HPC_KV4 tensors [num_blocks][H_kv][64][72],
+ * 0.28 of a bf16 cache's bytes. A row, one token's K or V of one KV head, is
+ *   bytes  0 .. 63  e2m1 codes (sign, two bits of exponent, one of mantissa: 0, 0.5,
+ *                   1, 1.5, 2, 3, 4, 6 and their negatives), element 2i of the head
+ *                   in the low four bits of byte i, element 2i + 1 in the high ones
+ *   bytes 64 .. 71  e4m3 scales, scale j of elements 16 j .. 16 j + 15
+ * and an element stands for code * scale * (the tensor's `scale`, which is positive
+ * and finite). Both caches have the same shape and strides; a (block, KV head) tile is
+ * 4608 contiguous bytes (stride 2 = 72, stride 3 = 1; else HPC_ERR_UNSUPPORTED), 16-byte
+ * aligned, strides 0 and 1 multiples of 16. Block tables, slots and positions are those of
+ * hpc_block_table_append / _truncate.
+ */
+
+/*
+ * hpc_rope_kv4_write -- hpc_rope_kv_write into a 4-bit cache: QK-norm (where weights
+ * are given), rotary positions of a ragged batch of tokens, q' to q_out in bf16, and
+ * k' and v as 4-bit rows at the tokens' slots. For each 16 elements x of a row, with
+ * ts the tensor's scale and products of floats rounded to fp32 (fl):
+ *   scale = e4m3(max |x| / fl(6 ts)),  code = e2m1(x / fl(scale ts)),
+ * each the nearest value to the exact quotient, ties to even, saturating (a largest
+ * element up to 1/16 above what the rounded scale reaches becomes 6; one beyond
+ * 2688 ts too). Elements of a scale that rounds to 0 (max |x| <= 3 * 2^-9 ts) become 0;
+ * NaN anywhere among the 16 makes their scale, and so all of them, NaN. k' is formed in
+ * fp32, so its codes can differ from those of exact arithmetic where an element lies
+ * within fp32's rounding of a border; v's do not.
+ *   q_in, k_in, v_in, positions, slots, rope, weights, eps, q_out, device_error: as
+ *       hpc_rope_kv_write (slots < 0: padding, nothing is written)
+ *   k_cache, v_cache  4-bit caches with `scale` in [2^-100, 2^100]; written in place,
+ *       72 bytes a row and nothing else. Tiles of neither may overlap each other's or
+ *       their own, nor their byte ranges meet q_in's, k_in's, v_in's or q_out's
+ *       (HPC_ERR_INVALID_ARG)
+ * H_q a multiple of H_kv. One launch; allocates nothing.
+ */
+hpc_status hpc_rope_kv4_write(const hpc_tensor* q_in, const hpc_tensor* k_in,
+                              const hpc_tensor* v_in, const hpc_tensor* positions,
+                              const hpc_tensor* slots, const hpc_rope* rope,
+                              const hpc_tensor* q_norm_weight, const hpc_tensor* k_norm_weight,
+                              float eps, hpc_tensor* q_out, hpc_tensor* k_cache,
+                              hpc_tensor* v_cache, int32_t* device_error, void* stream);
+
+/*
+ * hpc_decode_kv4_plan_create -- a plan for hpc_decode_kv4_attn: counters, partial states
+ * and error word of steps of at most max_seqs (<= 4096) sequences with max_q_len (1 .. 8)
+ * new tokens each and num_q_heads (<= 512) query heads, on num_sms CTAs (normally the SM
+ * count). All device memory is allocated here: 46 KB a CTA and token. The device
+ * is the current one. hpc_decode_plan_status and hpc_decode_plan_destroy take the plan; the
+ * other calls refuse it. Calls on one plan must not overlap on the GPU (graphs that share
+ * one included).
+ */
+hpc_status hpc_decode_kv4_plan_create(int32_t max_seqs, int32_t max_q_len, int32_t num_sms,
+                                      int32_t num_q_heads, hpc_plan_t* plan_out);
+
+/*
+ * hpc_decode_kv4_attn -- hpc_decode_step over a 4-bit cache: decode attention of q_len
+ * (1 .. 8) new tokens of every sequence, planned from the device lengths. One launch for
+ * one token, two for several.
+ *   q            device bf16 [B][H_q][128], or [B][q_len][H_q][128]: the last q_len
+ *                positions of each sequence; token t sees positions <
+ *                seq_lens[b] - (q_len - 1 - t). Rows contiguous, other strides multiples of
+ *                8 elements, base 16-byte aligned
+ *   k_cache, v_cache  4-bit caches with H_q == 8 * H_kv
+ *   block_table  device int32 [B][max_blocks], rows contiguous
+ *   seq_lens     device int32 [B]; a negative length, a sequence of more than INT32_MAX /
+ *                512 (tile, KV head) units, or more than INT32_MAX units in all set
+ *                HPC_DEVCHK_BAD_LENGTH and the step writes out = 0, lse = -inf throughout
+ *   plan         from hpc_decode_kv4_plan_create, for at least this step's sequences, new
+ *                tokens and heads, on the current device
+ *   out          device bf16, q's shape and rules (written). Its rows may not overlap each
+ *                other, q's or lse (HPC_ERR_INVALID_ARG)
+ *   lse          device f32 [B][H_q] or [B][q_len][H_q], natural log (written), or NULL
+ *   softmax_scale  > 0, or <= 0 for 1/sqrt(128)
+ * Cache slots past a sequence's end may hold anything; a NaN scale before it spoils the
+ * tokens that see it (K) or all of the sequence's (V, from the tile that holds it on).
+ * Codes times scales, and q (from bf16, by a power of two for each KV head's 8 rows: what is
+ * 2^-29 of their largest element, or less, may lose bits), are exact in f16; probabilities
+ * are rounded to f16 (2^-11 of each, and at least 2^-25 of the row's largest); sums,
+ * maxima and states are fp32. The states of the warps that share a piece of a sequence are
+ * handed over with o in f16 (2^-11, and 2^-25 ts absolute). A token that sees no position gets out
+ * = 0, lse = -inf. Bad block ids read zeros and set HPC_DEVCHK_BAD_BLOCK. Results do not
+ * depend on timing: equal steps give equal bits. Allocates nothing; may be captured in a
+ * CUDA graph after a first call outside the capture.
+ */
+hpc_status hpc_decode_kv4_attn(const hpc_tensor* q, const hpc_tensor* k_cache,
+                               const hpc_tensor* v_cache, const hpc_tensor* block_table,
+                               const hpc_tensor* seq_lens, hpc_plan_t plan, hpc_tensor* out,
+                               hpc_tensor* lse, float softmax_scale, void* stream);
+
+/*
+ * hpc_extend_kv4_attn -- hpc_extend_attn over a 4-bit cache: prefill / extend attention of
+ * ragged new tokens, which are in the cache already, on the tcgen05 tensor cores. Rows are
+ * converted exactly to f16 on the chip; q and probabilities as for hpc_decode_kv4_attn
+ * (q's power of two is each row's own).
+ *   q, out       device bf16 [total_q][H_q][128], ragged by cu_q_lens; rows contiguous, other
+ *                strides multiples of 8 elements, 16-byte aligned; out's rows may not overlap
+ *                each other, q's or lse
+ *   seq_lens     device int32 [B], L_b >= n_b = cu_q_lens[b + 1] - cu_q_lens[b]
+ *   cu_q_lens    device int32 [B + 1], non-decreasing from 0 to total_q; a sequence whose
+ *                rows would leave q, or with L_b < n_b, sets HPC_DEVCHK_BAD_LENGTH and its
+ *                rows are not written
+ *   lse          device f32 [total_q][H_q] (written), or NULL
+ *   device_error optional device int32 receiving HPC_DEVCHK_* bits
+ * Requirements: H_q == 8 * H_kv and ceil(total_q / T) + B <= 65535 with T = 16 or 32 new
+ * tokens to a CTA (else HPC_ERR_UNSUPPORTED). Slots past a sequence's end may hold
+ * anything. Allocates nothing.
+ */
+hpc_status hpc_extend_kv4_attn(const hpc_tensor* q, const hpc_tensor* k_cache,
+                               const hpc_tensor* v_cache, const hpc_tensor* block_table,
+                               const hpc_tensor* seq_lens, const hpc_tensor* cu_q_lens,
+                               hpc_tensor* out, hpc_tensor* lse, float softmax_scale,
+                               int32_t* device_error, void* stream);
 
 /* hpc_device_sm_count -- streaming multiprocessors of the current device. */
 hpc_status hpc_device_sm_count(int32_t* num_sms);

@@ -31,14 +31,15 @@ __all__ = [
     "hpc_rope_norm_kv_write", "hpc_extend_attn", "hpc_decode_tc_min_q_len",
     "hpc_block_table_append", "hpc_block_table_truncate", "HpcRope", "hpc_rope_init",
     "hpc_rope_kv_write", "hpc_decode_prefix_plan_create", "hpc_decode_prefix_attn",
+    "hpc_rope_kv4_write", "hpc_decode_kv4_plan_create", "hpc_decode_kv4_attn", "hpc_extend_kv4_attn",
     "HPC_OK", "HPC_ERR_INVALID_ARG", "HPC_ERR_UNSUPPORTED", "HPC_ERR_CUDA", "HPC_ERR_OOM",
     "HPC_ERR_DEVICE_CHECK",
 ]
 
 HPC_OK, HPC_ERR_INVALID_ARG, HPC_ERR_UNSUPPORTED, HPC_ERR_CUDA, HPC_ERR_OOM, \
     HPC_ERR_DEVICE_CHECK = range(6)
-HPC_BF16, HPC_FP8_E4M3, HPC_F32, HPC_I32 = range(4)
-HPC_PLAN_DYNAMIC, HPC_PLAN_STATIC, HPC_PLAN_STEP, HPC_PLAN_PREFIX = 0, 1, 2, 3
+HPC_BF16, HPC_FP8_E4M3, HPC_F32, HPC_I32, HPC_KV4 = range(5)
+HPC_PLAN_DYNAMIC, HPC_PLAN_STATIC, HPC_PLAN_STEP, HPC_PLAN_PREFIX, HPC_PLAN_KV4 = 0, 1, 2, 3, 4
 HPC_SEG_WHOLE = 1
 HPC_DEVCHK_BAD_LENGTH, HPC_DEVCHK_BAD_BLOCK, HPC_DEVCHK_TABLE_TOO_SHORT, \
     HPC_DEVCHK_TIMEOUT, HPC_DEVCHK_CAPACITY, HPC_DEVCHK_NO_BLOCKS = 1, 2, 4, 8, 16, 32
@@ -130,6 +131,11 @@ def load_library():
             "hpc_rope_init": [ctypes.POINTER(HpcRope), i32, i32, F64, i32, F64, i32, F64, F64, F64],
             "hpc_rope_kv_write": [D, D, D, D, D, ctypes.POINTER(HpcRope), D, D, ctypes.c_float,
                                   D, D, D, D, P, P],
+            "hpc_rope_kv4_write": [D, D, D, D, D, ctypes.POINTER(HpcRope), D, D, ctypes.c_float,
+                                   D, D, D, P, P],
+            "hpc_decode_kv4_plan_create": [i32, i32, i32, i32, ctypes.POINTER(P)],
+            "hpc_decode_kv4_attn": [D, D, D, D, D, P, D, D, ctypes.c_float, P],
+            "hpc_extend_kv4_attn": [D, D, D, D, D, D, D, D, ctypes.c_float, P, P],
         }
         for name, args in sigs.items():
             fn = getattr(lib, name)
@@ -161,7 +167,8 @@ def _load_native(lib):
     loader.exec_module(module)
     module.bind(_dtypes(), *(ctypes.cast(f, ctypes.c_void_p).value for f in (
         lib.hpc_block_table_append, lib.hpc_block_table_truncate, lib.hpc_rope_kv_write,
-        lib.hpc_decode_prefix_attn)))
+        lib.hpc_decode_prefix_attn, lib.hpc_rope_kv4_write, lib.hpc_decode_kv4_attn,
+        lib.hpc_extend_kv4_attn)))
     _native = module
 
 
@@ -646,3 +653,117 @@ def hpc_decode_prefix_attn(q, k_cache, v_cache, block_table, seq_lens, prefix_le
         _desc(q), _desc(k_cache, k_scale), _desc(v_cache, v_scale), _desc(block_table),
         _desc(seq_lens), _desc(cu_groups), _desc(prefix_lens), plan.handle, _desc(out), _desc(lse),
         -1.0 if softmax_scale is None else softmax_scale, _stream_ptr(stream)))
+
+
+_device_of = None  # () -> index of torch's current device
+
+
+def _device(t) -> int:
+    """The device of a call's first tensor, which all others have to share: the current
+    one (or -1, the CPU, whose tensors the library refuses)."""
+    global _device_of
+    device = -1 if t is None else t.get_device()
+    if device >= 0:
+        if _device_of is None:
+            import torch
+            _device_of = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        if device != _device_of():
+            raise HpcError(HPC_ERR_INVALID_ARG, "tensors must be on the current CUDA device")
+    return device
+
+
+def _desc_on(device: int, name: str, t, scale: float = 1.0, kv4: bool = False) -> Optional[bytes]:
+    """_desc of a tensor on `device`; kv4: the uint8 bytes of a 4-bit cache."""
+    if t is None:
+        return None
+    if t.get_device() != device:
+        raise HpcError(HPC_ERR_INVALID_ARG, f"{name} is not on the device of the other tensors")
+    n = t.dim()
+    if not kv4 or n > 4:
+        return _desc(t, scale)
+    if _dtype_code(t) != HPC_FP8_E4M3:
+        raise HpcError(HPC_ERR_INVALID_ARG, f"{name} must be uint8 [num_blocks][H_kv][64][72]")
+    return _PACKS[n](t.data_ptr(), HPC_KV4, n, *t.shape, *t.stride(), scale)
+
+
+def _err_on(device: int, t):
+    if t is None:
+        return None
+    if t.get_device() != device or _dtype_code(t) != HPC_I32:
+        raise HpcError(HPC_ERR_INVALID_ARG, "device_error must be int32 on the device of the other tensors")
+    return t.data_ptr()
+
+
+def hpc_rope_kv4_write(q_in, k_in, v_in, positions, slots, rope: HpcRope, q_out, k_cache, v_cache,
+                       q_norm_weight=None, k_norm_weight=None, eps: float = 1e-6,
+                       k_scale: float = 1.0, v_scale: float = 1.0, device_error=None, stream=None):
+    """hpc_rope_kv_write into a cache held in 4 bits: k_cache and v_cache are uint8
+    [num_blocks][H_kv][64][72], a row 64 bytes of e2m1 codes and 8 e4m3 scales of 16 elements
+    each; an element stands for code * scale * k_scale (v_scale)."""
+    lib, handle, device = _lib or load_library(), _stream_handle(stream), _device(q_in)
+    if _native is not None and isinstance(rope, HpcRope):
+        status = _native.rope_kv4_write(device, q_in, k_in, v_in, positions, slots, rope,
+                                        q_norm_weight, k_norm_weight, eps, q_out, k_cache, k_scale,
+                                        v_cache, v_scale, device_error, handle)
+        if status is not None:
+            return _check(status)
+    _check(lib.hpc_rope_kv4_write(
+        _desc_on(device, "q_in", q_in), _desc_on(device, "k_in", k_in),
+        _desc_on(device, "v_in", v_in), _desc_on(device, "positions", positions),
+        _desc_on(device, "slots", slots), rope, _desc_on(device, "q_norm_weight", q_norm_weight),
+        _desc_on(device, "k_norm_weight", k_norm_weight), eps, _desc_on(device, "q_out", q_out),
+        _desc_on(device, "k_cache", k_cache, k_scale, kv4=True),
+        _desc_on(device, "v_cache", v_cache, v_scale, kv4=True),
+        _err_on(device, device_error), handle))
+
+
+def hpc_decode_kv4_plan_create(max_seqs: int, max_q_len: int, num_sms: int,
+                               num_q_heads: int) -> Plan:
+    """A plan (counters, partial states, error word) for hpc_decode_kv4_attn."""
+    h = ctypes.c_void_p()
+    _check(load_library().hpc_decode_kv4_plan_create(int(max_seqs), int(max_q_len), int(num_sms),
+                                                     int(num_q_heads), ctypes.byref(h)))
+    return Plan(h, HPC_PLAN_KV4)
+
+
+def hpc_decode_kv4_attn(q, k_cache, v_cache, block_table, seq_lens, plan: Plan, out, lse=None,
+                        softmax_scale: Optional[float] = None, stream=None, k_scale: float = 1.0,
+                        v_scale: float = 1.0):
+    """Decode attention over a cache held in 4 bits (see hpc_rope_kv4_write): q, out and lse as
+    for hpc_decode_step (q_len 1 to 8), seq_lens an int32 CUDA tensor."""
+    lib, handle, device = _lib or load_library(), _stream_handle(stream), _device(q)
+    if _native is not None:
+        h = plan.handle
+        status = _native.decode_kv4_attn(device, q, k_cache, k_scale, v_cache, v_scale, block_table,
+                                         seq_lens, h.value if h else None, out, lse,
+                                         -1.0 if softmax_scale is None else softmax_scale, handle)
+        if status is not None:
+            return _check(status)
+    _check(lib.hpc_decode_kv4_attn(
+        _desc_on(device, "q", q), _desc_on(device, "k_cache", k_cache, k_scale, kv4=True),
+        _desc_on(device, "v_cache", v_cache, v_scale, kv4=True),
+        _desc_on(device, "block_table", block_table), _desc_on(device, "seq_lens", seq_lens),
+        plan.handle, _desc_on(device, "out", out), _desc_on(device, "lse", lse),
+        -1.0 if softmax_scale is None else softmax_scale, handle))
+
+
+def hpc_extend_kv4_attn(q, k_cache, v_cache, block_table, seq_lens, cu_q_lens, out, lse=None,
+                        softmax_scale: Optional[float] = None, device_error=None, stream=None,
+                        k_scale: float = 1.0, v_scale: float = 1.0):
+    """Prefill / extend attention over a cache held in 4 bits (see hpc_rope_kv4_write): q, out,
+    lse and cu_q_lens as for hpc_extend_attn."""
+    lib, handle, device = _lib or load_library(), _stream_handle(stream), _device(q)
+    if _native is not None:
+        status = _native.extend_kv4_attn(device, q, k_cache, k_scale, v_cache, v_scale, block_table,
+                                         seq_lens, cu_q_lens, out, lse,
+                                         -1.0 if softmax_scale is None else softmax_scale,
+                                         device_error, handle)
+        if status is not None:
+            return _check(status)
+    _check(lib.hpc_extend_kv4_attn(
+        _desc_on(device, "q", q), _desc_on(device, "k_cache", k_cache, k_scale, kv4=True),
+        _desc_on(device, "v_cache", v_cache, v_scale, kv4=True),
+        _desc_on(device, "block_table", block_table), _desc_on(device, "seq_lens", seq_lens),
+        _desc_on(device, "cu_q_lens", cu_q_lens), _desc_on(device, "out", out),
+        _desc_on(device, "lse", lse), -1.0 if softmax_scale is None else softmax_scale,
+        _err_on(device, device_error), handle))

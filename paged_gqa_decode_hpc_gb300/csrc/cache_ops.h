@@ -88,6 +88,7 @@ struct RopeParams {
   void* v_cache;
   int64_t c_sblk, c_shead, c_sslot;
   int32_t cache_fp8;
+  int32_t cache_kv4;            // 4-bit rows (kv4.cuh); strides in bytes
   E4m3Scale k_scale, v_scale;
   int32_t* err;                 // may be null
 };

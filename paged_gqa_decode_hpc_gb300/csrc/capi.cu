@@ -148,7 +148,7 @@ hpc_status ensure_workspace(hpc_plan_s* pl, int64_t num_q_heads, bool may_alloca
 int elt_bytes(int32_t dt) {
   switch (dt) {
     case HPC_BF16: return 2;
-    case HPC_FP8_E4M3: return 1;
+    case HPC_FP8_E4M3: case HPC_KV4: return 1;
     case HPC_F32: case HPC_I32: return 4;
     default: return 0;
   }
@@ -423,6 +423,7 @@ hpc_status hpc_decode_plan_export(hpc_plan_t plan, int32_t* buf, int64_t cap, in
   if (!plan || !len) return fail(HPC_ERR_INVALID_ARG, "plan or len is null");
   if (plan->kind == HPC_PLAN_PREFIX)
     return fail(HPC_ERR_UNSUPPORTED, "a prefix plan has no export");
+  if (plan->kind == HPC_PLAN_KV4) return fail(HPC_ERR_UNSUPPORTED, "a 4-bit plan has no export");
   const PlanLayout& L = plan->layout;
   std::vector<int32_t> w((size_t)L.words());
   HPC_CUDA_TRY(cudaDeviceSynchronize());
@@ -548,6 +549,8 @@ hpc_status attn_impl(const hpc_tensor* q, const hpc_tensor* k_cache, const hpc_t
   if (!plan) return fail(HPC_ERR_INVALID_ARG, "plan is null");
   if (plan->kind == HPC_PLAN_PREFIX)
     return fail(HPC_ERR_INVALID_ARG, "a prefix plan serves hpc_decode_prefix_attn only");
+  if (plan->kind == HPC_PLAN_KV4)
+    return fail(HPC_ERR_INVALID_ARG, "a 4-bit plan serves hpc_decode_kv4_attn only");
   const bool has_lse = lse && lse->data;
   const bool multi = qnd == 4;
   const int64_t B = q->shape[0], T = multi ? q->shape[1] : 1;
@@ -1000,6 +1003,8 @@ hpc_status hpc_decode_plan_set_timing_events(hpc_plan_t plan, void* ev_start, vo
   if (!plan) return fail(HPC_ERR_INVALID_ARG, "plan is null");
   if (plan->kind == HPC_PLAN_PREFIX)
     return fail(HPC_ERR_INVALID_ARG, "a prefix plan serves hpc_decode_prefix_attn only");
+  if (plan->kind == HPC_PLAN_KV4)
+    return fail(HPC_ERR_INVALID_ARG, "a 4-bit plan serves hpc_decode_kv4_attn only");
   plan->ev_start = (cudaEvent_t)ev_start;
   plan->ev_mid = (cudaEvent_t)ev_attn_done;
   plan->ev_end = (cudaEvent_t)ev_end;
@@ -1128,11 +1133,9 @@ hpc_status hpc_decode_attn(const hpc_tensor* q, const hpc_tensor* k_cache,
 // ------------------------------------------------------------------------
 // Prefill / extend attention (prefill_kernel.cu).
 namespace hpc {
-namespace {
-
 // 3-D TMA descriptor over q or out [total_q][H_q][128] bf16: box = 16 tokens
 // x 8 heads x 64 columns, 128-byte swizzle (one 16 KB half of a 128-row tile).
-hpc_status make_q_map(const hpc_tensor* q, CUtensorMap* map, const char* what = "q") {
+hpc_status make_q_map(const hpc_tensor* q, CUtensorMap* map, const char* what) {
   auto enc = encode_fn();
   if (!enc) return fail(HPC_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
   cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)q->shape[1], (cuuint64_t)q->shape[0]};
@@ -1148,7 +1151,11 @@ hpc_status make_q_map(const hpc_tensor* q, CUtensorMap* map, const char* what = 
   return HPC_OK;
 }
 
-}  // namespace
+int extend_tiles_per_cta(int64_t total_q, int64_t num_kv_heads, int sms) {
+  const int64_t pairs = (total_q + 2 * kExtendTileTokens - 1) / (2 * kExtendTileTokens);
+  return 2 * pairs * num_kv_heads >= sms ? 2 : 1;
+}
+
 }  // namespace hpc
 
 extern "C" hpc_status hpc_extend_attn_ex(const hpc_tensor* q, const hpc_tensor* k_cache,
@@ -1231,8 +1238,7 @@ extern "C" hpc_status hpc_extend_attn_ex(const hpc_tensor* q, const hpc_tensor* 
     int dev = 0, sms = 0;
     HPC_CUDA_TRY(cudaGetDevice(&dev));
     HPC_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-    const int64_t pairs = (total_q + 2 * kExtendTileTokens - 1) / (2 * kExtendTileTokens);
-    tiles_per_cta = 2 * pairs * Hkv >= sms ? 2 : 1;
+    tiles_per_cta = extend_tiles_per_cta(total_q, Hkv, sms);
   }
   // CTA tiles of T = 16 * tiles_per_cta tokens: sum_b ceil(n_b / T) <= total_q / T + B
   const int64_t tt = (int64_t)kExtendTileTokens * tiles_per_cta;
@@ -1240,7 +1246,7 @@ extern "C" hpc_status hpc_extend_attn_ex(const hpc_tensor* q, const hpc_tensor* 
   if (tiles > 65535)
     return fail(HPC_ERR_UNSUPPORTED, "too many query tiles in one call (split the batch)");
   CUtensorMap tq, tk, tv, to;
-  if ((st = make_q_map(q, &tq)) != HPC_OK) return st;
+  if ((st = make_q_map(q, &tq, "q")) != HPC_OK) return st;
   if ((st = make_q_map(out, &to, "out")) != HPC_OK) return st;  // full tiles leave by TMA
   if ((st = make_kv_map(k_cache, fp8, swap, &tk)) != HPC_OK) return st;
   if ((st = make_kv_map(v_cache, fp8, swap, &tv)) != HPC_OK) return st;

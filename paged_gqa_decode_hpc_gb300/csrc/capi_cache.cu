@@ -8,6 +8,7 @@
 
 #include "cache_ops.h"
 #include "hpc_internal.h"
+#include "kv4.cuh"
 
 using namespace hpc;
 
@@ -58,52 +59,7 @@ bool overlap(const hpc_tensor* a, const hpc_tensor* b) {
   return x < end(b) && y < end(a);
 }
 
-// Rows [tokens][heads] of a fixed number of bytes, strides in bytes.
-struct Rows {
-  const char* p;
-  int64_t n, h, sn, sh, row;
-  Rows(const hpc_tensor* t, int64_t elt)
-      : p((const char*)t->data), n(t->shape[0]), h(t->shape[1]), sn(t->stride[0] * elt),
-        sh(t->stride[1] * elt), row(kHeadDim * elt) {}
-  const char* end() const { return p + (n - 1) * sn + (h - 1) * sh + row; }
-};
-
 int64_t floor_div(int64_t a, int64_t b) { return a / b - (a % b != 0 && (a < 0) != (b < 0)); }
-
-// Whether a row of `a` shares bytes with one of `b` (itself: with another one of its
-// rows). Exact for equal strides, as views of one buffer have them. With unequal
-// token strides byte ranges that meet count as overlapping, with unequal head
-// strides the ranges of a token's rows.
-bool rows_overlap(Rows a, Rows b, bool itself = false) {
-  if (a.n == 0 || b.n == 0 || a.end() <= b.p || b.end() <= a.p) return false;
-  if (a.n == 1) a.sn = b.sn;  // a stride that no row is reached by
-  if (b.n == 1) b.sn = a.sn;
-  if (a.h == 1) a.sh = b.sh;
-  if (b.h == 1) b.sh = a.sh;
-  if (a.n == 1 && b.n == 1) a.sn = b.sn = 0;
-  if (a.h == 1 && b.h == 1) a.sh = b.sh = 0;
-  if (a.sn != b.sn) return true;
-  const int64_t sn = a.sn, d = b.p - a.p;
-  const int64_t ea = (a.h - 1) * a.sh + a.row, eb = (b.h - 1) * b.sh + b.row;  // a token's extent
-  if (itself) {
-    if ((a.h == 1 || a.sh >= a.row) && (a.n == 1 || sn >= ea)) return false;
-  } else if (sn > 0) {
-    const int64_t at = d - floor_div(d, sn) * sn;  // b's tokens behind a's, modulo the stride
-    if (ea <= at && at + eb <= sn) return false;
-  }
-  if (a.sh != b.sh) return true;
-  const int64_t sh = a.sh;
-  // row (n, h) of a and (n + i, h + j) of b are d + i sn + j sh bytes apart
-  for (int64_t j = -(a.h - 1); j < b.h; ++j) {
-    const int64_t x = d + j * sh;
-    int64_t lo = -(a.n - 1);
-    if (sn > 0) lo = std::max(lo, floor_div(-b.row - x, sn) + 1);  // the first with x + i sn > -b.row
-    if (itself && j == 0 && lo == 0) ++lo;
-    for (int64_t i = lo; i < b.n && x + i * sn < a.row; ++i)
-      if (x + i * sn > -b.row && !(itself && i == 0 && j == 0)) return true;
-  }
-  return false;
-}
 
 // What append and truncate have in common: the lengths, the table and the
 // stack of free blocks.
@@ -135,6 +91,224 @@ hpc_status check_pool(const hpc_tensor* seq_lens, const hpc_tensor* other, const
                                          " sequences in one call");
   if (!aligned(block_table->data, 4))
     return fail(HPC_ERR_INVALID_ARG, "block_table is misaligned");
+  return HPC_OK;
+}
+
+}  // namespace
+
+namespace hpc {
+
+// Whether a row of `a` shares bytes with one of `b` (itself: with another one of its
+// rows). Exact for equal strides, as views of one buffer have them. With unequal
+// token strides byte ranges that meet count as overlapping, with unequal head
+// strides the ranges of a token's rows.
+bool rows_overlap(Rows a, Rows b, bool itself) {
+  if (a.n == 0 || b.n == 0 || a.end() <= b.p || b.end() <= a.p) return false;
+  if (a.n == 1) a.sn = b.sn;  // a stride that no row is reached by
+  if (b.n == 1) b.sn = a.sn;
+  if (a.h == 1) a.sh = b.sh;
+  if (b.h == 1) b.sh = a.sh;
+  if (a.n == 1 && b.n == 1) a.sn = b.sn = 0;
+  if (a.h == 1 && b.h == 1) a.sh = b.sh = 0;
+  if (a.sn != b.sn) return true;
+  const int64_t sn = a.sn, d = b.p - a.p;
+  const int64_t ea = (a.h - 1) * a.sh + a.row, eb = (b.h - 1) * b.sh + b.row;  // a token's extent
+  if (itself) {
+    if ((a.h == 1 || a.sh >= a.row) && (a.n == 1 || sn >= ea)) return false;
+  } else if (sn > 0) {
+    const int64_t at = d - floor_div(d, sn) * sn;  // b's tokens behind a's, modulo the stride
+    if (ea <= at && at + eb <= sn) return false;
+  }
+  if (a.sh != b.sh) return true;
+  const int64_t sh = a.sh;
+  // row (n, h) of a and (n + i, h + j) of b are d + i sn + j sh bytes apart
+  for (int64_t j = -(a.h - 1); j < b.h; ++j) {
+    const int64_t x = d + j * sh;
+    int64_t lo = -(a.n - 1);
+    if (sn > 0) lo = std::max(lo, floor_div(-b.row - x, sn) + 1);  // the first with x + i sn > -b.row
+    if (itself && j == 0 && lo == 0) ++lo;
+    for (int64_t i = lo; i < b.n && x + i * sn < a.row; ++i)
+      if (x + i * sn > -b.row && !(itself && i == 0 && j == 0)) return true;
+  }
+  return false;
+}
+
+}  // namespace hpc
+
+namespace {
+
+// hpc_rope_kv_write, and hpc_rope_kv4_write where the caches are 4-bit rows.
+hpc_status rope_write(const hpc_tensor* q_in, const hpc_tensor* k_in, const hpc_tensor* v_in,
+                      const hpc_tensor* positions, const hpc_tensor* slots, const hpc_rope* rope,
+                      const hpc_tensor* q_norm_weight, const hpc_tensor* k_norm_weight, float eps,
+                      hpc_tensor* q_out, hpc_tensor* q_out_fp8, hpc_tensor* k_cache,
+                      hpc_tensor* v_cache, bool kv4, int32_t* device_error, void* stream) {
+  hpc_status st;
+  const hpc_tensor* rows[] = {q_in, k_in, v_in, q_out};
+  const char* names[] = {"q_in", "k_in", "v_in", "q_out"};
+  for (int i = 0; i < 4; ++i)
+    if (!empty(rows[i], 3) && (st = check_tensor(rows[i], names[i], 3)) != HPC_OK) return st;
+  const int64_t N = q_in->shape[0], Hq = q_in->shape[1], Hkv = k_in->shape[1];
+  if ((st = check_vec(positions, "positions", N)) != HPC_OK) return st;
+  if ((st = check_vec(slots, "slots", N)) != HPC_OK) return st;
+  if ((st = check_tensor(k_cache, "k_cache", 4)) != HPC_OK) return st;
+  if ((st = check_tensor(v_cache, "v_cache", 4)) != HPC_OK) return st;
+  if ((st = check_tensor(q_norm_weight, "q_norm_weight", 1, true)) != HPC_OK) return st;
+  if ((st = check_tensor(k_norm_weight, "k_norm_weight", 1, true)) != HPC_OK) return st;
+  const bool has_qf = q_out_fp8 && (q_out_fp8->data || empty(q_out_fp8, 3));
+  if (!rope) return fail(HPC_ERR_INVALID_ARG, "rope is null");
+  if (rope->rot_dim < 2 || rope->rot_dim > kHeadDim || rope->rot_dim % 2 ||
+      (rope->interleaved != 0 && rope->interleaved != 1) || !std::isfinite(rope->magnitude))
+    return fail(HPC_ERR_INVALID_ARG, "rope must come from hpc_rope_init");
+  for (int i = 0; i < rope->rot_dim / 2; ++i)
+    if (!(std::fabs(rope->freq_hi[i]) <= 1.f) || !(std::fabs(rope->freq_lo[i]) <= 1.f))
+      return fail(HPC_ERR_INVALID_ARG, "rope must come from hpc_rope_init");
+  for (const hpc_tensor* t : rows) {
+    if (t->dtype != HPC_BF16)
+      return fail(HPC_ERR_INVALID_ARG, "q_in, k_in, v_in and q_out must be bf16");
+    if (t->shape[2] != kHeadDim) return fail(HPC_ERR_UNSUPPORTED, "head_dim must be 128");
+    if (t->shape[0] != N) return fail(HPC_ERR_INVALID_ARG, "q/k/v/out hold different tokens");
+    if (t->stride[2] != 1 || t->stride[0] % 8 || t->stride[1] % 8 || !aligned(t->data, 16))
+      return fail(HPC_ERR_INVALID_ARG,
+                  "q/k/v/out rows must be contiguous and 16-byte aligned");
+  }
+  if (kv4) {
+    if ((st = check_kv4_caches(k_cache, v_cache)) != HPC_OK) return st;
+    // so that 6 * scale and an e4m3 times it are normal numbers, whose reciprocals are too
+    for (const hpc_tensor* t : {k_cache, v_cache})
+      if (!(t->scale >= 0x1p-100f && t->scale <= 0x1p100f))
+        return fail(HPC_ERR_INVALID_ARG, "4-bit caches are written with scales of 2^-100 to 2^100");
+    Rows k_tiles(k_cache, 1), v_tiles(v_cache, 1);  // [blocks][heads] of a tile's bytes
+    k_tiles.row = v_tiles.row = kKv4Tile;
+    if (rows_overlap(k_tiles, k_tiles, true) || rows_overlap(k_tiles, v_tiles))
+      return fail(HPC_ERR_INVALID_ARG, "tiles of the caches overlap");
+  } else {
+    if (k_cache->shape[3] != kHeadDim) return fail(HPC_ERR_UNSUPPORTED, "head_dim must be 128");
+    if (k_cache->shape[2] != kBlockTokens)
+      return fail(HPC_ERR_UNSUPPORTED, "KV blocks must hold 64 tokens");
+  }
+  if (Hkv <= 0 || Hq <= 0 || Hq % Hkv || v_in->shape[1] != Hkv || q_out->shape[1] != Hq ||
+      k_cache->shape[1] != Hkv)
+    return fail(HPC_ERR_INVALID_ARG, "inconsistent heads of q/k/v/out/cache");
+  if (Hq > 65536 || Hkv > 65536) return fail(HPC_ERR_UNSUPPORTED, "at most 65536 heads");
+  // q may be rotated in place, rows on their own rows; anything else would
+  // read what another CTA has written
+  const bool in_place = q_out->data == q_in->data &&
+                        (N <= 1 || q_out->stride[0] == q_in->stride[0]) &&
+                        (Hq == 1 || q_out->stride[1] == q_in->stride[1]);
+  const Rows out_rows(q_out, 2);
+  if (rows_overlap(out_rows, out_rows, true))
+    return fail(HPC_ERR_INVALID_ARG, "rows of q_out overlap");
+  if (!in_place && rows_overlap(out_rows, Rows(q_in, 2)))
+    return fail(HPC_ERR_INVALID_ARG, "q_out overlaps q_in other than in place (its rows and strides)");
+  if (rows_overlap(out_rows, Rows(k_in, 2)) || rows_overlap(out_rows, Rows(v_in, 2)))
+    return fail(HPC_ERR_INVALID_ARG, "q_out overlaps k_in or v_in");
+  if (has_qf && (q_out_fp8->dtype != HPC_FP8_E4M3 || q_out_fp8->ndim != 3 ||
+                 q_out_fp8->shape[0] != N || q_out_fp8->shape[1] != Hq ||
+                 q_out_fp8->shape[2] != kHeadDim || q_out_fp8->stride[2] != 1 ||
+                 q_out_fp8->stride[0] % 8 || q_out_fp8->stride[1] % 8 ||
+                 q_out_fp8->stride[0] < 0 || q_out_fp8->stride[1] < 0 ||
+                 !aligned(q_out_fp8->data, 8) || !(q_out_fp8->scale > 0.f) ||
+                 !std::isfinite(q_out_fp8->scale)))
+    return fail(HPC_ERR_INVALID_ARG, "q_out_fp8 must be e4m3 [N][H_q][128] with a positive scale");
+  if (has_qf) {
+    const Rows fp8_rows(q_out_fp8, 1);
+    if (rows_overlap(fp8_rows, fp8_rows, true))
+      return fail(HPC_ERR_INVALID_ARG, "rows of q_out_fp8 overlap");
+    for (const hpc_tensor* t : rows)
+      if (rows_overlap(fp8_rows, Rows(t, 2)))
+        return fail(HPC_ERR_INVALID_ARG, "q_out_fp8 overlaps q_in, k_in, v_in or q_out");
+  }
+  for (const hpc_tensor* w : {q_norm_weight, k_norm_weight})
+    if (w && w->data && ((w->dtype != HPC_BF16 && w->dtype != HPC_F32) ||
+                         w->shape[0] != kHeadDim || w->stride[0] != 1 || !aligned(w->data, 16)))
+      return fail(HPC_ERR_INVALID_ARG,
+                  "norm weights must be contiguous bf16/f32 [128], 16-B aligned");
+  if (!(eps >= 0.f) || !std::isfinite(eps))
+    return fail(HPC_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (!kv4 && (k_cache->dtype != v_cache->dtype ||
+               (k_cache->dtype != HPC_BF16 && k_cache->dtype != HPC_FP8_E4M3)))
+    return fail(HPC_ERR_INVALID_ARG, "k_cache/v_cache must both be bf16 or both fp8_e4m3");
+  const bool fp8 = k_cache->dtype == HPC_FP8_E4M3;
+  for (int i = 0; i < 4; ++i)
+    if (k_cache->shape[i] != v_cache->shape[i] || k_cache->stride[i] != v_cache->stride[i])
+      return fail(HPC_ERR_INVALID_ARG, "k_cache and v_cache must have the same shape and strides");
+  const uintptr_t unit = fp8 ? 8 : 16;  // bytes of one store
+  if (!kv4 &&
+      (k_cache->stride[3] != 1 || k_cache->stride[0] % 8 || k_cache->stride[1] % 8 ||
+       k_cache->stride[2] % 8 || !aligned(k_cache->data, unit) || !aligned(v_cache->data, unit)))
+    return fail(HPC_ERR_INVALID_ARG, "cache rows must be contiguous and aligned to 8 elements");
+  if (fp8 && (!(k_cache->scale > 0.f) || !(v_cache->scale > 0.f) ||
+              !std::isfinite(k_cache->scale) || !std::isfinite(v_cache->scale)))
+    return fail(HPC_ERR_INVALID_ARG, "FP8 caches need positive finite scales");
+  if (N == 0) return HPC_OK;
+  for (const hpc_tensor* c : {k_cache, v_cache}) {
+    int64_t last = c->shape[3] - 1;
+    for (int i = 0; i < 3; ++i) last += std::max<int64_t>(c->shape[i] - 1, 0) * c->stride[i];
+    const char* begin = (const char*)c->data;
+    const char* end = begin + (last + 1) * (fp8 || kv4 ? 1 : 2);
+    auto inside = [&](const Rows& r) { return r.p < end && begin < r.end(); };
+    if (inside(out_rows) || (has_qf && inside(Rows(q_out_fp8, 1))))
+      return fail(HPC_ERR_INVALID_ARG, "q_out or q_out_fp8 overlaps a cache");
+    if (kv4 && (inside(Rows(q_in, 2)) || inside(Rows(k_in, 2)) || inside(Rows(v_in, 2))))
+      return fail(HPC_ERR_INVALID_ARG, "q_in, k_in or v_in overlaps a cache");
+  }
+  if (kv4 && (st = check_device_memory(k_cache->data, "k_cache")) != HPC_OK) return st;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess)
+    return fail(HPC_ERR_CUDA, std::string("device query: ") + cudaGetErrorString(e));
+  RopeParams p;
+  std::memset(&p, 0, sizeof p);
+  p.q_in = (const __nv_bfloat16*)q_in->data; p.qi_sn = q_in->stride[0]; p.qi_sh = q_in->stride[1];
+  p.k_in = (const __nv_bfloat16*)k_in->data; p.ki_sn = k_in->stride[0]; p.ki_sh = k_in->stride[1];
+  p.v_in = (const __nv_bfloat16*)v_in->data; p.vi_sn = v_in->stride[0]; p.vi_sh = v_in->stride[1];
+  p.positions = (const int32_t*)positions->data;
+  p.slots = (const int32_t*)slots->data;
+  p.num_tokens = N;
+  p.num_q_heads = (int32_t)Hq;
+  p.num_kv_heads = (int32_t)Hkv;
+  p.num_blocks = (int32_t)(k_cache->shape[0] < INT_MAX ? k_cache->shape[0] : INT_MAX);
+  if (q_norm_weight && q_norm_weight->data) {
+    p.wq = q_norm_weight->data;
+    p.wq_dtype = q_norm_weight->dtype;
+  }
+  if (k_norm_weight && k_norm_weight->data) {
+    p.wk = k_norm_weight->data;
+    p.wk_dtype = k_norm_weight->dtype;
+  }
+  p.eps = eps;
+  p.rot_dim = rope->rot_dim;
+  p.interleaved = rope->interleaved;
+  p.magnitude = rope->magnitude;
+  std::memcpy(p.freq_hi, rope->freq_hi, sizeof p.freq_hi);
+  std::memcpy(p.freq_lo, rope->freq_lo, sizeof p.freq_lo);
+  // 2 pi = 6.28318530717958647692528676655900577; the double holds 53 bits,
+  // the third float takes what it leaves out as well
+  const double two_pi = 6.283185307179586;         // nearest double
+  const double rest = 2.4492935982947064e-16;      // 2 pi minus it
+  p.two_pi[0] = (float)two_pi;
+  p.two_pi[1] = (float)(two_pi - (double)p.two_pi[0]);
+  p.two_pi[2] = (float)(two_pi - (double)p.two_pi[0] - (double)p.two_pi[1] + rest);
+  p.q_out = (__nv_bfloat16*)q_out->data; p.qo_sn = q_out->stride[0]; p.qo_sh = q_out->stride[1];
+  if (has_qf) {
+    p.q_fp8 = (uint8_t*)q_out_fp8->data;
+    p.qf_sn = q_out_fp8->stride[0];
+    p.qf_sh = q_out_fp8->stride[1];
+    p.q_fp8_scale = e4m3_scale(q_out_fp8->scale);
+  }
+  p.k_cache = k_cache->data;
+  p.v_cache = v_cache->data;
+  p.c_sblk = k_cache->stride[0]; p.c_shead = k_cache->stride[1]; p.c_sslot = k_cache->stride[2];
+  p.cache_fp8 = fp8;
+  p.cache_kv4 = kv4;
+  p.k_scale = e4m3_scale(fp8 || kv4 ? k_cache->scale : 1.f);
+  p.v_scale = e4m3_scale(fp8 || kv4 ? v_cache->scale : 1.f);
+  p.err = device_error;
+  e = launch_rope(p, sms, (cudaStream_t)stream);
+  if (e != cudaSuccess)
+    return fail(HPC_ERR_CUDA, std::string("rope launch: ") + cudaGetErrorString(e));
   return HPC_OK;
 }
 
@@ -311,157 +485,21 @@ hpc_status hpc_rope_kv_write(const hpc_tensor* q_in, const hpc_tensor* k_in, con
                              const hpc_tensor* k_norm_weight, float eps, hpc_tensor* q_out,
                              hpc_tensor* q_out_fp8, hpc_tensor* k_cache, hpc_tensor* v_cache,
                              int32_t* device_error, void* stream) {
-  return guarded([&]() -> hpc_status {
-    hpc_status st;
-    const hpc_tensor* rows[] = {q_in, k_in, v_in, q_out};
-    const char* names[] = {"q_in", "k_in", "v_in", "q_out"};
-    for (int i = 0; i < 4; ++i)
-      if (!empty(rows[i], 3) && (st = check_tensor(rows[i], names[i], 3)) != HPC_OK) return st;
-    const int64_t N = q_in->shape[0], Hq = q_in->shape[1], Hkv = k_in->shape[1];
-    if ((st = check_vec(positions, "positions", N)) != HPC_OK) return st;
-    if ((st = check_vec(slots, "slots", N)) != HPC_OK) return st;
-    if ((st = check_tensor(k_cache, "k_cache", 4)) != HPC_OK) return st;
-    if ((st = check_tensor(v_cache, "v_cache", 4)) != HPC_OK) return st;
-    if ((st = check_tensor(q_norm_weight, "q_norm_weight", 1, true)) != HPC_OK) return st;
-    if ((st = check_tensor(k_norm_weight, "k_norm_weight", 1, true)) != HPC_OK) return st;
-    const bool has_qf = q_out_fp8 && (q_out_fp8->data || empty(q_out_fp8, 3));
-    if (!rope) return fail(HPC_ERR_INVALID_ARG, "rope is null");
-    if (rope->rot_dim < 2 || rope->rot_dim > kHeadDim || rope->rot_dim % 2 ||
-        (rope->interleaved != 0 && rope->interleaved != 1) || !std::isfinite(rope->magnitude))
-      return fail(HPC_ERR_INVALID_ARG, "rope must come from hpc_rope_init");
-    for (int i = 0; i < rope->rot_dim / 2; ++i)
-      if (!(std::fabs(rope->freq_hi[i]) <= 1.f) || !(std::fabs(rope->freq_lo[i]) <= 1.f))
-        return fail(HPC_ERR_INVALID_ARG, "rope must come from hpc_rope_init");
-    for (const hpc_tensor* t : rows) {
-      if (t->dtype != HPC_BF16)
-        return fail(HPC_ERR_INVALID_ARG, "q_in, k_in, v_in and q_out must be bf16");
-      if (t->shape[2] != kHeadDim) return fail(HPC_ERR_UNSUPPORTED, "head_dim must be 128");
-      if (t->shape[0] != N) return fail(HPC_ERR_INVALID_ARG, "q/k/v/out hold different tokens");
-      if (t->stride[2] != 1 || t->stride[0] % 8 || t->stride[1] % 8 || !aligned(t->data, 16))
-        return fail(HPC_ERR_INVALID_ARG,
-                    "q/k/v/out rows must be contiguous and 16-byte aligned");
-    }
-    if (k_cache->shape[3] != kHeadDim) return fail(HPC_ERR_UNSUPPORTED, "head_dim must be 128");
-    if (k_cache->shape[2] != kBlockTokens)
-      return fail(HPC_ERR_UNSUPPORTED, "KV blocks must hold 64 tokens");
-    if (Hkv <= 0 || Hq <= 0 || Hq % Hkv || v_in->shape[1] != Hkv || q_out->shape[1] != Hq ||
-        k_cache->shape[1] != Hkv)
-      return fail(HPC_ERR_INVALID_ARG, "inconsistent heads of q/k/v/out/cache");
-    if (Hq > 65536 || Hkv > 65536) return fail(HPC_ERR_UNSUPPORTED, "at most 65536 heads");
-    // q may be rotated in place, rows on their own rows; anything else would
-    // read what another CTA has written
-    const bool in_place = q_out->data == q_in->data &&
-                          (N <= 1 || q_out->stride[0] == q_in->stride[0]) &&
-                          (Hq == 1 || q_out->stride[1] == q_in->stride[1]);
-    const Rows out_rows(q_out, 2);
-    if (rows_overlap(out_rows, out_rows, true))
-      return fail(HPC_ERR_INVALID_ARG, "rows of q_out overlap");
-    if (!in_place && rows_overlap(out_rows, Rows(q_in, 2)))
-      return fail(HPC_ERR_INVALID_ARG, "q_out overlaps q_in other than in place (its rows and strides)");
-    if (rows_overlap(out_rows, Rows(k_in, 2)) || rows_overlap(out_rows, Rows(v_in, 2)))
-      return fail(HPC_ERR_INVALID_ARG, "q_out overlaps k_in or v_in");
-    if (has_qf && (q_out_fp8->dtype != HPC_FP8_E4M3 || q_out_fp8->ndim != 3 ||
-                   q_out_fp8->shape[0] != N || q_out_fp8->shape[1] != Hq ||
-                   q_out_fp8->shape[2] != kHeadDim || q_out_fp8->stride[2] != 1 ||
-                   q_out_fp8->stride[0] % 8 || q_out_fp8->stride[1] % 8 ||
-                   q_out_fp8->stride[0] < 0 || q_out_fp8->stride[1] < 0 ||
-                   !aligned(q_out_fp8->data, 8) || !(q_out_fp8->scale > 0.f) ||
-                   !std::isfinite(q_out_fp8->scale)))
-      return fail(HPC_ERR_INVALID_ARG, "q_out_fp8 must be e4m3 [N][H_q][128] with a positive scale");
-    if (has_qf) {
-      const Rows fp8_rows(q_out_fp8, 1);
-      if (rows_overlap(fp8_rows, fp8_rows, true))
-        return fail(HPC_ERR_INVALID_ARG, "rows of q_out_fp8 overlap");
-      for (const hpc_tensor* t : rows)
-        if (rows_overlap(fp8_rows, Rows(t, 2)))
-          return fail(HPC_ERR_INVALID_ARG, "q_out_fp8 overlaps q_in, k_in, v_in or q_out");
-    }
-    for (const hpc_tensor* w : {q_norm_weight, k_norm_weight})
-      if (w && w->data && ((w->dtype != HPC_BF16 && w->dtype != HPC_F32) ||
-                           w->shape[0] != kHeadDim || w->stride[0] != 1 || !aligned(w->data, 16)))
-        return fail(HPC_ERR_INVALID_ARG,
-                    "norm weights must be contiguous bf16/f32 [128], 16-B aligned");
-    if (!(eps >= 0.f) || !std::isfinite(eps))
-      return fail(HPC_ERR_INVALID_ARG, "eps must be finite and >= 0");
-    if (k_cache->dtype != v_cache->dtype ||
-        (k_cache->dtype != HPC_BF16 && k_cache->dtype != HPC_FP8_E4M3))
-      return fail(HPC_ERR_INVALID_ARG, "k_cache/v_cache must both be bf16 or both fp8_e4m3");
-    const bool fp8 = k_cache->dtype == HPC_FP8_E4M3;
-    for (int i = 0; i < 4; ++i)
-      if (k_cache->shape[i] != v_cache->shape[i] || k_cache->stride[i] != v_cache->stride[i])
-        return fail(HPC_ERR_INVALID_ARG, "k_cache and v_cache must have the same shape and strides");
-    const uintptr_t unit = fp8 ? 8 : 16;  // bytes of one store
-    if (k_cache->stride[3] != 1 || k_cache->stride[0] % 8 || k_cache->stride[1] % 8 ||
-        k_cache->stride[2] % 8 || !aligned(k_cache->data, unit) || !aligned(v_cache->data, unit))
-      return fail(HPC_ERR_INVALID_ARG, "cache rows must be contiguous and aligned to 8 elements");
-    if (fp8 && (!(k_cache->scale > 0.f) || !(v_cache->scale > 0.f) ||
-                !std::isfinite(k_cache->scale) || !std::isfinite(v_cache->scale)))
-      return fail(HPC_ERR_INVALID_ARG, "FP8 caches need positive finite scales");
-    if (N == 0) return HPC_OK;
-    for (const hpc_tensor* c : {k_cache, v_cache}) {
-      int64_t last = kHeadDim - 1;
-      for (int i = 0; i < 3; ++i) last += std::max<int64_t>(c->shape[i] - 1, 0) * c->stride[i];
-      const char* begin = (const char*)c->data;
-      const char* end = begin + (last + 1) * (fp8 ? 1 : 2);
-      auto inside = [&](const Rows& r) { return r.p < end && begin < r.end(); };
-      if (inside(out_rows) || (has_qf && inside(Rows(q_out_fp8, 1))))
-        return fail(HPC_ERR_INVALID_ARG, "q_out or q_out_fp8 overlaps a cache");
-    }
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess)
-      return fail(HPC_ERR_CUDA, std::string("device query: ") + cudaGetErrorString(e));
-    RopeParams p;
-    std::memset(&p, 0, sizeof p);
-    p.q_in = (const __nv_bfloat16*)q_in->data; p.qi_sn = q_in->stride[0]; p.qi_sh = q_in->stride[1];
-    p.k_in = (const __nv_bfloat16*)k_in->data; p.ki_sn = k_in->stride[0]; p.ki_sh = k_in->stride[1];
-    p.v_in = (const __nv_bfloat16*)v_in->data; p.vi_sn = v_in->stride[0]; p.vi_sh = v_in->stride[1];
-    p.positions = (const int32_t*)positions->data;
-    p.slots = (const int32_t*)slots->data;
-    p.num_tokens = N;
-    p.num_q_heads = (int32_t)Hq;
-    p.num_kv_heads = (int32_t)Hkv;
-    p.num_blocks = (int32_t)(k_cache->shape[0] < INT_MAX ? k_cache->shape[0] : INT_MAX);
-    if (q_norm_weight && q_norm_weight->data) {
-      p.wq = q_norm_weight->data;
-      p.wq_dtype = q_norm_weight->dtype;
-    }
-    if (k_norm_weight && k_norm_weight->data) {
-      p.wk = k_norm_weight->data;
-      p.wk_dtype = k_norm_weight->dtype;
-    }
-    p.eps = eps;
-    p.rot_dim = rope->rot_dim;
-    p.interleaved = rope->interleaved;
-    p.magnitude = rope->magnitude;
-    std::memcpy(p.freq_hi, rope->freq_hi, sizeof p.freq_hi);
-    std::memcpy(p.freq_lo, rope->freq_lo, sizeof p.freq_lo);
-    // 2 pi = 6.28318530717958647692528676655900577; the double holds 53 bits,
-    // the third float takes what it leaves out as well
-    const double two_pi = 6.283185307179586;         // nearest double
-    const double rest = 2.4492935982947064e-16;      // 2 pi minus it
-    p.two_pi[0] = (float)two_pi;
-    p.two_pi[1] = (float)(two_pi - (double)p.two_pi[0]);
-    p.two_pi[2] = (float)(two_pi - (double)p.two_pi[0] - (double)p.two_pi[1] + rest);
-    p.q_out = (__nv_bfloat16*)q_out->data; p.qo_sn = q_out->stride[0]; p.qo_sh = q_out->stride[1];
-    if (has_qf) {
-      p.q_fp8 = (uint8_t*)q_out_fp8->data;
-      p.qf_sn = q_out_fp8->stride[0];
-      p.qf_sh = q_out_fp8->stride[1];
-      p.q_fp8_scale = e4m3_scale(q_out_fp8->scale);
-    }
-    p.k_cache = k_cache->data;
-    p.v_cache = v_cache->data;
-    p.c_sblk = k_cache->stride[0]; p.c_shead = k_cache->stride[1]; p.c_sslot = k_cache->stride[2];
-    p.cache_fp8 = fp8;
-    p.k_scale = e4m3_scale(fp8 ? k_cache->scale : 1.f);
-    p.v_scale = e4m3_scale(fp8 ? v_cache->scale : 1.f);
-    p.err = device_error;
-    e = launch_rope(p, sms, (cudaStream_t)stream);
-    if (e != cudaSuccess)
-      return fail(HPC_ERR_CUDA, std::string("rope launch: ") + cudaGetErrorString(e));
-    return HPC_OK;
+  return guarded([&] {
+    return rope_write(q_in, k_in, v_in, positions, slots, rope, q_norm_weight, k_norm_weight, eps,
+                      q_out, q_out_fp8, k_cache, v_cache, false, device_error, stream);
+  });
+}
+
+hpc_status hpc_rope_kv4_write(const hpc_tensor* q_in, const hpc_tensor* k_in,
+                              const hpc_tensor* v_in, const hpc_tensor* positions,
+                              const hpc_tensor* slots, const hpc_rope* rope,
+                              const hpc_tensor* q_norm_weight, const hpc_tensor* k_norm_weight,
+                              float eps, hpc_tensor* q_out, hpc_tensor* k_cache,
+                              hpc_tensor* v_cache, int32_t* device_error, void* stream) {
+  return guarded([&] {
+    return rope_write(q_in, k_in, v_in, positions, slots, rope, q_norm_weight, k_norm_weight, eps,
+                      q_out, nullptr, k_cache, v_cache, true, device_error, stream);
   });
 }
 

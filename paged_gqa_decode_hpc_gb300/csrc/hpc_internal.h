@@ -72,6 +72,7 @@ struct hpc_plan_s {
   size_t stage_bytes = 0;
   int64_t ws_floats = 0;         // floats allocated at d_ws
   int32_t prefix_q_len = 0;      // HPC_PLAN_PREFIX: new tokens per sequence it was sized for
+  int32_t max_q_len = 0;         // HPC_PLAN_KV4: the same
 };
 
 namespace hpc {
@@ -256,6 +257,28 @@ bool aligned(const void* p, uintptr_t a);
 hpc_status check_tensor(const hpc_tensor* t, const char* name, int ndim, bool nullable = false);
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
 hpc_status make_kv_map(const hpc_tensor* t, bool fp8, bool swap, CUtensorMap* map);
+// The extend kernel's map of q or out, and its query tiles per CTA (2 where that leaves
+// no more than half of the SMs idle).
+hpc_status make_q_map(const hpc_tensor* q, CUtensorMap* map, const char* what);
+int extend_tiles_per_cta(int64_t total_q, int64_t num_kv_heads, int sms);
+
+// Rows [tokens][heads] of a fixed number of bytes, strides in bytes, and whether a row of
+// one shares bytes with one of another (itself: with another one of its rows). Exact for
+// equal strides; with unequal ones byte ranges decide (capi_cache.cu).
+struct Rows {
+  const char* p;
+  int64_t n, h, sn, sh, row;
+  Rows(const hpc_tensor* t, int64_t elt)
+      : p((const char*)t->data), n(t->shape[0]), h(t->shape[1]), sn(t->stride[0] * elt),
+        sh(t->stride[1] * elt), row(kHeadDim * elt) {}
+  const char* end() const { return p + (n - 1) * sn + (h - 1) * sh + row; }
+};
+bool rows_overlap(Rows a, Rows b, bool itself = false);
+
+// Of capi_kv4.cu: memory that the current device's kernels may write, and a 4-bit cache
+// pair as every call takes it (types, shapes, strides, alignment, scales).
+hpc_status check_device_memory(const void* data, const char* name);
+hpc_status check_kv4_caches(const hpc_tensor* k_cache, const hpc_tensor* v_cache);
 
 // Every argument check hpc_decode_attn makes, with no launch and no
 // allocation (capi.cu).

@@ -1,0 +1,68 @@
+// Internal declarations of the attention over a 4-bit cache (kv4_decode_kernel.cu,
+// kv4_merge_kernel.cu, capi_kv4.cu); not part of the public ABI.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "hpc_decode.h"
+
+namespace hpc {
+
+// Sequences of one step: their prefix array lies in shared memory.
+constexpr int32_t kKv4MaxSeqs = 4096;
+// The step plan's constants (see step_kernel.cu for the rule): a pool of an eighth of
+// the units, chunks of at least kKv4MinChunk units and at most kKv4ChunksPerCta to a CTA.
+constexpr int32_t kKv4PoolDiv = 8, kKv4MinChunk = 8, kKv4ChunksPerCta = 4, kKv4MinPartDiv = 8,
+                  kKv4PartChunks = 12;
+// Most owners (parts and chunks) and partial-state slots of a step on `grid` CTAs.
+inline int64_t kv4_owners(int32_t grid) { return (int64_t)(1 + kKv4ChunksPerCta) * grid; }
+inline int64_t kv4_slots(int32_t grid) { return 2 * kv4_owners(grid); }
+// One token's partial state: 8 accumulator slices and (m, m, l, l) of every lane.
+constexpr int kKv4PartFloat4 = 9 * 32;
+
+struct Kv4DecodeParams {
+  const __nv_bfloat16* q;       // [B][q_len][H_q][128]
+  int64_t q_sb, q_st, q_sh;
+  __nv_bfloat16* out;
+  int64_t o_sb, o_st, o_sh;
+  float* lse;                   // may be null
+  int64_t l_sb, l_st, l_sh;
+  const uint8_t* k;             // [blocks][H_kv][64][72], strides in bytes
+  const uint8_t* v;
+  int64_t c_sblk, c_shead;
+  const int32_t* block_table;
+  int64_t bt_sb;
+  int32_t max_blocks;
+  const int32_t* seq_lens;
+  int32_t num_seqs, num_kv_heads, num_blocks, q_len;
+  float score_scale_log2;       // softmax_scale * log2(e) * K's scale, > 0
+  float v_scale;
+  float4* ws;                   // [slots][q_len][9][32]
+  int32_t* pool;                // [2]: next pool chunk, CTAs done claiming
+  int32_t* pair_cnt;            // [B * H_kv] pieces (or groups of them) that have arrived
+  int32_t* slot_cnt;            // [slots] pieces of a group that have arrived
+  int32_t* owners;              // [1 + 4 owners] (q_len > 1): their number, and of each the pair
+                                //   that it begins and others go on with {b, h, pieces, slot}
+  int32_t* err;
+  unsigned long long timeout_ns;
+  int32_t withhold_copies;
+};
+// int32 words of a plan's counters and records, in the order of the fields above.
+inline int64_t kv4_pair_off() { return 2; }
+inline int64_t kv4_slot_off(int32_t max_seqs, int32_t kv_heads) {
+  return kv4_pair_off() + (int64_t)max_seqs * kv_heads;
+}
+inline int64_t kv4_owner_off(int32_t max_seqs, int32_t kv_heads, int32_t grid) {
+  return (kv4_slot_off(max_seqs, kv_heads) + kv4_slots(grid) + 3) / 4 * 4;
+}
+inline int64_t kv4_words(int32_t max_seqs, int32_t kv_heads, int32_t grid) {
+  return kv4_owner_off(max_seqs, kv_heads, grid) + 4 + 4 * kv4_owners(grid);
+}
+
+cudaError_t launch_kv4_decode(const Kv4DecodeParams& p, int grid, cudaStream_t stream);
+// The split pairs of a step of several tokens, joined.
+cudaError_t launch_kv4_merge(const Kv4DecodeParams& p, int grid, cudaStream_t stream);
+
+}  // namespace hpc

@@ -1,0 +1,826 @@
+// Decode attention of one to eight new tokens per sequence over a 4-bit paged cache:
+// planned, computed and (one token) merged by a single persistent kernel.
+//
+//   s_t = scale * q . k_t,  out = sum_t exp(s_t - m) v_t / sum_t exp(s_t - m)
+//
+// over a sequence's 64-token tiles, one (tile, KV head) unit after another with a
+// running maximum and sum; the 8 query heads of a KV head and up to two new tokens
+// share a unit's K and V in registers. The plan is the one-token step's
+// (step_kernel.cu): static parts and a pool of chunks of units, taken in pieces of one
+// (sequence, KV head) pair, whose states are joined by log-sum-exp.
+//
+// What bounds it: HBM in the first place. A unit is 9216 bytes, 206 ns of an SM's share
+// of 6.8 TB/s, in which its 16384 codes have to become f16 operands. So a warp takes a
+// unit by itself: no value moves between warps, and each code is converted once for
+// both tokens of the warp (several warps take a unit where there are more tokens).
+//
+// How a unit gets into the MMAs (mma.sync m16n8k16, f16; S^T = K Q^T, O^T = V^T P^T):
+//  * A tile is copied as it lies in memory, 64 rows of 72 bytes. Rows are 18 words
+//    apart, so rows 4i + s, i = 0..7 (s fixed) start 8 banks apart modulo 32, and four
+//    of them with eight bytes of four lanes each cover all banks once.
+//  * The MMAs do not care in which order tokens, or the elements of a head, come, as
+//    long as both operands agree. Row i of an 8-row group s of a 32-token half is
+//    token 4 I(i) + s with I = 0 6 1 7 2 4 3 5: rows 0..3 and 4..7, which one access of K
+//    takes together, and rows 0 2 4 6 and 1 3 5 7, which one access of V does, then lie
+//    in different banks.
+//  * K: lane (g, c) reads eight bytes, elements 16c .. 16c + 15 and 64 + 16c .. , of its
+//    rows: neighbouring codes are neighbours of the contraction, and a conversion of a
+//    byte gives a register of the operand. Two scales a row.
+//  * V: its contraction runs over tokens, whose codes lie 72 bytes apart. Lane (g, c)
+//    reads eight bytes, elements 16g .. 16g + 15, of two tokens, and two shifts and two
+//    bit selects make bytes of one element's codes of both tokens. One scale a token.
+//  * Codes times scales are exact in f16 (kv4.cuh). Q takes a power of two that puts the
+//    largest of its 8 rows in [2^14, 2^15), P is rounded to f16 (2^-11), sums and states
+//    are fp32. The row maximum moves only when a score passes it by 8 (in log2 units),
+//    so that most units neither reduce it over the lanes nor rescale the sums; P then
+//    stays below 2^8.
+//  * Slots past a sequence's end may hold anything: scores of theirs are masked after
+//    the product, and V's scales of theirs become 0 (codes are finite).
+#include <cfloat>
+
+#include "decode_common.cuh"
+#include "hpc_internal.h"
+#include "kv4.cuh"
+#include "kv4.h"
+#include "kv4_state.cuh"
+#include "ptx.cuh"
+#include "step_plan.cuh"
+
+namespace hpc {
+namespace {
+
+constexpr int kEpilogueWarps = 2;                 // taking pieces in turn
+constexpr int kPieceQ = 4;                        // piece descriptors in flight
+static_assert(kPieceQ % kEpilogueWarps == 0, "queue slots per epilogue warp");
+constexpr int kDescInts = 8;
+constexpr int kDepVec = 5;                        // 16-byte words per lane of a deposited state
+constexpr int kStage = 2 * kKv4Tile;
+// Bookkeeping waits give up this many data waits later (see step_kernel.cu).
+constexpr unsigned long long kBookkeepingWaits = 8;
+constexpr int kClaimAhead = 2;                    // units left to issue when the next chunk is asked for
+constexpr int kFlagEnd = 1, kFlagWhole = 2;
+constexpr int kFan = 16;                          // pieces of a pair that are joined at once
+
+// TW tokens to a warp, NP warps to a unit, NC consumer warps (a multiple of NP).
+template <int TW, int NP, int NC>
+struct Cfg {
+  static constexpr int kThreads = (NC + 1 + kEpilogueWarps) * 32;
+  static constexpr int kDepBytes = NC * TW * kDepVec * 32 * 16;
+  static constexpr int kFixed = kDepBytes + 2048 /* barriers, descriptors, scan */ + 128 + 4 * (kKv4MaxSeqs + 1);
+  static constexpr int kStages = (227 * 1024 - kFixed) / kStage;
+  static constexpr int kDepOff = kStages * kStage;
+  static constexpr int kBarOff = kDepOff + kDepBytes;
+  // full, empty, piece full, piece free, deposit full (one per epilogue warp), deposit free
+  static constexpr int kNumBars = 2 * kStages + 2 * kPieceQ + kEpilogueWarps + 1;
+  static constexpr int kIssuedOff = kBarOff + 8 * kNumBars;
+  static constexpr int kDescOff = kIssuedOff + ((4 * kStages + 15) / 16) * 16;
+  static constexpr int kMiscOff = kDescOff + 4 * kDescInts * kPieceQ;
+  static constexpr int kPlanOff = kMiscOff + 256;  // abort flag, flags, scan scratch
+  static constexpr int kSmemBytes = 128 /* alignment slack */ + kPlanOff;
+  static constexpr int kSmemBytesMax = kSmemBytes + 4 * (kKv4MaxSeqs + 1);
+  static_assert(kSmemBytesMax <= 227 * 1024, "shared memory");
+  static_assert(NC % NP == 0, "whole groups of warps");
+  static_assert(kThreads <= 512, "a scan pass");
+};
+
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 r;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t a) {
+  uint32_t r;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ uint32_t prmt2(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+  return r;
+}
+// (a & m) | (b & ~m)
+__device__ __forceinline__ uint32_t select_bits(uint32_t a, uint32_t b, uint32_t m) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xE2;" : "=r"(r) : "r"(a), "r"(m), "r"(b));
+  return r;
+}
+
+// The token of row i of group 0 of a half, over 4.
+__device__ __forceinline__ int row_token(int i) { return (int)((0x53427160u >> (4 * i)) & 7u); }
+
+// A row of Q as B operands in K's order of elements: register j of k-step ks holds
+// elements 64 (ks / 4) + 16 c + 4 (ks % 4) + 2 j, + 1 of query head g. Returns the
+// factor that undoes the power of two of the conversion.
+__device__ __forceinline__ float load_q4(const __nv_bfloat16* q0, int64_t q_sh, int lane,
+                                         uint32_t (&qf)[8][2]) {
+  const int g = lane >> 2, c = lane & 3;
+  const __nv_bfloat16* row = q0 + (int64_t)g * q_sh + 16 * c;
+  uint4 u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    u[i] = __ldg(reinterpret_cast<const uint4*>(row + 64 * (i >> 1) + 8 * (i & 1)));
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[e] << 16)),
+                               fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
+  }
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  int e = 0;
+  if (amax > 0.f) {
+    e = 14 - ((int)((__float_as_uint(amax) >> 23) & 0xFF) - 127);
+    e = e < -113 ? -113 : (e > 100 ? 100 : e);
+  }
+  const float sc = __uint_as_float((uint32_t)(e + 127) << 23);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      qf[2 * i + (x >> 1)][x & 1] =
+          pack_f16(__uint_as_float(w[x] << 16) * sc, __uint_as_float(w[x] & 0xFFFF0000u) * sc);
+  }
+  return __uint_as_float((uint32_t)(127 - e) << 23);
+}
+
+// One unit for TW tokens. seen[t]: tokens of the tile that token t sees; stored: tokens
+// of the tile that are in the sequence.
+template <int TW>
+__device__ __forceinline__ void compute_unit4(uint32_t kb, uint32_t vb,
+                                              const uint32_t (&qf)[TW][8][2],
+                                              const int (&seen)[TW], int stored,
+                                              const float (&sl2)[TW], float (&m)[TW][2],
+                                              float (&l)[TW][2], float (&acc)[TW][8][4], int lane) {
+  const int g = lane >> 2, c = lane & 3;
+  const int ig = row_token(g);
+  float s[TW][4][4];
+#pragma unroll
+  for (int t = 0; t < TW; ++t)
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt) s[t][mt][0] = s[t][mt][1] = s[t][mt][2] = s[t][mt][3] = 0.f;
+
+  // ---- S^T = K Q^T: rows g and g + 8 of step mt are tokens 32 (mt / 2) + 4 I(g) + 2 (mt % 2) + 0, 1
+  const uint32_t k_lane = kb + (uint32_t)(ig * 4 * kKv4Row + 8 * c);
+  const uint32_t ks_lane = kb + (uint32_t)(ig * 4 * kKv4Row + kKv4Codes);
+  const uint32_t sel = (uint32_t)(c | ((4 + c) << 4));
+#pragma unroll
+  for (int mt = 0; mt < 4; ++mt) {
+    const uint32_t off = (uint32_t)((32 * (mt >> 1) + 2 * (mt & 1)) * kKv4Row);
+    const uint2 f0 = lds64(ks_lane + off), f1 = lds64(ks_lane + off + kKv4Row);
+    const uint32_t p0 = kv4_scales(prmt2(f0.x, f0.y, sel)), p1 = kv4_scales(prmt2(f1.x, f1.y, sel));
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      const uint2 x0 = lds64(k_lane + off + 32 * hf), x1 = lds64(k_lane + off + 32 * hf + kKv4Row);
+      const uint32_t f0h = hf ? both_high(p0) : both_low(p0), f1h = hf ? both_high(p1) : both_low(p1);
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        uint32_t a[4], b[4];
+        e2m1x8_to_f16(w ? x0.y : x0.x, a);
+        e2m1x8_to_f16(w ? x1.y : x1.x, b);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          a[i] = mul_f16x2(a[i], f0h);
+          b[i] = mul_f16x2(b[i], f1h);
+        }
+#pragma unroll
+        for (int t = 0; t < TW; ++t) {
+          const int ks = 4 * hf + 2 * w;
+          mma_f16(s[t][mt], a[0], b[0], a[1], b[1], qf[t][ks][0], qf[t][ks][1]);
+          mma_f16(s[t][mt], a[2], b[2], a[3], b[3], qf[t][ks + 1][0], qf[t][ks + 1][1]);
+        }
+      }
+    }
+  }
+
+  // ---- online softmax in the log2 domain; columns 2c and 2c + 1
+  uint32_t pb[TW][4][2];
+#pragma unroll
+  for (int t = 0; t < TW; ++t) {
+    if (seen[t] < 64) {
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          if (32 * (mt >> 1) + 4 * ig + 2 * (mt & 1) + r >= seen[t])
+            s[t][mt][2 * r] = s[t][mt][2 * r + 1] = -INFINITY;
+    }
+    float mx0 = fmaxf(s[t][0][0], s[t][0][2]), mx1 = fmaxf(s[t][0][1], s[t][0][3]);
+#pragma unroll
+    for (int mt = 1; mt < 4; ++mt) {
+      mx0 = fmaxf(mx0, fmaxf(s[t][mt][0], s[t][mt][2]));
+      mx1 = fmaxf(mx1, fmaxf(s[t][mt][1], s[t][mt][3]));
+    }
+    mx0 *= sl2[t];
+    mx1 *= sl2[t];
+    if (__any_sync(0xffffffffu, mx0 > m[t][0] + 8.f || mx1 > m[t][1] + 8.f)) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
+        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
+      }
+      const float n0 = fmaxf(m[t][0], mx0), n1 = fmaxf(m[t][1], mx1);
+      const float al0 = n0 == -INFINITY ? 1.f : ex2(m[t][0] - n0);
+      const float al1 = n1 == -INFINITY ? 1.f : ex2(m[t][1] - n1);
+      m[t][0] = n0;
+      m[t][1] = n1;
+      l[t][0] *= al0;
+      l[t][1] *= al1;
+#pragma unroll
+      for (int dm = 0; dm < 8; ++dm) {
+        acc[t][dm][0] *= al0;
+        acc[t][dm][1] *= al1;
+        acc[t][dm][2] *= al0;
+        acc[t][dm][3] *= al1;
+      }
+    }
+    // (a row that has seen no position yet: its scores are all -inf, its P is 0)
+    const float r0 = m[t][0] == -INFINITY ? 0.f : -m[t][0];
+    const float r1 = m[t][1] == -INFINITY ? 0.f : -m[t][1];
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt) {
+      const float e0 = ex2(fmaf(s[t][mt][0], sl2[t], r0)), e1 = ex2(fmaf(s[t][mt][1], sl2[t], r1));
+      const float e2 = ex2(fmaf(s[t][mt][2], sl2[t], r0)), e3 = ex2(fmaf(s[t][mt][3], sl2[t], r1));
+      l[t][0] += e0 + e2;
+      l[t][1] += e1 + e3;
+      pb[t][mt][0] = movm_trans(pack_f16(e0, e1));
+      pb[t][mt][1] = movm_trans(pack_f16(e2, e3));
+    }
+  }
+
+  // ---- O^T += V^T P^T: the k pairs of step kt are tokens ta, tb (rows 2c, 2c + 1) and ta + 1, tb + 1
+  const int ta = 4 * row_token(2 * c), tb = 4 * row_token(2 * c + 1);
+  const uint32_t va_lane = vb + (uint32_t)(ta * kKv4Row), vb_lane = vb + (uint32_t)(tb * kKv4Row);
+#pragma unroll
+  for (int kt = 0; kt < 4; ++kt) {
+    const int tok = 32 * (kt >> 1) + 2 * (kt & 1);
+    const uint32_t off = (uint32_t)(tok * kKv4Row);
+    uint32_t f[2];
+    uint2 xa[2], xb[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const uint32_t o = off + (uint32_t)(r * kKv4Row);
+      xa[r] = lds64(va_lane + o + 8 * g);
+      xb[r] = lds64(vb_lane + o + 8 * g);
+      f[r] = lds_u8(va_lane + o + kKv4Codes + g) | (lds_u8(vb_lane + o + kKv4Codes + g) << 8);
+      if (stored < 64) {
+        if (ta + tok + r >= stored) f[r] &= 0xFF00u;
+        if (tb + tok + r >= stored) f[r] &= 0x00FFu;
+      }
+      f[r] = kv4_scales(f[r]);
+    }
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      uint32_t a[2][2][4];  // [token pair][even, odd elements][byte]
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const uint32_t x = w ? xa[r].y : xa[r].x, y = w ? xb[r].y : xb[r].x;
+        e2m1x8_to_f16(select_bits(x, y << 4, 0x0F0F0F0Fu), a[r][0]);
+        e2m1x8_to_f16(select_bits(x >> 4, y, 0x0F0F0F0Fu), a[r][1]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          a[r][0][i] = mul_f16x2(a[r][0][i], f[r]);
+          a[r][1][i] = mul_f16x2(a[r][1][i], f[r]);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < TW; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          mma_f16(acc[t][4 * w + i], a[0][0][i], a[0][1][i], a[1][0][i], a[1][1][i], pb[t][kt][0],
+                  pb[t][kt][1]);
+    }
+  }
+}
+
+template <int TW, int NP, int NC>
+__global__ void __launch_bounds__(Cfg<TW, NP, NC>::kThreads, 1)
+    kv4_decode_kernel(const __grid_constant__ Kv4DecodeParams p) {
+  using C = Cfg<TW, NP, NC>;
+  constexpr int STAGES = C::kStages, kThreads = C::kThreads, kGroups = NC / NP;
+  constexpr int kProducerWarp = NC, kEpilogueWarp0 = NC + 1;
+  constexpr bool kOneToken = TW == 1;  // pieces are merged here, not by a second kernel
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) &
+                                             ~uintptr_t(127));
+  const uint32_t smem_base = smem_u32(smem);
+  const uint32_t bar_full = smem_base + C::kBarOff;
+  const uint32_t bar_empty = bar_full + 8 * STAGES;
+  const uint32_t bar_pfull = bar_empty + 8 * STAGES;
+  const uint32_t bar_pfree = bar_pfull + 8 * kPieceQ;
+  const uint32_t bar_dfull = bar_pfree + 8 * kPieceQ;  // + 8 * (piece % kEpilogueWarps)
+  const uint32_t bar_dfree = bar_dfull + 8 * kEpilogueWarps;
+  const uint32_t issued_word = smem_base + C::kIssuedOff;
+  int* desc = reinterpret_cast<int*>(smem + C::kDescOff);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff);
+  int* s_bad = reinterpret_cast<int*>(smem + C::kMiscOff + 8);
+  const unsigned long long book_ns = p.timeout_ns * kBookkeepingWaits;
+  int32_t* warp_tot = reinterpret_cast<int32_t*>(smem + C::kMiscOff + 128);
+  int32_t* cu = reinterpret_cast<int32_t*>(smem + C::kPlanOff);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
+  const int B = p.num_seqs, H = p.num_kv_heads, G = (int)gridDim.x, T = p.q_len;
+
+  if (tid == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(bar_full + 8 * s, 1);
+      mbar_init(bar_empty + 8 * s, NP);  // the warps of a unit
+      reinterpret_cast<volatile uint32_t*>(smem + C::kIssuedOff)[s] = 0xFFFFFFFFu;
+    }
+    for (int s = 0; s < kPieceQ; ++s) {
+      mbar_init(bar_pfull + 8 * s, 1);
+      mbar_init(bar_pfree + 8 * s, NC + 1);  // the consumer warps and the piece's epilogue warp
+    }
+    for (int e = 0; e < kEpilogueWarps; ++e) mbar_init(bar_dfull + 8 * e, NC);
+    mbar_init(bar_dfree, 1);
+    *abort_flag = 0;
+    *s_bad = 0;
+    cu[0] = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+  __syncthreads();
+
+  // ---- plan: units per sequence, prefix in shared memory
+  int64_t carry = 0;
+  for (int base = 0; base < B; base += kThreads) {
+    const int b = base + tid;
+    int32_t n = 0;
+    if (b < B) {
+      const int32_t len = p.seq_lens[b];
+      // a sequence of more units than INT32_MAX / 512 is reported, so that no partial sum
+      // of a scan pass, of at most 512 sequences, wraps
+      const int64_t units = len > 0 ? ((int64_t)len + kBlockTokens - 1) / kBlockTokens * H : 0;
+      if (len < 0 || units > (int64_t)(INT32_MAX / 512)) *s_bad = 1;
+      else n = (int32_t)units;
+    }
+    int32_t tot;
+    const int32_t incl = cta_inclusive_scan(n, warp_tot, &tot);
+    if (b < B) cu[b + 1] = (int32_t)(carry + incl);
+    carry += tot;
+  }
+  __syncthreads();
+  const bool bad = *s_bad != 0 || carry > INT32_MAX;
+  StepMath M;
+  M.T = bad ? 0u : (uint32_t)carry;
+  const uint32_t W = M.T / kKv4PoolDiv;
+  M.S = M.T - W;
+  {
+    const uint32_t want = (M.S + kKv4MinPartDiv - 1) / kKv4MinPartDiv;
+    M.P = want < (uint32_t)G ? want : (uint32_t)G;
+    const uint32_t per = (uint32_t)kKv4ChunksPerCta * (uint32_t)G;
+    uint32_t c = (W + per - 1) / per;
+    const uint32_t frac = (uint32_t)kKv4PartChunks * M.P;
+    const uint32_t twelfth = M.P > 0 ? (M.S + frac - 1) / frac : 0;
+    c = c > twelfth ? c : twelfth;
+    M.C = c > (uint32_t)kKv4MinChunk ? c : (uint32_t)kKv4MinChunk;
+  }
+  M.chunks = (W + M.C - 1) / M.C;
+  M.small = (uint64_t)(M.S + 1) * (M.P + 1) < (uint64_t)UINT32_MAX;
+  if (blockIdx.x == 0 && tid == 0) {
+    if (bad) atomicOr(p.err, HPC_DEVCHK_BAD_LENGTH);
+    if (!kOneToken) p.owners[0] = (int32_t)(M.P + M.chunks);
+  }
+  // sequences without tiles (or a bad step): out = 0, lse = -inf
+  {
+    const uint32_t rows_of = (uint32_t)(T * H * kGroup);  // of a sequence: below 2^17
+    for (int64_t r = (int64_t)blockIdx.x * kThreads + tid; r < (int64_t)B * rows_of;
+         r += (int64_t)G * kThreads) {
+      const int b = (int)(r / rows_of);
+      if (!bad && cu[b + 1] != cu[b]) continue;
+      const uint32_t x = (uint32_t)(r - (int64_t)b * rows_of);
+      const uint32_t t = x / (uint32_t)(H * kGroup), j = x % (uint32_t)(H * kGroup);
+      uint4* o = reinterpret_cast<uint4*>(p.out + (int64_t)b * p.o_sb + (int64_t)t * p.o_st +
+                                          (int64_t)j * p.o_sh);
+#pragma unroll
+      for (int i = 0; i < kHeadDim / 8; ++i) o[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (p.lse)
+        p.lse[(int64_t)b * p.l_sb + (int64_t)t * p.l_st + (int64_t)j * p.l_sh] = -INFINITY;
+    }
+  }
+
+  if (warp == kProducerWarp) {
+    // ------------------------------------------------------------ producer
+    const uint64_t policy = evict_first_policy();
+    bool stop = p.withhold_copies != 0;  // failure-path test: no copy is issued
+    bool lost = false;                   // the consumers stopped taking pieces
+    uint32_t g = 0, issued = 0;
+    int j = 0;
+    // ask the pool for a chunk: the atomic's result is consumed only when the current
+    // owner is done, so its latency hides behind the copies
+    int pend = 0;
+    bool asked = false;
+    auto ask = [&]() {
+      if (lane == 0) pend = atomicAdd(p.pool, 1);
+      asked = true;
+    };
+    auto resolve = [&]() -> int {
+      const int c = __shfl_sync(0xffffffffu, pend, 0);
+      asked = false;
+      return (uint32_t)c < M.chunks ? (int)(M.P + (uint32_t)c) : -1;
+    };
+    auto publish = [&](int b, int h, int t0, int t1, int flags, int slot) {
+      if (lane == 0 && !lost) {
+        const int qs = j % kPieceQ;
+        if (!wait_phase(bar_pfree + 8 * qs, ((j / kPieceQ) & 1u) ^ 1u, abort_flag, p.err,
+                        book_ns, false)) {
+          lost = true;
+        } else {
+          int* d = desc + qs * kDescInts;
+          d[0] = b; d[1] = h; d[2] = t0; d[3] = t1;
+          d[4] = flags; d[5] = slot; d[6] = (int)g; d[7] = 0;
+          mbar_arrive(bar_pfull + 8 * qs);  // release: the descriptor is visible to its waiters
+        }
+      }
+      ++j;
+    };
+    int owner;
+    if (blockIdx.x < M.P) {
+      owner = blockIdx.x;
+    } else {
+      ask();
+      owner = resolve();
+    }
+    // the sequence holding unit x (cu[b] <= x < cu[b + 1])
+    auto seq_at = [&](uint32_t x) -> int {
+      int l0 = 0, h0 = B;  // last b with cu[b] <= x, then past empty sequences
+      while (h0 - l0 > 1) {
+        const int mid = (l0 + h0) >> 1;
+        if ((uint32_t)cu[mid] <= x) l0 = mid; else h0 = mid;
+      }
+      while ((uint32_t)cu[l0 + 1] <= x) ++l0;
+      return l0;
+    };
+    while (owner >= 0) {
+      const uint32_t lo = M.start(owner), hi = M.end(owner);
+      // The owner's first piece, then its last one where that is the head of a pair that
+      // goes on past hi, then the whole pairs between them: the pieces of split pairs are
+      // done early, and their merges overlap the rest (see step_kernel.cu).
+      uint32_t ra = lo, rb = hi;          // the range being walked
+      uint32_t rest_a = hi, rest_b = hi;  // whole pairs left for after it
+      bool first = false;                 // walking the first of several pieces
+      int4 begun = make_int4(0, 0, 0, 0);  // the pair that begins here and goes on elsewhere
+      int b = seq_at(lo);
+      {
+        const uint32_t nb0 = (uint32_t)(cu[b + 1] - cu[b]) / (uint32_t)H;
+        const uint32_t e0 = (uint32_t)cu[b] + ((lo - (uint32_t)cu[b]) / nb0 + 1) * nb0;
+        if (e0 < hi) {
+          rb = e0;
+          first = true;
+        }
+      }
+      uint32_t left = hi - lo;  // units of this owner from the current one on
+      for (;;) {
+        for (uint32_t u = ra; u < rb;) {
+          while ((uint32_t)cu[b + 1] <= u) ++b;
+          const uint32_t nb = (uint32_t)(cu[b + 1] - cu[b]) / (uint32_t)H;
+          const uint32_t rel = u - (uint32_t)cu[b];
+          const uint32_t hu = rel / nb;
+          const int h = (int)hu, t0 = (int)(rel - hu * nb);
+          const uint32_t pair_lo = (uint32_t)cu[b] + hu * nb, pair_hi = pair_lo + nb;
+          const uint32_t e = rb < pair_hi ? rb : pair_hi;
+          const int t1 = t0 + (int)(e - u);
+          const bool whole = t0 == 0 && t1 == (int)nb;
+          const int slot = whole ? -1 : (u == lo ? 2 * owner : 2 * owner + 1);
+          const int k = whole ? 1 : (int)(M.owner_of(pair_hi - 1) - M.owner_of(pair_lo) + 1);
+          if (!whole && t0 == 0) begun = make_int4(b, h, k, slot);
+          publish(b, h, t0, t1, (whole ? kFlagWhole : 0) | (k << 8), slot);
+          const int32_t* btrow = p.block_table + (int64_t)b * p.bt_sb;
+          const uint8_t* kh = p.k + (int64_t)h * p.c_shead;
+          const uint8_t* vh = p.v + (int64_t)h * p.c_shead;
+          const int n = t1 - t0;
+          for (int i0 = 0; i0 < n; i0 += 32) {
+            const int i = i0 + lane;
+            int blk = -1;  // no block: zeros are read in its place
+            if (i < n) {
+              const int t = t0 + i;
+              if (t < p.max_blocks) {
+                const int v = __ldg(btrow + t);
+                if (v >= 0 && v < p.num_blocks) blk = v;
+                else atomicOr(p.err, HPC_DEVCHK_BAD_BLOCK);
+              } else {
+                atomicOr(p.err, HPC_DEVCHK_TABLE_TOO_SHORT);
+              }
+            }
+            const int cnt = n - i0 < 32 ? n - i0 : 32;
+            for (int ii = 0; ii < cnt; ++ii, ++g, --left) {
+              const int bk = __shfl_sync(0xffffffffu, blk, ii);
+              if (!asked && left <= (uint32_t)kClaimAhead) ask();
+              if (lane != 0 || stop) continue;
+              const uint32_t slot_r = g % STAGES;
+              if (!wait_phase(bar_empty + 8 * slot_r, ((g / STAGES) & 1u) ^ 1u, abort_flag, p.err,
+                              p.timeout_ns)) {
+                stop = true;
+                continue;
+              }
+              const uint32_t fb = bar_full + 8 * slot_r;
+              const uint32_t dk = smem_base + slot_r * kStage;
+              const int64_t off = (int64_t)bk * p.c_sblk;
+              mbar_arrive_expect_tx(fb, kStage);
+              kv4_copy_tile(dk, bk < 0 ? (const void*)kKv4NoTile : kh + off, fb, policy);
+              kv4_copy_tile(dk + kKv4Tile, bk < 0 ? (const void*)kKv4NoTile : vh + off, fb, policy);
+              st_release_shared(issued_word + 4 * slot_r, g);
+              issued = g + 1;
+            }
+          }
+          u = e;
+        }
+        if (first) {  // then the last piece, if split, ahead of the whole pairs
+          first = false;
+          const uint32_t e0 = rb;
+          const int b1 = seq_at(hi - 1);
+          const uint32_t nb1 = (uint32_t)(cu[b1 + 1] - cu[b1]) / (uint32_t)H;
+          const uint32_t s1 = (uint32_t)cu[b1] + ((hi - 1 - (uint32_t)cu[b1]) / nb1) * nb1;
+          if (s1 + nb1 > hi && s1 > e0) {
+            rest_a = e0;
+            rest_b = s1;
+            ra = s1;
+            b = b1;
+          } else {
+            ra = e0;
+          }
+          rb = hi;
+          continue;
+        }
+        if (rest_a < rest_b) {
+          ra = rest_a;
+          rb = rest_b;
+          rest_a = rest_b;
+          b = seq_at(ra);
+          continue;
+        }
+        break;
+      }
+      if (!kOneToken && lane == 0) *reinterpret_cast<int4*>(p.owners + 4 + 4 * owner) = begun;
+      if (!asked) ask();
+      owner = resolve();
+    }
+    // This CTA's failed request ended its work; the last CTA to get there resets the pool
+    // for the next step (every CTA asked for the last time).
+    if (lane == 0 && atomicAdd(p.pool + 1, 1) == G - 1) {
+      p.pool[0] = 0;
+      p.pool[1] = 0;
+    }
+    // one end marker per epilogue warp (they take alternate pieces; the consumer warps
+    // stop at the first)
+    for (int e = 0; e < kEpilogueWarps; ++e) publish(0, 0, 0, 0, kFlagEnd, -1);
+    named_bar_sync(3, kThreads);
+    if (lane == 0 && *abort_flag) {  // copies may still be landing: wait for the last ones
+      for (uint32_t u = issued > (uint32_t)STAGES ? issued - STAGES : 0; u < issued; ++u)
+        wait_phase(bar_full + 8 * (u % STAGES), (u / STAGES) & 1u, abort_flag, p.err,
+                   1000000000ull, false);
+    }
+    return;
+  }
+
+  uint4* dep = reinterpret_cast<uint4*>(smem + C::kDepOff);  // [warp][token][vector][lane]
+  if (warp >= kEpilogueWarp0) {
+    // ------------------------------------------------------------ epilogue
+    // For every piece and token: join the states of the warps that shared its units,
+    // then write the result, or a partial state of a split pair; with one token a step
+    // the piece is counted and the last of a pair's merges them.
+    for (int j = warp - kEpilogueWarp0;; j += kEpilogueWarps) {
+      const int qs = j % kPieceQ;
+      if (!wait_phase(bar_pfull + 8 * qs, (j / kPieceQ) & 1u, abort_flag, p.err, book_ns, false))
+        break;
+      const int* d = desc + qs * kDescInts;
+      const int b = d[0], h = d[1], fl = d[4], slot = d[5];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_pfree + 8 * qs);
+      if (fl & kFlagEnd) break;
+      // the deposits of piece j complete phase j / kEpilogueWarps of this warp's barrier;
+      // its next phase needs this warp's read first, so the parity is exact
+      if (!wait_phase(bar_dfull + 8 * (j % kEpilogueWarps), (j / kEpilogueWarps) & 1u, abort_flag,
+                      p.err, book_ns, false))
+        break;
+      for (int t = 0; t < T; ++t) {
+        Kv4State st;
+        st.clear();
+        // the states of token t: warps t / TW, + NP, ...
+#pragma unroll
+        for (int v = 0; v < kGroups; ++v) {
+          const int at = ((t / TW + NP * v) * TW + t % TW) * kDepVec;
+          const float2 mv = *reinterpret_cast<const float2*>(dep + (at + 4) * 32 + lane);
+          st.m[0] = fmaxf(st.m[0], mv.x);
+          st.m[1] = fmaxf(st.m[1], mv.y);
+        }
+#pragma unroll 1
+        for (int v = 0; v < kGroups; ++v) {
+          const int at = ((t / TW + NP * v) * TW + t % TW) * kDepVec;
+          const float4 ml = *reinterpret_cast<const float4*>(dep + (at + 4) * 32 + lane);
+          const float w0 = ml.x == -INFINITY ? ml.z : ml.z * ex2(ml.x - st.m[0]);
+          const float w1 = ml.y == -INFINITY ? ml.w : ml.w * ex2(ml.y - st.m[1]);
+          st.l[0] += w0;
+          st.l[1] += w1;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint4 h4 = dep[(at + k) * 32 + lane];
+            const uint32_t hw[4] = {h4.x, h4.y, h4.z, h4.w};
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const float2 o = __half22float2(*reinterpret_cast<const __half2*>(&hw[x]));
+              st.acc[2 * k + (x >> 1)][2 * (x & 1)] += o.x * w0;
+              st.acc[2 * k + (x >> 1)][2 * (x & 1) + 1] += o.y * w1;
+            }
+          }
+        }
+        if (t == T - 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_dfree);  // the consumers may deposit the next piece
+        }
+        if (fl & kFlagWhole) {
+          st.write(p, b, t, h, lane);
+        } else {
+          st.store(p.ws + ((int64_t)slot * T + t) * kKv4PartFloat4 + lane);
+        }
+      }
+      if (!kOneToken || (fl & kFlagWhole)) continue;
+      // The piece of a split pair counts itself; the last one of a pair joins the states
+      // in the owners' order. More than kFan pieces are joined in groups of kFan first,
+      // each by its last piece, so that no warp reads more than a few dozen states. One
+      // acquire-release atomic by lane 0 covers the warp's writes (ordered before it by the
+      // warp barrier) and the other pieces', which the warp reads after the second one.
+      const int k = fl >> 8, owner = slot >> 1;
+      const uint32_t nb = (uint32_t)(cu[b + 1] - cu[b]) / (uint32_t)H;
+      const uint32_t A = (uint32_t)cu[b] + (uint32_t)h * nb;
+      const int first = (int)M.owner_of(A);
+      auto slot_of = [&](int ow) -> int64_t { return 2 * (int64_t)ow + (A <= M.start(ow) ? 0 : 1); };
+      auto arrive = [&](int32_t* cnt, int of) -> bool {
+        __syncwarp();
+        int last = 0;
+        if (lane == 0) {
+          last = atom_add_acq_rel_gpu(cnt, 1) == of - 1;
+          if (last) *cnt = 0;  // ready for the next step
+        }
+        last = __shfl_sync(0xffffffffu, last, 0);
+        __syncwarp();
+        return last != 0;
+      };
+      auto join = [&](Kv4State& st, int ow, int n, int step) {
+        st.clear();
+        for (int i = 0; i < n; i += 2) {
+          const float4* s0 = p.ws + slot_of(ow + i * step) * kKv4PartFloat4 + lane;
+          const float4* s1 =
+              i + 1 < n ? p.ws + slot_of(ow + (i + 1) * step) * kKv4PartFloat4 + lane : nullptr;
+          st.add2(s0, s1);
+        }
+      };
+      int groups = k, step = 1;
+      Kv4State st;
+      if (k > kFan) {
+        const int gi = (owner - first) / kFan, lead = first + gi * kFan;
+        const int n = k - gi * kFan < kFan ? k - gi * kFan : kFan;
+        const int64_t at = slot_of(lead);
+        if (!arrive(p.slot_cnt + at, n)) continue;
+        join(st, lead, n, 1);
+        st.store(p.ws + at * kKv4PartFloat4 + lane);
+        groups = (k + kFan - 1) / kFan;
+        step = kFan;
+      }
+      if (!arrive(p.pair_cnt + (int64_t)b * H + h, groups)) continue;
+      join(st, first, groups, step);
+      st.write(p, b, 0, h, lane);
+    }
+    named_bar_sync(3, kThreads);
+    return;
+  }
+
+  // -------------------------------------------------------------- consumers
+  // Groups of NP warps take a piece's units in turn, each warp for its own tokens, and
+  // deposit their states; they wait for each other only at the deposit buffer.
+  const int slice = warp % NP, grp = warp / NP;
+  bool dead = false;
+  for (int j = 0;; ++j) {
+    const int qs = j % kPieceQ;
+    if (!wait_phase(bar_pfull + 8 * qs, (j / kPieceQ) & 1u, abort_flag, p.err, book_ns, false))
+      break;  // no descriptor arrived: the producer is gone
+    const int* d = desc + qs * kDescInts;
+    const int b = d[0], h = d[1], t0 = d[2], t1 = d[3], fl = d[4], g0 = d[6];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_pfree + 8 * qs);  // this warp has read the descriptor
+    if (fl & kFlagEnd) break;
+    const int n = t1 - t0;
+    // a function of the piece alone, so a piece gives the same bits whichever CTA runs it
+    const int rot = (int)(((int64_t)t0 + (int64_t)b * H + h) % kGroups);
+    const int i0 = (grp - rot + kGroups) % kGroups;  // this group's first unit
+    float m[TW][2], l[TW][2], acc[TW][8][4];
+#pragma unroll
+    for (int t = 0; t < TW; ++t) {
+      m[t][0] = m[t][1] = -INFINITY;
+      l[t][0] = l[t][1] = 0.f;
+#pragma unroll
+      for (int dm = 0; dm < 8; ++dm)
+        acc[t][dm][0] = acc[t][dm][1] = acc[t][dm][2] = acc[t][dm][3] = 0.f;
+    }
+    if (i0 < n) {
+      const int len = __ldg(p.seq_lens + b);
+      uint32_t qf[TW][8][2];
+      float sl2[TW];
+      int off[TW];  // tokens that the warp's tokens do not see at the end
+#pragma unroll
+      for (int t = 0; t < TW; ++t) {
+        // (a warp's second token past the last one repeats it, and is not written)
+        const int tok = TW * slice + t < T ? TW * slice + t : T - 1;
+        const float qinv =
+            load_q4(p.q + (int64_t)b * p.q_sb + (int64_t)tok * p.q_st + (int64_t)(h * kGroup) * p.q_sh,
+                    p.q_sh, lane, qf[t]);
+        // (a factor of 0 would make NaN of masked scores, an infinite one of scores of 0)
+        sl2[t] = fminf(fmaxf(p.score_scale_log2 * qinv, FLT_MIN), FLT_MAX);
+        off[t] = T - 1 - tok;
+      }
+      for (int i = i0; i < n; i += kGroups) {
+        const uint32_t gu = (uint32_t)(g0 + i);
+        const uint32_t s = gu % STAGES;
+        if (dead) continue;
+        const bool ok = wait_issued(issued_word + 4 * s, gu, abort_flag, p.err, p.timeout_ns) &&
+                        wait_phase(bar_full + 8 * s, (gu / STAGES) & 1u, abort_flag, p.err,
+                                   p.timeout_ns);
+        if (!__all_sync(0xffffffffu, ok)) {  // warp-uniform decision
+          dead = true;
+          continue;
+        }
+        const int stored = len - (t0 + i) * kBlockTokens;
+        int seen[TW];
+#pragma unroll
+        for (int t = 0; t < TW; ++t) seen[t] = stored - off[t];
+        if (seen[TW - 1] > 0) {
+          const uint32_t kb = smem_base + s * kStage;
+          compute_unit4<TW>(kb, kb + kKv4Tile, qf, seen, stored, sl2, m, l, acc, lane);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_empty + 8 * s);
+      }
+    }
+    // row sums over the 8 lanes sharing a query-head pair
+#pragma unroll
+    for (int t = 0; t < TW; ++t)
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        l[t][0] += __shfl_xor_sync(0xffffffffu, l[t][0], o);
+        l[t][1] += __shfl_xor_sync(0xffffffffu, l[t][1], o);
+      }
+    // deposit once the epilogue warp has read the previous piece's states: o = acc / l in
+    // f16 (2^-11; |o| is at most the largest |code * scale|, 2688), m and l in fp32
+    wait_phase(bar_dfree, (j & 1u) ^ 1u, abort_flag, p.err, book_ns, false);
+#pragma unroll
+    for (int t = 0; t < TW; ++t) {
+      const float v0 = l[t][0] == 0.f ? 0.f : __fdividef(1.f, l[t][0]);
+      const float v1 = l[t][1] == 0.f ? 0.f : __fdividef(1.f, l[t][1]);
+      uint4* dw = dep + ((warp * TW + t) * kDepVec) * 32 + lane;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)  // slices 2k, 2k + 1
+        dw[k * 32] = make_uint4(pack_f16(acc[t][2 * k][0] * v0, acc[t][2 * k][1] * v1),
+                                pack_f16(acc[t][2 * k][2] * v0, acc[t][2 * k][3] * v1),
+                                pack_f16(acc[t][2 * k + 1][0] * v0, acc[t][2 * k + 1][1] * v1),
+                                pack_f16(acc[t][2 * k + 1][2] * v0, acc[t][2 * k + 1][3] * v1));
+      reinterpret_cast<float4*>(dw)[4 * 32] = make_float4(m[t][0], m[t][1], l[t][0], l[t][1]);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_dfull + 8 * (j % kEpilogueWarps));  // release to the epilogue
+  }
+  named_bar_sync(3, kThreads);  // see the producer's exit
+}
+
+template <int TW, int NP, int NC>
+cudaError_t launch_cfg(const Kv4DecodeParams& p, int grid, cudaStream_t stream) {
+  using C = Cfg<TW, NP, NC>;
+  auto kern = kv4_decode_kernel<TW, NP, NC>;
+  static std::atomic<uint64_t> configured{0};
+  cudaError_t e = once_per_device(configured, [&] {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                C::kSmemBytesMax);
+  });
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes + 4 * ((size_t)p.num_seqs + 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_decode(const Kv4DecodeParams& p, int grid, cudaStream_t stream) {
+  if (p.num_seqs > kKv4MaxSeqs) return cudaErrorInvalidValue;
+  switch ((p.q_len + 1) / 2) {
+    case 1:
+      return p.q_len == 1 ? launch_cfg<1, 1, 8>(p, grid, stream)
+                          : launch_cfg<2, 1, 8>(p, grid, stream);
+    case 2: return launch_cfg<2, 2, 8>(p, grid, stream);
+    case 3: return launch_cfg<2, 3, 6>(p, grid, stream);
+    default: return launch_cfg<2, 4, 8>(p, grid, stream);
+  }
+}
+
+}  // namespace hpc

@@ -30,6 +30,10 @@ struct ExtendParams {
   float v_scale;                // e4m3 V scale (1 for bf16)
   int32_t* err;                 // device flag word (HPC_DEVCHK_*) or null
   unsigned long long timeout_ns;
+  int32_t total_q;              // > 0: rows of q and out, which no sequence may leave
+  const uint8_t* k4;            // 4-bit rows [blocks][H_kv][64][72] (else null: tensor maps)
+  const uint8_t* v4;
+  int64_t c_sblk, c_shead;      // their strides in bytes
   int32_t withhold_copies;      // failure-path test: the producer issues no copy
 };
 

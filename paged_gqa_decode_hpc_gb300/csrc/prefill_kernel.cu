@@ -51,6 +51,7 @@
 
 #include "hpc_decode.h"
 #include "hpc_internal.h"
+#include "kv4.cuh"
 #include "prefill.h"
 #include "tc05.cuh"
 
@@ -66,7 +67,6 @@ constexpr uint32_t kQBytes = kRows * 128 * 2;         // 32 KB: two 16 KB column
 constexpr uint32_t kKVTileBytes = 64 * 128 * 2;       // 16 KB: two 8 KB column halves
 constexpr uint32_t kStageBytes = 2 * kKVTileBytes;    // K + V
 constexpr uint32_t kKVTileBytes8 = 64 * 128;          // 8 KB: one e4m3 K or V tile
-constexpr uint32_t kStageBytes8 = 2 * kKVTileBytes8;  // e4m3 K + V
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 
@@ -74,8 +74,11 @@ constexpr float kRescaleThreshold = 8.0f;  // log2 units
 // the softmax warpgroups (warpgroup g owns tile g: rows = TMEM lanes of its
 // own S and O columns), then one TMA producer warp and one MMA warp per query
 // tile, so the two tiles' S -> softmax -> P*V chains never wait on each other.
-template <int QT, bool FP8>
+// FP8: the cache is narrower than 16 bits and converted to f16; KV4: it holds 4-bit
+// rows (kv4.cuh), else e4m3.
+template <int QT, bool FP8, bool KV4>
 struct Layout {
+  static_assert(FP8 || !KV4, "4-bit rows are converted");
   // FP8 caches: 4 converter warps widen each e4m3 K / V tile to bf16 in place
   // of the TMA writing bf16 directly
   static constexpr int kConvWarps = FP8 ? 4 : 0;
@@ -83,11 +86,14 @@ struct Layout {
   static constexpr int kProducerWarp = 4 * QT + kConvWarps, kMmaWarp0 = kProducerWarp + 1;
   static constexpr int kThreads = 32 * (kMmaWarp0 + QT);
   static constexpr int kStages = FP8 ? 4 : (QT == 1 ? 6 : 5);            // 16-bit K+V ring
-  static constexpr int kStages8 = FP8 ? (QT == 1 ? 4 : 2) : 0;           // e4m3 K+V ring
+  static constexpr uint32_t kTile8 = KV4 ? kKv4Tile : kKVTileBytes8;     // a tile as copied
+  static constexpr uint32_t kStage8 = 2 * kTile8;
+  // e4m3 K+V ring; of 4-bit rows what fits
+  static constexpr int kStages8 = KV4 ? (QT == 1 ? 6 : 3) : FP8 ? (QT == 1 ? 4 : 2) : 0;
   static constexpr uint32_t kOffQ = 0;                                   // QT x 32 KB
   static constexpr uint32_t kOffKV = QT * kQBytes;                       // stages x 32 KB
   static constexpr uint32_t kOffKV8 = kOffKV + kStages * kStageBytes;    // stages8 x 16 KB
-  static constexpr uint32_t kOffBar = kOffKV8 + kStages8 * kStageBytes8;
+  static constexpr uint32_t kOffBar = kOffKV8 + kStages8 * kStage8;
   // q_full, kv_full[S], kv_empty[S], kv8_full[S8], kv8_empty[S8],
   // per tile: s_full, s_free, p_full[2], pv_done[2], drain, q_ready (FP8)
   static constexpr int kNumBars = 1 + 2 * kStages + 2 * kStages8 + 8 * QT;
@@ -239,7 +245,8 @@ __device__ TileInfo find_tile(const ExtendParams& p, int y, int lane, int tile_t
     base += chunk;
   }
   if (!ti.valid) return ti;
-  if (ti.L < ti.n) {  // more new tokens than positions
+  // more new tokens than positions, or than rows
+  if (ti.L < ti.n || (p.total_q > 0 && (ti.q0 < 0 || ti.q0 > p.total_q - ti.n))) {
     if (lane == 0 && p.err) atomicOr(p.err, HPC_DEVCHK_BAD_LENGTH);
     ti.valid = 0;
     return ti;
@@ -261,12 +268,12 @@ __device__ __forceinline__ int tile_kv(int L, int n, int t0g) {
 
 namespace {
 
-template <int QT, bool FP8>
-__global__ void __launch_bounds__(Layout<QT, FP8>::kThreads, 1)
+template <int QT, bool FP8, bool KV4>
+__global__ void __launch_bounds__(Layout<QT, FP8, KV4>::kThreads, 1)
     extend_kernel(const __grid_constant__ ExtendParams p, const __grid_constant__ CUtensorMap tmq,
                   const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                   const __grid_constant__ CUtensorMap tmo) {
-  using Lt = Layout<QT, FP8>;
+  using Lt = Layout<QT, FP8, KV4>;
   constexpr int S = Lt::kStages, S8 = Lt::kStages8;
   constexpr int S8n = S8 > 0 ? S8 : 1;  // e4m3 ring positions (the ring exists for FP8 only)
   extern __shared__ uint8_t smem_raw[];
@@ -392,10 +399,17 @@ __global__ void __launch_bounds__(Layout<QT, FP8>::kThreads, 1)
                               wait_bar(kv8_empty(slot), (round - 1) & 1, s_abort, err, lim_ns);
               if (ok) {
                 const uint32_t fb = kv8_full(slot);
-                const uint32_t dk = sKV8 + slot * kStageBytes8, dv = dk + kKVTileBytes8;
-                mbar_expect_tx(fb, kStageBytes8);
-                tma_load_4d(dk, &tmk, fb, 0, c1, c2, bk);
-                tma_load_4d(dv, &tmv, fb, 0, c1, c2, bk);
+                const uint32_t dk = sKV8 + slot * Lt::kStage8, dv = dk + Lt::kTile8;
+                mbar_expect_tx(fb, Lt::kStage8);
+                if constexpr (KV4) {
+                  const bool none = bk < 0 || bk >= p.num_blocks;
+                  const int64_t off = (int64_t)bk * p.c_sblk + (int64_t)h * p.c_shead;
+                  kv4_copy_tile(dk, none ? (const void*)kKv4NoTile : p.k4 + off, fb);
+                  kv4_copy_tile(dv, none ? (const void*)kKv4NoTile : p.v4 + off, fb);
+                } else {
+                  tma_load_4d(dk, &tmk, fb, 0, c1, c2, bk);
+                  tma_load_4d(dv, &tmv, fb, 0, c1, c2, bk);
+                }
                 issued = j + 1;
               } else {
                 stop = 1;
@@ -459,21 +473,36 @@ __global__ void __launch_bounds__(Layout<QT, FP8>::kThreads, 1)
         ok = __all_sync(0xffffffffu,
                         wait_bar(kv_empty(sb), ((j / S) - 1) & 1, s_abort, err, lim_ns));
       if (!ok) break;
-      const uint32_t e8 = sKV8 + s8 * kStageBytes8, kb = sKV + sb * kStageBytes;
+      const uint32_t e8 = sKV8 + s8 * Lt::kStage8, kb = sKV + sb * kStageBytes;
 #pragma unroll 2
       for (int it = 0; it < 2 * kRowSteps; ++it) {
         const int mat = it / kRowSteps;
         const int t = (it % kRowSteps) * (64 / kRowSteps) + (ct >> 4) * 2 + cr;
-        uint32_t x0, x1, x2, x3;
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(x0), "=r"(x1), "=r"(x2), "=r"(x3)
-                     : "r"(e8 + mat * kKVTileBytes8 + t * 128 + ((uint32_t)(c ^ (t & 7)) << 4)));
         uint32_t w[8];
-        const uint32_t xs[4] = {x0, x1, x2, x3};
+        if constexpr (KV4) {
+          // the same sixteen elements: eight bytes of codes times their scale, exactly.
+          // V's rows past the sequence become 0, whatever the slots hold (K's scores are masked)
+          const uint32_t row = e8 + mat * kKv4Tile + t * kKv4Row;
+          uint32_t x0, x1, f;
+          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(x0), "=r"(x1) : "r"(row + 8 * c));
+          asm volatile("ld.shared.u8 %0, [%1];" : "=r"(f) : "r"(row + kKv4Codes + c));
+          if (mat == 1 && 64 * j + t >= L) f = 0;
+          f = both_low(kv4_scales(f));
+          e2m1x8_to_f16(x0, *reinterpret_cast<uint32_t(*)[4]>(&w[0]));
+          e2m1x8_to_f16(x1, *reinterpret_cast<uint32_t(*)[4]>(&w[4]));
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          w[2 * q] = e4m3x2_to_f16x2((uint16_t)(xs[q] & 0xFFFFu));
-          w[2 * q + 1] = e4m3x2_to_f16x2((uint16_t)(xs[q] >> 16));
+          for (int q = 0; q < 8; ++q) w[q] = mul_f16x2(w[q], f);
+        } else {
+          uint32_t x0, x1, x2, x3;
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(x0), "=r"(x1), "=r"(x2), "=r"(x3)
+                       : "r"(e8 + mat * kKVTileBytes8 + t * 128 + ((uint32_t)(c ^ (t & 7)) << 4)));
+          const uint32_t xs[4] = {x0, x1, x2, x3};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            w[2 * q] = e4m3x2_to_f16x2((uint16_t)(xs[q] & 0xFFFFu));
+            w[2 * q + 1] = e4m3x2_to_f16x2((uint16_t)(xs[q] >> 16));
+          }
         }
         // elements 16c .. 16c+15 -> half c / 4, 8-element chunks 2(c % 4) and 2(c % 4) + 1
         const int cc = (c & 3) * 2;
@@ -804,19 +833,19 @@ __global__ void __launch_bounds__(Layout<QT, FP8>::kThreads, 1)
   }
 }
 
-template <int QT, bool FP8>
+template <int QT, bool FP8, bool KV4 = false>
 cudaError_t launch_qt(const ExtendParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
                       const CUtensorMap& tv, const CUtensorMap& to, int tiles,
                       cudaStream_t stream) {
-  using Lt = Layout<QT, FP8>;
+  using Lt = Layout<QT, FP8, KV4>;
   static std::atomic<uint64_t> configured{0};  // devices whose copy is configured
   const cudaError_t e = once_per_device(configured, [] {
-    return cudaFuncSetAttribute(extend_kernel<QT, FP8>,
+    return cudaFuncSetAttribute(extend_kernel<QT, FP8, KV4>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)Lt::kSmemBytes);
   });
   if (e != cudaSuccess) return e;
-  extend_kernel<QT, FP8><<<dim3(p.num_kv_heads, tiles), Lt::kThreads, Lt::kSmemBytes, stream>>>(
+  extend_kernel<QT, FP8, KV4><<<dim3(p.num_kv_heads, tiles), Lt::kThreads, Lt::kSmemBytes, stream>>>(
       p, tq, tk, tv, to);
   return cudaGetLastError();
 }
@@ -827,6 +856,10 @@ cudaError_t launch_extend(const ExtendParams& p, const CUtensorMap& tq, const CU
                           const CUtensorMap& tv, const CUtensorMap& to, int tiles,
                           int tiles_per_cta, cudaStream_t stream) {
   if (tiles <= 0 || p.num_kv_heads <= 0) return cudaSuccess;
+  if (p.k4) {
+    if (tiles_per_cta == 2) return launch_qt<2, true, true>(p, tq, tk, tv, to, tiles, stream);
+    return launch_qt<1, true, true>(p, tq, tk, tv, to, tiles, stream);
+  }
   if (p.kv_fp8) {
     if (tiles_per_cta == 2) return launch_qt<2, true>(p, tq, tk, tv, to, tiles, stream);
     return launch_qt<1, true>(p, tq, tk, tv, to, tiles, stream);

@@ -34,6 +34,7 @@
 #include "cache_ops.h"
 #include "convert.cuh"
 #include "hpc_internal.h"
+#include "kv4.cuh"
 #include "ptx.cuh"
 
 namespace hpc {
@@ -127,7 +128,67 @@ __device__ __forceinline__ int table_at(int e) { return (e & 4) * 16 + (e >> 3) 
 // CTAs per SM, which bounds the registers (8192 tokens: 52.7 us against 55.6 with 6).
 constexpr int kCtas = 8;
 
-template <int LAYOUT, bool NORM>
+// A chunk of 8 elements of a 4-bit row: the largest magnitude of its 16 neighbours is
+// `amax` (NaN where one of them is). Returns the codes; `scale` receives the e4m3 byte.
+// Both are correctly rounded from the exact quotients, ties to even: rounding is
+// monotone, so where the two products that enclose a quotient round alike, so does it
+// (1 / unit is within 2^-24, the factors and products within 2^-24 each: 2^-21 encloses
+// them); the others, near a border, are divided.
+__device__ __forceinline__ float quotient_odd(float x, float s) {
+  return fabsf(x) <= 3.4028235e38f ? div_round_odd(x, s) : x;
+}
+__device__ __forceinline__ uint32_t to_e2m1x8(const float (&y)[8]) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\tcvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\tmov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r)
+      : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
+  return r;
+}
+static __device__ __noinline__ uint32_t divide_e2m1x8(float4 a, float4 b, float unit) {
+  const float y[8] = {quotient_odd(a.x, unit), quotient_odd(a.y, unit), quotient_odd(a.z, unit),
+                      quotient_odd(a.w, unit), quotient_odd(b.x, unit), quotient_odd(b.y, unit),
+                      quotient_odd(b.z, unit), quotient_odd(b.w, unit)};
+  return to_e2m1x8(y);
+}
+__device__ __forceinline__ uint32_t quantise_e2m1x8(const float2* x, float amax, float tensor_scale,
+                                                    uint8_t* scale) {
+  const uint32_t byte =
+      to_e4m3x4(make_float4(quotient_odd(amax, 6.f * tensor_scale), 0.f, 0.f, 0.f)) & 0xFFu;
+  *scale = (uint8_t)byte;
+  const uint32_t h = kv4_scales(byte);
+  const float unit =
+      __half2float(__ushort_as_half((unsigned short)(h & 0xFFFFu))) * tensor_scale;
+  if (!(unit > 0.f)) return 0u;  // nothing the scale can hold, or NaN, which the scale says
+  const float inv = __frcp_rn(unit);
+  const float lo = inv * (1.f - 0x1p-21f), hi = inv * (1.f + 0x1p-21f);
+  float a[8], b[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 u = mul2(x[i], make_float2(lo, lo)), v = mul2(x[i], make_float2(hi, hi));
+    a[2 * i] = u.x; a[2 * i + 1] = u.y;
+    b[2 * i] = v.x; b[2 * i + 1] = v.y;
+  }
+  const uint32_t r = to_e2m1x8(a);
+  if (r == to_e2m1x8(b)) return r;
+  return divide_e2m1x8(make_float4(x[0].x, x[0].y, x[1].x, x[1].y),
+                       make_float4(x[2].x, x[2].y, x[3].x, x[3].y), unit);
+}
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float chunk_max(const float2* x) {
+  float m = max_nan(fabsf(x[0].x), fabsf(x[0].y));
+#pragma unroll
+  for (int i = 1; i < 4; ++i) m = max_nan(m, max_nan(fabsf(x[i].x), fabsf(x[i].y)));
+  return m;
+}
+
+// KV4: the caches hold 4-bit rows (kv4.cuh).
+template <int LAYOUT, bool NORM, bool KV4>
 __global__ void __launch_bounds__(kThreads, kCtas)
     rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr bool kTables = NORM || LAYOUT == kHalfAny;  // see table_at
@@ -138,6 +199,9 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   // the norm weights), of q and of k, by table_at
   __shared__ __align__(16) float s_own[kTables ? 1 + NORM : 1][kHeadDim];
   __shared__ __align__(16) float s_other[kTables ? 1 + NORM : 1][kHeadDim];
+  // KV4: the largest magnitude of each chunk of a row; a scale belongs to two neighbours,
+  // which are another lane's, or its other one, by the layout
+  __shared__ float s_max[KV4 ? kRowsAtOnce : 1][2 * kLanes];
   griddep_wait();
   griddep_launch_dependents();
   const int64_t n = blockIdx.x;
@@ -321,6 +385,20 @@ __global__ void __launch_bounds__(kThreads, kCtas)
               x[j] = fma2(x[j], c[j], mul2(make_float2(x[j].y, x[j].x), s[j]));
         }
       }
+      float max_a = 0.f, max_b = 0.f;
+      if constexpr (KV4) {
+        const bool is_kv = !is_q && r < num_rows;
+        if (__any_sync(0xffffffffu, is_kv)) {  // (whole warps are here)
+          max_a = chunk_max(x);
+          max_b = chunk_max(x + 4);
+          s_max[row_of][ca] = max_a;
+          s_max[row_of][cb] = max_b;
+          __syncwarp();
+          max_a = max_nan(max_a, s_max[row_of][ca ^ 1]);
+          max_b = max_nan(max_b, s_max[row_of][cb ^ 1]);
+          __syncwarp();
+        }
+      }
       if (is_q) {
         __nv_bfloat16* dst = p.q_out + n * p.qo_sn + r * p.qo_sh;
         *reinterpret_cast<uint4*>(dst + ea) = pack(x);
@@ -333,7 +411,15 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       } else if (r < num_rows && store_kv) {
         const int h = r - p.num_q_heads - (is_k ? 0 : p.num_kv_heads);
         const int64_t off = cache_row + h * p.c_shead;
-        if (p.cache_fp8) {
+        if constexpr (KV4) {
+          uint8_t* dst = (uint8_t*)(is_k ? p.k_cache : p.v_cache) + off;
+          const float ts = is_k ? p.k_scale.s : p.v_scale.s;
+          uint8_t sa, sb;
+          *reinterpret_cast<uint32_t*>(dst + 4 * ca) = quantise_e2m1x8(x, max_a, ts, &sa);
+          *reinterpret_cast<uint32_t*>(dst + 4 * cb) = quantise_e2m1x8(x + 4, max_b, ts, &sb);
+          if (!(ca & 1)) dst[kKv4Codes + ca / 2] = sa;
+          if (!(cb & 1)) dst[kKv4Codes + cb / 2] = sb;
+        } else if (p.cache_fp8) {
           uint8_t* dst = (uint8_t*)(is_k ? p.k_cache : p.v_cache) + off;
           const E4m3Scale sc = is_k ? p.k_scale : p.v_scale;
           *reinterpret_cast<uint2*>(dst + ea) = quantise(x, sc);
@@ -348,11 +434,12 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   }
 }
 
-template <bool NORM>
+template <bool NORM, bool KV4>
 cudaError_t launch_layout(const cudaLaunchConfig_t& cfg, const RopeParams& p, int layout) {
-  if (layout == kInterleaved) return cudaLaunchKernelEx(&cfg, rope_kernel<kInterleaved, NORM>, p);
-  if (layout == kHalfLanes) return cudaLaunchKernelEx(&cfg, rope_kernel<kHalfLanes, NORM>, p);
-  return cudaLaunchKernelEx(&cfg, rope_kernel<kHalfAny, NORM>, p);
+  if (layout == kInterleaved)
+    return cudaLaunchKernelEx(&cfg, rope_kernel<kInterleaved, NORM, KV4>, p);
+  if (layout == kHalfLanes) return cudaLaunchKernelEx(&cfg, rope_kernel<kHalfLanes, NORM, KV4>, p);
+  return cudaLaunchKernelEx(&cfg, rope_kernel<kHalfAny, NORM, KV4>, p);
 }
 
 }  // namespace
@@ -379,7 +466,10 @@ cudaError_t launch_rope(const RopeParams& p, int sm_count, cudaStream_t stream) 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return p.wq || p.wk ? launch_layout<true>(cfg, p, layout) : launch_layout<false>(cfg, p, layout);
+  const bool norm = p.wq || p.wk;
+  if (p.cache_kv4)
+    return norm ? launch_layout<true, true>(cfg, p, layout) : launch_layout<false, true>(cfg, p, layout);
+  return norm ? launch_layout<true, false>(cfg, p, layout) : launch_layout<false, false>(cfg, p, layout);
 }
 
 }  // namespace hpc
