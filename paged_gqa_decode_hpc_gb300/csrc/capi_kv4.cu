@@ -280,8 +280,7 @@ hpc_status hpc_decode_kv4_attn(const hpc_tensor* q, const hpc_tensor* k_cache,
     p.score_scale_log2 = factor;
     p.v_scale = v_cache->scale;
     p.ws = (float4*)plan->d_ws;
-    p.pool = plan->d_step;
-    p.pair_cnt = plan->d_step + kv4_pair_off();
+    p.pair_cnt = plan->d_step;
     p.slot_cnt = plan->d_step + kv4_slot_off(plan->max_seqs, kv_heads);
     p.owners = plan->d_step + kv4_owner_off(plan->max_seqs, kv_heads, plan->num_sms);
     p.err = plan->d_err;

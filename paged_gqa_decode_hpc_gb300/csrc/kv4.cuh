@@ -76,6 +76,15 @@ __device__ __forceinline__ void kv4_copy_tile(uint32_t dst, const void* src, uin
       : "memory");
 }
 
+// A row of 128 bf16.
+__device__ __forceinline__ void kv4_copy_row(uint32_t dst, const void* src, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], 256, [%2];" ::"r"(
+          dst),
+      "l"(__cvta_generic_to_global(src)), "r"(bar)
+      : "memory");
+}
+
 #endif  // __CUDACC__
 
 }  // namespace hpc

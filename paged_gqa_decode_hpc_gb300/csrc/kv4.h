@@ -12,13 +12,9 @@ namespace hpc {
 
 // Sequences of one step: their prefix array lies in shared memory.
 constexpr int32_t kKv4MaxSeqs = 4096;
-// The step plan's constants (see step_kernel.cu for the rule): a pool of an eighth of
-// the units, chunks of at least kKv4MinChunk units and at most kKv4ChunksPerCta to a CTA.
-constexpr int32_t kKv4PoolDiv = 8, kKv4MinChunk = 8, kKv4ChunksPerCta = 4, kKv4MinPartDiv = 8,
-                  kKv4PartChunks = 12;
-// Most owners (parts and chunks) and partial-state slots of a step on `grid` CTAs.
-inline int64_t kv4_owners(int32_t grid) { return (int64_t)(1 + kKv4ChunksPerCta) * grid; }
-inline int64_t kv4_slots(int32_t grid) { return 2 * kv4_owners(grid); }
+// Partial-state slots of a step on `grid` CTAs, each of which owns one part of the units:
+// a part's first piece and its last one can be split pairs'.
+inline int64_t kv4_slots(int32_t grid) { return 2LL * grid; }
 // One token's partial state: 8 accumulator slices and (m, m, l, l) of every lane.
 constexpr int kKv4PartFloat4 = 9 * 32;
 
@@ -40,25 +36,23 @@ struct Kv4DecodeParams {
   float score_scale_log2;       // softmax_scale * log2(e) * K's scale, > 0
   float v_scale;
   float4* ws;                   // [slots][q_len][9][32]
-  int32_t* pool;                // [2]: next pool chunk, CTAs done claiming
   int32_t* pair_cnt;            // [B * H_kv] pieces (or groups of them) that have arrived
   int32_t* slot_cnt;            // [slots] pieces of a group that have arrived
-  int32_t* owners;              // [1 + 4 owners] (q_len > 1): their number, and of each the pair
+  int32_t* owners;              // [4 + 4 owners] (q_len > 1): their number, and of each the pair
                                 //   that it begins and others go on with {b, h, pieces, slot}
   int32_t* err;
   unsigned long long timeout_ns;
   int32_t withhold_copies;
 };
 // int32 words of a plan's counters and records, in the order of the fields above.
-inline int64_t kv4_pair_off() { return 2; }
 inline int64_t kv4_slot_off(int32_t max_seqs, int32_t kv_heads) {
-  return kv4_pair_off() + (int64_t)max_seqs * kv_heads;
+  return (int64_t)max_seqs * kv_heads;
 }
 inline int64_t kv4_owner_off(int32_t max_seqs, int32_t kv_heads, int32_t grid) {
   return (kv4_slot_off(max_seqs, kv_heads) + kv4_slots(grid) + 3) / 4 * 4;
 }
 inline int64_t kv4_words(int32_t max_seqs, int32_t kv_heads, int32_t grid) {
-  return kv4_owner_off(max_seqs, kv_heads, grid) + 4 + 4 * kv4_owners(grid);
+  return kv4_owner_off(max_seqs, kv_heads, grid) + 4 + 4LL * grid;
 }
 
 cudaError_t launch_kv4_decode(const Kv4DecodeParams& p, int grid, cudaStream_t stream);

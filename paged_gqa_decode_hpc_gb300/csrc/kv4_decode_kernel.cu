@@ -55,25 +55,49 @@ static_assert(kPieceQ % kEpilogueWarps == 0, "queue slots per epilogue warp");
 constexpr int kDescInts = 8;
 constexpr int kDepVec = 5;                        // 16-byte words per lane of a deposited state
 constexpr int kStage = 2 * kKv4Tile;
+constexpr int kQPitch = 272;                      // bytes between rows of q in shared memory
 // Bookkeeping waits give up this many data waits later (see step_kernel.cu).
 constexpr unsigned long long kBookkeepingWaits = 8;
-constexpr int kClaimAhead = 2;                    // units left to issue when the next chunk is asked for
 constexpr int kFlagEnd = 1, kFlagWhole = 2;
+// What a (sequence, KV head) pair costs beside its units, in units: its q, its states' way
+// through the epilogue. The plan gives every pair so many units more, ahead of its own.
+constexpr int kPairCost = 4;
 constexpr int kFan = 16;                          // pieces of a pair that are joined at once
+
+constexpr int kMinPart = 8;                       // units that a CTA is worth starting for
+constexpr int kWarpPlan = 256;                    // sequences that one warp plans by itself
+
+// Equal parts [start(o), start(o + 1)) of T units, and the part of a unit. Every unit index
+// is below T <= INT32_MAX, so the arithmetic is 32-bit where products fit.
+struct PartPlan {
+  uint32_t T, P;
+  bool small;  // (T + 1) * (P + 1) < 2^32
+  __device__ __forceinline__ uint32_t start(uint32_t o) const {
+    return small ? o * T / P : (uint32_t)((uint64_t)o * T / P);
+  }
+  __device__ __forceinline__ uint32_t owner_of(uint32_t x) const {
+    return small ? ((x + 1) * P - 1) / T : (uint32_t)(((uint64_t)(x + 1) * P - 1) / T);
+  }
+};
 
 // TW tokens to a warp, NP warps to a unit, NC consumer warps (a multiple of NP).
 template <int TW, int NP, int NC>
 struct Cfg {
   static constexpr int kThreads = (NC + 1 + kEpilogueWarps) * 32;
+  // deposited states: two buffers, so that warps may run a piece ahead, where they fit
+  static constexpr int kBufs = TW == 1 ? 2 : 1;
   static constexpr int kDepBytes = NC * TW * kDepVec * 32 * 16;
-  static constexpr int kFixed = kDepBytes + 2048 /* barriers, descriptors, scan */ + 128 + 4 * (kKv4MaxSeqs + 1);
-  static constexpr int kStages = (227 * 1024 - kFixed) / kStage;
+  static constexpr int kQBytes = TW * NP * 8 * kQPitch;          // a piece's rows of q
+  static constexpr int kFixed = kBufs * kDepBytes + kPieceQ * kQBytes + 2048 /* barriers, descriptors, scan */ + 128 + 4 * (kKv4MaxSeqs + 1);
+  static constexpr int kGroups = NC / NP;  // units in work at once; each group has its own slots
+  static constexpr int kStages = (227 * 1024 - kFixed) / kStage / kGroups * kGroups;
+  static constexpr int kBatch = kStages < 16 ? 8 : 16;  // units whose blocks are looked up at once
   static constexpr int kDepOff = kStages * kStage;
-  static constexpr int kBarOff = kDepOff + kDepBytes;
+  static constexpr int kQOff = kDepOff + kBufs * kDepBytes;
+  static constexpr int kBarOff = kQOff + kPieceQ * kQBytes;
   // full, empty, piece full, piece free, deposit full (one per epilogue warp), deposit free
-  static constexpr int kNumBars = 2 * kStages + 2 * kPieceQ + kEpilogueWarps + 1;
-  static constexpr int kIssuedOff = kBarOff + 8 * kNumBars;
-  static constexpr int kDescOff = kIssuedOff + ((4 * kStages + 15) / 16) * 16;
+  static constexpr int kNumBars = 2 * kStages + 2 * kPieceQ + kEpilogueWarps + kBufs;
+  static constexpr int kDescOff = kBarOff + 8 * ((kNumBars + 1) / 2 * 2);
   static constexpr int kMiscOff = kDescOff + 4 * kDescInts * kPieceQ;
   static constexpr int kPlanOff = kMiscOff + 256;  // abort flag, flags, scan scratch
   static constexpr int kSmemBytes = 128 /* alignment slack */ + kPlanOff;
@@ -81,17 +105,14 @@ struct Cfg {
   static_assert(kSmemBytesMax <= 227 * 1024, "shared memory");
   static_assert(NC % NP == 0, "whole groups of warps");
   static_assert(kThreads <= 512, "a scan pass");
+  static_assert(kBatch <= kStages, "a slot to each lane");
 };
 
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 r;
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
-  return r;
+  return *reinterpret_cast<const uint2*>(__cvta_shared_to_generic(a));
 }
 __device__ __forceinline__ uint32_t lds_u8(uint32_t a) {
-  uint32_t r;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(a));
-  return r;
+  return *reinterpret_cast<const uint8_t*>(__cvta_shared_to_generic(a));
 }
 __device__ __forceinline__ uint32_t prmt2(uint32_t a, uint32_t b, uint32_t sel) {
   uint32_t r;
@@ -108,17 +129,18 @@ __device__ __forceinline__ uint32_t select_bits(uint32_t a, uint32_t b, uint32_t
 // The token of row i of group 0 of a half, over 4.
 __device__ __forceinline__ int row_token(int i) { return (int)((0x53427160u >> (4 * i)) & 7u); }
 
-// A row of Q as B operands in K's order of elements: register j of k-step ks holds
-// elements 64 (ks / 4) + 16 c + 4 (ks % 4) + 2 j, + 1 of query head g. Returns the
-// factor that undoes the power of two of the conversion.
-__device__ __forceinline__ float load_q4(const __nv_bfloat16* q0, int64_t q_sh, int lane,
-                                         uint32_t (&qf)[8][2]) {
+// 8 rows of q, kQPitch bytes apart in shared memory, as B operands in K's order of elements:
+// register j of k-step ks holds elements 64 (ks / 4) + 16 c + 4 (ks % 4) + 2 j, + 1 of query
+// head g. Returns the factor that undoes the power of two of the conversion.
+__device__ __forceinline__ float load_q4(uint32_t q, int lane, uint32_t (&qf)[8][2]) {
   const int g = lane >> 2, c = lane & 3;
-  const __nv_bfloat16* row = q0 + (int64_t)g * q_sh + 16 * c;
+  const uint32_t row = q + (uint32_t)(g * kQPitch + 32 * c);
   uint4 u[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    u[i] = __ldg(reinterpret_cast<const uint4*>(row + 64 * (i >> 1) + 8 * (i & 1)));
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(u[i].x), "=r"(u[i].y), "=r"(u[i].z), "=r"(u[i].w)
+                 : "r"(row + 128 * (i >> 1) + 16 * (i & 1)));
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -167,24 +189,37 @@ __device__ __forceinline__ void compute_unit4(uint32_t kb, uint32_t vb,
   const uint32_t k_lane = kb + (uint32_t)(ig * 4 * kKv4Row + 8 * c);
   const uint32_t ks_lane = kb + (uint32_t)(ig * 4 * kKv4Row + kKv4Codes);
   const uint32_t sel = (uint32_t)(c | ((4 + c) << 4));
+  uint32_t f0[4], f1[4];
 #pragma unroll
   for (int mt = 0; mt < 4; ++mt) {
     const uint32_t off = (uint32_t)((32 * (mt >> 1) + 2 * (mt & 1)) * kKv4Row);
-    const uint2 f0 = lds64(ks_lane + off), f1 = lds64(ks_lane + off + kKv4Row);
-    const uint32_t p0 = kv4_scales(prmt2(f0.x, f0.y, sel)), p1 = kv4_scales(prmt2(f1.x, f1.y, sel));
+    const uint2 y0 = lds64(ks_lane + off), y1 = lds64(ks_lane + off + kKv4Row);
+    f0[mt] = kv4_scales(prmt2(y0.x, y0.y, sel));
+    f1[mt] = kv4_scales(prmt2(y1.x, y1.y, sel));
+  }
+  // (the four steps mt side by side: their chains of MMAs are independent)
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      const uint2 x0 = lds64(k_lane + off + 32 * hf), x1 = lds64(k_lane + off + 32 * hf + kKv4Row);
-      const uint32_t f0h = hf ? both_high(p0) : both_low(p0), f1h = hf ? both_high(p1) : both_low(p1);
+  for (int hf = 0; hf < 2; ++hf) {
+    uint2 x0[4], x1[4];
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
+    for (int mt = 0; mt < 4; ++mt) {
+      const uint32_t off = (uint32_t)((32 * (mt >> 1) + 2 * (mt & 1)) * kKv4Row + 32 * hf);
+      x0[mt] = lds64(k_lane + off);
+      x1[mt] = lds64(k_lane + off + kKv4Row);
+    }
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt) {
+        const uint32_t g0 = hf ? both_high(f0[mt]) : both_low(f0[mt]);
+        const uint32_t g1 = hf ? both_high(f1[mt]) : both_low(f1[mt]);
         uint32_t a[4], b[4];
-        e2m1x8_to_f16(w ? x0.y : x0.x, a);
-        e2m1x8_to_f16(w ? x1.y : x1.x, b);
+        e2m1x8_to_f16(w ? x0[mt].y : x0[mt].x, a);
+        e2m1x8_to_f16(w ? x1[mt].y : x1[mt].x, b);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          a[i] = mul_f16x2(a[i], f0h);
-          b[i] = mul_f16x2(b[i], f1h);
+          a[i] = mul_f16x2(a[i], g0);
+          b[i] = mul_f16x2(b[i], g1);
         }
 #pragma unroll
         for (int t = 0; t < TW; ++t) {
@@ -300,7 +335,7 @@ template <int TW, int NP, int NC>
 __global__ void __launch_bounds__(Cfg<TW, NP, NC>::kThreads, 1)
     kv4_decode_kernel(const __grid_constant__ Kv4DecodeParams p) {
   using C = Cfg<TW, NP, NC>;
-  constexpr int STAGES = C::kStages, kThreads = C::kThreads, kGroups = NC / NP;
+  constexpr int STAGES = C::kStages, kThreads = C::kThreads, kGroups = C::kGroups;
   constexpr int kProducerWarp = NC, kEpilogueWarp0 = NC + 1;
   constexpr bool kOneToken = TW == 1;  // pieces are merged here, not by a second kernel
   extern __shared__ uint8_t smem_raw[];
@@ -313,7 +348,6 @@ __global__ void __launch_bounds__(Cfg<TW, NP, NC>::kThreads, 1)
   const uint32_t bar_pfree = bar_pfull + 8 * kPieceQ;
   const uint32_t bar_dfull = bar_pfree + 8 * kPieceQ;  // + 8 * (piece % kEpilogueWarps)
   const uint32_t bar_dfree = bar_dfull + 8 * kEpilogueWarps;
-  const uint32_t issued_word = smem_base + C::kIssuedOff;
   int* desc = reinterpret_cast<int*>(smem + C::kDescOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff);
   int* s_bad = reinterpret_cast<int*>(smem + C::kMiscOff + 8);
@@ -328,14 +362,13 @@ __global__ void __launch_bounds__(Cfg<TW, NP, NC>::kThreads, 1)
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(bar_full + 8 * s, 1);
       mbar_init(bar_empty + 8 * s, NP);  // the warps of a unit
-      reinterpret_cast<volatile uint32_t*>(smem + C::kIssuedOff)[s] = 0xFFFFFFFFu;
     }
     for (int s = 0; s < kPieceQ; ++s) {
       mbar_init(bar_pfull + 8 * s, 1);
       mbar_init(bar_pfree + 8 * s, NC + 1);  // the consumer warps and the piece's epilogue warp
     }
     for (int e = 0; e < kEpilogueWarps; ++e) mbar_init(bar_dfull + 8 * e, NC);
-    mbar_init(bar_dfree, 1);
+    for (int e = 0; e < C::kBufs; ++e) mbar_init(bar_dfree + 8 * e, 1);
     *abort_flag = 0;
     *s_bad = 0;
     cu[0] = 0;
@@ -346,124 +379,128 @@ __global__ void __launch_bounds__(Cfg<TW, NP, NC>::kThreads, 1)
   griddep_launch_dependents();
   __syncthreads();
 
-  // ---- plan: units per sequence, prefix in shared memory
+  // ---- plan: units per sequence (the pairs' costs among them), prefix in shared memory. The
+  // producer plans small batches by itself; whoever else looks at the plan has waited for a
+  // piece of it by then.
+  auto units_of = [&](int32_t len) -> int32_t {  // -1: cannot be
+    // a sequence of more units than INT32_MAX / 512 is refused, so that no partial sum of a
+    // scan pass, of at most 512 sequences, wraps
+    const int64_t n =
+        len > 0 ? (((int64_t)len + kBlockTokens - 1) / kBlockTokens + kPairCost) * H : 0;
+    return len < 0 || n > (int64_t)(INT32_MAX / 512) ? -1 : (int32_t)n;
+  };
   int64_t carry = 0;
-  for (int base = 0; base < B; base += kThreads) {
-    const int b = base + tid;
-    int32_t n = 0;
-    if (b < B) {
-      const int32_t len = p.seq_lens[b];
-      // a sequence of more units than INT32_MAX / 512 is reported, so that no partial sum
-      // of a scan pass, of at most 512 sequences, wraps
-      const int64_t units = len > 0 ? ((int64_t)len + kBlockTokens - 1) / kBlockTokens * H : 0;
-      if (len < 0 || units > (int64_t)(INT32_MAX / 512)) *s_bad = 1;
-      else n = (int32_t)units;
+  if (B > kWarpPlan) {
+    for (int base = 0; base < B; base += kThreads) {
+      const int b = base + tid;
+      int32_t n = b < B ? units_of(p.seq_lens[b]) : 0;
+      if (n < 0) {
+        *s_bad = 1;
+        n = 0;
+      }
+      int32_t tot;
+      const int32_t incl = cta_inclusive_scan(n, warp_tot, &tot);
+      if (b < B) cu[b + 1] = (int32_t)(carry + incl);
+      carry += tot;
     }
-    int32_t tot;
-    const int32_t incl = cta_inclusive_scan(n, warp_tot, &tot);
-    if (b < B) cu[b + 1] = (int32_t)(carry + incl);
-    carry += tot;
-  }
-  __syncthreads();
-  const bool bad = *s_bad != 0 || carry > INT32_MAX;
-  StepMath M;
-  M.T = bad ? 0u : (uint32_t)carry;
-  const uint32_t W = M.T / kKv4PoolDiv;
-  M.S = M.T - W;
-  {
-    const uint32_t want = (M.S + kKv4MinPartDiv - 1) / kKv4MinPartDiv;
-    M.P = want < (uint32_t)G ? want : (uint32_t)G;
-    const uint32_t per = (uint32_t)kKv4ChunksPerCta * (uint32_t)G;
-    uint32_t c = (W + per - 1) / per;
-    const uint32_t frac = (uint32_t)kKv4PartChunks * M.P;
-    const uint32_t twelfth = M.P > 0 ? (M.S + frac - 1) / frac : 0;
-    c = c > twelfth ? c : twelfth;
-    M.C = c > (uint32_t)kKv4MinChunk ? c : (uint32_t)kKv4MinChunk;
-  }
-  M.chunks = (W + M.C - 1) / M.C;
-  M.small = (uint64_t)(M.S + 1) * (M.P + 1) < (uint64_t)UINT32_MAX;
-  if (blockIdx.x == 0 && tid == 0) {
-    if (bad) atomicOr(p.err, HPC_DEVCHK_BAD_LENGTH);
-    if (!kOneToken) p.owners[0] = (int32_t)(M.P + M.chunks);
-  }
-  // sequences without tiles (or a bad step): out = 0, lse = -inf
-  {
-    const uint32_t rows_of = (uint32_t)(T * H * kGroup);  // of a sequence: below 2^17
-    for (int64_t r = (int64_t)blockIdx.x * kThreads + tid; r < (int64_t)B * rows_of;
-         r += (int64_t)G * kThreads) {
-      const int b = (int)(r / rows_of);
-      if (!bad && cu[b + 1] != cu[b]) continue;
-      const uint32_t x = (uint32_t)(r - (int64_t)b * rows_of);
-      const uint32_t t = x / (uint32_t)(H * kGroup), j = x % (uint32_t)(H * kGroup);
-      uint4* o = reinterpret_cast<uint4*>(p.out + (int64_t)b * p.o_sb + (int64_t)t * p.o_st +
-                                          (int64_t)j * p.o_sh);
+    if (tid == 0 && carry > INT32_MAX) *s_bad = 1;
+    __syncthreads();
+  } else if (warp == kProducerWarp) {
+    int32_t n[kWarpPlan / 32];
 #pragma unroll
-      for (int i = 0; i < kHeadDim / 8; ++i) o[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (p.lse)
-        p.lse[(int64_t)b * p.l_sb + (int64_t)t * p.l_st + (int64_t)j * p.l_sh] = -INFINITY;
+    for (int i = 0; i < kWarpPlan / 32; ++i)
+      n[i] = 32 * i + lane < B ? p.seq_lens[32 * i + lane] : 0;
+    bool cannot = false;
+#pragma unroll
+    for (int i = 0; i < kWarpPlan / 32; ++i) {
+      if (32 * i >= B) break;
+      int32_t v = units_of(n[i]);
+      cannot |= v < 0;
+      v = v < 0 ? 0 : v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int32_t x = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += x;
+      }
+      if (32 * i + lane < B) cu[32 * i + lane + 1] = (int32_t)(carry + v);
+      carry += __shfl_sync(0xffffffffu, v, 31);
     }
+    cannot = __any_sync(0xffffffffu, cannot) || carry > INT32_MAX;
+    if (cannot && lane == 0) *s_bad = 1;
+    __syncwarp();
   }
+  // equal parts of the units to the CTAs, each of at least kMinPart
+  auto plan = [&]() -> PartPlan {
+    PartPlan M;
+    M.T = *s_bad ? 0u : (uint32_t)cu[B];
+    const uint32_t want = (M.T + kMinPart - 1) / kMinPart;
+    M.P = want < (uint32_t)G ? want : (uint32_t)G;
+    M.small = (uint64_t)(M.T + 1) * (M.P + 1) < (uint64_t)UINT32_MAX;
+    return M;
+  };
 
   if (warp == kProducerWarp) {
     // ------------------------------------------------------------ producer
+    const PartPlan M = plan();
     const uint64_t policy = evict_first_policy();
     bool stop = p.withhold_copies != 0;  // failure-path test: no copy is issued
     bool lost = false;                   // the consumers stopped taking pieces
-    uint32_t g = 0, issued = 0;
+    uint32_t g = 0, issued = 0;          // units walked, units issued ...
+    uint32_t last_mask = 0;              // ... and, where a wait gave up, the lanes behind them
     int j = 0;
-    // ask the pool for a chunk: the atomic's result is consumed only when the current
-    // owner is done, so its latency hides behind the copies
-    int pend = 0;
-    bool asked = false;
-    auto ask = [&]() {
-      if (lane == 0) pend = atomicAdd(p.pool, 1);
-      asked = true;
-    };
-    auto resolve = [&]() -> int {
-      const int c = __shfl_sync(0xffffffffu, pend, 0);
-      asked = false;
-      return (uint32_t)c < M.chunks ? (int)(M.P + (uint32_t)c) : -1;
-    };
+    if (blockIdx.x == 0 && lane == 0) {
+      if (*s_bad) atomicOr(p.err, HPC_DEVCHK_BAD_LENGTH);
+      if (!kOneToken) p.owners[0] = (int32_t)M.P;
+    }
+    // A piece's descriptor and, with it, its rows of q: a row to a lane.
     auto publish = [&](int b, int h, int t0, int t1, int flags, int slot) {
+      const int qs = j % kPieceQ;
+      const uint32_t pf = bar_pfull + 8 * qs;
+      const bool rows = !(flags & kFlagEnd) && !stop;
       if (lane == 0 && !lost) {
-        const int qs = j % kPieceQ;
         if (!wait_phase(bar_pfree + 8 * qs, ((j / kPieceQ) & 1u) ^ 1u, abort_flag, p.err,
                         book_ns, false)) {
           lost = true;
         } else {
           int* d = desc + qs * kDescInts;
           d[0] = b; d[1] = h; d[2] = t0; d[3] = t1;
-          d[4] = flags; d[5] = slot; d[6] = (int)g; d[7] = 0;
-          mbar_arrive(bar_pfull + 8 * qs);  // release: the descriptor is visible to its waiters
+          d[4] = flags; d[5] = slot; d[6] = (int)(g % kGroups); d[7] = 0;
+          // release: the descriptor is visible to its waiters
+          if (rows) mbar_arrive_expect_tx(pf, (uint32_t)(T * kGroup * kHeadDim * 2));
+          else mbar_arrive(pf);
         }
+      }
+      lost = __shfl_sync(0xffffffffu, (int)lost, 0) != 0;
+      if (rows && !lost) {
+        const uint32_t dq = smem_base + C::kQOff + qs * C::kQBytes;
+        for (int r = lane; r < T * kGroup; r += 32)
+          kv4_copy_row(dq + r * kQPitch,
+                       p.q + (int64_t)b * p.q_sb + (int64_t)(r / kGroup) * p.q_st +
+                           (int64_t)(h * kGroup + r % kGroup) * p.q_sh, pf);
       }
       ++j;
     };
-    int owner;
-    if (blockIdx.x < M.P) {
-      owner = blockIdx.x;
-    } else {
-      ask();
-      owner = resolve();
-    }
-    // the sequence holding unit x (cu[b] <= x < cu[b + 1])
+    // the sequence holding unit x: the last b with cu[b] <= x (no empty one is)
     auto seq_at = [&](uint32_t x) -> int {
-      int l0 = 0, h0 = B;  // last b with cu[b] <= x, then past empty sequences
-      while (h0 - l0 > 1) {
-        const int mid = (l0 + h0) >> 1;
-        if ((uint32_t)cu[mid] <= x) l0 = mid; else h0 = mid;
+      int at = 0;
+      for (int n = B; n > 1;) {
+        const int step = (n + 31) / 32, i = at + lane * step;
+        const uint32_t under = __ballot_sync(0xffffffffu, lane * step < n && (uint32_t)cu[i] <= x);
+        const int k = 31 - __clz((int)under);  // (lane 0's is)
+        at += k * step;
+        n = n - k * step < step ? n - k * step : step;
       }
-      while ((uint32_t)cu[l0 + 1] <= x) ++l0;
-      return l0;
+      return at;
     };
-    while (owner >= 0) {
-      const uint32_t lo = M.start(owner), hi = M.end(owner);
-      // The owner's first piece, then its last one where that is the head of a pair that
-      // goes on past hi, then the whole pairs between them: the pieces of split pairs are
-      // done early, and their merges overlap the rest (see step_kernel.cu).
-      uint32_t ra = lo, rb = hi;          // the range being walked
-      uint32_t rest_a = hi, rest_b = hi;  // whole pairs left for after it
-      bool first = false;                 // walking the first of several pieces
+    if (blockIdx.x < M.P) {
+      const int owner = (int)blockIdx.x;
+      const uint32_t lo = M.start(owner), hi = M.start(owner + 1);
+      // The part's first piece, then its last one where that is the head of a pair that goes
+      // on past hi, then the whole pairs between them: the pieces of split pairs are done
+      // early, and their merges overlap the rest.
+      uint32_t ra = lo, rb = hi;           // the range being walked
+      uint32_t rest_a = hi, rest_b = hi;   // whole pairs left for after it
+      bool first = false;                  // walking the first of several pieces
       int4 begun = make_int4(0, 0, 0, 0);  // the pair that begins here and goes on elsewhere
       int b = seq_at(lo);
       {
@@ -474,59 +511,84 @@ __global__ void __launch_bounds__(Cfg<TW, NP, NC>::kThreads, 1)
           first = true;
         }
       }
-      uint32_t left = hi - lo;  // units of this owner from the current one on
       for (;;) {
         for (uint32_t u = ra; u < rb;) {
           while ((uint32_t)cu[b + 1] <= u) ++b;
           const uint32_t nb = (uint32_t)(cu[b + 1] - cu[b]) / (uint32_t)H;
           const uint32_t rel = u - (uint32_t)cu[b];
           const uint32_t hu = rel / nb;
-          const int h = (int)hu, t0 = (int)(rel - hu * nb);
-          const uint32_t pair_lo = (uint32_t)cu[b] + hu * nb, pair_hi = pair_lo + nb;
+          const int h = (int)hu;
+          const uint32_t pair_hi = (uint32_t)cu[b] + (hu + 1) * nb;
+          const uint32_t pair_lo = pair_hi - nb + kPairCost;  // of its own units
           const uint32_t e = rb < pair_hi ? rb : pair_hi;
-          const int t1 = t0 + (int)(e - u);
-          const bool whole = t0 == 0 && t1 == (int)nb;
-          const int slot = whole ? -1 : (u == lo ? 2 * owner : 2 * owner + 1);
-          const int k = whole ? 1 : (int)(M.owner_of(pair_hi - 1) - M.owner_of(pair_lo) + 1);
-          if (!whole && t0 == 0) begun = make_int4(b, h, k, slot);
-          publish(b, h, t0, t1, (whole ? kFlagWhole : 0) | (k << 8), slot);
+          if (e <= pair_lo) {  // nothing but the pair's cost is here
+            u = e;
+            continue;
+          }
+          const int t0 = u > pair_lo ? (int)(u - pair_lo) : 0, t1 = (int)(e - pair_lo);
+          const int n = t1 - t0;
           const int32_t* btrow = p.block_table + (int64_t)b * p.bt_sb;
           const uint8_t* kh = p.k + (int64_t)h * p.c_shead;
           const uint8_t* vh = p.v + (int64_t)h * p.c_shead;
-          const int n = t1 - t0;
-          for (int i0 = 0; i0 < n; i0 += 32) {
-            const int i = i0 + lane;
-            int blk = -1;  // no block: zeros are read in its place
-            if (i < n) {
-              const int t = t0 + i;
-              if (t < p.max_blocks) {
-                const int v = __ldg(btrow + t);
-                if (v >= 0 && v < p.num_blocks) blk = v;
-                else atomicOr(p.err, HPC_DEVCHK_BAD_BLOCK);
-              } else {
-                atomicOr(p.err, HPC_DEVCHK_TABLE_TOO_SHORT);
+          // the block of unit i0 + lane of the piece; -1: none, zeros are read in its place
+          auto block_of = [&](int i0) -> int {
+            const int i = i0 + lane, t = t0 + i;
+            if (lane >= C::kBatch || i >= n) return -1;
+            if (t >= p.max_blocks) {
+              atomicOr(p.err, HPC_DEVCHK_TABLE_TOO_SHORT);
+              return -1;
+            }
+            const int v = __ldg(btrow + t);
+            if (v >= 0 && v < p.num_blocks) return v;
+            atomicOr(p.err, HPC_DEVCHK_BAD_BLOCK);
+            return -1;
+          };
+          int blk = block_of(0);
+          {
+            const bool whole = t0 == 0 && e == pair_hi;
+            const int slot = whole ? -1 : 2 * owner + (pair_lo <= lo ? 0 : 1);
+            const int k = whole ? 1 : (int)(M.owner_of(pair_hi - 1) - M.owner_of(pair_lo) + 1);
+            if (!whole && t0 == 0) begun = make_int4(b, h, k, slot);
+            publish(b, h, t0, t1, (whole ? kFlagWhole : 0) | (k << 8), slot);
+          }
+          // the next units of the piece, one to a lane: no more than the ring has slots, so
+          // that each lane's slot was last used by a unit that has been issued already
+          for (int i0 = 0; i0 < n; i0 += C::kBatch) {
+            const int cnt = n - i0 < C::kBatch ? n - i0 : C::kBatch;
+            const int next = i0 + C::kBatch < n ? block_of(i0 + C::kBatch) : -1;
+            const uint32_t gu = g + (uint32_t)lane, slot_r = gu % STAGES;
+            const uint32_t be = bar_empty + 8 * slot_r, par = ((gu / STAGES) & 1u) ^ 1u;
+            const uint32_t fb = bar_full + 8 * slot_r, dk = smem_base + slot_r * kStage;
+            const int64_t off = (int64_t)blk * p.c_sblk;
+            const void* ks = blk < 0 ? (const void*)kKv4NoTile : kh + off;
+            const void* vs = blk < 0 ? (const void*)kKv4NoTile : vh + off;
+            blk = next;
+            g += (uint32_t)cnt;
+            if (stop) continue;
+            bool todo = lane < cnt;
+            if (todo) {  // every lane issues as soon as its slot is free
+              unsigned long long since = 0;
+              for (uint32_t it = 1; todo; ++it) {
+                if (mbar_try_wait(be, par)) {
+                  mbar_arrive_expect_tx(fb, kStage);
+                  kv4_copy_tile(dk, ks, fb, policy);
+                  kv4_copy_tile(dk + kKv4Tile, vs, fb, policy);
+                  todo = false;
+                } else if ((it & 63u) == 0) {
+                  if (*abort_flag) break;
+                  if (since == 0) since = globaltimer();
+                  if (globaltimer() - since > p.timeout_ns) {
+                    atomicOr(p.err, HPC_DEVCHK_TIMEOUT);
+                    *abort_flag = 1;
+                    break;
+                  }
+                }
               }
             }
-            const int cnt = n - i0 < 32 ? n - i0 : 32;
-            for (int ii = 0; ii < cnt; ++ii, ++g, --left) {
-              const int bk = __shfl_sync(0xffffffffu, blk, ii);
-              if (!asked && left <= (uint32_t)kClaimAhead) ask();
-              if (lane != 0 || stop) continue;
-              const uint32_t slot_r = g % STAGES;
-              if (!wait_phase(bar_empty + 8 * slot_r, ((g / STAGES) & 1u) ^ 1u, abort_flag, p.err,
-                              p.timeout_ns)) {
-                stop = true;
-                continue;
-              }
-              const uint32_t fb = bar_full + 8 * slot_r;
-              const uint32_t dk = smem_base + slot_r * kStage;
-              const int64_t off = (int64_t)bk * p.c_sblk;
-              mbar_arrive_expect_tx(fb, kStage);
-              kv4_copy_tile(dk, bk < 0 ? (const void*)kKv4NoTile : kh + off, fb, policy);
-              kv4_copy_tile(dk + kKv4Tile, bk < 0 ? (const void*)kKv4NoTile : vh + off, fb, policy);
-              st_release_shared(issued_word + 4 * slot_r, g);
-              issued = g + 1;
-            }
+            __syncwarp();
+            last_mask = __ballot_sync(0xffffffffu, lane < cnt && !todo);
+            stop = __any_sync(0xffffffffu, todo);
+            issued = stop ? g - (uint32_t)cnt : g;
           }
           u = e;
         }
@@ -557,28 +619,26 @@ __global__ void __launch_bounds__(Cfg<TW, NP, NC>::kThreads, 1)
         break;
       }
       if (!kOneToken && lane == 0) *reinterpret_cast<int4*>(p.owners + 4 + 4 * owner) = begun;
-      if (!asked) ask();
-      owner = resolve();
-    }
-    // This CTA's failed request ended its work; the last CTA to get there resets the pool
-    // for the next step (every CTA asked for the last time).
-    if (lane == 0 && atomicAdd(p.pool + 1, 1) == G - 1) {
-      p.pool[0] = 0;
-      p.pool[1] = 0;
     }
     // one end marker per epilogue warp (they take alternate pieces; the consumer warps
     // stop at the first)
     for (int e = 0; e < kEpilogueWarps; ++e) publish(0, 0, 0, 0, kFlagEnd, -1);
     named_bar_sync(3, kThreads);
     if (lane == 0 && *abort_flag) {  // copies may still be landing: wait for the last ones
-      for (uint32_t u = issued > (uint32_t)STAGES ? issued - STAGES : 0; u < issued; ++u)
-        wait_phase(bar_full + 8 * (u % STAGES), (u / STAGES) & 1u, abort_flag, p.err,
-                   1000000000ull, false);
+      for (int i = j > kPieceQ ? j - kPieceQ : 0; !lost && i < j; ++i)
+        wait_phase(bar_pfull + 8 * (i % kPieceQ), (i / kPieceQ) & 1u, abort_flag, p.err, 1000000000ull,
+                   false);
+      for (uint32_t u = issued > (uint32_t)STAGES ? issued - STAGES : 0; u < issued + 32; ++u)
+        // (of a slot that was issued again, the later unit is waited for)
+        if (u < issued ? !(stop && u + STAGES < issued + 32 && (last_mask >> (u + STAGES - issued)) & 1u)
+                       : stop && (last_mask >> (u - issued)) & 1u)
+          wait_phase(bar_full + 8 * (u % STAGES), (u / STAGES) & 1u, abort_flag, p.err,
+                     1000000000ull, false);
     }
     return;
   }
 
-  uint4* dep = reinterpret_cast<uint4*>(smem + C::kDepOff);  // [warp][token][vector][lane]
+  uint4* dep0 = reinterpret_cast<uint4*>(smem + C::kDepOff);  // [warp][token][vector][lane]
   if (warp >= kEpilogueWarp0) {
     // ------------------------------------------------------------ epilogue
     // For every piece and token: join the states of the warps that shared its units,
@@ -589,7 +649,7 @@ __global__ void __launch_bounds__(Cfg<TW, NP, NC>::kThreads, 1)
       if (!wait_phase(bar_pfull + 8 * qs, (j / kPieceQ) & 1u, abort_flag, p.err, book_ns, false))
         break;
       const int* d = desc + qs * kDescInts;
-      const int b = d[0], h = d[1], fl = d[4], slot = d[5];
+      const int b = d[0], h = d[1], fl = d[4], slot = d[5], rot = d[6];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_pfree + 8 * qs);
       if (fl & kFlagEnd) break;
@@ -598,40 +658,45 @@ __global__ void __launch_bounds__(Cfg<TW, NP, NC>::kThreads, 1)
       if (!wait_phase(bar_dfull + 8 * (j % kEpilogueWarps), (j / kEpilogueWarps) & 1u, abort_flag,
                       p.err, book_ns, false))
         break;
+      const uint4* dep = dep0 + (j % C::kBufs) * (C::kDepBytes / 16);
       for (int t = 0; t < T; ++t) {
         Kv4State st;
         st.clear();
-        // the states of token t: warps t / TW, + NP, ...
+        // the states of token t, from the group that had the piece's first unit on: the
+        // order, like each group's units, is a function of the piece alone
+        auto state = [&](int v) -> const uint4* {
+          const int grp = rot + v < kGroups ? rot + v : rot + v - kGroups;
+          return dep + ((grp * NP + t / TW) * TW + t % TW) * (kDepVec * 32) + lane;
+        };
 #pragma unroll
         for (int v = 0; v < kGroups; ++v) {
-          const int at = ((t / TW + NP * v) * TW + t % TW) * kDepVec;
-          const float2 mv = *reinterpret_cast<const float2*>(dep + (at + 4) * 32 + lane);
+          const float2 mv = *reinterpret_cast<const float2*>(state(v) + 4 * 32);
           st.m[0] = fmaxf(st.m[0], mv.x);
           st.m[1] = fmaxf(st.m[1], mv.y);
         }
 #pragma unroll 1
         for (int v = 0; v < kGroups; ++v) {
-          const int at = ((t / TW + NP * v) * TW + t % TW) * kDepVec;
-          const float4 ml = *reinterpret_cast<const float4*>(dep + (at + 4) * 32 + lane);
+          const uint4* x = state(v);
+          const float4 ml = *reinterpret_cast<const float4*>(x + 4 * 32);
           const float w0 = ml.x == -INFINITY ? ml.z : ml.z * ex2(ml.x - st.m[0]);
           const float w1 = ml.y == -INFINITY ? ml.w : ml.w * ex2(ml.y - st.m[1]);
           st.l[0] += w0;
           st.l[1] += w1;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const uint4 h4 = dep[(at + k) * 32 + lane];
+            const uint4 h4 = x[k * 32];
             const uint32_t hw[4] = {h4.x, h4.y, h4.z, h4.w};
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const float2 o = __half22float2(*reinterpret_cast<const __half2*>(&hw[x]));
-              st.acc[2 * k + (x >> 1)][2 * (x & 1)] += o.x * w0;
-              st.acc[2 * k + (x >> 1)][2 * (x & 1) + 1] += o.y * w1;
+            for (int y = 0; y < 4; ++y) {
+              const float2 o = __half22float2(*reinterpret_cast<const __half2*>(&hw[y]));
+              st.acc[2 * k + (y >> 1)][2 * (y & 1)] += o.x * w0;
+              st.acc[2 * k + (y >> 1)][2 * (y & 1) + 1] += o.y * w1;
             }
           }
         }
         if (t == T - 1) {
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar_dfree);  // the consumers may deposit the next piece
+          if (lane == 0) mbar_arrive(bar_dfree + 8 * (j % C::kBufs));  // the buffer is free
         }
         if (fl & kFlagWhole) {
           st.write(p, b, t, h, lane);
@@ -645,69 +710,82 @@ __global__ void __launch_bounds__(Cfg<TW, NP, NC>::kThreads, 1)
       // each by its last piece, so that no warp reads more than a few dozen states. One
       // acquire-release atomic by lane 0 covers the warp's writes (ordered before it by the
       // warp barrier) and the other pieces', which the warp reads after the second one.
+      const PartPlan M = plan();
       const int k = fl >> 8, owner = slot >> 1;
       const uint32_t nb = (uint32_t)(cu[b + 1] - cu[b]) / (uint32_t)H;
-      const uint32_t A = (uint32_t)cu[b] + (uint32_t)h * nb;
+      const uint32_t A = (uint32_t)cu[b] + (uint32_t)h * nb + kPairCost;
       const int first = (int)M.owner_of(A);
-      auto slot_of = [&](int ow) -> int64_t { return 2 * (int64_t)ow + (A <= M.start(ow) ? 0 : 1); };
-      auto arrive = [&](int32_t* cnt, int of) -> bool {
+      // piece i of the pair: the first one can be its part's last, the others are their parts' first
+      const int64_t slot0 = 2 * (int64_t)first + (A <= M.start(first) ? 0 : 1);
+      auto place = [&](int i) -> float4* {
+        return p.ws + (i == 0 ? slot0 : 2 * (int64_t)(first + i)) * kKv4PartFloat4 + lane;
+      };
+      bool last_level = k <= kFan;
+      int at = last_level ? 0 : (owner - first) / kFan * kFan, step = 1;
+      int count = k - at < kFan ? k - at : kFan;
+      for (;;) {  // (one piece of code for both levels: it runs cold)
+        int32_t* cnt = last_level ? p.pair_cnt + (int64_t)b * H + h
+                                  : p.slot_cnt + (at == 0 ? slot0 : 2 * (int64_t)(first + at));
         __syncwarp();
-        int last = 0;
+        int arrived = 0;
         if (lane == 0) {
-          last = atom_add_acq_rel_gpu(cnt, 1) == of - 1;
-          if (last) *cnt = 0;  // ready for the next step
+          arrived = atom_add_acq_rel_gpu(cnt, 1) == count - 1;
+          if (arrived) *cnt = 0;  // ready for the next step
         }
-        last = __shfl_sync(0xffffffffu, last, 0);
+        arrived = __shfl_sync(0xffffffffu, arrived, 0);
         __syncwarp();
-        return last != 0;
-      };
-      auto join = [&](Kv4State& st, int ow, int n, int step) {
+        if (!arrived) break;
+        Kv4State st;
         st.clear();
-        for (int i = 0; i < n; i += 2) {
-          const float4* s0 = p.ws + slot_of(ow + i * step) * kKv4PartFloat4 + lane;
-          const float4* s1 =
-              i + 1 < n ? p.ws + slot_of(ow + (i + 1) * step) * kKv4PartFloat4 + lane : nullptr;
-          st.add2(s0, s1);
+#pragma unroll 1
+        for (int i = 0; i < count; i += 2)
+          st.add2(place(at + i * step), i + 1 < count ? place(at + (i + 1) * step) : nullptr);
+        if (last_level) {
+          st.write(p, b, 0, h, lane);
+          break;
         }
-      };
-      int groups = k, step = 1;
-      Kv4State st;
-      if (k > kFan) {
-        const int gi = (owner - first) / kFan, lead = first + gi * kFan;
-        const int n = k - gi * kFan < kFan ? k - gi * kFan : kFan;
-        const int64_t at = slot_of(lead);
-        if (!arrive(p.slot_cnt + at, n)) continue;
-        join(st, lead, n, 1);
-        st.store(p.ws + at * kKv4PartFloat4 + lane);
-        groups = (k + kFan - 1) / kFan;
+        st.store(place(at));
+        last_level = true;
+        at = 0;
         step = kFan;
+        count = (k + kFan - 1) / kFan;
       }
-      if (!arrive(p.pair_cnt + (int64_t)b * H + h, groups)) continue;
-      join(st, first, groups, step);
-      st.write(p, b, 0, h, lane);
+    }
+    // sequences without tiles (or a step that cannot be): out = 0, lse = -inf
+    for (int b = (int)blockIdx.x * kEpilogueWarps + warp - kEpilogueWarp0; b < B;
+         b += G * kEpilogueWarps) {
+      if (!*s_bad && cu[b + 1] != cu[b]) continue;
+      for (int t = 0; t < T; ++t)
+        for (int j = lane; j < H * kGroup; j += 32) {
+          uint4* o = reinterpret_cast<uint4*>(p.out + (int64_t)b * p.o_sb + (int64_t)t * p.o_st +
+                                              (int64_t)j * p.o_sh);
+#pragma unroll
+          for (int i = 0; i < kHeadDim / 8; ++i) o[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (p.lse)
+            p.lse[(int64_t)b * p.l_sb + (int64_t)t * p.l_st + (int64_t)j * p.l_sh] = -INFINITY;
+        }
     }
     named_bar_sync(3, kThreads);
     return;
   }
 
   // -------------------------------------------------------------- consumers
-  // Groups of NP warps take a piece's units in turn, each warp for its own tokens, and
-  // deposit their states; they wait for each other only at the deposit buffer.
+  // Groups of NP warps take the CTA's units in turn, each warp for its own tokens, whatever
+  // pieces they belong to: a group's units come to its own slots in its own order, so the
+  // parities of its waits are exact. At a piece's end every warp deposits its states; warps
+  // wait for each other only at the deposit buffers.
   const int slice = warp % NP, grp = warp / NP;
+  uint32_t slot = (uint32_t)grp, phase = 0;  // of the group's next unit
   bool dead = false;
   for (int j = 0;; ++j) {
     const int qs = j % kPieceQ;
     if (!wait_phase(bar_pfull + 8 * qs, (j / kPieceQ) & 1u, abort_flag, p.err, book_ns, false))
       break;  // no descriptor arrived: the producer is gone
     const int* d = desc + qs * kDescInts;
-    const int b = d[0], h = d[1], t0 = d[2], t1 = d[3], fl = d[4], g0 = d[6];
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar_pfree + 8 * qs);  // this warp has read the descriptor
+    const int b = d[0], t0 = d[2], t1 = d[3], fl = d[4], rot = d[6];
     if (fl & kFlagEnd) break;
     const int n = t1 - t0;
-    // a function of the piece alone, so a piece gives the same bits whichever CTA runs it
-    const int rot = (int)(((int64_t)t0 + (int64_t)b * H + h) % kGroups);
-    const int i0 = (grp - rot + kGroups) % kGroups;  // this group's first unit
+    const int i0 = grp >= rot ? grp - rot : grp - rot + kGroups;  // this group's first unit
     float m[TW][2], l[TW][2], acc[TW][8][4];
 #pragma unroll
     for (int t = 0; t < TW; ++t) {
@@ -717,43 +795,45 @@ __global__ void __launch_bounds__(Cfg<TW, NP, NC>::kThreads, 1)
       for (int dm = 0; dm < 8; ++dm)
         acc[t][dm][0] = acc[t][dm][1] = acc[t][dm][2] = acc[t][dm][3] = 0.f;
     }
+    uint32_t qf[TW][8][2];
+    float sl2[TW];
+    int len = 0;
     if (i0 < n) {
-      const int len = __ldg(p.seq_lens + b);
-      uint32_t qf[TW][8][2];
-      float sl2[TW];
-      int off[TW];  // tokens that the warp's tokens do not see at the end
+      len = __ldg(p.seq_lens + b);
 #pragma unroll
       for (int t = 0; t < TW; ++t) {
         // (a warp's second token past the last one repeats it, and is not written)
         const int tok = TW * slice + t < T ? TW * slice + t : T - 1;
-        const float qinv =
-            load_q4(p.q + (int64_t)b * p.q_sb + (int64_t)tok * p.q_st + (int64_t)(h * kGroup) * p.q_sh,
-                    p.q_sh, lane, qf[t]);
+        const float qinv = load_q4(
+            smem_base + C::kQOff + qs * C::kQBytes + tok * (kGroup * kQPitch), lane, qf[t]);
         // (a factor of 0 would make NaN of masked scores, an infinite one of scores of 0)
         sl2[t] = fminf(fmaxf(p.score_scale_log2 * qinv, FLT_MIN), FLT_MAX);
-        off[t] = T - 1 - tok;
       }
-      for (int i = i0; i < n; i += kGroups) {
-        const uint32_t gu = (uint32_t)(g0 + i);
-        const uint32_t s = gu % STAGES;
-        if (dead) continue;
-        const bool ok = wait_issued(issued_word + 4 * s, gu, abort_flag, p.err, p.timeout_ns) &&
-                        wait_phase(bar_full + 8 * s, (gu / STAGES) & 1u, abort_flag, p.err,
-                                   p.timeout_ns);
-        if (!__all_sync(0xffffffffu, ok)) {  // warp-uniform decision
-          dead = true;
-          continue;
-        }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_pfree + 8 * qs);  // this warp has read the descriptor and q
+    for (int i = i0; i < n; i += kGroups) {
+      if (!dead) {
+        const bool ok = wait_phase(bar_full + 8 * slot, phase, abort_flag, p.err, p.timeout_ns);
+        dead = !__all_sync(0xffffffffu, ok);  // warp-uniform decision
+      }
+      if (!dead) {
         const int stored = len - (t0 + i) * kBlockTokens;
         int seen[TW];
 #pragma unroll
-        for (int t = 0; t < TW; ++t) seen[t] = stored - off[t];
+        for (int t = 0; t < TW; ++t)  // (the warp's tokens do not see the last ones)
+          seen[t] = stored - (TW * slice + t < T ? T - 1 - TW * slice - t : 0);
         if (seen[TW - 1] > 0) {
-          const uint32_t kb = smem_base + s * kStage;
+          const uint32_t kb = smem_base + slot * kStage;
           compute_unit4<TW>(kb, kb + kKv4Tile, qf, seen, stored, sl2, m, l, acc, lane);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar_empty + 8 * s);
+        if (lane == 0) mbar_arrive(bar_empty + 8 * slot);
+      }
+      slot += kGroups;
+      if (slot >= STAGES) {
+        slot -= STAGES;
+        phase ^= 1u;
       }
     }
     // row sums over the 8 lanes sharing a query-head pair
@@ -764,9 +844,11 @@ __global__ void __launch_bounds__(Cfg<TW, NP, NC>::kThreads, 1)
         l[t][0] += __shfl_xor_sync(0xffffffffu, l[t][0], o);
         l[t][1] += __shfl_xor_sync(0xffffffffu, l[t][1], o);
       }
-    // deposit once the epilogue warp has read the previous piece's states: o = acc / l in
+    // deposit once the epilogue warp has read its previous piece's states: o = acc / l in
     // f16 (2^-11; |o| is at most the largest |code * scale|, 2688), m and l in fp32
-    wait_phase(bar_dfree, (j & 1u) ^ 1u, abort_flag, p.err, book_ns, false);
+    wait_phase(bar_dfree + 8 * (j % C::kBufs), ((j / C::kBufs) & 1u) ^ 1u, abort_flag, p.err,
+               book_ns, false);
+    uint4* dep = dep0 + (j % C::kBufs) * (C::kDepBytes / 16);
 #pragma unroll
     for (int t = 0; t < TW; ++t) {
       const float v0 = l[t][0] == 0.f ? 0.f : __fdividef(1.f, l[t][0]);
