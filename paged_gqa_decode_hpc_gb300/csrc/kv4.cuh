@@ -60,13 +60,6 @@ __device__ __forceinline__ uint32_t both_high(uint32_t a) {
 }
 
 // One tile to shared memory: 16-byte aligned at both ends.
-__device__ __forceinline__ void kv4_copy_tile(uint32_t dst, const void* src, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-          "r"(dst),
-      "l"(__cvta_generic_to_global(src)), "r"((uint32_t)kKv4Tile), "r"(bar)
-      : "memory");
-}
 __device__ __forceinline__ void kv4_copy_tile(uint32_t dst, const void* src, uint32_t bar,
                                               uint64_t policy) {
   asm volatile(
@@ -76,12 +69,13 @@ __device__ __forceinline__ void kv4_copy_tile(uint32_t dst, const void* src, uin
       : "memory");
 }
 
-// A row of 128 bf16.
-__device__ __forceinline__ void kv4_copy_row(uint32_t dst, const void* src, uint32_t bar) {
+// Any multiple of 16 bytes.
+__device__ __forceinline__ void kv4_copy(uint32_t dst, const void* src, uint32_t bytes,
+                                         uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], 256, [%2];" ::"r"(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
           dst),
-      "l"(__cvta_generic_to_global(src)), "r"(bar)
+      "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(bar)
       : "memory");
 }
 

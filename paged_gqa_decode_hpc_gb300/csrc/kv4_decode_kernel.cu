@@ -49,21 +49,24 @@
 namespace hpc {
 namespace {
 
-constexpr int kEpilogueWarps = 2;                 // taking pieces in turn
+// Warpgroups 0 and 1: consumer warps. Warpgroup 2: epilogue, each of its warps a quarter of
+// every state. Warpgroup 3: the producer warp and three that leave at once.
+constexpr int kConsumerWarps = 8, kEpilogueWarp0 = 8, kEpilogueWarps = 4, kProducerWarp = 12;
+constexpr int kThreads = 512;
 constexpr int kPieceQ = 4;                        // piece descriptors in flight
-static_assert(kPieceQ % kEpilogueWarps == 0, "queue slots per epilogue warp");
 constexpr int kDescInts = 8;
 constexpr int kDepVec = 5;                        // 16-byte words per lane of a deposited state
 constexpr int kStage = 2 * kKv4Tile;
-constexpr int kQPitch = 272;                      // bytes between rows of q in shared memory
-// Bookkeeping waits give up this many data waits later (see step_kernel.cu).
+constexpr int kQRow = kHeadDim * 2;               // bytes of a row of q in shared memory
+// Bookkeeping waits give up this many data waits later: once a data wait has timed out
+// every role runs on without copies, and this bookkeeping must then still finish, so that
+// the arrival counters return to zero.
 constexpr unsigned long long kBookkeepingWaits = 8;
 constexpr int kFlagEnd = 1, kFlagWhole = 2;
 // What a (sequence, KV head) pair costs beside its units, in units: its q, its states' way
 // through the epilogue. The plan gives every pair so many units more, ahead of its own.
 constexpr int kPairCost = 4;
 constexpr int kFan = 16;                          // pieces of a pair that are joined at once
-
 constexpr int kMinPart = 8;                       // units that a CTA is worth starting for
 constexpr int kWarpPlan = 256;                    // sequences that one warp plans by itself
 
@@ -80,33 +83,46 @@ struct PartPlan {
   }
 };
 
-// TW tokens to a warp, NP warps to a unit, NC consumer warps (a multiple of NP).
-template <int TW, int NP, int NC>
+// TW tokens to a warp, NP warps to a unit.
+template <int TW, int NP>
 struct Cfg {
-  static constexpr int kThreads = (NC + 1 + kEpilogueWarps) * 32;
-  // deposited states: two buffers, so that warps may run a piece ahead, where they fit
+  static constexpr int kGroups = kConsumerWarps / NP;  // units in work at once, each group's in its own slots
+  static constexpr int kActive = kGroups * NP;         // warps that work (of 8)
+  // deposit buffers: two, so that warps may run a piece ahead, where they fit
   static constexpr int kBufs = TW == 1 ? 2 : 1;
-  static constexpr int kDepBytes = NC * TW * kDepVec * 32 * 16;
-  static constexpr int kQBytes = TW * NP * 8 * kQPitch;          // a piece's rows of q
-  static constexpr int kFixed = kBufs * kDepBytes + kPieceQ * kQBytes + 2048 /* barriers, descriptors, scan */ + 128 + 4 * (kKv4MaxSeqs + 1);
-  static constexpr int kGroups = NC / NP;  // units in work at once; each group has its own slots
+  static constexpr int kDepBytes = kActive * TW * kDepVec * 32 * 16;
+  static constexpr int kQBytes = TW * NP * kGroup * kQRow;  // a piece's rows of q
+  static constexpr int kFixed =
+      kBufs * kDepBytes + kPieceQ * kQBytes + 1024 /* barriers, descriptors, scan */ + 128 + 4 * (kKv4MaxSeqs + 1);
   static constexpr int kStages = (227 * 1024 - kFixed) / kStage / kGroups * kGroups;
-  static constexpr int kBatch = kStages < 16 ? 8 : 16;  // units whose blocks are looked up at once
+  static constexpr int kBatch = kStages < 16 ? 8 : 16;  // units that the producer takes at once
   static constexpr int kDepOff = kStages * kStage;
   static constexpr int kQOff = kDepOff + kBufs * kDepBytes;
   static constexpr int kBarOff = kQOff + kPieceQ * kQBytes;
-  // full, empty, piece full, piece free, deposit full (one per epilogue warp), deposit free
-  static constexpr int kNumBars = 2 * kStages + 2 * kPieceQ + kEpilogueWarps + kBufs;
+  // full, empty, piece full, piece free, deposit full, deposit free
+  static constexpr int kNumBars = 2 * kStages + 2 * kPieceQ + 2 * kBufs;
   static constexpr int kDescOff = kBarOff + 8 * ((kNumBars + 1) / 2 * 2);
   static constexpr int kMiscOff = kDescOff + 4 * kDescInts * kPieceQ;
   static constexpr int kPlanOff = kMiscOff + 256;  // abort flag, flags, scan scratch
   static constexpr int kSmemBytes = 128 /* alignment slack */ + kPlanOff;
   static constexpr int kSmemBytesMax = kSmemBytes + 4 * (kKv4MaxSeqs + 1);
   static_assert(kSmemBytesMax <= 227 * 1024, "shared memory");
-  static_assert(NC % NP == 0, "whole groups of warps");
-  static_assert(kThreads <= 512, "a scan pass");
-  static_assert(kBatch <= kStages, "a slot to each lane");
+  static_assert(kBatch <= kStages, "a slot to each unit of a batch");
+  // Registers a thread, of the 128 that the launch gives each (one warp of each warpgroup
+  // to an SM sub-partition, so that the four add up to 512).
+  static constexpr int kRegsConsumer = TW == 1 ? 168 : 192;
+  static constexpr int kRegsEpilogue = TW == 1 ? 104 : 72;
+  static constexpr int kRegsProducer = TW == 1 ? 72 : 56;
+  static_assert(2 * kRegsConsumer + kRegsEpilogue + kRegsProducer == 512, "registers");
 };
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N) : "memory");
+}
 
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
   return *reinterpret_cast<const uint2*>(__cvta_shared_to_generic(a));
@@ -129,12 +145,12 @@ __device__ __forceinline__ uint32_t select_bits(uint32_t a, uint32_t b, uint32_t
 // The token of row i of group 0 of a half, over 4.
 __device__ __forceinline__ int row_token(int i) { return (int)((0x53427160u >> (4 * i)) & 7u); }
 
-// 8 rows of q, kQPitch bytes apart in shared memory, as B operands in K's order of elements:
+// 8 rows of q in shared memory as B operands in K's order of elements:
 // register j of k-step ks holds elements 64 (ks / 4) + 16 c + 4 (ks % 4) + 2 j, + 1 of query
 // head g. Returns the factor that undoes the power of two of the conversion.
 __device__ __forceinline__ float load_q4(uint32_t q, int lane, uint32_t (&qf)[8][2]) {
   const int g = lane >> 2, c = lane & 3;
-  const uint32_t row = q + (uint32_t)(g * kQPitch + 32 * c);
+  const uint32_t row = q + (uint32_t)(g * kQRow + 32 * c);
   uint4 u[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -331,12 +347,11 @@ __device__ __forceinline__ void compute_unit4(uint32_t kb, uint32_t vb,
   }
 }
 
-template <int TW, int NP, int NC>
-__global__ void __launch_bounds__(Cfg<TW, NP, NC>::kThreads, 1)
+template <int TW, int NP>
+__global__ void __launch_bounds__(kThreads, 1)
     kv4_decode_kernel(const __grid_constant__ Kv4DecodeParams p) {
-  using C = Cfg<TW, NP, NC>;
-  constexpr int STAGES = C::kStages, kThreads = C::kThreads, kGroups = C::kGroups;
-  constexpr int kProducerWarp = NC, kEpilogueWarp0 = NC + 1;
+  using C = Cfg<TW, NP>;
+  constexpr int STAGES = C::kStages, kGroups = C::kGroups;
   constexpr bool kOneToken = TW == 1;  // pieces are merged here, not by a second kernel
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) &
@@ -346,29 +361,33 @@ __global__ void __launch_bounds__(Cfg<TW, NP, NC>::kThreads, 1)
   const uint32_t bar_empty = bar_full + 8 * STAGES;
   const uint32_t bar_pfull = bar_empty + 8 * STAGES;
   const uint32_t bar_pfree = bar_pfull + 8 * kPieceQ;
-  const uint32_t bar_dfull = bar_pfree + 8 * kPieceQ;  // + 8 * (piece % kEpilogueWarps)
-  const uint32_t bar_dfree = bar_dfull + 8 * kEpilogueWarps;
+  const uint32_t bar_dfull = bar_pfree + 8 * kPieceQ;
+  const uint32_t bar_dfree = bar_dfull + 8 * C::kBufs;
   int* desc = reinterpret_cast<int*>(smem + C::kDescOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kMiscOff);
-  int* s_bad = reinterpret_cast<int*>(smem + C::kMiscOff + 8);
+  volatile int* s_bad = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 8);
+  volatile int* s_last = reinterpret_cast<volatile int*>(smem + C::kMiscOff + 16);
   const unsigned long long book_ns = p.timeout_ns * kBookkeepingWaits;
   int32_t* warp_tot = reinterpret_cast<int32_t*>(smem + C::kMiscOff + 128);
-  int32_t* cu = reinterpret_cast<int32_t*>(smem + C::kPlanOff);
+  int32_t* cu = reinterpret_cast<int32_t*>(smem + C::kPlanOff);  // units of a KV head ahead of b
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
-  const int B = p.num_seqs, H = p.num_kv_heads, G = (int)gridDim.x, T = p.q_len;
+  const int B = p.num_seqs, G = (int)gridDim.x, T = p.q_len;
+  const uint32_t H = (uint32_t)p.num_kv_heads;
 
   if (tid == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(bar_full + 8 * s, 1);
+      mbar_init(bar_full + 8 * s, 2);   // K and V
       mbar_init(bar_empty + 8 * s, NP);  // the warps of a unit
     }
     for (int s = 0; s < kPieceQ; ++s) {
       mbar_init(bar_pfull + 8 * s, 1);
-      mbar_init(bar_pfree + 8 * s, NC + 1);  // the consumer warps and the piece's epilogue warp
+      mbar_init(bar_pfree + 8 * s, C::kActive + kEpilogueWarps);
     }
-    for (int e = 0; e < kEpilogueWarps; ++e) mbar_init(bar_dfull + 8 * e, NC);
-    for (int e = 0; e < C::kBufs; ++e) mbar_init(bar_dfree + 8 * e, 1);
+    for (int e = 0; e < C::kBufs; ++e) {
+      mbar_init(bar_dfull + 8 * e, C::kActive);
+      mbar_init(bar_dfree + 8 * e, kEpilogueWarps);
+    }
     *abort_flag = 0;
     *s_bad = 0;
     cu[0] = 0;
@@ -379,18 +398,17 @@ __global__ void __launch_bounds__(Cfg<TW, NP, NC>::kThreads, 1)
   griddep_launch_dependents();
   __syncthreads();
 
-  // ---- plan: units per sequence (the pairs' costs among them), prefix in shared memory. The
-  // producer plans small batches by itself; whoever else looks at the plan has waited for a
-  // piece of it by then.
+  // ---- plan: units of a KV head per sequence (the pair's cost among them), prefix in shared
+  // memory. The producer plans small batches by itself; whoever else looks at the plan has
+  // waited for a piece of it by then.
   auto units_of = [&](int32_t len) -> int32_t {  // -1: cannot be
-    // a sequence of more units than INT32_MAX / 512 is refused, so that no partial sum of a
-    // scan pass, of at most 512 sequences, wraps
-    const int64_t n =
-        len > 0 ? (((int64_t)len + kBlockTokens - 1) / kBlockTokens + kPairCost) * H : 0;
-    return len < 0 || n > (int64_t)(INT32_MAX / 512) ? -1 : (int32_t)n;
+    // more units than INT32_MAX / 512 are refused, so that no partial sum of a scan pass, of
+    // 512 sequences, wraps
+    const int64_t n = len > 0 ? ((int64_t)len + kBlockTokens - 1) / kBlockTokens + kPairCost : 0;
+    return len < 0 || n * H > (int64_t)(INT32_MAX / 512) ? -1 : (int32_t)n;
   };
-  int64_t carry = 0;
   if (B > kWarpPlan) {
+    int64_t carry = 0;
     for (int base = 0; base < B; base += kThreads) {
       const int b = base + tid;
       int32_t n = b < B ? units_of(p.seq_lens[b]) : 0;
@@ -403,7 +421,7 @@ __global__ void __launch_bounds__(Cfg<TW, NP, NC>::kThreads, 1)
       if (b < B) cu[b + 1] = (int32_t)(carry + incl);
       carry += tot;
     }
-    if (tid == 0 && carry > INT32_MAX) *s_bad = 1;
+    if (tid == 0 && carry * H > INT32_MAX) *s_bad = 1;
     __syncthreads();
   } else if (warp == kProducerWarp) {
     int32_t n[kWarpPlan / 32];
@@ -411,6 +429,7 @@ __global__ void __launch_bounds__(Cfg<TW, NP, NC>::kThreads, 1)
     for (int i = 0; i < kWarpPlan / 32; ++i)
       n[i] = 32 * i + lane < B ? p.seq_lens[32 * i + lane] : 0;
     bool cannot = false;
+    int64_t carry = 0;
 #pragma unroll
     for (int i = 0; i < kWarpPlan / 32; ++i) {
       if (32 * i >= B) break;
@@ -425,34 +444,40 @@ __global__ void __launch_bounds__(Cfg<TW, NP, NC>::kThreads, 1)
       if (32 * i + lane < B) cu[32 * i + lane + 1] = (int32_t)(carry + v);
       carry += __shfl_sync(0xffffffffu, v, 31);
     }
-    cannot = __any_sync(0xffffffffu, cannot) || carry > INT32_MAX;
+    cannot = __any_sync(0xffffffffu, cannot) || carry * H > INT32_MAX;
     if (cannot && lane == 0) *s_bad = 1;
     __syncwarp();
   }
   // equal parts of the units to the CTAs, each of at least kMinPart
   auto plan = [&]() -> PartPlan {
     PartPlan M;
-    M.T = *s_bad ? 0u : (uint32_t)cu[B];
+    M.T = *s_bad ? 0u : (uint32_t)cu[B] * H;
     const uint32_t want = (M.T + kMinPart - 1) / kMinPart;
     M.P = want < (uint32_t)G ? want : (uint32_t)G;
     M.small = (uint64_t)(M.T + 1) * (M.P + 1) < (uint64_t)UINT32_MAX;
     return M;
   };
 
-  if (warp == kProducerWarp) {
+  if (warp >= kProducerWarp) {
+    regs_dec<C::kRegsProducer>();
+    if (warp != kProducerWarp) {
+      named_bar_sync(3, kThreads);
+      return;
+    }
     // ------------------------------------------------------------ producer
     const PartPlan M = plan();
     const uint64_t policy = evict_first_policy();
     bool stop = p.withhold_copies != 0;  // failure-path test: no copy is issued
     bool lost = false;                   // the consumers stopped taking pieces
-    uint32_t g = 0, issued = 0;          // units walked, units issued ...
-    uint32_t last_mask = 0;              // ... and, where a wait gave up, the lanes behind them
+    uint32_t g = 0, issued = 0;          // units walked, units issued
+    uint32_t last_mask = 0;              // where a wait gave up, the lanes that issued behind them
     int j = 0;
     if (blockIdx.x == 0 && lane == 0) {
       if (*s_bad) atomicOr(p.err, HPC_DEVCHK_BAD_LENGTH);
       if (!kOneToken) p.owners[0] = (int32_t)M.P;
     }
-    // A piece's descriptor and, with it, its rows of q: a row to a lane.
+    // A piece's descriptor and, with it, its rows of q.
+    const bool q_whole = p.q_sh == kHeadDim;  // 8 rows in one piece of memory
     auto publish = [&](int b, int h, int t0, int t1, int flags, int slot) {
       const int qs = j % kPieceQ;
       const uint32_t pf = bar_pfull + 8 * qs;
@@ -462,35 +487,61 @@ __global__ void __launch_bounds__(Cfg<TW, NP, NC>::kThreads, 1)
                         book_ns, false)) {
           lost = true;
         } else {
-          int* d = desc + qs * kDescInts;
-          d[0] = b; d[1] = h; d[2] = t0; d[3] = t1;
-          d[4] = flags; d[5] = slot; d[6] = (int)(g % kGroups); d[7] = 0;
+          int4* d = reinterpret_cast<int4*>(desc + qs * kDescInts);
+          d[0] = make_int4(b, h, t0, t1);
+          d[1] = make_int4(flags, slot, (int)(g % kGroups), 0);
           // release: the descriptor is visible to its waiters
-          if (rows) mbar_arrive_expect_tx(pf, (uint32_t)(T * kGroup * kHeadDim * 2));
+          if (rows) mbar_arrive_expect_tx(pf, (uint32_t)(T * kGroup * kQRow));
           else mbar_arrive(pf);
         }
       }
       lost = __shfl_sync(0xffffffffu, (int)lost, 0) != 0;
       if (rows && !lost) {
         const uint32_t dq = smem_base + C::kQOff + qs * C::kQBytes;
-        for (int r = lane; r < T * kGroup; r += 32)
-          kv4_copy_row(dq + r * kQPitch,
-                       p.q + (int64_t)b * p.q_sb + (int64_t)(r / kGroup) * p.q_st +
-                           (int64_t)(h * kGroup + r % kGroup) * p.q_sh, pf);
+        const __nv_bfloat16* q0 =
+            p.q + (int64_t)b * p.q_sb + (int64_t)(h * kGroup) * p.q_sh;
+        if (q_whole) {
+          if (lane < T)
+            kv4_copy(dq + lane * (kGroup * kQRow), q0 + (int64_t)lane * p.q_st, kGroup * kQRow, pf);
+        } else {
+          for (int r = lane; r < T * kGroup; r += 32)
+            kv4_copy(dq + r * kQRow,
+                     q0 + (int64_t)(r / kGroup) * p.q_st + (int64_t)(r % kGroup) * p.q_sh, kQRow, pf);
+        }
       }
       ++j;
     };
-    // the sequence holding unit x: the last b with cu[b] <= x (no empty one is)
-    auto seq_at = [&](uint32_t x) -> int {
-      int at = 0;
+    // The pair that holds unit x: sequence, KV head, the pair's first unit and their number
+    // (the cost among them).
+    struct Pair {
+      int b;
+      uint32_t h, base, nb;
+    };
+    auto pair_at = [&](uint32_t x) -> Pair {
+      int at = 0;  // the last b with cu[b] * H <= x: no empty sequence
       for (int n = B; n > 1;) {
         const int step = (n + 31) / 32, i = at + lane * step;
-        const uint32_t under = __ballot_sync(0xffffffffu, lane * step < n && (uint32_t)cu[i] <= x);
+        const uint32_t under =
+            __ballot_sync(0xffffffffu, lane * step < n && (uint32_t)cu[i] * H <= x);
         const int k = 31 - __clz((int)under);  // (lane 0's is)
         at += k * step;
         n = n - k * step < step ? n - k * step : step;
       }
-      return at;
+      Pair r;
+      r.b = at;
+      r.base = (uint32_t)cu[at] * H;
+      r.nb = (uint32_t)(cu[at + 1] - cu[at]);
+      r.h = (x - r.base) / r.nb;
+      r.base += r.h * r.nb;
+      return r;
+    };
+    auto next = [&](Pair& r) {
+      r.base += r.nb;
+      if (++r.h < H) return;
+      r.h = 0;
+      do ++r.b;
+      while (r.b < B && cu[r.b + 1] == cu[r.b]);
+      if (r.b < B) r.nb = (uint32_t)(cu[r.b + 1] - cu[r.b]);
     };
     if (blockIdx.x < M.P) {
       const int owner = (int)blockIdx.x;
@@ -498,154 +549,130 @@ __global__ void __launch_bounds__(Cfg<TW, NP, NC>::kThreads, 1)
       // The part's first piece, then its last one where that is the head of a pair that goes
       // on past hi, then the whole pairs between them: the pieces of split pairs are done
       // early, and their merges overlap the rest.
-      uint32_t ra = lo, rb = hi;           // the range being walked
-      uint32_t rest_a = hi, rest_b = hi;   // whole pairs left for after it
-      bool first = false;                  // walking the first of several pieces
       int4 begun = make_int4(0, 0, 0, 0);  // the pair that begins here and goes on elsewhere
-      int b = seq_at(lo);
-      {
-        const uint32_t nb0 = (uint32_t)(cu[b + 1] - cu[b]) / (uint32_t)H;
-        const uint32_t e0 = (uint32_t)cu[b] + ((lo - (uint32_t)cu[b]) / nb0 + 1) * nb0;
-        if (e0 < hi) {
-          rb = e0;
-          first = true;
-        }
-      }
-      for (;;) {
-        for (uint32_t u = ra; u < rb;) {
-          while ((uint32_t)cu[b + 1] <= u) ++b;
-          const uint32_t nb = (uint32_t)(cu[b + 1] - cu[b]) / (uint32_t)H;
-          const uint32_t rel = u - (uint32_t)cu[b];
-          const uint32_t hu = rel / nb;
-          const int h = (int)hu;
-          const uint32_t pair_hi = (uint32_t)cu[b] + (hu + 1) * nb;
-          const uint32_t pair_lo = pair_hi - nb + kPairCost;  // of its own units
-          const uint32_t e = rb < pair_hi ? rb : pair_hi;
-          if (e <= pair_lo) {  // nothing but the pair's cost is here
-            u = e;
-            continue;
-          }
-          const int t0 = u > pair_lo ? (int)(u - pair_lo) : 0, t1 = (int)(e - pair_lo);
-          const int n = t1 - t0;
-          const int32_t* btrow = p.block_table + (int64_t)b * p.bt_sb;
-          const uint8_t* kh = p.k + (int64_t)h * p.c_shead;
-          const uint8_t* vh = p.v + (int64_t)h * p.c_shead;
-          // the block of unit i0 + lane of the piece; -1: none, zeros are read in its place
-          auto block_of = [&](int i0) -> int {
-            const int i = i0 + lane, t = t0 + i;
-            if (lane >= C::kBatch || i >= n) return -1;
-            if (t >= p.max_blocks) {
-              atomicOr(p.err, HPC_DEVCHK_TABLE_TOO_SHORT);
-              return -1;
-            }
-            const int v = __ldg(btrow + t);
-            if (v >= 0 && v < p.num_blocks) return v;
-            atomicOr(p.err, HPC_DEVCHK_BAD_BLOCK);
+      Pair at = pair_at(lo), second = at;
+      uint32_t end = hi;  // of the whole pairs between
+      for (int round = 0;; ++round) {
+        // ---- the piece [from, to) of pair `at`
+        const uint32_t own = at.base + kPairCost, pair_hi = at.base + at.nb;  // of its own units
+        const uint32_t from = lo > own ? lo : own, to = hi < pair_hi ? hi : pair_hi;
+        const int n = to > from ? (int)(to - from) : 0;  // (0: nothing but the pair's cost is here)
+        const int t0 = (int)(from - own), b = at.b, h = (int)at.h;
+        const int32_t* btrow = p.block_table + (int64_t)b * p.bt_sb;
+        const uint8_t* tiles = (lane & 1 ? p.v : p.k) + (int64_t)h * p.c_shead;
+        // the block of unit i0 + lane / 2 of the piece, of which even lanes copy K and odd
+        // ones V; -1: none, zeros are read in its place
+        auto block_of = [&](int i0) -> int {
+          const int i = i0 + (lane >> 1), t = t0 + i;
+          if (lane >= 2 * C::kBatch || i >= n) return -1;
+          if (t >= p.max_blocks) {
+            atomicOr(p.err, HPC_DEVCHK_TABLE_TOO_SHORT);
             return -1;
-          };
-          int blk = block_of(0);
-          {
-            const bool whole = t0 == 0 && e == pair_hi;
-            const int slot = whole ? -1 : 2 * owner + (pair_lo <= lo ? 0 : 1);
-            const int k = whole ? 1 : (int)(M.owner_of(pair_hi - 1) - M.owner_of(pair_lo) + 1);
-            if (!whole && t0 == 0) begun = make_int4(b, h, k, slot);
-            publish(b, h, t0, t1, (whole ? kFlagWhole : 0) | (k << 8), slot);
           }
-          // the next units of the piece, one to a lane: no more than the ring has slots, so
-          // that each lane's slot was last used by a unit that has been issued already
-          for (int i0 = 0; i0 < n; i0 += C::kBatch) {
-            const int cnt = n - i0 < C::kBatch ? n - i0 : C::kBatch;
-            const int next = i0 + C::kBatch < n ? block_of(i0 + C::kBatch) : -1;
-            const uint32_t gu = g + (uint32_t)lane, slot_r = gu % STAGES;
-            const uint32_t be = bar_empty + 8 * slot_r, par = ((gu / STAGES) & 1u) ^ 1u;
-            const uint32_t fb = bar_full + 8 * slot_r, dk = smem_base + slot_r * kStage;
-            const int64_t off = (int64_t)blk * p.c_sblk;
-            const void* ks = blk < 0 ? (const void*)kKv4NoTile : kh + off;
-            const void* vs = blk < 0 ? (const void*)kKv4NoTile : vh + off;
-            blk = next;
-            g += (uint32_t)cnt;
-            if (stop) continue;
-            bool todo = lane < cnt;
-            if (todo) {  // every lane issues as soon as its slot is free
-              unsigned long long since = 0;
-              for (uint32_t it = 1; todo; ++it) {
-                if (mbar_try_wait(be, par)) {
-                  mbar_arrive_expect_tx(fb, kStage);
-                  kv4_copy_tile(dk, ks, fb, policy);
-                  kv4_copy_tile(dk + kKv4Tile, vs, fb, policy);
-                  todo = false;
-                } else if ((it & 63u) == 0) {
-                  if (*abort_flag) break;
-                  if (since == 0) since = globaltimer();
-                  if (globaltimer() - since > p.timeout_ns) {
-                    atomicOr(p.err, HPC_DEVCHK_TIMEOUT);
-                    *abort_flag = 1;
-                    break;
-                  }
+          const int v = __ldg(btrow + t);
+          if (v >= 0 && v < p.num_blocks) return v;
+          atomicOr(p.err, HPC_DEVCHK_BAD_BLOCK);
+          return -1;
+        };
+        int blk = block_of(0);
+        if (n > 0) {
+          const bool whole = from == own && to == pair_hi;
+          int slot = -1, k = 1;
+          if (!whole) {
+            slot = 2 * owner + (own <= lo ? 0 : 1);
+            k = (int)(M.owner_of(pair_hi - 1) - M.owner_of(own) + 1);
+            if (from == own) begun = make_int4(b, h, k, slot);
+          }
+          publish(b, h, t0, t0 + n, (whole ? kFlagWhole : 0) | (k << 8), slot);
+        }
+        // the next units of the piece: no more than the ring has slots, so that a unit's slot
+        // was last used by one that has been issued already
+        for (int i0 = 0; i0 < n; i0 += C::kBatch) {
+          const int cnt = n - i0 < C::kBatch ? n - i0 : C::kBatch;
+          const int later = i0 + C::kBatch < n ? block_of(i0 + C::kBatch) : -1;
+          const uint32_t gu = g + (uint32_t)(lane >> 1), slot_r = gu % STAGES;
+          const uint32_t be = bar_empty + 8 * slot_r, par = ((gu / STAGES) & 1u) ^ 1u;
+          const uint32_t fb = bar_full + 8 * slot_r;
+          const uint32_t dst = smem_base + slot_r * kStage + (lane & 1) * kKv4Tile;
+          const void* src = blk < 0 ? (const void*)kKv4NoTile : tiles + (int64_t)blk * p.c_sblk;
+          blk = later;
+          g += (uint32_t)cnt;
+          if (stop) continue;
+          bool todo = lane < 2 * cnt;
+          if (todo) {  // every lane issues as soon as its slot is free
+            unsigned long long since = 0;
+            for (uint32_t it = 1; todo; ++it) {
+              if (mbar_try_wait(be, par)) {
+                mbar_arrive_expect_tx(fb, kKv4Tile);
+                kv4_copy_tile(dst, src, fb, policy);
+                todo = false;
+              } else if ((it & 63u) == 0) {
+                if (*abort_flag) break;
+                if (since == 0) since = globaltimer();
+                if (globaltimer() - since > p.timeout_ns) {
+                  atomicOr(p.err, HPC_DEVCHK_TIMEOUT);
+                  *abort_flag = 1;
+                  break;
                 }
               }
             }
-            __syncwarp();
-            last_mask = __ballot_sync(0xffffffffu, lane < cnt && !todo);
-            stop = __any_sync(0xffffffffu, todo);
-            issued = stop ? g - (uint32_t)cnt : g;
           }
-          u = e;
+          __syncwarp();
+          last_mask = __ballot_sync(0xffffffffu, lane < 2 * cnt && !todo);
+          stop = __any_sync(0xffffffffu, todo);
+          issued = stop ? g - (uint32_t)cnt : g;
         }
-        if (first) {  // then the last piece, if split, ahead of the whole pairs
-          first = false;
-          const uint32_t e0 = rb;
-          const int b1 = seq_at(hi - 1);
-          const uint32_t nb1 = (uint32_t)(cu[b1 + 1] - cu[b1]) / (uint32_t)H;
-          const uint32_t s1 = (uint32_t)cu[b1] + ((hi - 1 - (uint32_t)cu[b1]) / nb1) * nb1;
-          if (s1 + nb1 > hi && s1 > e0) {
-            rest_a = e0;
-            rest_b = s1;
-            ra = s1;
-            b = b1;
-          } else {
-            ra = e0;
+        // ---- the next piece
+        if (round == 0) {
+          if (pair_hi >= hi) break;
+          next(at);
+          const Pair tail = pair_at(hi - 1);
+          if (tail.base + tail.nb > hi) {  // it goes on: now, and the pairs before it afterwards
+            end = tail.base;
+            second = at;
+            at = tail;
+            continue;
           }
-          rb = hi;
-          continue;
+        } else if (round == 1 && end < hi) {
+          at = second;
+        } else {
+          next(at);
         }
-        if (rest_a < rest_b) {
-          ra = rest_a;
-          rb = rest_b;
-          rest_a = rest_b;
-          b = seq_at(ra);
-          continue;
-        }
-        break;
+        if (at.base >= end) break;
       }
       if (!kOneToken && lane == 0) *reinterpret_cast<int4*>(p.owners + 4 + 4 * owner) = begun;
     }
-    // one end marker per epilogue warp (they take alternate pieces; the consumer warps
-    // stop at the first)
-    for (int e = 0; e < kEpilogueWarps; ++e) publish(0, 0, 0, 0, kFlagEnd, -1);
+    publish(0, 0, 0, 0, kFlagEnd, -1);
     named_bar_sync(3, kThreads);
-    if (lane == 0 && *abort_flag) {  // copies may still be landing: wait for the last ones
-      for (int i = j > kPieceQ ? j - kPieceQ : 0; !lost && i < j; ++i)
+    if (*abort_flag) {  // copies may still be landing: wait for the last ones
+      for (int i = j > kPieceQ ? j - kPieceQ : 0; lane == 0 && !lost && i < j; ++i)
         wait_phase(bar_pfull + 8 * (i % kPieceQ), (i / kPieceQ) & 1u, abort_flag, p.err, 1000000000ull,
                    false);
-      for (uint32_t u = issued > (uint32_t)STAGES ? issued - STAGES : 0; u < issued + 32; ++u)
-        // (of a slot that was issued again, the later unit is waited for)
-        if (u < issued ? !(stop && u + STAGES < issued + 32 && (last_mask >> (u + STAGES - issued)) & 1u)
-                       : stop && (last_mask >> (u - issued)) & 1u)
-          wait_phase(bar_full + 8 * (u % STAGES), (u / STAGES) & 1u, abort_flag, p.err,
-                     1000000000ull, false);
+      // (a lane of a batch that was cut short: its own copy's barrier may lack the other
+      // tile's arrival, so the wait can run out)
+      for (uint32_t u = issued > (uint32_t)STAGES ? issued - STAGES : 0; lane == 0 && u < issued; ++u)
+        wait_phase(bar_full + 8 * (u % STAGES), (u / STAGES) & 1u, abort_flag, p.err, 1000000000ull,
+                   false);
+      if ((last_mask >> lane) & stop) {
+        const uint32_t u = issued + (uint32_t)(lane >> 1);
+        wait_phase(bar_full + 8 * (u % STAGES), (u / STAGES) & 1u, abort_flag, p.err, 1000000000ull,
+                   false);
+      }
     }
     return;
   }
 
   uint4* dep0 = reinterpret_cast<uint4*>(smem + C::kDepOff);  // [warp][token][vector][lane]
   if (warp >= kEpilogueWarp0) {
+    regs_dec<C::kRegsEpilogue>();
     // ------------------------------------------------------------ epilogue
-    // For every piece and token: join the states of the warps that shared its units,
-    // then write the result, or a partial state of a split pair; with one token a step
-    // the piece is counted and the last of a pair's merges them.
-    for (int j = warp - kEpilogueWarp0;; j += kEpilogueWarps) {
-      const int qs = j % kPieceQ;
+    // For every piece and token: join the states of the warps that shared its units, then
+    // write the result, or a partial state of a split pair; with one token a step the piece
+    // is counted and the last of a pair's merges them. Each warp does two of the states'
+    // eight slices.
+    const int e = warp - kEpilogueWarp0;
+    for (int j = 0;; ++j) {
+      const int qs = j % kPieceQ, buf = j % C::kBufs;
       if (!wait_phase(bar_pfull + 8 * qs, (j / kPieceQ) & 1u, abort_flag, p.err, book_ns, false))
         break;
       const int* d = desc + qs * kDescInts;
@@ -653,14 +680,11 @@ __global__ void __launch_bounds__(Cfg<TW, NP, NC>::kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_pfree + 8 * qs);
       if (fl & kFlagEnd) break;
-      // the deposits of piece j complete phase j / kEpilogueWarps of this warp's barrier;
-      // its next phase needs this warp's read first, so the parity is exact
-      if (!wait_phase(bar_dfull + 8 * (j % kEpilogueWarps), (j / kEpilogueWarps) & 1u, abort_flag,
-                      p.err, book_ns, false))
+      if (!wait_phase(bar_dfull + 8 * buf, (j / C::kBufs) & 1u, abort_flag, p.err, book_ns, false))
         break;
-      const uint4* dep = dep0 + (j % C::kBufs) * (C::kDepBytes / 16);
+      const uint4* dep = dep0 + buf * (C::kDepBytes / 16);
       for (int t = 0; t < T; ++t) {
-        Kv4State st;
+        Kv4Slices st;
         st.clear();
         // the states of token t, from the group that had the piece's first unit on: the
         // order, like each group's units, is a function of the piece alone
@@ -668,55 +692,50 @@ __global__ void __launch_bounds__(Cfg<TW, NP, NC>::kThreads, 1)
           const int grp = rot + v < kGroups ? rot + v : rot + v - kGroups;
           return dep + ((grp * NP + t / TW) * TW + t % TW) * (kDepVec * 32) + lane;
         };
+        float4 ml[kGroups];
 #pragma unroll
         for (int v = 0; v < kGroups; ++v) {
-          const float2 mv = *reinterpret_cast<const float2*>(state(v) + 4 * 32);
-          st.m[0] = fmaxf(st.m[0], mv.x);
-          st.m[1] = fmaxf(st.m[1], mv.y);
+          ml[v] = *reinterpret_cast<const float4*>(state(v) + 4 * 32);
+          st.m[0] = fmaxf(st.m[0], ml[v].x);
+          st.m[1] = fmaxf(st.m[1], ml[v].y);
         }
-#pragma unroll 1
+#pragma unroll
         for (int v = 0; v < kGroups; ++v) {
-          const uint4* x = state(v);
-          const float4 ml = *reinterpret_cast<const float4*>(x + 4 * 32);
-          const float w0 = ml.x == -INFINITY ? ml.z : ml.z * ex2(ml.x - st.m[0]);
-          const float w1 = ml.y == -INFINITY ? ml.w : ml.w * ex2(ml.y - st.m[1]);
+          const float w0 = ml[v].z * Kv4Slices::factor(ml[v].x, st.m[0]);
+          const float w1 = ml[v].w * Kv4Slices::factor(ml[v].y, st.m[1]);
           st.l[0] += w0;
           st.l[1] += w1;
+          const uint4 h4 = state(v)[e * 32];
+          const uint32_t hw[4] = {h4.x, h4.y, h4.z, h4.w};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint4 h4 = x[k * 32];
-            const uint32_t hw[4] = {h4.x, h4.y, h4.z, h4.w};
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const float2 o = __half22float2(*reinterpret_cast<const __half2*>(&hw[y]));
-              st.acc[2 * k + (y >> 1)][2 * (y & 1)] += o.x * w0;
-              st.acc[2 * k + (y >> 1)][2 * (y & 1) + 1] += o.y * w1;
-            }
+          for (int y = 0; y < 4; ++y) {
+            const float2 o = __half22float2(*reinterpret_cast<const __half2*>(&hw[y]));
+            st.acc[y >> 1][2 * (y & 1)] += o.x * w0;
+            st.acc[y >> 1][2 * (y & 1) + 1] += o.y * w1;
           }
         }
         if (t == T - 1) {
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar_dfree + 8 * (j % C::kBufs));  // the buffer is free
+          if (lane == 0) mbar_arrive(bar_dfree + 8 * buf);  // the buffer is free
         }
         if (fl & kFlagWhole) {
-          st.write(p, b, t, h, lane);
+          st.write(p, b, t, h, e, lane);
         } else {
-          st.store(p.ws + ((int64_t)slot * T + t) * kKv4PartFloat4 + lane);
+          st.store(p.ws + ((int64_t)slot * T + t) * kKv4PartFloat4 + lane, e);
         }
       }
       if (!kOneToken || (fl & kFlagWhole)) continue;
       // The piece of a split pair counts itself; the last one of a pair joins the states
       // in the owners' order. More than kFan pieces are joined in groups of kFan first,
-      // each by its last piece, so that no warp reads more than a few dozen states. One
-      // acquire-release atomic by lane 0 covers the warp's writes (ordered before it by the
-      // warp barrier) and the other pieces', which the warp reads after the second one.
+      // each by its last piece, so that no one reads more than a few dozen states. One
+      // acquire-release atomic covers the warps' writes (ordered before it by the barrier)
+      // and the other pieces', which the warps read after the second barrier.
       const PartPlan M = plan();
       const int k = fl >> 8, owner = slot >> 1;
-      const uint32_t nb = (uint32_t)(cu[b + 1] - cu[b]) / (uint32_t)H;
-      const uint32_t A = (uint32_t)cu[b] + (uint32_t)h * nb + kPairCost;
-      const int first = (int)M.owner_of(A);
+      const uint32_t own = (uint32_t)cu[b] * H + (uint32_t)h * (uint32_t)(cu[b + 1] - cu[b]) + kPairCost;
+      const int first = (int)M.owner_of(own);
       // piece i of the pair: the first one can be its part's last, the others are their parts' first
-      const int64_t slot0 = 2 * (int64_t)first + (A <= M.start(first) ? 0 : 1);
+      const int64_t slot0 = 2 * (int64_t)first + (own <= M.start(first) ? 0 : 1);
       auto place = [&](int i) -> float4* {
         return p.ws + (i == 0 ? slot0 : 2 * (int64_t)(first + i)) * kKv4PartFloat4 + lane;
       };
@@ -726,25 +745,25 @@ __global__ void __launch_bounds__(Cfg<TW, NP, NC>::kThreads, 1)
       for (;;) {  // (one piece of code for both levels: it runs cold)
         int32_t* cnt = last_level ? p.pair_cnt + (int64_t)b * H + h
                                   : p.slot_cnt + (at == 0 ? slot0 : 2 * (int64_t)(first + at));
-        __syncwarp();
-        int arrived = 0;
-        if (lane == 0) {
-          arrived = atom_add_acq_rel_gpu(cnt, 1) == count - 1;
+        named_bar_sync(2, kEpilogueWarps * 32);
+        if (e == 0 && lane == 0) {
+          const int arrived = atom_add_acq_rel_gpu(cnt, 1) == count - 1;
           if (arrived) *cnt = 0;  // ready for the next step
+          *s_last = arrived;
         }
-        arrived = __shfl_sync(0xffffffffu, arrived, 0);
-        __syncwarp();
-        if (!arrived) break;
-        Kv4State st;
+        named_bar_sync(2, kEpilogueWarps * 32);
+        if (!*s_last) break;
+        Kv4Slices st;
         st.clear();
-#pragma unroll 1
-        for (int i = 0; i < count; i += 2)
-          st.add2(place(at + i * step), i + 1 < count ? place(at + (i + 1) * step) : nullptr);
+        st.join(count, e, [&](int i) { return place(at + i * step); });
         if (last_level) {
-          st.write(p, b, 0, h, lane);
+          st.write(p, b, 0, h, e, lane);
           break;
         }
-        st.store(place(at));
+        // (every warp has read the leader's state where it overwrites it: its own slices and,
+        // the first warp, all warps' maxima and sums)
+        named_bar_sync(2, kEpilogueWarps * 32);
+        st.store(place(at), e);
         last_level = true;
         at = 0;
         step = kFan;
@@ -752,23 +771,23 @@ __global__ void __launch_bounds__(Cfg<TW, NP, NC>::kThreads, 1)
       }
     }
     // sequences without tiles (or a step that cannot be): out = 0, lse = -inf
-    for (int b = (int)blockIdx.x * kEpilogueWarps + warp - kEpilogueWarp0; b < B;
-         b += G * kEpilogueWarps) {
+    for (int b = (int)blockIdx.x * kEpilogueWarps + e; b < B; b += G * kEpilogueWarps) {
       if (!*s_bad && cu[b + 1] != cu[b]) continue;
       for (int t = 0; t < T; ++t)
-        for (int j = lane; j < H * kGroup; j += 32) {
+        for (int x = lane; x < (int)H * kGroup; x += 32) {
           uint4* o = reinterpret_cast<uint4*>(p.out + (int64_t)b * p.o_sb + (int64_t)t * p.o_st +
-                                              (int64_t)j * p.o_sh);
+                                              (int64_t)x * p.o_sh);
 #pragma unroll
           for (int i = 0; i < kHeadDim / 8; ++i) o[i] = make_uint4(0u, 0u, 0u, 0u);
           if (p.lse)
-            p.lse[(int64_t)b * p.l_sb + (int64_t)t * p.l_st + (int64_t)j * p.l_sh] = -INFINITY;
+            p.lse[(int64_t)b * p.l_sb + (int64_t)t * p.l_st + (int64_t)x * p.l_sh] = -INFINITY;
         }
     }
     named_bar_sync(3, kThreads);
     return;
   }
 
+  regs_inc<C::kRegsConsumer>();
   // -------------------------------------------------------------- consumers
   // Groups of NP warps take the CTA's units in turn, each warp for its own tokens, whatever
   // pieces they belong to: a group's units come to its own slots in its own order, so the
@@ -777,8 +796,8 @@ __global__ void __launch_bounds__(Cfg<TW, NP, NC>::kThreads, 1)
   const int slice = warp % NP, grp = warp / NP;
   uint32_t slot = (uint32_t)grp, phase = 0;  // of the group's next unit
   bool dead = false;
-  for (int j = 0;; ++j) {
-    const int qs = j % kPieceQ;
+  for (int j = 0; warp < C::kActive; ++j) {
+    const int qs = j % kPieceQ, buf = j % C::kBufs;
     if (!wait_phase(bar_pfull + 8 * qs, (j / kPieceQ) & 1u, abort_flag, p.err, book_ns, false))
       break;  // no descriptor arrived: the producer is gone
     const int* d = desc + qs * kDescInts;
@@ -805,7 +824,7 @@ __global__ void __launch_bounds__(Cfg<TW, NP, NC>::kThreads, 1)
         // (a warp's second token past the last one repeats it, and is not written)
         const int tok = TW * slice + t < T ? TW * slice + t : T - 1;
         const float qinv = load_q4(
-            smem_base + C::kQOff + qs * C::kQBytes + tok * (kGroup * kQPitch), lane, qf[t]);
+            smem_base + C::kQOff + qs * C::kQBytes + tok * (kGroup * kQRow), lane, qf[t]);
         // (a factor of 0 would make NaN of masked scores, an infinite one of scores of 0)
         sl2[t] = fminf(fmaxf(p.score_scale_log2 * qinv, FLT_MIN), FLT_MAX);
       }
@@ -844,11 +863,10 @@ __global__ void __launch_bounds__(Cfg<TW, NP, NC>::kThreads, 1)
         l[t][0] += __shfl_xor_sync(0xffffffffu, l[t][0], o);
         l[t][1] += __shfl_xor_sync(0xffffffffu, l[t][1], o);
       }
-    // deposit once the epilogue warp has read its previous piece's states: o = acc / l in
-    // f16 (2^-11; |o| is at most the largest |code * scale|, 2688), m and l in fp32
-    wait_phase(bar_dfree + 8 * (j % C::kBufs), ((j / C::kBufs) & 1u) ^ 1u, abort_flag, p.err,
-               book_ns, false);
-    uint4* dep = dep0 + (j % C::kBufs) * (C::kDepBytes / 16);
+    // deposit once the epilogue has read the buffer's previous states: o = acc / l in f16
+    // (2^-11; |o| is at most the largest |code * scale|, 2688), m and l in fp32
+    wait_phase(bar_dfree + 8 * buf, ((j / C::kBufs) & 1u) ^ 1u, abort_flag, p.err, book_ns, false);
+    uint4* dep = dep0 + buf * (C::kDepBytes / 16);
 #pragma unroll
     for (int t = 0; t < TW; ++t) {
       const float v0 = l[t][0] == 0.f ? 0.f : __fdividef(1.f, l[t][0]);
@@ -863,15 +881,15 @@ __global__ void __launch_bounds__(Cfg<TW, NP, NC>::kThreads, 1)
       reinterpret_cast<float4*>(dw)[4 * 32] = make_float4(m[t][0], m[t][1], l[t][0], l[t][1]);
     }
     __syncwarp();
-    if (lane == 0) mbar_arrive(bar_dfull + 8 * (j % kEpilogueWarps));  // release to the epilogue
+    if (lane == 0) mbar_arrive(bar_dfull + 8 * buf);  // release to the epilogue
   }
   named_bar_sync(3, kThreads);  // see the producer's exit
 }
 
-template <int TW, int NP, int NC>
+template <int TW, int NP>
 cudaError_t launch_cfg(const Kv4DecodeParams& p, int grid, cudaStream_t stream) {
-  using C = Cfg<TW, NP, NC>;
-  auto kern = kv4_decode_kernel<TW, NP, NC>;
+  using C = Cfg<TW, NP>;
+  auto kern = kv4_decode_kernel<TW, NP>;
   static std::atomic<uint64_t> configured{0};
   cudaError_t e = once_per_device(configured, [&] {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -880,7 +898,7 @@ cudaError_t launch_cfg(const Kv4DecodeParams& p, int grid, cudaStream_t stream) 
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(C::kThreads);
+  cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kSmemBytes + 4 * ((size_t)p.num_seqs + 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -896,12 +914,10 @@ cudaError_t launch_cfg(const Kv4DecodeParams& p, int grid, cudaStream_t stream) 
 cudaError_t launch_kv4_decode(const Kv4DecodeParams& p, int grid, cudaStream_t stream) {
   if (p.num_seqs > kKv4MaxSeqs) return cudaErrorInvalidValue;
   switch ((p.q_len + 1) / 2) {
-    case 1:
-      return p.q_len == 1 ? launch_cfg<1, 1, 8>(p, grid, stream)
-                          : launch_cfg<2, 1, 8>(p, grid, stream);
-    case 2: return launch_cfg<2, 2, 8>(p, grid, stream);
-    case 3: return launch_cfg<2, 3, 6>(p, grid, stream);
-    default: return launch_cfg<2, 4, 8>(p, grid, stream);
+    case 1: return p.q_len == 1 ? launch_cfg<1, 1>(p, grid, stream) : launch_cfg<2, 1>(p, grid, stream);
+    case 2: return launch_cfg<2, 2>(p, grid, stream);
+    case 3: return launch_cfg<2, 3>(p, grid, stream);
+    default: return launch_cfg<2, 4>(p, grid, stream);
   }
 }
 

@@ -404,8 +404,8 @@ __global__ void __launch_bounds__(Layout<QT, FP8, KV4>::kThreads, 1)
                 if constexpr (KV4) {
                   const bool none = bk < 0 || bk >= p.num_blocks;
                   const int64_t off = (int64_t)bk * p.c_sblk + (int64_t)h * p.c_shead;
-                  kv4_copy_tile(dk, none ? (const void*)kKv4NoTile : p.k4 + off, fb);
-                  kv4_copy_tile(dv, none ? (const void*)kKv4NoTile : p.v4 + off, fb);
+                  kv4_copy(dk, none ? (const void*)kKv4NoTile : p.k4 + off, kKv4Tile, fb);
+                  kv4_copy(dv, none ? (const void*)kKv4NoTile : p.v4 + off, kKv4Tile, fb);
                 } else {
                   tma_load_4d(dk, &tmk, fb, 0, c1, c2, bk);
                   tma_load_4d(dv, &tmv, fb, 0, c1, c2, bk);
