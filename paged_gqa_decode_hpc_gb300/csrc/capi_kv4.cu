@@ -2,6 +2,7 @@
 // See include/hpc_decode.h for the contract of every call.
 #include <climits>
 #include <cmath>
+#include <cstdlib>
 #include <cstring>
 #include <new>
 #include <string>
@@ -107,6 +108,33 @@ hpc_status score_factor(float softmax_scale, float k_scale, float* out) {
   *out = scale * 1.4426950408889634f * k_scale;
   if (!std::isfinite(*out))
     return fail(HPC_ERR_INVALID_ARG, "softmax_scale times K's scale exceeds fp32");
+  return HPC_OK;
+}
+
+int kv4_tc_min_q_len() {  // (for measurements)
+  const char* s = getenv("KV4_TC");
+  return s ? atoi(s) : 2;
+}
+
+// q [B][q_len][H_q][128]: a box is 64 columns of the query rows of a KV head.
+hpc_status make_kv4_q_map(const hpc_tensor* q, CUtensorMap* map) {
+  auto enc = encode_fn();
+  if (!enc) return fail(HPC_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  const bool multi = q->ndim == 4;
+  const int64_t B = q->shape[0], T = multi ? q->shape[1] : 1, Hq = q->shape[q->ndim - 2];
+  // (strides of dimensions of one element mean nothing, but have to be multiples of 16 bytes)
+  const int64_t sh = q->stride[q->ndim - 2];
+  const int64_t st = T > 1 ? q->stride[1] : Hq * kHeadDim, sb = B > 1 ? q->stride[0] : T * Hq * kHeadDim;
+  cuuint64_t dims[4] = {(cuuint64_t)kHeadDim, (cuuint64_t)Hq, (cuuint64_t)T, (cuuint64_t)B};
+  cuuint64_t strides[3] = {(cuuint64_t)sh * 2, (cuuint64_t)st * 2, (cuuint64_t)sb * 2};
+  cuuint32_t box[4] = {64, (cuuint32_t)kGroup, (cuuint32_t)T, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, q->data, dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(HPC_ERR_INVALID_ARG,
+                "cuTensorMapEncodeTiled rejected q (error " + std::to_string((int)r) + ")");
   return HPC_OK;
 }
 
@@ -286,8 +314,16 @@ hpc_status hpc_decode_kv4_attn(const hpc_tensor* q, const hpc_tensor* k_cache,
     p.err = plan->d_err;
     p.timeout_ns = wait_limit_ns();
     p.withhold_copies = withhold_copies();
-    e = launch_kv4_decode(p, plan->num_sms, (cudaStream_t)stream);
-    if (e == cudaSuccess && T > 1) e = launch_kv4_merge(p, plan->num_sms, (cudaStream_t)stream);
+    p.ws_ml = (float2*)(p.ws + kv4_slots(plan->num_sms) * T * (kGroup * kHeadDim / 4));
+    if (T >= kv4_tc_min_q_len()) {
+      CUtensorMap tq;
+      if ((st = make_kv4_q_map(q, &tq)) != HPC_OK) return st;
+      e = launch_kv4_tc(p, tq, plan->num_sms, (cudaStream_t)stream);
+      if (e == cudaSuccess) e = launch_kv4_tc_merge(p, plan->num_sms, (cudaStream_t)stream);
+    } else {
+      e = launch_kv4_decode(p, plan->num_sms, (cudaStream_t)stream);
+      if (e == cudaSuccess && T > 1) e = launch_kv4_merge(p, plan->num_sms, (cudaStream_t)stream);
+    }
     if (e != cudaSuccess)
       return fail(HPC_ERR_CUDA, std::string("4-bit decode launch: ") + cudaGetErrorString(e));
     return HPC_OK;

@@ -42,6 +42,7 @@
 #include "hpc_internal.h"
 #include "kv4.cuh"
 #include "kv4.h"
+#include "kv4_plan.cuh"
 #include "kv4_state.cuh"
 #include "ptx.cuh"
 #include "step_plan.cuh"
@@ -58,30 +59,7 @@ constexpr int kDescInts = 8;
 constexpr int kDepVec = 5;                        // 16-byte words per lane of a deposited state
 constexpr int kStage = 2 * kKv4Tile;
 constexpr int kQRow = kHeadDim * 2;               // bytes of a row of q in shared memory
-// Bookkeeping waits give up this many data waits later: once a data wait has timed out
-// every role runs on without copies, and this bookkeeping must then still finish, so that
-// the arrival counters return to zero.
-constexpr unsigned long long kBookkeepingWaits = 8;
-constexpr int kFlagEnd = 1, kFlagWhole = 2;
-// What a (sequence, KV head) pair costs beside its units, in units: its q, its states' way
-// through the epilogue. The plan gives every pair so many units more, ahead of its own.
-constexpr int kPairCost = 4;
 constexpr int kFan = 16;                          // pieces of a pair that are joined at once
-constexpr int kMinPart = 8;                       // units that a CTA is worth starting for
-constexpr int kWarpPlan = 256;                    // sequences that one warp plans by itself
-
-// Equal parts [start(o), start(o + 1)) of T units, and the part of a unit. Every unit index
-// is below T <= INT32_MAX, so the arithmetic is 32-bit where products fit.
-struct PartPlan {
-  uint32_t T, P;
-  bool small;  // (T + 1) * (P + 1) < 2^32
-  __device__ __forceinline__ uint32_t start(uint32_t o) const {
-    return small ? o * T / P : (uint32_t)((uint64_t)o * T / P);
-  }
-  __device__ __forceinline__ uint32_t owner_of(uint32_t x) const {
-    return small ? ((x + 1) * P - 1) / T : (uint32_t)(((uint64_t)(x + 1) * P - 1) / T);
-  }
-};
 
 // TW tokens to a warp, NP warps to a unit.
 template <int TW, int NP>
@@ -398,65 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_launch_dependents();
   __syncthreads();
 
-  // ---- plan: units of a KV head per sequence (the pair's cost among them), prefix in shared
-  // memory. The producer plans small batches by itself; whoever else looks at the plan has
-  // waited for a piece of it by then.
-  auto units_of = [&](int32_t len) -> int32_t {  // -1: cannot be
-    // more units than INT32_MAX / 512 are refused, so that no partial sum of a scan pass, of
-    // 512 sequences, wraps
-    const int64_t n = len > 0 ? ((int64_t)len + kBlockTokens - 1) / kBlockTokens + kPairCost : 0;
-    return len < 0 || n * H > (int64_t)(INT32_MAX / 512) ? -1 : (int32_t)n;
-  };
-  if (B > kWarpPlan) {
-    int64_t carry = 0;
-    for (int base = 0; base < B; base += kThreads) {
-      const int b = base + tid;
-      int32_t n = b < B ? units_of(p.seq_lens[b]) : 0;
-      if (n < 0) {
-        *s_bad = 1;
-        n = 0;
-      }
-      int32_t tot;
-      const int32_t incl = cta_inclusive_scan(n, warp_tot, &tot);
-      if (b < B) cu[b + 1] = (int32_t)(carry + incl);
-      carry += tot;
-    }
-    if (tid == 0 && carry * H > INT32_MAX) *s_bad = 1;
-    __syncthreads();
-  } else if (warp == kProducerWarp) {
-    int32_t n[kWarpPlan / 32];
-#pragma unroll
-    for (int i = 0; i < kWarpPlan / 32; ++i)
-      n[i] = 32 * i + lane < B ? p.seq_lens[32 * i + lane] : 0;
-    bool cannot = false;
-    int64_t carry = 0;
-#pragma unroll
-    for (int i = 0; i < kWarpPlan / 32; ++i) {
-      if (32 * i >= B) break;
-      int32_t v = units_of(n[i]);
-      cannot |= v < 0;
-      v = v < 0 ? 0 : v;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int32_t x = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += x;
-      }
-      if (32 * i + lane < B) cu[32 * i + lane + 1] = (int32_t)(carry + v);
-      carry += __shfl_sync(0xffffffffu, v, 31);
-    }
-    cannot = __any_sync(0xffffffffu, cannot) || carry * H > INT32_MAX;
-    if (cannot && lane == 0) *s_bad = 1;
-    __syncwarp();
-  }
-  // equal parts of the units to the CTAs, each of at least kMinPart
-  auto plan = [&]() -> PartPlan {
-    PartPlan M;
-    M.T = *s_bad ? 0u : (uint32_t)cu[B] * H;
-    const uint32_t want = (M.T + kMinPart - 1) / kMinPart;
-    M.P = want < (uint32_t)G ? want : (uint32_t)G;
-    M.small = (uint64_t)(M.T + 1) * (M.P + 1) < (uint64_t)UINT32_MAX;
-    return M;
-  };
+  plan_step(p, cu, s_bad, warp_tot, kThreads, warp == kProducerWarp);
 
   if (warp >= kProducerWarp) {
     regs_dec<C::kRegsProducer>();
@@ -465,12 +385,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       return;
     }
     // ------------------------------------------------------------ producer
-    const PartPlan M = plan();
-    const uint64_t policy = evict_first_policy();
-    bool stop = p.withhold_copies != 0;  // failure-path test: no copy is issued
-    bool lost = false;                   // the consumers stopped taking pieces
-    uint32_t g = 0, issued = 0;          // units walked, units issued
-    uint32_t last_mask = 0;              // where a wait gave up, the lanes that issued behind them
+    const PartPlan M = part_plan(p, cu, s_bad);
+    UnitCopies<STAGES, C::kBatch> copies;
+    copies.ring = smem_base;
+    copies.full = bar_full;
+    copies.empty = bar_empty;
+    copies.policy = evict_first_policy();
+    copies.abort_flag = abort_flag;
+    copies.stop = p.withhold_copies != 0;  // failure-path test: no copy is issued
+    bool lost = false;                     // the consumers stopped taking pieces
     int j = 0;
     if (blockIdx.x == 0 && lane == 0) {
       if (*s_bad) atomicOr(p.err, HPC_DEVCHK_BAD_LENGTH);
@@ -478,18 +401,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // A piece's descriptor and, with it, its rows of q.
     const bool q_whole = p.q_sh == kHeadDim;  // 8 rows in one piece of memory
-    auto publish = [&](int b, int h, int t0, int t1, int flags, int slot) {
+    auto publish = [&](const Piece& x) {
       const int qs = j % kPieceQ;
       const uint32_t pf = bar_pfull + 8 * qs;
-      const bool rows = !(flags & kFlagEnd) && !stop;
+      const bool rows = !(x.flags & kFlagEnd) && !copies.stop;
       if (lane == 0 && !lost) {
         if (!wait_phase(bar_pfree + 8 * qs, ((j / kPieceQ) & 1u) ^ 1u, abort_flag, p.err,
                         book_ns, false)) {
           lost = true;
         } else {
           int4* d = reinterpret_cast<int4*>(desc + qs * kDescInts);
-          d[0] = make_int4(b, h, t0, t1);
-          d[1] = make_int4(flags, slot, (int)(g % kGroups), 0);
+          d[0] = make_int4(x.b, x.h, x.t0, x.t0 + x.n);
+          d[1] = make_int4(x.flags, x.slot, (int)(copies.g % kGroups), 0);
           // release: the descriptor is visible to its waiters
           if (rows) mbar_arrive_expect_tx(pf, (uint32_t)(T * kGroup * kQRow));
           else mbar_arrive(pf);
@@ -499,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (rows && !lost) {
         const uint32_t dq = smem_base + C::kQOff + qs * C::kQBytes;
         const __nv_bfloat16* q0 =
-            p.q + (int64_t)b * p.q_sb + (int64_t)(h * kGroup) * p.q_sh;
+            p.q + (int64_t)x.b * p.q_sb + (int64_t)(x.h * kGroup) * p.q_sh;
         if (q_whole) {
           if (lane < T)
             kv4_copy(dq + lane * (kGroup * kQRow), q0 + (int64_t)lane * p.q_st, kGroup * kQRow, pf);
@@ -511,153 +434,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++j;
     };
-    // The pair that holds unit x: sequence, KV head, the pair's first unit and their number
-    // (the cost among them).
-    struct Pair {
-      int b;
-      uint32_t h, base, nb;
-    };
-    auto pair_at = [&](uint32_t x) -> Pair {
-      int at = 0;  // the last b with cu[b] * H <= x: no empty sequence
-      for (int n = B; n > 1;) {
-        const int step = (n + 31) / 32, i = at + lane * step;
-        const uint32_t under =
-            __ballot_sync(0xffffffffu, lane * step < n && (uint32_t)cu[i] * H <= x);
-        const int k = 31 - __clz((int)under);  // (lane 0's is)
-        at += k * step;
-        n = n - k * step < step ? n - k * step : step;
-      }
-      Pair r;
-      r.b = at;
-      r.base = (uint32_t)cu[at] * H;
-      r.nb = (uint32_t)(cu[at + 1] - cu[at]);
-      r.h = (x - r.base) / r.nb;
-      r.base += r.h * r.nb;
-      return r;
-    };
-    auto next = [&](Pair& r) {
-      r.base += r.nb;
-      if (++r.h < H) return;
-      r.h = 0;
-      do ++r.b;
-      while (r.b < B && cu[r.b + 1] == cu[r.b]);
-      if (r.b < B) r.nb = (uint32_t)(cu[r.b + 1] - cu[r.b]);
-    };
     if (blockIdx.x < M.P) {
-      const int owner = (int)blockIdx.x;
-      const uint32_t lo = M.start(owner), hi = M.start(owner + 1);
-      // The part's first piece, then its last one where that is the head of a pair that goes
-      // on past hi, then the whole pairs between them: the pieces of split pairs are done
-      // early, and their merges overlap the rest.
-      int4 begun = make_int4(0, 0, 0, 0);  // the pair that begins here and goes on elsewhere
-      Pair at = pair_at(lo), second = at;
-      uint32_t end = hi;  // of the whole pairs between
-      for (int round = 0;; ++round) {
-        // ---- the piece [from, to) of pair `at`
-        const uint32_t own = at.base + kPairCost, pair_hi = at.base + at.nb;  // of its own units
-        const uint32_t from = lo > own ? lo : own, to = hi < pair_hi ? hi : pair_hi;
-        const int n = to > from ? (int)(to - from) : 0;  // (0: nothing but the pair's cost is here)
-        const int t0 = (int)(from - own), b = at.b, h = (int)at.h;
-        const int32_t* btrow = p.block_table + (int64_t)b * p.bt_sb;
-        const uint8_t* tiles = (lane & 1 ? p.v : p.k) + (int64_t)h * p.c_shead;
-        // the block of unit i0 + lane / 2 of the piece, of which even lanes copy K and odd
-        // ones V; -1: none, zeros are read in its place
-        auto block_of = [&](int i0) -> int {
-          const int i = i0 + (lane >> 1), t = t0 + i;
-          if (lane >= 2 * C::kBatch || i >= n) return -1;
-          if (t >= p.max_blocks) {
-            atomicOr(p.err, HPC_DEVCHK_TABLE_TOO_SHORT);
-            return -1;
-          }
-          const int v = __ldg(btrow + t);
-          if (v >= 0 && v < p.num_blocks) return v;
-          atomicOr(p.err, HPC_DEVCHK_BAD_BLOCK);
-          return -1;
-        };
-        int blk = block_of(0);
-        if (n > 0) {
-          const bool whole = from == own && to == pair_hi;
-          int slot = -1, k = 1;
-          if (!whole) {
-            slot = 2 * owner + (own <= lo ? 0 : 1);
-            k = (int)(M.owner_of(pair_hi - 1) - M.owner_of(own) + 1);
-            if (from == own) begun = make_int4(b, h, k, slot);
-          }
-          publish(b, h, t0, t0 + n, (whole ? kFlagWhole : 0) | (k << 8), slot);
-        }
-        // the next units of the piece: no more than the ring has slots, so that a unit's slot
-        // was last used by one that has been issued already
-        for (int i0 = 0; i0 < n; i0 += C::kBatch) {
-          const int cnt = n - i0 < C::kBatch ? n - i0 : C::kBatch;
-          const int later = i0 + C::kBatch < n ? block_of(i0 + C::kBatch) : -1;
-          const uint32_t gu = g + (uint32_t)(lane >> 1), slot_r = gu % STAGES;
-          const uint32_t be = bar_empty + 8 * slot_r, par = ((gu / STAGES) & 1u) ^ 1u;
-          const uint32_t fb = bar_full + 8 * slot_r;
-          const uint32_t dst = smem_base + slot_r * kStage + (lane & 1) * kKv4Tile;
-          const void* src = blk < 0 ? (const void*)kKv4NoTile : tiles + (int64_t)blk * p.c_sblk;
-          blk = later;
-          g += (uint32_t)cnt;
-          if (stop) continue;
-          bool todo = lane < 2 * cnt;
-          if (todo) {  // every lane issues as soon as its slot is free
-            unsigned long long since = 0;
-            for (uint32_t it = 1; todo; ++it) {
-              if (mbar_try_wait(be, par)) {
-                mbar_arrive_expect_tx(fb, kKv4Tile);
-                kv4_copy_tile(dst, src, fb, policy);
-                todo = false;
-              } else if ((it & 63u) == 0) {
-                if (*abort_flag) break;
-                if (since == 0) since = globaltimer();
-                if (globaltimer() - since > p.timeout_ns) {
-                  atomicOr(p.err, HPC_DEVCHK_TIMEOUT);
-                  *abort_flag = 1;
-                  break;
-                }
-              }
-            }
-          }
-          __syncwarp();
-          last_mask = __ballot_sync(0xffffffffu, lane < 2 * cnt && !todo);
-          stop = __any_sync(0xffffffffu, todo);
-          issued = stop ? g - (uint32_t)cnt : g;
-        }
-        // ---- the next piece
-        if (round == 0) {
-          if (pair_hi >= hi) break;
-          next(at);
-          const Pair tail = pair_at(hi - 1);
-          if (tail.base + tail.nb > hi) {  // it goes on: now, and the pairs before it afterwards
-            end = tail.base;
-            second = at;
-            at = tail;
-            continue;
-          }
-        } else if (round == 1 && end < hi) {
-          at = second;
-        } else {
-          next(at);
-        }
-        if (at.base >= end) break;
-      }
-      if (!kOneToken && lane == 0) *reinterpret_cast<int4*>(p.owners + 4 + 4 * owner) = begun;
+      const int4 begun = walk_part(
+          M, cu, B, H, (int)blockIdx.x, [&](const Piece& x) { copies.ahead(p, x); },
+          [&](const Piece& x) {
+            publish(x);
+            copies.copy(p, x);
+          });
+      if (!kOneToken && lane == 0)
+        *reinterpret_cast<int4*>(p.owners + 4 + 4 * blockIdx.x) = begun;
     }
-    publish(0, 0, 0, 0, kFlagEnd, -1);
+    publish(Piece{0, 0, 0, 0, kFlagEnd, -1});
     named_bar_sync(3, kThreads);
-    if (*abort_flag) {  // copies may still be landing: wait for the last ones
+    if (*abort_flag) {
       for (int i = j > kPieceQ ? j - kPieceQ : 0; lane == 0 && !lost && i < j; ++i)
         wait_phase(bar_pfull + 8 * (i % kPieceQ), (i / kPieceQ) & 1u, abort_flag, p.err, 1000000000ull,
                    false);
-      // (a lane of a batch that was cut short: its own copy's barrier may lack the other
-      // tile's arrival, so the wait can run out)
-      for (uint32_t u = issued > (uint32_t)STAGES ? issued - STAGES : 0; lane == 0 && u < issued; ++u)
-        wait_phase(bar_full + 8 * (u % STAGES), (u / STAGES) & 1u, abort_flag, p.err, 1000000000ull,
-                   false);
-      if ((last_mask >> lane) & stop) {
-        const uint32_t u = issued + (uint32_t)(lane >> 1);
-        wait_phase(bar_full + 8 * (u % STAGES), (u / STAGES) & 1u, abort_flag, p.err, 1000000000ull,
-                   false);
-      }
+      copies.drain(p);
     }
     return;
   }
@@ -673,15 +466,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int e = warp - kEpilogueWarp0;
     for (int j = 0;; ++j) {
       const int qs = j % kPieceQ, buf = j % C::kBufs;
-      if (!wait_phase(bar_pfull + 8 * qs, (j / kPieceQ) & 1u, abort_flag, p.err, book_ns, false))
-        break;
+      bool ok = wait_phase(bar_pfull + 8 * qs, (j / kPieceQ) & 1u, abort_flag, p.err, book_ns, false);
       const int* d = desc + qs * kDescInts;
       const int b = d[0], h = d[1], fl = d[4], slot = d[5], rot = d[6];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_pfree + 8 * qs);
-      if (fl & kFlagEnd) break;
-      if (!wait_phase(bar_dfull + 8 * buf, (j / C::kBufs) & 1u, abort_flag, p.err, book_ns, false))
-        break;
+      if (ok && !(fl & kFlagEnd))
+        ok = wait_phase(bar_dfull + 8 * buf, (j / C::kBufs) & 1u, abort_flag, p.err, book_ns, false);
+      // (the warps leave together: barriers lie between)
+      if (any_of<2, kEpilogueWarps * 32>(!ok || (fl & kFlagEnd))) break;
       const uint4* dep = dep0 + buf * (C::kDepBytes / 16);
       for (int t = 0; t < T; ++t) {
         Kv4Slices st;
@@ -730,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // each by its last piece, so that no one reads more than a few dozen states. One
       // acquire-release atomic covers the warps' writes (ordered before it by the barrier)
       // and the other pieces', which the warps read after the second barrier.
-      const PartPlan M = plan();
+      const PartPlan M = part_plan(p, cu, s_bad);
       const int k = fl >> 8, owner = slot >> 1;
       const uint32_t own = (uint32_t)cu[b] * H + (uint32_t)h * (uint32_t)(cu[b + 1] - cu[b]) + kPairCost;
       const int first = (int)M.owner_of(own);

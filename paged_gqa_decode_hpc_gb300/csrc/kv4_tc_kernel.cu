@@ -1,0 +1,774 @@
+// Decode attention of several new tokens per sequence over a 4-bit paged cache on the
+// 5th-generation tensor cores (tcgen05).
+//
+// The 8 q_len query rows of a KV head share every tile. With mma.sync the products alone
+// take 64 q_len MMAs of 8 issue cycles a unit (kv4_decode_kernel.cu), and every two tokens
+// their own conversion of the codes; here the codes of a unit are converted once and the
+// products cost no issue slots. What bounds it: HBM (9216 bytes a unit, 206 ns of an SM's
+// share of 6.8 TB/s) and next to it shared memory, which V's f16 operand passes twice.
+//
+// Both products run with the wide side in M, so that few query rows cost little:
+//  * S^T[token, row] = K Q^T: M = 128 tokens (two tiles, a step), N = the query rows, K =
+//    128. A = K in tensor memory: a converter thread is a token; it reads its 72-byte row,
+//    multiplies codes by scales (exact in f16) and stores 64 columns of pairs. 72 bytes are 18
+//    words, so the 8-byte reads of 16 rows cover all banks once.
+//  * The softmax threads are tokens too: a row's maximum is over threads. They keep a
+//    reference per query row in shared memory, which moves only when some score passes it by
+//    8 (log2 units; a vote of the four warps), so that as a rule a thread subtracts, takes
+//    exponentials, adds its own sums and writes its row of P^T (f16) to shared memory.
+//  * O^T[d, row] += V^T P^T: M = 128 elements, K = tokens. A = V as the MN-major operand of
+//    its converted tile, B = P^T, MN-major as written. O^T stays in tensor memory for a
+//    piece (a thread is an element d then) and is rescaled there when references move.
+// A piece's states go to memory as a whole (out, lse) or as partial states, which a second
+// kernel joins.
+//
+// Warps: 4 softmax (and the pieces' ends), 4 converters of K, 4 of V, the producer, the MMA
+// issuer and 2 that convert q to f16. Plan, ring and copies are kv4_plan.cuh's. Every wait is
+// bounded; after one has run out every role leaves, the MMAs are waited for and tensor memory
+// is freed.
+#include <cfloat>
+
+#include "kv4_plan.cuh"
+#include "tc05.cuh"
+
+namespace hpc {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kKWarp0 = 4, kVWarp0 = 8, kProducerWarp = 12, kMmaWarp = 13, kQWarp0 = 14;
+constexpr int kPieceQ = 4;                  // piece descriptors in flight
+constexpr int kPieceReaders = 4 + 4 + 4 + 1 + 2;
+constexpr int kVBufs = 3;                   // converted V tiles
+constexpr uint32_t kVTile = 64 * 128 * 2;   // two 64-element halves of 64 x 128 bytes
+constexpr uint32_t kPBuf = 128 * 128;       // P^T of a step: 128 rows (tokens) of 128 bytes
+// tensor memory: K (2 x 64 columns), S^T (2 x 64), O^T (2 x 64)
+constexpr uint32_t kColK = 0, kColS = 128, kColO = 256, kTmemCols = 512;
+constexpr float kPassed = 8.f;              // log2 units by which a score may pass its reference
+
+// COLS: query rows that are computed (8, 16, 32, 48 or 64), of the MMAs' N.
+template <int COLS>
+struct Cfg {
+  static constexpr int kN = COLS < 16 ? 16 : COLS;
+  static constexpr uint32_t kQHalf = kN * 128, kQBuf = 2 * kQHalf;  // rows of 64 elements each
+  static constexpr uint32_t kOffV = 0;
+  static constexpr uint32_t kOffP = kOffV + kVBufs * kVTile;
+  static constexpr uint32_t kOffQ = kOffP + 2 * kPBuf;
+  static constexpr uint32_t kOffRing = kOffQ + 2 * kQBuf;
+  static constexpr int kFixed = kOffRing + 5120 /* barriers, descriptors, references */ + 1024 + 4 * (kKv4MaxSeqs + 1);
+  static constexpr int kStages = (227 * 1024 - kFixed) / (2 * kKv4Tile) < 16 ? (227 * 1024 - kFixed) / (2 * kKv4Tile) : 16;
+  static constexpr int kBatch = 8;
+  static constexpr uint32_t kOffBar = kOffRing + kStages * 2 * kKv4Tile;
+  // full, empty [stages]; piece full, free [4]; K full, free, S full, free, P full, PV done [2
+  // each]; V full, free [3 each]; q landed, full, free [2 each]; O free [2]; drain
+  static constexpr int kNumBars = 2 * kStages + 2 * kPieceQ + 12 + 2 * kVBufs + 8 + 1;
+  static constexpr uint32_t kOffDesc = kOffBar + (8 * kNumBars + 15) / 16 * 16;
+  static constexpr uint32_t kOffFloat = kOffDesc + kPieceQ * 32;
+  // references (true, used), factors, row maxima and sums of the four warps, 1 / sums, q's factors
+  static constexpr uint32_t kFloats = 4 * 64 + 4 * 64 + 4 * 64 + 64 + 8;
+  static constexpr uint32_t kOffMisc = kOffFloat + 4 * kFloats;
+  static constexpr uint32_t kOffPlan = kOffMisc + 256;
+  static constexpr uint32_t kSmemBytes = 1024 /* alignment slack */ + kOffPlan;
+  static constexpr uint32_t kSmemBytesMax = kSmemBytes + 4 * (kKv4MaxSeqs + 1);
+  static_assert(kSmemBytesMax <= 227 * 1024, "shared memory");
+  static_assert(kOffFloat + 4 * kFloats + 256 - kOffBar <= 5120, "small arrays");
+  static_assert(kStages >= 8, "units ahead");
+};
+// Registers a thread by warpgroup, of the 128 that the launch gives each: softmax, K, V, others.
+constexpr int kRegsSoftmax = 200, kRegsK = 112, kRegsV = 104, kRegsOther = 96;
+static_assert(kRegsSoftmax + kRegsK + kRegsV + kRegsOther == 512, "registers");
+
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N) : "memory");
+}
+
+// 8 columns of this warp's 32 lanes.
+__device__ __forceinline__ void tmem_ld8(uint32_t a, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                 "=r"(r[6]), "=r"(r[7])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t a, const float* v) {
+  const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(a),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+               "r"(r[7])
+               : "memory");
+}
+// Floats as integers of the same order (NaN beyond the infinities).
+__device__ __forceinline__ int ordered(float x) {
+  const int i = __float_as_int(x);
+  return i ^ ((i >> 31) & 0x7FFFFFFF);
+}
+__device__ __forceinline__ float from_ordered(int i) {
+  return __int_as_float(i ^ ((i >> 31) & 0x7FFFFFFF));
+}
+
+// Sums of l[0 .. N) over the warp's lanes, for rows `at` on: each exchange halves the rows that
+// a lane goes on with, while they are even.
+template <int W, int N, int COLS>
+__device__ __forceinline__ void sum_rows(float (&l)[COLS], int at, float* sums, int lane) {
+  if constexpr (W == 0) {
+#pragma unroll
+    for (int c = 0; c < N; ++c) sums[at + c] = l[c];
+  } else if constexpr (N % 2 == 0) {
+    const bool up = (lane & W) != 0;
+#pragma unroll
+    for (int c = 0; c < N / 2; ++c) {
+      const float give = up ? l[c] : l[c + N / 2];
+      l[c] = (up ? l[c + N / 2] : l[c]) + __shfl_xor_sync(0xffffffffu, give, W);
+    }
+    sum_rows<W / 2, N / 2>(l, up ? at + N / 2 : at, sums, lane);
+  } else {
+#pragma unroll
+    for (int c = 0; c < N; ++c) l[c] += __shfl_xor_sync(0xffffffffu, l[c], W);
+    sum_rows<W / 2, N>(l, at, sums, lane);
+  }
+}
+
+template <int COLS>
+__global__ void __launch_bounds__(kThreads, 1)
+    kv4_tc_kernel(const __grid_constant__ Kv4DecodeParams p, const __grid_constant__ CUtensorMap tmq) {
+  using C = Cfg<COLS>;
+  constexpr int R = C::kStages, kN = C::kN;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const uint32_t base = smem_u32(smem);
+  const uint32_t bars = base + C::kOffBar;
+  auto full = [&](uint32_t s) { return bars + 8u * s; };
+  auto empty = [&](uint32_t s) { return bars + 8u * (R + s); };
+  const uint32_t b2 = bars + 8u * 2 * R;
+  auto pfull = [&](int s) { return b2 + 8u * s; };
+  auto pfree = [&](int s) { return b2 + 8u * (kPieceQ + s); };
+  const uint32_t b3 = b2 + 8u * 2 * kPieceQ;
+  auto k_full = [&](uint32_t i) { return b3 + 8u * i; };
+  auto k_free = [&](uint32_t i) { return b3 + 8u * (2 + i); };
+  auto s_full = [&](uint32_t i) { return b3 + 8u * (4 + i); };
+  auto s_free = [&](uint32_t i) { return b3 + 8u * (6 + i); };
+  auto p_full = [&](uint32_t i) { return b3 + 8u * (8 + i); };
+  auto pv_done = [&](uint32_t i) { return b3 + 8u * (10 + i); };
+  const uint32_t b4 = b3 + 8u * 12;
+  auto v_full = [&](uint32_t i) { return b4 + 8u * i; };
+  auto v_free = [&](uint32_t i) { return b4 + 8u * (kVBufs + i); };
+  const uint32_t b5 = b4 + 8u * 2 * kVBufs;
+  auto q_landed = [&](int i) { return b5 + 8u * i; };
+  auto q_full = [&](int i) { return b5 + 8u * (2 + i); };
+  auto q_free = [&](int i) { return b5 + 8u * (4 + i); };
+  auto o_free = [&](int i) { return b5 + 8u * (6 + i); };
+  const uint32_t drain = b5 + 8u * 8;
+  const int4* desc = reinterpret_cast<const int4*>(smem + C::kOffDesc);
+  float* fl = reinterpret_cast<float*>(smem + C::kOffFloat);
+  float* s_true = fl;             // references: the largest score so far, or -inf
+  float* s_ref = fl + 64;         // what is subtracted: the same, 0 for -inf
+  float* s_alpha = fl + 128;
+  float* s_inv = fl + 192;
+  float* s_max = fl + 256;        // [4][64]
+  float* s_sum = fl + 512;        // [4][64]
+  float* s_qinv = fl + 768;       // [2], then scratch
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc);
+  volatile int* s_bad = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::kOffMisc + 16);
+  int32_t* warp_tot = reinterpret_cast<int32_t*>(smem + C::kOffMisc + 128);
+  int32_t* cu = reinterpret_cast<int32_t*>(smem + C::kOffPlan);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
+  const int B = p.num_seqs, T = p.q_len;
+  const uint32_t H = (uint32_t)p.num_kv_heads;
+  const unsigned long long lim = p.timeout_ns, book_ns = p.timeout_ns * kBookkeepingWaits;
+
+  if (tid == 0) {
+    for (int s = 0; s < R; ++s) {
+      mbar_init(full(s), 2);      // K and V
+      mbar_init(empty(s), 2 + 4);  // the warps of the tile's K, those of V
+    }
+    for (int s = 0; s < kPieceQ; ++s) {
+      mbar_init(pfull(s), 1);
+      mbar_init(pfree(s), kPieceReaders);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(k_full(i), 128);
+      mbar_init(k_free(i), 1);
+      mbar_init(s_full(i), 1);
+      mbar_init(s_free(i), 128);
+      mbar_init(p_full(i), 128);
+      mbar_init(pv_done(i), 1);
+      mbar_init(q_landed(i), 1);
+      mbar_init(q_full(i), 64);
+      mbar_init(q_free(i), 1);
+      mbar_init(o_free(i), 128);
+    }
+    for (int i = 0; i < kVBufs; ++i) {
+      mbar_init(v_full(i), 128);
+      mbar_init(v_free(i), 1);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    *s_bad = 0;
+    cu[0] = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kMmaWarp) {
+    tc05::tmem_alloc(smem_u32(s_tmem), kTmemCols);
+    tc05::tmem_relinquish();
+  }
+  // rows of q's operand that no query row fills stay 0
+  for (uint32_t i = tid; i < 2 * C::kQBuf / 16; i += kThreads)
+    reinterpret_cast<uint4*>(smem + C::kOffQ)[i] = make_uint4(0u, 0u, 0u, 0u);
+  tc05::fence_async_shared();
+  tc05::tc_fence_before();
+  griddep_wait();
+  griddep_launch_dependents();
+  __syncthreads();
+  tc05::tc_fence_after();
+  plan_step(p, cu, s_bad, warp_tot, kThreads, warp == kProducerWarp);
+  const uint32_t tmem = *s_tmem;
+
+  // Every role walks the pieces: piece(j) waits for descriptor j and returns whether there is
+  // one; the reader hands it back.
+  struct Desc {
+    int b, h, t0, n, flags, slot, len;
+    uint32_t g0;
+  };
+  auto piece = [&](int j, Desc& d) -> bool {
+    const int s = j % kPieceQ;
+    const bool ok = wait_phase(pfull(s), (j / kPieceQ) & 1u, abort_flag, p.err, book_ns);
+    if (!__all_sync(0xffffffffu, ok)) return false;
+    const int4 x = desc[2 * s], y = desc[2 * s + 1];
+    d.b = x.x; d.h = x.y; d.t0 = x.z; d.n = x.w;
+    d.flags = y.x; d.slot = y.y; d.g0 = (uint32_t)y.z; d.len = y.w;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(pfree(s));
+    return !(d.flags & kFlagEnd);
+  };
+  auto wait = [&](uint32_t bar, uint32_t parity) -> bool {  // a warp together
+    return __all_sync(0xffffffffu, wait_phase(bar, parity & 1u, abort_flag, p.err, lim));
+  };
+
+  if (warp >= kProducerWarp) {
+    regs_dec<kRegsOther>();
+    if (warp == kProducerWarp) {
+      // ---------------------------------------------------------- producer
+      const PartPlan M = part_plan(p, cu, s_bad);
+      UnitCopies<R, C::kBatch> copies;
+      copies.ring = base + C::kOffRing;
+      copies.full = full(0);
+      copies.empty = empty(0);
+      copies.policy = evict_first_policy();
+      copies.abort_flag = abort_flag;
+      copies.stop = p.withhold_copies != 0;  // failure-path test: no copy is issued
+      bool lost = false;
+      int j = 0;
+      if (blockIdx.x == 0 && lane == 0) {
+        if (*s_bad) atomicOr(p.err, HPC_DEVCHK_BAD_LENGTH);
+        p.owners[0] = (int32_t)M.P;
+      }
+      auto publish = [&](const Piece& x) {
+        const int s = j % kPieceQ;
+        const bool end = (x.flags & kFlagEnd) != 0;
+        if (lane == 0 && !lost) {
+          if (!wait_phase(pfree(s), ((j / kPieceQ) & 1u) ^ 1u, abort_flag, p.err, book_ns)) {
+            lost = true;
+          } else {
+            int4* d = const_cast<int4*>(desc) + 2 * s;
+            d[0] = make_int4(x.b, x.h, x.t0, x.n);
+            d[1] = make_int4(x.flags, x.slot, (int)copies.g, end ? 0 : __ldg(p.seq_lens + x.b));
+            mbar_arrive(pfull(s));  // release: the descriptor is visible to its waiters
+          }
+        }
+        lost = __shfl_sync(0xffffffffu, (int)lost, 0) != 0;
+        ++j;
+      };
+      if (blockIdx.x < M.P) {
+        const int4 begun = walk_part(
+            M, cu, B, H, (int)blockIdx.x, [&](const Piece& x) { copies.ahead(p, x); },
+            [&](const Piece& x) {
+              publish(x);
+              copies.copy(p, x);
+            });
+        if (lane == 0) *reinterpret_cast<int4*>(p.owners + 4 + 4 * blockIdx.x) = begun;
+      }
+      publish(Piece{0, 0, 0, 0, kFlagEnd, -1});
+      named_bar_sync(3, kThreads);
+      if (*abort_flag) copies.drain(p);
+      return;
+    }
+    if (warp == kMmaWarp) {
+      // -------------------------------------------------------- MMA issue
+      // The whole warp runs the schedule; one elected lane issues. S^T of a step goes ahead
+      // of the products with V of the step before it.
+      const bool leader = tc05::elect_one() != 0;
+      constexpr uint32_t kIdS = tc05::idesc_f16_f32(128, kN, false, false);
+      constexpr uint32_t kIdO = tc05::idesc_f16_f32(128, kN, true, true);
+      const uint64_t qd = tc05::smem_desc_sw128(base + C::kOffQ, 16, 1024);
+      const uint64_t vd = tc05::smem_desc_sw128(base + C::kOffV, kVTile / 2, 1024);
+      const uint64_t pd = tc05::smem_desc_sw128(base + C::kOffP, 16, 1024);
+      bool ok = true, any = false;
+      uint32_t step = 0;
+      struct Pv {
+        uint32_t step, u;
+        int j, tiles;
+        bool first;
+      } pv = {0, 0, 0, 0, false};  // tiles 0: none waits
+      auto issue_pv = [&]() -> bool {
+        const uint32_t i = pv.step & 1;
+        const uint32_t od = tmem + kColO + 64u * (pv.j & 1);
+        if (pv.first && pv.j >= 2 && !wait(o_free(pv.j & 1), ((pv.j >> 1) - 1))) return false;
+        if (!wait(p_full(i), pv.step >> 1)) return false;
+        for (int q = 0; q < pv.tiles; ++q) {
+          const uint32_t u = pv.u + q, vb = u % kVBufs;
+          if (!wait(v_full(vb), u / kVBufs)) return false;
+          tc05::tc_fence_after();
+          if (leader) {
+            const uint64_t a = vd + (uint64_t)(vb * (kVTile >> 4));
+            const uint64_t b = pd + (uint64_t)(i * (kPBuf >> 4) + q * (8192 >> 4));
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc05::mma_f16_ss(od, a + kk * (2048 >> 4), b + kk * (2048 >> 4), kIdO,
+                               pv.first && q == 0 && kk == 0 ? 0u : 1u);
+            tc05::mma_commit(v_free(vb));
+          }
+          __syncwarp();
+        }
+        if (leader) tc05::mma_commit(pv_done(i));
+        __syncwarp();
+        pv.tiles = 0;
+        return true;
+      };
+      Desc d;
+      for (int j = 0; ok && piece(j, d); ++j) {
+        const int steps = (d.n + 1) / 2;
+        ok = wait(q_full(j & 1), j >> 1);
+        for (int k = 0; ok && k < steps; ++k, ++step) {
+          const uint32_t i = step & 1;
+          ok = wait(k_full(i), step >> 1) && (step < 2 || wait(s_free(i), (step >> 1) - 1));
+          if (!ok) break;
+          tc05::tc_fence_after();
+          if (leader) {
+            const uint32_t sd = tmem + kColS + 64u * i, a = tmem + kColK + 64u * i;
+            const uint64_t b = qd + (uint64_t)((j & 1) * (C::kQBuf >> 4));
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              tc05::mma_f16_ts(sd, a + 8 * kk, b + (kk >> 2) * (C::kQHalf >> 4) + (kk & 3) * 2, kIdS,
+                               kk > 0 ? 1u : 0u);
+            tc05::mma_commit(s_full(i));
+            tc05::mma_commit(k_free(i));
+            if (k == steps - 1) tc05::mma_commit(q_free(j & 1));
+          }
+          __syncwarp();
+          any = true;
+          if (pv.tiles > 0) ok = issue_pv();
+          pv.step = step;
+          pv.u = d.g0 + 2 * k;
+          pv.j = j;
+          pv.tiles = d.n - 2 * k < 2 ? 1 : 2;
+          pv.first = k == 0;
+        }
+      }
+      if (ok && pv.tiles > 0) issue_pv();
+      if (leader && any) {
+        tc05::mma_commit(drain);  // every MMA this lane issued has completed
+        wait_phase(drain, 0, abort_flag, p.err, 1000000000ull, false);
+      }
+      __syncwarp();
+      tc05::tc_fence_before();
+      named_bar_sync(3, kThreads);
+      tc05::tc_fence_after();
+      tc05::tmem_dealloc(tmem, kTmemCols);
+      return;
+    }
+    // ------------------------------------------------------- q to f16
+    // A thread is a query row of the piece; both halves of it in place, with one power of two
+    // for all rows that puts the largest element in [2^14, 2^15). Elementwise, so that the
+    // swizzled order of a row's chunks does not matter.
+    const int r = tid - 32 * kQWarp0;
+    Desc d = {};
+    for (int j = 0;; ++j) {
+      const int i = j & 1;
+      bool ok = piece(j, d);
+      // once the MMAs on the buffer's previous rows are done
+      if (ok) ok = j < 2 || wait(q_free(i), (j >> 1) - 1);
+      if (any_of<5, 64>(!ok)) break;  // (both warps leave together)
+      if (r == 0 && !p.withhold_copies) {
+        mbar_arrive_expect_tx(q_landed(i), (uint32_t)(T * kGroup * kHeadDim * 2));
+        const uint32_t dq = base + C::kOffQ + i * C::kQBuf;
+        tc05::tma_load_4d(dq, &tmq, q_landed(i), 0, d.h * kGroup, 0, d.b);
+        tc05::tma_load_4d(dq + C::kQHalf, &tmq, q_landed(i), 64, d.h * kGroup, 0, d.b);
+      }
+      ok = wait(q_landed(i), j >> 1);
+      if (any_of<5, 64>(!ok)) {  // the rows may still be landing
+        if (r == 0 && !p.withhold_copies)
+          wait_phase(q_landed(i), (j >> 1) & 1u, abort_flag, p.err, 1000000000ull, false);
+        break;
+      }
+      uint8_t* row = smem + C::kOffQ + i * C::kQBuf + r * 128;
+      auto chunk = [&](int c) -> uint4* {
+        return reinterpret_cast<uint4*>(row + (c >> 3) * C::kQHalf + ((c ^ r) & 7) * 16);
+      };
+      const bool mine = r < T * kGroup;
+      float mx = 0.f;
+      if (mine) {
+        for (int c = 0; c < 16; ++c) {
+          const uint4 x = *chunk(c);
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[e] << 16)),
+                                 fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
+        }
+      }
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      if (lane == 0) s_qinv[2 + (warp - kQWarp0)] = mx;
+      named_bar_sync(5, 64);
+      mx = fmaxf(s_qinv[2], s_qinv[3]);
+      int e = 0;
+      if (mx > 0.f) {
+        e = 14 - ((int)((__float_as_uint(mx) >> 23) & 0xFF) - 127);
+        e = e < -113 ? -113 : (e > 100 ? 100 : e);
+      }
+      const float sc = __uint_as_float((uint32_t)(e + 127) << 23);
+      if (mine) {
+        for (int c = 0; c < 16; ++c) {
+          uint4 x = *chunk(c);
+          uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            w[y] = pack_f16(__uint_as_float(w[y] << 16) * sc,
+                            __uint_as_float(w[y] & 0xFFFF0000u) * sc);
+          *chunk(c) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      // (a factor of 0 would make NaN of masked scores, an infinite one of scores of 0)
+      if (r == 0)
+        s_qinv[i] = fminf(
+            fmaxf(p.score_scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23), FLT_MIN), FLT_MAX);
+      tc05::fence_async_shared();  // the MMAs read q through the async proxy
+      named_bar_sync(5, 64);       // (the maxima are read before the next piece's are written)
+      mbar_arrive(q_full(i));
+    }
+    named_bar_sync(3, kThreads);
+    return;
+  }
+
+  if (warp >= kVWarp0) {
+    regs_dec<kRegsV>();
+    // ------------------------------------------------------ V to f16
+    // Sixteen elements of a token to a thread: eight bytes of codes times their scale, into
+    // the two 64-element halves of the tile, 128-byte swizzle. A 16-byte store is served 8
+    // threads at a time: four chunks of one row and the other four of a row of the opposite
+    // swizzle parity, so that they lie in different banks. Rows past the sequence become 0,
+    // whatever the slots hold.
+    const int ct = tid - 32 * kVWarp0;
+    const int cq = ct & 15, c = cq & 7, cr = ((cq >> 2) & 1) ^ (cq >> 3);
+    Desc d;
+    bool ok = true;
+    for (int j = 0; ok && piece(j, d); ++j) {
+      for (int k = 0; ok && k < d.n; ++k) {
+        const uint32_t u = d.g0 + k, slot = u % R, vb = u % kVBufs;
+        ok = wait(full(slot), u / R) && (u < kVBufs || wait(v_free(vb), u / kVBufs - 1));
+        if (!ok) break;
+        const uint32_t src = base + C::kOffRing + slot * (2 * kKv4Tile) + kKv4Tile;
+        const uint32_t dst = base + C::kOffV + vb * kVTile + (c >> 2) * (kVTile / 2);
+        const int stored = d.len - (d.t0 + k) * kBlockTokens;
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+          const int t = it * 16 + (ct >> 4) * 2 + cr;
+          const uint32_t row = src + t * kKv4Row;
+          const uint2 x = *reinterpret_cast<const uint2*>(__cvta_shared_to_generic(row + 8 * c));
+          uint32_t f = *reinterpret_cast<const uint8_t*>(__cvta_shared_to_generic(row + kKv4Codes + c));
+          if (t >= stored) f = 0;
+          f = both_low(kv4_scales(f));
+          uint32_t w[2][4];
+          e2m1x8_to_f16(x.x, w[0]);
+          e2m1x8_to_f16(x.y, w[1]);
+          const int cc = (c & 3) * 2;
+          const uint32_t to = dst + t * 128;
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+#pragma unroll
+            for (int z = 0; z < 4; ++z) w[y][z] = mul_f16x2(w[y][z], f);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             to + ((uint32_t)((cc + y) ^ (t & 7)) << 4)),
+                         "r"(w[y][0]), "r"(w[y][1]), "r"(w[y][2]), "r"(w[y][3])
+                         : "memory");
+          }
+        }
+        tc05::fence_async_shared();  // the MMAs read the tile through the async proxy
+        mbar_arrive(v_full(vb));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty(slot));
+      }
+    }
+    named_bar_sync(3, kThreads);
+    return;
+  }
+
+  if (warp >= kKWarp0) {
+    regs_dec<kRegsK>();
+    // --------------------------------------- K to f16, in tensor memory
+    // A thread is a token of the step, its lane of tensor memory.
+    const int row = tid - 32 * kKWarp0, tile = row >> 6;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    uint32_t step = 0;
+    Desc d;
+    bool ok = true;
+    for (int j = 0; ok && piece(j, d); ++j) {
+      const int steps = (d.n + 1) / 2;
+      for (int k = 0; ok && k < steps; ++k, ++step) {
+        const uint32_t i = step & 1, u = d.g0 + 2 * k + tile, slot = u % R;
+        const bool there = 2 * k + tile < d.n;
+        ok = (!there || wait(full(slot), u / R)) && (step < 2 || wait(k_free(i), (step >> 1) - 1));
+        if (!ok) break;
+        if (there) {
+          tc05::tc_fence_after();
+          const uint32_t src = base + C::kOffRing + slot * (2 * kKv4Tile) + (row & 63) * kKv4Row;
+          auto load = [&](int x) {
+            return *reinterpret_cast<const uint2*>(__cvta_shared_to_generic(src + 8 * x));
+          };
+          const uint2 sc = load(8);
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            uint32_t w[32];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const uint2 c = load(4 * hf + x);
+              const uint32_t pair = kv4_scales((hf ? sc.y : sc.x) >> (16 * (x >> 1)));
+              const uint32_t f = x & 1 ? both_high(pair) : both_low(pair);
+              uint32_t a[4], b[4];
+              e2m1x8_to_f16(c.x, a);
+              e2m1x8_to_f16(c.y, b);
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                w[8 * x + y] = mul_f16x2(a[y], f);
+                w[8 * x + 4 + y] = mul_f16x2(b[y], f);
+              }
+            }
+            tc05::tmem_st32(tmem + kColK + 64u * i + 32u * hf + lanes, w);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(empty(slot));  // (the row has been read)
+          tc05::tmem_wait_st();
+          tc05::tc_fence_before();
+        }
+        mbar_arrive(k_full(i));
+      }
+    }
+    named_bar_sync(3, kThreads);
+    return;
+  }
+
+  regs_inc<kRegsSoftmax>();
+  // ------------------------------------------------- softmax, pieces' ends
+  const int row = tid;  // token of the step, element d of the head
+  const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+  // (the four warps take every way out together: barriers lie between)
+  uint32_t step = 0;
+  Desc d = {};
+  for (int j = 0;; ++j) {
+    bool ok = piece(j, d);
+    if (ok) ok = wait(q_full(j & 1), j >> 1);
+    if (any_of<4, 128>(!ok)) break;
+    const int steps = (d.n + 1) / 2;
+    const float sl2 = s_qinv[j & 1];
+    float l[COLS];
+#pragma unroll
+    for (int c = 0; c < COLS; ++c) l[c] = 0.f;
+    const int end = (d.t0 + d.n) * kBlockTokens < d.len ? (d.t0 + d.n) * kBlockTokens : d.len;
+    const uint32_t od = tmem + kColO + 64u * (j & 1) + lanes;
+    for (int k = 0; k < steps; ++k, ++step) {
+      const uint32_t i = step & 1;
+      // scores, and P^T's buffer free of the products of two steps before
+      ok = wait(s_full(i), step >> 1) && (step < 2 || wait(pv_done(i), (step >> 1) - 1));
+      tc05::tc_fence_after();
+      float s[COLS];
+#pragma unroll
+      for (int c = 0; c < COLS; c += 8) tmem_ld8(tmem + kColS + 64u * i + lanes + c, s + c);
+      tc05::tmem_wait_ld();
+      tc05::tc_fence_before();
+      mbar_arrive(s_free(i));
+      const int at = (d.t0 + 2 * k) * kBlockTokens, pos = at + row;
+      if (at + 128 > end || at + 128 > d.len - (T - 1)) {  // some see less than all 128
+#pragma unroll
+        for (int t = 0; t < COLS / 8; ++t) {
+          const int mine = d.len - (T - 1 - t);  // (of rows that no token fills: any value)
+          if (pos >= mine || pos >= end) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) s[8 * t + c] = -INFINITY;
+          }
+        }
+      }
+      bool passed = k == 0;
+      if (k > 0) {
+        float over = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < COLS; ++c) over = fmaxf(over, fmaf(s[c], sl2, -s_ref[c]));
+        passed = over > kPassed;
+      }
+      if (any_of<4, 128>(passed || !ok)) {
+        if (any_of<4, 128>(!ok)) {
+          ok = false;
+          break;
+        }
+        // references: the rows' maxima over the step, of each warp and then of all
+#pragma unroll
+        for (int c = 0; c < COLS; ++c) {
+          const int m = __reduce_max_sync(0xffffffffu, ordered(s[c]));
+          if (lane == (c & 31)) s_max[warp * 64 + c] = from_ordered(m);
+        }
+        named_bar_sync(6, 128);
+        if (tid < COLS) {
+          const float old = k == 0 ? -INFINITY : s_true[tid];
+          const float mx = fmaxf(fmaxf(s_max[tid], s_max[64 + tid]),
+                                 fmaxf(s_max[128 + tid], s_max[192 + tid])) * sl2;
+          const float now = fmaxf(old, mx);
+          s_true[tid] = now;
+          s_ref[tid] = now == -INFINITY ? 0.f : now;
+          s_alpha[tid] = now == -INFINITY ? 1.f : ex2(old - now);
+        }
+        named_bar_sync(6, 128);
+        if (k > 0) {
+          // O is stable once the products of the step before are done
+          ok = wait(pv_done(i ^ 1), (step - 1) >> 1);
+          if (any_of<4, 128>(!ok)) {
+            ok = false;
+            break;
+          }
+          tc05::tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < COLS; c += 8) {
+            float o[8];
+            tmem_ld8(od + c, o);
+            tc05::tmem_wait_ld();
+#pragma unroll
+            for (int x = 0; x < 8; ++x) o[x] *= s_alpha[c + x];
+            tmem_st8(od + c, o);
+          }
+          tc05::tmem_wait_st();
+#pragma unroll
+          for (int c = 0; c < COLS; ++c) l[c] *= s_alpha[c];
+        }
+      }
+      const uint32_t prow = base + C::kOffP + i * kPBuf + row * 128;
+#pragma unroll
+      for (int c = 0; c < COLS; c += 8) {
+        float e[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          e[x] = ex2(fmaf(s[c + x], sl2, -s_ref[c + x]));
+          l[c + x] += e[x];
+        }
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                         prow + ((uint32_t)((c >> 3) ^ (row & 7)) << 4)),
+                     "r"(pack_f16(e[0], e[1])), "r"(pack_f16(e[2], e[3])),
+                     "r"(pack_f16(e[4], e[5])), "r"(pack_f16(e[6], e[7]))
+                     : "memory");
+      }
+      tc05::fence_async_shared();
+      tc05::tc_fence_before();  // (O was rescaled before the products that this allows)
+      mbar_arrive(p_full(i));
+    }
+    if (!ok) break;  // (of all, see above)
+    // ---- the piece's end: sums over the tokens (each lane ends with some of the rows)
+    sum_rows<16, COLS>(l, 0, s_sum + warp * 64, lane);
+    named_bar_sync(6, 128);
+    if (tid < T * kGroup) {
+      const float sum = (s_sum[tid] + s_sum[64 + tid]) + (s_sum[128 + tid] + s_sum[192 + tid]);
+      const float m = s_true[tid];
+      s_inv[tid] = sum == 0.f ? 0.f : p.v_scale / sum;
+      if (!(d.flags & kFlagWhole)) {
+        reinterpret_cast<float2*>(p.ws_ml)[(int64_t)d.slot * T * kGroup + tid] = make_float2(m, sum);
+      } else if (p.lse) {
+        p.lse[(int64_t)d.b * p.l_sb + (int64_t)(tid / kGroup) * p.l_st +
+              (int64_t)(d.h * kGroup + tid % kGroup) * p.l_sh] =
+            sum == 0.f ? -INFINITY : (m + __log2f(sum)) * kLn2;
+      }
+    }
+    named_bar_sync(6, 128);
+    ok = wait(pv_done((step - 1) & 1), (step - 1) >> 1);
+    if (any_of<4, 128>(!ok)) break;
+    tc05::tc_fence_after();
+#pragma unroll
+    for (int t = 0; t < COLS / 8; ++t) {
+      if (t >= T) break;
+      float o[8];
+      tmem_ld8(od + 8 * t, o);
+      tc05::tmem_wait_ld();
+      if (d.flags & kFlagWhole) {
+        __nv_bfloat16* out = p.out + (int64_t)d.b * p.o_sb + (int64_t)t * p.o_st +
+                             (int64_t)(d.h * kGroup) * p.o_sh + row;
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+          out[x * p.o_sh] = __float2bfloat16_rn(o[x] * s_inv[8 * t + x]);
+      } else {
+        float* ws = reinterpret_cast<float*>(p.ws) +
+                    ((int64_t)d.slot * T + t) * (kGroup * kHeadDim) + row;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) ws[x * kHeadDim] = o[x];
+      }
+    }
+    tc05::tc_fence_before();
+    mbar_arrive(o_free(j & 1));
+  }
+  // sequences without tiles (or a step that cannot be): out = 0, lse = -inf
+  if (d.flags & kFlagEnd) {
+    for (int b = (int)blockIdx.x * 4 + warp; b < B; b += (int)gridDim.x * 4) {
+      if (!*s_bad && cu[b + 1] != cu[b]) continue;
+      for (int t = 0; t < T; ++t)
+        for (int x = lane; x < (int)H * kGroup; x += 32) {
+          uint4* o = reinterpret_cast<uint4*>(p.out + (int64_t)b * p.o_sb + (int64_t)t * p.o_st +
+                                              (int64_t)x * p.o_sh);
+#pragma unroll
+          for (int i = 0; i < kHeadDim / 8; ++i) o[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (p.lse)
+            p.lse[(int64_t)b * p.l_sb + (int64_t)t * p.l_st + (int64_t)x * p.l_sh] = -INFINITY;
+        }
+    }
+  }
+  tc05::tc_fence_before();
+  named_bar_sync(3, kThreads);
+}
+
+template <int COLS>
+cudaError_t launch_cols(const Kv4DecodeParams& p, const CUtensorMap& tq, int grid, cudaStream_t stream) {
+  using C = Cfg<COLS>;
+  auto kern = kv4_tc_kernel<COLS>;
+  static std::atomic<uint64_t> configured{0};
+  cudaError_t e = once_per_device(configured, [&] {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)C::kSmemBytesMax);
+  });
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes + 4 * ((size_t)p.num_seqs + 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p, tq);
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_tc(const Kv4DecodeParams& p, const CUtensorMap& tq, int grid,
+                          cudaStream_t stream) {
+  if (p.num_seqs > kKv4MaxSeqs) return cudaErrorInvalidValue;
+  if (p.q_len == 1) return launch_cols<8>(p, tq, grid, stream);
+  if (p.q_len == 2) return launch_cols<16>(p, tq, grid, stream);
+  if (p.q_len <= 4) return launch_cols<32>(p, tq, grid, stream);
+  if (p.q_len <= 6) return launch_cols<48>(p, tq, grid, stream);
+  return launch_cols<64>(p, tq, grid, stream);
+}
+
+}  // namespace hpc
