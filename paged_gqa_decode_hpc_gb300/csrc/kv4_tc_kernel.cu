@@ -34,14 +34,14 @@
 namespace hpc {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kKWarp0 = 4, kVWarp0 = 8, kProducerWarp = 12, kMmaWarp = 13, kQWarp0 = 14;
+constexpr int kThreads = 640;
+constexpr int kKWarp0 = 4, kVWarp0 = 8, kProducerWarp = 16, kMmaWarp = 17, kQWarp0 = 18;
 constexpr int kPieceQ = 4;                  // piece descriptors in flight
-constexpr int kPieceReaders = 4 + 4 + 4 + 1 + 2;
-constexpr int kVBufs = 3;                   // converted V tiles
+constexpr int kPieceReaders = 4 + 4 + 8 + 1 + 2;
+constexpr int kVBufs = 4;                   // converted V tiles: two steps
 constexpr uint32_t kVTile = 64 * 128 * 2;   // two 64-element halves of 64 x 128 bytes
 constexpr uint32_t kPBuf = 128 * 128;       // P^T of a step: 128 rows (tokens) of 128 bytes
-// tensor memory: K (2 x 64 columns), S^T (2 x 64), O^T (2 x 64)
+// tensor memory: K (2 x 64 columns), S^T (2 x 64), O^T (64)
 constexpr uint32_t kColK = 0, kColS = 128, kColO = 256, kTmemCols = 512;
 constexpr float kPassed = 8.f;              // log2 units by which a score may pass its reference
 
@@ -58,9 +58,9 @@ struct Cfg {
   static constexpr int kStages = (227 * 1024 - kFixed) / (2 * kKv4Tile) < 16 ? (227 * 1024 - kFixed) / (2 * kKv4Tile) : 16;
   static constexpr int kBatch = 8;
   static constexpr uint32_t kOffBar = kOffRing + kStages * 2 * kKv4Tile;
-  // full, empty [stages]; piece full, free [4]; K full, free, S full, free, P full, PV done [2
-  // each]; V full, free [3 each]; q landed, full, free [2 each]; O free [2]; drain
-  static constexpr int kNumBars = 2 * kStages + 2 * kPieceQ + 12 + 2 * kVBufs + 8 + 1;
+  // full, empty [stages]; piece full, free [4]; K full, S full, P full, V full, PV done [2
+  // each]; q landed, free [2 each], full [4]; drain
+  static constexpr int kNumBars = 2 * kStages + 2 * kPieceQ + 10 + 8 + 1;
   static constexpr uint32_t kOffDesc = kOffBar + (8 * kNumBars + 15) / 16 * 16;
   static constexpr uint32_t kOffFloat = kOffDesc + kPieceQ * 32;
   // references (true, used), factors, row maxima and sums of the four warps, 1 / sums, q's factors
@@ -73,9 +73,10 @@ struct Cfg {
   static_assert(kOffFloat + 4 * kFloats + 256 - kOffBar <= 5120, "small arrays");
   static_assert(kStages >= 8, "units ahead");
 };
-// Registers a thread by warpgroup, of the 128 that the launch gives each: softmax, K, V, others.
-constexpr int kRegsSoftmax = 200, kRegsK = 112, kRegsV = 104, kRegsOther = 96;
-static_assert(kRegsSoftmax + kRegsK + kRegsV + kRegsOther == 512, "registers");
+// Registers a thread by warpgroup, of the 96 that the launch gives each: softmax, K, V (two),
+// others.
+constexpr int kRegsSoftmax = 184, kRegsK = 88, kRegsV = 64, kRegsOther = 80;
+static_assert(kRegsSoftmax + kRegsK + 2 * kRegsV + kRegsOther == 5 * 96, "registers");
 
 template <int N>
 __device__ __forceinline__ void regs_inc() {
@@ -150,20 +151,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto pfree = [&](int s) { return b2 + 8u * (kPieceQ + s); };
   const uint32_t b3 = b2 + 8u * 2 * kPieceQ;
   auto k_full = [&](uint32_t i) { return b3 + 8u * i; };
-  auto k_free = [&](uint32_t i) { return b3 + 8u * (2 + i); };
-  auto s_full = [&](uint32_t i) { return b3 + 8u * (4 + i); };
-  auto s_free = [&](uint32_t i) { return b3 + 8u * (6 + i); };
-  auto p_full = [&](uint32_t i) { return b3 + 8u * (8 + i); };
-  auto pv_done = [&](uint32_t i) { return b3 + 8u * (10 + i); };
-  const uint32_t b4 = b3 + 8u * 12;
-  auto v_full = [&](uint32_t i) { return b4 + 8u * i; };
-  auto v_free = [&](uint32_t i) { return b4 + 8u * (kVBufs + i); };
-  const uint32_t b5 = b4 + 8u * 2 * kVBufs;
-  auto q_landed = [&](int i) { return b5 + 8u * i; };
-  auto q_full = [&](int i) { return b5 + 8u * (2 + i); };
-  auto q_free = [&](int i) { return b5 + 8u * (4 + i); };
-  auto o_free = [&](int i) { return b5 + 8u * (6 + i); };
-  const uint32_t drain = b5 + 8u * 8;
+  auto s_full = [&](uint32_t i) { return b3 + 8u * (2 + i); };
+  auto p_full = [&](uint32_t i) { return b3 + 8u * (4 + i); };
+  auto v_full = [&](uint32_t i) { return b3 + 8u * (6 + i); };
+  auto pv_done = [&](uint32_t i) { return b3 + 8u * (8 + i); };
+  const uint32_t b4 = b3 + 8u * 10;
+  auto q_landed = [&](int i) { return b4 + 8u * i; };
+  auto q_free = [&](int i) { return b4 + 8u * (2 + i); };
+  auto q_full = [&](int i) { return b4 + 8u * (4 + i); };
+  const uint32_t drain = b4 + 8u * 8;
   const int4* desc = reinterpret_cast<const int4*>(smem + C::kOffDesc);
   float* fl = reinterpret_cast<float*>(smem + C::kOffFloat);
   float* s_true = fl;             // references: the largest score so far, or -inf
@@ -172,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* s_inv = fl + 192;
   float* s_max = fl + 256;        // [4][64]
   float* s_sum = fl + 512;        // [4][64]
-  float* s_qinv = fl + 768;       // [2], then scratch
+  float* s_qinv = fl + 768;       // [4], then scratch
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc);
   volatile int* s_bad = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::kOffMisc + 16);
@@ -192,22 +188,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < kPieceQ; ++s) {
       mbar_init(pfull(s), 1);
       mbar_init(pfree(s), kPieceReaders);
+      mbar_init(q_full(s), 64);  // (four: pieces j + 2 may be ready before the softmax is at j)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(k_full(i), 128);
-      mbar_init(k_free(i), 1);
       mbar_init(s_full(i), 1);
-      mbar_init(s_free(i), 128);
       mbar_init(p_full(i), 128);
+      mbar_init(v_full(i), 256);
       mbar_init(pv_done(i), 1);
       mbar_init(q_landed(i), 1);
-      mbar_init(q_full(i), 64);
       mbar_init(q_free(i), 1);
-      mbar_init(o_free(i), 128);
-    }
-    for (int i = 0; i < kVBufs; ++i) {
-      mbar_init(v_full(i), 128);
-      mbar_init(v_free(i), 1);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -303,7 +293,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kMmaWarp) {
       // -------------------------------------------------------- MMA issue
       // The whole warp runs the schedule; one elected lane issues. S^T of a step goes ahead
-      // of the products with V of the step before it.
+      // of the products with V of the step before it. A wait costs about 100 clk when the
+      // phase is there already, and this warp's are in every step's chain: the two that
+      // remain. That S^T's columns have been read and O^T's rows written out follows from
+      // P^T of a later step; a commit stands for all products issued before it, so that S^T
+      // full also says that the step's K, and P^T of two steps before, are free.
       const bool leader = tc05::elect_one() != 0;
       constexpr uint32_t kIdS = tc05::idesc_f16_f32(128, kN, false, false);
       constexpr uint32_t kIdO = tc05::idesc_f16_f32(128, kN, true, true);
@@ -312,43 +306,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t pd = tc05::smem_desc_sw128(base + C::kOffP, 16, 1024);
       bool ok = true, any = false;
       uint32_t step = 0;
-      struct Pv {
-        uint32_t step, u;
-        int j, tiles;
-        bool first;
-      } pv = {0, 0, 0, 0, false};  // tiles 0: none waits
-      auto issue_pv = [&]() -> bool {
-        const uint32_t i = pv.step & 1;
-        const uint32_t od = tmem + kColO + 64u * (pv.j & 1);
-        if (pv.first && pv.j >= 2 && !wait(o_free(pv.j & 1), ((pv.j >> 1) - 1))) return false;
-        if (!wait(p_full(i), pv.step >> 1)) return false;
-        for (int q = 0; q < pv.tiles; ++q) {
-          const uint32_t u = pv.u + q, vb = u % kVBufs;
-          if (!wait(v_full(vb), u / kVBufs)) return false;
-          tc05::tc_fence_after();
-          if (leader) {
-            const uint64_t a = vd + (uint64_t)(vb * (kVTile >> 4));
-            const uint64_t b = pd + (uint64_t)(i * (kPBuf >> 4) + q * (8192 >> 4));
+      int pv_tiles = 0;  // of the step before, whose products with V wait; 0: none
+      bool pv_first = false;
+      auto issue_pv = [&](uint32_t st) -> bool {
+        const uint32_t i = st & 1;
+        if (!wait(lane & 1 ? v_full(i) : p_full(i), st >> 1)) return false;
+        tc05::tc_fence_after();
+        if (leader) {
+          const uint64_t a = vd + (uint64_t)(i * (2 * kVTile >> 4));
+          const uint64_t b = pd + (uint64_t)(i * (kPBuf >> 4));
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              tc05::mma_f16_ss(od, a + kk * (2048 >> 4), b + kk * (2048 >> 4), kIdO,
-                               pv.first && q == 0 && kk == 0 ? 0u : 1u);
-            tc05::mma_commit(v_free(vb));
+          for (int kk = 0; kk < 8; ++kk) {
+            if (kk == 4 && pv_tiles < 2) break;
+            tc05::mma_f16_ss(tmem + kColO, a + (kk >> 2) * (kVTile >> 4) + (kk & 3) * (2048 >> 4),
+                             b + kk * (2048 >> 4), kIdO, pv_first && kk == 0 ? 0u : 1u);
           }
-          __syncwarp();
+          tc05::mma_commit(pv_done(i));
         }
-        if (leader) tc05::mma_commit(pv_done(i));
         __syncwarp();
-        pv.tiles = 0;
+        pv_tiles = 0;
         return true;
       };
       Desc d;
       for (int j = 0; ok && piece(j, d); ++j) {
         const int steps = (d.n + 1) / 2;
-        ok = wait(q_full(j & 1), j >> 1);
+        ok = wait(q_full(j & 3), j >> 2);
         for (int k = 0; ok && k < steps; ++k, ++step) {
           const uint32_t i = step & 1;
-          ok = wait(k_full(i), step >> 1) && (step < 2 || wait(s_free(i), (step >> 1) - 1));
+          ok = wait(k_full(i), step >> 1);
           if (!ok) break;
           tc05::tc_fence_after();
           if (leader) {
@@ -359,20 +344,16 @@ __global__ void __launch_bounds__(kThreads, 1)
               tc05::mma_f16_ts(sd, a + 8 * kk, b + (kk >> 2) * (C::kQHalf >> 4) + (kk & 3) * 2, kIdS,
                                kk > 0 ? 1u : 0u);
             tc05::mma_commit(s_full(i));
-            tc05::mma_commit(k_free(i));
             if (k == steps - 1) tc05::mma_commit(q_free(j & 1));
           }
           __syncwarp();
           any = true;
-          if (pv.tiles > 0) ok = issue_pv();
-          pv.step = step;
-          pv.u = d.g0 + 2 * k;
-          pv.j = j;
-          pv.tiles = d.n - 2 * k < 2 ? 1 : 2;
-          pv.first = k == 0;
+          if (pv_tiles > 0) ok = issue_pv(step - 1);
+          pv_tiles = d.n - 2 * k < 2 ? 1 : 2;
+          pv_first = k == 0;
         }
       }
-      if (ok && pv.tiles > 0) issue_pv();
+      if (ok && pv_tiles > 0) issue_pv(step - 1);
       if (leader && any) {
         tc05::mma_commit(drain);  // every MMA this lane issued has completed
         wait_phase(drain, 0, abort_flag, p.err, 1000000000ull, false);
@@ -426,9 +407,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      if (lane == 0) s_qinv[2 + (warp - kQWarp0)] = mx;
+      if (lane == 0) s_qinv[4 + (warp - kQWarp0)] = mx;
       named_bar_sync(5, 64);
-      mx = fmaxf(s_qinv[2], s_qinv[3]);
+      mx = fmaxf(s_qinv[4], s_qinv[5]);
       int e = 0;
       if (mx > 0.f) {
         e = 14 - ((int)((__float_as_uint(mx) >> 23) & 0xFF) - 127);
@@ -446,13 +427,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           *chunk(c) = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
-      // (a factor of 0 would make NaN of masked scores, an infinite one of scores of 0)
+      // A factor of 0 would make NaN of masked scores, an infinite one of scores of 0. Four
+      // factors and barriers, for the softmax lags: piece j + 4's q waits for scores of piece
+      // j + 2, which follow P^T of piece j.
       if (r == 0)
-        s_qinv[i] = fminf(
+        s_qinv[j & 3] = fminf(
             fmaxf(p.score_scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23), FLT_MIN), FLT_MAX);
       tc05::fence_async_shared();  // the MMAs read q through the async proxy
       named_bar_sync(5, 64);       // (the maxima are read before the next piece's are written)
-      mbar_arrive(q_full(i));
+      mbar_arrive(q_full(j & 3));
     }
     named_bar_sync(3, kThreads);
     return;
@@ -466,17 +449,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     // threads at a time: four chunks of one row and the other four of a row of the opposite
     // swizzle parity, so that they lie in different banks. Rows past the sequence become 0,
     // whatever the slots hold.
-    const int ct = tid - 32 * kVWarp0;
+    const int tile = (warp - kVWarp0) >> 2;  // of the step's two
+    const int ct = tid & 127;
     const int cq = ct & 15, c = cq & 7, cr = ((cq >> 2) & 1) ^ (cq >> 3);
+    uint32_t step = 0;
     Desc d;
     bool ok = true;
     for (int j = 0; ok && piece(j, d); ++j) {
-      for (int k = 0; ok && k < d.n; ++k) {
-        const uint32_t u = d.g0 + k, slot = u % R, vb = u % kVBufs;
-        ok = wait(full(slot), u / R) && (u < kVBufs || wait(v_free(vb), u / kVBufs - 1));
+      for (int k = tile; ok && k < d.n + tile; k += 2, ++step) {
+        const uint32_t i = step & 1, u = d.g0 + k, slot = u % R;
+        const bool there = k < d.n;
+        // the copy, and the products of two steps before (for a step's missing second tile too:
+        // an arrival counts for the barrier's current phase)
+        const bool other = lane & 1 && step >= 2;
+        if (there || other)
+          ok = wait_phase(other ? pv_done(i) : full(slot), (other ? (step >> 1) - 1 : u / R) & 1u,
+                          abort_flag, p.err, lim);
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
+        if (!there) {
+          mbar_arrive(v_full(i));
+          continue;
+        }
         const uint32_t src = base + C::kOffRing + slot * (2 * kKv4Tile) + kKv4Tile;
-        const uint32_t dst = base + C::kOffV + vb * kVTile + (c >> 2) * (kVTile / 2);
+        const uint32_t dst =
+            base + C::kOffV + (i * 2 + tile) * kVTile + (c >> 2) * (kVTile / 2);
         const int stored = d.len - (d.t0 + k) * kBlockTokens;
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
@@ -502,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         tc05::fence_async_shared();  // the MMAs read the tile through the async proxy
-        mbar_arrive(v_full(vb));
+        mbar_arrive(v_full(i));
         __syncwarp();
         if (lane == 0) mbar_arrive(empty(slot));
       }
@@ -525,7 +522,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; ok && k < steps; ++k, ++step) {
         const uint32_t i = step & 1, u = d.g0 + 2 * k + tile, slot = u % R;
         const bool there = 2 * k + tile < d.n;
-        ok = (!there || wait(full(slot), u / R)) && (step < 2 || wait(k_free(i), (step >> 1) - 1));
+        // the copy, and the scores of two steps before
+        const bool other = lane & 1 && step >= 2;
+        if (there || other)
+          ok = wait_phase(other ? s_full(i) : full(slot), (other ? (step >> 1) - 1 : u / R) & 1u,
+                          abort_flag, p.err, lim);
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (there) {
           tc05::tc_fence_after();
@@ -574,50 +576,55 @@ __global__ void __launch_bounds__(kThreads, 1)
   Desc d = {};
   for (int j = 0;; ++j) {
     bool ok = piece(j, d);
-    if (ok) ok = wait(q_full(j & 1), j >> 1);
+    if (ok) ok = wait(q_full(j & 3), j >> 2);
     if (any_of<4, 128>(!ok)) break;
     const int steps = (d.n + 1) / 2;
-    const float sl2 = s_qinv[j & 1];
+    const float sl2 = s_qinv[j & 3];
     float l[COLS];
 #pragma unroll
     for (int c = 0; c < COLS; ++c) l[c] = 0.f;
     const int end = (d.t0 + d.n) * kBlockTokens < d.len ? (d.t0 + d.n) * kBlockTokens : d.len;
-    const uint32_t od = tmem + kColO + 64u * (j & 1) + lanes;
+    const uint32_t od = tmem + kColO + lanes;
     for (int k = 0; k < steps; ++k, ++step) {
       const uint32_t i = step & 1;
-      // scores, and P^T's buffer free of the products of two steps before
-      ok = wait(s_full(i), step >> 1) && (step < 2 || wait(pv_done(i), (step >> 1) - 1));
+      ok = wait(s_full(i), step >> 1);
       tc05::tc_fence_after();
-      float s[COLS];
-#pragma unroll
-      for (int c = 0; c < COLS; c += 8) tmem_ld8(tmem + kColS + 64u * i + lanes + c, s + c);
-      tc05::tmem_wait_ld();
-      tc05::tc_fence_before();
-      mbar_arrive(s_free(i));
       const int at = (d.t0 + 2 * k) * kBlockTokens, pos = at + row;
-      if (at + 128 > end || at + 128 > d.len - (T - 1)) {  // some see less than all 128
+      float s[COLS];
+      auto scores = [&] {
 #pragma unroll
-        for (int t = 0; t < COLS / 8; ++t) {
-          const int mine = d.len - (T - 1 - t);  // (of rows that no token fills: any value)
-          if (pos >= mine || pos >= end) {
+        for (int c = 0; c < COLS; c += 8) tmem_ld8(tmem + kColS + 64u * i + lanes + c, s + c);
+        tc05::tmem_wait_ld();
+        if (at + 128 > end || at + 128 > d.len - (T - 1)) {  // some see less than all 128
 #pragma unroll
-            for (int c = 0; c < 8; ++c) s[8 * t + c] = -INFINITY;
+          for (int t = 0; t < COLS / 8; ++t) {
+            const int mine = d.len - (T - 1 - t);  // (of rows that no token fills: any value)
+            if (pos >= mine || pos >= end) {
+#pragma unroll
+              for (int c = 0; c < 8; ++c) s[8 * t + c] = -INFINITY;
+            }
           }
         }
-      }
-      bool passed = k == 0;
-      if (k > 0) {
-        float over = -INFINITY;
+      };
+      auto less_reference = [&] {
+        float over[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < COLS; ++c) over = fmaxf(over, fmaf(s[c], sl2, -s_ref[c]));
-        passed = over > kPassed;
-      }
+        for (int c = 0; c < COLS; ++c) {
+          s[c] = fmaf(s[c], sl2, -s_ref[c]);
+          over[c & 3] = fmaxf(over[c & 3], s[c]);
+        }
+        return fmaxf(fmaxf(over[0], over[1]), fmaxf(over[2], over[3]));
+      };
+      scores();
+      bool passed = k == 0;
+      if (k > 0) passed = less_reference() > kPassed;
       if (any_of<4, 128>(passed || !ok)) {
         if (any_of<4, 128>(!ok)) {
           ok = false;
           break;
         }
         // references: the rows' maxima over the step, of each warp and then of all
+        if (k > 0) scores();
 #pragma unroll
         for (int c = 0; c < COLS; ++c) {
           const int m = __reduce_max_sync(0xffffffffu, ordered(s[c]));
@@ -655,6 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c = 0; c < COLS; ++c) l[c] *= s_alpha[c];
         }
+        less_reference();
       }
       const uint32_t prow = base + C::kOffP + i * kPBuf + row * 128;
 #pragma unroll
@@ -662,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float e[8];
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
-          e[x] = ex2(fmaf(s[c + x], sl2, -s_ref[c + x]));
+          e[x] = ex2(s[c + x]);
           l[c + x] += e[x];
         }
         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
@@ -714,8 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int x = 0; x < 8; ++x) ws[x * kHeadDim] = o[x];
       }
     }
-    tc05::tc_fence_before();
-    mbar_arrive(o_free(j & 1));
+    tc05::tc_fence_before();  // (before the next piece's P^T, which lets O^T be written again)
   }
   // sequences without tiles (or a step that cannot be): out = 0, lse = -inf
   if (d.flags & kFlagEnd) {
