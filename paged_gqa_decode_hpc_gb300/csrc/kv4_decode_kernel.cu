@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok && !(fl & kFlagEnd))
         ok = wait_phase(bar_dfull + 8 * buf, (j / C::kBufs) & 1u, abort_flag, p.err, book_ns, false);
       // (the warps leave together: barriers lie between)
-      if (any_of<2, kEpilogueWarps * 32>(!ok || (fl & kFlagEnd))) break;
+      if (any_of(2, kEpilogueWarps * 32, !ok || (fl & kFlagEnd))) break;
       const uint4* dep = dep0 + buf * (C::kDepBytes / 16);
       for (int t = 0; t < T; ++t) {
         Kv4Slices st;

@@ -29,16 +29,15 @@ constexpr int kFlagEnd = 1, kFlagWhole = 2;  // of a piece; its pair's number of
 // the arrival counters return to zero.
 constexpr unsigned long long kBookkeepingWaits = 8;
 
-// Whether any of the N threads of barrier ID says so; they all learn it, and wait for each
-// other.
-template <int ID, int N>
-__device__ __forceinline__ bool any_of(bool x) {
+// Whether any of the `threads` threads of barrier `id` says so; they all learn it, and wait for
+// each other.
+__device__ __forceinline__ bool any_of(int id, int threads, bool x) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, %3, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)x), "n"(ID), "n"(N)
+      : "r"((uint32_t)x), "r"(id), "r"(threads)
       : "memory");
   return r != 0;
 }

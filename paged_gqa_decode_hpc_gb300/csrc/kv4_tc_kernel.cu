@@ -34,15 +34,16 @@
 namespace hpc {
 namespace {
 
-constexpr int kThreads = 640;
-constexpr int kKWarp0 = 4, kVWarp0 = 8, kProducerWarp = 16, kMmaWarp = 17, kQWarp0 = 18;
+constexpr int kThreads = 768;
+constexpr int kKWarp0 = 8, kVWarp0 = 12, kProducerWarp = 20, kScoreWarp = 21, kValueWarp = 22;
+// (and the last warp: q)
 constexpr int kPieceQ = 4;                  // piece descriptors in flight
-constexpr int kPieceReaders = 4 + 4 + 8 + 1 + 2;
+constexpr int kPieceReaders = 8 + 4 + 8 + 1 + 1 + 1;
 constexpr int kVBufs = 4;                   // converted V tiles: two steps
 constexpr uint32_t kVTile = 64 * 128 * 2;   // two 64-element halves of 64 x 128 bytes
 constexpr uint32_t kPBuf = 128 * 128;       // P^T of a step: 128 rows (tokens) of 128 bytes
-// tensor memory: K (2 x 64 columns), S^T (2 x 64), O^T (64)
-constexpr uint32_t kColK = 0, kColS = 128, kColO = 256, kTmemCols = 512;
+// tensor memory: K (2 x 64 columns), S^T (4 x 64), O^T (64)
+constexpr uint32_t kColK = 0, kColS = 128, kColO = 384, kTmemCols = 512;
 constexpr float kPassed = 8.f;              // log2 units by which a score may pass its reference
 
 // COLS: query rows that are computed (8, 16, 32, 48 or 64), of the MMAs' N.
@@ -58,13 +59,13 @@ struct Cfg {
   static constexpr int kStages = (227 * 1024 - kFixed) / (2 * kKv4Tile) < 16 ? (227 * 1024 - kFixed) / (2 * kKv4Tile) : 16;
   static constexpr int kBatch = 8;
   static constexpr uint32_t kOffBar = kOffRing + kStages * 2 * kKv4Tile;
-  // full, empty [stages]; piece full, free [4]; K full, S full, P full, V full, PV done [2
-  // each]; q landed, free [2 each], full [4]; drain
-  static constexpr int kNumBars = 2 * kStages + 2 * kPieceQ + 10 + 8 + 1;
+  // full, empty [stages]; piece full, free [4]; K full [2], S full, free [4 each], P full, V
+  // full, PV done [2 each]; q landed, free [2 each], full [4]; drains [2]
+  static constexpr int kNumBars = 2 * kStages + 2 * kPieceQ + 16 + 8 + 2;
   static constexpr uint32_t kOffDesc = kOffBar + (8 * kNumBars + 15) / 16 * 16;
   static constexpr uint32_t kOffFloat = kOffDesc + kPieceQ * 32;
-  // references (true, used), factors, row maxima and sums of the four warps, 1 / sums, q's factors
-  static constexpr uint32_t kFloats = 4 * 64 + 4 * 64 + 4 * 64 + 64 + 8;
+  // references (true, used), factors, 1 / sums, row maxima or sums of four warps; q's factors
+  static constexpr uint32_t kFloats = 64 * (4 + 4) + 8;
   static constexpr uint32_t kOffMisc = kOffFloat + 4 * kFloats;
   static constexpr uint32_t kOffPlan = kOffMisc + 256;
   static constexpr uint32_t kSmemBytes = 1024 /* alignment slack */ + kOffPlan;
@@ -72,12 +73,12 @@ struct Cfg {
   static_assert(kSmemBytesMax <= 227 * 1024, "shared memory");
   static_assert(kOffFloat + 4 * kFloats + 256 - kOffBar <= 5120, "small arrays");
   static_assert(kStages >= 8, "units ahead");
+  static constexpr int kHalf = COLS / 2;  // the rows of a softmax group
+  // Registers a thread by warpgroup, of the 80 that the launch gives each: softmax (two), K, V
+  // (two), others.
+  static constexpr int kRegsSoftmax = 112, kRegsK = 72, kRegsV = 56, kRegsOther = 72;
+  static_assert(2 * kRegsSoftmax + kRegsK + 2 * kRegsV + kRegsOther == 6 * 80, "registers");
 };
-// Registers a thread by warpgroup, of the 96 that the launch gives each: softmax, K, V (two),
-// others.
-constexpr int kRegsSoftmax = 184, kRegsK = 88, kRegsV = 64, kRegsOther = 80;
-static_assert(kRegsSoftmax + kRegsK + 2 * kRegsV + kRegsOther == 5 * 96, "registers");
-
 template <int N>
 __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N) : "memory");
@@ -152,30 +153,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t b3 = b2 + 8u * 2 * kPieceQ;
   auto k_full = [&](uint32_t i) { return b3 + 8u * i; };
   auto s_full = [&](uint32_t i) { return b3 + 8u * (2 + i); };
-  auto p_full = [&](uint32_t i) { return b3 + 8u * (4 + i); };
-  auto v_full = [&](uint32_t i) { return b3 + 8u * (6 + i); };
-  auto pv_done = [&](uint32_t i) { return b3 + 8u * (8 + i); };
-  const uint32_t b4 = b3 + 8u * 10;
+  auto s_free = [&](uint32_t i) { return b3 + 8u * (6 + i); };
+  auto p_full = [&](uint32_t i) { return b3 + 8u * (10 + i); };
+  auto v_full = [&](uint32_t i) { return b3 + 8u * (12 + i); };
+  auto pv_done = [&](uint32_t i) { return b3 + 8u * (14 + i); };
+  const uint32_t b4 = b3 + 8u * 16;
   auto q_landed = [&](int i) { return b4 + 8u * i; };
   auto q_free = [&](int i) { return b4 + 8u * (2 + i); };
   auto q_full = [&](int i) { return b4 + 8u * (4 + i); };
   const uint32_t drain = b4 + 8u * 8;
   const int4* desc = reinterpret_cast<const int4*>(smem + C::kOffDesc);
   float* fl = reinterpret_cast<float*>(smem + C::kOffFloat);
-  float* s_true = fl;             // references: the largest score so far, or -inf
-  float* s_ref = fl + 64;         // what is subtracted: the same, 0 for -inf
-  float* s_alpha = fl + 128;
-  float* s_inv = fl + 192;
-  float* s_max = fl + 256;        // [4][64]
-  float* s_sum = fl + 512;        // [4][64]
-  float* s_qinv = fl + 768;       // [4], then scratch
+  float* s_qinv = fl + 64 * 8;  // [4], then scratch
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc);
   volatile int* s_bad = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::kOffMisc + 16);
   int32_t* warp_tot = reinterpret_cast<int32_t*>(smem + C::kOffMisc + 128);
   int32_t* cu = reinterpret_cast<int32_t*>(smem + C::kOffPlan);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
+  const int lane = threadIdx.x & 31, tid = threadIdx.x;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int B = p.num_seqs, T = p.q_len;
   const uint32_t H = (uint32_t)p.num_kv_heads;
   const unsigned long long lim = p.timeout_ns, book_ns = p.timeout_ns * kBookkeepingWaits;
@@ -185,27 +182,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(full(s), 2);      // K and V
       mbar_init(empty(s), 2 + 4);  // the warps of the tile's K, those of V
     }
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(s_full(s), 1);
+      mbar_init(s_free(s), 8);
+    }
     for (int s = 0; s < kPieceQ; ++s) {
       mbar_init(pfull(s), 1);
       mbar_init(pfree(s), kPieceReaders);
-      mbar_init(q_full(s), 64);  // (four: pieces j + 2 may be ready before the softmax is at j)
+      mbar_init(q_full(s), 32);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(k_full(i), 128);
-      mbar_init(s_full(i), 1);
-      mbar_init(p_full(i), 128);
+      mbar_init(p_full(i), 256);
       mbar_init(v_full(i), 256);
       mbar_init(pv_done(i), 1);
       mbar_init(q_landed(i), 1);
       mbar_init(q_free(i), 1);
     }
     mbar_init(drain, 1);
+    mbar_init(drain + 8, 1);
     *abort_flag = 0;
     *s_bad = 0;
     cu[0] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == kMmaWarp) {
+  if (warp == kScoreWarp) {
     tc05::tmem_alloc(smem_u32(s_tmem), kTmemCols);
     tc05::tmem_relinquish();
   }
@@ -227,23 +228,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     int b, h, t0, n, flags, slot, len;
     uint32_t g0;
   };
-  auto piece = [&](int j, Desc& d) -> bool {
+  auto hand_back = [&](int j) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(pfree(j % kPieceQ));
+  };
+  auto piece = [&](int j, Desc& d, bool back = true) -> bool {
     const int s = j % kPieceQ;
     const bool ok = wait_phase(pfull(s), (j / kPieceQ) & 1u, abort_flag, p.err, book_ns);
     if (!__all_sync(0xffffffffu, ok)) return false;
     const int4 x = desc[2 * s], y = desc[2 * s + 1];
-    d.b = x.x; d.h = x.y; d.t0 = x.z; d.n = x.w;
-    d.flags = y.x; d.slot = y.y; d.g0 = (uint32_t)y.z; d.len = y.w;
-    __syncwarp();
-    if (lane == 0) mbar_arrive(pfree(s));
+    // (broadcast, so that the compiler keeps what follows from them in uniform registers)
+    auto uni = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+    d.b = uni(x.x); d.h = uni(x.y); d.t0 = uni(x.z); d.n = uni(x.w);
+    d.flags = uni(y.x); d.slot = uni(y.y); d.g0 = (uint32_t)uni(y.z); d.len = uni(y.w);
+    if (back) hand_back(j);
     return !(d.flags & kFlagEnd);
   };
   auto wait = [&](uint32_t bar, uint32_t parity) -> bool {  // a warp together
     return __all_sync(0xffffffffu, wait_phase(bar, parity & 1u, abort_flag, p.err, lim));
   };
+  // Two barriers (the second only if `also`): looked at by half of the lanes each, which costs
+  // one latency where both phases are there already. Else one after the other: a warp that
+  // waits at one barrier sleeps, at two it spins, and takes issue slots from the others.
+  auto wait2 = [&](uint32_t a, uint32_t pa, uint32_t b, uint32_t pb, bool also) -> bool {
+    const bool second = also && (lane & 1);
+    return wait(second ? b : a, second ? pb : pa);
+  };
 
   if (warp >= kProducerWarp) {
-    regs_dec<kRegsOther>();
+    regs_dec<C::kRegsOther>();
     if (warp == kProducerWarp) {
       // ---------------------------------------------------------- producer
       const PartPlan M = part_plan(p, cu, s_bad);
@@ -290,151 +303,149 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (*abort_flag) copies.drain(p);
       return;
     }
-    if (warp == kMmaWarp) {
-      // -------------------------------------------------------- MMA issue
-      // The whole warp runs the schedule; one elected lane issues. S^T of a step goes ahead
-      // of the products with V of the step before it. A wait costs about 100 clk when the
-      // phase is there already, and this warp's are in every step's chain: the two that
-      // remain. That S^T's columns have been read and O^T's rows written out follows from
-      // P^T of a later step; a commit stands for all products issued before it, so that S^T
-      // full also says that the step's K, and P^T of two steps before, are free.
+    if (warp == kScoreWarp || warp == kValueWarp) {
+      // ------------------------------------------------------- MMA issue
+      // A warp for each product; it runs the whole schedule, one elected lane issues. Two,
+      // since waits and issue are a serial chain of about 600 clk a step for each: a wait
+      // takes 100 clk even when the phase is there already.
       const bool leader = tc05::elect_one() != 0;
-      constexpr uint32_t kIdS = tc05::idesc_f16_f32(128, kN, false, false);
-      constexpr uint32_t kIdO = tc05::idesc_f16_f32(128, kN, true, true);
-      const uint64_t qd = tc05::smem_desc_sw128(base + C::kOffQ, 16, 1024);
-      const uint64_t vd = tc05::smem_desc_sw128(base + C::kOffV, kVTile / 2, 1024);
-      const uint64_t pd = tc05::smem_desc_sw128(base + C::kOffP, 16, 1024);
       bool ok = true, any = false;
       uint32_t step = 0;
-      int pv_tiles = 0;  // of the step before, whose products with V wait; 0: none
-      bool pv_first = false;
-      auto issue_pv = [&](uint32_t st) -> bool {
-        const uint32_t i = st & 1;
-        if (!wait(lane & 1 ? v_full(i) : p_full(i), st >> 1)) return false;
-        tc05::tc_fence_after();
-        if (leader) {
-          const uint64_t a = vd + (uint64_t)(i * (2 * kVTile >> 4));
-          const uint64_t b = pd + (uint64_t)(i * (kPBuf >> 4));
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            if (kk == 4 && pv_tiles < 2) break;
-            tc05::mma_f16_ss(tmem + kColO, a + (kk >> 2) * (kVTile >> 4) + (kk & 3) * (2048 >> 4),
-                             b + kk * (2048 >> 4), kIdO, pv_first && kk == 0 ? 0u : 1u);
-          }
-          tc05::mma_commit(pv_done(i));
-        }
-        __syncwarp();
-        pv_tiles = 0;
-        return true;
-      };
       Desc d;
-      for (int j = 0; ok && piece(j, d); ++j) {
-        const int steps = (d.n + 1) / 2;
-        ok = wait(q_full(j & 3), j >> 2);
-        for (int k = 0; ok && k < steps; ++k, ++step) {
-          const uint32_t i = step & 1;
-          ok = wait(k_full(i), step >> 1);
-          if (!ok) break;
-          tc05::tc_fence_after();
-          if (leader) {
-            const uint32_t sd = tmem + kColS + 64u * i, a = tmem + kColK + 64u * i;
-            const uint64_t b = qd + (uint64_t)((j & 1) * (C::kQBuf >> 4));
+      if (warp == kScoreWarp) {
+        constexpr uint32_t kIdS = tc05::idesc_f16_f32(128, kN, false, false);
+        const uint64_t qd = tc05::smem_desc_sw128(base + C::kOffQ, 16, 1024);
+        for (int j = 0; ok && piece(j, d); ++j) {
+          const int steps = (d.n + 1) / 2;
+          ok = wait(q_full(j & 3), j >> 2);
+          for (int k = 0; ok && k < steps; ++k, ++step) {
+            const uint32_t i = step & 1, s4 = step & 3;
+            // K, and the scores of four steps before read
+            ok = wait2(k_full(i), step >> 1, s_free(s4), (step >> 2) - 1, step >= 4);
+            if (!ok) break;
+            tc05::tc_fence_after();
+            if (leader) {
+              const uint32_t sd = tmem + kColS + 64u * s4, a = tmem + kColK + 64u * i;
+              const uint64_t b = qd + (uint64_t)((j & 1) * (C::kQBuf >> 4));
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              tc05::mma_f16_ts(sd, a + 8 * kk, b + (kk >> 2) * (C::kQHalf >> 4) + (kk & 3) * 2, kIdS,
-                               kk > 0 ? 1u : 0u);
-            tc05::mma_commit(s_full(i));
-            if (k == steps - 1) tc05::mma_commit(q_free(j & 1));
+              for (int kk = 0; kk < 8; ++kk)
+                tc05::mma_f16_ts(sd, a + 8 * kk, b + (kk >> 2) * (C::kQHalf >> 4) + (kk & 3) * 2,
+                                 kIdS, kk > 0 ? 1u : 0u);
+              tc05::mma_commit(s_full(s4));
+              if (k == steps - 1) tc05::mma_commit(q_free(j & 1));
+            }
+            __syncwarp();
+            any = true;
           }
-          __syncwarp();
-          any = true;
-          if (pv_tiles > 0) ok = issue_pv(step - 1);
-          pv_tiles = d.n - 2 * k < 2 ? 1 : 2;
-          pv_first = k == 0;
+        }
+      } else {
+        constexpr uint32_t kIdO = tc05::idesc_f16_f32(128, kN, true, true);
+        const uint64_t vd = tc05::smem_desc_sw128(base + C::kOffV, kVTile / 2, 1024);
+        const uint64_t pd = tc05::smem_desc_sw128(base + C::kOffP, 16, 1024);
+        for (int j = 0; ok && piece(j, d); ++j) {
+          const int steps = (d.n + 1) / 2;
+          for (int k = 0; ok && k < steps; ++k, ++step) {
+            const uint32_t i = step & 1;
+            // (that O^T's rows of the piece before were written out follows from P^T)
+            ok = wait2(p_full(i), step >> 1, v_full(i), step >> 1, true);
+            if (!ok) break;
+            tc05::tc_fence_after();
+            if (leader) {
+              const uint64_t a = vd + (uint64_t)(i * (2 * kVTile >> 4));
+              const uint64_t b = pd + (uint64_t)(i * (kPBuf >> 4));
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk) {
+                if (kk == 4 && 2 * k + 1 == d.n) break;
+                tc05::mma_f16_ss(tmem + kColO,
+                                 a + (kk >> 2) * (kVTile >> 4) + (kk & 3) * (2048 >> 4),
+                                 b + kk * (2048 >> 4), kIdO, k == 0 && kk == 0 ? 0u : 1u);
+              }
+              tc05::mma_commit(pv_done(i));
+            }
+            __syncwarp();
+            any = true;
+          }
         }
       }
-      if (ok && pv_tiles > 0) issue_pv(step - 1);
       if (leader && any) {
-        tc05::mma_commit(drain);  // every MMA this lane issued has completed
-        wait_phase(drain, 0, abort_flag, p.err, 1000000000ull, false);
+        const uint32_t mine = drain + (warp == kScoreWarp ? 0 : 8);
+        tc05::mma_commit(mine);  // every MMA this lane issued has completed
+        wait_phase(mine, 0, abort_flag, p.err, 1000000000ull, false);
       }
       __syncwarp();
       tc05::tc_fence_before();
       named_bar_sync(3, kThreads);
-      tc05::tc_fence_after();
-      tc05::tmem_dealloc(tmem, kTmemCols);
+      if (warp == kScoreWarp) {
+        tc05::tc_fence_after();
+        tc05::tmem_dealloc(tmem, kTmemCols);
+      }
       return;
     }
     // ------------------------------------------------------- q to f16
-    // A thread is a query row of the piece; both halves of it in place, with one power of two
+    // A thread is one or two query rows of the piece, each in place, with one power of two
     // for all rows that puts the largest element in [2^14, 2^15). Elementwise, so that the
     // swizzled order of a row's chunks does not matter.
-    const int r = tid - 32 * kQWarp0;
     Desc d = {};
-    for (int j = 0;; ++j) {
+    bool ok = true;
+    for (int j = 0; ok && piece(j, d); ++j) {
       const int i = j & 1;
-      bool ok = piece(j, d);
       // once the MMAs on the buffer's previous rows are done
-      if (ok) ok = j < 2 || wait(q_free(i), (j >> 1) - 1);
-      if (any_of<5, 64>(!ok)) break;  // (both warps leave together)
-      if (r == 0 && !p.withhold_copies) {
+      ok = j < 2 || wait(q_free(i), (j >> 1) - 1);
+      if (!ok || p.withhold_copies) break;
+      if (lane == 0) {
         mbar_arrive_expect_tx(q_landed(i), (uint32_t)(T * kGroup * kHeadDim * 2));
         const uint32_t dq = base + C::kOffQ + i * C::kQBuf;
         tc05::tma_load_4d(dq, &tmq, q_landed(i), 0, d.h * kGroup, 0, d.b);
         tc05::tma_load_4d(dq + C::kQHalf, &tmq, q_landed(i), 64, d.h * kGroup, 0, d.b);
       }
       ok = wait(q_landed(i), j >> 1);
-      if (any_of<5, 64>(!ok)) {  // the rows may still be landing
-        if (r == 0 && !p.withhold_copies)
+      if (!ok) {  // the rows may still be landing
+        if (lane == 0)
           wait_phase(q_landed(i), (j >> 1) & 1u, abort_flag, p.err, 1000000000ull, false);
         break;
       }
-      uint8_t* row = smem + C::kOffQ + i * C::kQBuf + r * 128;
-      auto chunk = [&](int c) -> uint4* {
-        return reinterpret_cast<uint4*>(row + (c >> 3) * C::kQHalf + ((c ^ r) & 7) * 16);
-      };
-      const bool mine = r < T * kGroup;
+      // chunks of 16 bytes: 16 to a row, in the order in which they lie (all of them below
+      // the swizzle, the two halves one after the other)
+      uint8_t* qb = smem + C::kOffQ + i * C::kQBuf;
+      const int chunks = T * kGroup * 8;  // of a half
       float mx = 0.f;
-      if (mine) {
-        for (int c = 0; c < 16; ++c) {
-          const uint4 x = *chunk(c);
+#pragma unroll 1
+      for (int hf = 0; hf < 2; ++hf)
+#pragma unroll 4
+        for (int c = lane; c < chunks; c += 32) {
+          const uint4 x = *reinterpret_cast<const uint4*>(qb + hf * C::kQHalf + 16 * c);
           const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[e] << 16)),
                                  fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
         }
-      }
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      if (lane == 0) s_qinv[4 + (warp - kQWarp0)] = mx;
-      named_bar_sync(5, 64);
-      mx = fmaxf(s_qinv[4], s_qinv[5]);
+      mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
       int e = 0;
       if (mx > 0.f) {
         e = 14 - ((int)((__float_as_uint(mx) >> 23) & 0xFF) - 127);
         e = e < -113 ? -113 : (e > 100 ? 100 : e);
       }
       const float sc = __uint_as_float((uint32_t)(e + 127) << 23);
-      if (mine) {
-        for (int c = 0; c < 16; ++c) {
-          uint4 x = *chunk(c);
+#pragma unroll 1
+      for (int hf = 0; hf < 2; ++hf)
+#pragma unroll 4
+        for (int c = lane; c < chunks; c += 32) {
+          uint4* at = reinterpret_cast<uint4*>(qb + hf * C::kQHalf + 16 * c);
+          const uint4 x = *at;
           uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
           for (int y = 0; y < 4; ++y)
             w[y] = pack_f16(__uint_as_float(w[y] << 16) * sc,
                             __uint_as_float(w[y] & 0xFFFF0000u) * sc);
-          *chunk(c) = make_uint4(w[0], w[1], w[2], w[3]);
+          *at = make_uint4(w[0], w[1], w[2], w[3]);
         }
-      }
       // A factor of 0 would make NaN of masked scores, an infinite one of scores of 0. Four
-      // factors and barriers, for the softmax lags: piece j + 4's q waits for scores of piece
-      // j + 2, which follow P^T of piece j.
-      if (r == 0)
+      // factors and barriers, as descriptors: the softmax may be behind by that many pieces.
+      if (lane == 0)
         s_qinv[j & 3] = fminf(
             fmaxf(p.score_scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23), FLT_MIN), FLT_MAX);
       tc05::fence_async_shared();  // the MMAs read q through the async proxy
-      named_bar_sync(5, 64);       // (the maxima are read before the next piece's are written)
       mbar_arrive(q_full(j & 3));
     }
     named_bar_sync(3, kThreads);
@@ -442,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   if (warp >= kVWarp0) {
-    regs_dec<kRegsV>();
+    regs_dec<C::kRegsV>();
     // ------------------------------------------------------ V to f16
     // Sixteen elements of a token to a thread: eight bytes of codes times their scale, into
     // the two 64-element halves of the tile, 128-byte swizzle. A 16-byte store is served 8
@@ -461,11 +472,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool there = k < d.n;
         // the copy, and the products of two steps before (for a step's missing second tile too:
         // an arrival counts for the barrier's current phase)
-        const bool other = lane & 1 && step >= 2;
-        if (there || other)
-          ok = wait_phase(other ? pv_done(i) : full(slot), (other ? (step >> 1) - 1 : u / R) & 1u,
-                          abort_flag, p.err, lim);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = there ? wait2(full(slot), u / R, pv_done(i), (step >> 1) - 1, step >= 2)
+                   : step < 2 || wait(pv_done(i), (step >> 1) - 1);
         if (!ok) break;
         if (!there) {
           mbar_arrive(v_full(i));
@@ -509,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   if (warp >= kKWarp0) {
-    regs_dec<kRegsK>();
+    regs_dec<C::kRegsK>();
     // --------------------------------------- K to f16, in tensor memory
     // A thread is a token of the step, its lane of tensor memory.
     const int row = tid - 32 * kKWarp0, tile = row >> 6;
@@ -523,11 +531,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t i = step & 1, u = d.g0 + 2 * k + tile, slot = u % R;
         const bool there = 2 * k + tile < d.n;
         // the copy, and the scores of two steps before
-        const bool other = lane & 1 && step >= 2;
-        if (there || other)
-          ok = wait_phase(other ? s_full(i) : full(slot), (other ? (step >> 1) - 1 : u / R) & 1u,
-                          abort_flag, p.err, lim);
-        ok = __all_sync(0xffffffffu, ok);
+        const uint32_t before = s_full((step - 2) & 3);
+        ok = there ? wait2(full(slot), u / R, before, (step - 2) >> 2, step >= 2)
+                   : step < 2 || wait(before, (step - 2) >> 2);
         if (!ok) break;
         if (there) {
           tc05::tc_fence_after();
@@ -567,38 +573,50 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
 
-  regs_inc<kRegsSoftmax>();
+  regs_inc<C::kRegsSoftmax>();
   // ------------------------------------------------- softmax, pieces' ends
-  const int row = tid;  // token of the step, element d of the head
-  const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-  // (the four warps take every way out together: barriers lie between)
+  // Two groups of four warps share the query rows. The warps of a group take every way out
+  // together: barriers lie between.
+  constexpr int N = C::kHalf;
+  const int grp = warp >> 2, c0 = grp * N;  // this group's rows: c0 .. c0 + N - 1
+  const int row = tid & 127;                // token of the step, element d of the head
+  const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+  const uint32_t od = tmem + kColO + lanes + c0;
+  const int bar = 6 + grp;
+  float* s_true = fl + c0;        // references: the largest score so far, or -inf
+  float* s_ref = fl + 64 + c0;    // what is subtracted: the same, 0 for -inf
+  float* s_alpha = fl + 128 + c0;
+  float* s_inv = fl + 192 + c0;
+  float* s_part = fl + 256 + c0;  // [4][64]
   uint32_t step = 0;
   Desc d = {};
   for (int j = 0;; ++j) {
-    bool ok = piece(j, d);
+    bool ok = piece(j, d, false);
     if (ok) ok = wait(q_full(j & 3), j >> 2);
-    if (any_of<4, 128>(!ok)) break;
+    if (any_of(bar, 128, !ok)) break;
     const int steps = (d.n + 1) / 2;
     const float sl2 = s_qinv[j & 3];
-    float l[COLS];
+    hand_back(j);
+    float l[N];
 #pragma unroll
-    for (int c = 0; c < COLS; ++c) l[c] = 0.f;
+    for (int c = 0; c < N; ++c) l[c] = 0.f;
     const int end = (d.t0 + d.n) * kBlockTokens < d.len ? (d.t0 + d.n) * kBlockTokens : d.len;
-    const uint32_t od = tmem + kColO + lanes;
     for (int k = 0; k < steps; ++k, ++step) {
       const uint32_t i = step & 1;
-      ok = wait(s_full(i), step >> 1);
+      // the scores; P^T's buffer free after the products of two steps before
+      ok = wait2(s_full(step & 3), step >> 2, pv_done(i), (step >> 1) - 1, step >= 2);
       tc05::tc_fence_after();
       const int at = (d.t0 + 2 * k) * kBlockTokens, pos = at + row;
-      float s[COLS];
+      float s[N];
       auto scores = [&] {
+        const uint32_t sd = tmem + kColS + 64u * (step & 3) + lanes + c0;
 #pragma unroll
-        for (int c = 0; c < COLS; c += 8) tmem_ld8(tmem + kColS + 64u * i + lanes + c, s + c);
+        for (int c = 0; c < N; c += 8) tmem_ld8(sd + c, s + c);
         tc05::tmem_wait_ld();
         if (at + 128 > end || at + 128 > d.len - (T - 1)) {  // some see less than all 128
 #pragma unroll
-          for (int t = 0; t < COLS / 8; ++t) {
-            const int mine = d.len - (T - 1 - t);  // (of rows that no token fills: any value)
+          for (int t = 0; t < N / 8; ++t) {
+            const int mine = d.len - (T - 1 - (c0 / 8 + t));  // (of rows that no token fills: any)
             if (pos >= mine || pos >= end) {
 #pragma unroll
               for (int c = 0; c < 8; ++c) s[8 * t + c] = -INFINITY;
@@ -607,50 +625,51 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       auto less_reference = [&] {
-        float over[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < COLS; ++c) {
-          s[c] = fmaf(s[c], sl2, -s_ref[c]);
-          over[c & 3] = fmaxf(over[c & 3], s[c]);
-        }
-        return fmaxf(fmaxf(over[0], over[1]), fmaxf(over[2], over[3]));
+        for (int c = 0; c < N; ++c) s[c] = fmaf(s[c], sl2, -s_ref[c]);
       };
       scores();
       bool passed = k == 0;
-      if (k > 0) passed = less_reference() > kPassed;
-      if (any_of<4, 128>(passed || !ok)) {
-        if (any_of<4, 128>(!ok)) {
+      if (!passed) {
+        float over[2] = {-INFINITY, -INFINITY};
+        less_reference();
+#pragma unroll
+        for (int c = 0; c < N; ++c) over[c & 1] = fmaxf(over[c & 1], s[c]);
+        passed = fmaxf(over[0], over[1]) > kPassed;
+      }
+      if (any_of(bar, 128, passed || !ok)) {
+        if (any_of(bar, 128, !ok)) {
           ok = false;
           break;
         }
         // references: the rows' maxima over the step, of each warp and then of all
         if (k > 0) scores();
 #pragma unroll
-        for (int c = 0; c < COLS; ++c) {
+        for (int c = 0; c < N; ++c) {
           const int m = __reduce_max_sync(0xffffffffu, ordered(s[c]));
-          if (lane == (c & 31)) s_max[warp * 64 + c] = from_ordered(m);
+          if (lane == (c & 31)) s_part[(warp & 3) * 64 + c] = from_ordered(m);
         }
-        named_bar_sync(6, 128);
-        if (tid < COLS) {
-          const float old = k == 0 ? -INFINITY : s_true[tid];
-          const float mx = fmaxf(fmaxf(s_max[tid], s_max[64 + tid]),
-                                 fmaxf(s_max[128 + tid], s_max[192 + tid])) * sl2;
+        named_bar_sync(bar, 128);
+        if (row < N) {
+          const float old = k == 0 ? -INFINITY : s_true[row];
+          const float mx = fmaxf(fmaxf(s_part[row], s_part[64 + row]),
+                                 fmaxf(s_part[128 + row], s_part[192 + row])) * sl2;
           const float now = fmaxf(old, mx);
-          s_true[tid] = now;
-          s_ref[tid] = now == -INFINITY ? 0.f : now;
-          s_alpha[tid] = now == -INFINITY ? 1.f : ex2(old - now);
+          s_true[row] = now;
+          s_ref[row] = now == -INFINITY ? 0.f : now;
+          s_alpha[row] = now == -INFINITY ? 1.f : ex2(old - now);
         }
-        named_bar_sync(6, 128);
+        named_bar_sync(bar, 128);
         if (k > 0) {
           // O is stable once the products of the step before are done
           ok = wait(pv_done(i ^ 1), (step - 1) >> 1);
-          if (any_of<4, 128>(!ok)) {
+          if (any_of(bar, 128, !ok)) {
             ok = false;
             break;
           }
           tc05::tc_fence_after();
 #pragma unroll
-          for (int c = 0; c < COLS; c += 8) {
+          for (int c = 0; c < N; c += 8) {
             float o[8];
             tmem_ld8(od + c, o);
             tc05::tmem_wait_ld();
@@ -660,13 +679,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc05::tmem_wait_st();
 #pragma unroll
-          for (int c = 0; c < COLS; ++c) l[c] *= s_alpha[c];
+          for (int c = 0; c < N; ++c) l[c] *= s_alpha[c];
         }
         less_reference();
       }
       const uint32_t prow = base + C::kOffP + i * kPBuf + row * 128;
 #pragma unroll
-      for (int c = 0; c < COLS; c += 8) {
+      for (int c = 0; c < N; c += 8) {
         float e[8];
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
@@ -674,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           l[c + x] += e[x];
         }
         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                         prow + ((uint32_t)((c >> 3) ^ (row & 7)) << 4)),
+                         prow + ((uint32_t)(((c0 + c) >> 3) ^ (row & 7)) << 4)),
                      "r"(pack_f16(e[0], e[1])), "r"(pack_f16(e[2], e[3])),
                      "r"(pack_f16(e[4], e[5])), "r"(pack_f16(e[6], e[7]))
                      : "memory");
@@ -682,39 +701,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc05::fence_async_shared();
       tc05::tc_fence_before();  // (O was rescaled before the products that this allows)
       mbar_arrive(p_full(i));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(s_free(step & 3));
     }
     if (!ok) break;  // (of all, see above)
     // ---- the piece's end: sums over the tokens (each lane ends with some of the rows)
-    sum_rows<16, COLS>(l, 0, s_sum + warp * 64, lane);
-    named_bar_sync(6, 128);
-    if (tid < T * kGroup) {
-      const float sum = (s_sum[tid] + s_sum[64 + tid]) + (s_sum[128 + tid] + s_sum[192 + tid]);
-      const float m = s_true[tid];
-      s_inv[tid] = sum == 0.f ? 0.f : p.v_scale / sum;
+    sum_rows<16, N>(l, 0, s_part + (warp & 3) * 64, lane);
+    named_bar_sync(bar, 128);
+    const int mine = c0 + row;  // a query row
+    if (row < N && mine < T * kGroup) {
+      const float sum = (s_part[row] + s_part[64 + row]) + (s_part[128 + row] + s_part[192 + row]);
+      const float m = s_true[row];
+      s_inv[row] = sum == 0.f ? 0.f : p.v_scale / sum;
       if (!(d.flags & kFlagWhole)) {
-        reinterpret_cast<float2*>(p.ws_ml)[(int64_t)d.slot * T * kGroup + tid] = make_float2(m, sum);
+        reinterpret_cast<float2*>(p.ws_ml)[(int64_t)d.slot * T * kGroup + mine] = make_float2(m, sum);
       } else if (p.lse) {
-        p.lse[(int64_t)d.b * p.l_sb + (int64_t)(tid / kGroup) * p.l_st +
-              (int64_t)(d.h * kGroup + tid % kGroup) * p.l_sh] =
+        p.lse[(int64_t)d.b * p.l_sb + (int64_t)(mine / kGroup) * p.l_st +
+              (int64_t)(d.h * kGroup + mine % kGroup) * p.l_sh] =
             sum == 0.f ? -INFINITY : (m + __log2f(sum)) * kLn2;
       }
     }
-    named_bar_sync(6, 128);
+    named_bar_sync(bar, 128);
     ok = wait(pv_done((step - 1) & 1), (step - 1) >> 1);
-    if (any_of<4, 128>(!ok)) break;
+    if (any_of(bar, 128, !ok)) break;
     tc05::tc_fence_after();
 #pragma unroll
-    for (int t = 0; t < COLS / 8; ++t) {
+    for (int x8 = 0; x8 < N / 8; ++x8) {
+      const int t = c0 / 8 + x8;
       if (t >= T) break;
       float o[8];
-      tmem_ld8(od + 8 * t, o);
+      tmem_ld8(od + 8 * x8, o);
       tc05::tmem_wait_ld();
       if (d.flags & kFlagWhole) {
         __nv_bfloat16* out = p.out + (int64_t)d.b * p.o_sb + (int64_t)t * p.o_st +
                              (int64_t)(d.h * kGroup) * p.o_sh + row;
 #pragma unroll
         for (int x = 0; x < 8; ++x)
-          out[x * p.o_sh] = __float2bfloat16_rn(o[x] * s_inv[8 * t + x]);
+          out[x * p.o_sh] = __float2bfloat16_rn(o[x] * s_inv[8 * x8 + x]);
       } else {
         float* ws = reinterpret_cast<float*>(p.ws) +
                     ((int64_t)d.slot * T + t) * (kGroup * kHeadDim) + row;
@@ -726,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // sequences without tiles (or a step that cannot be): out = 0, lse = -inf
   if (d.flags & kFlagEnd) {
-    for (int b = (int)blockIdx.x * 4 + warp; b < B; b += (int)gridDim.x * 4) {
+    for (int b = (int)blockIdx.x * 8 + warp; b < B; b += (int)gridDim.x * 8) {
       if (!*s_bad && cu[b + 1] != cu[b]) continue;
       for (int t = 0; t < T; ++t)
         for (int x = lane; x < (int)H * kGroup; x += 32) {
@@ -771,8 +794,7 @@ cudaError_t launch_cols(const Kv4DecodeParams& p, const CUtensorMap& tq, int gri
 cudaError_t launch_kv4_tc(const Kv4DecodeParams& p, const CUtensorMap& tq, int grid,
                           cudaStream_t stream) {
   if (p.num_seqs > kKv4MaxSeqs) return cudaErrorInvalidValue;
-  if (p.q_len == 1) return launch_cols<8>(p, tq, grid, stream);
-  if (p.q_len == 2) return launch_cols<16>(p, tq, grid, stream);
+  if (p.q_len <= 2) return launch_cols<16>(p, tq, grid, stream);
   if (p.q_len <= 4) return launch_cols<32>(p, tq, grid, stream);
   if (p.q_len <= 6) return launch_cols<48>(p, tq, grid, stream);
   return launch_cols<64>(p, tq, grid, stream);
