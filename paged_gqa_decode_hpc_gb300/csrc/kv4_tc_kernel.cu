@@ -456,13 +456,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_dec<C::kRegsV>();
     // ------------------------------------------------------ V to f16
     // Sixteen elements of a token to a thread: eight bytes of codes times their scale, into
-    // the two 64-element halves of the tile, 128-byte swizzle. A 16-byte store is served 8
-    // threads at a time: four chunks of one row and the other four of a row of the opposite
-    // swizzle parity, so that they lie in different banks. Rows past the sequence become 0,
-    // whatever the slots hold.
+    // the two 64-element halves of the tile, 128-byte swizzle. Shared memory's bandwidth is
+    // what this kernel has least of, so no access here meets another's bank: an 8-byte load is
+    // served 16 threads at a time, two rows that lie 8 apart (8 rows of 18 words move 16
+    // banks); a 16-byte store 8 at a time, one row of which the upper half's threads store
+    // their second eight elements first. Rows past the sequence become 0, whatever the slots
+    // hold.
     const int tile = (warp - kVWarp0) >> 2;  // of the step's two
     const int ct = tid & 127;
-    const int cq = ct & 15, c = cq & 7, cr = ((cq >> 2) & 1) ^ (cq >> 3);
+    const int c = ct & 7, up = c >> 2;
+    const int r0 = ((ct >> 3) & 1) * 8 + (ct >> 5) * 2 + ((ct >> 4) & 1);
     uint32_t step = 0;
     Desc d;
     bool ok = true;
@@ -485,15 +488,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int stored = d.len - (d.t0 + k) * kBlockTokens;
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
-          const int t = it * 16 + (ct >> 4) * 2 + cr;
+          const int t = it * 16 + r0;
           const uint32_t row = src + t * kKv4Row;
           const uint2 x = *reinterpret_cast<const uint2*>(__cvta_shared_to_generic(row + 8 * c));
           uint32_t f = *reinterpret_cast<const uint8_t*>(__cvta_shared_to_generic(row + kKv4Codes + c));
           if (t >= stored) f = 0;
           f = both_low(kv4_scales(f));
           uint32_t w[2][4];
-          e2m1x8_to_f16(x.x, w[0]);
-          e2m1x8_to_f16(x.y, w[1]);
+          e2m1x8_to_f16(up ? x.y : x.x, w[0]);
+          e2m1x8_to_f16(up ? x.x : x.y, w[1]);
           const int cc = (c & 3) * 2;
           const uint32_t to = dst + t * 128;
 #pragma unroll
@@ -501,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int z = 0; z < 4; ++z) w[y][z] = mul_f16x2(w[y][z], f);
             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                             to + ((uint32_t)((cc + y) ^ (t & 7)) << 4)),
+                             to + ((uint32_t)((cc + (y ^ up)) ^ (t & 7)) << 4)),
                          "r"(w[y][0]), "r"(w[y][1]), "r"(w[y][2]), "r"(w[y][3])
                          : "memory");
           }
