@@ -2,7 +2,6 @@
 // See include/hpc_decode.h for the contract of every call.
 #include <climits>
 #include <cmath>
-#include <cstdlib>
 #include <cstring>
 #include <new>
 #include <string>
@@ -109,11 +108,6 @@ hpc_status score_factor(float softmax_scale, float k_scale, float* out) {
   if (!std::isfinite(*out))
     return fail(HPC_ERR_INVALID_ARG, "softmax_scale times K's scale exceeds fp32");
   return HPC_OK;
-}
-
-int kv4_tc_min_q_len() {  // (for measurements)
-  const char* s = getenv("KV4_TC");
-  return s ? atoi(s) : 2;
 }
 
 // q [B][q_len][H_q][128]: a box is 64 columns of the query rows of a KV head.
@@ -315,14 +309,17 @@ hpc_status hpc_decode_kv4_attn(const hpc_tensor* q, const hpc_tensor* k_cache,
     p.timeout_ns = wait_limit_ns();
     p.withhold_copies = withhold_copies();
     p.ws_ml = (float2*)(p.ws + kv4_slots(plan->num_sms) * T * (kGroup * kHeadDim / 4));
-    if (T >= kv4_tc_min_q_len()) {
+    // One token on mma.sync, whose time is then memory's and less fixed (55.7 us for 32 x 4096
+    // and 131072 positions of 8 KV heads; the other kernel 80.8); more on tcgen05, which
+    // converts a unit's codes once for all of them (2 tokens 83.6 and 82.9 us, 4: 151.6 and
+    // 104.0, 8: 293.5 and 152.2).
+    if (T == 1) {
+      e = launch_kv4_decode(p, plan->num_sms, (cudaStream_t)stream);
+    } else {
       CUtensorMap tq;
       if ((st = make_kv4_q_map(q, &tq)) != HPC_OK) return st;
       e = launch_kv4_tc(p, tq, plan->num_sms, (cudaStream_t)stream);
-      if (e == cudaSuccess) e = launch_kv4_tc_merge(p, plan->num_sms, (cudaStream_t)stream);
-    } else {
-      e = launch_kv4_decode(p, plan->num_sms, (cudaStream_t)stream);
-      if (e == cudaSuccess && T > 1) e = launch_kv4_merge(p, plan->num_sms, (cudaStream_t)stream);
+      if (e == cudaSuccess) e = launch_kv4_merge(p, plan->num_sms, (cudaStream_t)stream);
     }
     if (e != cudaSuccess)
       return fail(HPC_ERR_CUDA, std::string("4-bit decode launch: ") + cudaGetErrorString(e));

@@ -1,5 +1,5 @@
 // Internal declarations of the attention over a 4-bit cache (kv4_decode_kernel.cu,
-// kv4_merge_kernel.cu, capi_kv4.cu); not part of the public ABI.
+// kv4_tc_kernel.cu, kv4_merge_kernel.cu, capi_kv4.cu); not part of the public ABI.
 #pragma once
 
 #include <cuda.h>
@@ -36,8 +36,9 @@ struct Kv4DecodeParams {
   int32_t num_seqs, num_kv_heads, num_blocks, q_len;
   float score_scale_log2;       // softmax_scale * log2(e) * K's scale, > 0
   float v_scale;
-  float4* ws;                   // [slots][q_len][9][32]; kv4_tc_kernel: [slots][q_len][8][128] floats
-  float2* ws_ml;                // kv4_tc_kernel: (m, l) [slots][q_len][8]
+  float4* ws;                   // partial states. One token: [slots][9][32]; several:
+                                //   accumulators [slots][q_len][8 heads][32]
+  float2* ws_ml;                // (several tokens) maximum, sum [slots][q_len][8]
   int32_t* pair_cnt;            // [B * H_kv] pieces (or groups of them) that have arrived
   int32_t* slot_cnt;            // [slots] pieces of a group that have arrived
   int32_t* owners;              // [4 + 4 owners] (q_len > 1): their number, and of each the pair
@@ -57,11 +58,12 @@ inline int64_t kv4_words(int32_t max_seqs, int32_t kv_heads, int32_t grid) {
   return kv4_owner_off(max_seqs, kv_heads, grid) + 4 + 4LL * grid;
 }
 
+// One new token a sequence.
+cudaError_t launch_kv4_decode(const Kv4DecodeParams& p, int grid, cudaStream_t stream);
+// 2 to 8.
 cudaError_t launch_kv4_tc(const Kv4DecodeParams& p, const CUtensorMap& tq, int grid,
                           cudaStream_t stream);
-cudaError_t launch_kv4_tc_merge(const Kv4DecodeParams& p, int grid, cudaStream_t stream);
-cudaError_t launch_kv4_decode(const Kv4DecodeParams& p, int grid, cudaStream_t stream);
-// The split pairs of a step of several tokens, joined.
+// The split pairs of its step, joined.
 cudaError_t launch_kv4_merge(const Kv4DecodeParams& p, int grid, cudaStream_t stream);
 
 }  // namespace hpc

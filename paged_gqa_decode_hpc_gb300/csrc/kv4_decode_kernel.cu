@@ -1,18 +1,16 @@
-// Decode attention of one to eight new tokens per sequence over a 4-bit paged cache:
-// planned, computed and (one token) merged by a single persistent kernel.
+// Decode attention of one new token per sequence over a 4-bit paged cache: planned, computed
+// and merged by a single persistent kernel. (Several tokens: kv4_tc_kernel.cu.)
 //
 //   s_t = scale * q . k_t,  out = sum_t exp(s_t - m) v_t / sum_t exp(s_t - m)
 //
 // over a sequence's 64-token tiles, one (tile, KV head) unit after another with a
-// running maximum and sum; the 8 query heads of a KV head and up to two new tokens
-// share a unit's K and V in registers. The plan is the one-token step's
-// (step_kernel.cu): static parts and a pool of chunks of units, taken in pieces of one
-// (sequence, KV head) pair, whose states are joined by log-sum-exp.
+// running maximum and sum; the 8 query heads of a KV head share a unit's K and V in
+// registers. The plan (kv4_plan.cuh) gives every CTA an equal part of the units, taken in
+// pieces of one (sequence, KV head) pair, whose states are joined by log-sum-exp.
 //
 // What bounds it: HBM in the first place. A unit is 9216 bytes, 206 ns of an SM's share
 // of 6.8 TB/s, in which its 16384 codes have to become f16 operands. So a warp takes a
-// unit by itself: no value moves between warps, and each code is converted once for
-// both tokens of the warp (several warps take a unit where there are more tokens).
+// unit by itself: no value moves between warps.
 //
 // How a unit gets into the MMAs (mma.sync m16n8k16, f16; S^T = K Q^T, O^T = V^T P^T):
 //  * A tile is copied as it lies in memory, 64 rows of 72 bytes. Rows are 18 words
@@ -61,15 +59,11 @@ constexpr int kStage = 2 * kKv4Tile;
 constexpr int kQRow = kHeadDim * 2;               // bytes of a row of q in shared memory
 constexpr int kFan = 16;                          // pieces of a pair that are joined at once
 
-// TW tokens to a warp, NP warps to a unit.
-template <int TW, int NP>
 struct Cfg {
-  static constexpr int kGroups = kConsumerWarps / NP;  // units in work at once, each group's in its own slots
-  static constexpr int kActive = kGroups * NP;         // warps that work (of 8)
-  // deposit buffers: two, so that warps may run a piece ahead, where they fit
-  static constexpr int kBufs = TW == 1 ? 2 : 1;
-  static constexpr int kDepBytes = kActive * TW * kDepVec * 32 * 16;
-  static constexpr int kQBytes = TW * NP * kGroup * kQRow;  // a piece's rows of q
+  static constexpr int kGroups = kConsumerWarps;  // units in work at once, each warp's in its own slots
+  static constexpr int kBufs = 2;                 // deposit buffers: warps may run a piece ahead
+  static constexpr int kDepBytes = kConsumerWarps * kDepVec * 32 * 16;
+  static constexpr int kQBytes = kGroup * kQRow;  // a piece's rows of q
   static constexpr int kFixed =
       kBufs * kDepBytes + kPieceQ * kQBytes + 1024 /* barriers, descriptors, scan */ + 128 + 4 * (kKv4MaxSeqs + 1);
   static constexpr int kStages = (227 * 1024 - kFixed) / kStage / kGroups * kGroups;
@@ -88,9 +82,9 @@ struct Cfg {
   static_assert(kBatch <= kStages, "a slot to each unit of a batch");
   // Registers a thread, of the 128 that the launch gives each (one warp of each warpgroup
   // to an SM sub-partition, so that the four add up to 512).
-  static constexpr int kRegsConsumer = TW == 1 ? 168 : 192;
-  static constexpr int kRegsEpilogue = TW == 1 ? 104 : 72;
-  static constexpr int kRegsProducer = TW == 1 ? 72 : 56;
+  static constexpr int kRegsConsumer = 168;
+  static constexpr int kRegsEpilogue = 104;
+  static constexpr int kRegsProducer = 72;
   static_assert(2 * kRegsConsumer + kRegsEpilogue + kRegsProducer == 512, "registers");
 };
 template <int N>
@@ -163,21 +157,16 @@ __device__ __forceinline__ float load_q4(uint32_t q, int lane, uint32_t (&qf)[8]
   return __uint_as_float((uint32_t)(127 - e) << 23);
 }
 
-// One unit for TW tokens. seen[t]: tokens of the tile that token t sees; stored: tokens
-// of the tile that are in the sequence.
-template <int TW>
+// One unit, of whose tokens `stored` are in the sequence.
 __device__ __forceinline__ void compute_unit4(uint32_t kb, uint32_t vb,
-                                              const uint32_t (&qf)[TW][8][2],
-                                              const int (&seen)[TW], int stored,
-                                              const float (&sl2)[TW], float (&m)[TW][2],
-                                              float (&l)[TW][2], float (&acc)[TW][8][4], int lane) {
+                                              const uint32_t (&qf)[8][2], int stored, float sl2,
+                                              float (&m)[2], float (&l)[2], float (&acc)[8][4],
+                                              int lane) {
   const int g = lane >> 2, c = lane & 3;
   const int ig = row_token(g);
-  float s[TW][4][4];
+  float s[4][4];
 #pragma unroll
-  for (int t = 0; t < TW; ++t)
-#pragma unroll
-    for (int mt = 0; mt < 4; ++mt) s[t][mt][0] = s[t][mt][1] = s[t][mt][2] = s[t][mt][3] = 0.f;
+  for (int mt = 0; mt < 4; ++mt) s[mt][0] = s[mt][1] = s[mt][2] = s[mt][3] = 0.f;
 
   // ---- S^T = K Q^T: rows g and g + 8 of step mt are tokens 32 (mt / 2) + 4 I(g) + 2 (mt % 2) + 0, 1
   const uint32_t k_lane = kb + (uint32_t)(ig * 4 * kKv4Row + 8 * c);
@@ -215,69 +204,63 @@ __device__ __forceinline__ void compute_unit4(uint32_t kb, uint32_t vb,
           a[i] = mul_f16x2(a[i], g0);
           b[i] = mul_f16x2(b[i], g1);
         }
-#pragma unroll
-        for (int t = 0; t < TW; ++t) {
-          const int ks = 4 * hf + 2 * w;
-          mma_f16(s[t][mt], a[0], b[0], a[1], b[1], qf[t][ks][0], qf[t][ks][1]);
-          mma_f16(s[t][mt], a[2], b[2], a[3], b[3], qf[t][ks + 1][0], qf[t][ks + 1][1]);
-        }
+        const int ks = 4 * hf + 2 * w;
+        mma_f16(s[mt], a[0], b[0], a[1], b[1], qf[ks][0], qf[ks][1]);
+        mma_f16(s[mt], a[2], b[2], a[3], b[3], qf[ks + 1][0], qf[ks + 1][1]);
       }
     }
   }
 
   // ---- online softmax in the log2 domain; columns 2c and 2c + 1
-  uint32_t pb[TW][4][2];
+  uint32_t pb[4][2];
+  if (stored < 64) {
 #pragma unroll
-  for (int t = 0; t < TW; ++t) {
-    if (seen[t] < 64) {
+    for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-      for (int mt = 0; mt < 4; ++mt)
+      for (int r = 0; r < 2; ++r)
+        if (32 * (mt >> 1) + 4 * ig + 2 * (mt & 1) + r >= stored)
+          s[mt][2 * r] = s[mt][2 * r + 1] = -INFINITY;
+  }
+  float mx0 = fmaxf(s[0][0], s[0][2]), mx1 = fmaxf(s[0][1], s[0][3]);
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
-          if (32 * (mt >> 1) + 4 * ig + 2 * (mt & 1) + r >= seen[t])
-            s[t][mt][2 * r] = s[t][mt][2 * r + 1] = -INFINITY;
+  for (int mt = 1; mt < 4; ++mt) {
+    mx0 = fmaxf(mx0, fmaxf(s[mt][0], s[mt][2]));
+    mx1 = fmaxf(mx1, fmaxf(s[mt][1], s[mt][3]));
+  }
+  mx0 *= sl2;
+  mx1 *= sl2;
+  if (__any_sync(0xffffffffu, mx0 > m[0] + 8.f || mx1 > m[1] + 8.f)) {
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
+      mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
     }
-    float mx0 = fmaxf(s[t][0][0], s[t][0][2]), mx1 = fmaxf(s[t][0][1], s[t][0][3]);
+    const float n0 = fmaxf(m[0], mx0), n1 = fmaxf(m[1], mx1);
+    const float al0 = n0 == -INFINITY ? 1.f : ex2(m[0] - n0);
+    const float al1 = n1 == -INFINITY ? 1.f : ex2(m[1] - n1);
+    m[0] = n0;
+    m[1] = n1;
+    l[0] *= al0;
+    l[1] *= al1;
 #pragma unroll
-    for (int mt = 1; mt < 4; ++mt) {
-      mx0 = fmaxf(mx0, fmaxf(s[t][mt][0], s[t][mt][2]));
-      mx1 = fmaxf(mx1, fmaxf(s[t][mt][1], s[t][mt][3]));
+    for (int dm = 0; dm < 8; ++dm) {
+      acc[dm][0] *= al0;
+      acc[dm][1] *= al1;
+      acc[dm][2] *= al0;
+      acc[dm][3] *= al1;
     }
-    mx0 *= sl2[t];
-    mx1 *= sl2[t];
-    if (__any_sync(0xffffffffu, mx0 > m[t][0] + 8.f || mx1 > m[t][1] + 8.f)) {
+  }
+  // (a row that has seen no position yet: its scores are all -inf, its P is 0)
+  const float r0 = m[0] == -INFINITY ? 0.f : -m[0];
+  const float r1 = m[1] == -INFINITY ? 0.f : -m[1];
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) {
-        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
-        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
-      }
-      const float n0 = fmaxf(m[t][0], mx0), n1 = fmaxf(m[t][1], mx1);
-      const float al0 = n0 == -INFINITY ? 1.f : ex2(m[t][0] - n0);
-      const float al1 = n1 == -INFINITY ? 1.f : ex2(m[t][1] - n1);
-      m[t][0] = n0;
-      m[t][1] = n1;
-      l[t][0] *= al0;
-      l[t][1] *= al1;
-#pragma unroll
-      for (int dm = 0; dm < 8; ++dm) {
-        acc[t][dm][0] *= al0;
-        acc[t][dm][1] *= al1;
-        acc[t][dm][2] *= al0;
-        acc[t][dm][3] *= al1;
-      }
-    }
-    // (a row that has seen no position yet: its scores are all -inf, its P is 0)
-    const float r0 = m[t][0] == -INFINITY ? 0.f : -m[t][0];
-    const float r1 = m[t][1] == -INFINITY ? 0.f : -m[t][1];
-#pragma unroll
-    for (int mt = 0; mt < 4; ++mt) {
-      const float e0 = ex2(fmaf(s[t][mt][0], sl2[t], r0)), e1 = ex2(fmaf(s[t][mt][1], sl2[t], r1));
-      const float e2 = ex2(fmaf(s[t][mt][2], sl2[t], r0)), e3 = ex2(fmaf(s[t][mt][3], sl2[t], r1));
-      l[t][0] += e0 + e2;
-      l[t][1] += e1 + e3;
-      pb[t][mt][0] = movm_trans(pack_f16(e0, e1));
-      pb[t][mt][1] = movm_trans(pack_f16(e2, e3));
-    }
+  for (int mt = 0; mt < 4; ++mt) {
+    const float e0 = ex2(fmaf(s[mt][0], sl2, r0)), e1 = ex2(fmaf(s[mt][1], sl2, r1));
+    const float e2 = ex2(fmaf(s[mt][2], sl2, r0)), e3 = ex2(fmaf(s[mt][3], sl2, r1));
+    l[0] += e0 + e2;
+    l[1] += e1 + e3;
+    pb[mt][0] = movm_trans(pack_f16(e0, e1));
+    pb[mt][1] = movm_trans(pack_f16(e2, e3));
   }
 
   // ---- O^T += V^T P^T: the k pairs of step kt are tokens ta, tb (rows 2c, 2c + 1) and ta + 1, tb + 1
@@ -316,21 +299,16 @@ __device__ __forceinline__ void compute_unit4(uint32_t kb, uint32_t vb,
         }
       }
 #pragma unroll
-      for (int t = 0; t < TW; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          mma_f16(acc[t][4 * w + i], a[0][0][i], a[0][1][i], a[1][0][i], a[1][1][i], pb[t][kt][0],
-                  pb[t][kt][1]);
+      for (int i = 0; i < 4; ++i)
+        mma_f16(acc[4 * w + i], a[0][0][i], a[0][1][i], a[1][0][i], a[1][1][i], pb[kt][0], pb[kt][1]);
     }
   }
 }
 
-template <int TW, int NP>
 __global__ void __launch_bounds__(kThreads, 1)
     kv4_decode_kernel(const __grid_constant__ Kv4DecodeParams p) {
-  using C = Cfg<TW, NP>;
+  using C = Cfg;
   constexpr int STAGES = C::kStages, kGroups = C::kGroups;
-  constexpr bool kOneToken = TW == 1;  // pieces are merged here, not by a second kernel
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) &
                                              ~uintptr_t(127));
@@ -350,20 +328,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   int32_t* cu = reinterpret_cast<int32_t*>(smem + C::kPlanOff);  // units of a KV head ahead of b
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
-  const int B = p.num_seqs, G = (int)gridDim.x, T = p.q_len;
+  const int B = p.num_seqs, G = (int)gridDim.x;
   const uint32_t H = (uint32_t)p.num_kv_heads;
 
   if (tid == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(bar_full + 8 * s, 2);   // K and V
-      mbar_init(bar_empty + 8 * s, NP);  // the warps of a unit
+      mbar_init(bar_full + 8 * s, 2);  // K and V
+      mbar_init(bar_empty + 8 * s, 1);
     }
     for (int s = 0; s < kPieceQ; ++s) {
       mbar_init(bar_pfull + 8 * s, 1);
-      mbar_init(bar_pfree + 8 * s, C::kActive + kEpilogueWarps);
+      mbar_init(bar_pfree + 8 * s, kConsumerWarps + kEpilogueWarps);
     }
     for (int e = 0; e < C::kBufs; ++e) {
-      mbar_init(bar_dfull + 8 * e, C::kActive);
+      mbar_init(bar_dfull + 8 * e, kConsumerWarps);
       mbar_init(bar_dfree + 8 * e, kEpilogueWarps);
     }
     *abort_flag = 0;
@@ -395,10 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     copies.stop = p.withhold_copies != 0;  // failure-path test: no copy is issued
     bool lost = false;                     // the consumers stopped taking pieces
     int j = 0;
-    if (blockIdx.x == 0 && lane == 0) {
-      if (*s_bad) atomicOr(p.err, HPC_DEVCHK_BAD_LENGTH);
-      if (!kOneToken) p.owners[0] = (int32_t)M.P;
-    }
+    if (blockIdx.x == 0 && lane == 0 && *s_bad) atomicOr(p.err, HPC_DEVCHK_BAD_LENGTH);
     // A piece's descriptor and, with it, its rows of q.
     const bool q_whole = p.q_sh == kHeadDim;  // 8 rows in one piece of memory
     auto publish = [&](const Piece& x) {
@@ -414,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           d[0] = make_int4(x.b, x.h, x.t0, x.t0 + x.n);
           d[1] = make_int4(x.flags, x.slot, (int)(copies.g % kGroups), 0);
           // release: the descriptor is visible to its waiters
-          if (rows) mbar_arrive_expect_tx(pf, (uint32_t)(T * kGroup * kQRow));
+          if (rows) mbar_arrive_expect_tx(pf, (uint32_t)(kGroup * kQRow));
           else mbar_arrive(pf);
         }
       }
@@ -424,25 +399,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const __nv_bfloat16* q0 =
             p.q + (int64_t)x.b * p.q_sb + (int64_t)(x.h * kGroup) * p.q_sh;
         if (q_whole) {
-          if (lane < T)
-            kv4_copy(dq + lane * (kGroup * kQRow), q0 + (int64_t)lane * p.q_st, kGroup * kQRow, pf);
-        } else {
-          for (int r = lane; r < T * kGroup; r += 32)
-            kv4_copy(dq + r * kQRow,
-                     q0 + (int64_t)(r / kGroup) * p.q_st + (int64_t)(r % kGroup) * p.q_sh, kQRow, pf);
+          if (lane == 0) kv4_copy(dq, q0, kGroup * kQRow, pf);
+        } else if (lane < kGroup) {
+          kv4_copy(dq + lane * kQRow, q0 + (int64_t)lane * p.q_sh, kQRow, pf);
         }
       }
       ++j;
     };
     if (blockIdx.x < M.P) {
-      const int4 begun = walk_part(
+      walk_part(
           M, cu, B, H, (int)blockIdx.x, [&](const Piece& x) { copies.ahead(p, x); },
           [&](const Piece& x) {
             publish(x);
             copies.copy(p, x);
           });
-      if (!kOneToken && lane == 0)
-        *reinterpret_cast<int4*>(p.owners + 4 + 4 * blockIdx.x) = begun;
     }
     publish(Piece{0, 0, 0, 0, kFlagEnd, -1});
     named_bar_sync(3, kThreads);
@@ -455,14 +425,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
 
-  uint4* dep0 = reinterpret_cast<uint4*>(smem + C::kDepOff);  // [warp][token][vector][lane]
+  uint4* dep0 = reinterpret_cast<uint4*>(smem + C::kDepOff);  // [warp][vector][lane]
   if (warp >= kEpilogueWarp0) {
     regs_dec<C::kRegsEpilogue>();
     // ------------------------------------------------------------ epilogue
-    // For every piece and token: join the states of the warps that shared its units, then
-    // write the result, or a partial state of a split pair; with one token a step the piece
-    // is counted and the last of a pair's merges them. Each warp does two of the states'
-    // eight slices.
+    // For every piece: join the states of the warps that shared its units, then write the
+    // result, or a partial state of a split pair; the piece is counted, and the last of a
+    // pair's merges them. Each warp does two of the states' eight slices.
     const int e = warp - kEpilogueWarp0;
     for (int j = 0;; ++j) {
       const int qs = j % kPieceQ, buf = j % C::kBufs;
@@ -476,48 +445,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       // (the warps leave together: barriers lie between)
       if (any_of(2, kEpilogueWarps * 32, !ok || (fl & kFlagEnd))) break;
       const uint4* dep = dep0 + buf * (C::kDepBytes / 16);
-      for (int t = 0; t < T; ++t) {
-        Kv4Slices st;
-        st.clear();
-        // the states of token t, from the group that had the piece's first unit on: the
-        // order, like each group's units, is a function of the piece alone
-        auto state = [&](int v) -> const uint4* {
-          const int grp = rot + v < kGroups ? rot + v : rot + v - kGroups;
-          return dep + ((grp * NP + t / TW) * TW + t % TW) * (kDepVec * 32) + lane;
-        };
-        float4 ml[kGroups];
+      Kv4Slices st;
+      st.clear();
+      // the states from the warp that had the piece's first unit on: the order, like each
+      // warp's units, is a function of the piece alone
+      auto state = [&](int v) -> const uint4* {
+        const int from = rot + v < kGroups ? rot + v : rot + v - kGroups;
+        return dep + from * (kDepVec * 32) + lane;
+      };
+      float4 ml[kGroups];
 #pragma unroll
-        for (int v = 0; v < kGroups; ++v) {
-          ml[v] = *reinterpret_cast<const float4*>(state(v) + 4 * 32);
-          st.m[0] = fmaxf(st.m[0], ml[v].x);
-          st.m[1] = fmaxf(st.m[1], ml[v].y);
-        }
+      for (int v = 0; v < kGroups; ++v) {
+        ml[v] = *reinterpret_cast<const float4*>(state(v) + 4 * 32);
+        st.m[0] = fmaxf(st.m[0], ml[v].x);
+        st.m[1] = fmaxf(st.m[1], ml[v].y);
+      }
 #pragma unroll
-        for (int v = 0; v < kGroups; ++v) {
-          const float w0 = ml[v].z * Kv4Slices::factor(ml[v].x, st.m[0]);
-          const float w1 = ml[v].w * Kv4Slices::factor(ml[v].y, st.m[1]);
-          st.l[0] += w0;
-          st.l[1] += w1;
-          const uint4 h4 = state(v)[e * 32];
-          const uint32_t hw[4] = {h4.x, h4.y, h4.z, h4.w};
+      for (int v = 0; v < kGroups; ++v) {
+        const float w0 = ml[v].z * Kv4Slices::factor(ml[v].x, st.m[0]);
+        const float w1 = ml[v].w * Kv4Slices::factor(ml[v].y, st.m[1]);
+        st.l[0] += w0;
+        st.l[1] += w1;
+        const uint4 h4 = state(v)[e * 32];
+        const uint32_t hw[4] = {h4.x, h4.y, h4.z, h4.w};
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const float2 o = __half22float2(*reinterpret_cast<const __half2*>(&hw[y]));
-            st.acc[y >> 1][2 * (y & 1)] += o.x * w0;
-            st.acc[y >> 1][2 * (y & 1) + 1] += o.y * w1;
-          }
-        }
-        if (t == T - 1) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar_dfree + 8 * buf);  // the buffer is free
-        }
-        if (fl & kFlagWhole) {
-          st.write(p, b, t, h, e, lane);
-        } else {
-          st.store(p.ws + ((int64_t)slot * T + t) * kKv4PartFloat4 + lane, e);
+        for (int y = 0; y < 4; ++y) {
+          const float2 o = __half22float2(*reinterpret_cast<const __half2*>(&hw[y]));
+          st.acc[y >> 1][2 * (y & 1)] += o.x * w0;
+          st.acc[y >> 1][2 * (y & 1) + 1] += o.y * w1;
         }
       }
-      if (!kOneToken || (fl & kFlagWhole)) continue;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_dfree + 8 * buf);  // the buffer is free
+      if (fl & kFlagWhole) {
+        st.write(p, b, h, e, lane);
+        continue;
+      }
+      st.store(p.ws + (int64_t)slot * kKv4PartFloat4 + lane, e);
       // The piece of a split pair counts itself; the last one of a pair joins the states
       // in the owners' order. More than kFan pieces are joined in groups of kFan first,
       // each by its last piece, so that no one reads more than a few dozen states. One
@@ -546,11 +510,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         named_bar_sync(2, kEpilogueWarps * 32);
         if (!*s_last) break;
-        Kv4Slices st;
         st.clear();
         st.join(count, e, [&](int i) { return place(at + i * step); });
         if (last_level) {
-          st.write(p, b, 0, h, e, lane);
+          st.write(p, b, h, e, lane);
           break;
         }
         // (every warp has read the leader's state where it overwrites it: its own slices and,
@@ -566,15 +529,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // sequences without tiles (or a step that cannot be): out = 0, lse = -inf
     for (int b = (int)blockIdx.x * kEpilogueWarps + e; b < B; b += G * kEpilogueWarps) {
       if (!*s_bad && cu[b + 1] != cu[b]) continue;
-      for (int t = 0; t < T; ++t)
-        for (int x = lane; x < (int)H * kGroup; x += 32) {
-          uint4* o = reinterpret_cast<uint4*>(p.out + (int64_t)b * p.o_sb + (int64_t)t * p.o_st +
-                                              (int64_t)x * p.o_sh);
+      for (int x = lane; x < (int)H * kGroup; x += 32) {
+        uint4* o = reinterpret_cast<uint4*>(p.out + (int64_t)b * p.o_sb + (int64_t)x * p.o_sh);
 #pragma unroll
-          for (int i = 0; i < kHeadDim / 8; ++i) o[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (p.lse)
-            p.lse[(int64_t)b * p.l_sb + (int64_t)t * p.l_st + (int64_t)x * p.l_sh] = -INFINITY;
-        }
+        for (int i = 0; i < kHeadDim / 8; ++i) o[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (p.lse) p.lse[(int64_t)b * p.l_sb + (int64_t)x * p.l_sh] = -INFINITY;
+      }
     }
     named_bar_sync(3, kThreads);
     return;
@@ -582,14 +542,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   regs_inc<C::kRegsConsumer>();
   // -------------------------------------------------------------- consumers
-  // Groups of NP warps take the CTA's units in turn, each warp for its own tokens, whatever
-  // pieces they belong to: a group's units come to its own slots in its own order, so the
-  // parities of its waits are exact. At a piece's end every warp deposits its states; warps
-  // wait for each other only at the deposit buffers.
-  const int slice = warp % NP, grp = warp / NP;
-  uint32_t slot = (uint32_t)grp, phase = 0;  // of the group's next unit
+  // The warps take the CTA's units in turn, whatever pieces they belong to: a warp's units
+  // come to its own slots in its own order, so the parities of its waits are exact. At a
+  // piece's end every warp deposits its state; warps wait for each other only at the deposit
+  // buffers.
+  uint32_t slot = (uint32_t)warp, phase = 0;  // of the warp's next unit
   bool dead = false;
-  for (int j = 0; warp < C::kActive; ++j) {
+  for (int j = 0;; ++j) {
     const int qs = j % kPieceQ, buf = j % C::kBufs;
     if (!wait_phase(bar_pfull + 8 * qs, (j / kPieceQ) & 1u, abort_flag, p.err, book_ns, false))
       break;  // no descriptor arrived: the producer is gone
@@ -597,30 +556,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int b = d[0], t0 = d[2], t1 = d[3], fl = d[4], rot = d[6];
     if (fl & kFlagEnd) break;
     const int n = t1 - t0;
-    const int i0 = grp >= rot ? grp - rot : grp - rot + kGroups;  // this group's first unit
-    float m[TW][2], l[TW][2], acc[TW][8][4];
+    const int i0 = warp >= rot ? warp - rot : warp - rot + kGroups;  // this warp's first unit
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, acc[8][4];
 #pragma unroll
-    for (int t = 0; t < TW; ++t) {
-      m[t][0] = m[t][1] = -INFINITY;
-      l[t][0] = l[t][1] = 0.f;
-#pragma unroll
-      for (int dm = 0; dm < 8; ++dm)
-        acc[t][dm][0] = acc[t][dm][1] = acc[t][dm][2] = acc[t][dm][3] = 0.f;
-    }
-    uint32_t qf[TW][8][2];
-    float sl2[TW];
+    for (int dm = 0; dm < 8; ++dm) acc[dm][0] = acc[dm][1] = acc[dm][2] = acc[dm][3] = 0.f;
+    uint32_t qf[8][2];
+    float sl2 = 0.f;
     int len = 0;
     if (i0 < n) {
       len = __ldg(p.seq_lens + b);
-#pragma unroll
-      for (int t = 0; t < TW; ++t) {
-        // (a warp's second token past the last one repeats it, and is not written)
-        const int tok = TW * slice + t < T ? TW * slice + t : T - 1;
-        const float qinv = load_q4(
-            smem_base + C::kQOff + qs * C::kQBytes + tok * (kGroup * kQRow), lane, qf[t]);
-        // (a factor of 0 would make NaN of masked scores, an infinite one of scores of 0)
-        sl2[t] = fminf(fmaxf(p.score_scale_log2 * qinv, FLT_MIN), FLT_MAX);
-      }
+      const float qinv = load_q4(smem_base + C::kQOff + qs * C::kQBytes, lane, qf);
+      // (a factor of 0 would make NaN of masked scores, an infinite one of scores of 0)
+      sl2 = fminf(fmaxf(p.score_scale_log2 * qinv, FLT_MIN), FLT_MAX);
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(bar_pfree + 8 * qs);  // this warp has read the descriptor and q
@@ -631,14 +578,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!dead) {
         const int stored = len - (t0 + i) * kBlockTokens;
-        int seen[TW];
-#pragma unroll
-        for (int t = 0; t < TW; ++t)  // (the warp's tokens do not see the last ones)
-          seen[t] = stored - (TW * slice + t < T ? T - 1 - TW * slice - t : 0);
-        if (seen[TW - 1] > 0) {
-          const uint32_t kb = smem_base + slot * kStage;
-          compute_unit4<TW>(kb, kb + kKv4Tile, qf, seen, stored, sl2, m, l, acc, lane);
-        }
+        const uint32_t kb = smem_base + slot * kStage;
+        compute_unit4(kb, kb + kKv4Tile, qf, stored, sl2, m, l, acc, lane);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_empty + 8 * slot);
       }
@@ -650,42 +591,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // row sums over the 8 lanes sharing a query-head pair
 #pragma unroll
-    for (int t = 0; t < TW; ++t)
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) {
-        l[t][0] += __shfl_xor_sync(0xffffffffu, l[t][0], o);
-        l[t][1] += __shfl_xor_sync(0xffffffffu, l[t][1], o);
-      }
+    for (int o = 4; o < 32; o <<= 1) {
+      l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
+      l[1] += __shfl_xor_sync(0xffffffffu, l[1], o);
+    }
     // deposit once the epilogue has read the buffer's previous states: o = acc / l in f16
     // (2^-11; |o| is at most the largest |code * scale|, 2688), m and l in fp32
     wait_phase(bar_dfree + 8 * buf, ((j / C::kBufs) & 1u) ^ 1u, abort_flag, p.err, book_ns, false);
     uint4* dep = dep0 + buf * (C::kDepBytes / 16);
+    const float v0 = l[0] == 0.f ? 0.f : __fdividef(1.f, l[0]);
+    const float v1 = l[1] == 0.f ? 0.f : __fdividef(1.f, l[1]);
+    uint4* dw = dep + warp * (kDepVec * 32) + lane;
 #pragma unroll
-    for (int t = 0; t < TW; ++t) {
-      const float v0 = l[t][0] == 0.f ? 0.f : __fdividef(1.f, l[t][0]);
-      const float v1 = l[t][1] == 0.f ? 0.f : __fdividef(1.f, l[t][1]);
-      uint4* dw = dep + ((warp * TW + t) * kDepVec) * 32 + lane;
-#pragma unroll
-      for (int k = 0; k < 4; ++k)  // slices 2k, 2k + 1
-        dw[k * 32] = make_uint4(pack_f16(acc[t][2 * k][0] * v0, acc[t][2 * k][1] * v1),
-                                pack_f16(acc[t][2 * k][2] * v0, acc[t][2 * k][3] * v1),
-                                pack_f16(acc[t][2 * k + 1][0] * v0, acc[t][2 * k + 1][1] * v1),
-                                pack_f16(acc[t][2 * k + 1][2] * v0, acc[t][2 * k + 1][3] * v1));
-      reinterpret_cast<float4*>(dw)[4 * 32] = make_float4(m[t][0], m[t][1], l[t][0], l[t][1]);
-    }
+    for (int k = 0; k < 4; ++k)  // slices 2k, 2k + 1
+      dw[k * 32] = make_uint4(
+          pack_f16(acc[2 * k][0] * v0, acc[2 * k][1] * v1), pack_f16(acc[2 * k][2] * v0, acc[2 * k][3] * v1),
+          pack_f16(acc[2 * k + 1][0] * v0, acc[2 * k + 1][1] * v1),
+          pack_f16(acc[2 * k + 1][2] * v0, acc[2 * k + 1][3] * v1));
+    reinterpret_cast<float4*>(dw)[4 * 32] = make_float4(m[0], m[1], l[0], l[1]);
     __syncwarp();
     if (lane == 0) mbar_arrive(bar_dfull + 8 * buf);  // release to the epilogue
   }
   named_bar_sync(3, kThreads);  // see the producer's exit
 }
 
-template <int TW, int NP>
-cudaError_t launch_cfg(const Kv4DecodeParams& p, int grid, cudaStream_t stream) {
-  using C = Cfg<TW, NP>;
-  auto kern = kv4_decode_kernel<TW, NP>;
+}  // namespace
+
+cudaError_t launch_kv4_decode(const Kv4DecodeParams& p, int grid, cudaStream_t stream) {
+  using C = Cfg;
+  if (p.num_seqs > kKv4MaxSeqs || p.q_len != 1) return cudaErrorInvalidValue;
   static std::atomic<uint64_t> configured{0};
   cudaError_t e = once_per_device(configured, [&] {
-    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(kv4_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 C::kSmemBytesMax);
   });
   if (e != cudaSuccess) return e;
@@ -699,19 +636,7 @@ cudaError_t launch_cfg(const Kv4DecodeParams& p, int grid, cudaStream_t stream) 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, p);
-}
-
-}  // namespace
-
-cudaError_t launch_kv4_decode(const Kv4DecodeParams& p, int grid, cudaStream_t stream) {
-  if (p.num_seqs > kKv4MaxSeqs) return cudaErrorInvalidValue;
-  switch ((p.q_len + 1) / 2) {
-    case 1: return p.q_len == 1 ? launch_cfg<1, 1>(p, grid, stream) : launch_cfg<2, 1>(p, grid, stream);
-    case 2: return launch_cfg<2, 2>(p, grid, stream);
-    case 3: return launch_cfg<2, 3>(p, grid, stream);
-    default: return launch_cfg<2, 4>(p, grid, stream);
-  }
+  return cudaLaunchKernelEx(&cfg, kv4_decode_kernel, p);
 }
 
 }  // namespace hpc

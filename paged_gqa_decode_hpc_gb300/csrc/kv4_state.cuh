@@ -1,4 +1,4 @@
-// A quarter of a softmax state, as the 4-bit decode kernels store and join it. A state is
+// A quarter of a softmax state, as the 4-bit decode kernel stores and joins it. A state is
 // one token's 8 query heads of one KV head in a warp's lanes: lane (g, c) has query heads
 // 2c and 2c + 1 at elements 16 g .. 16 g + 15 of the head, as eight slices of two elements,
 // and both heads' maximum and sum. Quarter e is slices 2e and 2e + 1. Stored, a state is
@@ -96,20 +96,19 @@ struct Kv4Slices {
     }
   }
 
-  // out = acc * v_scale / l and lse of token t of pair (b, h); 0 and -inf where nothing was seen
-  __device__ __forceinline__ void write(const Kv4DecodeParams& p, int b, int t, int h, int e,
-                                        int lane) const {
+  // out = acc * v_scale / l and lse of pair (b, h); 0 and -inf where nothing was seen
+  __device__ __forceinline__ void write(const Kv4DecodeParams& p, int b, int h, int e, int lane) const {
     const int g = lane >> 2, c = lane & 3;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int j = 8 * h + 2 * c + x;
       const float inv = l[x] == 0.f ? 0.f : p.v_scale / l[x];
-      uint2* o = reinterpret_cast<uint2*>(p.out + (int64_t)b * p.o_sb + (int64_t)t * p.o_st +
-                                          (int64_t)j * p.o_sh + 16 * g + 4 * e);
+      uint2* o = reinterpret_cast<uint2*>(p.out + (int64_t)b * p.o_sb + (int64_t)j * p.o_sh +
+                                          16 * g + 4 * e);
       *o = make_uint2(pack_bf16(acc[0][x] * inv, acc[0][2 + x] * inv),
                       pack_bf16(acc[1][x] * inv, acc[1][2 + x] * inv));
       if (e == 0 && g == 0 && p.lse)
-        p.lse[(int64_t)b * p.l_sb + (int64_t)t * p.l_st + (int64_t)j * p.l_sh] =
+        p.lse[(int64_t)b * p.l_sb + (int64_t)j * p.l_sh] =
             l[x] == 0.f ? -INFINITY : (m[x] + __log2f(l[x])) * 0.6931471805599453f;
     }
   }

@@ -46,11 +46,10 @@ constexpr uint32_t kPBuf = 128 * 128;       // P^T of a step: 128 rows (tokens) 
 constexpr uint32_t kColK = 0, kColS = 128, kColO = 384, kTmemCols = 512;
 constexpr float kPassed = 8.f;              // log2 units by which a score may pass its reference
 
-// COLS: query rows that are computed (8, 16, 32, 48 or 64), of the MMAs' N.
+// COLS: query rows that are computed (16, 32, 48 or 64), the MMAs' N.
 template <int COLS>
 struct Cfg {
-  static constexpr int kN = COLS < 16 ? 16 : COLS;
-  static constexpr uint32_t kQHalf = kN * 128, kQBuf = 2 * kQHalf;  // rows of 64 elements each
+  static constexpr uint32_t kQHalf = COLS * 128, kQBuf = 2 * kQHalf;  // rows of 64 elements each
   static constexpr uint32_t kOffV = 0;
   static constexpr uint32_t kOffP = kOffV + kVBufs * kVTile;
   static constexpr uint32_t kOffQ = kOffP + 2 * kPBuf;
@@ -64,8 +63,9 @@ struct Cfg {
   static constexpr int kNumBars = 2 * kStages + 2 * kPieceQ + 16 + 8 + 2;
   static constexpr uint32_t kOffDesc = kOffBar + (8 * kNumBars + 15) / 16 * 16;
   static constexpr uint32_t kOffFloat = kOffDesc + kPieceQ * 32;
-  // references (true, used), factors, 1 / sums, row maxima or sums of four warps; q's factors
-  static constexpr uint32_t kFloats = 64 * (4 + 4) + 8;
+  // references (true, used), factors, 1 / sums, row maxima or sums of four warps; q's factors of
+  // four pieces
+  static constexpr uint32_t kFloats = 64 * (4 + 4 + 4);
   static constexpr uint32_t kOffMisc = kOffFloat + 4 * kFloats;
   static constexpr uint32_t kOffPlan = kOffMisc + 256;
   static constexpr uint32_t kSmemBytes = 1024 /* alignment slack */ + kOffPlan;
@@ -104,34 +104,26 @@ __device__ __forceinline__ void tmem_st8(uint32_t a, const float* v) {
                "r"(r[7])
                : "memory");
 }
-// Floats as integers of the same order (NaN beyond the infinities).
-__device__ __forceinline__ int ordered(float x) {
-  const int i = __float_as_int(x);
-  return i ^ ((i >> 31) & 0x7FFFFFFF);
-}
-__device__ __forceinline__ float from_ordered(int i) {
-  return __int_as_float(i ^ ((i >> 31) & 0x7FFFFFFF));
-}
-
-// Sums of l[0 .. N) over the warp's lanes, for rows `at` on: each exchange halves the rows that
-// a lane goes on with, while they are even.
-template <int W, int N, int COLS>
-__device__ __forceinline__ void sum_rows(float (&l)[COLS], int at, float* sums, int lane) {
+// Sums (or maxima) of l[0 .. N) over the warp's lanes, for rows `at` on, to out[]: each exchange
+// halves the rows that a lane goes on with, while they are even.
+template <bool MAX, int W, int N, int COLS>
+__device__ __forceinline__ void reduce_rows(float (&l)[COLS], int at, float* out, int lane) {
+  auto join = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
   if constexpr (W == 0) {
 #pragma unroll
-    for (int c = 0; c < N; ++c) sums[at + c] = l[c];
+    for (int c = 0; c < N; ++c) out[at + c] = l[c];
   } else if constexpr (N % 2 == 0) {
     const bool up = (lane & W) != 0;
 #pragma unroll
     for (int c = 0; c < N / 2; ++c) {
       const float give = up ? l[c] : l[c + N / 2];
-      l[c] = (up ? l[c + N / 2] : l[c]) + __shfl_xor_sync(0xffffffffu, give, W);
+      l[c] = join(up ? l[c + N / 2] : l[c], __shfl_xor_sync(0xffffffffu, give, W));
     }
-    sum_rows<W / 2, N / 2>(l, up ? at + N / 2 : at, sums, lane);
+    reduce_rows<MAX, W / 2, N / 2>(l, up ? at + N / 2 : at, out, lane);
   } else {
 #pragma unroll
-    for (int c = 0; c < N; ++c) l[c] += __shfl_xor_sync(0xffffffffu, l[c], W);
-    sum_rows<W / 2, N>(l, at, sums, lane);
+    for (int c = 0; c < N; ++c) l[c] = join(l[c], __shfl_xor_sync(0xffffffffu, l[c], W));
+    reduce_rows<MAX, W / 2, N>(l, at, out, lane);
   }
 }
 
@@ -139,7 +131,7 @@ template <int COLS>
 __global__ void __launch_bounds__(kThreads, 1)
     kv4_tc_kernel(const __grid_constant__ Kv4DecodeParams p, const __grid_constant__ CUtensorMap tmq) {
   using C = Cfg<COLS>;
-  constexpr int R = C::kStages, kN = C::kN;
+  constexpr int R = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -164,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t drain = b4 + 8u * 8;
   const int4* desc = reinterpret_cast<const int4*>(smem + C::kOffDesc);
   float* fl = reinterpret_cast<float*>(smem + C::kOffFloat);
-  float* s_qinv = fl + 64 * 8;  // [4], then scratch
+  float* s_qfac = fl + 64 * 8;  // [4][64] of log2 of a score, by row of q
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc);
   volatile int* s_bad = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::kOffMisc + 16);
@@ -189,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < kPieceQ; ++s) {
       mbar_init(pfull(s), 1);
       mbar_init(pfree(s), kPieceReaders);
-      mbar_init(q_full(s), 32);
+      mbar_init(q_full(s), 128);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(k_full(i), 128);
@@ -213,6 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // rows of q's operand that no query row fills stay 0
   for (uint32_t i = tid; i < 2 * C::kQBuf / 16; i += kThreads)
     reinterpret_cast<uint4*>(smem + C::kOffQ)[i] = make_uint4(0u, 0u, 0u, 0u);
+  if (tid < 4 * 64) s_qfac[tid] = 0.f;
   tc05::fence_async_shared();
   tc05::tc_fence_before();
   griddep_wait();
@@ -313,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t step = 0;
       Desc d;
       if (warp == kScoreWarp) {
-        constexpr uint32_t kIdS = tc05::idesc_f16_f32(128, kN, false, false);
+        constexpr uint32_t kIdS = tc05::idesc_f16_f32(128, COLS, false, false);
         const uint64_t qd = tc05::smem_desc_sw128(base + C::kOffQ, 16, 1024);
         for (int j = 0; ok && piece(j, d); ++j) {
           const int steps = (d.n + 1) / 2;
@@ -339,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       } else {
-        constexpr uint32_t kIdO = tc05::idesc_f16_f32(128, kN, true, true);
+        constexpr uint32_t kIdO = tc05::idesc_f16_f32(128, COLS, true, true);
         const uint64_t vd = tc05::smem_desc_sw128(base + C::kOffV, kVTile / 2, 1024);
         const uint64_t pd = tc05::smem_desc_sw128(base + C::kOffP, 16, 1024);
         for (int j = 0; ok && piece(j, d); ++j) {
@@ -381,73 +374,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return;
     }
-    // ------------------------------------------------------- q to f16
-    // A thread is one or two query rows of the piece, each in place, with one power of two
-    // for all rows that puts the largest element in [2^14, 2^15). Elementwise, so that the
-    // swizzled order of a row's chunks does not matter.
+    // ------------------------------------------------------ copies of q
     Desc d = {};
-    bool ok = true;
-    for (int j = 0; ok && piece(j, d); ++j) {
+    int q_pieces = 0;
+    for (int j = 0; piece(j, d); ++j) {
       const int i = j & 1;
       // once the MMAs on the buffer's previous rows are done
-      ok = j < 2 || wait(q_free(i), (j >> 1) - 1);
-      if (!ok || p.withhold_copies) break;
+      if (j >= 2 && !wait(q_free(i), (j >> 1) - 1)) break;
+      if (p.withhold_copies) break;
       if (lane == 0) {
         mbar_arrive_expect_tx(q_landed(i), (uint32_t)(T * kGroup * kHeadDim * 2));
         const uint32_t dq = base + C::kOffQ + i * C::kQBuf;
         tc05::tma_load_4d(dq, &tmq, q_landed(i), 0, d.h * kGroup, 0, d.b);
         tc05::tma_load_4d(dq + C::kQHalf, &tmq, q_landed(i), 64, d.h * kGroup, 0, d.b);
       }
-      ok = wait(q_landed(i), j >> 1);
-      if (!ok) {  // the rows may still be landing
-        if (lane == 0)
-          wait_phase(q_landed(i), (j >> 1) & 1u, abort_flag, p.err, 1000000000ull, false);
-        break;
-      }
-      // chunks of 16 bytes: 16 to a row, in the order in which they lie (all of them below
-      // the swizzle, the two halves one after the other)
-      uint8_t* qb = smem + C::kOffQ + i * C::kQBuf;
-      const int chunks = T * kGroup * 8;  // of a half
-      float mx = 0.f;
-#pragma unroll 1
-      for (int hf = 0; hf < 2; ++hf)
-#pragma unroll 4
-        for (int c = lane; c < chunks; c += 32) {
-          const uint4 x = *reinterpret_cast<const uint4*>(qb + hf * C::kQHalf + 16 * c);
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[e] << 16)),
-                                 fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
-        }
-      mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
-      int e = 0;
-      if (mx > 0.f) {
-        e = 14 - ((int)((__float_as_uint(mx) >> 23) & 0xFF) - 127);
-        e = e < -113 ? -113 : (e > 100 ? 100 : e);
-      }
-      const float sc = __uint_as_float((uint32_t)(e + 127) << 23);
-#pragma unroll 1
-      for (int hf = 0; hf < 2; ++hf)
-#pragma unroll 4
-        for (int c = lane; c < chunks; c += 32) {
-          uint4* at = reinterpret_cast<uint4*>(qb + hf * C::kQHalf + 16 * c);
-          const uint4 x = *at;
-          uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int y = 0; y < 4; ++y)
-            w[y] = pack_f16(__uint_as_float(w[y] << 16) * sc,
-                            __uint_as_float(w[y] & 0xFFFF0000u) * sc);
-          *at = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-      // A factor of 0 would make NaN of masked scores, an infinite one of scores of 0. Four
-      // factors and barriers, as descriptors: the softmax may be behind by that many pieces.
-      if (lane == 0)
-        s_qinv[j & 3] = fminf(
-            fmaxf(p.score_scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23), FLT_MIN), FLT_MAX);
-      tc05::fence_async_shared();  // the MMAs read q through the async proxy
-      mbar_arrive(q_full(j & 3));
+      q_pieces = j + 1;
     }
+    // (rows that nobody waited for may still be landing)
+    for (int j = q_pieces > 2 ? q_pieces - 2 : 0; *abort_flag && lane == 0 && j < q_pieces; ++j)
+      wait_phase(q_landed(j & 1), (j >> 1) & 1u, abort_flag, p.err, 1000000000ull, false);
     named_bar_sync(3, kThreads);
     return;
   }
@@ -521,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= kKWarp0) {
     regs_dec<C::kRegsK>();
-    // --------------------------------------- K to f16, in tensor memory
+    // ------------------------ q to f16; K to f16, in tensor memory
     // A thread is a token of the step, its lane of tensor memory.
     const int row = tid - 32 * kKWarp0, tile = row >> 6;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -529,6 +474,44 @@ __global__ void __launch_bounds__(kThreads, 1)
     Desc d;
     bool ok = true;
     for (int j = 0; ok && piece(j, d); ++j) {
+      // The piece's query rows, in place: eight threads a row, 16 bytes of each half to a
+      // thread in the order in which they lie (below the swizzle). A power of two of the row's
+      // own puts its largest element in [2^14, 2^15).
+      if (!(ok = wait(q_landed(j & 1), j >> 1))) break;
+#pragma unroll
+      for (int r = row >> 3; r < T * kGroup; r += 16) {
+        uint4* at = reinterpret_cast<uint4*>(smem + C::kOffQ + (j & 1) * C::kQBuf) + r * 8 + (row & 7);
+        uint4 w[2] = {at[0], at[C::kQHalf / 16]};
+        uint32_t big = 0;  // the largest bf16 without its sign, as an integer
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const uint32_t x[4] = {w[y].x, w[y].y, w[y].z, w[y].w};
+#pragma unroll
+          for (int z = 0; z < 4; ++z) big = max(big, max(x[z] & 0x7FFF0000u, (x[z] & 0x7FFFu) << 16));
+        }
+        const uint32_t eight = 0xFFu << (lane & 24);
+        big = __reduce_max_sync(eight, big);
+        int e = 0;
+        if (big > 0) {
+          e = 14 - ((int)(big >> 23) - 127);
+          e = e < -113 ? -113 : (e > 100 ? 100 : e);
+        }
+        const float sc = __uint_as_float((uint32_t)(e + 127) << 23);
+        auto scaled = [&](uint32_t x) {
+          return pack_f16(__uint_as_float(x << 16) * sc, __uint_as_float(x & 0xFFFF0000u) * sc);
+        };
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+          at[y * (C::kQHalf / 16)] = make_uint4(scaled(w[y].x), scaled(w[y].y), scaled(w[y].z), scaled(w[y].w));
+        // A factor of 0 would make NaN of masked scores, an infinite one of scores of 0. Four
+        // sets of factors and barriers, as descriptors: the softmax may be behind by that many
+        // pieces.
+        if ((row & 7) == 0)
+          s_qfac[(j & 3) * 64 + r] = fminf(
+              fmaxf(p.score_scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23), FLT_MIN), FLT_MAX);
+      }
+      tc05::fence_async_shared();  // the MMAs read q through the async proxy
+      mbar_arrive(q_full(j & 3));
       const int steps = (d.n + 1) / 2;
       for (int k = 0; ok && k < steps; ++k, ++step) {
         const uint32_t i = step & 1, u = d.g0 + 2 * k + tile, slot = u % R;
@@ -598,8 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok) ok = wait(q_full(j & 3), j >> 2);
     if (any_of(bar, 128, !ok)) break;
     const int steps = (d.n + 1) / 2;
-    const float sl2 = s_qinv[j & 3];
-    hand_back(j);
+    const float* fac = s_qfac + (j & 3) * 64 + c0;
     float l[N];
 #pragma unroll
     for (int c = 0; c < N; ++c) l[c] = 0.f;
@@ -629,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       auto less_reference = [&] {
 #pragma unroll
-        for (int c = 0; c < N; ++c) s[c] = fmaf(s[c], sl2, -s_ref[c]);
+        for (int c = 0; c < N; ++c) s[c] = fmaf(s[c], fac[c], -s_ref[c]);
       };
       scores();
       bool passed = k == 0;
@@ -647,16 +629,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // references: the rows' maxima over the step, of each warp and then of all
         if (k > 0) scores();
-#pragma unroll
-        for (int c = 0; c < N; ++c) {
-          const int m = __reduce_max_sync(0xffffffffu, ordered(s[c]));
-          if (lane == (c & 31)) s_part[(warp & 3) * 64 + c] = from_ordered(m);
-        }
+        reduce_rows<true, 16, N>(s, 0, s_part + (warp & 3) * 64, lane);
         named_bar_sync(bar, 128);
         if (row < N) {
           const float old = k == 0 ? -INFINITY : s_true[row];
           const float mx = fmaxf(fmaxf(s_part[row], s_part[64 + row]),
-                                 fmaxf(s_part[128 + row], s_part[192 + row])) * sl2;
+                                 fmaxf(s_part[128 + row], s_part[192 + row])) * fac[row];
           const float now = fmaxf(old, mx);
           s_true[row] = now;
           s_ref[row] = now == -INFINITY ? 0.f : now;
@@ -684,6 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c = 0; c < N; ++c) l[c] *= s_alpha[c];
         }
+        scores();
         less_reference();
       }
       const uint32_t prow = base + C::kOffP + i * kPBuf + row * 128;
@@ -707,9 +686,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(s_free(step & 3));
     }
+    hand_back(j);     // (q's factors were read until here)
     if (!ok) break;  // (of all, see above)
     // ---- the piece's end: sums over the tokens (each lane ends with some of the rows)
-    sum_rows<16, N>(l, 0, s_part + (warp & 3) * 64, lane);
+    reduce_rows<false, 16, N>(l, 0, s_part + (warp & 3) * 64, lane);
     named_bar_sync(bar, 128);
     const int mine = c0 + row;  // a query row
     if (row < N && mine < T * kGroup) {
