@@ -741,7 +741,7 @@ hpc_status hpc_rope_kv4_write(const hpc_tensor* q_in, const hpc_tensor* k_in,
  * hpc_decode_kv4_plan_create -- a plan for hpc_decode_kv4_attn: counters, partial states
  * and error word of steps of at most max_seqs (<= 4096) sequences with max_q_len (1 .. 8)
  * new tokens each and num_q_heads (<= 512) query heads, on num_sms CTAs (normally the SM
- * count). All device memory is allocated here: 46 KB a CTA and token. The device
+ * count). All device memory is allocated here: 9.2 KB a CTA and token. The device
  * is the current one. hpc_decode_plan_status and hpc_decode_plan_destroy take the plan; the
  * other calls refuse it. Calls on one plan must not overlap on the GPU (graphs that share
  * one included).
@@ -760,8 +760,9 @@ hpc_status hpc_decode_kv4_plan_create(int32_t max_seqs, int32_t max_q_len, int32
  *   k_cache, v_cache  4-bit caches with H_q == 8 * H_kv
  *   block_table  device int32 [B][max_blocks], rows contiguous
  *   seq_lens     device int32 [B]; a negative length, a sequence of more than INT32_MAX /
- *                512 (tile, KV head) units, or more than INT32_MAX units in all set
- *                HPC_DEVCHK_BAD_LENGTH and the step writes out = 0, lse = -inf throughout
+ *                1024 (tile, KV head) units, or more than INT32_MAX units in all (four more
+ *                counted for each sequence and KV head) set HPC_DEVCHK_BAD_LENGTH and the
+ *                step writes out = 0, lse = -inf throughout
  *   plan         from hpc_decode_kv4_plan_create, for at least this step's sequences, new
  *                tokens and heads, on the current device
  *   out          device bf16, q's shape and rules (written). Its rows may not overlap each
@@ -770,11 +771,13 @@ hpc_status hpc_decode_kv4_plan_create(int32_t max_seqs, int32_t max_q_len, int32
  *   softmax_scale  > 0, or <= 0 for 1/sqrt(128)
  * Cache slots past a sequence's end may hold anything; a NaN scale before it spoils the
  * tokens that see it (K) or all of the sequence's (V, from the tile that holds it on).
- * Codes times scales, and q (from bf16, by a power of two for each KV head's 8 rows: what is
- * 2^-29 of their largest element, or less, may lose bits), are exact in f16; probabilities
- * are rounded to f16 (2^-11 of each, and at least 2^-25 of the row's largest); sums,
- * maxima and states are fp32. The states of the warps that share a piece of a sequence are
- * handed over with o in f16 (2^-11, and 2^-25 ts absolute). A token that sees no position gets out
+ * Codes times scales, and q (from bf16, by a power of two: what is 2^-29 of the largest
+ * element, or less, may lose bits), are exact in f16; the power of two is one for the 8 rows
+ * of a KV head where q_len is 1 (a row that is not finite spoils the other seven), each row's
+ * own where it is more. Probabilities are rounded to f16 (2^-11 of each, and at least 2^-25
+ * of the row's largest); sums, maxima and states are fp32. With q_len 1 the states of the
+ * warps that share a piece of a sequence are handed over with o in f16 (2^-11, and 2^-25 ts
+ * absolute). A token that sees no position gets out
  * = 0, lse = -inf. Bad block ids read zeros and set HPC_DEVCHK_BAD_BLOCK. Results do not
  * depend on timing: equal steps give equal bits. Allocates nothing; may be captured in a
  * CUDA graph after a first call outside the capture.

@@ -1,5 +1,6 @@
 // C ABI of the attention calls over a 4-bit cache (the write is in capi_cache.cu).
 // See include/hpc_decode.h for the contract of every call.
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstring>
@@ -67,6 +68,21 @@ bool ranges_meet(const hpc_tensor* x, int64_t a, const hpc_tensor* y, int64_t b)
   return (const char*)x->data < end(y, b) && (const char*)y->data < end(x, a);
 }
 
+// Whether the first n dimensions of t, over pieces of `inner` elements, lie inside each other
+// in some order: then no two pieces meet.
+bool nested(const hpc_tensor* t, int n, int64_t inner) {
+  int order[4] = {0, 1, 2, 3};
+  std::sort(order, order + n, [&](int a, int b) { return t->stride[a] < t->stride[b]; });
+  int64_t extent = inner;
+  for (int i = 0; i < n; ++i) {
+    const int64_t size = t->shape[order[i]], stride = t->stride[order[i]];
+    if (size <= 1) continue;
+    if (stride < extent) return false;
+    extent += (size - 1) * stride;
+  }
+  return true;
+}
+
 // out's rows are written while other CTAs read q, in no order: they may not share bytes
 // with q's, with each other or with lse.
 hpc_status check_overlap(const hpc_tensor* q, const hpc_tensor* out, const hpc_tensor* lse,
@@ -85,16 +101,14 @@ hpc_status check_overlap(const hpc_tensor* q, const hpc_tensor* out, const hpc_t
   };
   bool fq, fo;
   const Rows rq = rows(q, &fq), ro = rows(out, &fo);
-  if (fo ? rows_overlap(ro, ro, true)
-         : out->stride[1] < (out->shape[2] - 1) * out->stride[2] + kHeadDim ||
-               out->stride[2] < kHeadDim ||
-               out->stride[0] < (out->shape[1] - 1) * out->stride[1] +
-                                    (out->shape[2] - 1) * out->stride[2] + kHeadDim)
+  if (fo ? rows_overlap(ro, ro, true) : !nested(out, out->ndim - 1, kHeadDim))
     return fail(HPC_ERR_INVALID_ARG, "rows of out overlap");
   if (fq && fo ? rows_overlap(ro, rq) : ranges_meet(out, 2, q, 2))
     return fail(HPC_ERR_INVALID_ARG, "out overlaps q");
   if (has_lse && (ranges_meet(lse, 4, q, 2) || ranges_meet(lse, 4, out, 2)))
     return fail(HPC_ERR_INVALID_ARG, "lse overlaps q or out");
+  if (has_lse && !nested(lse, lse->ndim, 1))
+    return fail(HPC_ERR_INVALID_ARG, "elements of lse overlap");
   return HPC_OK;
 }
 

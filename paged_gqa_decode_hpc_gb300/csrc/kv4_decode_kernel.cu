@@ -251,12 +251,15 @@ __device__ __forceinline__ void compute_unit4(uint32_t kb, uint32_t vb,
     }
   }
   // (a row that has seen no position yet: its scores are all -inf, its P is 0)
-  const float r0 = m[0] == -INFINITY ? 0.f : -m[0];
-  const float r1 = m[1] == -INFINITY ? 0.f : -m[1];
+  // (a product and a difference, not one FMA: the largest product has to give exactly 0, and
+  // what rounding took from a maximum of 2^30 is no small number)
+  const float r0 = m[0] == -INFINITY ? 0.f : m[0];
+  const float r1 = m[1] == -INFINITY ? 0.f : m[1];
+  auto less = [&](float x, float r) { return ex2(__fsub_rn(__fmul_rn(x, sl2), r)); };
 #pragma unroll
   for (int mt = 0; mt < 4; ++mt) {
-    const float e0 = ex2(fmaf(s[mt][0], sl2, r0)), e1 = ex2(fmaf(s[mt][1], sl2, r1));
-    const float e2 = ex2(fmaf(s[mt][2], sl2, r0)), e3 = ex2(fmaf(s[mt][3], sl2, r1));
+    const float e0 = less(s[mt][0], r0), e1 = less(s[mt][1], r1);
+    const float e2 = less(s[mt][2], r0), e3 = less(s[mt][3], r1);
     l[0] += e0 + e2;
     l[1] += e1 + e3;
     pb[mt][0] = movm_trans(pack_f16(e0, e1));

@@ -56,7 +56,7 @@ struct PartPlan {
 };
 
 // Units of a KV head ahead of each sequence, into cu[0 .. B] (cu[0] = 0 is there already);
-// *bad where the lengths cannot be. Called by all `threads` (at most 512) threads of the CTA
+// *bad where the lengths cannot be. Called by all `threads` (at most 1024) threads of the CTA
 // after a barrier. The warp `planner` plans small batches by itself; other warps may look at
 // the result only after they have waited for something that it did later.
 __device__ __forceinline__ void plan_step(const Kv4DecodeParams& p, int32_t* cu, volatile int* bad,
@@ -64,10 +64,10 @@ __device__ __forceinline__ void plan_step(const Kv4DecodeParams& p, int32_t* cu,
   const int B = p.num_seqs, tid = threadIdx.x, lane = tid & 31;
   const uint32_t H = (uint32_t)p.num_kv_heads;
   auto units_of = [&](int32_t len) -> int32_t {  // -1: cannot be
-    // more units than INT32_MAX / 512 are refused, so that no partial sum of a scan pass, of
-    // at most 512 sequences, wraps
+    // more units than INT32_MAX / 1024 are refused, so that no partial sum of a scan pass, of
+    // at most 1024 sequences, wraps
     const int64_t n = len > 0 ? ((int64_t)len + kBlockTokens - 1) / kBlockTokens + kPairCost : 0;
-    return len < 0 || n * H > (int64_t)(INT32_MAX / 512) ? -1 : (int32_t)n;
+    return len < 0 || n * H > (int64_t)(INT32_MAX / 1024) ? -1 : (int32_t)n;
   };
   if (B > kWarpPlan) {
     int64_t carry = 0;

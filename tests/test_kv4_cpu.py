@@ -174,3 +174,18 @@ def test_other_calls_refuse_the_rows(cache):
         with pytest.raises(hpc.HpcError) as e:
             call()
         assert e.value.status in (I, U)
+
+
+@pytest.mark.parametrize("kw,message", [
+    (dict(lse=torch.zeros(5, 1).expand(5, 16)), "lse overlap"), (dict(lse=torch.zeros(1, 16).expand(5, 16)), "lse overlap"),
+    (dict(lse=torch.zeros(200).as_strided((5, 16), (15, 1))), "lse overlap"), (dict(out=_bf(1, 16, 128).expand(5, 16, 128)), "out overlap")])
+def test_overlapping_results_are_refused(kw, message):
+    got = outcome(extend, kw)
+    assert got[2] == I and message in got[1]
+
+
+def test_results_in_other_orders_are_not_refused():
+    if torch.cuda.is_available():
+        pytest.skip("the CPU's tensors are refused where there is a device")
+    for kw in (dict(lse=torch.zeros(16, 5).T), dict(out=_bf(16, 5, 128).transpose(0, 1)), dict(lse=torch.zeros(5, 40)[:, 3:19])):
+        assert outcome(extend, kw)[2] == hpc.HPC_ERR_CUDA
