@@ -129,3 +129,19 @@ def test_free_memory_stays():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.cuda.mem_get_info()[0] == before
+
+
+def test_rows_of_very_different_sizes_in_a_prompt():
+    c = Paged([300, 70], hkv=1, q_rows=170, seed=46, q_scale=6.0, ks=0.5)
+    big = torch.rand(c.q.shape[:2], generator=torch.Generator().manual_seed(2)) < 0.3
+    c.q[big] = c.q[big] * 2.0 ** 70
+    d, cu = c.device(), cu_of([100, 70])
+    out, lse = torch.empty_like(d["q"]), torch.empty(170, 8, device="cuda")
+    hpc.hpc_extend_kv4_attn(d["q"], d["k"], d["v"], d["bt"], d["sl"], i32(cu), out, lse, k_scale=c.ks, v_scale=c.vs)
+    c.check(out, lse, cu)
+
+
+def test_one_token_with_large_scores():
+    """The maximum's probability is 1 whatever the scores' size (one power of two for the KV head's rows)."""
+    c = Paged([300, 70, 5000], hkv=2, q_rows=3, seed=47, q_scale=2.0 ** 70, ks=0.5)
+    c.check(*decode(c, 1), cu_of([1] * 3))
