@@ -1,11 +1,9 @@
-// Decode attention of several new tokens per sequence over a 4-bit paged cache on the
+// Decode attention of 2 to 8 new tokens per sequence over a 4-bit paged cache on the
 // 5th-generation tensor cores (tcgen05).
 //
 // The 8 q_len query rows of a KV head share every tile. With mma.sync the products alone
-// take 64 q_len MMAs of 8 issue cycles a unit (kv4_decode_kernel.cu), and every two tokens
-// their own conversion of the codes; here the codes of a unit are converted once and the
-// products cost no issue slots. What bounds it: HBM (9216 bytes a unit, 206 ns of an SM's
-// share of 6.8 TB/s) and next to it shared memory, which V's f16 operand passes twice.
+// take 64 q_len MMAs of 8 issue cycles a unit, and every two tokens their own conversion of the
+// codes; here the codes of a unit are converted once and the products cost no issue slots.
 //
 // Both products run with the wide side in M, so that few query rows cost little:
 //  * S^T[token, row] = K Q^T: M = 128 tokens (two tiles, a step), N = the query rows, K =
@@ -14,18 +12,31 @@
 //    words, so the 8-byte reads of 16 rows cover all banks once.
 //  * The softmax threads are tokens too: a row's maximum is over threads. They keep a
 //    reference per query row in shared memory, which moves only when some score passes it by
-//    8 (log2 units; a vote of the four warps), so that as a rule a thread subtracts, takes
-//    exponentials, adds its own sums and writes its row of P^T (f16) to shared memory.
+//    8 (log2 units; a vote of the group's four warps), so that as a rule a thread subtracts,
+//    takes exponentials, adds its own sums and writes its row of P^T (f16) to shared memory.
 //  * O^T[d, row] += V^T P^T: M = 128 elements, K = tokens. A = V as the MN-major operand of
 //    its converted tile, B = P^T, MN-major as written. O^T stays in tensor memory for a
 //    piece (a thread is an element d then) and is rescaled there when references move.
 // A piece's states go to memory as a whole (out, lse) or as partial states, which a second
 // kernel joins.
 //
-// Warps: 4 softmax (and the pieces' ends), 4 converters of K, 4 of V, the producer, the MMA
-// issuer and 2 that convert q to f16. Plan, ring and copies are kv4_plan.cuh's. Every wait is
-// bounded; after one has run out every role leaves, the MMAs are waited for and tensor memory
-// is freed.
+// Warps: two groups of 4 for the softmax (half of the rows each, and their ends of a piece), 4
+// that convert q and K, 8 for V (4 to a tile), and one each for the copies of K and V, the
+// issue of either product and the copies of q. Plan, ring and copies are kv4_plan.cuh's. Every
+// wait is bounded; after one has run out every role leaves, the MMAs are waited for and tensor
+// memory is freed.
+//
+// What bounds it (32 sequences of 4096 and one of 131072 positions, 8 KV heads; HBM's share is
+// 44 us, 780 clk a step): with 2 tokens 84 us, of which shared memory takes most (710
+// wavefronts a step for threads, 315 for the MMAs, 144 for the copies, of 1440 clk; V passes
+// twice). With 4 tokens 107 us and with 8 153 us: the chain from a step's scores to its
+// P^T, a fixed 1000 clk of waits, vote and fences and 25 to 30 clk a row of the group, on warps
+// that share the SM's issue (0.5 to 0.6 a cycle) with the conversions. What it took, 4 and 8
+// tokens: one softmax group and one warp for both products 151 and 203 us; two waits a step
+// in that warp and 8 warps for V 121 and 182; two groups, a warp for each product 102 and
+// 162. Groups that take alternate steps instead of rows were slower (118 and 214: their
+// states need more registers). A wait on two barriers takes half of the lanes each, one
+// latency instead of two: one after the other they cost 8 to 10 %.
 #include <cfloat>
 
 #include "kv4_plan.cuh"
@@ -240,9 +251,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto wait = [&](uint32_t bar, uint32_t parity) -> bool {  // a warp together
     return __all_sync(0xffffffffu, wait_phase(bar, parity & 1u, abort_flag, p.err, lim));
   };
-  // Two barriers (the second only if `also`): looked at by half of the lanes each, which costs
-  // one latency where both phases are there already. Else one after the other: a warp that
-  // waits at one barrier sleeps, at two it spins, and takes issue slots from the others.
+  // Two barriers (the second only if `also`), half of the lanes at each: one latency where both
+  // phases are there already. (A sleeping wait for one after the other was slower, see above.)
   auto wait2 = [&](uint32_t a, uint32_t pa, uint32_t b, uint32_t pb, bool also) -> bool {
     const bool second = also && (lane & 1);
     return wait(second ? b : a, second ? pb : pa);
