@@ -86,26 +86,34 @@ __device__ __forceinline__ void plan_step(const Kv4DecodeParams& p, int32_t* cu,
     if (tid == 0 && carry * H > INT32_MAX) *bad = 1;
     __syncthreads();
   } else if (planner) {
-    int32_t n[kWarpPlan / 32];
+    // A lane takes up to 8 neighbouring sequences. (No code for more of them than there are
+    // runs: it runs once, and cold.)
+    constexpr int kMost = kWarpPlan / 32;
+    const int each = (B + 31) >> 5, first = lane * each;
+    int32_t n[kMost], sum = 0;
 #pragma unroll
-    for (int i = 0; i < kWarpPlan / 32; ++i)
-      n[i] = 32 * i + lane < B ? p.seq_lens[32 * i + lane] : 0;
+    for (int i = 0; i < kMost; ++i) n[i] = i < each && first + i < B ? p.seq_lens[first + i] : 0;
     bool cannot = false;
-    int64_t carry = 0;
 #pragma unroll
-    for (int i = 0; i < kWarpPlan / 32; ++i) {
-      if (32 * i >= B) break;
-      int32_t v = units_of(n[i]);
+    for (int i = 0; i < kMost; ++i) {
+      if (i >= each) break;
+      const int32_t v = units_of(n[i]);
       cannot |= v < 0;
-      v = v < 0 ? 0 : v;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int32_t x = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += x;
-      }
-      if (32 * i + lane < B) cu[32 * i + lane + 1] = (int32_t)(carry + v);
-      carry += __shfl_sync(0xffffffffu, v, 31);
+      sum += v < 0 ? 0 : v;
+      n[i] = sum;
     }
+    int32_t incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+      if (i >= each) break;
+      if (first + i < B) cu[first + i + 1] = incl - sum + n[i];
+    }
+    const int64_t carry = __shfl_sync(0xffffffffu, incl, 31);
     cannot = __any_sync(0xffffffffu, cannot) || carry * H > INT32_MAX;
     if (cannot && lane == 0) *bad = 1;
     __syncwarp();
