@@ -85,9 +85,11 @@ struct Cfg {
   static_assert(kOffFloat + 4 * kFloats + 256 - kOffBar <= 5120, "small arrays");
   static_assert(kStages >= 8, "units ahead");
   static constexpr int kHalf = COLS / 2;  // the rows of a softmax group
-  // Registers a thread by warpgroup, of the 80 that the launch gives each: softmax (two), K, V
-  // (two), others.
-  static constexpr int kRegsSoftmax = 112, kRegsK = 72, kRegsV = 56, kRegsOther = 72;
+  // Registers a thread by warpgroup, of the 80 that the launch gives each: softmax (two; four
+  // for each of its rows and what they are made from), K, V (two), others. With 64 rows the
+  // others are short of some (spills of a dozen words), and wait most of the time.
+  static constexpr int kRegsSoftmax = COLS > 48 ? 152 : 128, kRegsK = COLS > 48 ? 48 : 56,
+                       kRegsV = COLS > 48 ? 40 : 56, kRegsOther = COLS > 48 ? 48 : 56;
   static_assert(2 * kRegsSoftmax + kRegsK + 2 * kRegsV + kRegsOther == 6 * 80, "registers");
 };
 template <int N>
@@ -592,6 +594,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (any_of(bar, 128, !ok)) break;
     const int steps = (d.n + 1) / 2;
     const float* fac = s_qfac + (j & 3) * 64 + c0;
+    // References and factors stay in registers: a 16-byte broadcast takes shared memory four
+    // cycles, as any 512 bytes do (6 tokens 130 -> 113 us, 8 153 -> 131).
+    float ref[N] = {}, factor[N];
+#pragma unroll
+    for (int c = 0; c < N; ++c) factor[c] = fac[c];
     float l[N];
 #pragma unroll
     for (int c = 0; c < N; ++c) l[c] = 0.f;
@@ -623,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // and what rounding took from a reference of 2^30 is no small number)
       auto less_reference = [&] {
 #pragma unroll
-        for (int c = 0; c < N; ++c) s[c] = __fsub_rn(__fmul_rn(s[c], fac[c]), s_ref[c]);
+        for (int c = 0; c < N; ++c) s[c] = __fsub_rn(__fmul_rn(s[c], factor[c]), ref[c]);
       };
       scores();
       bool passed = k == 0;
@@ -653,6 +660,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           s_alpha[row] = now == -INFINITY ? 1.f : ex2(old - now);
         }
         named_bar_sync(bar, 128);
+#pragma unroll
+        for (int c = 0; c < N; ++c) ref[c] = s_ref[c];
         if (k > 0) {
           // O is stable once the products of the step before are done
           ok = wait(pv_done(i ^ 1), (step - 1) >> 1);
