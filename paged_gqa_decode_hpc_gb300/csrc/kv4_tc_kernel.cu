@@ -27,16 +27,17 @@
 // memory is freed.
 //
 // What bounds it (32 sequences of 4096 and one of 131072 positions, 8 KV heads; HBM's share is
-// 44 us, 780 clk a step): with 2 tokens 84 us, of which shared memory takes most (710
-// wavefronts a step for threads, 315 for the MMAs, 144 for the copies, of 1440 clk; V passes
-// twice). With 4 tokens 107 us and with 8 153 us: the chain from a step's scores to its
-// P^T, a fixed 1000 clk of waits, vote and fences and 25 to 30 clk a row of the group, on warps
-// that share the SM's issue (0.5 to 0.6 a cycle) with the conversions. What it took, 4 and 8
-// tokens: one softmax group and one warp for both products 151 and 203 us; two waits a step
-// in that warp and 8 warps for V 121 and 182; two groups, a warp for each product 102 and
-// 162. Groups that take alternate steps instead of rows were slower (118 and 214: their
-// states need more registers). A wait on two barriers takes half of the lanes each, one
-// latency instead of two: one after the other they cost 8 to 10 %.
+// 44 us, 780 clk a step): the chain from a step's scores to its P^T, about 1000 clk of waits,
+// vote and fences that no row count changes and 15 to 25 a row of the group, on warps that share
+// the SM's issue (0.5 to 0.6 a cycle) and its shared memory (2 tokens: 710 wavefronts a step
+// for threads, 315 for the MMAs, 144 for the copies; V passes twice) with the conversions.
+// 2 tokens take 82 us, 4 take 102, 6 113, 8 131. What it took, 4 and 8 tokens: one softmax
+// group and one warp for both products 151 and 203 us; two waits a step in that warp and 8
+// warps for V 121 and 182; two groups, a warp for each product 102 and 162; a factor for each
+// row (see below) 107 and 153; references and factors in registers 102 and 131. Groups that
+// take alternate steps instead of rows were slower (118 and 214: their states need more
+// registers). A wait on two barriers takes half of the lanes each, one latency instead of two:
+// one after the other they cost 8 to 10 %.
 #include <cfloat>
 
 #include "kv4_plan.cuh"
