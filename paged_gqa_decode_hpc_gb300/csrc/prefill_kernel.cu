@@ -79,18 +79,26 @@ constexpr float kRescaleThreshold = 8.0f;  // log2 units
 // rows (kv4.cuh), else e4m3.
 template <int QT, bool FP8, bool KV4>
 struct Layout {
-  static_assert(FP8 || !KV4, "4-bit rows are converted");
-  // FP8 caches: 4 converter warps widen each e4m3 K / V tile to bf16 in place
-  // of the TMA writing bf16 directly
-  static constexpr int kConvWarps = FP8 ? 4 : 0;
+  static_assert(!KV4 || (FP8 && QT == 2), "4-bit rows are converted, for two chains");
+  // FP8 caches: 4 converter warps widen each e4m3 K / V tile to f16 in place
+  // of the TMA writing bf16 directly. 4-bit rows take 8: with 4 a tile took 0.74 us, which is
+  // more than its MMAs do (chunks of 1024 tokens of 4 long sequences 1336 -> 1241 us).
+  static constexpr int kConvWarps = KV4 ? 8 : FP8 ? 4 : 0;
   static constexpr int kConvWarp0 = 4 * QT;
   static constexpr int kProducerWarp = 4 * QT + kConvWarps, kMmaWarp0 = kProducerWarp + 1;
-  static constexpr int kThreads = 32 * (kMmaWarp0 + QT);
+  // (whole warpgroups where registers are moved between them: the last warp is idle)
+  static constexpr bool kMoveRegs = KV4 && QT == 2;
+  static constexpr int kThreads = 32 * (kMoveRegs ? (kMmaWarp0 + QT + 3) / 4 * 4 : kMmaWarp0 + QT);
+  // registers a thread of softmax (QT warpgroups), converters (two) and the others, of the 96
+  // that the launch gives each
+  static constexpr int kRegsSoftmax = 136, kRegsConv = 64, kRegsOther = 80;
+  static_assert(!kMoveRegs || 2 * kRegsSoftmax + 2 * kRegsConv + kRegsOther == kThreads / 128 * 96,
+                "registers");
   static constexpr int kStages = FP8 ? 4 : (QT == 1 ? 6 : 5);            // 16-bit K+V ring
   static constexpr uint32_t kTile8 = KV4 ? kKv4Tile : kKVTileBytes8;     // a tile as copied
   static constexpr uint32_t kStage8 = 2 * kTile8;
   // e4m3 K+V ring; of 4-bit rows what fits
-  static constexpr int kStages8 = KV4 ? (QT == 1 ? 6 : 3) : FP8 ? (QT == 1 ? 4 : 2) : 0;
+  static constexpr int kStages8 = KV4 ? 3 : FP8 ? (QT == 1 ? 4 : 2) : 0;
   static constexpr uint32_t kOffQ = 0;                                   // QT x 32 KB
   static constexpr uint32_t kOffKV = QT * kQBytes;                       // stages x 32 KB
   static constexpr uint32_t kOffKV8 = kOffKV + kStages * kStageBytes;    // stages8 x 16 KB
@@ -154,6 +162,15 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 }
 __device__ __forceinline__ void named_bar_sync(int id, int nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N) : "memory");
 }
 
 // Bounded wait on an mbarrier phase; false when the CTA aborts or the limit
@@ -269,12 +286,19 @@ __device__ __forceinline__ int tile_kv(int L, int n, int t0g) {
 
 namespace {
 
-template <int QT, bool FP8, bool KV4>
+// SPLIT (with two chains, QT = 2): both work for one query tile of 16 tokens, one on the even
+// KV tiles and one on the odd ones, and join their states at the end. For 4-bit rows in place
+// of one chain, where CTAs are few and the walk over the context is what takes the time (300
+// tokens after 8000, 2 KV heads: 87 -> 77 us; 16 sequences of 1 to 16 after up to 4000 45 -> 41).
+template <int QT, bool FP8, bool KV4, bool SPLIT = false>
 __global__ void __launch_bounds__(Layout<QT, FP8, KV4>::kThreads, 1)
     extend_kernel(const __grid_constant__ ExtendParams p, const __grid_constant__ CUtensorMap tmq,
                   const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                   const __grid_constant__ CUtensorMap tmo) {
   using Lt = Layout<QT, FP8, KV4>;
+  static_assert(!SPLIT || QT == 2, "two chains");
+  constexpr int kTilesOfQ = SPLIT ? 1 : QT;       // query tiles of the CTA
+  constexpr int kStride = SPLIT ? 2 : 1;          // a chain's KV tiles are every kStride-th
   constexpr int S = Lt::kStages, S8 = Lt::kStages8;
   constexpr int S8n = S8 > 0 ? S8 : 1;  // e4m3 ring positions (the ring exists for FP8 only)
   extern __shared__ uint8_t smem_raw[];
@@ -304,7 +328,7 @@ __global__ void __launch_bounds__(Layout<QT, FP8, KV4>::kThreads, 1)
   const unsigned long long lim_ns = p.timeout_ns;
 
   if (warp == 0) {
-    const TileInfo ti = find_tile(p, blockIdx.y, lane, kExtendTileTokens * QT);
+    const TileInfo ti = find_tile(p, blockIdx.y, lane, kExtendTileTokens * kTilesOfQ);
     if (lane == 0) {
       s_info[0] = ti.valid;
       s_info[1] = ti.b;
@@ -319,7 +343,7 @@ __global__ void __launch_bounds__(Layout<QT, FP8, KV4>::kThreads, 1)
       for (int s = 0; s < S; ++s) {
         // bf16 tile landed: the TMA's transaction count, or the converter threads
         mbar_init(kv_full(s), FP8 ? 32 * Lt::kConvWarps : 1);
-        mbar_init(kv_empty(s), QT);  // one arrival per query tile's MMA warp
+        mbar_init(kv_empty(s), kTilesOfQ);  // one arrival per query tile's MMA warp
       }
       for (int s = 0; s < S8; ++s) {
         mbar_init(kv8_full(s), 1);
@@ -356,13 +380,21 @@ __global__ void __launch_bounds__(Layout<QT, FP8, KV4>::kThreads, 1)
   int n_kv = 0;
 #pragma unroll
   for (int g = 0; g < QT; ++g) {
-    nkv[g] = valid ? tile_kv(L, n, t0 + kExtendTileTokens * g) : 0;
+    nkv[g] = valid ? tile_kv(L, n, t0 + (SPLIT ? 0 : kExtendTileTokens * g)) : 0;
     n_kv = nkv[g] > n_kv ? nkv[g] : n_kv;
+  }
+  if constexpr (SPLIT) {
+    nkv[0] = (n_kv + 1) / 2;
+    nkv[QT - 1] = n_kv / 2;
   }
   const uint32_t tmem = *s_tmem;
   int32_t* err = p.err;
 
-  if (warp == Lt::kProducerWarp) {
+  // (a warpgroup's warps take one and the same instruction)
+  if (Lt::kMoveRegs && warp >= Lt::kProducerWarp) regs_dec<Lt::kRegsOther>();
+  if (Lt::kMoveRegs && warp >= Lt::kMmaWarp0 + QT) {
+    named_bar_sync(1, Lt::kThreads);
+  } else if (warp == Lt::kProducerWarp) {
     // ------------------------------------------------------------ producer
     int issued = 0;  // K/V tiles whose copies were issued (in order)
     if (n_kv > 0 && !p.withhold_copies) {  // failure-path test: nothing is issued
@@ -370,7 +402,7 @@ __global__ void __launch_bounds__(Layout<QT, FP8, KV4>::kThreads, 1)
         mbar_expect_tx(bar_q, QT * kQBytes);
 #pragma unroll
         for (int g = 0; g < QT; ++g) {
-          const int row = q0 + t0 + kExtendTileTokens * g;
+          const int row = q0 + t0 + (SPLIT ? 0 : kExtendTileTokens * g);
           tma_load_3d(sQ + g * kQBytes, &tmq, bar_q, 0, kGroupRows * h, row);
           tma_load_3d(sQ + g * kQBytes + kQBytes / 2, &tmq, bar_q, 64, kGroupRows * h, row);
         }
@@ -448,6 +480,7 @@ __global__ void __launch_bounds__(Layout<QT, FP8, KV4>::kThreads, 1)
       }
     }
   } else if (FP8 && warp >= Lt::kConvWarp0 && warp < Lt::kProducerWarp) {
+    if constexpr (Lt::kMoveRegs) regs_dec<Lt::kRegsConv>();
     // -------------------------------------------- e4m3 -> f16 converters
     // Each e4m3 tile (64 token rows x 128 bytes, 128-byte swizzle: 16-byte
     // chunk c of row t at c ^ (t % 8)) is widened exactly (e4m3 values are
@@ -455,7 +488,7 @@ __global__ void __launch_bounds__(Layout<QT, FP8, KV4>::kThreads, 1)
     // 8-element chunk c' of row t at c' ^ (t % 8). The scales stay out:
     // k_scale is in the logit scale, v_scale in the epilogue.
     constexpr int kNT = FP8 ? 32 * Lt::kConvWarps : 128;  // (no converters with a bf16 cache)
-    static_assert(kNT == 64 || kNT == 128, "2 or 4 converter warps");
+    static_assert(kNT == 64 || kNT == 128 || kNT == 256, "2, 4 or 8 converter warps");
     constexpr int kRowSteps = 1024 / kNT / 2;  // items per matrix: rows t in kRowSteps bands
     const int ct = threadIdx.x - 32 * Lt::kConvWarp0;  // 0 .. kNT - 1
     // Work item it of thread ct: matrix it / kRowSteps, row t, 16-byte chunk
@@ -475,7 +508,7 @@ __global__ void __launch_bounds__(Layout<QT, FP8, KV4>::kThreads, 1)
                         wait_bar(kv_empty(sb), ((j / S) - 1) & 1, s_abort, err, lim_ns));
       if (!ok) break;
       const uint32_t e8 = sKV8 + s8 * Lt::kStage8, kb = sKV + sb * kStageBytes;
-#pragma unroll 2
+#pragma unroll(KV4 ? 4 : 2)
       for (int it = 0; it < 2 * kRowSteps; ++it) {
         const int mat = it / kRowSteps;
         const int t = (it % kRowSteps) * (64 / kRowSteps) + (ct >> 4) * 2 + cr;
@@ -549,7 +582,8 @@ __global__ void __launch_bounds__(Layout<QT, FP8, KV4>::kThreads, 1)
                         wait_bar(p_full(g, i & 1), (i >> 1) & 1, s_abort, err, lim_ns)))
           return false;
         tc_fence_after();
-        const uint64_t vd = vd0 + (uint64_t)((i % S) * (kStageBytes >> 4));
+        const int slot = (kStride * i + (SPLIT ? g : 0)) % S;
+        const uint64_t vd = vd0 + (uint64_t)(slot * (kStageBytes >> 4));
         const uint32_t pa = tmem + 256u * g + kColP + 32u * (uint32_t)(i & 1);
         if (leader) {
           mma_f16_ts(od, pa, vd, kIdPV, i > 0 ? 1u : 0u);
@@ -557,7 +591,7 @@ __global__ void __launch_bounds__(Layout<QT, FP8, KV4>::kThreads, 1)
           for (int kk = 1; kk < 4; ++kk)
             mma_f16_ts(od, pa + 8 * kk, vd + kk * (2048 >> 4), kIdPV, 1u);
           mma_commit(pv_done(g, i & 1));
-          mma_commit(kv_empty(i % S));
+          mma_commit(kv_empty(slot));
         }
         __syncwarp();
         return true;
@@ -565,9 +599,9 @@ __global__ void __launch_bounds__(Layout<QT, FP8, KV4>::kThreads, 1)
       // S_g(j) = Q_g K_j^T; S is single-buffered, so S(j) waits until the
       // softmax warps have copied S(j-1) out (early in their tile j-1)
       auto issue_s = [&](int j) -> bool {
-        const int slot = j % S;
+        const int tile = kStride * j + (SPLIT ? g : 0), slot = tile % S;
         if (!__all_sync(0xffffffffu,
-                        wait_bar(kv_full(slot), (j / S) & 1, s_abort, err, lim_ns)))
+                        wait_bar(kv_full(slot), (tile / S) & 1, s_abort, err, lim_ns)))
           return false;
         if (j >= 1 && !__all_sync(0xffffffffu,
                                   wait_bar(s_free(g), (j - 1) & 1, s_abort, err, lim_ns)))
@@ -601,7 +635,7 @@ __global__ void __launch_bounds__(Layout<QT, FP8, KV4>::kThreads, 1)
       }
       // K/V tiles this query tile does not read still get its arrival, in the
       // right round: once the tile has landed, the slot's previous round is over
-      for (int j = nkg; ok && j < n_kv; ++j) {
+      for (int j = nkg; !SPLIT && ok && j < n_kv; ++j) {
         ok = __all_sync(0xffffffffu, wait_bar(kv_full(j % S), (j / S) & 1, s_abort, err, lim_ns));
         if (ok && leader) mbar_arrive(kv_empty(j % S));
         __syncwarp();
@@ -617,17 +651,19 @@ __global__ void __launch_bounds__(Layout<QT, FP8, KV4>::kThreads, 1)
     tc_fence_after();
     if (warp == Lt::kMmaWarp0) tmem_dealloc(tmem, Lt::kTmemCols);
   } else {
+    if constexpr (Lt::kMoveRegs) regs_inc<Lt::kRegsSoftmax>();
     // ------------------------------------------------ softmax warpgroup g
     const int g = warp >> 2;
     const int r = threadIdx.x - kRows * g;  // query row = TMEM lane
-    const int tok = t0 + kExtendTileTokens * g + (r >> 3), head = kGroupRows * h + (r & 7);
+    const int tg = SPLIT ? 0 : kExtendTileTokens * g;  // the tile's first token from t0
+    const int tok = t0 + tg + (r >> 3), head = kGroupRows * h + (r & 7);
     const bool row_ok = valid && tok < n;
     int lim = L - n + 1 + tok;  // keys visible to this row: positions < lim
     if (lim > L) lim = L;
     const int nk = g == 0 ? nkv[0] : nkv[QT - 1];
     // the tile leaves by TMA when all its 16 tokens are new tokens of this
     // sequence (see the epilogue); uniform over the warpgroup
-    const bool full = valid && nk > 0 && t0 + kExtendTileTokens * (g + 1) <= n;
+    const bool full = valid && n_kv > 0 && (SPLIT || nk > 0) && t0 + tg + kExtendTileTokens <= n;
     const uint32_t trow = tmem + 256u * g + ((uint32_t)((warp & 3) * 32) << 16);
     bool ok = nk > 0;
     float qinv = 1.f;  // FP8: 2^-e, the scale this row's Q was converted with
@@ -706,7 +742,7 @@ __global__ void __launch_bounds__(Layout<QT, FP8, KV4>::kThreads, 1)
       tmem_wait_ld();
       tc_fence_before();
       mbar_arrive(s_free(g));
-      const int kv0 = j * 64;
+      const int kv0 = (kStride * j + (SPLIT ? g : 0)) * 64;
       if (kv0 + 64 > lim) {
 #pragma unroll
         for (int c = 0; c < 64; ++c)
@@ -731,7 +767,9 @@ __global__ void __launch_bounds__(Layout<QT, FP8, KV4>::kThreads, 1)
       const float alpha = need ? ex2(m - m_new) : 1.f;
       // exponents s*sc - m in packed pairs; row sum in four packed accumulators
       uint32_t pk[32];
-      const uint64_t sc2 = pack2(sc, sc), nm2 = pack2(-m_use, -m_use);
+      // (a chain's first tile may hide all of its keys from a row; then the row's P is 0)
+      const float nm = SPLIT && m_use == -INFINITY ? 0.f : -m_use;
+      const uint64_t sc2 = pack2(sc, sc), nm2 = pack2(nm, nm);
       uint64_t acc2[4] = {0ull, 0ull, 0ull, 0ull};
       auto exponentials = [&](auto apart) {
 #pragma unroll
@@ -796,50 +834,113 @@ __global__ void __launch_bounds__(Layout<QT, FP8, KV4>::kThreads, 1)
     // sequence, so it is stored row by row. `full` is uniform over the
     // warpgroup, so every thread reaches the staging barrier even when some
     // warp stopped early.
-    const uint32_t sQg = sQ + g * kQBytes;
-    if (ok) {
-      tc_fence_after();
-      const float inv = l > 0.f ? p.v_scale / l : 0.f;
-      __nv_bfloat16* orow = p.out + (int64_t)(q0 + tok) * p.o_st + (int64_t)head * p.o_sh;
-      // O in two rounds of 64 columns: two tensor-memory loads in flight per wait
+    if constexpr (SPLIT) {
+      // Both chains' states of the tile: each row's thread of chain g joins and stores the
+      // columns of half g. Maxima and sums are exchanged through the chains' Q buffers, whose
+      // MMAs are done, before rows are staged in the first one.
+      float2* ml = reinterpret_cast<float2*>(smem + Lt::kOffQ + g * kQBytes);
+      const float2* others = reinterpret_cast<const float2*>(smem + Lt::kOffQ + (g ^ 1) * kQBytes);
+      if (nk == 0 && n_kv > 0)  // (the only tile is chain 0's; the copies of Q have landed)
+        ok = __all_sync(0xffffffffu, wait_bar(bar_q, 0, s_abort, err, lim_ns));
+      ml[r] = make_float2(m, l);
+      tc_fence_before();
+      named_bar_sync(4, 2 * kRows);
+      const float2 other = others[r];
+      named_bar_sync(4, 2 * kRows);
+      if (ok && !*s_abort) {
+        tc_fence_after();
+        const bool both = n_kv > 1;
+        const float mx = fmaxf(m, other.x);
+        const float mine = m == -INFINITY ? 0.f : ex2(m - mx);
+        const float theirs = other.x == -INFINITY ? 0.f : ex2(other.x - mx);
+        const float all = l * mine + other.y * theirs;
+        const float inv = all > 0.f ? p.v_scale / all : 0.f;
+        const float f0 = (g == 0 ? mine : theirs) * inv, f1 = (g == 0 ? theirs : mine) * inv;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        __nv_bfloat16* orow = p.out + (int64_t)(q0 + tok) * p.o_st + (int64_t)head * p.o_sh;
+        const uint32_t srow = sQ + g * (kQBytes / 2) + r * 128;
 #pragma unroll
-      for (int q = 0; q < 4; q += 2) {
-        float o[64];
-        tmem_ld32(trow + kColO + q * 32, *reinterpret_cast<float(*)[32]>(&o[0]));
-        tmem_ld32(trow + kColO + q * 32 + 32, *reinterpret_cast<float(*)[32]>(&o[32]));
-        tmem_wait_ld();
-        const uint32_t srow = sQg + (q >> 1) * (kQBytes / 2) + r * 128;
+        for (int q = 0; q < 2; ++q) {
+          const uint32_t col = kColO + 64u * g + 32u * q;
+          float o[32], x[32];
+          tmem_ld32(tmem + lanes + col, o);
+          if (both) tmem_ld32(tmem + 256u + lanes + col, x);
+          tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          uint4 v;
-          v.x = pack_bf16(o[8 * c + 0] * inv, o[8 * c + 1] * inv);
-          v.y = pack_bf16(o[8 * c + 2] * inv, o[8 * c + 3] * inv);
-          v.z = pack_bf16(o[8 * c + 4] * inv, o[8 * c + 5] * inv);
-          v.w = pack_bf16(o[8 * c + 6] * inv, o[8 * c + 7] * inv);
-          if (full) {
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                             srow + ((uint32_t)(c ^ (r & 7)) << 4)),
-                         "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                         : "memory");
-          } else if (row_ok) {
-            *reinterpret_cast<uint4*>(orow + q * 32 + c * 8) = v;
+          for (int i = 0; i < 32; ++i) o[i] = both ? fmaf(x[i], f1, o[i] * f0) : o[i] * f0;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint4 v = make_uint4(pack_bf16(o[8 * c], o[8 * c + 1]), pack_bf16(o[8 * c + 2], o[8 * c + 3]),
+                                       pack_bf16(o[8 * c + 4], o[8 * c + 5]), pack_bf16(o[8 * c + 6], o[8 * c + 7]));
+            if (full) {
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                               srow + ((uint32_t)((4 * q + c) ^ (r & 7)) << 4)),
+                           "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                           : "memory");
+            } else if (row_ok) {
+              *reinterpret_cast<uint4*>(orow + 64 * g + 32 * q + 8 * c) = v;
+            }
           }
         }
+        if (g == 0 && row_ok && p.lse)
+          p.lse[(int64_t)(q0 + tok) * p.l_st + (int64_t)head * p.l_sh] =
+              all > 0.f ? (mx + __log2f(all)) * kLn2 : -INFINITY;
       }
-      if (row_ok && p.lse)
-        p.lse[(int64_t)(q0 + tok) * p.l_st + (int64_t)head * p.l_sh] =
-            l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
-    }
-    if (full) {
-      fence_async_shared();  // the TMA store reads the rows through the async proxy
-      if (g == 0) named_bar_sync(2, kRows); else named_bar_sync(3, kRows);
-      if (r == 0 && !*s_abort) {
-        // the tile's first row, re-read here rather than held through the loop
-        const volatile int* si = s_info;
-        const int row = si[5] + si[2] + kExtendTileTokens * g;
-        tma_store_3d(&tmo, sQg, 0, kGroupRows * h, row);
-        tma_store_3d(&tmo, sQg + kQBytes / 2, 64, kGroupRows * h, row);
-        bulk_commit_and_wait_read();  // the buffer is read before the CTA retires
+      if (full) {
+        fence_async_shared();  // the TMA store reads the rows through the async proxy
+        if (g == 0) named_bar_sync(2, kRows); else named_bar_sync(3, kRows);
+        if (r == 0 && !*s_abort) {
+          const volatile int* si = s_info;
+          tma_store_3d(&tmo, sQ + g * (kQBytes / 2), 64 * g, kGroupRows * h, si[5] + si[2]);
+          bulk_commit_and_wait_read();  // the buffer is read before the CTA retires
+        }
+      }
+    } else {
+      const uint32_t sQg = sQ + g * kQBytes;
+      if (ok) {
+        tc_fence_after();
+        const float inv = l > 0.f ? p.v_scale / l : 0.f;
+        __nv_bfloat16* orow = p.out + (int64_t)(q0 + tok) * p.o_st + (int64_t)head * p.o_sh;
+        // O in two rounds of 64 columns: two tensor-memory loads in flight per wait
+#pragma unroll
+        for (int q = 0; q < 4; q += 2) {
+          float o[64];
+          tmem_ld32(trow + kColO + q * 32, *reinterpret_cast<float(*)[32]>(&o[0]));
+          tmem_ld32(trow + kColO + q * 32 + 32, *reinterpret_cast<float(*)[32]>(&o[32]));
+          tmem_wait_ld();
+          const uint32_t srow = sQg + (q >> 1) * (kQBytes / 2) + r * 128;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            uint4 v;
+            v.x = pack_bf16(o[8 * c + 0] * inv, o[8 * c + 1] * inv);
+            v.y = pack_bf16(o[8 * c + 2] * inv, o[8 * c + 3] * inv);
+            v.z = pack_bf16(o[8 * c + 4] * inv, o[8 * c + 5] * inv);
+            v.w = pack_bf16(o[8 * c + 6] * inv, o[8 * c + 7] * inv);
+            if (full) {
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                               srow + ((uint32_t)(c ^ (r & 7)) << 4)),
+                           "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                           : "memory");
+            } else if (row_ok) {
+              *reinterpret_cast<uint4*>(orow + q * 32 + c * 8) = v;
+            }
+          }
+        }
+        if (row_ok && p.lse)
+          p.lse[(int64_t)(q0 + tok) * p.l_st + (int64_t)head * p.l_sh] =
+              l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+      }
+      if (full) {
+        fence_async_shared();  // the TMA store reads the rows through the async proxy
+        if (g == 0) named_bar_sync(2, kRows); else named_bar_sync(3, kRows);
+        if (r == 0 && !*s_abort) {
+          // the tile's first row, re-read here rather than held through the loop
+          const volatile int* si = s_info;
+          const int row = si[5] + si[2] + kExtendTileTokens * g;
+          tma_store_3d(&tmo, sQg, 0, kGroupRows * h, row);
+          tma_store_3d(&tmo, sQg + kQBytes / 2, 64, kGroupRows * h, row);
+          bulk_commit_and_wait_read();  // the buffer is read before the CTA retires
+        }
       }
     }
     tc_fence_before();
@@ -847,19 +948,19 @@ __global__ void __launch_bounds__(Layout<QT, FP8, KV4>::kThreads, 1)
   }
 }
 
-template <int QT, bool FP8, bool KV4 = false>
+template <int QT, bool FP8, bool KV4 = false, bool SPLIT = false>
 cudaError_t launch_qt(const ExtendParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
                       const CUtensorMap& tv, const CUtensorMap& to, int tiles,
                       cudaStream_t stream) {
   using Lt = Layout<QT, FP8, KV4>;
   static std::atomic<uint64_t> configured{0};  // devices whose copy is configured
   const cudaError_t e = once_per_device(configured, [] {
-    return cudaFuncSetAttribute(extend_kernel<QT, FP8, KV4>,
+    return cudaFuncSetAttribute(extend_kernel<QT, FP8, KV4, SPLIT>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)Lt::kSmemBytes);
   });
   if (e != cudaSuccess) return e;
-  extend_kernel<QT, FP8, KV4><<<dim3(p.num_kv_heads, tiles), Lt::kThreads, Lt::kSmemBytes, stream>>>(
+  extend_kernel<QT, FP8, KV4, SPLIT><<<dim3(p.num_kv_heads, tiles), Lt::kThreads, Lt::kSmemBytes, stream>>>(
       p, tq, tk, tv, to);
   return cudaGetLastError();
 }
@@ -872,7 +973,7 @@ cudaError_t launch_extend(const ExtendParams& p, const CUtensorMap& tq, const CU
   if (tiles <= 0 || p.num_kv_heads <= 0) return cudaSuccess;
   if (p.k4) {
     if (tiles_per_cta == 2) return launch_qt<2, true, true>(p, tq, tk, tv, to, tiles, stream);
-    return launch_qt<1, true, true>(p, tq, tk, tv, to, tiles, stream);
+    return launch_qt<2, true, true, true>(p, tq, tk, tv, to, tiles, stream);
   }
   if (p.kv_fp8) {
     if (tiles_per_cta == 2) return launch_qt<2, true>(p, tq, tk, tv, to, tiles, stream);

@@ -1,5 +1,10 @@
 """What only a step of several new tokens can get wrong: rows of q of very different sizes, strides and orders of q and
 out, more sequences than one warp plans, pieces of every length, and that nothing is allocated."""
+import json
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -145,3 +150,55 @@ def test_one_token_with_large_scores():
     """The maximum's probability is 1 whatever the scores' size (one power of two for the KV head's rows)."""
     c = Paged([300, 70, 5000], hkv=2, q_rows=3, seed=47, q_scale=2.0 ** 70, ks=0.5)
     c.check(*decode(c, 1), cu_of([1] * 3))
+
+
+@pytest.mark.parametrize("new,old", [([1, 2, 16], [0, 63, 64]), ([5, 300], [8000, 0]), ([16] * 4, [64 * i for i in range(4)]),
+                                     ([700, 1, 90], [100, 6000, 5])])
+@pytest.mark.parametrize("hkv", [1, 8])
+def test_chunks_whose_rows_see_few_or_many_tiles(new, old, hkv):
+    """Both kinds of CTA: two query tiles, and one whose keys two chains share (one tile, an odd one, none of a chain's
+    keys visible to some rows)."""
+    c = Paged([n + o for n, o in zip(new, old)], hkv=hkv, q_rows=sum(new), seed=48, q_scale=4.0)
+    d, cu = c.device(), cu_of(new)
+    for _ in range(2):
+        out, lse = torch.full_like(d["q"], float("nan")), torch.full(d["q"].shape[:2], float("nan"), device="cuda")
+        hpc.hpc_extend_kv4_attn(d["q"], d["k"], d["v"], d["bt"], d["sl"], i32(cu), out, lse, k_scale=c.ks, v_scale=c.vs)
+        c.check(out, lse, cu)
+
+
+CHILD = r"""
+import json, os, sys, time
+sys.path.insert(0, sys.argv[1])
+import torch
+import paged_gqa_decode_hpc_gb300 as hpc
+from tests.kv4_util import Paged, cu_of, i32
+hpc.load_library()
+res = []
+for new, old in (([3, 20], [500, 0]), ([700, 900], [100, 0])):
+    c = Paged([n + o for n, o in zip(new, old)], hkv=8, q_rows=sum(new), seed=1)
+    d, cu = c.device(), cu_of(new)
+    out, lse, err = torch.empty_like(d["q"]), torch.empty(d["q"].shape[:2], device="cuda"), i32([0])
+    call = lambda: hpc.hpc_extend_kv4_attn(d["q"], d["k"], d["v"], d["bt"], d["sl"], i32(cu), out, lse, device_error=err,
+                                           k_scale=c.ks, v_scale=c.vs)
+    os.environ["HPC_DECODE_TEST_WITHHOLD_COPIES"] = "1"
+    t0 = time.time()
+    call()
+    bits = err.item()
+    seconds = time.time() - t0
+    os.environ["HPC_DECODE_TEST_WITHHOLD_COPIES"] = "0"
+    err.zero_()
+    call()
+    c.check(out, lse, cu)
+    res.append([bits, seconds, err.item()])
+print(json.dumps(res))
+"""
+
+
+def test_copies_of_a_prompt_that_never_come():
+    """The waits give up, the call reports it, and the next one is served."""
+    env = dict(os.environ, HPC_DECODE_WAIT_LIMIT_MS="100")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", CHILD, root], capture_output=True, text=True, env=env, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+    for bits, seconds, after in json.loads(r.stdout.strip().splitlines()[-1]):
+        assert bits & 8 and after == 0 and seconds < 60
