@@ -133,7 +133,8 @@ constexpr int kCtas = 8;
 // Both are correctly rounded from the exact quotients, ties to even: rounding is
 // monotone, so where the two products that enclose a quotient round alike, so does it
 // (1 / unit is within 2^-24, the factors and products within 2^-24 each: 2^-21 encloses
-// them); the others, near a border, are divided.
+// them); others lie near a border, ties of short bf16 values among them, and are decided by
+// their remainders.
 __device__ __forceinline__ float quotient_odd(float x, float s) {
   return fabsf(x) <= 3.4028235e38f ? div_round_odd(x, s) : x;
 }
@@ -146,11 +147,15 @@ __device__ __forceinline__ uint32_t to_e2m1x8(const float (&y)[8]) {
       : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
   return r;
 }
-static __device__ __noinline__ uint32_t divide_e2m1x8(float4 a, float4 b, float unit) {
-  const float y[8] = {quotient_odd(a.x, unit), quotient_odd(a.y, unit), quotient_odd(a.z, unit),
-                      quotient_odd(a.w, unit), quotient_odd(b.x, unit), quotient_odd(b.y, unit),
-                      quotient_odd(b.z, unit), quotient_odd(b.w, unit)};
-  return to_e2m1x8(y);
+// x / unit rounded to odd, which the codes' borders, floats of few bits, never are unless the
+// quotient is one: a product with inv, the reciprocal within 2^-24, a correction by its
+// remainder, and the sign of the exact remainder that is left. (Quotients beyond 8 stay there.)
+__device__ __forceinline__ float code_quotient(float x, float unit, float inv) {
+  const float ax = fabsf(x), q0 = fminf(ax * inv, 8.f);
+  const float q = fminf(fmaf(fmaf(-q0, unit, ax), inv, q0), 8.f), rest = fmaf(-q, unit, ax);
+  uint32_t bits = __float_as_uint(q);
+  if (rest != 0.f && !(bits & 1u)) bits += rest > 0.f ? 1u : ~0u;
+  return copysignf(__uint_as_float(bits), x);
 }
 __device__ __forceinline__ uint32_t quantise_e2m1x8(const float2* x, float amax, float tensor_scale,
                                                     uint8_t* scale) {
@@ -172,8 +177,12 @@ __device__ __forceinline__ uint32_t quantise_e2m1x8(const float2* x, float amax,
   }
   const uint32_t r = to_e2m1x8(a);
   if (r == to_e2m1x8(b)) return r;
-  return divide_e2m1x8(make_float4(x[0].x, x[0].y, x[1].x, x[1].y),
-                       make_float4(x[2].x, x[2].y, x[3].x, x[3].y), unit);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    a[2 * i] = code_quotient(x[i].x, unit, inv);
+    a[2 * i + 1] = code_quotient(x[i].y, unit, inv);
+  }
+  return to_e2m1x8(a);
 }
 __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
   float r;
