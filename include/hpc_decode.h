@@ -760,7 +760,7 @@ hpc_status hpc_decode_kv4_plan_create(int32_t max_seqs, int32_t max_q_len, int32
  *   k_cache, v_cache  4-bit caches with H_q == 8 * H_kv
  *   block_table  device int32 [B][max_blocks], rows contiguous
  *   seq_lens     device int32 [B]; a negative length, a sequence of more than INT32_MAX /
- *                1024 (tile, KV head) units, or more than INT32_MAX units in all (four more
+ *                1024 (tile, KV head) units, or more than INT32_MAX units in all (a few more
  *                counted for each sequence and KV head) set HPC_DEVCHK_BAD_LENGTH and the
  *                step writes out = 0, lse = -inf throughout
  *   plan         from hpc_decode_kv4_plan_create, for at least this step's sequences, new

@@ -55,6 +55,10 @@ namespace {
 // Warpgroups 0 and 1: consumer warps. Warpgroup 2: epilogue, each of its warps a quarter of
 // every state. Warpgroup 3: the producer warp and three that leave at once.
 constexpr int kConsumerWarps = 8, kEpilogueWarp0 = 8, kEpilogueWarps = 4, kProducerWarp = 12;
+// Units that a pair counts for beside its own, and that a CTA is worth starting for (64
+// sequences of 200 to 6000 positions 32.9 us with 2, 29.7 with 4, 30.2 with 6; 8 short ones 9.4
+// us with parts of at least 8 units, 7.9 with 4).
+constexpr int kPairCost = 4, kMinPart = 4;
 constexpr int kThreads = 512;
 constexpr int kPieceQ = 4;                        // piece descriptors in flight
 constexpr int kDescInts = 8;
@@ -361,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_launch_dependents();
   __syncthreads();
 
-  plan_step(p, cu, s_bad, warp_tot, kThreads, warp == kProducerWarp);
+  plan_step<kPairCost>(p, cu, s_bad, warp_tot, kThreads, warp == kProducerWarp);
 
   if (warp >= kProducerWarp) {
     regs_dec<C::kRegsProducer>();
@@ -370,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return;
     }
     // ------------------------------------------------------------ producer
-    const PartPlan M = part_plan(p, cu, s_bad);
+    const PartPlan M = part_plan<kMinPart>(p, cu, s_bad);
     UnitCopies<STAGES, C::kBatch> copies;
     copies.ring = smem_base;
     copies.full = bar_full;
@@ -414,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++j;
     };
     if (blockIdx.x < M.P) {
-      walk_part(
+      walk_part<kPairCost>(
           M, cu, B, H, (int)blockIdx.x, [&](const Piece& x) { copies.ahead(p, x); },
           [&](const Piece& x) {
             publish(x);
@@ -494,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // each by its last piece, so that no one reads more than a few dozen states. One
       // acquire-release atomic covers the warps' writes (ordered before it by the barrier)
       // and the other pieces', which the warps read after the second barrier.
-      const PartPlan M = part_plan(p, cu, s_bad);
+      const PartPlan M = part_plan<kMinPart>(p, cu, s_bad);
       const int k = fl >> 8, owner = slot >> 1;
       const uint32_t own = (uint32_t)cu[b] * H + (uint32_t)h * (uint32_t)(cu[b + 1] - cu[b]) + kPairCost;
       const int first = (int)M.owner_of(own);

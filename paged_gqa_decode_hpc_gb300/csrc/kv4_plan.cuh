@@ -2,7 +2,7 @@
 // the device lengths, and the walk of a CTA's part of it.
 //
 // A unit is one 64-token tile of one KV head. Units are ordered by sequence, KV head and
-// tile, and every (sequence, KV head) pair has kPairCost units more ahead of its own, which
+// tile, and every (sequence, KV head) pair has PAIR units more ahead of its own, which
 // stand for what it costs beside them (its q, its states' way to memory). The units are cut
 // into equal parts, one to a CTA; a piece is what of one pair's own units lies in a part.
 // (A pool of an eighth of the units in chunks, taken by whoever is done, as the one-token
@@ -20,8 +20,6 @@
 namespace hpc {
 namespace {
 
-constexpr int kPairCost = 4;
-constexpr int kMinPart = 8;     // units that a CTA is worth starting for
 constexpr int kWarpPlan = 256;  // sequences that one warp plans by itself
 constexpr int kFlagEnd = 1, kFlagWhole = 2;  // of a piece; its pair's number of pieces << 8
 // Bookkeeping waits give up this many data waits later: once a data wait has timed out
@@ -59,6 +57,7 @@ struct PartPlan {
 // *bad where the lengths cannot be. Called by all `threads` (at most 1024) threads of the CTA
 // after a barrier. The warp `planner` plans small batches by itself; other warps may look at
 // the result only after they have waited for something that it did later.
+template <int PAIR>
 __device__ __forceinline__ void plan_step(const Kv4DecodeParams& p, int32_t* cu, volatile int* bad,
                                           int32_t* warp_tot, int threads, bool planner) {
   const int B = p.num_seqs, tid = threadIdx.x, lane = tid & 31;
@@ -66,7 +65,7 @@ __device__ __forceinline__ void plan_step(const Kv4DecodeParams& p, int32_t* cu,
   auto units_of = [&](int32_t len) -> int32_t {  // -1: cannot be
     // more units than INT32_MAX / 1024 are refused, so that no partial sum of a scan pass, of
     // at most 1024 sequences, wraps
-    const int64_t n = len > 0 ? ((int64_t)len + kBlockTokens - 1) / kBlockTokens + kPairCost : 0;
+    const int64_t n = len > 0 ? ((int64_t)len + kBlockTokens - 1) / kBlockTokens + PAIR : 0;
     return len < 0 || n * H > (int64_t)(INT32_MAX / 1024) ? -1 : (int32_t)n;
   };
   if (B > kWarpPlan) {
@@ -120,11 +119,13 @@ __device__ __forceinline__ void plan_step(const Kv4DecodeParams& p, int32_t* cu,
   }
 }
 
+// At least MIN units to a CTA.
+template <int MIN>
 __device__ __forceinline__ PartPlan part_plan(const Kv4DecodeParams& p, const int32_t* cu,
                                               const volatile int* bad) {
   PartPlan M;
   M.T = *bad ? 0u : (uint32_t)cu[p.num_seqs] * (uint32_t)p.num_kv_heads;
-  const uint32_t want = (M.T + kMinPart - 1) / kMinPart;
+  const uint32_t want = (M.T + MIN - 1) / MIN;
   M.P = want < gridDim.x ? want : gridDim.x;
   M.small = (uint64_t)(M.T + 1) * (M.P + 1) < (uint64_t)UINT32_MAX;
   return M;
@@ -176,7 +177,7 @@ struct Piece {
 // them. The pieces of split pairs are done early, and their merges overlap the rest.
 // ahead(piece) is called before the piece's flags are known, then piece(piece). Returns the
 // pair that begins here and goes on: {b, h, pieces, slot}, 0 pieces for none.
-template <typename A, typename F>
+template <int PAIR, typename A, typename F>
 __device__ __forceinline__ int4 walk_part(const PartPlan& M, const int32_t* cu, int B, uint32_t H,
                                           int owner, A ahead, F piece) {
   int4 begun = make_int4(0, 0, 0, 0);
@@ -184,7 +185,7 @@ __device__ __forceinline__ int4 walk_part(const PartPlan& M, const int32_t* cu, 
   Pair at = pair_at(cu, B, H, lo), second = at;
   uint32_t end = hi;  // of the whole pairs between
   for (int round = 0;; ++round) {
-    const uint32_t own = at.base + kPairCost, pair_hi = at.base + at.nb;  // the pair's own units
+    const uint32_t own = at.base + PAIR, pair_hi = at.base + at.nb;  // the pair's own units
     const uint32_t from = lo > own ? lo : own, to = hi < pair_hi ? hi : pair_hi;
     if (to > from) {  // (else nothing but the pair's cost is here)
       Piece x;

@@ -31,10 +31,11 @@
 // vote and fences that no row count changes and 15 to 25 a row of the group, on warps that share
 // the SM's issue (0.5 to 0.6 a cycle) and its shared memory (2 tokens: 710 wavefronts a step
 // for threads, 315 for the MMAs, 144 for the copies; V passes twice) with the conversions.
-// 2 tokens take 82 us, 4 take 102, 6 113, 8 131. What it took, 4 and 8 tokens: one softmax
+// 2 tokens take 83 us, 4 take 101, 6 111, 8 128. What it took, 4 and 8 tokens: one softmax
 // group and one warp for both products 151 and 203 us; two waits a step in that warp and 8
 // warps for V 121 and 182; two groups, a warp for each product 102 and 162; a factor for each
-// row (see below) 107 and 153; references and factors in registers 102 and 131. Groups that
+// row (see below) 107 and 153; references and factors in registers 102 and 131; a pair counted
+// with 7 units 101 and 128. Groups that
 // take alternate steps instead of rows were slower (118 and 214: their states need more
 // registers). A wait on two barriers takes half of the lanes each, one latency instead of two:
 // one after the other they cost 8 to 10 %.
@@ -46,6 +47,10 @@
 namespace hpc {
 namespace {
 
+// Units that a pair counts for beside its own, and that a CTA is worth starting for (13 short
+// sequences with 8 drafts 26.1 us with 4, 23.5 with 6 to 8; 8 short ones of 2 tokens 12.2 us with
+// parts of at least 8 units, 10.7 with 4).
+constexpr int kPairCost = 7, kMinPart = 4;
 constexpr int kThreads = 768;
 constexpr int kKWarp0 = 8, kVWarp0 = 12, kProducerWarp = 20, kScoreWarp = 21, kValueWarp = 22;
 // (and the last warp: q)
@@ -226,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_launch_dependents();
   __syncthreads();
   tc05::tc_fence_after();
-  plan_step(p, cu, s_bad, warp_tot, kThreads, warp == kProducerWarp);
+  plan_step<kPairCost>(p, cu, s_bad, warp_tot, kThreads, warp == kProducerWarp);
   const uint32_t tmem = *s_tmem;
 
   // Every role walks the pieces: piece(j) waits for descriptor j and returns whether there is
@@ -265,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_dec<C::kRegsOther>();
     if (warp == kProducerWarp) {
       // ---------------------------------------------------------- producer
-      const PartPlan M = part_plan(p, cu, s_bad);
+      const PartPlan M = part_plan<kMinPart>(p, cu, s_bad);
       UnitCopies<R, C::kBatch> copies;
       copies.ring = base + C::kOffRing;
       copies.full = full(0);
@@ -296,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++j;
       };
       if (blockIdx.x < M.P) {
-        const int4 begun = walk_part(
+        const int4 begun = walk_part<kPairCost>(
             M, cu, B, H, (int)blockIdx.x, [&](const Piece& x) { copies.ahead(p, x); },
             [&](const Piece& x) {
               publish(x);
