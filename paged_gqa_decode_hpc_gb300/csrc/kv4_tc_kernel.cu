@@ -31,11 +31,11 @@
 // vote and fences that no row count changes and 15 to 25 a row of the group, on warps that share
 // the SM's issue (0.5 to 0.6 a cycle) and its shared memory (2 tokens: 710 wavefronts a step
 // for threads, 315 for the MMAs, 144 for the copies; V passes twice) with the conversions.
-// 2 tokens take 83 us, 4 take 101, 6 111, 8 128. What it took, 4 and 8 tokens: one softmax
+// 2 tokens take 83 us, 4 take 99, 6 110, 8 126. What it took, 4 and 8 tokens: one softmax
 // group and one warp for both products 151 and 203 us; two waits a step in that warp and 8
 // warps for V 121 and 182; two groups, a warp for each product 102 and 162; a factor for each
 // row (see below) 107 and 153; references and factors in registers 102 and 131; a pair counted
-// with 7 units 101 and 128. Groups that
+// with 7 units 101 and 128; K's two halves in a loop 99 and 126. Groups that
 // take alternate steps instead of rows were slower (118 and 214: their states need more
 // registers). A wait on two barriers takes half of the lanes each, one latency instead of two:
 // one after the other they cost 8 to 10 %.
@@ -73,7 +73,7 @@ struct Cfg {
   static constexpr uint32_t kOffRing = kOffQ + 2 * kQBuf;
   static constexpr int kFixed = kOffRing + 5120 /* barriers, descriptors, references */ + 1024 + 4 * (kKv4MaxSeqs + 1);
   static constexpr int kStages = (227 * 1024 - kFixed) / (2 * kKv4Tile) < 16 ? (227 * 1024 - kFixed) / (2 * kKv4Tile) : 16;
-  static constexpr int kBatch = 8;
+  static constexpr int kBatch = 4;
   static constexpr uint32_t kOffBar = kOffRing + kStages * 2 * kKv4Tile;
   // full, empty [stages]; piece full, free [4]; K full [2], S full, free [4 each], P full, V
   // full, PV done [2 each]; q landed, free [2 each], full [4]; drains [2]
@@ -546,7 +546,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             return *reinterpret_cast<const uint2*>(__cvta_shared_to_generic(src + 8 * x));
           };
           const uint2 sc = load(8);
-#pragma unroll
+          // (unrolled it is faster only beside 48 rows: 109.6 us for 112.2 with 6 tokens, but
+          // 100.7 for 98.6 with 4 and 127.3 for 126.4 with 8)
+#pragma unroll(COLS == 48 ? 2 : 1)
           for (int hf = 0; hf < 2; ++hf) {
             uint32_t w[32];
 #pragma unroll

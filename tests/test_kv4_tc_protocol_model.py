@@ -250,7 +250,7 @@ def test_no_schedule_breaks_the_protocol(seed):
     pieces = [1] * n if kind == 0 else [rng.randint(1, 3) for _ in range(n)] if kind == 1 else \
         [rng.randint(1, 25) for _ in range(min(n, 6))] if kind == 2 else [rng.choice([1, 2, 30]) for _ in range(min(n, 8))]
     stages = rng.choice([8, 9, 10])
-    c = Cta(pieces, stages, 8, rng)
+    c = Cta(pieces, stages, rng.choice([4, 8]), rng)
     c.run()
     assert len(c.results) == len(pieces)
 
@@ -261,7 +261,7 @@ def test_the_model_finds_a_lagging_reader():
     for seed in range(24):
         rng = random.Random(seed)
         try:
-            Cta([1] * 14, 10, 8, rng, q_ring=2).run()
+            Cta([1] * 14, 10, 4, rng, q_ring=2).run()
         except AssertionError:
             found += 1
     assert found > 0
