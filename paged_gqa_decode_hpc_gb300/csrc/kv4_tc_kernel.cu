@@ -261,9 +261,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   // Two barriers (the second only if `also`), half of the lanes at each: one latency where both
   // phases are there already. (A sleeping wait for one after the other was slower, see above.)
+  // A lane's own wait acquires only the phase that it looked at, and a vote orders no memory. The
+  // warp barrier does, and what is released, acquired and passed through a barrier is ordered for
+  // every lane behind it: the arrivals' writes, and a bulk copy's or an MMA's results, whose
+  // completion is followed by the proxy fence before it arrives. (What MMAs read or wrote needs
+  // tc_fence_after besides, as after any wait.)
   auto wait2 = [&](uint32_t a, uint32_t pa, uint32_t b, uint32_t pb, bool also) -> bool {
     const bool second = also && (lane & 1);
-    return wait(second ? b : a, second ? pb : pa);
+    const bool ok = wait(second ? b : a, second ? pb : pa);
+    __syncwarp();
+    return ok;
   };
 
   if (warp >= kProducerWarp) {

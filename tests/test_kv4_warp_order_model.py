@@ -1,0 +1,70 @@
+"""What a warp's lanes may rely on after a wait that only some of them made (CPU model of the memory order, and the order
+of the statements in the kernels' sources). A lane that sees a barrier's phase acquires what its arrivals released; a vote
+or a shuffle orders no memory; a warp barrier hands on what any lane has acquired."""
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "paged_gqa_decode_hpc_gb300", "csrc")
+
+
+def source(name):
+    with open(os.path.join(CSRC, name)) as f:
+        return re.sub(r"//[^\n]*", "", f.read())
+
+
+class Warp:
+    def __init__(self):
+        self.known = [set() for _ in range(32)]
+
+    def look(self, lane, released):
+        self.known[lane] |= released
+
+    def vote(self):
+        pass
+
+    def barrier(self):
+        every = set().union(*self.known)
+        self.known = [set(every) for _ in range(32)]
+
+    def use(self, lanes, needs):
+        return all(needs <= self.known[i] for i in lanes)
+
+
+# the waits on two barriers of kv4_tc_kernel.cu: what either releases, and the lanes that then rely on both
+WAITS = {
+    "K to f16": ({"ring slot's bytes"}, {"K's columns read by the MMAs"}, range(32)),
+    "V to f16": ({"ring slot's bytes"}, {"V's tile read by the MMAs"}, range(32)),
+    "scores' MMAs": ({"K's columns"}, {"scores read"}, [0]),
+    "values' MMAs": ({"P^T"}, {"V's tile"}, [0]),
+    "values' MMAs, by another lane": ({"P^T"}, {"V's tile"}, [31]),
+    "softmax": ({"scores"}, {"P^T read by the MMAs"}, range(32)),
+}
+
+
+def two_barriers(a, b, steps):
+    w = Warp()
+    for lane in range(32):
+        w.look(lane, b if lane & 1 else a)
+    for step in steps:
+        getattr(w, step)()
+    return w
+
+
+def steps_of_wait2():
+    """What wait2 does after the lanes' looks, in the order of its statements: the vote lies in wait()."""
+    body = re.search(r"auto wait2 = \[&\].*?\n  };", source("kv4_tc_kernel.cu"), re.S).group(0)
+    return [{"wait(": "vote", "__syncwarp()": "barrier"}[x] for x in re.findall(r"\bwait\(|__syncwarp\(\)", body)]
+
+
+@pytest.mark.parametrize("name", WAITS)
+def test_a_wait_on_two_barriers_orders_both_for_every_lane(name):
+    a, b, lanes = WAITS[name]
+    assert two_barriers(a, b, steps_of_wait2()).use(lanes, a | b)
+
+
+@pytest.mark.parametrize("name", WAITS)
+def test_a_vote_alone_does_not(name):
+    a, b, lanes = WAITS[name]
+    assert not two_barriers(a, b, ["vote"]).use(lanes, a | b)
