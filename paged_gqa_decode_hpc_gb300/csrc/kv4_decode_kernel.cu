@@ -405,6 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       lost = __shfl_sync(0xffffffffu, (int)lost, 0) != 0;
+      __syncwarp();  // (a shuffle orders no memory: lane 0 has seen the slot's rows read, others copy)
       if (rows && !lost) {
         const uint32_t dq = smem_base + C::kQOff + qs * C::kQBytes;
         const __nv_bfloat16* q0 =

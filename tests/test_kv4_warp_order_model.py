@@ -68,3 +68,18 @@ def test_a_wait_on_two_barriers_orders_both_for_every_lane(name):
 def test_a_vote_alone_does_not(name):
     a, b, lanes = WAITS[name]
     assert not two_barriers(a, b, ["vote"]).use(lanes, a | b)
+
+
+def test_rows_of_q_are_copied_behind_what_lane_0_has_seen():
+    """kv4_decode_kernel.cu: lane 0 waits for a piece's slot, eight lanes copy rows of q into it."""
+    body = re.search(r"auto publish = .*?\n    };", source("kv4_decode_kernel.cu"), re.S).group(0)
+    before = body[body.index("wait_phase("):body.index("kv4_copy(")]
+    steps = [{"__shfl_sync(": "vote", "__syncwarp()": "barrier"}[x] for x in re.findall(r"__shfl_sync\(|__syncwarp\(\)", before)]
+
+    def after(steps):
+        w = Warp()
+        w.look(0, {"the slot's rows read"})
+        for step in steps:
+            getattr(w, step)()
+        return w.use(range(8), {"the slot's rows read"})
+    assert after(steps) and not after(["vote"])
