@@ -847,7 +847,8 @@ __global__ void __launch_bounds__(Layout<QT, FP8, KV4>::kThreads, 1)
       named_bar_sync(4, 2 * kRows);
       const float2 other = others[r];
       named_bar_sync(4, 2 * kRows);
-      if (ok && !*s_abort) {
+      // (a warp together, whenever its lanes see the flag turn: loads of tensor memory follow)
+      if (__all_sync(0xffffffffu, ok && !*s_abort)) {
         tc_fence_after();
         const bool both = n_kv > 1;
         const float mx = fmaxf(m, other.x);

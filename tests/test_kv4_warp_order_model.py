@@ -83,3 +83,26 @@ def test_rows_of_q_are_copied_behind_what_lane_0_has_seen():
             getattr(w, step)()
         return w.use(range(8), {"the slot's rows read"})
     assert after(steps) and not after(["vote"])
+
+
+def lanes_that_go_on(guard, turns_at):
+    """The lanes that a guard lets through where they read the abort flag one after another and it turns between two."""
+    mine = [lane < turns_at for lane in range(32)]
+    return sum([all(mine)] * 32 if "__all_sync(" in guard or "any_of(" in guard else mine)
+
+
+def guards_of_flag(name, start, end):
+    """The conditions that read the abort flag between two marks of a source, of code that a whole warp runs."""
+    body = source(name)
+    body = body[body.index(start):]
+    body = body[:body.index(end)]
+    return [x for x in re.findall(r"if \((.*)\) (?:\{|break)", body) if "s_abort" in x or "wait_phase(" in x]
+
+
+def test_the_extend_epilogue_of_two_chains_stays_together():
+    """Loads of tensor memory are a whole warp's: all of its lanes make them or none does."""
+    guards = guards_of_flag("prefill_kernel.cu", "const float2 other = others[r];", "tmem_ld32(")
+    assert len(guards) == 1
+    for guard in guards:
+        assert all(lanes_that_go_on(guard, t) in (0, 32) for t in range(33))
+    assert lanes_that_go_on("ok && !*s_abort", 7) == 7
