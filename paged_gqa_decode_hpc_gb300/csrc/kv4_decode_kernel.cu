@@ -562,8 +562,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   bool dead = false;
   for (int j = 0;; ++j) {
     const int qs = j % kPieceQ, buf = j % C::kBufs;
-    if (!wait_phase(bar_pfull + 8 * qs, (j / kPieceQ) & 1u, abort_flag, p.err, book_ns, false))
-      break;  // no descriptor arrived: the producer is gone
+    const bool came =
+        wait_phase(bar_pfull + 8 * qs, (j / kPieceQ) & 1u, abort_flag, p.err, book_ns, false);
+    // no descriptor arrived: the producer is gone (a warp together, whichever lane's time is up)
+    if (!__all_sync(0xffffffffu, came)) break;
     const int* d = desc + qs * kDescInts;
     const int b = d[0], t0 = d[2], t1 = d[3], fl = d[4], rot = d[6];
     if (fl & kFlagEnd) break;

@@ -106,3 +106,16 @@ def test_the_extend_epilogue_of_two_chains_stays_together():
     for guard in guards:
         assert all(lanes_that_go_on(guard, t) in (0, 32) for t in range(33))
     assert lanes_that_go_on("ok && !*s_abort", 7) == 7
+
+
+def test_a_consumer_warp_leaves_together():
+    """kv4_decode_kernel.cu: a lane whose wait for a descriptor has run out takes its warp along, for the others would go on
+    to shuffles."""
+    body = source("kv4_decode_kernel.cu")
+    body = body[body.index("regs_inc<C::kRegsConsumer>();"):]
+    body = body[:body.index("named_bar_sync(3")]
+    ways_out = re.findall(r"if \((.*)\)\s+break;", body)
+    assert "fl & kFlagEnd" in ways_out  # (of the descriptor: the same for all)
+    ways_out.remove("fl & kFlagEnd")
+    assert len(ways_out) == 1
+    assert all(lanes_that_go_on(ways_out[0], t) in (0, 32) for t in range(33))
