@@ -418,6 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // (rows that nobody waited for may still be landing)
     for (int j = q_pieces > 2 ? q_pieces - 2 : 0; *abort_flag && lane == 0 && j < q_pieces; ++j)
       wait_phase(q_landed(j & 1), (j >> 1) & 1u, abort_flag, p.err, 1000000000ull, false);
+    __syncwarp();  // (lane 0 alone may have waited; the barrier is the whole warp's)
     named_bar_sync(3, kThreads);
     return;
   }

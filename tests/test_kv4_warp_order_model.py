@@ -119,3 +119,11 @@ def test_a_consumer_warp_leaves_together():
     ways_out.remove("fl & kFlagEnd")
     assert len(ways_out) == 1
     assert all(lanes_that_go_on(ways_out[0], t) in (0, 32) for t in range(33))
+
+
+def test_the_warp_that_copies_q_is_together_at_the_last_barrier():
+    """kv4_tc_kernel.cu: after an abort lane 0 alone waits for copies under way; the barrier behind is the whole warp's."""
+    body = source("kv4_tc_kernel.cu")
+    body = body[body.index("for (int j = q_pieces"):]
+    assert "lane == 0" in body[:body.index("wait_phase(")]
+    assert "__syncwarp()" in body[body.index("wait_phase("):body.index("named_bar_sync(3")]
