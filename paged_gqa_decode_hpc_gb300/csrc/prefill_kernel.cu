@@ -885,7 +885,7 @@ __global__ void __launch_bounds__(Layout<QT, FP8, KV4>::kThreads, 1)
         }
         if (g == 0 && row_ok && p.lse)
           p.lse[(int64_t)(q0 + tok) * p.l_st + (int64_t)head * p.l_sh] =
-              all > 0.f ? (mx + __log2f(all)) * kLn2 : -INFINITY;
+              all == 0.f ? -INFINITY : (mx + __log2f(all)) * kLn2;  // (NaN, as out, of a NaN)
       }
       if (full) {
         fence_async_shared();  // the TMA store reads the rows through the async proxy
@@ -929,7 +929,7 @@ __global__ void __launch_bounds__(Layout<QT, FP8, KV4>::kThreads, 1)
         }
         if (row_ok && p.lse)
           p.lse[(int64_t)(q0 + tok) * p.l_st + (int64_t)head * p.l_sh] =
-              l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+              l == 0.f ? -INFINITY : (m + __log2f(l)) * kLn2;  // (NaN, as out, of a NaN)
       }
       if (full) {
         fence_async_shared();  // the TMA store reads the rows through the async proxy
