@@ -771,10 +771,9 @@ hpc_status hpc_decode_kv4_plan_create(int32_t max_seqs, int32_t max_q_len, int32
  *   softmax_scale  > 0, or <= 0 for 1/sqrt(128)
  * Cache slots past a sequence's end may hold anything; a NaN scale before it spoils the
  * tokens that see it (K) or all of the sequence's (V, from the tile that holds it on).
- * Codes times scales, and q (from bf16, by a power of two: what is 2^-29 of the largest
- * element, or less, may lose bits), are exact in f16; the power of two is one for the 8 rows
- * of a KV head where q_len is 1 (a row that is not finite spoils the other seven), each row's
- * own where it is more. Probabilities are rounded to f16 (2^-11 of each, and at least 2^-25
+ * Codes times scales, and q (from bf16, by a power of two of each row's own: what is 2^-29 of
+ * a row's largest element, or less, may lose bits), are exact in f16; a row that is not finite
+ * spoils no other. Probabilities are rounded to f16 (2^-11 of each, and at least 2^-25
  * of the row's largest); sums, maxima and states are fp32. With q_len 1 the states of the
  * warps that share a piece of a sequence are handed over with o in f16 (2^-11, and 2^-25 ts
  * absolute). A token that sees no position gets out
@@ -790,8 +789,7 @@ hpc_status hpc_decode_kv4_attn(const hpc_tensor* q, const hpc_tensor* k_cache,
 /*
  * hpc_extend_kv4_attn -- hpc_extend_attn over a 4-bit cache: prefill / extend attention of
  * ragged new tokens, which are in the cache already, on the tcgen05 tensor cores. Rows are
- * converted exactly to f16 on the chip; q and probabilities as for hpc_decode_kv4_attn
- * (q's power of two is each row's own).
+ * converted exactly to f16 on the chip; q and probabilities as for hpc_decode_kv4_attn.
  *   q, out       device bf16 [total_q][H_q][128], ragged by cu_q_lens; rows contiguous, other
  *                strides multiples of 8 elements, 16-byte aligned; out's rows may not overlap
  *                each other, q's or lse

@@ -31,8 +31,8 @@
 //  * V: its contraction runs over tokens, whose codes lie 72 bytes apart. Lane (g, c)
 //    reads eight bytes, elements 16g .. 16g + 15, of two tokens, and two shifts and two
 //    bit selects make bytes of one element's codes of both tokens. One scale a token.
-//  * Codes times scales are exact in f16 (kv4.cuh). Q takes a power of two that puts the
-//    largest of its 8 rows in [2^14, 2^15), P is rounded to f16 (2^-11), sums and states
+//  * Codes times scales are exact in f16 (kv4.cuh). Each row of Q takes a power of two that puts
+//    its largest element in [2^14, 2^15), P is rounded to f16 (2^-11), sums and states
 //    are fp32. The row maximum moves only when a score passes it by 8 (in log2 units),
 //    so that most units neither reduce it over the lanes nor rescale the sums; P then
 //    stays below 2^8.
@@ -127,8 +127,10 @@ __device__ __forceinline__ int row_token(int i) { return (int)((0x53427160u >> (
 
 // 8 rows of q in shared memory as B operands in K's order of elements:
 // register j of k-step ks holds elements 64 (ks / 4) + 16 c + 4 (ks % 4) + 2 j, + 1 of query
-// head g. Returns the factor that undoes the power of two of the conversion.
-__device__ __forceinline__ float load_q4(uint32_t q, int lane, uint32_t (&qf)[8][2]) {
+// head g. Each row takes a power of two of its own, so that no head's size (or infinity)
+// costs another one bits; inv receives the factors that undo those of this lane's columns of
+// the scores, 2c and 2c + 1.
+__device__ __forceinline__ void load_q4(uint32_t q, int lane, uint32_t (&qf)[8][2], float (&inv)[2]) {
   const int g = lane >> 2, c = lane & 3;
   const uint32_t row = q + (uint32_t)(g * kQRow + 32 * c);
   uint4 u[4];
@@ -147,7 +149,7 @@ __device__ __forceinline__ float load_q4(uint32_t q, int lane, uint32_t (&qf)[8]
                                fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
   }
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  for (int o = 1; o < 4; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   int e = 0;
   if (amax > 0.f) {
     e = 14 - ((int)((__float_as_uint(amax) >> 23) & 0xFF) - 127);
@@ -162,13 +164,15 @@ __device__ __forceinline__ float load_q4(uint32_t q, int lane, uint32_t (&qf)[8]
       qf[2 * i + (x >> 1)][x & 1] =
           pack_f16(__uint_as_float(w[x] << 16) * sc, __uint_as_float(w[x] & 0xFFFF0000u) * sc);
   }
-  return __uint_as_float((uint32_t)(127 - e) << 23);
+  const float undo = __uint_as_float((uint32_t)(127 - e) << 23);
+  inv[0] = __shfl_sync(0xffffffffu, undo, 8 * c);  // (a lane of row 2c)
+  inv[1] = __shfl_sync(0xffffffffu, undo, 8 * c + 4);
 }
 
 // One unit, of whose tokens `stored` are in the sequence.
 __device__ __forceinline__ void compute_unit4(uint32_t kb, uint32_t vb,
-                                              const uint32_t (&qf)[8][2], int stored, float sl2,
-                                              float (&m)[2], float (&l)[2], float (&acc)[8][4],
+                                              const uint32_t (&qf)[8][2], int stored,
+                                              const float (&sl2)[2], float (&m)[2], float (&l)[2], float (&acc)[8][4],
                                               int lane) {
   const int g = lane >> 2, c = lane & 3;
   const int ig = row_token(g);
@@ -235,8 +239,8 @@ __device__ __forceinline__ void compute_unit4(uint32_t kb, uint32_t vb,
     mx0 = fmaxf(mx0, fmaxf(s[mt][0], s[mt][2]));
     mx1 = fmaxf(mx1, fmaxf(s[mt][1], s[mt][3]));
   }
-  mx0 *= sl2;
-  mx1 *= sl2;
+  mx0 *= sl2[0];
+  mx1 *= sl2[1];
   if (__any_sync(0xffffffffu, mx0 > m[0] + 8.f || mx1 > m[1] + 8.f)) {
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) {
@@ -263,11 +267,11 @@ __device__ __forceinline__ void compute_unit4(uint32_t kb, uint32_t vb,
   // what rounding took from a maximum of 2^30 is no small number)
   const float r0 = m[0] == -INFINITY ? 0.f : m[0];
   const float r1 = m[1] == -INFINITY ? 0.f : m[1];
-  auto less = [&](float x, float r) { return ex2(__fsub_rn(__fmul_rn(x, sl2), r)); };
+  auto less = [&](float x, float f, float r) { return ex2(__fsub_rn(__fmul_rn(x, f), r)); };
 #pragma unroll
   for (int mt = 0; mt < 4; ++mt) {
-    const float e0 = less(s[mt][0], r0), e1 = less(s[mt][1], r1);
-    const float e2 = less(s[mt][2], r0), e3 = less(s[mt][3], r1);
+    const float e0 = less(s[mt][0], sl2[0], r0), e1 = less(s[mt][1], sl2[1], r1);
+    const float e2 = less(s[mt][2], sl2[0], r0), e3 = less(s[mt][3], sl2[1], r1);
     l[0] += e0 + e2;
     l[1] += e1 + e3;
     pb[mt][0] = movm_trans(pack_f16(e0, e1));
@@ -575,13 +579,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int dm = 0; dm < 8; ++dm) acc[dm][0] = acc[dm][1] = acc[dm][2] = acc[dm][3] = 0.f;
     uint32_t qf[8][2];
-    float sl2 = 0.f;
+    float sl2[2] = {0.f, 0.f};  // factors of the lane's two columns
     int len = 0;
     if (i0 < n) {
       len = __ldg(p.seq_lens + b);
-      const float qinv = load_q4(smem_base + C::kQOff + qs * C::kQBytes, lane, qf);
+      load_q4(smem_base + C::kQOff + qs * C::kQBytes, lane, qf, sl2);
       // (a factor of 0 would make NaN of masked scores, an infinite one of scores of 0)
-      sl2 = fminf(fmaxf(p.score_scale_log2 * qinv, FLT_MIN), FLT_MAX);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) sl2[x] = fminf(fmaxf(p.score_scale_log2 * sl2[x], FLT_MIN), FLT_MAX);
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(bar_pfree + 8 * qs);  // this warp has read the descriptor and q
