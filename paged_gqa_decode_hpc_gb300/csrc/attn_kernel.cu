@@ -417,10 +417,12 @@ __global__ void __launch_bounds__((NC + 1) * 32, 1)
       const int len_t = len - (p.q_len - 1 - tok);
       if (active && i_lo + tphase < i_hi) {
         uint32_t qf[8][2];
-        const float qinv = load_q<FP8>(p.q + (int64_t)b * p.q_sb + (int64_t)tok * p.q_st +
-                                           (int64_t)(h * kGroup) * p.q_sh,
-                                       p.q_sh, lane, qf);
-        const float sl2 = p.score_scale_log2 * qinv;
+        float sl2[2];
+        load_q<FP8>(p.q + (int64_t)b * p.q_sb + (int64_t)tok * p.q_st +
+                        (int64_t)(h * kGroup) * p.q_sh,
+                    p.q_sh, lane, qf, sl2);
+        sl2[0] *= p.score_scale_log2;
+        sl2[1] *= p.score_scale_log2;
         for (int i = i_lo + tphase; i < i_hi; i += tph) {
           // position of unit (tile t0 + i, head hl) in the order of issue
           const uint32_t gu = U > 1 ? gbase + (uint32_t)((t0 + i) * U + hl - tb)

@@ -79,10 +79,12 @@ __device__ __forceinline__ int acc_d(int dm, int r, int g) {
 
 // Q of one (sequence, kv head) as mma B fragments (B[k = d][n = q head]).
 // q0 points at the first query head of the KV head's group, q_sh is the
-// stride between query heads (elements).
+// stride between query heads (elements). inv receives the factors that undo the conversion of
+// this lane's columns of the scores, query heads 2c and 2c + 1: with an FP8 cache each head
+// takes a power of two of its own, so that no head's size (or infinity) costs another one bits.
 template <bool FP8>
-__device__ __forceinline__ float load_q(const __nv_bfloat16* q0, int64_t q_sh, int lane,
-                                        uint32_t (&qf)[8][2]) {
+__device__ __forceinline__ void load_q(const __nv_bfloat16* q0, int64_t q_sh, int lane,
+                                       uint32_t (&qf)[8][2], float (&inv)[2]) {
   const int g = lane >> 2, c = lane & 3;
   const __nv_bfloat16* qrow = q0 + (int64_t)g * q_sh;
   if constexpr (!FP8) {
@@ -91,7 +93,7 @@ __device__ __forceinline__ float load_q(const __nv_bfloat16* q0, int64_t q_sh, i
       qf[ks][0] = __ldg(reinterpret_cast<const uint32_t*>(qrow + 16 * ks + 2 * c));
       qf[ks][1] = __ldg(reinterpret_cast<const uint32_t*>(qrow + 16 * ks + 2 * c + 8));
     }
-    return 1.0f;
+    inv[0] = inv[1] = 1.0f;
   } else {
     // Logical k (2c, 2c+1 | 2c+8, 2c+9) of k-step ks maps to d = 16ks + 4c + (0,1 | 2,3),
     // matching the byte order ldmatrix gives the FP8 K tile.
@@ -108,8 +110,8 @@ __device__ __forceinline__ float load_q(const __nv_bfloat16* q0, int64_t q_sh, i
       for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fabsf(v[ks][e]));
     }
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    // Power-of-two scale putting max|q| in [2^14, 2^15): f16 holds every
+    for (int o = 1; o < 4; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    // Power-of-two scale putting the head's max|q| in [2^14, 2^15): f16 holds every
     // bf16 value of that range exactly.
     int e = 0;
     if (amax > 0.f) {
@@ -123,15 +125,17 @@ __device__ __forceinline__ float load_q(const __nv_bfloat16* q0, int64_t q_sh, i
       qf[ks][0] = pack_f16(v[ks][0] * sc, v[ks][1] * sc);
       qf[ks][1] = pack_f16(v[ks][2] * sc, v[ks][3] * sc);
     }
-    return __uint_as_float((uint32_t)(127 - e) << 23);  // 2^-e
+    const float undo = __uint_as_float((uint32_t)(127 - e) << 23);  // 2^-e
+    inv[0] = __shfl_sync(0xffffffffu, undo, 8 * c);                 // (a lane of head 2c)
+    inv[1] = __shfl_sync(0xffffffffu, undo, 8 * c + 4);
   }
 }
 
 // One (tile, kv head) unit: scores, online softmax update, P.V accumulate.
 template <bool FP8>
 __device__ __forceinline__ void compute_unit(uint32_t kbase, uint32_t vbase,
-                                             const uint32_t (&qf)[8][2], int valid, float sl2,
-                                             float (&m)[2], float (&l)[2], float (&acc)[8][4],
+                                             const uint32_t (&qf)[8][2], int valid,
+                                             const float (&sl2)[2], float (&m)[2], float (&l)[2], float (&acc)[8][4],
                                              int lane) {
   const int r8 = lane & 7;
   const int mi = lane >> 3;
@@ -176,7 +180,7 @@ __device__ __forceinline__ void compute_unit(uint32_t kbase, uint32_t vbase,
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int tok = mt * 16 + g + 8 * r;
-      float x0 = s[mt][2 * r] * sl2, x1 = s[mt][2 * r + 1] * sl2;
+      float x0 = s[mt][2 * r] * sl2[0], x1 = s[mt][2 * r + 1] * sl2[1];
       if (tok >= valid) x0 = x1 = -INFINITY;
       s[mt][2 * r] = x0;
       s[mt][2 * r + 1] = x1;

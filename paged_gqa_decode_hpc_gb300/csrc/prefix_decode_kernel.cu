@@ -845,10 +845,11 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
         const int j0 = (warp - k0) & 7;
         if (j0 < n) {
           uint32_t qf[8][2];
-          const float sl2 =
-              p.score_scale_log2 * load_q<FP8>(p.q + (int64_t)walk.ra.x * p.q_sp +
-                                                   (int64_t)(kGroupRows * pc.h) * p.q_sh,
-                                               p.q_sh, lane, qf);
+          float sl2[2];
+          load_q<FP8>(p.q + (int64_t)walk.ra.x * p.q_sp + (int64_t)(kGroupRows * pc.h) * p.q_sh,
+                      p.q_sh, lane, qf, sl2);
+          sl2[0] *= p.score_scale_log2;
+          sl2[1] *= p.score_scale_log2;
           for (int j = j0; j < n; j += 8) {
             const int k = k0 + j, slot = k % Lt::kWStages;
             ok = __all_sync(0xffffffffu, wait_word(base + Lt::kOffWord + 4 * slot, (uint32_t)k,

@@ -653,9 +653,10 @@ __global__ void __launch_bounds__(kSThreads, 1)
     if (i0 < n) {
       const int len = __ldg(p.seq_lens + b);
       uint32_t qf[8][2];
-      const float qinv = load_q<FP8>(p.q + (int64_t)b * p.q_sb + (int64_t)(h * kGroup) * p.q_sh,
-                                     p.q_sh, lane, qf);
-      const float sl2 = p.score_scale_log2 * qinv;
+      float sl2[2];
+      load_q<FP8>(p.q + (int64_t)b * p.q_sb + (int64_t)(h * kGroup) * p.q_sh, p.q_sh, lane, qf, sl2);
+      sl2[0] *= p.score_scale_log2;
+      sl2[1] *= p.score_scale_log2;
       for (int i = i0; i < n; i += kSNC) {
         const uint32_t gu = (uint32_t)(g0 + i);
         const uint32_t s = gu % STAGES;
