@@ -766,7 +766,9 @@ hpc_status hpc_decode_kv4_plan_create(int32_t max_seqs, int32_t max_q_len, int32
  *   plan         from hpc_decode_kv4_plan_create, for at least this step's sequences, new
  *                tokens and heads, on the current device
  *   out          device bf16, q's shape and rules (written). Its rows may not overlap each
- *                other, q's or lse (HPC_ERR_INVALID_ARG)
+ *                other, q's or lse (HPC_ERR_INVALID_ARG). In one buffer they may lie between
+ *                q's, and lse between both, where sequences and heads have the same strides in
+ *                bytes; with other strides byte ranges that meet count as overlapping
  *   lse          device f32 [B][H_q] or [B][q_len][H_q], natural log (written), or NULL
  *   softmax_scale  > 0, or <= 0 for 1/sqrt(128)
  * Cache slots past a sequence's end may hold anything; a NaN scale before it spoils the

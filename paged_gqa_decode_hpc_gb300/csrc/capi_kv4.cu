@@ -83,32 +83,57 @@ bool nested(const hpc_tensor* t, int n, int64_t inner) {
   return true;
 }
 
+// Results of one kind as the checks see them: pieces [sequences][q_len][heads] of a tensor, a row
+// of 128 bf16 each or (lse) a float.
+struct Pieces {
+  const hpc_tensor* t;
+  int heads;             // the heads' dimension; [rows][heads] has no tokens of its own
+  int64_t elt, inner;    // bytes of an element, elements of a piece
+  Pieces(const hpc_tensor* x, bool row)
+      : t(x), heads(x->ndim - (row ? 2 : 1)), elt(row ? 2 : 4), inner(row ? kHeadDim : 1) {}
+  int64_t tokens() const { return heads == 2 ? t->shape[1] : 1; }
+  // [sequences][heads] of one token
+  Rows at(int64_t token) const {
+    Rows r(t, elt);
+    if (heads == 2) r.p += token * t->stride[1] * elt;
+    r.h = t->shape[heads];
+    r.sh = t->stride[heads] * elt;
+    r.row = inner * elt;
+    return r;
+  }
+};
+
+// Whether a piece of a meets one of b: exact where sequences and heads have the same strides
+// in both, as in views of one buffer; else byte ranges decide (rows_overlap).
+bool pieces_meet(const Pieces& a, const Pieces& b) {
+  if (!ranges_meet(a.t, a.elt, b.t, b.elt)) return false;
+  for (int64_t i = 0; i < a.tokens(); ++i)
+    for (int64_t j = 0; j < b.tokens(); ++j)
+      if (rows_overlap(a.at(i), b.at(j))) return true;
+  return false;
+}
+
+// Whether two of its own pieces meet.
+bool pieces_meet(const Pieces& a) {
+  if (nested(a.t, a.heads + 1, a.inner)) return false;
+  if (rows_overlap(a.at(0), a.at(0), true)) return true;
+  for (int64_t i = 1; i < a.tokens(); ++i)
+    if (rows_overlap(a.at(0), a.at(i))) return true;
+  return false;
+}
+
 // out's rows are written while other CTAs read q, in no order: they may not share bytes
 // with q's, with each other or with lse.
 hpc_status check_overlap(const hpc_tensor* q, const hpc_tensor* out, const hpc_tensor* lse,
                          bool has_lse) {
-  auto rows = [](const hpc_tensor* t, bool* flat) {  // [B][q_len] as one dimension where it is one
-    hpc_tensor r = *t;
-    *flat = true;
-    if (t->ndim == 4) {
-      *flat = t->shape[0] <= 1 || t->shape[1] <= 1 || t->stride[0] == t->shape[1] * t->stride[1];
-      r.shape[0] = t->shape[0] * t->shape[1];
-      r.stride[0] = t->shape[1] > 1 ? t->stride[1] : t->stride[0];
-      r.shape[1] = t->shape[2];
-      r.stride[1] = t->stride[2];
-    }
-    return Rows(&r, 2);
-  };
-  bool fq, fo;
-  const Rows rq = rows(q, &fq), ro = rows(out, &fo);
-  if (fo ? rows_overlap(ro, ro, true) : !nested(out, out->ndim - 1, kHeadDim))
-    return fail(HPC_ERR_INVALID_ARG, "rows of out overlap");
-  if (fq && fo ? rows_overlap(ro, rq) : ranges_meet(out, 2, q, 2))
-    return fail(HPC_ERR_INVALID_ARG, "out overlaps q");
-  if (has_lse && (ranges_meet(lse, 4, q, 2) || ranges_meet(lse, 4, out, 2)))
+  const Pieces rq(q, true), ro(out, true);
+  if (pieces_meet(ro)) return fail(HPC_ERR_INVALID_ARG, "rows of out overlap");
+  if (pieces_meet(ro, rq)) return fail(HPC_ERR_INVALID_ARG, "out overlaps q");
+  if (!has_lse) return HPC_OK;
+  const Pieces rl(lse, false);
+  if (pieces_meet(rl, rq) || pieces_meet(rl, ro))
     return fail(HPC_ERR_INVALID_ARG, "lse overlaps q or out");
-  if (has_lse && !nested(lse, lse->ndim, 1))
-    return fail(HPC_ERR_INVALID_ARG, "elements of lse overlap");
+  if (pieces_meet(rl)) return fail(HPC_ERR_INVALID_ARG, "elements of lse overlap");
   return HPC_OK;
 }
 
