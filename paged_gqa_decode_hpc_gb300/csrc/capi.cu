@@ -1139,7 +1139,9 @@ hpc_status make_q_map(const hpc_tensor* q, CUtensorMap* map, const char* what) {
   auto enc = encode_fn();
   if (!enc) return fail(HPC_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
   cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)q->shape[1], (cuuint64_t)q->shape[0]};
-  cuuint64_t strides[2] = {(cuuint64_t)q->stride[1] * 2, (cuuint64_t)q->stride[0] * 2};
+  // (the stride of a single token means nothing, but has to be a multiple of 16 bytes)
+  const int64_t st = q->shape[0] > 1 ? q->stride[0] : q->shape[1] * kHeadDim;
+  cuuint64_t strides[2] = {(cuuint64_t)q->stride[1] * 2, (cuuint64_t)st * 2};
   cuuint32_t box[3] = {64, (cuuint32_t)kGroup, (cuuint32_t)kExtendTileTokens};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q->data, dims, strides, box, estr,
