@@ -229,6 +229,12 @@ __device__ TileInfo find_tile(const ExtendParams& p, int y, int lane, int tile_t
       n = p.cu_q_lens[b + 1] - q0;
       L = p.seq_lens[b];
     }
+    // Rows past q's end (where the entry gives it): no tile, so that the others keep theirs. Every
+    // first CTA looks over all sequences, and one says it.
+    if (p.total_q > 0 && n > 0 && (q0 < 0 || q0 > p.total_q - n)) {
+      if (y == 0 && blockIdx.x == 0 && p.err) atomicOr(p.err, HPC_DEVCHK_BAD_LENGTH);
+      n = 0;
+    }
     return n > 0 ? (n + tile_tokens - 1) / tile_tokens : 0;
   };
   int total = 0;
@@ -263,8 +269,7 @@ __device__ TileInfo find_tile(const ExtendParams& p, int y, int lane, int tile_t
     base += chunk;
   }
   if (!ti.valid) return ti;
-  // more new tokens than positions, or than rows
-  if (ti.L < ti.n || (p.total_q > 0 && (ti.q0 < 0 || ti.q0 > p.total_q - ti.n))) {
+  if (ti.L < ti.n) {  // more new tokens than positions
     if (lane == 0 && p.err) atomicOr(p.err, HPC_DEVCHK_BAD_LENGTH);
     ti.valid = 0;
     return ti;
