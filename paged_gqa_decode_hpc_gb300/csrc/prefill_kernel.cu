@@ -223,15 +223,17 @@ __device__ TileInfo find_tile(const ExtendParams& p, int y, int lane, int tile_t
   int q0 = 0, n = 0, L = 0;
   auto lane_seq = [&](int c) -> int {  // tiles of sequence c + lane
     const int b = c + lane;
+    int end = 0;
     q0 = n = L = 0;
     if (b < B) {
       q0 = p.cu_q_lens[b];
-      n = p.cu_q_lens[b + 1] - q0;
+      end = p.cu_q_lens[b + 1];
+      n = end - q0;
       L = p.seq_lens[b];
     }
     // Rows past q's end (where the entry gives it): no tile, so that the others keep theirs. Every
     // first CTA looks over all sequences, and one says it.
-    if (p.total_q > 0 && n > 0 && (q0 < 0 || q0 > p.total_q - n)) {
+    if (p.total_q > 0 && end > q0 && (q0 < 0 || end > p.total_q)) {  // (n may have wrapped)
       if (y == 0 && blockIdx.x == 0 && p.err) atomicOr(p.err, HPC_DEVCHK_BAD_LENGTH);
       n = 0;
     }
