@@ -284,9 +284,13 @@ __device__ TileInfo find_tile(const ExtendParams& p, int y, int lane, int tile_t
 // its last row sees (rows past n clamp to L); 0 when the tile has no row.
 __device__ __forceinline__ int tile_kv(int L, int n, int t0g) {
   if (t0g >= n) return 0;
-  int kv_len = L - n + t0g + kExtendTileTokens;
-  if (kv_len > L) kv_len = L;
-  return (kv_len + 63) / 64;
+  const int behind = n - t0g - kExtendTileTokens;  // new tokens past the tile
+  return ((behind > 0 ? L - behind : L) - 1) / 64 + 1;  // (no sum here passes INT32_MAX)
+}
+
+// Keys visible to new token `tok`: positions below this (rows past n: any number up to L).
+__device__ __forceinline__ int keys_seen(int L, int n, int tok) {
+  return tok < n ? L - (n - 1 - tok) : L;
 }
 
 }  // namespace
@@ -665,8 +669,7 @@ __global__ void __launch_bounds__(Layout<QT, FP8, KV4>::kThreads, 1)
     const int tg = SPLIT ? 0 : kExtendTileTokens * g;  // the tile's first token from t0
     const int tok = t0 + tg + (r >> 3), head = kGroupRows * h + (r & 7);
     const bool row_ok = valid && tok < n;
-    int lim = L - n + 1 + tok;  // keys visible to this row: positions < lim
-    if (lim > L) lim = L;
+    const int lim = keys_seen(L, n, tok);
     const int nk = g == 0 ? nkv[0] : nkv[QT - 1];
     // the tile leaves by TMA when all its 16 tokens are new tokens of this
     // sequence (see the epilogue); uniform over the warpgroup
@@ -750,7 +753,7 @@ __global__ void __launch_bounds__(Layout<QT, FP8, KV4>::kThreads, 1)
       tc_fence_before();
       mbar_arrive(s_free(g));
       const int kv0 = (kStride * j + (SPLIT ? g : 0)) * 64;
-      if (kv0 + 64 > lim) {
+      if (kv0 > lim - 64) {
 #pragma unroll
         for (int c = 0; c < 64; ++c)
           if (kv0 + c >= lim) s[c] = -INFINITY;
