@@ -47,7 +47,6 @@
 #include "kv4_plan.cuh"
 #include "kv4_state.cuh"
 #include "ptx.cuh"
-#include "step_plan.cuh"
 
 namespace hpc {
 namespace {
@@ -95,15 +94,6 @@ struct Cfg {
   static constexpr int kRegsProducer = 72;
   static_assert(2 * kRegsConsumer + kRegsEpilogue + kRegsProducer == 512, "registers");
 };
-template <int N>
-__device__ __forceinline__ void regs_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N) : "memory");
-}
-template <int N>
-__device__ __forceinline__ void regs_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N) : "memory");
-}
-
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
   return *reinterpret_cast<const uint2*>(__cvta_shared_to_generic(a));
 }

@@ -98,15 +98,6 @@ struct Cfg {
                        kRegsV = COLS > 48 ? 40 : 56, kRegsOther = COLS > 48 ? 48 : 56;
   static_assert(2 * kRegsSoftmax + kRegsK + 2 * kRegsV + kRegsOther == 6 * 80, "registers");
 };
-template <int N>
-__device__ __forceinline__ void regs_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N) : "memory");
-}
-template <int N>
-__device__ __forceinline__ void regs_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N) : "memory");
-}
-
 // 8 columns of this warp's 32 lanes.
 __device__ __forceinline__ void tmem_ld8(uint32_t a, float* v) {
   uint32_t* r = reinterpret_cast<uint32_t*>(v);

@@ -54,6 +54,7 @@
 #include "hpc_internal.h"
 #include "kv4.cuh"
 #include "prefill.h"
+#include "ptx.cuh"
 #include "tc05.cuh"
 
 namespace hpc {
@@ -162,15 +163,6 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 }
 __device__ __forceinline__ void named_bar_sync(int id, int nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
-}
-
-template <int N>
-__device__ __forceinline__ void regs_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N) : "memory");
-}
-template <int N>
-__device__ __forceinline__ void regs_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N) : "memory");
 }
 
 // Bounded wait on an mbarrier phase; false when the CTA aborts or the limit

@@ -125,12 +125,6 @@ struct Lay {
 // Of the launch's 512 x 128 registers (e4m3; bf16 384 x 168) the softmax
 // warpgroups take 176 a thread and the other warps keep 80: 256 * 176 + 256 * 80 = 65536.
 constexpr int kRegsSoftmax = 176, kRegsOther = 80;
-__device__ __forceinline__ void regs_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax) : "memory");
-}
-__device__ __forceinline__ void regs_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther) : "memory");
-}
 
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
   uint64_t r;
@@ -422,7 +416,7 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
 
   if (warp == Lt::kProducerWarp) {
     // ------------------------------------------------------------ producer
-    regs_dec();
+    regs_dec<kRegsOther>();
     walk.begin(p, part);
     uint64_t read_once, shared_tiles;  // own tiles leave L2 first: row tiles read shared ones again
     asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(read_once));
@@ -555,7 +549,7 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
     // c' ^ (t % 8)). Each group of 8 threads serving one 16-byte access covers
     // all 8 bank groups on the load and both stores. V rows behind the end of
     // the sequence become zeros.
-    regs_dec();
+    regs_dec<kRegsOther>();
     walk.begin(p, part);
     constexpr int kNT = 128;
     const int ct = threadIdx.x - 32 * Lt::kConvWarp0;
@@ -624,13 +618,13 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
     }
     named_bar_sync(1, Lt::kThreads);
   } else if (warp >= Lt::kMmaWarp0 + 2) {
-    regs_dec();  // the idle warp of the last warpgroup
+    regs_dec<kRegsOther>();  // the idle warp of the last warpgroup
     named_bar_sync(1, Lt::kThreads);
   } else if (warp >= Lt::kMmaWarp0) {
     // ------------------------------------------- MMA issue for pipeline g
     // The whole warp runs the schedule so its values stay warp-uniform; one
     // elected lane issues the MMAs and commits.
-    regs_dec();
+    regs_dec<kRegsOther>();
     walk.begin(p, part);
     const int g = warp - Lt::kMmaWarp0;
     const bool leader = elect_one() != 0;
@@ -821,7 +815,7 @@ __global__ void __launch_bounds__(Lay<FP8>::kThreads, 1)
     if (warp == Lt::kMmaWarp0) tmem_dealloc(tmem, 2 * kColsPerPipe);
   } else {
     // ------------------------------------------- softmax warpgroup of pipeline g
-    regs_inc();
+    regs_inc<kRegsSoftmax>();
     walk.begin(p, part);
     const int g = warp >> 2;
     const int r = threadIdx.x - kRows * g;  // query row = TMEM lane

@@ -48,7 +48,6 @@
 #include "decode_common.cuh"
 #include "hpc_internal.h"
 #include "ptx.cuh"
-#include "step_plan.cuh"
 
 namespace hpc {
 namespace {
@@ -107,6 +106,30 @@ __device__ __forceinline__ float2 unpack_dep(uint32_t v) {
     return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
   }
 }
+
+// Owner arithmetic of the step plan: parts [0, P) over the first S units,
+// then chunks of C units up to T. Every unit index is below T <= INT32_MAX,
+// so the arithmetic is 32-bit (short, fast code on a path that runs cold once
+// per step); the part formulas take 64 bits only when S * P does not fit.
+struct StepMath {
+  uint32_t T, S, P, C, chunks;
+  bool small;  // (S + 1) * (P + 1) < 2^32
+  __device__ __forceinline__ uint32_t part_start(uint32_t o) const {
+    return small ? o * S / P : (uint32_t)((uint64_t)o * S / P);
+  }
+  __device__ __forceinline__ uint32_t start(uint32_t o) const {
+    return o < P ? part_start(o) : S + (o - P) * C;
+  }
+  __device__ __forceinline__ uint32_t end(uint32_t o) const {
+    if (o < P) return o + 1 < P ? part_start(o + 1) : S;
+    const uint32_t e = S + (o - P + 1) * C;
+    return e < T ? e : T;
+  }
+  __device__ __forceinline__ uint32_t owner_of(uint32_t x) const {
+    if (x < S) return small ? ((x + 1) * P - 1) / S : (uint32_t)(((uint64_t)(x + 1) * P - 1) / S);
+    return P + (x - S) / C;
+  }
+};
 
 // Output dims held by a lane in accumulator slice dm (see acc_d).
 template <bool FP8>
