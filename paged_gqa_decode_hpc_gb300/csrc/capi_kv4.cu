@@ -348,10 +348,10 @@ hpc_status hpc_decode_kv4_attn(const hpc_tensor* q, const hpc_tensor* k_cache,
     p.timeout_ns = wait_limit_ns();
     p.withhold_copies = withhold_copies();
     p.ws_ml = (float2*)(p.ws + kv4_slots(plan->num_sms) * T * (kGroup * kHeadDim / 4));
-    // One token on mma.sync, whose time is then memory's and less fixed (55 us for 32 x 4096 and
-    // 131072 positions of 8 KV heads; the other kernel 77); more on tcgen05, which converts a
-    // unit's codes once for all of them (2 tokens 83.6 and 83.3 us, 4: 151.6 and 98.6, 8:
-    // 293.5 and 126.4).
+    // One token on mma.sync, which has less fixed cost (56 us for 31 x 4096 and 131072 positions
+    // of 8 KV heads; the other kernel 77); more on tcgen05, which converts a unit's codes once
+    // for all of them (2 tokens 83.6 on mma.sync and 84.3 us, 4: 151.6 and 98.7, 8: 293.5 and
+    // 127.8).
     if (T == 1) {
       e = launch_kv4_decode(p, plan->num_sms, (cudaStream_t)stream);
     } else {

@@ -8,13 +8,15 @@
 // registers. The plan (kv4_plan.cuh) gives every CTA an equal part of the units, taken in
 // pieces of one (sequence, KV head) pair, whose states are joined by log-sum-exp.
 //
-// What bounds it: HBM, and next to it the issue of instructions. A unit is 9216 bytes, 206 ns
-// of an SM's share of 6.8 TB/s, in which its 16384 codes have to become f16 operands: about
-// 1020 warp instructions, among them 64 MMAs of 8 issue cycles, 1650 cycles of one of the four
-// sub-partitions (412 of the SM, 390 are HBM's). So a warp takes a unit by itself, and no value
-// moves between warps. Measured: 32 sequences of 4096 and one of 131072 positions of 8 KV
-// heads 55 us (298 MB, 5.4 TB/s); 64 of 200 to 6000 30 us, of which 5 are the plan, the first
-// unit's two dependent loads and the last states' way to memory.
+// What bounds it: the consumer warps' own latencies; nothing that they share is full. A unit is
+// 9216 bytes, 206 ns of an SM's share of 6.8 TB/s (390 cycles), in which its 16384 codes have to
+// become f16 operands: about 1080 warp instructions, 64 of them MMAs, 270 issue cycles of the
+// SM. So a warp takes a unit by itself, and no value moves between warps. Measured: 31 sequences
+// of 4096 and one of 131072 positions of 8 KV heads 55.9 us (298 MB, 5.3 TB/s); while its SMs are
+// active they issue in 52 % of the cycles, and no pipe is busier than the ALU (47 %; FMA 31 %,
+// tensor 25 %): two consumer warps to a scheduler, and a warp goes 7.7 cycles between two
+// instructions. 64 sequences of 200 to 6000 30.2 us, of which 5 are the plan, the first unit's
+// two dependent loads and the last states' way to memory.
 //
 // How a unit gets into the MMAs (mma.sync m16n8k16, f16; S^T = K Q^T, O^T = V^T P^T):
 //  * A tile is copied as it lies in memory, 64 rows of 72 bytes. Rows are 18 words

@@ -26,19 +26,20 @@
 // wait is bounded; after one has run out every role leaves, the MMAs are waited for and tensor
 // memory is freed.
 //
-// What bounds it (32 sequences of 4096 and one of 131072 positions, 8 KV heads; HBM's share is
+// What bounds it (31 sequences of 4096 and one of 131072 positions, 8 KV heads; HBM's share is
 // 44 us, 780 clk a step): the chain from a step's scores to its P^T, about 1000 clk of waits,
 // vote and fences that no row count changes and 15 to 25 a row of the group, on warps that share
 // the SM's issue (0.5 to 0.6 a cycle) and its shared memory (2 tokens: 710 wavefronts a step
 // for threads, 315 for the MMAs, 144 for the copies; V passes twice) with the conversions.
-// 2 tokens take 83 us, 4 take 99, 6 110, 8 126. What it took, 4 and 8 tokens: one softmax
+// 2 tokens take 84 us, 4 take 99, 6 112, 8 128. What it took, 4 and 8 tokens: one softmax
 // group and one warp for both products 151 and 203 us; two waits a step in that warp and 8
 // warps for V 121 and 182; two groups, a warp for each product 102 and 162; a factor for each
 // row (see below) 107 and 153; references and factors in registers 102 and 131; a pair counted
-// with 7 units 101 and 128; K's two halves in a loop 99 and 126. Groups that
-// take alternate steps instead of rows were slower (118 and 214: their states need more
-// registers). A wait on two barriers takes half of the lanes each, one latency instead of two:
-// one after the other they cost 8 to 10 %.
+// with 7 units 101 and 128; K's two halves in a loop 99 and 126; the
+// warp barrier behind a wait on two barriers 99 and 128. Groups that take alternate steps
+// instead of rows were slower (118 and 214: their states need more registers). A wait on two
+// barriers takes half of the lanes each, one latency instead of two: with every lane at one and
+// then at the other 2 tokens take 103 us, 4 129, 8 165.
 #include <cfloat>
 
 #include "kv4_plan.cuh"
