@@ -556,8 +556,10 @@ __global__ void __launch_bounds__(kSThreads, 1)
     const int g8 = lane >> 2, c4 = lane & 3;
     for (int j = warp - kEpilogueWarp0;; j += kEpilogueWarps) {
       const int qs = j % kPieceQ;
-      if (!wait_phase(bar_pfull + 8 * qs, (j / kPieceQ) & 1u, abort_flag, p.err, book_ns, false))
-        break;
+      // (a warp leaves together, whichever lane's time is up: the others would wait for it)
+      bool came =
+          wait_phase(bar_pfull + 8 * qs, (j / kPieceQ) & 1u, abort_flag, p.err, book_ns, false);
+      if (!__all_sync(0xffffffffu, came)) break;
       const int* d = desc + qs * kDescInts;
       const int b = d[0], h = d[1], fl = d[4], slot = d[5];
       __syncwarp();
@@ -566,9 +568,9 @@ __global__ void __launch_bounds__(kSThreads, 1)
       // the deposits of piece j complete phase j / kEpilogueWarps of this
       // warp's barrier; its next phase needs this warp's read first, so the
       // barrier is at most one phase ahead of the wait and the parity is exact
-      if (!wait_phase(bar_dfull + 8 * (j % kEpilogueWarps), (j / kEpilogueWarps) & 1u, abort_flag,
-                      p.err, book_ns, false))
-        break;
+      came = wait_phase(bar_dfull + 8 * (j % kEpilogueWarps), (j / kEpilogueWarps) & 1u, abort_flag,
+                        p.err, book_ns, false);
+      if (!__all_sync(0xffffffffu, came)) break;
       // the 8 warps' states, combined in warp order
       // acc = sum_v o_v l_v 2^(m_v - M): the unnormalised sum of the 8 states
       const uint4* dep4 = reinterpret_cast<const uint4*>(dep);
@@ -657,8 +659,9 @@ __global__ void __launch_bounds__(kSThreads, 1)
   bool dead = false;
   for (int j = 0;; ++j) {
     const int qs = j % kPieceQ;
-    if (!wait_phase(bar_pfull + 8 * qs, (j / kPieceQ) & 1u, abort_flag, p.err, book_ns, false))
-      break;  // no descriptor arrived: the producer is gone
+    const bool came =
+        wait_phase(bar_pfull + 8 * qs, (j / kPieceQ) & 1u, abort_flag, p.err, book_ns, false);
+    if (!__all_sync(0xffffffffu, came)) break;  // no descriptor arrived: the producer is gone
     const int* d = desc + qs * kDescInts;
     const int b = d[0], h = d[1], t0 = d[2], t1 = d[3], fl = d[4], g0 = d[6];
     __syncwarp();

@@ -127,3 +127,15 @@ def test_the_warp_that_copies_q_is_together_at_the_last_barrier():
     body = body[body.index("for (int j = q_pieces"):]
     assert "lane == 0" in body[:body.index("wait_phase(")]
     assert "__syncwarp()" in body[body.index("wait_phase("):body.index("named_bar_sync(3")]
+
+
+def test_the_step_kernel_s_warps_leave_together():
+    """step_kernel.cu: the same waits, of its consumer and its epilogue warps, behind which shuffles and warp barriers come."""
+    body = source("step_kernel.cu")
+    for start in ("for (int j = warp - kEpilogueWarp0;;", "const int w = warp;"):
+        part = body[body.index(start):]
+        part = part[:part.index("named_bar_sync(3")]
+        ways_out = [x for x in re.findall(r"if \(([^;{}]*)\)\s+break;", part) if x != "fl & kFlagEnd"]
+        assert ways_out
+        for guard in ways_out:
+            assert all(lanes_that_go_on(guard, t) in (0, 32) for t in range(33)), guard
